@@ -67,7 +67,8 @@ typedef enum {
   SV_ERR_WORKSPACE = 5,   /* workspace too small */
   SV_ERR_CUDA = 6,        /* a CUDA runtime call or kernel launch failed */
   SV_ERR_TIMEOUT = 7,     /* a device-side wait gave up (reported by sv_workspace_status) */
-  SV_ERR_DEVICE_SHAPE = 8 /* device-side length check failed (sv_workspace_status) */
+  SV_ERR_DEVICE_SHAPE = 8, /* device-side length check failed (sv_workspace_status) */
+  SV_ERR_NO_PAGES = 9      /* too few free pages (sv_workspace_status, spec_pages_extend) */
 } sv_status;
 
 typedef enum { SV_BF16 = 0, SV_FP8_E4M3 = 1, SV_FP32 = 2 } sv_dtype;
@@ -177,6 +178,114 @@ SV_API sv_status spec_verify_attn_paged(const sv_attn_desc* desc, const void* q,
                                  int32_t max_blocks_per_seq, const int32_t* seq_lens,
                                  const int32_t* draft_len, const float* kv_scale, void* out,
                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Pages of a paged KV cache ("GPU and LLM, chapter 5", "PagedAttention (2)": blocks of a
+ * fixed number of positions, found through a per-sequence block table; sequences with a
+ * common beginning may name the same blocks). The four calls below keep the block tables
+ * that spec_verify_attn_paged and spec_verify_attn_shared read.
+ *
+ * State, all of it device memory of the caller's, shared by every layer of a model:
+ *   ref_count[p]   how many table entries in use name page p; p is free iff it is 0
+ *   cached_len[r]  positions held by table row r (one row per sequence; 0: unused)
+ *   block_table[r, j], j < ceil(cached_len[r] / block_size): the entries in use
+ * A fresh pool has every count and length at 0. The page data of a layer's K or V is a
+ * pool [num_blocks, block_size, ...] of page_bytes bytes a page.
+ * One verification step on rows with T_b cached positions: extend the rows to T_b + 1 +
+ * D_b, write the window's K/V, attend, accept, trim the rows to T_b + accept_len[b].
+ *
+ * Every call is asynchronous, allocates nothing and may be captured into a graph. The rows
+ * of a call are checked on the device before anything is changed; a call that fails a
+ * check changes nothing and sets the workspace flag (sv_workspace_status:
+ * SV_ERR_DEVICE_SHAPE). A row may stand in a call once only. An entry in use that names
+ * no page of the pool, or a free one, means that the state was damaged before the call:
+ * it is reported, and no memory outside the arrays is touched, but the call's effect on
+ * the other entries is then unspecified (spec_pages_compact changes nothing).
+ */
+typedef struct {
+  int32_t num_blocks;         /* pages of the pool, >= 1; times block_size <= 2^31 - 1025 */
+  int32_t block_size;         /* positions per page: a power of two in [8, 65536] */
+  int32_t table_rows;         /* rows of block_table and cached_len, >= 0 */
+  int32_t max_blocks_per_seq; /* entries of a row, >= 1 */
+  int32_t* ref_count;         /* [num_blocks], 16-byte aligned */
+  int32_t* block_table;       /* [table_rows, max_blocks_per_seq], row-major */
+  int32_t* cached_len;        /* [table_rows] */
+} sv_page_table;
+
+/* One pool of page data: page p is the page_bytes bytes from base + p * page_bytes. */
+typedef struct {
+  void* base;          /* device memory, 16-byte aligned */
+  int64_t page_bytes;  /* a multiple of 16 * block_size, <= 2^30 */
+} sv_page_data;
+
+#define SV_MAX_PAGE_POOLS 256
+
+/* Bytes of workspace the spec_pages_ calls need. 0 if invalid. */
+SV_API size_t spec_pages_workspace_size(int32_t num_blocks, int32_t table_rows);
+
+/*
+ * spec_pages_fork -- rows that begin as copies of others, without copying page data.
+ * For i < n: row children[i] (unused: cached_len 0) gets the first
+ * ceil(len / block_size) entries of row parents[i], each of these pages' counts grows by
+ * one, and cached_len[children[i]] = len, where len = fork_len[i], or the parent's length
+ * if fork_len is NULL. 0 <= fork_len[i] <= the parent's length. A parent may have any
+ * number of children; a row that is a child in the call is no parent in it. Entries of the
+ * children past those are left as they were. A page shared in part is parted on the next
+ * spec_pages_extend of its rows.
+ *   parents, children  int32 [n], rows of the table; 0 <= n <= table_rows
+ *   fork_len           int32 [n] or NULL
+ */
+SV_API sv_status spec_pages_fork(const sv_page_table* table, int32_t n, const int32_t* parents,
+                                 const int32_t* children, const int32_t* fork_len,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * spec_pages_extend -- makes positions cached_len[r] .. new_len[i] - 1 of row r = rows[i]
+ * writable. As if row after row, in the order of the call, and with the free pages taken
+ * lowest first:
+ *   - if the row grows and its last page is partly filled and named by another entry too,
+ *     the row takes a free page, the filled positions' data is copied to it in every pool
+ *     (copy on write; the rest of the page is left as it was), and the shared page's count
+ *     falls by one;
+ *   - the row takes free pages for its entries up to ceil(new_len[i] / block_size);
+ *   - cached_len[r] = new_len[i] (>= cached_len[r], <= max_blocks_per_seq * block_size).
+ * Pages that were free before the call only: the pool must have enough of them, or the
+ * call changes nothing and sv_workspace_status reports SV_ERR_NO_PAGES.
+ *   rows     int32 [n], or NULL: rows 0 .. n - 1; 0 <= n <= table_rows
+ *   new_len  int32 [n]
+ *   pools    HOST array of num_pools pools (0 .. SV_MAX_PAGE_POOLS; K and V of each layer);
+ *            read during the call only. The pools must not overlap.
+ */
+SV_API sv_status spec_pages_extend(const sv_page_table* table, int32_t n, const int32_t* rows,
+                                   const int32_t* new_len, int32_t num_pools,
+                                   const sv_page_data* pools, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * spec_pages_trim -- gives positions back: after a rejection (new_len = T_b +
+ * accept_len[b]), or a whole row (0). For r = rows[i]: the counts of the pages at entries
+ * ceil(new_len[i] / block_size) .. ceil(cached_len[r] / block_size) - 1 fall by one (at 0
+ * a page is free), these entries become -1, and cached_len[r] = new_len[i], 0 <=
+ * new_len[i] <= cached_len[r].
+ *   rows     int32 [n], or NULL: rows 0 .. n - 1; 0 <= n <= table_rows
+ *   new_len  int32 [n]
+ */
+SV_API sv_status spec_pages_trim(const sv_page_table* table, int32_t n, const int32_t* rows,
+                                 const int32_t* new_len, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * spec_pages_compact -- moves the pages in use to the front of the pool: with L of them,
+ * the k-th (in ascending order) at or above L moves to the k-th free page below L, in every
+ * pool, with its count; every entry in use of every row follows. Pages L .. num_blocks - 1
+ * are free afterwards (their data is left as it was).
+ *   pools     HOST array of num_pools pools, as for spec_pages_extend
+ *   remap     int32 [num_blocks] or NULL: out, the page that page p is now, -1 if p was free
+ *   num_live  int32 [1] or NULL: out, L
+ */
+SV_API sv_status spec_pages_compact(const sv_page_table* table, int32_t num_pools,
+                                    const sv_page_data* pools, int32_t* remap, int32_t* num_live,
+                                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace spec_accept needs on the current CUDA device. 0 if invalid. */
 SV_API size_t spec_accept_workspace_size(int32_t batch, int32_t max_draft_len, int32_t vocab);
@@ -355,7 +464,8 @@ SV_API sv_status sv_plan_preview(const sv_attn_desc* desc, int32_t block_size,
                                  int32_t capacity_units);
 
 /* Synchronises `stream`, then reads the sticky device-side flags of a workspace used by
- * either call: SV_OK, SV_ERR_DEVICE_SHAPE or SV_ERR_TIMEOUT. clear != 0 resets them. */
+ * any call: SV_OK, SV_ERR_TIMEOUT, SV_ERR_DEVICE_SHAPE or SV_ERR_NO_PAGES (the first of
+ * these that holds). clear != 0 resets them. */
 SV_API sv_status sv_workspace_status(void* workspace, int clear, void* stream);
 
 /* Human-readable name of a status code (static string). */

@@ -9,6 +9,8 @@ include/specverify.h:
 * ``spec_verify_attn_paged`` -- the same over a paged cache (block pool + block table).
 * ``spec_verify_attn_host_lengths`` -- the same with host copies of the lengths (plan on
   the host, no planning kernel).
+* ``spec_pages_fork``, ``spec_pages_extend``, ``spec_pages_trim``, ``spec_pages_compact`` --
+  the block tables and pages of a paged cache (shared pages, copy on write).
 * ``spec_accept`` -- greedy acceptance (argmax per window row, first mismatch).
 * ``spec_accept_stochastic`` -- distribution-preserving acceptance for sampled decoding.
 """
@@ -28,7 +30,7 @@ LIB_PATH = os.path.join(_HERE, "libspecverify.so")
 SV_BF16, SV_FP8_E4M3, SV_FP32 = 0, 1, 2
 STATUS = {0: "SV_OK", 1: "SV_ERR_NULL", 2: "SV_ERR_SHAPE", 3: "SV_ERR_DTYPE",
           4: "SV_ERR_ALIGN", 5: "SV_ERR_WORKSPACE", 6: "SV_ERR_CUDA", 7: "SV_ERR_TIMEOUT",
-          8: "SV_ERR_DEVICE_SHAPE"}
+          8: "SV_ERR_DEVICE_SHAPE", 9: "SV_ERR_NO_PAGES"}
 EXPORTS = ("spec_verify_attn_workspace_size", "spec_verify_attn", "spec_verify_attn_paged",
            "spec_verify_attn_host_lengths",
            "spec_accept_workspace_size",
@@ -38,7 +40,9 @@ EXPORTS = ("spec_verify_attn_workspace_size", "spec_verify_attn", "spec_verify_a
            "sv_inject_launch_failure", "sv_inject_wait_timeout", "sv_set_row_pairs",
            "sv_row_pair_mode", "sv_set_kv_rings",
            "spec_accept_stochastic_workspace_size",
-           "spec_accept_stochastic")
+           "spec_accept_stochastic",
+           "spec_pages_workspace_size", "spec_pages_fork", "spec_pages_extend",
+           "spec_pages_trim", "spec_pages_compact")
 
 
 class SpecVerifyError(RuntimeError):
@@ -61,6 +65,19 @@ class AttnDesc(ctypes.Structure):
                 ("kv_dtype", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
                 ("sliding_window", ctypes.c_int32)]
 
+
+class PageTable(ctypes.Structure):
+    _fields_ = [("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("table_rows", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32),
+                ("ref_count", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("cached_len", ctypes.c_void_p)]
+
+
+class PageData(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64)]
+
+
+MAX_PAGE_POOLS = 256
 
 _lock = threading.Lock()
 _lib = None
@@ -116,6 +133,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.spec_accept_stochastic.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp,
                                                ctypes.c_float, vp, vp, vp, sz, vp]
         lib.spec_accept_stochastic.restype = ctypes.c_int
+        pt = ctypes.POINTER(PageTable)
+        lib.spec_pages_workspace_size.argtypes = [i32, i32]
+        lib.spec_pages_workspace_size.restype = sz
+        lib.spec_pages_fork.argtypes = [pt, i32, vp, vp, vp, vp, sz, vp]
+        lib.spec_pages_fork.restype = ctypes.c_int
+        lib.spec_pages_extend.argtypes = [pt, i32, vp, vp, i32, vp, vp, sz, vp]
+        lib.spec_pages_extend.restype = ctypes.c_int
+        lib.spec_pages_trim.argtypes = [pt, i32, vp, vp, vp, sz, vp]
+        lib.spec_pages_trim.restype = ctypes.c_int
+        lib.spec_pages_compact.argtypes = [pt, i32, vp, vp, vp, vp, sz, vp]
+        lib.spec_pages_compact.restype = ctypes.c_int
         lib.sv_inject_launch_failure.argtypes = [ctypes.c_int]
         lib.sv_inject_launch_failure.restype = ctypes.c_int
         lib.sv_inject_wait_timeout.argtypes = [ctypes.c_int64]
@@ -306,6 +334,161 @@ def spec_verify_attn_paged(q, k_pages, v_pages, block_table, seq_lens, draft_len
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "spec_verify_attn_paged")
     return out
+
+
+def _here(device, **tensors):
+    """Every tensor given lies on `device`, and it is the current one: a launch goes to the
+    current device's stream."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError("%s lies on %s, the call's tensors on %s" % (name, t.device, device))
+    if device.index != torch.cuda.current_device():
+        raise ValueError("the tensors lie on %s, the current device is cuda:%d"
+                         % (device, torch.cuda.current_device()))
+
+
+class PagePools:
+    """The pools of page data that spec_pages_extend and spec_pages_compact move pages in:
+    contiguous CUDA tensors [num_blocks, block_size, ...] (K and V of each layer). Build it
+    once and pass it to every call; it keeps the tensors alive."""
+
+    def __init__(self, tensors):
+        self.tensors = tuple(tensors)
+        if len(self.tensors) > MAX_PAGE_POOLS:
+            raise ValueError("at most %d pools" % MAX_PAGE_POOLS)
+        spans = []
+        for t in self.tensors:
+            if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                raise TypeError("a pool must be a CUDA tensor")
+            if t.dim() < 2 or not t.is_contiguous() or t.numel() == 0:
+                raise ValueError("a pool must be contiguous, [num_blocks, block_size, ...]")
+            if t.shape[:2] != self.tensors[0].shape[:2] or t.device != self.tensors[0].device:
+                raise ValueError("the pools must have the same pages, on one device")
+            spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()))
+        spans.sort()
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("the pools must not overlap")
+        self.array = (PageData * len(self.tensors))(*[
+            PageData(t.data_ptr(), t.numel() // t.shape[0] * t.element_size())
+            for t in self.tensors])
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def page_pools(tensors) -> PagePools:
+    """The handle of the pools of page data (see PagePools)."""
+    return PagePools(tensors)
+
+
+def pages_workspace_bytes(num_blocks: int, table_rows: int) -> int:
+    n = load_library().spec_pages_workspace_size(num_blocks, table_rows)
+    if n == 0:
+        raise SpecVerifyError(2, "spec_pages_workspace_size")
+    return n
+
+
+_I32 = (torch.int32,)
+
+
+def _page_table(ref_count, block_table, cached_len, block_size, lists, pools, workspace):
+    """The C descriptor of the pages' state, after the checks; (table, workspace)."""
+    for t, n in ((ref_count, "ref_count"), (block_table, "block_table"),
+                 (cached_len, "cached_len")):
+        _need(t, n, _I32)
+    if ref_count.dim() != 1 or cached_len.dim() != 1 or block_table.dim() != 2 or \
+            block_table.shape[0] != cached_len.shape[0]:
+        raise ValueError("ref_count must be [num_blocks], cached_len [rows], block_table "
+                         "[rows, max_blocks]")
+    n = None
+    for name, t in lists.items():
+        if t is None:
+            continue
+        _need(t, name, _I32)
+        if t.dim() != 1 or (n is not None and t.shape[0] != n):
+            raise ValueError("the call's lists must be one-dimensional and of one length")
+        n = t.shape[0]
+    dev = ref_count.device
+    _here(dev, block_table=block_table, cached_len=cached_len, **lists)
+    if pools is not None and len(pools):
+        if pools.tensors[0].device != dev:
+            raise ValueError("the pools lie on %s, the state on %s" % (pools.tensors[0].device, dev))
+        if tuple(pools.tensors[0].shape[:2]) != (ref_count.shape[0], block_size):
+            raise ValueError("a pool must be [num_blocks, block_size, ...] of the state's pages")
+    if workspace is None:
+        workspace = new_workspace(pages_workspace_bytes(ref_count.shape[0], cached_len.shape[0]),
+                                  dev)
+    _need(workspace, "workspace", (torch.uint8,))
+    _here(dev, workspace=workspace)
+    return PageTable(ref_count.shape[0], block_size, cached_len.shape[0], block_table.shape[1],
+                     ref_count.data_ptr(), block_table.data_ptr(),
+                     cached_len.data_ptr()), workspace
+
+
+def _as_pools(pools) -> PagePools:
+    return pools if isinstance(pools, PagePools) else PagePools(pools)
+
+
+def spec_pages_fork(ref_count, block_table, cached_len, parents, children, *, block_size: int,
+                    fork_len=None, workspace=None, stream=None) -> None:
+    """Rows ``children`` (unused so far) begin as copies of rows ``parents`` (int32 [n] each),
+    of their first ``fork_len`` (int32 [n]) positions or whole: the same pages, each counted
+    once more; no page data moves. State, changed in place: ref_count int32 [num_blocks],
+    block_table int32 [rows, max_blocks], cached_len int32 [rows]."""
+    t, ws = _page_table(ref_count, block_table, cached_len, block_size,
+                        dict(parents=parents, children=children, fork_len=fork_len), None,
+                        workspace)
+    st = load_library().spec_pages_fork(
+        ctypes.byref(t), parents.shape[0], _ptr(parents), _ptr(children), _ptr(fork_len),
+        _ptr(ws), ws.numel(), _stream(stream))
+    _check(st, "spec_pages_fork")
+
+
+def spec_pages_extend(ref_count, block_table, cached_len, rows, new_len, *, block_size: int,
+                      pools=(), workspace=None, stream=None) -> None:
+    """Make positions cached_len[r] .. new_len[i] - 1 of row r = rows[i] writable (``rows``
+    None: rows 0 .. n - 1): a shared partial last page is parted from first (its filled
+    positions copied in every pool), then free pages are taken, lowest first. ``pools``: a
+    PagePools (``page_pools``) or a list of pool tensors. Too few free pages: nothing
+    changes and ``workspace_status`` returns 9 (SV_ERR_NO_PAGES)."""
+    pools = _as_pools(pools)
+    t, ws = _page_table(ref_count, block_table, cached_len, block_size,
+                        dict(new_len=new_len, rows=rows), pools, workspace)
+    st = load_library().spec_pages_extend(
+        ctypes.byref(t), new_len.shape[0], _ptr(rows), _ptr(new_len), len(pools), pools.array,
+        _ptr(ws), ws.numel(), _stream(stream))
+    _check(st, "spec_pages_extend")
+
+
+def spec_pages_trim(ref_count, block_table, cached_len, rows, new_len, *, block_size: int,
+                    workspace=None, stream=None) -> None:
+    """Give back the positions of row r = rows[i] from new_len[i] on (``rows`` None: rows
+    0 .. n - 1): the pages past them lose a count, and their entries become -1."""
+    t, ws = _page_table(ref_count, block_table, cached_len, block_size,
+                        dict(new_len=new_len, rows=rows), None, workspace)
+    st = load_library().spec_pages_trim(
+        ctypes.byref(t), new_len.shape[0], _ptr(rows), _ptr(new_len), _ptr(ws), ws.numel(),
+        _stream(stream))
+    _check(st, "spec_pages_trim")
+
+
+def spec_pages_compact(ref_count, block_table, cached_len, *, block_size: int, pools=(),
+                       remap=None, num_live=None, workspace=None, stream=None) -> None:
+    """Move the L pages in use to pages 0 .. L - 1 in every pool, with their counts, and let
+    every row's entries follow. Fills ``remap`` (int32 [num_blocks]: the new page of each
+    page, -1 if it was free) and ``num_live`` (int32 [1]: L) when they are given."""
+    pools = _as_pools(pools)
+    t, ws = _page_table(ref_count, block_table, cached_len, block_size, {}, pools, workspace)
+    for o, name, n in ((remap, "remap", ref_count.shape[0]), (num_live, "num_live", 1)):
+        if o is not None:
+            _need(o, name, _I32)
+            if o.numel() != n:
+                raise ValueError("%s must hold %d values" % (name, n))
+    _here(ref_count.device, remap=remap, num_live=num_live)
+    st = load_library().spec_pages_compact(
+        ctypes.byref(t), len(pools), pools.array, _ptr(remap), _ptr(num_live), _ptr(ws),
+        ws.numel(), _stream(stream))
+    _check(st, "spec_pages_compact")
 
 
 def spec_accept(logits, draft_tokens, draft_len, *, max_draft_len: int, accept_len=None,

@@ -130,6 +130,7 @@ SV_API const char* sv_status_string(sv_status s) {
     case SV_ERR_CUDA: return "CUDA error";
     case SV_ERR_TIMEOUT: return "device-side wait timed out";
     case SV_ERR_DEVICE_SHAPE: return "device-side length check failed";
+    case SV_ERR_NO_PAGES: return "too few free pages";
   }
   return "unknown status";
 }
@@ -427,6 +428,114 @@ SV_API int sv_row_pair_mode(const sv_attn_desc* desc, int32_t block_size, int32_
   return use_row_pairs(p, desc->kv_dtype == SV_FP8_E4M3, attn_kernel, num_sms) ? 1 : 0;
 }
 
+}  // extern "C"
+
+namespace {
+
+bool pool_sizes_ok(int32_t num_blocks, int32_t block_size) {
+  return block_size >= 8 && block_size <= (1 << 16) && (block_size & (block_size - 1)) == 0 &&
+         num_blocks >= 1 && num_blocks <= MAX_KV_ROWS / block_size;
+}
+
+// The checks that the spec_pages_ calls share. `n`: rows of the call (null lists allowed
+// where they have a meaning are checked by the caller).
+sv_status check_pages(const sv_page_table* t, int32_t n, const void* ws, size_t ws_bytes) {
+  if (!t) return SV_ERR_NULL;
+  if (!pool_sizes_ok(t->num_blocks, t->block_size) || t->table_rows < 0 ||
+      t->max_blocks_per_seq < 1 || n < 0 || n > t->table_rows)
+    return SV_ERR_SHAPE;
+  if (!t->ref_count || (t->table_rows > 0 && (!t->block_table || !t->cached_len)) || !ws)
+    return SV_ERR_NULL;
+  if (!aligned(t->ref_count, 16) || !aligned(t->block_table, 4) || !aligned(t->cached_len, 4) ||
+      !aligned(ws, 256))
+    return SV_ERR_ALIGN;
+  return ws_bytes < pages_ws_bytes(t->num_blocks, t->table_rows) ? SV_ERR_WORKSPACE : SV_OK;
+}
+
+sv_status check_pools(const sv_page_table* t, int32_t num_pools, const sv_page_data* pools) {
+  if (num_pools < 0 || num_pools > SV_MAX_PAGE_POOLS) return SV_ERR_SHAPE;
+  if (num_pools > 0 && !pools) return SV_ERR_NULL;
+  for (int i = 0; i < num_pools; ++i) {
+    if (!pools[i].base) return SV_ERR_NULL;
+    if (pools[i].page_bytes < 1 || pools[i].page_bytes > (1 << 30) ||
+        pools[i].page_bytes % (16 * (int64_t)t->block_size) != 0)
+      return SV_ERR_SHAPE;
+    if (!aligned(pools[i].base, 16)) return SV_ERR_ALIGN;
+  }
+  return SV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+SV_API size_t spec_pages_workspace_size(int32_t num_blocks, int32_t table_rows) {
+  if (!pool_sizes_ok(num_blocks, 8) || table_rows < 0) return 0;
+  return pages_ws_bytes(num_blocks, table_rows);
+}
+
+SV_API sv_status spec_pages_fork(const sv_page_table* table, int32_t n, const int32_t* parents,
+                                 const int32_t* children, const int32_t* fork_len,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  const sv_status st = check_pages(table, n, workspace, workspace_bytes);
+  if (st != SV_OK || n == 0) return st;
+  if (!parents || !children) return SV_ERR_NULL;
+  if (!aligned(parents, 4) || !aligned(children, 4) || !aligned(fork_len, 4)) return SV_ERR_ALIGN;
+  const int sms = current_sms();
+  if (sms <= 0) return SV_ERR_CUDA;
+  return launch_pages_fork(*table, n, parents, children, fork_len, workspace, sms,
+                           (cudaStream_t)stream) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
+SV_API sv_status spec_pages_extend(const sv_page_table* table, int32_t n, const int32_t* rows,
+                                   const int32_t* new_len, int32_t num_pools,
+                                   const sv_page_data* pools, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  sv_status st = check_pages(table, n, workspace, workspace_bytes);
+  if (st == SV_OK) st = check_pools(table, num_pools, pools);
+  if (st != SV_OK || n == 0) return st;
+  if (!new_len) return SV_ERR_NULL;
+  if (!aligned(rows, 4) || !aligned(new_len, 4)) return SV_ERR_ALIGN;
+  const int sms = current_sms();
+  if (sms <= 0) return SV_ERR_CUDA;
+  return launch_pages_extend(*table, n, rows, new_len, num_pools, pools, workspace, sms,
+                             (cudaStream_t)stream) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
+SV_API sv_status spec_pages_trim(const sv_page_table* table, int32_t n, const int32_t* rows,
+                                 const int32_t* new_len, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  const sv_status st = check_pages(table, n, workspace, workspace_bytes);
+  if (st != SV_OK || n == 0) return st;
+  if (!new_len) return SV_ERR_NULL;
+  if (!aligned(rows, 4) || !aligned(new_len, 4)) return SV_ERR_ALIGN;
+  const int sms = current_sms();
+  if (sms <= 0) return SV_ERR_CUDA;
+  return launch_pages_trim(*table, n, rows, new_len, workspace, sms, (cudaStream_t)stream) ==
+                 cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
+SV_API sv_status spec_pages_compact(const sv_page_table* table, int32_t num_pools,
+                                    const sv_page_data* pools, int32_t* remap, int32_t* num_live,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  sv_status st = check_pages(table, 0, workspace, workspace_bytes);
+  if (st == SV_OK) st = check_pools(table, num_pools, pools);
+  if (st != SV_OK) return st;
+  if (!aligned(remap, 4) || !aligned(num_live, 4)) return SV_ERR_ALIGN;
+  const int sms = current_sms();
+  if (sms <= 0) return SV_ERR_CUDA;
+  return launch_pages_compact(*table, num_pools, pools, remap, num_live, workspace, sms,
+                              (cudaStream_t)stream) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
 SV_API size_t spec_accept_workspace_size(int32_t batch, int32_t max_draft_len, int32_t vocab) {
   if (batch < 0 || max_draft_len < 0 || max_draft_len > 255 || vocab <= 0) return 0;
   const int sms = current_sms();
@@ -532,7 +641,8 @@ SV_API sv_status sv_workspace_status(void* workspace, int clear, void* stream) {
   if (clear && cudaMemsetAsync(workspace, 0, sizeof flags, s) != cudaSuccess) return SV_ERR_CUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return SV_ERR_CUDA;
   if (flags & FLAG_TIMEOUT) return SV_ERR_TIMEOUT;
-  if (flags & (FLAG_ATTN_SHAPE | FLAG_ACCEPT_SHAPE)) return SV_ERR_DEVICE_SHAPE;
+  if (flags & (FLAG_ATTN_SHAPE | FLAG_ACCEPT_SHAPE | FLAG_PAGES_SHAPE)) return SV_ERR_DEVICE_SHAPE;
+  if (flags & FLAG_NO_PAGES) return SV_ERR_NO_PAGES;
   return SV_OK;
 }
 

@@ -46,6 +46,8 @@ namespace sv {
 constexpr uint32_t FLAG_ATTN_SHAPE = 1u;
 constexpr uint32_t FLAG_TIMEOUT = 2u;
 constexpr uint32_t FLAG_ACCEPT_SHAPE = 4u;
+constexpr uint32_t FLAG_PAGES_SHAPE = 8u;
+constexpr uint32_t FLAG_NO_PAGES = 16u;
 
 constexpr int MT = 128;  // query rows per unit (one tensor-core M tile)
 
@@ -253,6 +255,21 @@ cudaError_t launch_accept_stochastic(int B, int max_draft, int vocab, int dtype,
                                      const float* u_accept, const float* u_sample,
                                      float inv_temp, int32_t* accept_len, int32_t* next_token,
                                      void* ws, cudaStream_t s);
+
+// Pages of a paged cache (pages.cu). Workspace: the flag word, a ticket that every call
+// leaves at zero, and scratch that is written before it is read in each call.
+size_t pages_ws_bytes(int32_t num_blocks, int32_t table_rows);
+cudaError_t launch_pages_fork(const sv_page_table& t, int n, const int32_t* parents,
+                              const int32_t* children, const int32_t* fork_len, void* ws, int sms,
+                              cudaStream_t s);
+cudaError_t launch_pages_extend(const sv_page_table& t, int n, const int32_t* rows,
+                                const int32_t* new_len, int num_pools, const sv_page_data* pools,
+                                void* ws, int sms, cudaStream_t s);
+cudaError_t launch_pages_trim(const sv_page_table& t, int n, const int32_t* rows,
+                              const int32_t* new_len, void* ws, int sms, cudaStream_t s);
+cudaError_t launch_pages_compact(const sv_page_table& t, int num_pools, const sv_page_data* pools,
+                                 int32_t* remap, int32_t* num_live, void* ws, int sms,
+                                 cudaStream_t s);
 
 // Draft signals.
 struct SigWs {

@@ -1,0 +1,379 @@
+"""GPU tests of the page operators (fork, extend with copy on write, trim, compact) against
+the plain model: whole numbers and moved bits, so everything is compared for equality."""
+import random
+
+import pytest
+import torch
+
+import speculative_decoding_verification_gqa_gb300 as sv
+
+from gpu_util import ensure_built
+from page_model import Pages, pages_of
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+class Device:
+    """The model's state on the device; the data of page position (p, j) is a number that
+    stands in every pool (with the pool's index added)."""
+
+    def __init__(self, m, pools=2, width=8, dtype=torch.int32):
+        ensure_built()
+        self.m, nb, bs = m, len(m.ref), m.bs
+        self.ref = torch.tensor(m.ref, dtype=torch.int32, device=DEV)
+        self.lens = torch.tensor(m.lens, dtype=torch.int32, device=DEV)
+        self.table = torch.tensor(m.table, dtype=torch.int32, device=DEV)
+        ident = torch.arange(nb * bs, dtype=torch.int32, device=DEV).view(nb, bs, 1)
+        self.pools = [(ident + 1000000 * k).expand(nb, bs, width).contiguous().to(dtype)
+                      for k in range(pools)]
+        m.data = [[p * bs + j for j in range(bs)] for p in range(nb)]
+        self.handle = sv.page_pools(self.pools)
+        self.ws = sv.new_workspace(sv.pages_workspace_bytes(nb, len(m.lens)))
+
+    def i32(self, v):
+        return None if v is None else torch.tensor(v, dtype=torch.int32, device=DEV)
+
+    def fork(self, p, c, n=None):
+        sv.spec_pages_fork(self.ref, self.table, self.lens, self.i32(p), self.i32(c),
+                           fork_len=self.i32(n), block_size=self.m.bs, workspace=self.ws)
+
+    def extend(self, rows, n):
+        sv.spec_pages_extend(self.ref, self.table, self.lens, self.i32(rows), self.i32(n),
+                             block_size=self.m.bs, pools=self.handle, workspace=self.ws)
+
+    def trim(self, rows, n):
+        sv.spec_pages_trim(self.ref, self.table, self.lens, self.i32(rows), self.i32(n),
+                           block_size=self.m.bs, workspace=self.ws)
+
+    def compact(self):
+        remap = torch.full_like(self.ref, -7)
+        live = torch.full((1,), -7, dtype=torch.int32, device=DEV)
+        sv.spec_pages_compact(self.ref, self.table, self.lens, block_size=self.m.bs,
+                              pools=self.handle, remap=remap, num_live=live, workspace=self.ws)
+        return remap.tolist(), int(live)
+
+    def status(self):
+        return sv.workspace_status(self.ws, clear=True)
+
+    def same(self, data=True):
+        m = self.m
+        assert self.ref.tolist() == m.ref
+        assert self.lens.tolist() == m.lens
+        assert self.table.tolist() == m.table
+        if data:
+            want = torch.tensor(m.data, dtype=torch.int64)
+            for k, p in enumerate(self.pools):
+                assert bool((p.cpu().long() == (want + 1000000 * k)[..., None]).all()), "pool %d" % k
+
+
+def filled(rows, blocks, bs, lens, max_blocks=None, seed=0):
+    """A state in which row r holds lens[r] positions on pages placed at random."""
+    m = Pages(blocks, rows, max_blocks or max(1, max(pages_of(n, bs) for n in lens) + 2), bs)
+    ids = list(range(blocks))
+    random.Random(seed).shuffle(ids)
+    for r, n in enumerate(lens):
+        for j in range(pages_of(n, bs)):
+            p = ids.pop()
+            m.table[r][j], m.ref[p] = p, 1
+        m.lens[r] = n
+    return m
+
+
+@pytest.mark.parametrize("bs", [8, 16, 64])
+@pytest.mark.parametrize("seed", range(4))
+def test_random_life_of_a_pool(bs, seed):
+    """A hundred calls of all four operators on ragged batches, each compared with the model:
+    state, page data, and the too-few-pages answer."""
+    rng = random.Random(100 * bs + seed)
+    R, nb, mb = 12, 60, 9
+    m = Pages(nb, R, mb, bs)
+    d = Device(m, pools=3)
+    full = 0
+    for _ in range(100):
+        op = rng.choice(["fork", "extend", "extend", "extend", "trim", "compact"])
+        if op == "fork":
+            empty = [r for r in range(R) if m.lens[r] == 0]
+            par = [r for r in range(R) if m.lens[r] > 0]
+            ch = rng.sample(empty, rng.randint(0, len(empty)))
+            if not par or not ch:
+                continue
+            ps = [rng.choice(par) for _ in ch]
+            n = None if rng.random() < 0.4 else [rng.randint(0, m.lens[p]) for p in ps]
+            d.fork(ps, ch, n)
+            m.fork(ps, ch, n)
+            assert d.status() == 0
+        elif op == "compact":
+            assert d.compact() == m.compact()
+            assert d.status() == 0
+        else:
+            rows = rng.sample(range(R), rng.randint(1, R))
+            if rng.random() < 0.3:
+                rows = list(range(len(rows)))
+            as_null = rows == list(range(len(rows)))
+            if op == "extend":
+                n = [rng.choice([m.lens[r], min(mb * bs, m.lens[r] + rng.randint(0, 3 * bs))]) for r in rows]
+                d.extend(None if as_null else rows, n)
+                ok = m.extend(rows, n)
+                assert d.status() == (0 if ok else 9)
+                full += not ok
+            else:
+                n = [rng.choice([m.lens[r], rng.randint(0, m.lens[r]), 0]) for r in rows]
+                d.trim(None if as_null else rows, n)
+                m.trim(rows, n)
+                assert d.status() == 0
+        m.check()
+        d.same()
+
+
+@pytest.mark.parametrize("family,share_outside", [(2, 0), (5, 0), (5, 1)])
+def test_copy_on_write_leaves_the_last_holder_in_place(family, share_outside):
+    """All holders of a partial page in one call: every row but the last of the call takes a
+    copy; with a holder outside the call all rows of the call take one."""
+    bs, n = 16, 37
+    m = filled(family + share_outside, 40, bs, [n] + [0] * (family + share_outside - 1))
+    kids = list(range(1, family + share_outside))
+    d = Device(m)
+    d.fork([0] * len(kids), kids)
+    m.fork([0] * len(kids), kids)
+    rows = list(range(family))[::-1]
+    d.extend(rows, [n + 1 + r for r in rows])
+    assert m.extend(rows, [n + 1 + r for r in rows])
+    d.same()
+    shared = m.table[0][2]
+    assert (shared in [m.table[r][2] for r in range(1, family)]) is False
+    assert m.ref[shared] == 1
+    if share_outside:
+        assert m.table[family][2] != shared
+
+
+def test_many_rows_and_pages_span_chunks():
+    """More rows than one block of the planning kernel has threads, and a pool of several
+    counting chunks with pages taken and moved across their borders."""
+    bs, R, nb = 8, 2500, 13001
+    lens = [(7 * r) % 33 for r in range(R)]
+    m = filled(R, nb, bs, lens, max_blocks=9, seed=4)
+    d = Device(m, pools=1, width=4)
+    rows = list(range(R))
+    random.Random(1).shuffle(rows)
+    to = [lens[r] + (r % 17) for r in rows]
+    d.extend(rows, to)
+    assert m.extend(rows, to)
+    d.same()
+    rows = rows[:2100]
+    to = [m.lens[r] // 2 for r in rows]
+    d.trim(rows, to)
+    m.trim(rows, to)
+    assert d.compact() == m.compact()
+    assert d.status() == 0
+    d.same()
+
+
+@pytest.mark.parametrize("children", [1, 7, 8, 9, 31])
+def test_fork_many_children_across_table_segments(children):
+    bs, n = 8, 8 * 1100 + 3
+    m = filled(2 + 2 * children, 2300, bs, [n, n - 900] + [0] * (2 * children), seed=2)
+    d = Device(m, pools=1, width=4)
+    kids = list(range(2, 2 + 2 * children))
+    par = [k % 2 for k in kids] if children % 2 else [k >= 2 + children for k in kids]
+    par = [int(p) for p in par]
+    length = [(313 * k) % (m.lens[p] + 1) for k, p in zip(kids, par)]
+    d.fork(par, kids, length)
+    m.fork(par, kids, length)
+    assert d.status() == 0
+    d.same(data=False)
+
+
+@pytest.mark.parametrize("page_bytes_per_pos", [16, 48, 4096])
+def test_page_sizes(page_bytes_per_pos):
+    """Pages below, above and off the copying granule."""
+    bs = 32
+    m = filled(4, 64, bs, [100, 0, 33, 64], seed=9)
+    d = Device(m, pools=2, width=page_bytes_per_pos // 4)
+    d.fork([0], [1])
+    m.fork([0], [1])
+    d.extend([1, 0, 2], [101, 130, 34])
+    assert m.extend([1, 0, 2], [101, 130, 34])
+    d.same()
+    assert d.compact() == m.compact()
+    d.same()
+
+
+def test_pool_used_up_exactly_and_by_one_page_too_many():
+    bs = 8
+    m = filled(3, 10, bs, [8, 5, 0], max_blocks=12, seed=1)
+    d = Device(m)
+    d.extend([2, 0], [bs * 6, bs * 4])  # nine pages: one too many
+    assert d.status() == 9
+    d.same()
+    d.extend([2, 0], [bs * 5, bs * 4])  # the eight that are free
+    assert m.extend([2, 0], [bs * 5, bs * 4])
+    assert d.status() == 0
+    d.same()
+    d.extend(None, m.lens)  # nothing to take from an empty pool
+    assert d.status() == 0
+    d.extend([1], [9])
+    assert d.status() == 9
+    d.same()
+    assert d.compact() == (list(range(10)), 10)
+    d.same()
+
+
+def test_empty_pool_and_rows():
+    m = Pages(9, 2, 3, 8)
+    d = Device(m)
+    assert d.compact() == ([-1] * 9, 0)
+    d.trim([1], [0])
+    d.fork([0], [1])
+    d.extend([0, 1], [0, 0])
+    assert d.status() == 0
+    d.same()
+
+
+@pytest.mark.parametrize("bad", ["twice", "below", "above", "short", "long"])
+@pytest.mark.parametrize("op", ["extend", "trim"])
+def test_bad_rows_change_nothing(op, bad):
+    bs = 8
+    m = filled(4, 30, bs, [20, 9, 0, 16], max_blocks=6, seed=3)
+    d = Device(m)
+    rows, n = [0, 3, 1], ([25, 16, 10] if op == "extend" else [4, 16, 0])
+    if bad == "twice":
+        rows[2] = 0
+        n[2] = n[0]
+    elif bad == "below":
+        rows[1] = -1
+    elif bad == "above":
+        rows[1] = 4
+    elif bad == "short":
+        n[0] = 19 if op == "extend" else -1
+    else:
+        n[0] = 6 * bs + 1 if op == "extend" else 21
+    getattr(d, op)(rows, n)
+    assert d.status() == 8
+    d.same()
+
+
+@pytest.mark.parametrize("p,c,n", [
+    ([0, 1], [2, 2], None), ([0], [1], None), ([0, 2], [2, 3], None), ([0], [4], None),
+    ([-1], [2], None), ([0], [2], [21]), ([0], [2], [-1])])
+def test_bad_forks_change_nothing(p, c, n):
+    m = filled(4, 30, 8, [20, 9, 0, 0], max_blocks=6, seed=3)
+    d = Device(m)
+    d.fork(p, c, n)
+    assert d.status() == 8
+    d.same()
+
+
+@pytest.mark.parametrize("entry", [-1, 30, 1 << 30])
+def test_damaged_tables_touch_nothing_else(entry):
+    """An entry in use that names no page: reported; compact changes nothing, extend neither
+    where it needs the entry; trim and fork leave every count of other pages right."""
+    m = filled(4, 30, 8, [20, 9, 0, 16], max_blocks=6, seed=3)
+    m.table[0][2] = entry
+    d = Device(m)
+    d.compact()
+    assert d.status() == 8
+    d.same()
+    d.extend([0], [21])
+    assert d.status() == 8
+    d.same()
+    d.fork([0], [2])
+    assert d.status() == 8
+    want = list(m.ref)
+    for j in (0, 1):
+        want[m.table[0][j]] += 1
+    assert d.ref.tolist() == want
+    d.trim([2, 0], [0, 0])
+    assert d.status() == 8
+    for j in (0, 1):
+        want[m.table[0][j]] -= 2
+    assert d.ref.tolist() == want and min(want) >= 0
+
+
+def test_free_page_named_by_a_row():
+    m = filled(2, 20, 8, [20, 9], seed=5)
+    d = Device(m)
+    d.ref[m.table[0][1]] = 0
+    before = d.ref.tolist()
+    d.compact()
+    assert d.status() == 8 and d.ref.tolist() == before
+    d.trim([0], [0])
+    assert d.status() == 8 and min(d.ref.tolist()) == 0
+
+
+def test_graph_replays_a_step_on_its_own_stream():
+    """fork, extend, trim and compact in one captured graph, replayed: the state at the start
+    of every replay is put back, and the results are those of eager calls."""
+    bs = 16
+    m = filled(6, 50, bs, [40, 0, 0, 33, 16, 0], max_blocks=5, seed=7)
+    d = Device(m)
+    first = [t.clone() for t in (d.ref, d.lens, d.table)]
+    par, kids, rows, to, back = d.i32([0, 3]), d.i32([1, 5]), d.i32([1, 0, 5]), d.i32([44, 47, 50]), d.i32([41, 41, 33])
+    live = torch.zeros(1, dtype=torch.int32, device=DEV)
+
+    def step():
+        for t, f in zip((d.ref, d.lens, d.table), first):
+            t.copy_(f)
+        sv.spec_pages_fork(d.ref, d.table, d.lens, par, kids, block_size=bs, workspace=d.ws)
+        sv.spec_pages_extend(d.ref, d.table, d.lens, rows, to, block_size=bs, pools=d.handle, workspace=d.ws)
+        sv.spec_pages_trim(d.ref, d.table, d.lens, rows, back, block_size=bs, workspace=d.ws)
+        sv.spec_pages_compact(d.ref, d.table, d.lens, block_size=bs, pools=d.handle, num_live=live, workspace=d.ws)
+
+    m.fork([0, 3], [1, 5])
+    assert m.extend([1, 0, 5], [44, 47, 50])
+    m.trim([1, 0, 5], [41, 41, 33])
+    _, L = m.compact()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        d.same(data=False)
+        assert int(live) == L
+    assert d.status() == 0
+
+
+@pytest.mark.parametrize("op,launches", [("fork", 2), ("extend", 3), ("trim", 2), ("compact", 3)])
+def test_failed_launch_is_reported_and_the_workspace_serves_on(op, launches):
+    for k in range(launches):
+        m = filled(4, 30, 8, [20, 9, 0, 16], max_blocks=6, seed=3)
+        d = Device(m)
+        args = dict(fork=([0], [2]), extend=([0], [25]), trim=([0], [3]), compact=())[op]
+        sv.api.inject_launch_failure(k)
+        with pytest.raises(sv.SpecVerifyError) as e:
+            getattr(d, op)(*args)
+        assert e.value.status == 6
+        d.same()  # the state changes in the last kernel only
+        getattr(d, op)(*args)
+        getattr(m, op)(*args)
+        assert d.status() == 0
+        d.same()
+
+
+def test_binding_refuses():
+    m = filled(4, 30, 8, [20, 9, 0, 16], max_blocks=6, seed=3)
+    d = Device(m)
+    one = d.i32([0])
+    kw = dict(block_size=8, workspace=d.ws)
+    with pytest.raises(TypeError):
+        sv.spec_pages_trim(d.ref.long(), d.table, d.lens, one, one, **kw)
+    with pytest.raises(ValueError):
+        sv.spec_pages_trim(d.ref, d.table[:, ::2], d.lens, one, one, **kw)
+    with pytest.raises(ValueError):
+        sv.spec_pages_trim(d.ref, d.table, d.lens, one, d.i32([0, 1]), **kw)
+    with pytest.raises(ValueError):
+        sv.spec_pages_extend(d.ref, d.table, d.lens, one, one, pools=[d.pools[0][:5].contiguous()], **kw)
+    with pytest.raises(ValueError):
+        sv.page_pools([d.pools[0], d.pools[0]])
+    with pytest.raises(ValueError):
+        sv.spec_pages_compact(d.ref, d.table, d.lens, remap=one, **kw)
+    with pytest.raises(sv.SpecVerifyError) as e:
+        sv.spec_pages_trim(d.ref, d.table, d.lens, one, one, block_size=8, workspace=d.ws[:256])
+    assert e.value.status == 5
+    d.same()
