@@ -179,6 +179,44 @@ SV_API sv_status spec_verify_attn_paged(const sv_attn_desc* desc, const void* q,
                                  const int32_t* draft_len, const float* kv_scale, void* out,
                                  void* workspace, size_t workspace_bytes, void* stream);
 
+/* Bytes of workspace spec_verify_attn_shared needs on the current CUDA device. 0 if
+ * invalid. */
+SV_API size_t spec_verify_attn_shared_workspace_size(const sv_attn_desc* desc,
+                                                     int32_t num_groups);
+
+/*
+ * spec_verify_attn_shared -- spec_verify_attn_paged for a batch whose sequences share long
+ * prefixes (a common system prompt, samples of one request), which are attended once for
+ * all of their sequences: the rows of a whole group meet each tile of its prefix together,
+ * and the result is joined with that over each sequence's own positions by the rule of the
+ * online softmax. The results are those of spec_verify_attn_paged up to rounding.
+ *
+ * The batch is in num_groups groups of consecutive sequences: group n is sequences
+ * group_begin[n] .. group_begin[n + 1] - 1, and positions 0 .. prefix_len[n] - 1 of all of
+ * them hold the same K/V (such as spec_pages_fork leaves them). Those are read through the
+ * block-table row of the group's first sequence; the other rows' entries for blocks wholly
+ * before prefix_len[n] are not read and may hold anything. Positions from prefix_len[n] on
+ * are read through each sequence's own row, and what a block of another sequence than the
+ * first holds before them is not used.
+ *
+ *   group_begin  int32 [num_groups + 1], from 0 to batch, not decreasing (a group may be
+ *                empty); 1 <= num_groups <= batch
+ *   prefix_len   int32 [num_groups], 0 <= prefix_len[n] <= every seq_lens[b] of the group;
+ *                any number of positions, not only whole blocks. 0: nothing shared
+ * The other arguments are those of spec_verify_attn_paged; desc->sliding_window must be 0.
+ * Group or prefix lengths out of range are reported by sv_workspace_status
+ * (SV_ERR_DEVICE_SHAPE), and the outputs are left as they were.
+ */
+SV_API sv_status spec_verify_attn_shared(const sv_attn_desc* desc, const void* q,
+                                         const void* k_pages, const void* v_pages,
+                                         int64_t num_blocks, int32_t block_size,
+                                         const int32_t* block_table, int32_t max_blocks_per_seq,
+                                         const int32_t* seq_lens, const int32_t* draft_len,
+                                         int32_t num_groups, const int32_t* group_begin,
+                                         const int32_t* prefix_len, const float* kv_scale,
+                                         void* out, void* workspace, size_t workspace_bytes,
+                                         void* stream);
+
 /*
  * Pages of a paged KV cache ("GPU and LLM, chapter 5", "PagedAttention (2)": blocks of a
  * fixed number of positions, found through a per-sequence block table; sequences with a

@@ -9,6 +9,8 @@ include/specverify.h:
 * ``spec_verify_attn_paged`` -- the same over a paged cache (block pool + block table).
 * ``spec_verify_attn_host_lengths`` -- the same with host copies of the lengths (plan on
   the host, no planning kernel).
+* ``spec_verify_attn_shared`` -- the paged call for groups of sequences with a common prefix,
+  attended once per group.
 * ``spec_pages_fork``, ``spec_pages_extend``, ``spec_pages_trim``, ``spec_pages_compact`` --
   the block tables and pages of a paged cache (shared pages, copy on write).
 * ``spec_accept`` -- greedy acceptance (argmax per window row, first mismatch).
@@ -41,6 +43,7 @@ EXPORTS = ("spec_verify_attn_workspace_size", "spec_verify_attn", "spec_verify_a
            "sv_row_pair_mode", "sv_set_kv_rings",
            "spec_accept_stochastic_workspace_size",
            "spec_accept_stochastic",
+           "spec_verify_attn_shared_workspace_size", "spec_verify_attn_shared",
            "spec_pages_workspace_size", "spec_pages_fork", "spec_pages_extend",
            "spec_pages_trim", "spec_pages_compact")
 
@@ -103,6 +106,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.spec_verify_attn_paged.argtypes = [ctypes.POINTER(AttnDesc), vp, vp, vp, i64, i32,
                                                vp, i32, vp, vp, vp, vp, vp, sz, vp]
         lib.spec_verify_attn_paged.restype = ctypes.c_int
+        lib.spec_verify_attn_shared_workspace_size.argtypes = [ctypes.POINTER(AttnDesc), i32]
+        lib.spec_verify_attn_shared_workspace_size.restype = sz
+        lib.spec_verify_attn_shared.argtypes = [ctypes.POINTER(AttnDesc), vp, vp, vp, i64, i32,
+                                                vp, i32, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp]
+        lib.spec_verify_attn_shared.restype = ctypes.c_int
         lib.spec_verify_attn_host_lengths.argtypes = [ctypes.POINTER(AttnDesc), vp, vp, vp, vp,
                                                       vp, vp, vp, vp, vp, vp, sz, vp]
         lib.spec_verify_attn_host_lengths.restype = ctypes.c_int
@@ -345,6 +353,61 @@ def _here(device, **tensors):
     if device.index != torch.cuda.current_device():
         raise ValueError("the tensors lie on %s, the current device is cuda:%d"
                          % (device, torch.cuda.current_device()))
+
+
+def shared_workspace_bytes(desc: AttnDesc, num_groups: int) -> int:
+    n = load_library().spec_verify_attn_shared_workspace_size(ctypes.byref(desc), num_groups)
+    if n == 0:
+        raise SpecVerifyError(2, "spec_verify_attn_shared_workspace_size")
+    return n
+
+
+def spec_verify_attn_shared(q, k_pages, v_pages, block_table, seq_lens, draft_len, group_begin,
+                            prefix_len, *, max_draft_len: int, max_seq_len: int, kv_scale=None,
+                            out=None, workspace=None, softmax_scale: float = 0.0,
+                            stream=None) -> torch.Tensor:
+    """spec_verify_attn_paged for a batch in groups that share a prefix: sequences
+    group_begin[n] .. group_begin[n + 1] - 1 (int32 [groups + 1]) hold the same K/V at
+    positions 0 .. prefix_len[n] - 1 (int32 [groups]), read through the block-table row of
+    the group's first sequence and attended once for all of them."""
+    _need(q, "q", (torch.bfloat16,))
+    _need(k_pages, "k_pages", (torch.bfloat16, torch.uint8, torch.float8_e4m3fn))
+    _need(v_pages, "v_pages", (k_pages.dtype,))
+    for t, n in ((block_table, "block_table"), (seq_lens, "seq_lens"), (draft_len, "draft_len"),
+                 (group_begin, "group_begin"), (prefix_len, "prefix_len")):
+        _need(t, n, _I32)
+    if kv_scale is not None:
+        _need(kv_scale, "kv_scale", (torch.float32,))
+    if q.dim() != 3 or k_pages.dim() != 4 or v_pages.shape != k_pages.shape or \
+            q.shape[2] != k_pages.shape[3]:
+        raise ValueError("q must be [rows, Hq, d], k/v pages [num_blocks, block_size, Hkv, d]")
+    B = seq_lens.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] != B or draft_len.shape != (B,):
+        raise ValueError("block_table must be [B, max_blocks], draft_len [B]")
+    groups = prefix_len.shape[0]
+    if group_begin.shape != (groups + 1,) or prefix_len.dim() != 1:
+        raise ValueError("group_begin must be [groups + 1], prefix_len [groups]")
+    nb, bs, hkv, d = k_pages.shape
+    if kv_scale is not None and kv_scale.shape != (2, hkv):
+        raise ValueError("kv_scale must be [2, Hkv]")
+    desc = attn_desc(q, k_pages.view(nb * bs, hkv, d), B, max_draft_len, max_seq_len, softmax_scale)
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "out", (torch.bfloat16,))
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if workspace is None:
+        workspace = new_workspace(shared_workspace_bytes(desc, groups), q.device)
+    _here(q.device, k_pages=k_pages, v_pages=v_pages, block_table=block_table, seq_lens=seq_lens,
+          draft_len=draft_len, group_begin=group_begin, prefix_len=prefix_len, kv_scale=kv_scale,
+          out=out, workspace=workspace)
+    st = load_library().spec_verify_attn_shared(
+        ctypes.byref(desc), _ptr(q), _ptr(k_pages), _ptr(v_pages), nb, bs, _ptr(block_table),
+        block_table.shape[1], _ptr(seq_lens), _ptr(draft_len), groups, _ptr(group_begin),
+        _ptr(prefix_len), _ptr(kv_scale), _ptr(out), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "spec_verify_attn_shared")
+    return out
 
 
 class PagePools:

@@ -3,6 +3,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "internal.cuh"
@@ -372,6 +373,106 @@ SV_API sv_status spec_verify_attn_paged(const sv_attn_desc* desc, const void* q,
   const PagedArgs pg = {block_table, max_blocks_per_seq, block_size, num_blocks};
   return verify_impl(desc, q, k_pages, v_pages, pg, seq_lens, draft_len, kv_scale, out,
                      workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// Units of 128 query rows that a shared-prefix call may have: the tables of the plan and
+// the partials' slots are indexed with 32 bits.
+constexpr int64_t MAX_SHARED_UNITS = 1 << 22;
+
+sv_status check_shared(const sv_attn_desc* desc, int32_t num_groups) {
+  const sv_status st = check_desc(desc);
+  if (st != SV_OK) return st;
+  if (desc->sliding_window != 0 || num_groups < 1 || num_groups > std::max(desc->batch, 1))
+    return SV_ERR_SHAPE;
+  return shared_ws_layout(desc, num_groups, 0).max_units > MAX_SHARED_UNITS ? SV_ERR_SHAPE : SV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+SV_API size_t spec_verify_attn_shared_workspace_size(const sv_attn_desc* desc, int32_t num_groups) {
+  if (check_shared(desc, num_groups) != SV_OK) return 0;
+  const int sms = current_sms();
+  return sms > 0 ? shared_ws_layout(desc, num_groups, sms).total : 0;
+}
+
+SV_API sv_status spec_verify_attn_shared(const sv_attn_desc* desc, const void* q,
+                                         const void* k_pages, const void* v_pages,
+                                         int64_t num_blocks, int32_t block_size,
+                                         const int32_t* block_table, int32_t max_blocks_per_seq,
+                                         const int32_t* seq_lens, const int32_t* draft_len,
+                                         int32_t num_groups, const int32_t* group_begin,
+                                         const int32_t* prefix_len, const float* kv_scale,
+                                         void* out, void* workspace, size_t workspace_bytes,
+                                         void* stream) {
+  if (block_size < 8 || block_size > (1 << 16) || (block_size & (block_size - 1)) != 0 ||
+      num_blocks < 1 || num_blocks > MAX_KV_ROWS / block_size || max_blocks_per_seq < 1)
+    return SV_ERR_SHAPE;
+  const sv_status st = check_shared(desc, num_groups);
+  if (st != SV_OK || desc->batch == 0) return st;
+  if (!q || !k_pages || !v_pages || !block_table || !seq_lens || !draft_len || !group_begin ||
+      !prefix_len || !out || !workspace)
+    return SV_ERR_NULL;
+  const bool fp8 = desc->kv_dtype == SV_FP8_E4M3;
+  if (fp8 && !kv_scale) return SV_ERR_NULL;
+  if (!fp8 && kv_scale) return SV_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) ||
+      !aligned(workspace, 256) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(draft_len, 4) || !aligned(group_begin, 4) || !aligned(prefix_len, 4) ||
+      !aligned(kv_scale, 4))
+    return SV_ERR_ALIGN;
+  const int sms = current_sms();
+  if (sms <= 0) return SV_ERR_CUDA;
+  const SharedWs lay = shared_ws_layout(desc, num_groups, sms);
+  if (workspace_bytes < lay.total) return SV_ERR_WORKSPACE;
+
+  const int which = pick_kernel(desc);
+  const int kt = which == 2 ? attn_tc_kt() : attn_mma_kt();
+  const PagedArgs pg = {block_table, max_blocks_per_seq, block_size, num_blocks};
+  AttnParams p = shape_params(desc, pg, which, sms);
+  if (which == 2) {  // a pending wait-timeout injection applies to this launch
+    const long long lim = g_stall_limit.exchange(0);
+    if (lim > 0) {
+      p.wait_limit = lim;
+      p.stall_first_tile = 1;
+    }
+  }
+  uint8_t* ws = (uint8_t*)workspace;
+  p.q = q;
+  p.k = k_pages;
+  p.v = v_pages;
+  p.out = out;
+  p.kv_scale = kv_scale;
+  p.seq_lens = seq_lens;
+  p.draft_len = draft_len;
+  p.block_table = block_table;
+  p.num_groups = num_groups;
+  p.group_begin = group_begin;
+  p.prefix_len = prefix_len;
+  p.max_units = (int)lay.max_units;
+  p.n_ctas = sms;
+  p.flags = (uint32_t*)(ws + lay.ctrl);
+  p.hdr = (PlanHdr*)(ws + lay.hdr);
+  p.parts = (SharedSeq*)(ws + lay.parts);
+  p.units = (int4*)(ws + lay.units);
+  p.ubeg = (int32_t*)(ws + lay.ubeg);
+  p.cta_tab = (int2*)(ws + lay.cta_tab);
+  p.part_o = (float*)(ws + lay.part_o);
+  p.part_ml = (float2*)(ws + lay.part_ml);
+
+  cudaStream_t s = (cudaStream_t)stream;
+  if (launch_plan_shared(p, kt, s) != cudaSuccess) return SV_ERR_CUDA;
+  if (g_ev_start && cudaEventRecord(g_ev_start, s) != cudaSuccess) return SV_ERR_CUDA;
+  const cudaError_t e =
+      which == 2 ? launch_attn_tc_shared(p, fp8, s) : launch_attn_mma_shared(p, fp8, s);
+  if (e != cudaSuccess) return SV_ERR_CUDA;
+  if (g_ev_stop && cudaEventRecord(g_ev_stop, s) != cudaSuccess) return SV_ERR_CUDA;
+  return launch_combine_shared(p, s) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 SV_API sv_status sv_plan_preview(const sv_attn_desc* desc, int32_t block_size,

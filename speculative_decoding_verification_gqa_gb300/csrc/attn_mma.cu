@@ -123,7 +123,9 @@ struct Layout {
   }
 };
 
-template <int HD, bool FP8>
+// SHARED: the units are over parts (internal.cuh, SharedSeq): keys [start, nkeys) of a
+// group's prefix, which every row sees, or of a sequence behind it.
+template <int HD, bool FP8, bool SHARED>
 __global__ void __launch_bounds__(NTHREADS, 1) attn_mma_kernel(const AttnParams p) {
   using L = Layout<HD>;
   constexpr int KS = HD / 16;   // k-steps of S = Q K^T
@@ -154,17 +156,21 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_mma_kernel(const AttnParams 
     const int l1 = (int)(min(t_end, ub + nt) - ub);
     if (l1 <= l0) break;  // cannot happen for a valid plan
     t = ub + l1;
-    const int T = p.seq_lens[b];
-    const int D = p.draft_len[b];
+    const SharedSeq part = SHARED ? p.parts[b] : SharedSeq{};
+    const int T = SHARED ? part.last0 : p.seq_lens[b];
+    const int D = SHARED ? part.rows - 1 : p.draft_len[b];
     // key tiles [j0, j1) of the sequence (tile j holds positions j*KT ..), out of the
     // unit's tiles [kb, kb + nt)
-    const int kb = info.w / KT;
+    // (SHARED: the unit's first key is info.w itself, a multiple of the block size)
+    const int kb = SHARED ? 0 : info.w / KT;
+    const int kofs = SHARED ? info.w : 0;
     const int j0 = kb + l0, j1 = kb + l1;
     const int rows_total = p.G * (D + 1);
     const int rows = min(MT, rows_total - mt * MT);
-    const int nkeys = T + D + 1;
-    const int kvis = first_visible_key(T, p.window);  // earlier rows left the window
-    const int64_t qo = p.q_off[b], ko = p.kv_off[b];
+    const int nkeys = SHARED ? part.nkeys : T + D + 1;
+    const int kvis = SHARED ? part.start : first_visible_key(T, p.window);  // earlier rows
+                                                                            // left the window
+    const int64_t qo = SHARED ? part.q_off : p.q_off[b], ko = SHARED ? 0 : p.kv_off[b];
     const float ks = FP8 ? p.kv_scale[g] : 1.f;
     const float sc = p.scale_log2 * ks;
 
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_mma_kernel(const AttnParams 
     // cache row of position `key`: packed, ko + key; paged, row key % block_size of the
     // block the block table names (an entry outside the pool sets the shape flag and
     // reads as zeros).
-    const int32_t* tab = p.block_table + (size_t)b * p.bt_stride;
+    const int32_t* tab = p.block_table + (size_t)(SHARED ? part.table_row : b) * p.bt_stride;
     auto cache_row = [&](int key, bool& ok) -> int64_t {
       if (p.block_size == 0) return ko + key;
       if (!ok) return 0;
@@ -204,7 +210,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_mma_kernel(const AttnParams 
     auto load_tile = [&](int j, int stage) {
       uint8_t* dK = sKV + stage * STAGE_BYTES;
       uint8_t* dV = dK + STAGE_BYTES / 2;
-      const int key0 = j * KT;
+      const int key0 = kofs + j * KT;
       if constexpr (FP8) {
         constexpr int CH8 = HD / 16;
         for (int idx = tid; idx < KT * CH8; idx += NTHREADS) {
@@ -252,9 +258,9 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_mma_kernel(const AttnParams 
     const int iA = rgA < rows_total ? rgA / p.G : D;  // padding rows see every key
     const int iB = rgB < rows_total ? rgB / p.G : D;
     // sliding window: first visible key of each row, and the largest over the unit
-    const int loA = p.window > 0 ? max(T + iA + 1 - p.window, 0) : 0;
-    const int loB = p.window > 0 ? max(T + iB + 1 - p.window, 0) : 0;
-    const int lo_max = p.window > 0 ? max(T + D + 1 - p.window, 0) : 0;
+    const int loA = SHARED ? kvis : p.window > 0 ? max(T + iA + 1 - p.window, 0) : 0;
+    const int loB = SHARED ? kvis : p.window > 0 ? max(T + iB + 1 - p.window, 0) : 0;
+    const int lo_max = SHARED ? kvis : p.window > 0 ? max(T + D + 1 - p.window, 0) : 0;
     float o[NO][4];
 #pragma unroll
     for (int n = 0; n < NO; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
@@ -319,7 +325,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_mma_kernel(const AttnParams 
       }
       // ---- scale (log2 units) and window-causal mask: key j visible to row i iff j <= T+i
       // (and, under a sliding window, j >= T+i-window+1)
-      const int key0 = j * KT;
+      const int key0 = kofs + j * KT;
       const bool edge = key0 + KT > T || key0 < lo_max;
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
@@ -328,7 +334,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_mma_kernel(const AttnParams 
           float x = s[n][e] * sc;
           if (edge) {
             const int key = key0 + n * 8 + 2 * (lane & 3) + (e & 1);
-            const int lim = T + (e < 2 ? iA : iB);
+            const int row_lim = T + (e < 2 ? iA : iB);
+            const int lim = SHARED ? min(row_lim, nkeys - 1) : row_lim;
             if (key > lim || key < (e < 2 ? loA : loB)) x = -INFINITY;
           }
           s[n][e] = x;
@@ -399,7 +406,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_mma_kernel(const AttnParams 
       lB += __shfl_xor_sync(0xffffffffu, lB, 1);
       lB += __shfl_xor_sync(0xffffffffu, lB, 2);
       const int col = 2 * (lane & 3);
-      if (j0 == kb && j1 == kb + nt) {
+      if (j0 == kb && j1 == kb + nt && (!SHARED || part.alone)) {
         // this CTA saw every key of the unit: normalise and store bf16
         const float vs = FP8 ? p.kv_scale[p.Hkv + g] : 1.f;
 #pragma unroll
@@ -433,13 +440,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_mma_kernel(const AttnParams 
   }
 }
 
-template <int HD, bool FP8>
+template <int HD, bool FP8, bool SHARED>
 cudaError_t launch_one(const AttnParams& p, cudaStream_t s) {
   const size_t smem = Layout<HD>::smem_bytes(FP8);
-  cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<HD, FP8>,
+  cudaError_t e = cudaFuncSetAttribute(attn_mma_kernel<HD, FP8, SHARED>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_mma_kernel<HD, FP8>, dim3(p.n_ctas), dim3(NTHREADS), smem, s, p);
+  return launch_pdl(attn_mma_kernel<HD, FP8, SHARED>, dim3(p.n_ctas), dim3(NTHREADS), smem, s, p);
 }
 
 }  // namespace
@@ -447,8 +454,13 @@ cudaError_t launch_one(const AttnParams& p, cudaStream_t s) {
 int attn_mma_kt() { return KT; }
 
 cudaError_t launch_attn_mma(const AttnParams& p, bool fp8, cudaStream_t s) {
-  if (p.d == 128) return fp8 ? launch_one<128, true>(p, s) : launch_one<128, false>(p, s);
-  return fp8 ? launch_one<64, true>(p, s) : launch_one<64, false>(p, s);
+  if (p.d == 128) return fp8 ? launch_one<128, true, false>(p, s) : launch_one<128, false, false>(p, s);
+  return fp8 ? launch_one<64, true, false>(p, s) : launch_one<64, false, false>(p, s);
+}
+
+cudaError_t launch_attn_mma_shared(const AttnParams& p, bool fp8, cudaStream_t s) {
+  if (p.d == 128) return fp8 ? launch_one<128, true, true>(p, s) : launch_one<128, false, true>(p, s);
+  return fp8 ? launch_one<64, true, true>(p, s) : launch_one<64, false, true>(p, s);
 }
 
 }  // namespace sv

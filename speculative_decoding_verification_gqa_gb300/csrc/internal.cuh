@@ -92,6 +92,26 @@ inline AttnWs attn_ws_layout(int B, int Hkv, int G, int d, int max_draft, int n_
   return w;
 }
 
+// Shared prefixes (spec_verify_attn_shared): the keys of a call fall into parts, a group's
+// prefix and each sequence's own positions behind it. A part's units are (part, KV head,
+// row tile), its query rows the G * rows of consecutive window rows, so that a prefix is
+// read once per 128 rows of its whole group. A sequence's rows are then the join of two
+// parts by the rule of the online softmax, except where its group's prefix is empty.
+// Parts 0 .. num_groups - 1 are the prefixes, part num_groups + b is sequence b.
+struct SharedSeq {
+  int64_t q_off;      // first window row
+  int32_t rows;       // window rows (0: no units)
+  int32_t start;      // first key
+  int32_t nkeys;      // end of the keys (position)
+  int32_t last0;      // last key seen by the first row; row i sees min(last0 + i, nkeys - 1)
+  int32_t table_row;  // block-table row that the keys are read through
+  int32_t alone;      // a sequence whose prefix is empty: no other part to join
+  int32_t group;      // a sequence's group
+  int32_t nmt, nt;    // row tiles and key tiles of a (part, KV head)
+  int32_t ubase;      // first unit
+  int32_t tbase;      // its first tile on the tile line
+};
+
 struct AttnParams {
   const void* q;
   const void* k;               // packed cache [kv_rows, Hkv, d], or the block pool
@@ -128,6 +148,10 @@ struct AttnParams {
   int block_size;             // positions per block, a power of two; 0: packed cache
   int bs_log2;
   int64_t num_blocks;
+  SharedSeq* parts;           // shared prefixes only: [num_groups + B]
+  int num_groups;
+  const int32_t* group_begin;  // [num_groups + 1]
+  const int32_t* prefix_len;   // [num_groups]
   int window;                 // sliding window in positions (0: every earlier key); set to 0
                               // when it covers max_seq + max_draft + 1 positions
   float scale_log2;           // softmax_scale * log2(e)
@@ -220,6 +244,17 @@ struct HostPlan {
 // buffers, or SV_ERR_WORKSPACE when the plan does not fit a HostPlan.
 sv_status host_plan(const AttnParams& p, int kt, const int32_t* T, const int32_t* D,
                     HostPlan* hp);
+
+// Byte offsets inside a spec_verify_attn_shared workspace, and the units it has room for.
+struct SharedWs {
+  size_t ctrl, hdr, parts, units, ubeg, cta_tab, part_o, part_ml, total;
+  int64_t max_units;
+};
+SharedWs shared_ws_layout(const sv_attn_desc* d, int num_groups, int n_ctas);
+cudaError_t launch_plan_shared(const AttnParams& p, int kt, cudaStream_t s);
+cudaError_t launch_combine_shared(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_attn_mma_shared(const AttnParams& p, bool fp8, cudaStream_t s);
+cudaError_t launch_attn_tc_shared(const AttnParams& p, bool fp8, cudaStream_t s);
 
 // Launchers (each returns the cudaGetLastError() of its launch).
 cudaError_t launch_plan(const AttnParams& p, int kt, cudaStream_t s);

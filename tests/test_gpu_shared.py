@@ -1,0 +1,325 @@
+"""GPU tests of spec_verify_attn_shared (groups of sequences with a common prefix, attended
+once per group) against the fp64 oracle, with NaN in everything that must not be read."""
+import numpy as np
+import pytest
+import torch
+
+import speculative_decoding_verification_gqa_gb300 as sv
+
+from gpu_util import bf16_to_f64, ensure_built
+from shared_util import assert_within, inputs, pages, run, to_device
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(params=[1, 2], ids=["mma", "tcgen05"])
+def kernel(request):
+    ensure_built()
+    lib = sv.api.load_library()
+    prev = lib.sv_set_attn_kernel(request.param)
+    if prev < 0:
+        pytest.skip("kernel not built")
+    yield request.param
+    lib.sv_set_attn_kernel(prev)
+
+
+TWO = [(300, [(300, 3), (301, 0), (455, 7), (700, 2)]), (129, [(129, 1), (1000, 5)])]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bs", [8, 16, 64, 128, 512])
+def test_two_groups_ragged(kernel, bs, d, kv):
+    w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=d, kv=kv, seed=bs + d)
+    assert_within(run(x, pages(x, gb, P, bs, seed=bs), gb, P), w, x)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("P", [1, 7, 8, 63, 64, 65, 127, 128, 129, 255, 256, 257, 1000])
+def test_prefix_lengths_around_tiles_and_pages(kernel, P, kv):
+    """Own parts of no cached position (T = P), one, and more than a tile."""
+    w, x, gb, p = inputs([(P, [(P, 0), (P + 1, 3), (P + 140, 1)])], Hq=4, Hkv=2, d=128, kv=kv, seed=P)
+    assert_within(run(x, pages(x, gb, p, 16, seed=P), gb, p), w, x)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (7, 1), (28, 4), (3, 3), (64, 8), (48, 1)])
+def test_head_layouts(kernel, Hq, Hkv):
+    w, x, gb, P = inputs([(200, [(210, 2), (200, 4), (300, 0)])], Hq=Hq, Hkv=Hkv, d=128, seed=Hq)
+    assert_within(run(x, pages(x, gb, P, 16, seed=1), gb, P), w, x)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("n,D", [(1, 0), (2, 31), (8, 15), (17, 7), (33, 3), (64, 4)])
+def test_many_rows_of_a_group(kernel, n, D, kv):
+    """Groups of under one to many 128-row tiles, whole and ragged."""
+    seqs = [(257 + (5 * b) % 40, (D + b) % (D + 1)) for b in range(n)]
+    w, x, gb, P = inputs([(257, seqs)], Hq=16, Hkv=2, d=128, kv=kv, seed=n)
+    assert_within(run(x, pages(x, gb, P, 32, seed=2), gb, P), w, x)
+
+
+def test_groups_without_prefix_without_sequences_and_of_one(kernel):
+    groups = [(0, [(90, 2), (0, 0), (400, 1)]), (77, []), (500, [(640, 3)]), (0, []),
+              (40, [(40, 0), (1500, 2)])]
+    w, x, gb, P = inputs(groups, Hq=8, Hkv=2, d=128, seed=6)
+    assert_within(run(x, pages(x, gb, P, 16, seed=3), gb, P), w, x)
+
+
+def test_nothing_shared_is_the_paged_call(kernel):
+    w, x, gb, P = inputs([(0, [(300, 3), (41, 0), (700, 2)])], Hq=8, Hkv=2, d=128, seed=8)
+    pg = pages(x, gb, P, 16, seed=3)
+    got = run(x, pg, gb, P)
+    assert_within(got, w, x)
+
+
+@pytest.mark.parametrize("junk", [-1, 1 << 30])
+def test_entries_before_the_prefix_end_are_not_read(kernel, junk):
+    w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=9)
+    ws = sv.new_workspace(1 << 25)
+    assert_within(run(x, pages(x, gb, P, 16, seed=4, junk=junk), gb, P, workspace=ws), w, x)
+    assert sv.workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("scale", [0.0, 0.02, 1.5])
+def test_softmax_scale(kernel, scale):
+    import oracle
+    w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=64, seed=10)
+    got = bf16_to_f64(run(x, pages(x, gb, P, 16, seed=4), gb, P, softmax_scale=scale))
+    ref = oracle.verify_attn(x["q"], x["k"], x["v"], x["seq_lens"], x["draft_len"], Hq=w.Hq,
+                             Hkv=w.Hkv, d=w.d, scale=scale if scale else 64 ** -0.5)
+    mag = oracle.verify_attn(x["q"], x["k"], x["v"] & 0x7FFF, x["seq_lens"], x["draft_len"], Hq=w.Hq,
+                             Hkv=w.Hkv, d=w.d, scale=scale if scale else 64 ** -0.5)
+    # the bound of assert_within; under a scale 12 times the default's the scores' rounding
+    # changes a probability by 12 times as much: 12 * 2^-11 < 2^-7
+    assert (np.abs(got - ref) <= np.abs(ref) * 2.0 ** -8 + mag * (2.0 ** -8 + 2.0 ** -6)).all()
+
+
+def test_prefix_that_dominates_or_is_dominated(kernel):
+    """Scores hundreds of units apart on the two sides of the border: the join neither
+    overflows nor loses the larger part."""
+    for sign in (1, -1):
+        w, x, gb, P = inputs([(200, [(260, 3), (333, 1)])], Hq=4, Hkv=2, d=128, seed=11)
+        off = np.cumsum([0] + [int(t + n + 1) for t, n in zip(x["seq_lens"], x["draft_len"])])
+        k = bf16_to_f64(x["k"])
+        for b in range(2):
+            k[off[b]:off[b] + 200] *= 16.0 if sign > 0 else 1 / 16.0
+            k[off[b] + 200:off[b + 1]] *= 1 / 16.0 if sign > 0 else 16.0
+        x["k"] = (k.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+        assert np.array_equal(bf16_to_f64(x["k"]), k)  # powers of two: exact
+        got = bf16_to_f64(run(x, pages(x, gb, P, 16, seed=4), gb, P))
+        from shared_util import reference
+        ref, mag = reference(w, x)
+        # scores 16 times as large: their rounding counts 16 * 2^-11 = 2^-7 (both ways 2^-6)
+        assert (np.abs(got - ref) <= np.abs(ref) * 2.0 ** -8 + mag * (2.0 ** -8 + 2.0 ** -6)).all()
+
+
+def test_infinite_and_nan_queries_stay_in_their_rows(kernel):
+    """A row of q that holds NaN or infinity spoils its own output only."""
+    w, x, gb, P = inputs([(150, [(160, 1), (150, 2)])], Hq=4, Hkv=2, d=128, seed=12)
+    pg = pages(x, gb, P, 16, seed=4)
+    clean = run(x, pg, gb, P)
+    x["q"][1, 2, 5] = 0x7F80
+    x["q"][3, 0, 7] = 0x7FC0
+    got = run(x, pg, gb, P)
+    spoilt = np.zeros(got.shape[:2], dtype=bool)
+    spoilt[1, 2] = spoilt[3, 0] = True
+    assert np.array_equal(got[~spoilt], clean[~spoilt])
+
+
+def test_rows_behind_the_batch_are_left(kernel):
+    w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=13)
+    pg = pages(x, gb, P, 16, seed=4)
+    n = x["q"].shape[0]
+    x["q"] = np.concatenate([x["q"], np.full((5, 8, 128), 0x7FC0, dtype=np.uint16)])
+    out = torch.full((n + 5, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    got = run(x, pg, gb, P, out=out)
+    assert (bf16_to_f64(got[n:]) == 7.0).all()
+    x["q"] = x["q"][:n]
+    assert_within(got, w, x)
+
+
+def test_same_bits_every_time_and_on_a_used_workspace(kernel):
+    w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=14)
+    pg = pages(x, gb, P, 16, seed=4)
+    ws = sv.new_workspace(1 << 25)
+    first = run(x, pg, gb, P, workspace=ws)
+    ws[256:] = 0xFF  # NaN in all but the flags: nothing stale is read
+    assert np.array_equal(run(x, pg, gb, P, workspace=ws), first)
+    assert np.array_equal(run(x, pg, gb, P, workspace=ws), first)
+
+
+@pytest.mark.parametrize("field,at,value", [
+    ("gb", 0, 1), ("gb", 1, 7), ("gb", 2, 5), ("gb", 1, -1), ("P", 0, 301), ("P", 1, 130),
+    ("P", 0, -1), ("P", 0, 1 << 30), ("T", 0, 1001), ("T", 1, -1), ("D", 2, 8), ("D", 0, -1)])
+def test_lengths_out_of_range_are_reported(kernel, field, at, value):
+    w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=15)
+    pg = pages(x, gb, P, 16, seed=4)
+    ws = sv.new_workspace(1 << 25)
+    out = torch.full(x["q"].shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    bad = dict(gb=gb.copy(), P=P.copy(), T=x["seq_lens"].copy(), D=x["draft_len"].copy())
+    bad[field][at] = value
+    y = dict(x, seq_lens=bad["T"], draft_len=bad["D"])
+    got = run(y, pg, bad["gb"], bad["P"], workspace=ws, out=out, max_draft=7, max_seq=1000)
+    assert sv.workspace_status(ws, clear=True) == 8
+    assert (bf16_to_f64(got) == 7.0).all()
+    assert_within(run(x, pg, gb, P, workspace=ws), w, x)
+    assert sv.workspace_status(ws) == 0
+
+
+def test_more_rows_than_q_holds_and_narrow_tables(kernel):
+    w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=16)
+    pg = pages(x, gb, P, 16, seed=4)
+    ws = sv.new_workspace(1 << 25)
+    run(dict(x, q=x["q"][:-1]), pg, gb, P, workspace=ws)
+    assert sv.workspace_status(ws, clear=True) == 8
+    narrow = dict(pg, block_table=np.ascontiguousarray(pg["block_table"][:, :20]))
+    run(x, narrow, gb, P, workspace=ws)
+    assert sv.workspace_status(ws, clear=True) == 8
+
+
+def test_table_entry_outside_the_pool_is_reported(kernel):
+    w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=17)
+    ws = sv.new_workspace(1 << 25)
+    for row, col in ((0, 3), (1, 18), (5, 20)):  # a prefix's, and two own entries
+        pg = pages(x, gb, P, 16, seed=4)
+        assert pg["block_table"][row, col] >= 0
+        pg["block_table"][row, col] = 1 << 29
+        run(x, pg, gb, P, workspace=ws)
+        assert sv.workspace_status(ws, clear=True) == 8
+
+
+def test_graph_replay_follows_new_lengths(kernel):
+    """One captured call, replayed with other lengths, groups and queries in place."""
+    w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=18)
+    pg = pages(x, gb, P, 16, seed=4)
+    q, k, v, bt, T, D, _ = to_device(x, pg)
+    i32 = lambda a: torch.from_numpy(np.asarray(a, dtype=np.int32)).cuda()  # noqa: E731
+    g_, p_ = i32(gb), i32(P)
+    out = torch.empty_like(q)
+    ws = sv.new_workspace(1 << 25)
+    call = lambda: sv.spec_verify_attn_shared(q, k, v, bt, T, D, g_, p_, max_draft_len=7,  # noqa: E731
+                                              max_seq_len=1000, out=out, workspace=ws)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert_within(out.view(torch.int16).cpu().numpy().view(np.uint16), w, x)
+    # the prefixes shortened: the same attention (all of it in the pool's first rows)
+    p_.copy_(i32([288, 128]))
+    pg2 = pages(x, gb, np.array([288, 128]), 16, seed=4)
+    _, k2, v2, bt2, _, _, _ = to_device(x, pg2)
+    k.copy_(k2), v.copy_(v2), bt.copy_(bt2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert_within(out.view(torch.int16).cpu().numpy().view(np.uint16), w, x)
+    assert sv.workspace_status(ws) == 0
+
+
+def test_positions_past_32_bits_of_bytes(kernel):
+    """A pool whose far pages lie past 2^32 bytes; the prefix and own pages among them."""
+    w, x, gb, P = inputs([(100, [(130, 2), (100, 0)])], Hq=8, Hkv=8, d=128, seed=19)
+    pg = pages(x, gb, P, 64, seed=4)
+    q, k, v, bt, T, D, _ = to_device(x, pg)
+    far = 40000  # pages of 128 KiB: 5.2 GB
+    K = torch.zeros(far + k.shape[0], 64, 8, 128, dtype=torch.bfloat16, device="cuda")
+    V = torch.zeros_like(K)
+    K[far:], V[far:] = k, v
+    i32 = lambda a: torch.from_numpy(np.asarray(a, dtype=np.int32)).cuda()  # noqa: E731
+    out = sv.spec_verify_attn_shared(q, K, V, torch.where(bt >= 0, bt + far, bt), T, D, i32(gb), i32(P),
+                                     max_draft_len=2, max_seq_len=130)
+    torch.cuda.synchronize()
+    assert_within(out.view(torch.int16).cpu().numpy().view(np.uint16), w, x)
+
+
+@pytest.mark.parametrize("after", [0, 1, 2])
+def test_failed_launch_is_reported_and_the_workspace_serves_on(after):
+    ensure_built()
+    w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=20)
+    pg = pages(x, gb, P, 16, seed=4)
+    ws = sv.new_workspace(1 << 25)
+    sv.api.inject_launch_failure(after)
+    with pytest.raises(sv.SpecVerifyError) as e:
+        run(x, pg, gb, P, workspace=ws)
+    assert e.value.status == 6
+    assert_within(run(x, pg, gb, P, workspace=ws), w, x)
+    assert sv.workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+def test_bounded_wait_runs_out_and_the_call_returns(kv):
+    ensure_built()
+    w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, kv=kv, seed=21)
+    pg = pages(x, gb, P, 16, seed=4)
+    ws = sv.new_workspace(1 << 25)
+    sv.api.inject_wait_timeout(100000)
+    run(x, pg, gb, P, workspace=ws)
+    assert sv.workspace_status(ws, clear=True) == 7
+    assert sv.api.inject_wait_timeout(0) == 0  # taken by that call
+    assert_within(run(x, pg, gb, P, workspace=ws), w, x)
+    assert sv.workspace_status(ws) == 0
+
+
+def test_fork_extend_attend_trim_compact_together(kernel):
+    """A prompt is forked, the samples extend their windows (parting from the shared page),
+    write K/V, attend under the shared prefix, roll back and are compacted; the attention
+    over the moved pages gives the same bits."""
+    bs, Hkv, Hq, d, P = 16, 2, 8, 128, 200
+    w, x, gb, Pl = inputs([(P, [(P, 3), (P, 1), (P, 2)])], Hq=Hq, Hkv=Hkv, d=d, seed=22)
+    nb, stride = 64, 20
+    ref = torch.zeros(nb, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(4, dtype=torch.int32, device="cuda")
+    table = torch.full((4, stride), -1, dtype=torch.int32, device="cuda")
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    k = torch.full((nb, bs, Hkv, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    v = torch.full_like(k, float("nan"))
+    pools = sv.page_pools([k, v])
+    ws = sv.new_workspace(sv.pages_workspace_bytes(nb, 4))
+    kw = dict(block_size=bs, workspace=ws)
+    bits = lambda a: torch.from_numpy(a.view(np.int16)).view(torch.bfloat16).cuda()  # noqa: E731
+    packed = (bits(x["k"]), bits(x["v"]))
+    off = np.cumsum([0] + [int(P + n + 1) for n in x["draft_len"]])
+
+    def write(r, b, lo, hi):
+        at = torch.arange(lo, hi, device="cuda")
+        page = table[r, at // bs].long()
+        for pool, src in zip((k, v), packed):
+            pool[page, at % bs] = src[off[b] + lo:off[b] + hi]
+
+    # scattered on purpose: row 3 takes pages first and hands them back later
+    sv.spec_pages_extend(ref, table, lens, i32([3]), i32([100]), pools=pools, **kw)
+    sv.spec_pages_extend(ref, table, lens, i32([0]), i32([P]), pools=pools, **kw)
+    write(0, 0, 0, P)
+    sv.spec_pages_fork(ref, table, lens, i32([0, 0]), i32([1, 2]), **kw)
+    T = lens[:3].clone()
+    D = i32(x["draft_len"].tolist())
+    sv.spec_pages_extend(ref, table, lens, None, (T + 1 + D).contiguous(), pools=pools, **kw)
+    for b in range(3):
+        write(b, b, P, P + 1 + int(x["draft_len"][b]))
+    q = bits(x["q"])
+
+    def attend():
+        o = sv.spec_verify_attn_shared(q, k, v, table[:3], T, D, i32(gb.tolist()), i32([P]),
+                                       max_draft_len=3, max_seq_len=P)
+        p = sv.spec_verify_attn_paged(q, k, v, table[:3], T, D, max_draft_len=3, max_seq_len=P)
+        torch.cuda.synchronize()
+        return o.view(torch.int16).cpu().numpy().view(np.uint16), p.view(torch.int16).cpu().numpy().view(np.uint16)
+
+    shared, paged = attend()
+    assert_within(shared, w, x)
+    assert_within(paged, w, x)
+    sv.spec_pages_trim(ref, table, lens, i32([3]), i32([0]), **kw)
+    live = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sv.spec_pages_compact(ref, table, lens, pools=pools, num_live=live, **kw)
+    assert int(live) == 12 + 3 * 1  # whole prefix pages once, one last page each
+    assert int(table[:3].max()) < int(live)
+    again, _ = attend()
+    assert np.array_equal(again, shared)
+    al, _ = sv.spec_accept(torch.randn(9, 50, device="cuda"), i32([0] * 6), D, max_draft_len=3)
+    sv.spec_pages_trim(ref, table, lens, None, (T + al).contiguous(), **kw)
+    assert lens[:3].tolist() == (T + al).tolist()
+    assert sv.workspace_status(ws) == 0
