@@ -22,6 +22,7 @@ namespace {
 constexpr int SWITCH_TILES_TC_FP8 = SV_SWITCH_F8;
 constexpr int SWITCH_TILES_TC_BF16 = SV_SWITCH_BF16;
 constexpr int SWITCH_TILES_MMA = 2;
+constexpr int SWITCH_TILES_PREFIX = 3;
 // Per-tile compute floor of each kernel, in CTAs streaming at once (a 128-key tile's
 // compute time x HBM bandwidth / the tile's bytes: bf16 about 0.9 us x 6.8 TB/s / 64 KB,
 // E4M3 about 0.89 us x 6.8 TB/s / 32 KB). The cost model is not applied to the mma.sync
@@ -388,7 +389,8 @@ sv_status check_shared(const sv_attn_desc* desc, int32_t num_groups) {
   if (st != SV_OK) return st;
   if (desc->sliding_window != 0 || num_groups < 1 || num_groups > std::max(desc->batch, 1))
     return SV_ERR_SHAPE;
-  return shared_ws_layout(desc, num_groups, 0).max_units > MAX_SHARED_UNITS ? SV_ERR_SHAPE : SV_OK;
+  const SharedWs lay = shared_ws_layout(desc, num_groups, 0, false);
+  return lay.max_units[1] > MAX_SHARED_UNITS ? SV_ERR_SHAPE : SV_OK;
 }
 
 }  // namespace
@@ -398,7 +400,10 @@ extern "C" {
 SV_API size_t spec_verify_attn_shared_workspace_size(const sv_attn_desc* desc, int32_t num_groups) {
   if (check_shared(desc, num_groups) != SV_OK) return 0;
   const int sms = current_sms();
-  return sms > 0 ? shared_ws_layout(desc, num_groups, sms).total : 0;
+  if (sms <= 0) return 0;
+  // whichever attention kernel a call will take
+  return std::max(shared_ws_layout(desc, num_groups, sms, true).total,
+                  shared_ws_layout(desc, num_groups, sms, false).total);
 }
 
 SV_API sv_status spec_verify_attn_shared(const sv_attn_desc* desc, const void* q,
@@ -428,10 +433,13 @@ SV_API sv_status spec_verify_attn_shared(const sv_attn_desc* desc, const void* q
     return SV_ERR_ALIGN;
   const int sms = current_sms();
   if (sms <= 0) return SV_ERR_CUDA;
-  const SharedWs lay = shared_ws_layout(desc, num_groups, sms);
-  if (workspace_bytes < lay.total) return SV_ERR_WORKSPACE;
+  if (workspace_bytes < std::max(shared_ws_layout(desc, num_groups, sms, true).total,
+                                 shared_ws_layout(desc, num_groups, sms, false).total))
+    return SV_ERR_WORKSPACE;
 
   const int which = pick_kernel(desc);
+  const bool lines = which == 2;
+  const SharedWs lay = shared_ws_layout(desc, num_groups, sms, lines);
   const int kt = which == 2 ? attn_tc_kt() : attn_mma_kt();
   const PagedArgs pg = {block_table, max_blocks_per_seq, block_size, num_blocks};
   AttnParams p = shape_params(desc, pg, which, sms);
@@ -454,25 +462,39 @@ SV_API sv_status spec_verify_attn_shared(const sv_attn_desc* desc, const void* q
   p.num_groups = num_groups;
   p.group_begin = group_begin;
   p.prefix_len = prefix_len;
-  p.max_units = (int)lay.max_units;
   p.n_ctas = sms;
-  p.flags = (uint32_t*)(ws + lay.ctrl);
-  p.hdr = (PlanHdr*)(ws + lay.hdr);
+  p.flags = (uint32_t*)ws;
   p.parts = (SharedSeq*)(ws + lay.parts);
-  p.units = (int4*)(ws + lay.units);
-  p.ubeg = (int32_t*)(ws + lay.ubeg);
-  p.cta_tab = (int2*)(ws + lay.cta_tab);
-  p.part_o = (float*)(ws + lay.part_o);
-  p.part_ml = (float2*)(ws + lay.part_ml);
+  p.row_begin = (int32_t*)(ws + lay.row_begin);
+  p.row_seq = (int32_t*)(ws + lay.row_seq);
+  p.tile_unit = (int32_t*)(ws + lay.tile_unit);
+  p.row_tile = lines ? 2 * MT : MT;
+  AttnParams line[2] = {p, p};
+  for (int k = 0; k < 2; ++k) {
+    AttnParams& l = line[k];
+    l.max_units = (int)lay.max_units[k];
+    l.hdr = (PlanHdr*)(ws + lay.line[k].hdr);
+    l.units = (int4*)(ws + lay.line[k].units);
+    l.ubeg = (int32_t*)(ws + lay.line[k].ubeg);
+    l.unit_ctas = (int2*)(ws + lay.line[k].unit_ctas);
+    l.cta_tab = (int2*)(ws + lay.line[k].cta_tab);
+    l.part_o = (float*)(ws + lay.line[k].part_o);
+    l.part_ml = (float2*)(ws + lay.line[k].part_ml);
+  }
+  line[0].switch_tiles = SWITCH_TILES_PREFIX;
 
   cudaStream_t s = (cudaStream_t)stream;
-  if (launch_plan_shared(p, kt, s) != cudaSuccess) return SV_ERR_CUDA;
+  if (launch_plan_shared(line[0], line[1], lines, kt, s) != cudaSuccess) return SV_ERR_CUDA;
   if (g_ev_start && cudaEventRecord(g_ev_start, s) != cudaSuccess) return SV_ERR_CUDA;
-  const cudaError_t e =
-      which == 2 ? launch_attn_tc_shared(p, fp8, s) : launch_attn_mma_shared(p, fp8, s);
-  if (e != cudaSuccess) return SV_ERR_CUDA;
+  if (lines) {
+    if (launch_attn_prefix(line[0], fp8, s) != cudaSuccess) return SV_ERR_CUDA;
+    if (launch_attn_tc_shared(line[1], fp8, s) != cudaSuccess) return SV_ERR_CUDA;
+  } else if (launch_attn_mma_shared(line[1], fp8, s) != cudaSuccess) {
+    return SV_ERR_CUDA;
+  }
   if (g_ev_stop && cudaEventRecord(g_ev_stop, s) != cudaSuccess) return SV_ERR_CUDA;
-  return launch_combine_shared(p, s) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  return launch_combine_shared(lines ? line[0] : line[1], line[1], s) == cudaSuccess ? SV_OK
+                                                                                  : SV_ERR_CUDA;
 }
 
 SV_API sv_status sv_plan_preview(const sv_attn_desc* desc, int32_t block_size,

@@ -227,7 +227,10 @@ __device__ __forceinline__ void attn_tc_body(const AttnParams& p, const CUtensor
   volatile int* abort = &bars->abort;
   const Waiter wt{abort, p.flags, p.wait_limit > 0 ? p.wait_limit : TIMEOUT_CYCLES};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();  // the plan of this call is complete
+  // The plan of this call is complete. (Shared prefixes: the kernel before this one is the
+  // prefixes', whose CTAs let this grid start once each had waited for the plan; this grid
+  // waits for it at its end.)
+  if constexpr (!Plan::SHARED) pdl_wait();
 
   const int num_units = pl.num_units();
   const int2 rb = pl.cta(blockIdx.x), re = pl.cta(blockIdx.x + 1);
@@ -918,11 +921,14 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + 128 : NTHREADS, 1)
 
 // Shared prefixes: the plan in the workspace, units over parts (see SharedPlan). Built on
 // the sliding-window form, whose lower mask edge and cleared V rows serve the part's start.
+// It runs beside the tail of the prefixes' kernel (attn_prefix.cu), and its completion
+// stands for that kernel's too: each CTA waits for it before it ends.
 template <int HD, bool F8, bool SPLIT>
 __global__ void __launch_bounds__(F8 ? NTHREADS + 128 : NTHREADS, 1)
     attn_tc_kernel_shared(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
                           const __grid_constant__ CUtensorMap tmv) {
   attn_tc_body<HD, F8, true, SPLIT>(p, tmk, tmv, SharedPlan{p});
+  pdl_wait();
 }
 
 // ---------------------------------------------------------------- host side

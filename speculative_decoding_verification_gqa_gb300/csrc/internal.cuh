@@ -108,8 +108,9 @@ struct SharedSeq {
   int32_t alone;      // a sequence whose prefix is empty: no other part to join
   int32_t group;      // a sequence's group
   int32_t nmt, nt;    // row tiles and key tiles of a (part, KV head)
-  int32_t ubase;      // first unit
+  int32_t ubase;      // a sequence's first unit
   int32_t tbase;      // its first tile on the tile line
+  int32_t mbase;      // a prefix's first row tile among those of all prefixes
 };
 
 struct AttnParams {
@@ -148,7 +149,13 @@ struct AttnParams {
   int block_size;             // positions per block, a power of two; 0: packed cache
   int bs_log2;
   int64_t num_blocks;
-  SharedSeq* parts;           // shared prefixes only: [num_groups + B]
+  // shared prefixes only
+  SharedSeq* parts;           // [num_groups + B]
+  int32_t* row_begin;         // [B] first window row of each sequence
+  int32_t* row_seq;           // [window rows] each one's sequence
+  int32_t* tile_unit;         // [row tiles of the prefixes] first of the Hkv units of each
+  int2* unit_ctas;            // [U] first and last CTA that a unit's tiles fall to
+  int row_tile;               // query rows of a prefix's unit
   int num_groups;
   const int32_t* group_begin;  // [num_groups + 1]
   const int32_t* prefix_len;   // [num_groups]
@@ -245,14 +252,21 @@ struct HostPlan {
 sv_status host_plan(const AttnParams& p, int kt, const int32_t* T, const int32_t* D,
                     HostPlan* hp);
 
-// Byte offsets inside a spec_verify_attn_shared workspace, and the units it has room for.
+// Byte offsets inside a spec_verify_attn_shared workspace, and the units it has room for:
+// two lines of units (0 the prefixes', 1 the sequences') or one for all (`lines` false).
 struct SharedWs {
-  size_t ctrl, hdr, parts, units, ubeg, cta_tab, part_o, part_ml, total;
-  int64_t max_units;
+  struct Line {
+    size_t hdr, units, ubeg, unit_ctas, cta_tab, part_o, part_ml;
+  };
+  size_t parts, row_begin, row_seq, tile_unit, total;
+  Line line[2];
+  int64_t max_units[2];
 };
-SharedWs shared_ws_layout(const sv_attn_desc* d, int num_groups, int n_ctas);
-cudaError_t launch_plan_shared(const AttnParams& p, int kt, cudaStream_t s);
-cudaError_t launch_combine_shared(const AttnParams& p, cudaStream_t s);
+SharedWs shared_ws_layout(const sv_attn_desc* d, int num_groups, int n_ctas, bool lines);
+cudaError_t launch_plan_shared(const AttnParams& pa, const AttnParams& pb, bool lines, int kt,
+                               cudaStream_t s);
+cudaError_t launch_combine_shared(const AttnParams& pa, const AttnParams& pb, cudaStream_t s);
+cudaError_t launch_attn_prefix(const AttnParams& p, bool fp8, cudaStream_t s);
 cudaError_t launch_attn_mma_shared(const AttnParams& p, bool fp8, cudaStream_t s);
 cudaError_t launch_attn_tc_shared(const AttnParams& p, bool fp8, cudaStream_t s);
 
