@@ -88,6 +88,15 @@ __device__ __forceinline__ void mma_ss_e4m3(uint32_t d_tmem, uint64_t a, uint64_
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
 }
 
+// True in one lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(e));
+  return e != 0;
+}
+
 // Four scaled Q elements as hi + lo E4M3 terms (attn_tc.cu, split_q_e4m3).
 __device__ __forceinline__ void split_q(const float* x, uint32_t& whi, uint32_t& wlo) {
   const uint32_t h01 = f32x2_to_e4m3x2(x[0], x[1]), h23 = f32x2_to_e4m3x2(x[2], x[3]);
@@ -141,7 +150,8 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
   Bars* bars = (Bars*)(smem + L::BARS);
   volatile int* abort = &bars->abort;
   const Waiter wt{abort, p.flags, p.wait_limit > 0 ? p.wait_limit : TIMEOUT_CYCLES};
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform: the roles' branches too
   pdl_wait();     // the plan of this call is complete
   pdl_trigger();  // the sequences' kernel, which needs the plan only, may fill SMs as they empty
 
@@ -186,7 +196,10 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = bars->tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
+  auto wwait = [&](uint64_t* bar, uint32_t par) -> bool {  // by a whole warp
+    return __all_sync(0xffffffffu, mbar_wait(bar, par, wt));
+  };
 
   if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ TMA producers
@@ -264,7 +277,10 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ S_r = Q_r K^T issuer
-    if (lane == 0) {
+    // The whole warp walks the units and waits, and one elected lane issues: descriptors
+    // stay in uniform registers. An issuer that is one divergent thread needs 45 clocks a
+    // 64-column MMA, more than the 32 that the MMA takes.
+    {
       constexpr uint32_t ID_S = F8 ? idesc_e4m3(HK) : idesc_bf16(HK, 0);
       // K and Q: K-major, 128-byte rows, 8-row groups 1024 B apart, 32 B per K step
       const uint64_t kdesc0 = smem_desc(saddr(smem + L::K), 16, 1024);
@@ -277,52 +293,60 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
         const int nr = tiles_of(s);
         for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
           const uint32_t st = it % L::NS;
-          if (!(ok = mbar_wait(&bars->k_full[st], (it / L::NS) & 1, wt))) break;
+          if (!(ok = wwait(&bars->k_full[st], (it / L::NS) & 1))) break;
           const int steps = steps_of(s, j);
           for (int h = 0; ok && h < steps; ++h) {
             const uint64_t kd = kdesc0 + ((st * L::RAW + h * HK * 128) >> 4);
             for (int r = 0; r < nr; ++r) {
-              if ((j == s.j0 && h == 0 && !mbar_wait(&bars->q_full[r], units[r] & 1, wt)) ||
-                  (n[r] >= 1 && !mbar_wait(&bars->s_free[r], (n[r] - 1) & 1, wt))) {
+              if ((j == s.j0 && h == 0 && !wwait(&bars->q_full[r], units[r] & 1)) ||
+                  (n[r] >= 1 && !wwait(&bars->s_free[r], (n[r] - 1) & 1))) {
                 ok = false;
                 break;
               }
               fence_after();
-              const uint32_t d = tmem + COL_S + r * HK, a = tmem + COL_Q + r * 32;
-              const uint64_t qd = qdesc0 + ((r * L::QB) >> 4);
-              if constexpr (F8) {
-#pragma unroll
-                for (int kk = 0; kk < HD / 32; ++kk) {
-                  mma_ts_e4m3(d, a + kk * 8, kd + ((kk * 32) >> 4), ID_S, kk > 0 ? 1u : 0u);
-                  mma_ss_e4m3(d, qd + ((kk * 32) >> 4), kd + ((kk * 32) >> 4), ID_S, 1u);
-                }
-              } else {
-#pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk) {
-                  const uint64_t ko = ((kk >> 2) * L::BLK + (kk & 3) * 32) >> 4;
-                  if (kk < 4)
-                    mma_ts(d, a + kk * 8, kd + ko, ID_S, kk > 0 ? 1u : 0u);
-                  else
-                    mma_ss(d, qd + (((kk & 3) * 32) >> 4), kd + ko, ID_S, 1u);
-                }
-              }
-              mma_commit(&bars->s_full[r]);
               ++n[r];
+              if (elect_one()) {
+                const uint32_t d = tmem + COL_S + r * HK, a = tmem + COL_Q + r * 32;
+                const uint64_t qd = qdesc0 + ((r * L::QB) >> 4);
+                if constexpr (F8) {
+#pragma unroll
+                  for (int kk = 0; kk < HD / 32; ++kk) {
+                    mma_ts_e4m3(d, a + kk * 8, kd + ((kk * 32) >> 4), ID_S, kk > 0 ? 1u : 0u);
+                    mma_ss_e4m3(d, qd + ((kk * 32) >> 4), kd + ((kk * 32) >> 4), ID_S, 1u);
+                  }
+                } else {
+#pragma unroll
+                  for (int kk = 0; kk < HD / 16; ++kk) {
+                    const uint64_t ko = ((kk >> 2) * L::BLK + (kk & 3) * 32) >> 4;
+                    if (kk < 4)
+                      mma_ts(d, a + kk * 8, kd + ko, ID_S, kk > 0 ? 1u : 0u);
+                    else
+                      mma_ss(d, qd + (((kk & 3) * 32) >> 4), kd + ko, ID_S, 1u);
+                  }
+                }
+                mma_commit(&bars->s_full[r]);
+              }
+              __syncwarp();
             }
           }
-          if (ok) mma_commit(&bars->k_empty[st]);
+          if (ok && elect_one()) mma_commit(&bars->k_empty[st]);
+          __syncwarp();
         }
         for (int r = 0; r < nr; ++r) ++units[r];
       }
-      mma_commit(&bars->s_final);
-      const long long t0 = clock64();
-      while (!mbar_try(&bars->s_final, 0) && clock64() - t0 < TIMEOUT_CYCLES) {
+      __syncwarp();
+      if (elect_one()) {
+        mma_commit(&bars->s_final);
+        const long long t0 = clock64();
+        while (!mbar_try(&bars->s_final, 0) && clock64() - t0 < TIMEOUT_CYCLES) {
+        }
       }
+      __syncwarp();
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------ O_r += P_r V issuer
     // In every step row tile 0 first: its warpgroup clears the V rows past the prefix.
-    if (lane == 0) {
+    {
       constexpr uint32_t ID_PV = F8 ? idesc_f16(HD, 1) : idesc_bf16(HD, 1);
       // V: MN-major, 64-column blocks L::BLK apart (LBO), 8-key groups 1024 B apart (SBO)
       const uint64_t vdesc0 = smem_desc(saddr(smem + (F8 ? L::CV : L::V)), L::BLK, 1024);
@@ -335,38 +359,43 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
         for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
           constexpr uint32_t NV = F8 ? NCV : L::NS;
           const uint32_t st = it % NV;
-          if (!(ok = mbar_wait(F8 ? &bars->vc_full[st] : &bars->v_full[st], (it / NV) & 1, wt))) break;
+          if (!(ok = wwait(F8 ? &bars->vc_full[st] : &bars->v_full[st], (it / NV) & 1))) break;
           const int steps = steps_of(s, j);
           for (int h = 0; ok && h < steps; ++h) {
             const uint64_t vd = vdesc0 + ((st * L::TILE + h * HK * 128) >> 4);
             for (int r = 0; r < nr; ++r) {
-              if (!(ok = mbar_wait(&bars->p_full[r], n[r] & 1, wt))) break;
+              if (!(ok = wwait(&bars->p_full[r], n[r] & 1))) break;
               fence_after();
-#pragma unroll
-              for (int kk = 0; kk < HK / 16; ++kk)
-                mma_ts(tmem + COL_O + r * 128, tmem + COL_P + r * 32 + kk * 8,
-                       vd + ((kk * 16 * 128) >> 4), ID_PV,
-                       (j == s.j0 && h == 0 && kk == 0) ? 0u : 1u);
-              mma_commit(&bars->o_done[r]);
               ++n[r];
+              if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < HK / 16; ++kk)
+                  mma_ts(tmem + COL_O + r * 128, tmem + COL_P + r * 32 + kk * 8,
+                         vd + ((kk * 16 * 128) >> 4), ID_PV,
+                         (j == s.j0 && h == 0 && kk == 0) ? 0u : 1u);
+                mma_commit(&bars->o_done[r]);
+              }
+              __syncwarp();
             }
           }
-          if (ok) mma_commit(F8 ? &bars->vc_empty[st] : &bars->v_empty[st]);
+          if (ok && elect_one()) mma_commit(F8 ? &bars->vc_empty[st] : &bars->v_empty[st]);
+          __syncwarp();
         }
       }
-      mma_commit(&bars->pv_final);
-      const long long t0 = clock64();
-      while (!mbar_try(&bars->pv_final, 0) && clock64() - t0 < TIMEOUT_CYCLES) {
+      __syncwarp();
+      if (elect_one()) {
+        mma_commit(&bars->pv_final);
+        const long long t0 = clock64();
+        while (!mbar_try(&bars->pv_final, 0) && clock64() - t0 < TIMEOUT_CYCLES) {
+        }
       }
+      __syncwarp();
     }
   } else if (warp < CONV_WARP0) {
     // ------------------------------------------------------------ softmax of row tile r
     const int r = (warp - SOFTMAX_WARP0) >> 2;
     const int rr = (warp & 3) * 32 + lane;  // the thread's row in its tile = TMEM lane
     const uint32_t tq = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    auto wwait = [&](uint64_t* bar, uint32_t par) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, par, wt));
-    };
     int t = t_begin, u = u_first;
     Seg s;
     uint32_t it = 0, n = 0;  // tiles of the range; steps of this row tile
