@@ -22,7 +22,8 @@ namespace {
 constexpr int SWITCH_TILES_TC_FP8 = SV_SWITCH_F8;
 constexpr int SWITCH_TILES_TC_BF16 = SV_SWITCH_BF16;
 constexpr int SWITCH_TILES_MMA = 2;
-constexpr int SWITCH_TILES_PREFIX = 3;
+constexpr int SWITCH_TILES_PREFIX = 3;    // 128-key tiles of 256 rows
+constexpr int SWITCH_TILES_SEQUENCE = 4;  // 64-key tiles, two CTAs per SM
 // Per-tile compute floor of each kernel, in CTAs streaming at once (a 128-key tile's
 // compute time x HBM bandwidth / the tile's bytes: bf16 about 0.9 us x 6.8 TB/s / 64 KB,
 // E4M3 about 0.89 us x 6.8 TB/s / 32 KB). The cost model is not applied to the mma.sync
@@ -440,7 +441,6 @@ SV_API sv_status spec_verify_attn_shared(const sv_attn_desc* desc, const void* q
   const int which = pick_kernel(desc);
   const bool lines = which == 2;
   const SharedWs lay = shared_ws_layout(desc, num_groups, sms, lines);
-  const int kt = which == 2 ? attn_tc_kt() : attn_mma_kt();
   const PagedArgs pg = {block_table, max_blocks_per_seq, block_size, num_blocks};
   AttnParams p = shape_params(desc, pg, which, sms);
   if (which == 2) {  // a pending wait-timeout injection applies to this launch
@@ -462,17 +462,19 @@ SV_API sv_status spec_verify_attn_shared(const sv_attn_desc* desc, const void* q
   p.num_groups = num_groups;
   p.group_begin = group_begin;
   p.prefix_len = prefix_len;
-  p.n_ctas = sms;
   p.flags = (uint32_t*)ws;
   p.parts = (SharedSeq*)(ws + lay.parts);
   p.row_begin = (int32_t*)(ws + lay.row_begin);
-  p.row_seq = (int32_t*)(ws + lay.row_seq);
+  p.rows = (RowInfo*)(ws + lay.rows);
   p.tile_unit = (int32_t*)(ws + lay.tile_unit);
   p.row_tile = lines ? 2 * MT : MT;
   AttnParams line[2] = {p, p};
   for (int k = 0; k < 2; ++k) {
     AttnParams& l = line[k];
     l.max_units = (int)lay.max_units[k];
+    l.n_ctas = lay.n_ctas[k];
+    l.kt = !lines ? attn_mma_kt() : k == 0 ? 128 : 64;
+    if (lines) l.switch_tiles = k == 0 ? SWITCH_TILES_PREFIX : SWITCH_TILES_SEQUENCE;
     l.hdr = (PlanHdr*)(ws + lay.line[k].hdr);
     l.units = (int4*)(ws + lay.line[k].units);
     l.ubeg = (int32_t*)(ws + lay.line[k].ubeg);
@@ -481,14 +483,13 @@ SV_API sv_status spec_verify_attn_shared(const sv_attn_desc* desc, const void* q
     l.part_o = (float*)(ws + lay.line[k].part_o);
     l.part_ml = (float2*)(ws + lay.line[k].part_ml);
   }
-  line[0].switch_tiles = SWITCH_TILES_PREFIX;
 
   cudaStream_t s = (cudaStream_t)stream;
-  if (launch_plan_shared(line[0], line[1], lines, kt, s) != cudaSuccess) return SV_ERR_CUDA;
+  if (launch_plan_shared(line[0], line[1], lines, s) != cudaSuccess) return SV_ERR_CUDA;
   if (g_ev_start && cudaEventRecord(g_ev_start, s) != cudaSuccess) return SV_ERR_CUDA;
   if (lines) {
-    if (launch_attn_prefix(line[0], fp8, s) != cudaSuccess) return SV_ERR_CUDA;
-    if (launch_attn_tc_shared(line[1], fp8, s) != cudaSuccess) return SV_ERR_CUDA;
+    if (launch_attn_prefixes(line[0], fp8, s) != cudaSuccess) return SV_ERR_CUDA;
+    if (launch_attn_sequences(line[1], fp8, s) != cudaSuccess) return SV_ERR_CUDA;
   } else if (launch_attn_mma_shared(line[1], fp8, s) != cudaSuccess) {
     return SV_ERR_CUDA;
   }

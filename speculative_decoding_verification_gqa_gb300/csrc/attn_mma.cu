@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_mma_kernel(const AttnParams 
       lB += __shfl_xor_sync(0xffffffffu, lB, 1);
       lB += __shfl_xor_sync(0xffffffffu, lB, 2);
       const int col = 2 * (lane & 3);
-      if (j0 == kb && j1 == kb + nt && (!SHARED || part.alone)) {
+      if (!SHARED && j0 == kb && j1 == kb + nt) {
         // this CTA saw every key of the unit: normalise and store bf16
         const float vs = FP8 ? p.kv_scale[p.Hkv + g] : 1.f;
 #pragma unroll

@@ -1,28 +1,33 @@
-// attn_prefix.cu -- attention of a group's rows over their shared prefix on the
-// fifth-generation tensor cores: the compute-bound part of spec_verify_attn_shared.
+// attn_parts.cu -- attention over the parts of a shared-prefix call on the fifth-generation
+// tensor cores (spec_verify_attn_shared; parts and units: internal.cuh, SharedSeq).
 //
-// A unit is (group, KV head, pair of 128-row tiles): up to 256 of the G * sum W query rows
-// of the group's sequences. Its CTA reads each 128-key K/V tile once for both row tiles and
-// works through it in steps of 64 keys. Row tile r has a softmax warpgroup of its own, a
-// score buffer S_r, a probability buffer P_r and an accumulator O_r in TMEM:
-//   columns   0-255  O_0, O_1 (128 each; 64 used for d = 64)
-//           256-383  S_0, S_1 (64 each)      384-447  P_0, P_1 (32 each, 16-bit pairs)
-//           448-511  Q_0, Q_1 (32 each): bf16 elements 0-63 of a row, or the E4M3 hi term
+// A CTA works through a unit's keys in steps of 64. Row tile r (128 query rows) has a softmax
+// warpgroup of its own, a score buffer S_r, a probability buffer P_r and an accumulator O_r
+// in TMEM, and half of Q_r there; the other half of Q_r is in shared memory:
+//   columns   O_r  128 each (64 used for d = 64)      P_r  32 each, 16-bit pairs
+//             S_r   64 each                           Q_r  32 each: bf16 elements 0-63 of a
+//                                                          row, or its E4M3 hi terms
 // P has columns of its own, so S_r of the next step is issued as soon as the warpgroup has
-// read this step's scores into registers and runs under its softmax. What that leaves of
-// TMEM holds half of Q; the other half (bf16 elements 64-127, or the E4M3 lo term) is read
-// by the score MMA from shared memory. Both operands from shared memory would need 192 bytes
-// a clock of it at N = 64, half of Q in TMEM brings a step's shared-memory traffic (scores,
-// P V and the TMA writes) to about 128.
+// read this step's scores into registers, and runs under its softmax. What that leaves of
+// TMEM holds half of Q; the score MMA reads the other half (bf16 elements 64-127, or the
+// E4M3 lo terms) from shared memory. With both operands there an MMA of 64 columns takes 48
+// clocks, with Q in TMEM 32 (measured; shared memory gives 128 bytes a clock).
+//
+//   RT = 2  the prefixes. Units of 256 rows, all 512 columns, one CTA per SM: each 128-key
+//           K/V tile is read once for both row tiles, whose softmaxes alternate on the
+//           tensor cores. Bound by those: a step of both row tiles is 1152 clocks of MMAs.
+//   RT = 1  the sequences behind them. Units of 128 rows, 256 columns, 64-key tiles, two
+//           CTAs per SM: the units are short (a few hundred keys) and each starts with a
+//           read of Q and ends with one of O, which the other CTA's unit covers. Bound by
+//           the K/V stream.
 //
 //   warp 0   TMA producer of K tiles     warp 2   TMA producer of V tiles
-//   warp 1   S issuer: S_r = Q_r K^T, r = 0, 1 (one thread)
-//   warp 3   P V issuer: O_r += P_r V, r = 0, 1 (one thread)
-//   warps 4-7, 8-11   softmax of row tile 0, 1: a thread owns one query row
-//   warps 12-15 (E4M3 only)  decode V tiles to f16
+//   warp 1   S issuer: S_r = Q_r K^T     warp 3   P V issuer: O_r += P_r V
+//   then a softmax warpgroup per row tile: a thread owns one query row
+//   then (E4M3 only) a warpgroup that decodes V tiles to f16
 // A step's mathematics is that of attn_tc.cu (lazily rescaled online softmax, E4M3 keys met
-// by Q as the exact sum of two E4M3 terms); the prefix needs no causal mask. The results are
-// partials (O unnormalised, m, l) for combine_shared. Every wait is bounded as in attn_tc.cu.
+// by Q as the exact sum of two E4M3 terms). The results are partials (O unnormalised, m, l)
+// for combine_shared. Every wait is bounded as in attn_tc.cu.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -33,16 +38,11 @@
 namespace sv {
 namespace {
 
-constexpr int KT = 128;  // keys per tile
-constexpr int HK = 64;   // keys per step
-constexpr int NTHREADS = 384;
+constexpr int HK = 64;  // keys per step
 constexpr int SOFTMAX_WARP0 = 4;
-constexpr int CONV_WARP0 = 12;
 constexpr int NCONV = 128;
-constexpr int NST = 4;   // ring stages at most
-constexpr int NCV = 2;   // E4M3: decoded V tiles
-constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t COL_O = 0, COL_S = 256, COL_P = 384, COL_Q = 448;
+constexpr int NST = 4;  // ring stages at most
+constexpr int NCV = 2;  // E4M3: decoded V tiles
 
 struct __align__(8) Bars {
   uint64_t k_full[NST], k_empty[NST], v_full[NST], v_empty[NST];
@@ -53,8 +53,12 @@ struct __align__(8) Bars {
   int abort;
 };
 
-template <int HD, bool F8>
+template <int HD, bool F8, int RT>
 struct Layout {
+  static constexpr int KT = RT * HK;        // keys per tile
+  static constexpr uint32_t TMEM_COLS = RT * 256;
+  static constexpr uint32_t COL_O = 0, COL_S = RT * 128, COL_P = RT * 192, COL_Q = RT * 224;
+  static constexpr int CONV_WARP0 = SOFTMAX_WARP0 + 4 * RT;
   static constexpr int BLK = KT * 128;      // one 128-byte-wide column block of a tile
   static constexpr int TILE = KT * HD * 2;  // one 16-bit tile
   static constexpr int RAW = F8 ? KT * HD : TILE;  // a tile as the cache has it
@@ -65,11 +69,12 @@ struct Layout {
   static constexpr int Q = CV + (F8 ? NCV * TILE : 0);
   static constexpr bool QS = F8 || HD == 128;        // part of Q is in shared memory
   static constexpr int QB = QS ? 128 * 128 : 0;      // bytes of it per row tile
-  static constexpr int BARS = Q + 2 * QB;
+  static constexpr int BARS = Q + RT * QB;
   static constexpr size_t SMEM = (size_t)BARS + sizeof(Bars);
   static_assert(!F8 || HD == 128, "E4M3 rows of one head are one 128-byte swizzle row");
-  static_assert(SMEM <= 227 * 1024, "dynamic shared memory above the per-CTA limit");
-  static constexpr int THREADS = NTHREADS + (F8 ? NCONV : 0);
+  // 227 KB for a CTA, 228 KB with 1 KB per CTA of the SM's for two
+  static_assert(SMEM <= (RT == 2 ? 227 : 113) * 1024, "shared memory above the limit");
+  static constexpr int THREADS = 32 * CONV_WARP0 + (F8 ? NCONV : 0);
 };
 
 // D[tmem] (+)= A[smem] * B[smem], 16-bit and E4M3 operands
@@ -107,13 +112,16 @@ __device__ __forceinline__ void split_q(const float* x, uint32_t& whi, uint32_t&
   wlo = l01 | (l23 << 16);
 }
 
-// One unit's share of a CTA's range: tiles [j0, j1) of part v, KV head g, row pair mt.
+// One unit's share of a CTA's range: tiles [j0, j1) of part v, KV head g, rows mt * RT * 128
+// on. Positions are relative to the unit's first tile, at cache position kbase.
 struct Seg {
-  int u, v, g, mt, j0, j1;
-  int nkeys, rows, table_row;  // of the part; rows: live query rows of the pair
+  int u, g, mt, j0, j1, kbase;
+  int start, nkeys, last0;  // of the part
+  int rows, table_row;      // rows: live query rows of the unit
   int64_t q_off;
 };
 
+template <int RT>
 __device__ __forceinline__ bool seg_next(const AttnParams& p, int num_units, int& t, int t_end,
                                          int& u, Seg& s) {
   if (t >= t_end || u >= num_units) return false;
@@ -121,13 +129,15 @@ __device__ __forceinline__ bool seg_next(const AttnParams& p, int num_units, int
   const int ub = p.ubeg[u], ue = p.ubeg[u + 1];
   const SharedSeq part = p.parts[info.x];
   s.u = u;
-  s.v = info.x;
   s.g = info.y;
   s.mt = info.z;
+  s.kbase = RT == 2 ? 0 : info.w;
   s.j0 = t - ub;
   s.j1 = min(t_end, ue) - ub;
-  s.nkeys = part.nkeys;
-  s.rows = min(2 * MT, p.G * part.rows - info.z * 2 * MT);
+  s.start = RT == 2 ? 0 : part.start - s.kbase;
+  s.nkeys = part.nkeys - s.kbase;
+  s.last0 = part.last0 - s.kbase;
+  s.rows = min(RT * MT, p.G * part.rows - info.z * RT * MT);
   s.table_row = part.table_row;
   s.q_off = part.q_off;
   if (s.j1 <= s.j0) return false;
@@ -136,31 +146,43 @@ __device__ __forceinline__ bool seg_next(const AttnParams& p, int num_units, int
   return true;
 }
 // Row tiles of a segment, and steps of its tile j.
-__device__ __forceinline__ int tiles_of(const Seg& s) { return s.rows > MT ? 2 : 1; }
+template <int RT>
+__device__ __forceinline__ int tiles_of(const Seg& s) {
+  return RT == 2 && s.rows > MT ? 2 : 1;
+}
+template <int RT>
 __device__ __forceinline__ int steps_of(const Seg& s, int j) {
-  return s.nkeys - j * KT > HK ? 2 : 1;
+  return RT == 2 && s.nkeys - j * RT * HK > HK ? 2 : 1;
 }
 
-template <int HD, bool F8>
-__global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
-    attn_prefix_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
-                       const __grid_constant__ CUtensorMap tmv) {
-  using L = Layout<HD, F8>;
+template <int HD, bool F8, int RT>
+__global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
+    attn_parts_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
+                      const __grid_constant__ CUtensorMap tmv) {
+  using L = Layout<HD, F8, RT>;
+  constexpr int KT = L::KT;
+  constexpr uint32_t TMEM_COLS = L::TMEM_COLS, COL_O = L::COL_O, COL_S = L::COL_S,
+                     COL_P = L::COL_P, COL_Q = L::COL_Q;
   extern __shared__ __align__(1024) uint8_t smem[];  // 128-byte swizzled tiles: 1 KiB aligned
   Bars* bars = (Bars*)(smem + L::BARS);
   volatile int* abort = &bars->abort;
   const Waiter wt{abort, p.flags, p.wait_limit > 0 ? p.wait_limit : TIMEOUT_CYCLES};
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform: the roles' branches too
-  pdl_wait();     // the plan of this call is complete
-  pdl_trigger();  // the sequences' kernel, which needs the plan only, may fill SMs as they empty
+  // The prefixes' kernel waits for the plan and lets the sequences' kernel, which needs the
+  // plan only, fill the SMs as they empty. The sequences' kernel therefore knows that the
+  // plan is complete (every CTA before it had waited for it), and waits for the prefixes'
+  // kernel at its end, so that its completion stands for both.
+  if constexpr (RT == 2) pdl_wait();
+  pdl_trigger();
 
   const int num_units = p.hdr->num_units;
   const int2 rb = p.cta_tab[blockIdx.x], re = p.cta_tab[blockIdx.x + 1];
   const int t_begin = rb.x, t_end = re.x, u_first = rb.y;
-  if (t_begin >= t_end) return;  // uniform across the CTA
-  if (saddr(smem) & 1023) {      // the swizzle phases below assume a 1 KiB-aligned base
-    if (tid == 0) atomicOr(p.flags, FLAG_ATTN_SHAPE);
+  const bool aligned = (saddr(smem) & 1023) == 0;  // the swizzle phases below assume it
+  if (t_begin >= t_end || !aligned) {              // uniform across the CTA
+    if (!aligned && tid == 0) atomicOr(p.flags, FLAG_ATTN_SHAPE);
+    if constexpr (RT == 1) pdl_wait();
     return;
   }
   if (tid == 0) {
@@ -205,7 +227,8 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
     // ------------------------------------------------------------ TMA producers
     // A tile is KT / box boxes of box = min(block_size, KT) rows, lane n loading box n from
     // the page its table entry names. Entries are requested a group of tiles ahead (one per
-    // lane); boxes past the prefix load from a negative row, which fills them with zeros.
+    // lane); boxes without a key of the part load from a negative row, which fills them with
+    // zeros.
     const bool is_k = warp == 0;
     const CUtensorMap* tm = is_k ? &tmk : &tmv;
     uint64_t* full = is_k ? bars->k_full : bars->v_full;
@@ -220,12 +243,13 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
     Seg s;
     uint32_t it = 0;
     bool ok = true;
-    while (ok && seg_next(p, num_units, t, t_end, u, s)) {
+    while (ok && seg_next<RT>(p, num_units, t, t_end, u, s)) {
       const int32_t* tab = p.block_table + (size_t)s.table_row * p.bt_stride;
       auto box_pos = [&](int j, int n) { return j * KT + n * box; };
+      auto seen = [&](int pos) { return pos < s.nkeys && pos + box > s.start; };
       auto fetch = [&](int jg) -> int {  // this lane's entry of the group starting at tile jg
         const int j = jg + lane / nbox, pos = box_pos(j, lane % nbox);
-        return j < s.j1 && pos < s.nkeys ? __ldg(tab + (pos >> p.bs_log2)) : 0;
+        return j < s.j1 && seen(pos) ? __ldg(tab + ((s.kbase + pos) >> p.bs_log2)) : 0;
       };
       int ent_cur = fetch(s.j0), ent_nxt = fetch(s.j0 + tg);
       for (int j = s.j0; j < s.j1; ++j, ++it) {
@@ -238,11 +262,11 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
         const int blk = __shfl_sync(0xffffffffu, ent_cur, q * nbox + lane % nbox);
         int grow = -box;
         const int pos = box_pos(j, lane % nbox);
-        if (mine && pos < s.nkeys) {
+        if (mine && seen(pos)) {
           if (blk < 0 || blk >= p.num_blocks) {  // a table entry outside the pool
             atomicOr(p.flags, FLAG_ATTN_SHAPE);
           } else {
-            grow = blk * p.block_size + (pos & (p.block_size - 1));
+            grow = blk * p.block_size + ((s.kbase + pos) & (p.block_size - 1));
           }
         }
         bool w = true;
@@ -287,17 +311,19 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
       const uint64_t qdesc0 = smem_desc(saddr(smem + L::Q), 16, 1024);
       int t = t_begin, u = u_first;
       Seg s;
-      uint32_t it = 0, n[2] = {0, 0}, units[2] = {0, 0};
+      uint32_t it = 0, n[RT] = {}, units[RT] = {};
       bool ok = true;
-      while (ok && seg_next(p, num_units, t, t_end, u, s)) {
-        const int nr = tiles_of(s);
+      while (ok && seg_next<RT>(p, num_units, t, t_end, u, s)) {
+        const int nr = tiles_of<RT>(s);
         for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
           const uint32_t st = it % L::NS;
           if (!(ok = wwait(&bars->k_full[st], (it / L::NS) & 1))) break;
-          const int steps = steps_of(s, j);
+          const int steps = steps_of<RT>(s, j);
           for (int h = 0; ok && h < steps; ++h) {
             const uint64_t kd = kdesc0 + ((st * L::RAW + h * HK * 128) >> 4);
-            for (int r = 0; r < nr; ++r) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+              if (r >= nr) break;
               if ((j == s.j0 && h == 0 && !wwait(&bars->q_full[r], units[r] & 1)) ||
                   (n[r] >= 1 && !wwait(&bars->s_free[r], (n[r] - 1) & 1))) {
                 ok = false;
@@ -332,7 +358,8 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
           if (ok && elect_one()) mma_commit(&bars->k_empty[st]);
           __syncwarp();
         }
-        for (int r = 0; r < nr; ++r) ++units[r];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) units[r] += r < nr;
       }
       __syncwarp();
       if (elect_one()) {
@@ -352,18 +379,20 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
       const uint64_t vdesc0 = smem_desc(saddr(smem + (F8 ? L::CV : L::V)), L::BLK, 1024);
       int t = t_begin, u = u_first;
       Seg s;
-      uint32_t it = 0, n[2] = {0, 0};
+      uint32_t it = 0, n[RT] = {};
       bool ok = true;
-      while (ok && seg_next(p, num_units, t, t_end, u, s)) {
-        const int nr = tiles_of(s);
+      while (ok && seg_next<RT>(p, num_units, t, t_end, u, s)) {
+        const int nr = tiles_of<RT>(s);
         for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
           constexpr uint32_t NV = F8 ? NCV : L::NS;
           const uint32_t st = it % NV;
           if (!(ok = wwait(F8 ? &bars->vc_full[st] : &bars->v_full[st], (it / NV) & 1))) break;
-          const int steps = steps_of(s, j);
+          const int steps = steps_of<RT>(s, j);
           for (int h = 0; ok && h < steps; ++h) {
             const uint64_t vd = vdesc0 + ((st * L::TILE + h * HK * 128) >> 4);
-            for (int r = 0; r < nr; ++r) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+              if (r >= nr) break;
               if (!(ok = wwait(&bars->p_full[r], n[r] & 1))) break;
               fence_after();
               ++n[r];
@@ -391,7 +420,7 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
       }
       __syncwarp();
     }
-  } else if (warp < CONV_WARP0) {
+  } else if (warp < L::CONV_WARP0) {
     // ------------------------------------------------------------ softmax of row tile r
     const int r = (warp - SOFTMAX_WARP0) >> 2;
     const int rr = (warp & 3) * 32 + lane;  // the thread's row in its tile = TMEM lane
@@ -400,14 +429,16 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
     Seg s;
     uint32_t it = 0, n = 0;  // tiles of the range; steps of this row tile
     bool ok = true;
-    while (ok && seg_next(p, num_units, t, t_end, u, s)) {
-      if (r >= tiles_of(s)) {
+    while (ok && seg_next<RT>(p, num_units, t, t_end, u, s)) {
+      if (r >= tiles_of<RT>(s)) {
         it += s.j1 - s.j0;
         continue;
       }
       const int row = r * MT + rr;
       const bool live = row < s.rows;
-      const int rg = s.mt * 2 * MT + (live ? row : r * MT);  // a dead row repeats a live one
+      const int rg = s.mt * RT * MT + (live ? row : r * MT);  // a dead row repeats a live one
+      // the row's last visible key (every row of a prefix sees all of it)
+      const int last = RT == 2 ? s.nkeys - 1 : s.last0 + rg / p.G;
       const uint4* qsrc = reinterpret_cast<const uint4*>(
           (const __nv_bfloat16*)p.q +
           ((s.q_off + rg / p.G) * p.Hq + (int64_t)s.g * p.G + rg % p.G) * HD);
@@ -415,28 +446,31 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
       uint8_t* qrow = smem + L::Q + r * L::QB + rr * 128;
       if constexpr (F8) {
         // Q row x 2^e, its largest magnitude in [128, 256), as hi + lo (attn_tc.cu)
-        uint32_t rq[HD / 2];
         uint32_t amax = 0;
 #pragma unroll
         for (int e = 0; e < HD / 8; ++e) {
           const uint4 v = __ldg(qsrc + e);
-          rq[4 * e] = v.x;
-          rq[4 * e + 1] = v.y;
-          rq[4 * e + 2] = v.z;
-          rq[4 * e + 3] = v.w;
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            amax = max(amax, max(rq[4 * e + k] & 0x7fffu, (rq[4 * e + k] >> 16) & 0x7fffu));
+          for (int k = 0; k < 4; ++k) amax = max(amax, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
         }
         const int eb = max((int)(amax >> 7), 1);
         const int e2 = amax == 0 ? 0 : min(max(134 - eb, -120), 120);
         const float f = __int_as_float((e2 + 127) << 23);
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 4; ++c) {  // 32 elements: 8 TMEM columns, two 16-byte chunks
-          uint32_t hi[8], lo[8];
+          uint32_t hi[8], lo[8], rq[16];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {  // the second read of the row
+            const uint4 v = __ldg(qsrc + 4 * c + e);
+            rq[4 * e] = v.x;
+            rq[4 * e + 1] = v.y;
+            rq[4 * e + 2] = v.z;
+            rq[4 * e + 3] = v.w;
+          }
 #pragma unroll
           for (int w = 0; w < 8; ++w) {
-            const uint32_t a = rq[16 * c + 2 * w], b = rq[16 * c + 2 * w + 1];
+            const uint32_t a = rq[2 * w], b = rq[2 * w + 1];
             const float x[4] = {__uint_as_float(a << 16) * f, __uint_as_float(a & 0xffff0000u) * f,
                                 __uint_as_float(b << 16) * f, __uint_as_float(b & 0xffff0000u) * f};
             split_q(x, hi[w], lo[w]);
@@ -473,7 +507,7 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
       float m_ref = -INFINITY, lh = 0.f;
       bool good = true;
       for (int j = s.j0; good && j < s.j1; ++j, ++it) {
-        const int steps = steps_of(s, j);
+        const int steps = steps_of<RT>(s, j);
         for (int h = 0; h < steps; ++h, ++n) {
           if (!(good = wwait(&bars->s_full[r], n & 1))) break;
           fence_after();
@@ -488,11 +522,18 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
           }
           fence_before();
           mbar_arrive(&bars->s_free[r]);  // the scores are in registers: the next S may start
-          const int left = s.nkeys - (j * KT + h * HK);  // keys of the prefix in this step
-          if (left < HK) {
+          const int key0 = j * KT + h * HK;
+          if (key0 + HK - 1 > last) {
+            const int left = last - key0;
 #pragma unroll
             for (int c = 0; c < HK; ++c)
-              if (c >= left) x[c] = -INFINITY;
+              if (c > left) x[c] = -INFINITY;
+          }
+          if (RT == 1 && key0 < s.start) {
+            const int low = s.start - key0;
+#pragma unroll
+            for (int c = 0; c < HK; ++c)
+              if (c < low) x[c] = -INFINITY;
           }
           float m8[8];
 #pragma unroll
@@ -548,17 +589,18 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
           }
           tmem_st32(tq + COL_P + r * 32, pk);
           tmem_wait_st();
-          if (!F8 && r == 0 && left < HK) {
-            // V rows past the prefix (another page's bits): zeros, so that P = 0 never meets
-            // non-finite data
+          const int first = RT == 1 ? max(s.start - key0, 0) : 0, end = min(s.nkeys - key0, HK);
+          if (!F8 && r == 0 && (first > 0 || end < HK)) {
+            // V rows before and past the part's keys may hold any bits: zeros, so that P = 0
+            // never meets non-finite data
             const uint32_t st = it % L::NS;
             if (!(good = wwait(&bars->v_full[st], (it / L::NS) & 1))) break;
-            uint8_t* vt = smem + L::V + st * L::RAW;
-            const int chunks = (HK - left) * 8;  // 16-byte chunks per column block
-            for (int q = rr; q < chunks * (HD / 64); q += 128) {
-              const int blk = q / chunks, rem = q % chunks;
-              *reinterpret_cast<uint4*>(vt + blk * L::BLK + (h * HK + left + rem / 8) * 128 +
-                                        (rem % 8) * 16) = make_uint4(0, 0, 0, 0);
+            uint8_t* vt = smem + L::V + st * L::RAW + h * HK * 128;
+            for (int q = rr; q < HK * 8 * (HD / 64); q += 128) {  // 16-byte chunks
+              const int key = (q / 8) % HK;
+              if (key < first || key >= end)
+                *reinterpret_cast<uint4*>(vt + q / (8 * HK) * L::BLK + key * 128 + (q % 8) * 16) =
+                    make_uint4(0, 0, 0, 0);
             }
             fence_proxy_async();
           }
@@ -575,7 +617,7 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
         ok = false;
         break;
       }
-      const size_t at = ((size_t)blockIdx.x + s.u) * (2 * MT) + row;
+      const size_t at = ((size_t)blockIdx.x + s.u) * (RT * MT) + row;
 #pragma unroll 1
       for (int c = 0; c < HD / 32; ++c) {
         uint32_t ro[32];
@@ -595,11 +637,11 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
   }
 
   if constexpr (F8) {
-    if (warp >= CONV_WARP0) {
+    if (warp >= L::CONV_WARP0) {
       // ---------------------------------------------------------- E4M3 -> f16 V decoding
       // As in attn_tc.cu: raw 128-byte swizzled rows in, the 16-bit MN-major operand layout
-      // out; rows past the prefix become zeros.
-      const int ct = (warp - CONV_WARP0) * 32 + lane;
+      // out; rows that are no keys of the part become zeros.
+      const int ct = (warp - L::CONV_WARP0) * 32 + lane;
       const int c = ct & 7;
       const int rw = (ct >> 3) ^ (c >> 2);
       const int ph = rw & 7;
@@ -611,7 +653,7 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
       Seg s;
       uint32_t it = 0;
       bool ok = true;
-      while (ok && seg_next(p, num_units, t, t_end, u, s)) {
+      while (ok && seg_next<RT>(p, num_units, t, t_end, u, s)) {
         for (int j = s.j0; j < s.j1; ++j, ++it) {
           const uint32_t rs = it % L::NS, cs = it % NCV;
           if (!mbar_wait(&bars->v_full[rs], (it / L::NS) & 1, wt) ||
@@ -627,7 +669,7 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
           for (int k = 0; k < KT / 16; ++k)
             w[k] = *reinterpret_cast<const uint4*>(rsrc + k * RSTEP);
           mbar_arrive(&bars->v_empty[rs]);
-          const int lim = s.nkeys - j * KT;  // rows >= lim lie past the prefix
+          const int lim = s.nkeys - j * KT, low = s.start - j * KT;  // the part's keys
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k) {
             uint32_t h[8];
@@ -635,7 +677,7 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
             e4m3x4_to_f16x4(w[k].y, h[2], h[3]);
             e4m3x4_to_f16x4(w[k].z, h[4], h[5]);
             e4m3x4_to_f16x4(w[k].w, h[6], h[7]);
-            if (rw + 16 * k >= lim) {
+            if (rw + 16 * k >= lim || rw + 16 * k < low) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) h[e] = 0u;
             }
@@ -658,29 +700,38 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + NCONV : NTHREADS, 1)
                  "r"(TMEM_COLS)
                  : "memory");
   }
+  if constexpr (RT == 1) pdl_wait();
 }
 
-template <int HD, bool F8>
+template <int HD, bool F8, int RT>
 cudaError_t launch_hd(const AttnParams& p, cudaStream_t s) {
-  using L = Layout<HD, F8>;
+  using L = Layout<HD, F8, RT>;
   CUtensorMap mk, mv;
-  const int box = p.block_size < KT ? p.block_size : KT;
+  const int box = p.block_size < L::KT ? p.block_size : L::KT;
   if (!kv_tensor_map(&mk, p.k, p.kv_rows, p.Hkv, HD, F8, box) ||
       !kv_tensor_map(&mv, p.v, p.kv_rows, p.Hkv, HD, F8, box))
     return cudaErrorInvalidValue;
-  auto kernel = attn_prefix_kernel<HD, F8>;
+  auto kernel = attn_parts_kernel<HD, F8, RT>;
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::SMEM);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(p.n_ctas), dim3(L::THREADS), L::SMEM, s, p, mk, mv);
 }
 
+template <int RT>
+cudaError_t launch_rt(const AttnParams& p, bool fp8, cudaStream_t s) {
+  if (!attn_tc_supports(p.d, fp8) || p.block_size == 0) return cudaErrorNotSupported;
+  if (fp8) return launch_hd<128, true, RT>(p, s);
+  return p.d == 128 ? launch_hd<128, false, RT>(p, s) : launch_hd<64, false, RT>(p, s);
+}
+
 }  // namespace
 
-cudaError_t launch_attn_prefix(const AttnParams& p, bool fp8, cudaStream_t s) {
-  if (!attn_tc_supports(p.d, fp8) || p.block_size == 0) return cudaErrorNotSupported;
-  if (fp8) return launch_hd<128, true>(p, s);
-  return p.d == 128 ? launch_hd<128, false>(p, s) : launch_hd<64, false>(p, s);
+cudaError_t launch_attn_prefixes(const AttnParams& p, bool fp8, cudaStream_t s) {
+  return launch_rt<2>(p, fp8, s);
+}
+cudaError_t launch_attn_sequences(const AttnParams& p, bool fp8, cudaStream_t s) {
+  return launch_rt<1>(p, fp8, s);
 }
 
 }  // namespace sv

@@ -102,7 +102,6 @@ __device__ __forceinline__ void split_q_e4m3(const float* x, uint32_t& whi, uint
 // HostPlan passed with the launch (kernel parameter space, read through the constant
 // cache; every read below is uniform across the threads that make it).
 struct WsPlan {
-  static constexpr bool SHARED = false;
   const AttnParams& p;
   __device__ int num_units() const { return p.hdr->num_units; }
   __device__ int2 cta(int c) const { return p.cta_tab[c]; }
@@ -112,13 +111,8 @@ struct WsPlan {
   __device__ int64_t kv_off(int b) const { return p.kv_off[b]; }
   __device__ int T(int b) const { return p.seq_lens[b]; }
   __device__ int D(int b) const { return p.draft_len[b]; }
-  __device__ int nkeys(int b) const { return T(b) + D(b) + 1; }
-  __device__ int table_row(int b) const { return b; }
-  __device__ int start(int) const { return 0; }
-  __device__ bool alone(int) const { return true; }
 };
 struct ParamPlan {
-  static constexpr bool SHARED = false;
   const HostPlan& h;
   __device__ int num_units() const { return h.num_units; }
   __device__ int2 cta(int c) const { return h.cta_tab[c]; }
@@ -128,29 +122,6 @@ struct ParamPlan {
   __device__ int64_t kv_off(int b) const { return h.kv_off[b]; }
   __device__ int T(int b) const { return h.T[b]; }
   __device__ int D(int b) const { return h.D[b]; }
-  __device__ int nkeys(int b) const { return T(b) + D(b) + 1; }
-  __device__ int table_row(int b) const { return b; }
-  __device__ int start(int) const { return 0; }
-  __device__ bool alone(int) const { return true; }
-};
-// Shared prefixes (internal.cuh, SharedSeq): units over the keys [start, nkeys) of a part,
-// a group's prefix or a sequence's own positions; their results are partials that the
-// combining kernel joins unless a sequence has one part only (alone).
-struct SharedPlan {
-  static constexpr bool SHARED = true;
-  const AttnParams& p;
-  __device__ int num_units() const { return p.hdr->num_units; }
-  __device__ int2 cta(int c) const { return p.cta_tab[c]; }
-  __device__ int4 unit(int u) const { return p.units[u]; }
-  __device__ int32_t ubeg(int u) const { return p.ubeg[u]; }
-  __device__ int64_t q_off(int b) const { return p.parts[b].q_off; }
-  __device__ int64_t kv_off(int) const { return 0; }  // paged caches only
-  __device__ int T(int b) const { return p.parts[b].last0; }
-  __device__ int D(int b) const { return p.parts[b].rows - 1; }
-  __device__ int nkeys(int b) const { return p.parts[b].nkeys; }
-  __device__ int table_row(int b) const { return p.parts[b].table_row; }
-  __device__ int start(int b) const { return p.parts[b].start; }
-  __device__ bool alone(int b) const { return p.parts[b].alone != 0; }
 };
 
 // One unit's share of a CTA's range: the unit's tiles [j0, j1), tile j holding cache
@@ -227,10 +198,7 @@ __device__ __forceinline__ void attn_tc_body(const AttnParams& p, const CUtensor
   volatile int* abort = &bars->abort;
   const Waiter wt{abort, p.flags, p.wait_limit > 0 ? p.wait_limit : TIMEOUT_CYCLES};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // The plan of this call is complete. (Shared prefixes: the kernel before this one is the
-  // prefixes', whose CTAs let this grid start once each had waited for the plan; this grid
-  // waits for it at its end.)
-  if constexpr (!Plan::SHARED) pdl_wait();
+  pdl_wait();  // the plan of this call is complete
 
   const int num_units = pl.num_units();
   const int2 rb = pl.cta(blockIdx.x), re = pl.cta(blockIdx.x + 1);
@@ -335,9 +303,9 @@ __device__ __forceinline__ void attn_tc_body(const AttnParams& p, const CUtensor
     while (ok && seg_next<WIN>(pl, num_units, t, t_end, u, s)) {
       const int row0 = (int)pl.kv_off(s.b) + s.kbase;
       const int T = pl.T(s.b);
-      const int nkeys = pl.nkeys(s.b);
-      const int kvis = Plan::SHARED ? pl.start(s.b) : first_visible_key(T, window);
-      const int32_t* tab = p.block_table + (size_t)pl.table_row(s.b) * p.bt_stride;
+      const int nkeys = T + pl.D(s.b) + 1;
+      const int kvis = first_visible_key(T, window);
+      const int32_t* tab = p.block_table + (size_t)s.b * p.bt_stride;
       // Paged: the block-table entries of a group of tg = 32 / nbox tiles are loaded one
       // per lane (lane l: tile l / nbox of the group, box l % nbox) a whole group ahead of
       // their use, so that no lookup waits behind this SM's copies in flight; at its tile
@@ -526,12 +494,11 @@ __device__ __forceinline__ void attn_tc_body(const AttnParams& p, const CUtensor
       const int D = pl.D(s.b);
       const int rows_total = p.G * (D + 1);
       const int rows = min(MT, rows_total - s.mt * MT);
-      const int nkeys = pl.nkeys(s.b) - s.kbase;
+      const int nkeys = T + D + 1;
       const int rg = s.mt * MT + r;
       const bool live = r < rows;
       const int i_row = live ? rg / p.G : D;
-      // the row's last visible key (every row of a shared prefix sees all of it)
-      const int hi_row = Plan::SHARED ? min(T + i_row, nkeys - 1) : T + i_row;
+      const int hi_row = T + i_row;  // the row's last visible key
       const int hl = live ? rg % p.G : 0;
       const int64_t qrow = pl.q_off(s.b) + i_row;
       float sc = p.scale_log2;  // score scale in log2 units
@@ -619,8 +586,7 @@ __device__ __forceinline__ void attn_tc_body(const AttnParams& p, const CUtensor
         const int key0 = j * KT + wg * HK;
         // the window-causal mask (key <= T + i) or the sliding window's lower edge
         // (key >= T + i - window + 1) reaches into this half tile for this row
-        // (used only under a sliding window, or behind a shared prefix)
-        const int lo_row = Plan::SHARED ? pl.start(s.b) - s.kbase : hi_row + 1 - window;
+        const int lo_row = hi_row + 1 - window;  // (used only under a sliding window)
         if (key0 + HK - 1 > hi_row) {
           const int lim = hi_row - key0;
 #pragma unroll
@@ -716,7 +682,7 @@ __device__ __forceinline__ void attn_tc_body(const AttnParams& p, const CUtensor
         tmem_wait_st();
         bool zeroed = false;
         // under a sliding window, keys before T - window + 1 left every row's window
-        const int kvis = Plan::SHARED ? lo_row : WIN ? T + 1 - window : -1;
+        const int kvis = WIN ? T + 1 - window : -1;
         if (!F8 && (key0 + HK > nkeys || key0 < kvis)) {
           // clear this half's V rows past the sequence's end (they may hold the next
           // sequence or unwritten memory) and, under a sliding window, before the first
@@ -763,7 +729,7 @@ __device__ __forceinline__ void attn_tc_body(const AttnParams& p, const CUtensor
       const float a0 = m0 == -INFINITY ? 0.f : ex2(m0 - m);
       const float a1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
       const float l = a0 * bars->xl[0][r] + a1 * bars->xl[1][r];
-      const bool whole = s.whole && pl.alone(s.b);
+      const bool whole = s.whole;
       const float inv = whole ? vs / l : 1.f;
       auto merged = [&](uint32_t o0, uint32_t o1) {  // an accumulator without tiles is skipped
         return (a0 != 0.f ? a0 * __uint_as_float(o0) : 0.f) +
@@ -832,8 +798,8 @@ __device__ __forceinline__ void attn_tc_body(const AttnParams& p, const CUtensor
       while (ok && seg_next<WIN>(pl, num_units, t, t_end, u, s)) {
         // cache positions relative to the unit's first tile
         const int T = pl.T(s.b) - s.kbase;
-        const int nkeys = pl.nkeys(s.b) - s.kbase;
-        const int kvis = Plan::SHARED ? pl.start(s.b) - s.kbase : WIN ? T + 1 - window : -1;
+        const int nkeys = T + pl.D(s.b) + 1;
+        const int kvis = WIN ? T + 1 - window : -1;
         for (int j = s.j0; j < s.j1; ++j, ++it) {
           const uint32_t rs = it % L::NR, cs = it % NCV;
           if (!mbar_wait(&bars->v_full[rs], (it / L::NR) & 1, wt) ||
@@ -919,18 +885,6 @@ __global__ void __launch_bounds__(F8 ? NTHREADS + 128 : NTHREADS, 1)
   attn_tc_body<HD, F8, WIN, SPLIT>(p, tmk, tmv, ParamPlan{hp});
 }
 
-// Shared prefixes: the plan in the workspace, units over parts (see SharedPlan). Built on
-// the sliding-window form, whose lower mask edge and cleared V rows serve the part's start.
-// It runs beside the tail of the prefixes' kernel (attn_prefix.cu), and its completion
-// stands for that kernel's too: each CTA waits for it before it ends.
-template <int HD, bool F8, bool SPLIT>
-__global__ void __launch_bounds__(F8 ? NTHREADS + 128 : NTHREADS, 1)
-    attn_tc_kernel_shared(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
-                          const __grid_constant__ CUtensorMap tmv) {
-  attn_tc_body<HD, F8, true, SPLIT>(p, tmk, tmv, SharedPlan{p});
-  pdl_wait();
-}
-
 // ---------------------------------------------------------------- host side
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -1004,21 +958,6 @@ cudaError_t launch_hd(const AttnParams& p, cudaStream_t s) {
   return p.window > 0 ? launch_hd<HD, F8, true>(p, s) : launch_hd<HD, F8, false>(p, s);
 }
 
-template <int HD, bool F8, bool SPLIT>
-cudaError_t launch_hd_shared(const AttnParams& p, cudaStream_t s) {
-  using L = TcLayout<HD, F8, SPLIT>;
-  CUtensorMap mk, mv;
-  const int box = min(p.block_size, KT);
-  if (!make_kv_map(&mk, p.k, p.kv_rows, p.Hkv, HD, F8, box) ||
-      !make_kv_map(&mv, p.v, p.kv_rows, p.Hkv, HD, F8, box))
-    return cudaErrorInvalidValue;
-  auto kernel = attn_tc_kernel_shared<HD, F8, SPLIT>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::SMEM);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(p.n_ctas), dim3(L::THREADS), L::SMEM, s, p, mk, mv);
-}
-
 template <int HD, bool F8, bool WIN, bool SPLIT>
 cudaError_t launch_hd_hp(const AttnParams& p, const HostPlan& hp, cudaStream_t s) {
   using L = TcLayout<HD, F8, SPLIT>;
@@ -1067,16 +1006,6 @@ cudaError_t launch_attn_tc_hp(const AttnParams& p, bool fp8, const HostPlan& hp,
     return cudaErrorNotSupported;
   if (fp8) return launch_hd_hp<128, true>(p, hp, s);
   return p.d == 128 ? launch_hd_hp<128, false>(p, hp, s) : launch_hd_hp<64, false>(p, hp, s);
-}
-
-cudaError_t launch_attn_tc_shared(const AttnParams& p, bool fp8, cudaStream_t s) {
-  if (!attn_tc_supports(p.d, fp8) || p.block_size == 0) return cudaErrorNotSupported;
-  if (fp8) return launch_hd_shared<128, true, false>(p, s);
-  if (p.kv_rings)
-    return p.d == 128 ? launch_hd_shared<128, false, true>(p, s)
-                      : launch_hd_shared<64, false, true>(p, s);
-  return p.d == 128 ? launch_hd_shared<128, false, false>(p, s)
-                    : launch_hd_shared<64, false, false>(p, s);
 }
 
 cudaError_t launch_attn_tc(const AttnParams& p, bool fp8, cudaStream_t s) {

@@ -110,7 +110,17 @@ struct SharedSeq {
   int32_t nmt, nt;    // row tiles and key tiles of a (part, KV head)
   int32_t ubase;      // a sequence's first unit
   int32_t tbase;      // its first tile on the tile line
-  int32_t mbase;      // a prefix's first row tile among those of all prefixes
+  int32_t mbase;      // the place of a prefix's first row tile among those of all prefixes
+};
+
+// Where a window row's partial results are.
+struct RowInfo {
+  int32_t i;         // row of its sequence's window
+  int32_t ubase;     // the sequence's first unit
+  int32_t nmt;       // the sequence's row tiles per KV head
+  int32_t mbase;     // the first place of its prefix's row tiles (-1: no prefix)
+  int32_t of_group;  // row among those of its group
+  int32_t pad[3];
 };
 
 struct AttnParams {
@@ -152,10 +162,11 @@ struct AttnParams {
   // shared prefixes only
   SharedSeq* parts;           // [num_groups + B]
   int32_t* row_begin;         // [B] first window row of each sequence
-  int32_t* row_seq;           // [window rows] each one's sequence
+  RowInfo* rows;              // [window rows]
   int32_t* tile_unit;         // [row tiles of the prefixes] first of the Hkv units of each
   int2* unit_ctas;            // [U] first and last CTA that a unit's tiles fall to
   int row_tile;               // query rows of a prefix's unit
+  int kt;                     // keys per tile of the line
   int num_groups;
   const int32_t* group_begin;  // [num_groups + 1]
   const int32_t* prefix_len;   // [num_groups]
@@ -258,17 +269,18 @@ struct SharedWs {
   struct Line {
     size_t hdr, units, ubeg, unit_ctas, cta_tab, part_o, part_ml;
   };
-  size_t parts, row_begin, row_seq, tile_unit, total;
+  size_t parts, row_begin, rows, tile_unit, total;
   Line line[2];
   int64_t max_units[2];
+  int n_ctas[2];
 };
-SharedWs shared_ws_layout(const sv_attn_desc* d, int num_groups, int n_ctas, bool lines);
-cudaError_t launch_plan_shared(const AttnParams& pa, const AttnParams& pb, bool lines, int kt,
+SharedWs shared_ws_layout(const sv_attn_desc* d, int num_groups, int sms, bool lines);
+cudaError_t launch_plan_shared(const AttnParams& pa, const AttnParams& pb, bool lines,
                                cudaStream_t s);
 cudaError_t launch_combine_shared(const AttnParams& pa, const AttnParams& pb, cudaStream_t s);
-cudaError_t launch_attn_prefix(const AttnParams& p, bool fp8, cudaStream_t s);
+cudaError_t launch_attn_prefixes(const AttnParams& p, bool fp8, cudaStream_t s);
+cudaError_t launch_attn_sequences(const AttnParams& p, bool fp8, cudaStream_t s);
 cudaError_t launch_attn_mma_shared(const AttnParams& p, bool fp8, cudaStream_t s);
-cudaError_t launch_attn_tc_shared(const AttnParams& p, bool fp8, cudaStream_t s);
 
 // Launchers (each returns the cudaGetLastError() of its launch).
 cudaError_t launch_plan(const AttnParams& p, int kt, cudaStream_t s);

@@ -8,9 +8,9 @@
 // (G * sum W rows: full tensor-core tiles, and one read of the prefix per unit's rows instead
 // of one per sequence), and what is behind it one part per sequence (internal.cuh,
 // SharedSeq). Units lie on a tile line split over the CTAs like that of spec_verify_attn
-// (internal.cuh). tcgen05 kernels: the prefixes' units, of 256 rows, on a line of their own
-// (attn_prefix.cu), the sequences' on another (attn_tc.cu). mma.sync kernel: all units, of
-// 128 rows, on one line. A row's partial results are joined by combine_shared.
+// (internal.cuh). tcgen05 kernels (attn_parts.cu): the prefixes' units, of 256 rows, on a
+// line of their own, the sequences' on another. mma.sync kernel: all units, of 128 rows, on
+// one line. A row's partial results are joined by combine_shared.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -64,6 +64,12 @@ __device__ void scan_block(const int64_t (&v)[N], int64_t (&ex)[N], int64_t (&to
 
 constexpr int MAJOR_ENTRIES = 16384;
 
+// The place of a prefix's first row tile among those of all prefixes: with q_off window rows
+// and n prefixes before it there are at most this many row tiles before it.
+__device__ __forceinline__ int32_t tile_base(int64_t q_off, int G, int row_tile, int n) {
+  return (int32_t)(q_off * G / row_tile + n);
+}
+
 // The last index in [0, n) whose key is at most x (keys not decreasing, key(0) <= x).
 template <class F>
 __device__ __forceinline__ int last_at_most(int n, int64_t x, F key) {
@@ -78,11 +84,11 @@ __device__ __forceinline__ int last_at_most(int n, int64_t x, F key) {
 // CTA `line` of 2 (or the one CTA of a single line) checks the call, describes its parts and
 // writes its line: line 0 the prefixes (pa), line 1 the sequences (pb). Both CTAs make the
 // same checks, so a call is skipped as a whole.
-__global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, AttnParams pb, int kt) {
+__global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, AttnParams pb) {
   const bool both = gridDim.x == 1;  // one line for all parts
   const bool prefixes = both || blockIdx.x == 0, sequences = both || blockIdx.x == 1;
   const AttnParams& p = prefixes && !both ? pa : pb;
-  const int tid = threadIdx.x, NG = p.num_groups, B = p.B;
+  const int tid = threadIdx.x, NG = p.num_groups, B = p.B, kt = p.kt;
   __shared__ int s_maxmt;
   pdl_trigger();
   pdl_wait();
@@ -137,40 +143,33 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
     bad = __syncthreads_or(bad);
   }
   bad = bad || q_total > p.q_rows;
-  // the prefixes: their parts, and the first of each one's row tiles
-  const int rows_of_tile = p.row_tile;
-  int64_t n_tiles = 0;  // row tiles of all prefixes
-  for (int base = 0; base < NG && prefixes && !bad; base += PLAN_T) {
-    const int n = base + tid;
+  // the prefixes: their parts
+  const int row_tile = p.row_tile;
+  for (int n = tid; n < NG && prefixes && !bad; n += PLAN_T) {
+    const int g0 = p.group_begin[n], g1 = p.group_begin[n + 1], P = p.prefix_len[n];
     SharedSeq s = {};
-    if (n < NG) {
-      const int g0 = p.group_begin[n], g1 = p.group_begin[n + 1], P = p.prefix_len[n];
-      s.q_off = g0 < B ? p.row_begin[g0] : q_total;
-      const int64_t end = g1 < B ? p.row_begin[g1] : q_total;
-      s.rows = P > 0 ? (int)(end - s.q_off) : 0;
-      s.nkeys = P;
-      s.last0 = P - 1;
-      s.table_row = g0;
-      s.group = n;
-      s.nmt = (int)(((int64_t)p.G * s.rows + rows_of_tile - 1) / rows_of_tile);
-      s.nt = (P + kt - 1) / kt;
-      atomicMax(&s_maxmt, s.nmt);
-    }
-    const int64_t c[1] = {s.nmt};
-    int64_t ex[1], tot[1];
-    scan_block<1>(c, ex, tot);
-    s.mbase = (int32_t)(n_tiles + ex[0]);
-    if (n < NG) p.parts[n] = s;
-    n_tiles += tot[0];
+    s.q_off = g0 < B ? p.row_begin[g0] : q_total;
+    const int64_t end = g1 < B ? p.row_begin[g1] : q_total;
+    s.rows = P > 0 ? (int)(end - s.q_off) : 0;
+    s.nkeys = P;
+    s.last0 = P - 1;
+    s.table_row = g0;
+    s.group = n;
+    s.nmt = (int)(((int64_t)p.G * s.rows + row_tile - 1) / row_tile);
+    s.nt = (P + kt - 1) / kt;
+    s.mbase = tile_base(s.q_off, p.G, row_tile, n);
+    atomicMax(&s_maxmt, s.nmt);
+    p.parts[n] = s;
   }
   __syncthreads();
   // Units of the prefixes, entry (row tile mt, part v) by entry, the KV heads of an entry
   // together. Row-tile-major (mt first), so that the slices of the line that read the same
   // prefix are read by their CTAs at about the same time and share it through L2; with very
-  // many groups of very different sizes part-major, which needs no empty entries.
+  // many groups of very different sizes part-major, over the row tiles' places.
   const int maxmt = s_maxmt;
   const bool major = (int64_t)maxmt * NG <= MAJOR_ENTRIES;
-  const int64_t entries = prefixes && !bad ? (major ? (int64_t)maxmt * NG : n_tiles) : 0;
+  const int64_t entries =
+      prefixes && !bad ? (major ? (int64_t)maxmt * NG : tile_base(q_total, p.G, row_tile, NG)) : 0;
   int64_t U = 0, TT = 0;
   for (int64_t base = 0; base < entries; base += PLAN_T) {
     const int64_t e = base + tid;
@@ -226,7 +225,6 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
     p.hdr->num_units = (int32_t)U;
     p.hdr->total_tiles = (int32_t)TT;
     p.hdr->kt = kt;
-    p.hdr->unit_ctas = 0;
     p.hdr->sum_w = bad ? 0 : q_total;
     p.ubeg[U] = (int32_t)TT;
   }
@@ -239,16 +237,25 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
     p.ubeg[u] = s.tbase + k * s.nt;
   }
   if (sequences && !bad)
-    for (int b = tid; b < B; b += PLAN_T)
-      for (int i = 0; i < seq[b].rows; ++i) p.row_seq[seq[b].q_off + i] = b;
+    for (int b = tid; b < B; b += PLAN_T) {
+      const SharedSeq s = seq[b];
+      const int64_t q0 = seq[p.group_begin[s.group]].q_off;  // the group's first row
+      RowInfo r = {0, s.ubase, s.nmt, s.alone ? -1 : tile_base(q0, p.G, row_tile, s.group), 0, {}};
+      for (int i = 0; i < s.rows; ++i) {
+        r.i = i;
+        r.of_group = (int)(s.q_off - q0) + i;
+        p.rows[s.q_off + i] = r;
+      }
+    }
   __syncthreads();
-  // CTA c starts at the first tile at or after position c * VT / C of the virtual line;
-  // which CTAs' partials make up a unit
+  // CTA c starts at the first tile at or after position c * VT / C of the virtual line, C at
+  // most VT, so that every CTA between the first and the last of a unit has tiles of it
   const int64_t X = p.switch_tiles, VT = TT + U * X;
+  const int C = (int)min((int64_t)p.n_ctas, max(VT, (int64_t)1));
   for (int c = tid; c <= p.n_ctas; c += PLAN_T) {
     int2 e = make_int2((int32_t)TT, (int32_t)U);
-    if (c < p.n_ctas && TT > 0) {
-      const int64_t v0 = (int64_t)c * VT / p.n_ctas;
+    if (c < C && TT > 0) {
+      const int64_t v0 = (int64_t)c * VT / C;
       const int u = last_at_most((int)U, v0, [&](int i) { return p.ubeg[i] + (int64_t)i * X; });
       const int64_t into = v0 - (p.ubeg[u] + (int64_t)u * X) - X;  // < 0: before its tiles
       e = make_int2((int32_t)(p.ubeg[u] + (into > 0 ? into : 0)), u);
@@ -256,17 +263,19 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
     p.cta_tab[c] = e;
   }
   for (int u = tid; u < (int)U; u += PLAN_T)
-    p.unit_ctas[u] = make_int2(cta_of_tile(vpos_of_tile(p.ubeg[u], u, (int)X), VT, p.n_ctas),
-                               cta_of_tile(vpos_of_tile((int64_t)p.ubeg[u + 1] - 1, u, (int)X), VT, p.n_ctas));
+    p.unit_ctas[u] =
+        make_int2(cta_of_tile(vpos_of_tile(p.ubeg[u], u, (int)X), VT, C),
+                  cta_of_tile(vpos_of_tile((int64_t)p.ubeg[u + 1] - 1, u, (int)X), VT, C));
 }
 
-// One output row (window row, query head) per group of 8 lanes, PER columns a lane: joins
-// the partials that the row's prefix unit and its sequence's unit left, in batches whose
-// loads are all issued before any use. A unit's CTAs with no tile of it (an empty range, or
-// one that ends in the unit's switch) left none.
+// One output row (window row, query head) per group of 8 lanes, HD / 8 columns a lane: joins
+// the partials that the row's prefix unit and its sequence's unit left, two at a time.
+// Memory-bound: reads each partial row (4 d + 8 bytes) once and writes 2 d bytes; what costs
+// is the chain of dependent reads before the partials (row, units, their CTAs), so rows are
+// many to a warp and their tables small.
 template <int HD>
 __global__ void __launch_bounds__(256) combine_shared_kernel(AttnParams pa, AttnParams pb) {
-  constexpr int PER = HD / 8, MAXP = 4;
+  constexpr int PER = HD / 8, MAXP = 2;
   pdl_trigger();
   pdl_wait();
   const int64_t rows = min(pa.hdr->sum_w, pb.hdr->sum_w) * pb.Hq;  // 0: the call was refused
@@ -274,23 +283,22 @@ __global__ void __launch_bounds__(256) combine_shared_kernel(AttnParams pa, Attn
   for (int64_t o = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3); o < rows;
        o += (int64_t)gridDim.x * 32) {
     const int64_t w = o / pb.Hq;
-    const int h = (int)(o % pb.Hq), g = h / pb.G;
-    const SharedSeq* sp = pb.parts + pb.num_groups + pb.row_seq[w];
-    const int rg = (int)(w - sp->q_off) * pb.G + h % pb.G;
-    const int us = sp->ubase + g * sp->nmt + rg / MT;
+    const int h = (int)(o - w * pb.Hq), g = h / pb.G, hl = h - g * pb.G;
+    const RowInfo r = pb.rows[w];
+    const int rs = r.i * pb.G + hl, us = r.ubase + g * r.nmt + rs / MT;
     const int2 cs = pb.unit_ctas[us];
-    const bool alone = sp->alone != 0;
-    if (alone && cs.x == cs.y) continue;  // one CTA saw the unit and wrote the output
     int ua = 0, ra = 0;
     int2 ca = make_int2(0, -1);
-    if (!alone) {
-      const SharedSeq* pre = pa.parts + sp->group;
-      const int64_t pr = (w - pre->q_off) * pb.G + h % pb.G;
-      ua = pa.tile_unit[pre->mbase + (int)(pr / pa.row_tile)] + g;
+    if (r.mbase >= 0) {
+      const int64_t pr = (int64_t)r.of_group * pb.G + hl;
+      ua = pa.tile_unit[r.mbase + (int)(pr / pa.row_tile)] + g;
       ra = (int)(pr % pa.row_tile);
       ca = pa.unit_ctas[ua];
     }
+    // the partials' rows, first those of the sequence's unit
     const int ns = cs.y - cs.x + 1, n = ns + ca.y - ca.x + 1;
+    const int64_t at_s = ((int64_t)cs.x + us) * MT + rs % MT;
+    const int64_t at_a = ((int64_t)ca.x + ua) * pa.row_tile + ra;
     float m = -INFINITY, l = 0.f, acc[PER];
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] = 0.f;
@@ -298,34 +306,28 @@ __global__ void __launch_bounds__(256) combine_shared_kernel(AttnParams pa, Attn
       float2 ml[MAXP];
       float4 ov[MAXP][PER / 4];
 #pragma unroll
-      for (int k = 0; k < MAXP; ++k) {
-        const int i = k0 + k;
+      for (int k = 0; k < MAXP; ++k) {  // an unused place repeats the last one, with l = 0
+        const int i = min(k0 + k, n - 1);
         const bool own = i < ns;
-        const AttnParams& p = own ? pb : pa;
-        const int c = own ? cs.x + i : ca.x + i - ns, u = own ? us : ua;
-        bool use = i < n;
-        if (use) {  // has CTA c tiles of unit u?
-          const int b0 = p.cta_tab[c].x, b1 = p.cta_tab[c + 1].x;
-          use = max(b0, p.ubeg[u]) < min(b1, p.ubeg[u + 1]);
-        }
-        const size_t at = ((size_t)c + u) * (own ? MT : pa.row_tile) + (own ? rg % MT : ra);
-        ml[k] = use ? p.part_ml[at] : make_float2(-INFINITY, 0.f);
-        const float4* src = reinterpret_cast<const float4*>(p.part_o + at * HD) + sub;
+        const int64_t at = own ? at_s + (int64_t)i * MT : at_a + (int64_t)(i - ns) * pa.row_tile;
+        ml[k] = (own ? pb.part_ml : pa.part_ml)[at];
+        if (k0 + k >= n) ml[k] = make_float2(-INFINITY, 0.f);
+        const float4* src = reinterpret_cast<const float4*>((own ? pb.part_o : pa.part_o) + at * HD) + sub;
 #pragma unroll
-        for (int e = 0; e < PER / 4; ++e)
-          ov[k][e] = use ? __ldcs(src + e * 8) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int e = 0; e < PER / 4; ++e) ov[k][e] = __ldcs(src + e * 8);
       }
       float bm = m;
 #pragma unroll
       for (int k = 0; k < MAXP; ++k) bm = fmaxf(bm, ml[k].x);
       const float mu = bm == -INFINITY ? 0.f : bm;
-      const float rs = exp2f(m - mu);
-      l *= rs;
+      const float rescale = exp2f(m - mu);
+      l *= rescale;
 #pragma unroll
-      for (int e = 0; e < PER; ++e) acc[e] *= rs;
+      for (int e = 0; e < PER; ++e) acc[e] *= rescale;
 #pragma unroll
       for (int k = 0; k < MAXP; ++k) {
-        const float wgt = exp2f(ml[k].x - mu);  // 0 for unused slots (m = -inf)
+        if (k0 + k >= n) continue;
+        const float wgt = exp2f(ml[k].x - mu);
         l += ml[k].y * wgt;
 #pragma unroll
         for (int e = 0; e < PER / 4; ++e) {
@@ -350,7 +352,7 @@ __global__ void __launch_bounds__(256) combine_shared_kernel(AttnParams pa, Attn
 
 }  // namespace
 
-SharedWs shared_ws_layout(const sv_attn_desc* d, int num_groups, int n_ctas, bool lines) {
+SharedWs shared_ws_layout(const sv_attn_desc* d, int num_groups, int sms, bool lines) {
   SharedWs w = {};
   const int64_t G = d->num_q_heads / d->num_kv_heads;
   const int64_t rows = std::min(d->q_rows, (int64_t)d->batch * (1 + d->max_draft_len));
@@ -364,11 +366,12 @@ SharedWs shared_ws_layout(const sv_attn_desc* d, int num_groups, int n_ctas, boo
   size_t o = 256;  // the flag word
   w.parts = o;     o = align_up(o + sizeof(SharedSeq) * ((size_t)num_groups + d->batch), 256);
   w.row_begin = o; o = align_up(o + sizeof(int32_t) * d->batch, 256);
-  w.row_seq = o;   o = align_up(o + sizeof(int32_t) * rows, 256);
+  w.rows = o;      o = align_up(o + sizeof(RowInfo) * rows, 256);
   w.tile_unit = o; o = align_up(o + sizeof(int32_t) * prefix_tiles, 256);
   for (int k = lines ? 0 : 1; k < 2; ++k) {
     SharedWs::Line& l = w.line[k];
-    const size_t U = (size_t)w.max_units[k], slots = U + n_ctas;
+    w.n_ctas[k] = lines && k == 1 ? 2 * sms : sms;
+    const size_t n_ctas = w.n_ctas[k], U = (size_t)w.max_units[k], slots = U + n_ctas;
     l.hdr = o;       o += 256;
     l.units = o;     o = align_up(o + sizeof(int4) * U, 256);
     l.ubeg = o;      o = align_up(o + sizeof(int32_t) * (U + 1), 256);
@@ -378,19 +381,22 @@ SharedWs shared_ws_layout(const sv_attn_desc* d, int num_groups, int n_ctas, boo
     l.part_o = o;    o = align_up(o + sizeof(float) * slot_rows * d->head_dim, 256);
     l.part_ml = o;   o = align_up(o + sizeof(float2) * slot_rows, 256);
   }
-  if (!lines) w.line[0] = w.line[1];
+  if (!lines) {
+    w.line[0] = w.line[1];
+    w.n_ctas[0] = w.n_ctas[1];
+  }
   w.total = o;
   return w;
 }
 
-cudaError_t launch_plan_shared(const AttnParams& pa, const AttnParams& pb, bool lines, int kt,
+cudaError_t launch_plan_shared(const AttnParams& pa, const AttnParams& pb, bool lines,
                                cudaStream_t s) {
-  return launch_pdl(plan_shared_kernel, dim3(lines ? 2 : 1), dim3(PLAN_T), 0, s, pa, pb, kt);
+  return launch_pdl(plan_shared_kernel, dim3(lines ? 2 : 1), dim3(PLAN_T), 0, s, pa, pb);
 }
 
 cudaError_t launch_combine_shared(const AttnParams& pa, const AttnParams& pb, cudaStream_t s) {
   const int64_t ctas = (pb.q_rows * pb.Hq + 31) / 32;
-  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(ctas, 8 * (int64_t)pb.n_ctas));
+  const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(ctas, 8 * (int64_t)pa.n_ctas));
   return pb.d == 128 ? launch_pdl(combine_shared_kernel<128>, dim3(grid), dim3(256), 0, s, pa, pb)
                      : launch_pdl(combine_shared_kernel<64>, dim3(grid), dim3(256), 0, s, pa, pb);
 }

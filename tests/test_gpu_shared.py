@@ -74,7 +74,7 @@ def test_nothing_shared_is_the_paged_call(kernel):
 @pytest.mark.parametrize("junk", [-1, 1 << 30])
 def test_entries_before_the_prefix_end_are_not_read(kernel, junk):
     w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=9)
-    ws = sv.new_workspace(1 << 25)
+    ws = sv.new_workspace(1 << 27)
     assert_within(run(x, pages(x, gb, P, 16, seed=4, junk=junk), gb, P, workspace=ws), w, x)
     assert sv.workspace_status(ws) == 0
 
@@ -140,7 +140,7 @@ def test_rows_behind_the_batch_are_left(kernel):
 def test_same_bits_every_time_and_on_a_used_workspace(kernel):
     w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=14)
     pg = pages(x, gb, P, 16, seed=4)
-    ws = sv.new_workspace(1 << 25)
+    ws = sv.new_workspace(1 << 27)
     first = run(x, pg, gb, P, workspace=ws)
     ws[256:] = 0xFF  # NaN in all but the flags: nothing stale is read
     assert np.array_equal(run(x, pg, gb, P, workspace=ws), first)
@@ -153,7 +153,7 @@ def test_same_bits_every_time_and_on_a_used_workspace(kernel):
 def test_lengths_out_of_range_are_reported(kernel, field, at, value):
     w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=15)
     pg = pages(x, gb, P, 16, seed=4)
-    ws = sv.new_workspace(1 << 25)
+    ws = sv.new_workspace(1 << 27)
     out = torch.full(x["q"].shape, 7.0, dtype=torch.bfloat16, device="cuda")
     bad = dict(gb=gb.copy(), P=P.copy(), T=x["seq_lens"].copy(), D=x["draft_len"].copy())
     bad[field][at] = value
@@ -168,7 +168,7 @@ def test_lengths_out_of_range_are_reported(kernel, field, at, value):
 def test_more_rows_than_q_holds_and_narrow_tables(kernel):
     w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=16)
     pg = pages(x, gb, P, 16, seed=4)
-    ws = sv.new_workspace(1 << 25)
+    ws = sv.new_workspace(1 << 27)
     run(dict(x, q=x["q"][:-1]), pg, gb, P, workspace=ws)
     assert sv.workspace_status(ws, clear=True) == 8
     narrow = dict(pg, block_table=np.ascontiguousarray(pg["block_table"][:, :20]))
@@ -178,7 +178,7 @@ def test_more_rows_than_q_holds_and_narrow_tables(kernel):
 
 def test_table_entry_outside_the_pool_is_reported(kernel):
     w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=17)
-    ws = sv.new_workspace(1 << 25)
+    ws = sv.new_workspace(1 << 27)
     for row, col in ((0, 3), (1, 18), (5, 20)):  # a prefix's, and two own entries
         pg = pages(x, gb, P, 16, seed=4)
         assert pg["block_table"][row, col] >= 0
@@ -195,7 +195,7 @@ def test_graph_replay_follows_new_lengths(kernel):
     i32 = lambda a: torch.from_numpy(np.asarray(a, dtype=np.int32)).cuda()  # noqa: E731
     g_, p_ = i32(gb), i32(P)
     out = torch.empty_like(q)
-    ws = sv.new_workspace(1 << 25)
+    ws = sv.new_workspace(1 << 27)
     call = lambda: sv.spec_verify_attn_shared(q, k, v, bt, T, D, g_, p_, max_draft_len=7,  # noqa: E731
                                               max_seq_len=1000, out=out, workspace=ws)
     s = torch.cuda.Stream()
@@ -241,7 +241,7 @@ def test_failed_launch_is_reported_and_the_workspace_serves_on(after):
     ensure_built()
     w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=20)
     pg = pages(x, gb, P, 16, seed=4)
-    ws = sv.new_workspace(1 << 25)
+    ws = sv.new_workspace(1 << 27)
     sv.api.inject_launch_failure(after)
     with pytest.raises(sv.SpecVerifyError) as e:
         run(x, pg, gb, P, workspace=ws)
@@ -255,7 +255,7 @@ def test_bounded_wait_runs_out_and_the_call_returns(kv):
     ensure_built()
     w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, kv=kv, seed=21)
     pg = pages(x, gb, P, 16, seed=4)
-    ws = sv.new_workspace(1 << 25)
+    ws = sv.new_workspace(1 << 27)
     sv.api.inject_wait_timeout(100000)
     run(x, pg, gb, P, workspace=ws)
     assert sv.workspace_status(ws, clear=True) == 7
