@@ -477,6 +477,7 @@ SV_API sv_status spec_verify_attn_shared(const sv_attn_desc* desc, const void* q
     if (lines) l.switch_tiles = k == 0 ? SWITCH_TILES_PREFIX : SWITCH_TILES_SEQUENCE;
     l.hdr = (PlanHdr*)(ws + lay.line[k].hdr);
     l.units = (int4*)(ws + lay.line[k].units);
+    l.sunits = (SharedUnit*)(ws + lay.line[k].sunits);
     l.ubeg = (int32_t*)(ws + lay.line[k].ubeg);
     l.unit_ctas = (int2*)(ws + lay.line[k].unit_ctas);
     l.cta_tab = (int2*)(ws + lay.line[k].cta_tab);

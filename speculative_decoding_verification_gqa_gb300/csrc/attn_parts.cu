@@ -53,6 +53,22 @@ struct __align__(8) Bars {
   int abort;
 };
 
+// The 128 threads of row tile r's warpgroup meet; with `v`, whether it held for all of them.
+__device__ __forceinline__ void wg_sync(int r) {
+  asm volatile("barrier.sync %0, 128;" ::"r"(1 + r) : "memory");
+}
+__device__ __forceinline__ bool wg_and(int r, bool v) {
+  __syncwarp();  // the reduction counts whole warps: arrive converged
+  uint32_t o;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.and.pred q, %2, 128, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(o)
+      : "r"((uint32_t)v), "r"(1 + r)
+      : "memory");
+  return o != 0;
+}
+
 template <int HD, bool F8, int RT>
 struct Layout {
   static constexpr int KT = RT * HK;        // keys per tile
@@ -62,15 +78,20 @@ struct Layout {
   static constexpr int BLK = KT * 128;      // one 128-byte-wide column block of a tile
   static constexpr int TILE = KT * HD * 2;  // one 16-bit tile
   static constexpr int RAW = F8 ? KT * HD : TILE;  // a tile as the cache has it
-  static constexpr int NS = (F8 || HD == 64) ? 4 : 3;  // stages of each ring
+  static constexpr int NS = HD == 64 && RT == 2 ? 4 : 3;  // stages of each ring
   static constexpr int K = 0;
   static constexpr int V = K + NS * RAW;
   static constexpr int CV = V + NS * RAW;            // E4M3: decoded V tiles
   static constexpr int Q = CV + (F8 ? NCV * TILE : 0);
   static constexpr bool QS = F8 || HD == 128;        // part of Q is in shared memory
-  static constexpr int QB = QS ? 128 * 128 : 0;      // bytes of it per row tile
-  static constexpr int BARS = Q + RT * QB;
-  static constexpr size_t SMEM = (size_t)BARS + sizeof(Bars);
+  static constexpr int QB = 128 * 128;               // bytes of it per row tile
+  // a row tile's 128 bytes a row for reordering Q and O: its part of Q before that is
+  // written and after it is used, or (E4M3, whose hi and lo terms come together) another
+  static constexpr int STG = F8 ? Q + RT * QB : Q;
+  static constexpr int BARS = (F8 ? STG : Q) + RT * QB;
+  static constexpr int AMAX = BARS + (int)sizeof(Bars);  // E4M3: each query row's largest
+                                                         // magnitude (bf16 bits)
+  static constexpr size_t SMEM = (size_t)AMAX + (F8 ? RT * 512 : 0);
   static_assert(!F8 || HD == 128, "E4M3 rows of one head are one 128-byte swizzle row");
   // 227 KB for a CTA, 228 KB with 1 KB per CTA of the SM's for two
   static_assert(SMEM <= (RT == 2 ? 227 : 113) * 1024, "shared memory above the limit");
@@ -112,47 +133,35 @@ __device__ __forceinline__ void split_q(const float* x, uint32_t& whi, uint32_t&
   wlo = l01 | (l23 << 16);
 }
 
-// One unit's share of a CTA's range: tiles [j0, j1) of part v, KV head g, rows mt * RT * 128
-// on. Positions are relative to the unit's first tile, at cache position kbase.
+// One unit's share of a CTA's range: its tiles [j0, j1).
 struct Seg {
-  int u, g, mt, j0, j1, kbase;
-  int start, nkeys, last0;  // of the part
-  int rows, table_row;      // rows: live query rows of the unit
-  int64_t q_off;
+  SharedUnit d;
+  int u, j0, j1;
 };
 
-template <int RT>
 __device__ __forceinline__ bool seg_next(const AttnParams& p, int num_units, int& t, int t_end,
                                          int& u, Seg& s) {
   if (t >= t_end || u >= num_units) return false;
-  const int4 info = p.units[u];
-  const int ub = p.ubeg[u], ue = p.ubeg[u + 1];
-  const SharedSeq part = p.parts[info.x];
+  const int4* src = reinterpret_cast<const int4*>(p.sunits + u);
+  const int4 a = src[0], b = src[1], c = src[2];
+  s.d = SharedUnit{(int64_t)(uint32_t)a.x | (int64_t)a.y << 32, a.z, a.w, b.x, b.y, b.z, b.w,
+                   c.x, c.y, c.z, c.w};
   s.u = u;
-  s.g = info.y;
-  s.mt = info.z;
-  s.kbase = RT == 2 ? 0 : info.w;
-  s.j0 = t - ub;
-  s.j1 = min(t_end, ue) - ub;
-  s.start = RT == 2 ? 0 : part.start - s.kbase;
-  s.nkeys = part.nkeys - s.kbase;
-  s.last0 = part.last0 - s.kbase;
-  s.rows = min(RT * MT, p.G * part.rows - info.z * RT * MT);
-  s.table_row = part.table_row;
-  s.q_off = part.q_off;
+  s.j0 = t - s.d.tile;
+  s.j1 = min(t_end - s.d.tile, s.d.nt);
   if (s.j1 <= s.j0) return false;
-  t = ub + s.j1;
+  t = s.d.tile + s.j1;
   ++u;
   return true;
 }
 // Row tiles of a segment, and steps of its tile j.
 template <int RT>
 __device__ __forceinline__ int tiles_of(const Seg& s) {
-  return RT == 2 && s.rows > MT ? 2 : 1;
+  return RT == 2 && s.d.rows > MT ? 2 : 1;
 }
 template <int RT>
 __device__ __forceinline__ int steps_of(const Seg& s, int j) {
-  return RT == 2 && s.nkeys - j * RT * HK > HK ? 2 : 1;
+  return RT == 2 && s.d.nkeys - j * RT * HK > HK ? 2 : 1;
 }
 
 template <int HD, bool F8, int RT>
@@ -243,13 +252,13 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
     Seg s;
     uint32_t it = 0;
     bool ok = true;
-    while (ok && seg_next<RT>(p, num_units, t, t_end, u, s)) {
-      const int32_t* tab = p.block_table + (size_t)s.table_row * p.bt_stride;
+    while (ok && seg_next(p, num_units, t, t_end, u, s)) {
+      const int32_t* tab = p.block_table + (size_t)s.d.table_row * p.bt_stride;
       auto box_pos = [&](int j, int n) { return j * KT + n * box; };
-      auto seen = [&](int pos) { return pos < s.nkeys && pos + box > s.start; };
+      auto seen = [&](int pos) { return pos < s.d.nkeys && pos + box > s.d.start; };
       auto fetch = [&](int jg) -> int {  // this lane's entry of the group starting at tile jg
         const int j = jg + lane / nbox, pos = box_pos(j, lane % nbox);
-        return j < s.j1 && seen(pos) ? __ldg(tab + ((s.kbase + pos) >> p.bs_log2)) : 0;
+        return j < s.j1 && seen(pos) ? __ldg(tab + ((s.d.kbase + pos) >> p.bs_log2)) : 0;
       };
       int ent_cur = fetch(s.j0), ent_nxt = fetch(s.j0 + tg);
       for (int j = s.j0; j < s.j1; ++j, ++it) {
@@ -266,7 +275,7 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
           if (blk < 0 || blk >= p.num_blocks) {  // a table entry outside the pool
             atomicOr(p.flags, FLAG_ATTN_SHAPE);
           } else {
-            grow = blk * p.block_size + ((s.kbase + pos) & (p.block_size - 1));
+            grow = blk * p.block_size + ((s.d.kbase + pos) & (p.block_size - 1));
           }
         }
         bool w = true;
@@ -281,11 +290,11 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
         if (mine) {
           const uint32_t dst = ring + st * L::RAW + lane * box * 128;
           if constexpr (F8) {
-            tma_load_3d(dst, tm, &full[st], 0, s.g, grow);
+            tma_load_3d(dst, tm, &full[st], 0, s.d.g, grow);
           } else {
 #pragma unroll
             for (int c = 0; c < HD / 64; ++c)
-              tma_load_3d(dst + c * L::BLK, tm, &full[st], c * 64, s.g, grow);
+              tma_load_3d(dst + c * L::BLK, tm, &full[st], c * 64, s.d.g, grow);
           }
         }
       }
@@ -313,7 +322,7 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
       Seg s;
       uint32_t it = 0, n[RT] = {}, units[RT] = {};
       bool ok = true;
-      while (ok && seg_next<RT>(p, num_units, t, t_end, u, s)) {
+      while (ok && seg_next(p, num_units, t, t_end, u, s)) {
         const int nr = tiles_of<RT>(s);
         for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
           const uint32_t st = it % L::NS;
@@ -381,7 +390,7 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
       Seg s;
       uint32_t it = 0, n[RT] = {};
       bool ok = true;
-      while (ok && seg_next<RT>(p, num_units, t, t_end, u, s)) {
+      while (ok && seg_next(p, num_units, t, t_end, u, s)) {
         const int nr = tiles_of<RT>(s);
         for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
           constexpr uint32_t NV = F8 ? NCV : L::NS;
@@ -429,80 +438,111 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
     Seg s;
     uint32_t it = 0, n = 0;  // tiles of the range; steps of this row tile
     bool ok = true;
-    while (ok && seg_next<RT>(p, num_units, t, t_end, u, s)) {
+    uint8_t* stg = smem + L::STG + r * L::QB;  // 128 bytes a row, 16-byte chunks swizzled
+    uint8_t* qsm = smem + L::Q + r * L::QB;
+    uint32_t* row_amax = reinterpret_cast<uint32_t*>(smem + L::AMAX) + r * MT;
+    auto chunk_at = [](int row, int k) -> uint32_t { return row * 128 + ((k ^ (row & 7)) << 4); };
+    // A warp whose wait failed stays until its warpgroup meets at the next unit, where all of
+    // its warps leave together: none is left waiting at a barrier.
+    while (seg_next(p, num_units, t, t_end, u, s)) {
       if (r >= tiles_of<RT>(s)) {
         it += s.j1 - s.j0;
         continue;
       }
+      if (!wg_and(r, ok)) break;  // (and the staging rows of the last unit have been read)
       const int row = r * MT + rr;
-      const bool live = row < s.rows;
-      const int rg = s.mt * RT * MT + (live ? row : r * MT);  // a dead row repeats a live one
-      // the row's last visible key (every row of a prefix sees all of it)
-      const int last = RT == 2 ? s.nkeys - 1 : s.last0 + rg / p.G;
-      const uint4* qsrc = reinterpret_cast<const uint4*>(
-          (const __nv_bfloat16*)p.q +
-          ((s.q_off + rg / p.G) * p.Hq + (int64_t)s.g * p.G + rg % p.G) * HD);
+      const bool live = row < s.d.rows;
       float sc = p.scale_log2;  // score scale in log2 units
-      uint8_t* qrow = smem + L::Q + r * L::QB + rr * 128;
+      // ---- Q: 16-byte chunk qc of rows q0 + i * QI, whole rows side by side (coalesced);
+      // rows that are none become zeros
+      constexpr int QC = HD / 8, QI = 128 / QC;
+      const int qc = rr % QC, q0 = rr / QC;
+      auto load_q = [&](int i) -> uint4 {
+        const int qr = r * MT + q0 + i * QI;
+        if (qr >= s.d.rows) return make_uint4(0, 0, 0, 0);
+        const int rg = s.d.mt * RT * MT + qr;
+        return __ldg(reinterpret_cast<const uint4*>(
+                         (const __nv_bfloat16*)p.q +
+                         ((s.d.q_off + rg / p.G) * p.Hq + (int64_t)s.d.g * p.G + rg % p.G) * HD) +
+                     qc);
+      };
       if constexpr (F8) {
-        // Q row x 2^e, its largest magnitude in [128, 256), as hi + lo (attn_tc.cu)
-        uint32_t amax = 0;
-#pragma unroll
-        for (int e = 0; e < HD / 8; ++e) {
-          const uint4 v = __ldg(qsrc + e);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) amax = max(amax, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-        }
-        const int eb = max((int)(amax >> 7), 1);
-        const int e2 = amax == 0 ? 0 : min(max(134 - eb, -120), 120);
-        const float f = __int_as_float((e2 + 127) << 23);
+        // row x 2^e, its largest magnitude in [128, 256), as hi + lo (attn_tc.cu); 2^-e joins
+        // the K scale in the score scale
+        auto exponent = [](uint32_t amax) -> int {
+          const int eb = max((int)(amax >> 7), 1);
+          return amax == 0 ? 0 : min(max(134 - eb, -120), 120);
+        };
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {  // 32 elements: 8 TMEM columns, two 16-byte chunks
-          uint32_t hi[8], lo[8], rq[16];
+        for (int i0 = 0; i0 < QC; i0 += 8) {
+          uint4 v[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {  // the second read of the row
-            const uint4 v = __ldg(qsrc + 4 * c + e);
-            rq[4 * e] = v.x;
-            rq[4 * e + 1] = v.y;
-            rq[4 * e + 2] = v.z;
-            rq[4 * e + 3] = v.w;
-          }
+          for (int i = 0; i < 8; ++i) v[i] = load_q(i0 + i);
 #pragma unroll
-          for (int w = 0; w < 8; ++w) {
-            const uint32_t a = rq[2 * w], b = rq[2 * w + 1];
-            const float x[4] = {__uint_as_float(a << 16) * f, __uint_as_float(a & 0xffff0000u) * f,
-                                __uint_as_float(b << 16) * f, __uint_as_float(b & 0xffff0000u) * f};
-            split_q(x, hi[w], lo[w]);
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t amax = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) amax = max(amax, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+#pragma unroll
+            for (int o = 1; o < QC; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const float f = __int_as_float((exponent(amax) + 127) << 23);
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t a = w[2 * k], b = w[2 * k + 1];
+              const float x[4] = {__uint_as_float(a << 16) * f, __uint_as_float(a & 0xffff0000u) * f,
+                                  __uint_as_float(b << 16) * f, __uint_as_float(b & 0xffff0000u) * f};
+              split_q(x, hi[k], lo[k]);
+            }
+            const int qr = q0 + (i0 + i) * QI;
+            const uint32_t at = chunk_at(qr, qc >> 1) + (qc & 1) * 8;
+            *reinterpret_cast<uint2*>(stg + at) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(qsm + at) = make_uint2(lo[0], lo[1]);
+            if (qc == 0) row_amax[qr] = amax;
           }
-          tmem_st8(tq + COL_Q + r * 32 + 8 * c, hi);
-          *reinterpret_cast<uint4*>(qrow + (((2 * c) ^ (rr & 7)) << 4)) =
-              make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          *reinterpret_cast<uint4*>(qrow + (((2 * c + 1) ^ (rr & 7)) << 4)) =
-              make_uint4(lo[4], lo[5], lo[6], lo[7]);
         }
-        sc = p.scale_log2 * p.kv_scale[s.g] * __int_as_float((127 - e2) << 23);
+        wg_sync(r);
+        sc = p.scale_log2 * p.kv_scale[s.d.g] *
+             __int_as_float((127 - exponent(row_amax[rr])) << 23);
       } else {
+        uint4 v[QC];
+#pragma unroll
+        for (int i = 0; i < QC; ++i) v[i] = load_q(i);
+        if (qc < 8) {
+#pragma unroll
+          for (int i = 0; i < QC; ++i)
+            *reinterpret_cast<uint4*>(stg + chunk_at(q0 + i * QI, qc)) = v[i];
+        }
+        wg_sync(r);
+        if constexpr (L::QS) {  // the other half of the row waits for the first
+          uint32_t rq[32];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(rq + 4 * k) = *reinterpret_cast<uint4*>(stg + chunk_at(rr, k));
+          tmem_st32(tq + COL_Q + r * 32, rq);
+          wg_sync(r);
+          if (qc >= 8) {
+#pragma unroll
+            for (int i = 0; i < QC; ++i)
+              *reinterpret_cast<uint4*>(qsm + chunk_at(q0 + i * QI, qc - 8)) = v[i];
+          }
+        }
+      }
+      if constexpr (F8 || !L::QS) {
         uint32_t rq[32];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint4 v = __ldg(qsrc + e);
-          rq[4 * e] = v.x;
-          rq[4 * e + 1] = v.y;
-          rq[4 * e + 2] = v.z;
-          rq[4 * e + 3] = v.w;
-        }
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4*>(rq + 4 * k) = *reinterpret_cast<uint4*>(stg + chunk_at(rr, k));
         tmem_st32(tq + COL_Q + r * 32, rq);
-        if constexpr (L::QS) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            *reinterpret_cast<uint4*>(qrow + ((e ^ (rr & 7)) << 4)) = __ldg(qsrc + 8 + e);
-        }
       }
       tmem_wait_st();
       if constexpr (L::QS) fence_proxy_async();
       fence_before();
       mbar_arrive(&bars->q_full[r]);
+      // the row's last visible key (every row of a prefix sees all of it)
+      const int last = RT == 2 ? s.d.nkeys - 1
+                               : s.d.last0 + (s.d.mt * MT + (live ? row : 0)) / p.G;
 
       float m_ref = -INFINITY, lh = 0.f;
       bool good = true;
@@ -529,8 +569,8 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
             for (int c = 0; c < HK; ++c)
               if (c > left) x[c] = -INFINITY;
           }
-          if (RT == 1 && key0 < s.start) {
-            const int low = s.start - key0;
+          if (RT == 1 && key0 < s.d.start) {
+            const int low = s.d.start - key0;
 #pragma unroll
             for (int c = 0; c < HK; ++c)
               if (c < low) x[c] = -INFINITY;
@@ -589,7 +629,7 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
           }
           tmem_st32(tq + COL_P + r * 32, pk);
           tmem_wait_st();
-          const int first = RT == 1 ? max(s.start - key0, 0) : 0, end = min(s.nkeys - key0, HK);
+          const int first = RT == 1 ? max(s.d.start - key0, 0) : 0, end = min(s.d.nkeys - key0, HK);
           if (!F8 && r == 0 && (first > 0 || end < HK)) {
             // V rows before and past the part's keys may hold any bits: zeros, so that P = 0
             // never meets non-finite data
@@ -615,23 +655,32 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
       }
       if (!good) {
         ok = false;
-        break;
+        continue;
       }
-      const size_t at = ((size_t)blockIdx.x + s.u) * (RT * MT) + row;
+      // 32 columns at a time through the staging rows (a warp's own 32), so that whole
+      // 128-byte lines are written
+      const size_t at = ((size_t)blockIdx.x + s.u) * (RT * MT) + r * MT;
+      const int w0 = (warp & 3) * 32;
 #pragma unroll 1
       for (int c = 0; c < HD / 32; ++c) {
         uint32_t ro[32];
         tmem_ld32(tq + COL_O + r * 128 + c * 32, ro);
         tmem_wait_ld();
         reg_fence32(ro);
-        if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * HD + c * 32);
+        __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[e] = make_uint4(ro[4 * e], ro[4 * e + 1], ro[4 * e + 2], ro[4 * e + 3]);
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4*>(stg + chunk_at(rr, k)) = *reinterpret_cast<uint4*>(ro + 4 * k);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int o = w0 + i * 4 + lane / 8;
+          if (r * MT + o < s.d.rows)
+            *reinterpret_cast<uint4*>(p.part_o + (at + o) * HD + c * 32 + (lane % 8) * 4) =
+                *reinterpret_cast<uint4*>(stg + chunk_at(o, lane % 8));
         }
       }
-      if (live) p.part_ml[at] = make_float2(m_ref, lh);
+      if (live) p.part_ml[at + rr] = make_float2(m_ref, lh);
       fence_before();  // TMEM reads above complete before the next unit's MMAs
     }
   }
@@ -653,7 +702,7 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
       Seg s;
       uint32_t it = 0;
       bool ok = true;
-      while (ok && seg_next<RT>(p, num_units, t, t_end, u, s)) {
+      while (ok && seg_next(p, num_units, t, t_end, u, s)) {
         for (int j = s.j0; j < s.j1; ++j, ++it) {
           const uint32_t rs = it % L::NS, cs = it % NCV;
           if (!mbar_wait(&bars->v_full[rs], (it / L::NS) & 1, wt) ||
@@ -669,7 +718,7 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
           for (int k = 0; k < KT / 16; ++k)
             w[k] = *reinterpret_cast<const uint4*>(rsrc + k * RSTEP);
           mbar_arrive(&bars->v_empty[rs]);
-          const int lim = s.nkeys - j * KT, low = s.start - j * KT;  // the part's keys
+          const int lim = s.d.nkeys - j * KT, low = s.d.start - j * KT;  // the part's keys
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k) {
             uint32_t h[8];

@@ -113,6 +113,16 @@ struct SharedSeq {
   int32_t mbase;      // the place of a prefix's first row tile among those of all prefixes
 };
 
+// A unit of a line, as attn_parts.cu reads it: three 16-byte loads. Positions are relative to
+// kbase, the cache position of the unit's first tile.
+struct alignas(16) SharedUnit {
+  int64_t q_off;              // the part's first window row
+  int32_t g, mt;              // KV head, row tile
+  int32_t kbase, start, nkeys, last0;  // as in SharedSeq
+  int32_t rows, table_row;    // live query rows of the unit
+  int32_t tile, nt;           // first tile on the line, tiles
+};
+
 // Where a window row's partial results are.
 struct RowInfo {
   int32_t i;         // row of its sequence's window
@@ -163,6 +173,7 @@ struct AttnParams {
   SharedSeq* parts;           // [num_groups + B]
   int32_t* row_begin;         // [B] first window row of each sequence
   RowInfo* rows;              // [window rows]
+  SharedUnit* sunits;         // [U] (tcgen05 kernels)
   int32_t* tile_unit;         // [row tiles of the prefixes] first of the Hkv units of each
   int2* unit_ctas;            // [U] first and last CTA that a unit's tiles fall to
   int row_tile;               // query rows of a prefix's unit
@@ -267,7 +278,7 @@ sv_status host_plan(const AttnParams& p, int kt, const int32_t* T, const int32_t
 // two lines of units (0 the prefixes', 1 the sequences') or one for all (`lines` false).
 struct SharedWs {
   struct Line {
-    size_t hdr, units, ubeg, unit_ctas, cta_tab, part_o, part_ml;
+    size_t hdr, units, sunits, ubeg, unit_ctas, cta_tab, part_o, part_ml;
   };
   size_t parts, row_begin, rows, tile_unit, total;
   Line line[2];

@@ -81,6 +81,21 @@ __device__ __forceinline__ int last_at_most(int n, int64_t x, F key) {
   return lo;
 }
 
+// Unit u: row tile mt and KV head g of part v = s, from cache position kbase on, its first
+// tile `tile` of the line. `both`: for the mma.sync kernel, which reads parts and units.
+__device__ __forceinline__ void put_unit(const AttnParams& p, bool both, int u, int v,
+                                         const SharedSeq& s, int g, int mt, int kbase, int tile) {
+  p.ubeg[u] = tile;
+  if (both) {
+    p.units[u] = make_int4(v, g, mt, kbase);
+    return;
+  }
+  const int rt = v < p.num_groups ? p.row_tile : MT;
+  const int rows = (int)min((int64_t)rt, (int64_t)p.G * s.rows - (int64_t)mt * rt);
+  p.sunits[u] = SharedUnit{s.q_off, g, mt, kbase, s.start - kbase, s.nkeys - kbase,
+                           s.last0 - kbase, rows, s.table_row, tile, s.nt};
+}
+
 // CTA `line` of 2 (or the one CTA of a single line) checks the call, describes its parts and
 // writes its line: line 0 the prefixes (pa), line 1 the sequences (pb). Both CTAs make the
 // same checks, so a call is skipped as a whole.
@@ -193,10 +208,8 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
     scan_block<2>(c, ex, tot);
     if (c[0] > 0 && TT + ex[1] + c[1] < 0x7fffffffll && U + ex[0] + c[0] <= p.max_units) {
       p.tile_unit[s.mbase + mt] = (int32_t)(U + ex[0]);
-      for (int g = 0; g < p.Hkv; ++g) {
-        p.units[U + ex[0] + g] = make_int4(v, g, mt, 0);
-        p.ubeg[U + ex[0] + g] = (int32_t)(TT + ex[1] + (int64_t)g * s.nt);
-      }
+      for (int g = 0; g < p.Hkv; ++g)
+        put_unit(p, both, (int)(U + ex[0]) + g, v, s, g, mt, 0, (int32_t)(TT + ex[1] + (int64_t)g * s.nt));
     }
     U += tot[0];
     TT += tot[1];
@@ -233,8 +246,8 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
   for (int64_t u = U0 + tid; u < U; u += PLAN_T) {
     const SharedSeq s = seq[last_at_most(B, u, [&](int i) { return seq[i].ubase; })];
     const int k = (int)(u - s.ubase);
-    p.units[u] = make_int4(NG + s.table_row, k / s.nmt, k % s.nmt, s.start / box * box);
-    p.ubeg[u] = s.tbase + k * s.nt;
+    put_unit(p, both, (int)u, NG + s.table_row, s, k / s.nmt, k % s.nmt, s.start / box * box,
+             s.tbase + k * s.nt);
   }
   if (sequences && !bad)
     for (int b = tid; b < B; b += PLAN_T) {
@@ -373,7 +386,8 @@ SharedWs shared_ws_layout(const sv_attn_desc* d, int num_groups, int sms, bool l
     w.n_ctas[k] = lines && k == 1 ? 2 * sms : sms;
     const size_t n_ctas = w.n_ctas[k], U = (size_t)w.max_units[k], slots = U + n_ctas;
     l.hdr = o;       o += 256;
-    l.units = o;     o = align_up(o + sizeof(int4) * U, 256);
+    l.units = l.sunits = o;
+    o = align_up(o + (lines ? sizeof(SharedUnit) : sizeof(int4)) * U, 256);
     l.ubeg = o;      o = align_up(o + sizeof(int32_t) * (U + 1), 256);
     l.unit_ctas = o; o = align_up(o + sizeof(int2) * U, 256);
     l.cta_tab = o;   o = align_up(o + sizeof(int2) * ((size_t)n_ctas + 1), 256);
