@@ -40,7 +40,6 @@ namespace {
 
 constexpr int HK = 64;  // keys per step
 constexpr int SOFTMAX_WARP0 = 4;
-constexpr int NCONV = 128;
 constexpr int NST = 4;  // ring stages at most
 constexpr int NCV = 2;  // E4M3: decoded V tiles
 
@@ -75,6 +74,7 @@ struct Layout {
   static constexpr uint32_t TMEM_COLS = RT * 256;
   static constexpr uint32_t COL_O = 0, COL_S = RT * 128, COL_P = RT * 192, COL_Q = RT * 224;
   static constexpr int CONV_WARP0 = SOFTMAX_WARP0 + 4 * RT;
+  static constexpr int NCONV = 64 * RT;  // decoding threads
   static constexpr int BLK = KT * 128;      // one 128-byte-wide column block of a tile
   static constexpr int TILE = KT * HD * 2;  // one 16-bit tile
   static constexpr int RAW = F8 ? KT * HD : TILE;  // a tile as the cache has it
@@ -123,14 +123,16 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0;
 }
 
-// Four scaled Q elements as hi + lo E4M3 terms (attn_tc.cu, split_q_e4m3).
-__device__ __forceinline__ void split_q(const float* x, uint32_t& whi, uint32_t& wlo) {
-  const uint32_t h01 = f32x2_to_e4m3x2(x[0], x[1]), h23 = f32x2_to_e4m3x2(x[2], x[3]);
-  const float2 d01 = e4m3x2_to_f32x2(h01), d23 = e4m3x2_to_f32x2(h23);
-  const uint32_t l01 = f32x2_to_e4m3x2(x[0] - d01.x, x[1] - d01.y);
-  const uint32_t l23 = f32x2_to_e4m3x2(x[2] - d23.x, x[3] - d23.y);
-  whi = h01 | (h23 << 16);
-  wlo = l01 | (l23 << 16);
+// Two scaled Q elements (|x| < 256, at most 8 significant bits) as hi + lo E4M3 terms
+// (attn_tc.cu, split_q_e4m3). f16 holds such an x and x - hi exactly down to its finest step
+// of 2^-24; E4M3's is 2^-9.
+__device__ __forceinline__ void split_q(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  asm("{\n .reg .b32 h, b;\n .reg .b16 c, d;\n cvt.rn.f16x2.f32 h, %3, %2;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 c, h;\n cvt.rn.f16x2.e4m3x2 b, c;\n"
+      " sub.rn.f16x2 h, h, b;\n cvt.rn.satfinite.e4m3x2.f16x2 d, h;\n"
+      " mov.b32 %0, {c, 0};\n mov.b32 %1, {d, 0};\n}\n"
+      : "=r"(hi), "=r"(lo)
+      : "f"(x0), "f"(x1));
 }
 
 // One unit's share of a CTA's range: its tiles [j0, j1).
@@ -199,10 +201,10 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->k_empty[s], 1);  // the commit after the tile's last score MMA
       mbar_init(&bars->v_full[s], 1);
-      mbar_init(&bars->v_empty[s], F8 ? NCONV : 1);  // decoded, or the last P V's commit
+      mbar_init(&bars->v_empty[s], F8 ? L::NCONV : 1);  // decoded, or the last P V's commit
     }
     for (int s = 0; s < NCV; ++s) {
-      mbar_init(&bars->vc_full[s], NCONV);
+      mbar_init(&bars->vc_full[s], L::NCONV);
       mbar_init(&bars->vc_empty[s], 1);
     }
     for (int r = 0; r < 2; ++r) {
@@ -457,14 +459,22 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
       // rows that are none become zeros
       constexpr int QC = HD / 8, QI = 128 / QC;
       const int qc = rr % QC, q0 = rr / QC;
-      auto load_q = [&](int i) -> uint4 {
-        const int qr = r * MT + q0 + i * QI;
-        if (qr >= s.d.rows) return make_uint4(0, 0, 0, 0);
-        const int rg = s.d.mt * RT * MT + qr;
-        return __ldg(reinterpret_cast<const uint4*>(
-                         (const __nv_bfloat16*)p.q +
-                         ((s.d.q_off + rg / p.G) * p.Hq + (int64_t)s.d.g * p.G + rg % p.G) * HD) +
-                     qc);
+      // (window row, head of the group) of row q0 + i * QI, stepped from row to row
+      int qw = (s.d.mt * RT * MT + r * MT + q0) / p.G, qh = (s.d.mt * RT * MT + r * MT + q0) % p.G;
+      const int dw = QI / p.G, dh = QI % p.G;
+      const uint4* qbase = reinterpret_cast<const uint4*>(
+                               (const __nv_bfloat16*)p.q + (s.d.q_off * p.Hq + (int64_t)s.d.g * p.G) * HD) +
+                           qc;
+      auto load_q = [&](int i) -> uint4 {  // called for i = 0, 1, ..
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r * MT + q0 + i * QI < s.d.rows) v = __ldg(qbase + (int64_t)(qw * p.Hq + qh) * QC);
+        qw += dw;
+        qh += dh;
+        if (qh >= p.G) {
+          qh -= p.G;
+          ++qw;
+        }
+        return v;
       };
       if constexpr (F8) {
         // row x 2^e, its largest magnitude in [128, 256), as hi + lo (attn_tc.cu); 2^-e joins
@@ -487,18 +497,14 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
 #pragma unroll
             for (int o = 1; o < QC; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
             const float f = __int_as_float((exponent(amax) + 127) << 23);
-            uint32_t hi[2], lo[2];
+            uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t a = w[2 * k], b = w[2 * k + 1];
-              const float x[4] = {__uint_as_float(a << 16) * f, __uint_as_float(a & 0xffff0000u) * f,
-                                  __uint_as_float(b << 16) * f, __uint_as_float(b & 0xffff0000u) * f};
-              split_q(x, hi[k], lo[k]);
-            }
+            for (int k = 0; k < 4; ++k)
+              split_q(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f, hi[k], lo[k]);
             const int qr = q0 + (i0 + i) * QI;
             const uint32_t at = chunk_at(qr, qc >> 1) + (qc & 1) * 8;
-            *reinterpret_cast<uint2*>(stg + at) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(qsm + at) = make_uint2(lo[0], lo[1]);
+            *reinterpret_cast<uint2*>(stg + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+            *reinterpret_cast<uint2*>(qsm + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
             if (qc == 0) row_amax[qr] = amax;
           }
         }
@@ -697,7 +703,7 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
       const uint32_t src_off = rw * 128 + ((c ^ ph) << 4);
       const uint32_t dst_off = (c >> 2) * L::BLK + rw * 128;
       const uint32_t w0 = ((2 * (c & 3)) ^ ph) << 4, w1 = ((2 * (c & 3) + 1) ^ ph) << 4;
-      constexpr int RSTEP = 16 * 128;
+      constexpr int CR = L::NCONV / 8, RSTEP = CR * 128;  // rows of a pass
       int t = t_begin, u = u_first;
       Seg s;
       uint32_t it = 0;
@@ -713,20 +719,20 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
           fence_after();
           const uint8_t* rsrc = smem + L::V + rs * L::RAW + src_off;
           uint8_t* cdst = smem + L::CV + cs * L::TILE + dst_off;
-          uint4 w[KT / 16];
+          uint4 w[KT / CR];
 #pragma unroll
-          for (int k = 0; k < KT / 16; ++k)
+          for (int k = 0; k < KT / CR; ++k)
             w[k] = *reinterpret_cast<const uint4*>(rsrc + k * RSTEP);
           mbar_arrive(&bars->v_empty[rs]);
           const int lim = s.d.nkeys - j * KT, low = s.d.start - j * KT;  // the part's keys
 #pragma unroll
-          for (int k = 0; k < KT / 16; ++k) {
+          for (int k = 0; k < KT / CR; ++k) {
             uint32_t h[8];
             e4m3x4_to_f16x4(w[k].x, h[0], h[1]);
             e4m3x4_to_f16x4(w[k].y, h[2], h[3]);
             e4m3x4_to_f16x4(w[k].z, h[4], h[5]);
             e4m3x4_to_f16x4(w[k].w, h[6], h[7]);
-            if (rw + 16 * k >= lim || rw + 16 * k < low) {
+            if (rw + CR * k >= lim || rw + CR * k < low) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) h[e] = 0u;
             }
