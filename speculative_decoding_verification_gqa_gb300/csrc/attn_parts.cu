@@ -494,8 +494,8 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
             uint32_t amax = 0;
 #pragma unroll
             for (int k = 0; k < 4; ++k) amax = max(amax, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-#pragma unroll
-            for (int o = 1; o < QC; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            // the row's 16 lanes
+            amax = lane < 16 ? __reduce_max_sync(0x0000ffffu, amax) : __reduce_max_sync(0xffff0000u, amax);
             const float f = __int_as_float((exponent(amax) + 127) << 23);
             uint32_t hi[4], lo[4];
 #pragma unroll
@@ -678,12 +678,15 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
         for (int k = 0; k < 8; ++k)
           *reinterpret_cast<uint4*>(stg + chunk_at(rr, k)) = *reinterpret_cast<uint4*>(ro + 4 * k);
         __syncwarp();
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          v[i] = *reinterpret_cast<uint4*>(stg + chunk_at(w0 + i * 4 + lane / 8, lane % 8));
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int o = w0 + i * 4 + lane / 8;
           if (r * MT + o < s.d.rows)
-            *reinterpret_cast<uint4*>(p.part_o + (at + o) * HD + c * 32 + (lane % 8) * 4) =
-                *reinterpret_cast<uint4*>(stg + chunk_at(o, lane % 8));
+            *reinterpret_cast<uint4*>(p.part_o + (at + o) * HD + c * 32 + (lane % 8) * 4) = v[i];
         }
       }
       if (live) p.part_ml[at + rr] = make_float2(m_ref, lh);
