@@ -467,7 +467,7 @@ SV_API sv_status spec_verify_attn_shared(const sv_attn_desc* desc, const void* q
   p.row_begin = (int32_t*)(ws + lay.row_begin);
   p.rows = (RowInfo*)(ws + lay.rows);
   p.tile_unit = (int32_t*)(ws + lay.tile_unit);
-  p.row_tile = lines ? 2 * MT : MT;
+  p.row_log2 = lines ? 8 : 7;  // 2 * MT or MT rows
   AttnParams line[2] = {p, p};
   for (int k = 0; k < 2; ++k) {
     AttnParams& l = line[k];

@@ -124,7 +124,7 @@ struct alignas(16) SharedUnit {
 };
 
 // Where a window row's partial results are.
-struct RowInfo {
+struct alignas(16) RowInfo {
   int32_t i;         // row of its sequence's window
   int32_t ubase;     // the sequence's first unit
   int32_t nmt;       // the sequence's row tiles per KV head
@@ -176,7 +176,7 @@ struct AttnParams {
   SharedUnit* sunits;         // [U] (tcgen05 kernels)
   int32_t* tile_unit;         // [row tiles of the prefixes] first of the Hkv units of each
   int2* unit_ctas;            // [U] first and last CTA that a unit's tiles fall to
-  int row_tile;               // query rows of a prefix's unit
+  int row_log2;               // log2 of the query rows of a prefix's unit
   int kt;                     // keys per tile of the line
   int num_groups;
   const int32_t* group_begin;  // [num_groups + 1]

@@ -66,13 +66,14 @@ constexpr int MAJOR_ENTRIES = 16384;
 
 // The place of a prefix's first row tile among those of all prefixes: with q_off window rows
 // and n prefixes before it there are at most this many row tiles before it.
-__device__ __forceinline__ int32_t tile_base(int64_t q_off, int G, int row_tile, int n) {
-  return (int32_t)(q_off * G / row_tile + n);
+// (32 bits: a call has at most 2^22 units, api.cu.)
+__device__ __forceinline__ int32_t tile_base(int q_off, int G, int row_log2, int n) {
+  return ((q_off * G) >> row_log2) + n;
 }
 
 // The last index in [0, n) whose key is at most x (keys not decreasing, key(0) <= x).
-template <class F>
-__device__ __forceinline__ int last_at_most(int n, int64_t x, F key) {
+template <class T, class F>
+__device__ __forceinline__ int last_at_most(int n, T x, F key) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -90,24 +91,49 @@ __device__ __forceinline__ void put_unit(const AttnParams& p, bool both, int u, 
     p.units[u] = make_int4(v, g, mt, kbase);
     return;
   }
-  const int rt = v < p.num_groups ? p.row_tile : MT;
-  const int rows = (int)min((int64_t)rt, (int64_t)p.G * s.rows - (int64_t)mt * rt);
+  const int rt = v < p.num_groups ? 1 << p.row_log2 : MT;
+  const int rows = min(rt, p.G * s.rows - mt * rt);
   p.sunits[u] = SharedUnit{s.q_off, g, mt, kbase, s.start - kbase, s.nkeys - kbase,
                            s.last0 - kbase, rows, s.table_row, tile, s.nt};
 }
 
+constexpr int CACHED = 1024;        // sequences, and groups, kept in shared memory
+constexpr int CACHED_UNITS = 1024;  // unit starts kept in shared memory
+constexpr int CACHED_CTAS = 1024;   // CTA starts (a launch has two per SM at most)
+
+struct PlanShared {
+  int32_t gb[CACHED + 1], len[CACHED];                      // groups
+  int32_t q[CACHED], T[CACHED], ub[CACHED], tb[CACHED];  // sequences
+  uint16_t n[CACHED];
+  uint8_t D[CACHED];
+  int32_t ubeg[CACHED_UNITS + 1];
+  union {  // first the one, then the other
+    int4 entry[PLAN_T];
+    int32_t cta[CACHED_CTAS + 1];
+  };
+  int maxmt;
+};
+
 // CTA `line` of 2 (or the one CTA of a single line) checks the call, describes its parts and
 // writes its line: line 0 the prefixes (pa), line 1 the sequences (pb). Both CTAs make the
-// same checks, so a call is skipped as a whole.
+// same checks, so a call is skipped as a whole. All of it is latency, a chain of dependent
+// steps, hence the tables in shared memory and arithmetic in 32 bits where it suffices.
 __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, AttnParams pb) {
   const bool both = gridDim.x == 1;  // one line for all parts
   const bool prefixes = both || blockIdx.x == 0, sequences = both || blockIdx.x == 1;
   const AttnParams& p = prefixes && !both ? pa : pb;
-  const int tid = threadIdx.x, NG = p.num_groups, B = p.B, kt = p.kt;
-  __shared__ int s_maxmt;
+  const int tid = threadIdx.x, NG = p.num_groups, B = p.B, kt = p.kt, G = p.G;
+  const int box = min(p.block_size, kt), row_log2 = p.row_log2;
+  __shared__ PlanShared sm;
   pdl_trigger();
   pdl_wait();
-  if (tid == 0) s_maxmt = 0;
+  // the first lengths are asked for before the groups are looked at
+  int T0 = 0, D0 = 0;
+  if (tid < B) {
+    T0 = p.seq_lens[tid];
+    D0 = p.draft_len[tid];
+  }
+  if (tid == 0) sm.maxmt = 0;
   bool bad = false;
   // the groups: consecutive ranges of the batch
   for (int n = tid; n < NG; n += PLAN_T) {
@@ -115,121 +141,170 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
     if (g0 < 0 || g1 < g0 || g1 > B || (n == 0 && g0 != 0) || (n == NG - 1 && g1 != B) || P < 0 ||
         P > p.max_seq)
       bad = true;
+    if (n < CACHED) {
+      sm.gb[n] = g0;
+      sm.len[n] = P;
+      if (n == NG - 1 || n == CACHED - 1) sm.gb[n + 1] = g1;
+    }
   }
   bad = __syncthreads_or(bad);
-  // the sequences; line 0 keeps their row offsets in its own scratch
+  auto group_at = [&](int n) -> int { return NG <= CACHED ? sm.gb[n] : p.group_begin[n]; };
+  auto prefix_at = [&](int n) -> int { return NG <= CACHED ? sm.len[n] : p.prefix_len[n]; };
+  // the sequences, and their units and tiles, which come first on a line for both
   SharedSeq* seq = p.parts + NG;
-  int64_t q_total = 0;
+  auto describe = [&](int b, int T, int D, int n) {
+    const int P = prefix_at(n);
+    SharedSeq s = {};
+    s.rows = 1 + D;
+    s.start = P;
+    s.nkeys = T + 1 + D;
+    s.last0 = T;
+    s.table_row = b;
+    s.alone = P == 0;
+    s.group = n;
+    s.nmt = (G * s.rows + MT - 1) / MT;
+    s.nt = (s.nkeys - (P & ~(box - 1)) + kt - 1) / kt;
+    return s;
+  };
+  int64_t q_total = 0, U = 0, TT = 0;
   for (int base = 0; base < B && !bad; base += PLAN_T) {
     const int b = base + tid;
-    int T = 0, D = -1, P = 0, n = 0;
+    SharedSeq s = {};
     if (b < B) {
-      T = p.seq_lens[b];
-      D = p.draft_len[b];
-      n = last_at_most(NG, b, [&](int i) { return p.group_begin[i]; });
-      P = p.prefix_len[n];
-      if (T < P || T > p.max_seq || D < 0 || D > p.max_draft ||
+      const int T = base == 0 ? T0 : p.seq_lens[b], D = base == 0 ? D0 : p.draft_len[b];
+      const int n = last_at_most(NG, b, group_at);
+      if (T < prefix_at(n) || T > p.max_seq || D < 0 || D > p.max_draft ||
           (((int64_t)T + D + p.block_size) >> p.bs_log2) > p.bt_stride)
         bad = true;
+      else
+        s = describe(b, T, D, n);
     }
-    const int64_t w[1] = {b < B && !bad ? 1 + D : 0};
-    int64_t ex[1], tot[1];
-    scan_block<1>(w, ex, tot);
-    if (b < B && !bad) {
-      if (prefixes) p.row_begin[b] = (int32_t)(q_total + ex[0]);
-      if (sequences) {
-        SharedSeq s;
-        s.q_off = q_total + ex[0];
-        s.rows = 1 + D;
-        s.start = P;
-        s.nkeys = T + 1 + D;
-        s.last0 = T;
-        s.table_row = b;
-        s.alone = P == 0;
-        s.group = n;
-        s.nmt = (int)(((int64_t)p.G * s.rows + MT - 1) / MT);
-        const int box = min(p.block_size, kt), k0 = P / box * box;
-        s.nt = (int)(((int64_t)s.nkeys - k0 + kt - 1) / kt);
-        s.ubase = s.tbase = s.mbase = 0;
-        seq[b] = s;
+    const int64_t c[2] = {(int64_t)s.rows << 32 | (uint32_t)(p.Hkv * s.nmt),  // two sums in one
+                          (int64_t)p.Hkv * s.nmt * s.nt};
+    int64_t ex[2], tot[2];
+    scan_block<2>(c, ex, tot);
+    if (b < B) {
+      s.q_off = q_total + (ex[0] >> 32);
+      s.ubase = (int32_t)(U + (int64_t)(uint32_t)ex[0]);
+      s.tbase = (int32_t)(TT + ex[1]);
+      if (B <= CACHED) {
+        sm.q[b] = (int32_t)s.q_off;
+        sm.T[b] = s.last0;
+        sm.D[b] = (uint8_t)(s.rows - 1);
+        sm.n[b] = (uint16_t)s.group;  // (below B)
+        sm.ub[b] = s.ubase;
+        sm.tb[b] = s.tbase;
+      } else {
+        p.row_begin[b] = (int32_t)s.q_off;
       }
+      if (sequences && (both || B > CACHED)) seq[b] = s;
     }
-    q_total += tot[0];
+    q_total += tot[0] >> 32;
+    U += (uint32_t)tot[0];
+    TT += tot[1];
     bad = __syncthreads_or(bad);
   }
-  bad = bad || q_total > p.q_rows;
-  // the prefixes: their parts
-  const int row_tile = p.row_tile;
-  for (int n = tid; n < NG && prefixes && !bad; n += PLAN_T) {
-    const int g0 = p.group_begin[n], g1 = p.group_begin[n + 1], P = p.prefix_len[n];
+  if (!sequences) U = TT = 0;
+  bad = bad || q_total > p.q_rows || U > p.max_units || TT >= 0x7fffffffll;
+  auto seq_at = [&](int b) {
+    if (B > CACHED) return seq[b];
+    SharedSeq s = describe(b, sm.T[b], sm.D[b], sm.n[b]);
+    s.q_off = sm.q[b];
+    s.ubase = sm.ub[b];
+    s.tbase = sm.tb[b];
+    return s;
+  };
+  auto first_row = [&](int b) -> int {
+    return b >= B ? (int)q_total : B <= CACHED ? sm.q[b] : p.row_begin[b];
+  };
+  // the prefixes
+  auto prefix_part = [&](int n) {
+    const int g0 = group_at(n), P = prefix_at(n), q0 = first_row(g0);
     SharedSeq s = {};
-    s.q_off = g0 < B ? p.row_begin[g0] : q_total;
-    const int64_t end = g1 < B ? p.row_begin[g1] : q_total;
-    s.rows = P > 0 ? (int)(end - s.q_off) : 0;
+    s.q_off = q0;
+    s.rows = P > 0 ? first_row(group_at(n + 1)) - q0 : 0;
     s.nkeys = P;
     s.last0 = P - 1;
     s.table_row = g0;
     s.group = n;
-    s.nmt = (int)(((int64_t)p.G * s.rows + row_tile - 1) / row_tile);
+    s.nmt = (G * s.rows + (1 << row_log2) - 1) >> row_log2;
     s.nt = (P + kt - 1) / kt;
-    s.mbase = tile_base(s.q_off, p.G, row_tile, n);
-    atomicMax(&s_maxmt, s.nmt);
-    p.parts[n] = s;
+    s.mbase = tile_base(q0, G, row_log2, n);
+    return s;
+  };
+  if (!bad && sequences) {  // (TT and U are in range: every unit below is)
+    for (int u = tid; u < (int)U; u += PLAN_T) {
+      const int b = B <= CACHED ? last_at_most(B, u, [&](int i) { return sm.ub[i]; })
+                                : last_at_most(B, u, [&](int i) { return seq[i].ubase; });
+      const SharedSeq s = seq_at(b);
+      const int k = u - s.ubase, g = k / s.nmt, tile = s.tbase + k * s.nt;
+      put_unit(p, both, u, NG + b, s, g, k - g * s.nmt, s.start & ~(box - 1), tile);
+      if (u < CACHED_UNITS) sm.ubeg[u] = tile;
+    }
+    // every window row, a warp per sequence
+    for (int b = tid >> 5; b < B; b += PLAN_T / 32) {
+      const SharedSeq s = seq_at(b);
+      const int q0 = first_row(group_at(s.group));  // the group's first row
+      const int mbase = s.alone ? -1 : tile_base(q0, G, row_log2, s.group);
+      for (int i = tid & 31; i < s.rows; i += 32) {
+        int4* dst = reinterpret_cast<int4*>(p.rows + s.q_off + i);
+        dst[0] = make_int4(i, s.ubase, s.nmt, mbase);
+        dst[1] = make_int4((int)s.q_off - q0 + i, 0, 0, 0);
+      }
+    }
+  }
+  if (!bad && prefixes) {
+    for (int n = tid; n < NG; n += PLAN_T) {
+      const SharedSeq s = prefix_part(n);
+      atomicMax(&sm.maxmt, s.nmt);
+      if (both) p.parts[n] = s;
+    }
   }
   __syncthreads();
   // Units of the prefixes, entry (row tile mt, part v) by entry, the KV heads of an entry
   // together. Row-tile-major (mt first), so that the slices of the line that read the same
   // prefix are read by their CTAs at about the same time and share it through L2; with very
   // many groups of very different sizes part-major, over the row tiles' places.
-  const int maxmt = s_maxmt;
+  const int maxmt = sm.maxmt;
   const bool major = (int64_t)maxmt * NG <= MAJOR_ENTRIES;
-  const int64_t entries =
-      prefixes && !bad ? (major ? (int64_t)maxmt * NG : tile_base(q_total, p.G, row_tile, NG)) : 0;
-  int64_t U = 0, TT = 0;
-  for (int64_t base = 0; base < entries; base += PLAN_T) {
-    const int64_t e = base + tid;
+  const int entries =
+      prefixes && !bad ? (major ? maxmt * NG : tile_base((int)q_total, G, row_log2, NG)) : 0;
+  for (int base = 0; base < entries; base += PLAN_T) {
+    const int e = base + tid;
     int v = 0, mt = 0;
     int64_t c[2] = {0, 0}, ex[2], tot[2];
-    SharedSeq s = {};
     if (e < entries) {
       if (major) {
-        mt = (int)(e / NG);
-        v = (int)(e % NG);
+        mt = e / NG;
+        v = e - mt * NG;
       } else {
-        v = last_at_most(NG, e, [&](int i) { return p.parts[i].mbase; });
-        mt = (int)(e - p.parts[v].mbase);
+        auto place = [&](int i) { return tile_base(first_row(group_at(i)), G, row_log2, i); };
+        v = last_at_most(NG, e, place);
+        mt = e - place(v);
       }
-      s = p.parts[v];
+      const SharedSeq s = prefix_part(v);
       if (mt < s.nmt) {
         c[0] = p.Hkv;
         c[1] = (int64_t)p.Hkv * s.nt;
       }
     }
     scan_block<2>(c, ex, tot);
-    if (c[0] > 0 && TT + ex[1] + c[1] < 0x7fffffffll && U + ex[0] + c[0] <= p.max_units) {
-      p.tile_unit[s.mbase + mt] = (int32_t)(U + ex[0]);
-      for (int g = 0; g < p.Hkv; ++g)
-        put_unit(p, both, (int)(U + ex[0]) + g, v, s, g, mt, 0, (int32_t)(TT + ex[1] + (int64_t)g * s.nt));
+    const bool fits = U + tot[0] <= p.max_units && TT + tot[1] < 0x7fffffffll;
+    sm.entry[tid] = c[0] > 0 ? make_int4(v, mt, (int)(U + ex[0]), (int)(TT + ex[1])) : make_int4(-1, 0, 0, 0);
+    __syncthreads();
+    const int pairs = min(entries - base, PLAN_T) * p.Hkv;
+    for (int k = tid; fits && k < pairs; k += PLAN_T) {
+      const int4 en = sm.entry[k / p.Hkv];
+      if (en.x < 0) continue;
+      const int g = k % p.Hkv, u = en.z + g;
+      const SharedSeq s = prefix_part(en.x);
+      if (g == 0) p.tile_unit[s.mbase + en.y] = u;
+      put_unit(p, both, u, en.x, s, g, en.y, 0, en.w + g * s.nt);
+      if (u < CACHED_UNITS) sm.ubeg[u] = en.w + g * s.nt;
     }
     U += tot[0];
     TT += tot[1];
-  }
-  // units of the sequences
-  const int64_t U0 = U;
-  for (int base = 0; base < B && sequences && !bad; base += PLAN_T) {
-    const int b = base + tid;
-    int64_t c[2] = {0, 0}, ex[2], tot[2];
-    if (b < B) {
-      c[0] = (int64_t)p.Hkv * seq[b].nmt;
-      c[1] = c[0] * seq[b].nt;
-    }
-    scan_block<2>(c, ex, tot);
-    if (b < B) {
-      seq[b].ubase = (int32_t)(U + ex[0]);
-      seq[b].tbase = (int32_t)(TT + ex[1]);
-    }
-    U += tot[0];
-    TT += tot[1];
+    __syncthreads();
   }
   bad = bad || U > p.max_units || TT >= 0x7fffffffll;
   if (bad) U = TT = 0;  // (every thread: nothing below is then written or run)
@@ -240,45 +315,34 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
     p.hdr->kt = kt;
     p.hdr->sum_w = bad ? 0 : q_total;
     p.ubeg[U] = (int32_t)TT;
+    if (U <= CACHED_UNITS) sm.ubeg[U] = (int32_t)TT;
   }
-  __syncthreads();
-  const int box = min(p.block_size, kt);
-  for (int64_t u = U0 + tid; u < U; u += PLAN_T) {
-    const SharedSeq s = seq[last_at_most(B, u, [&](int i) { return seq[i].ubase; })];
-    const int k = (int)(u - s.ubase);
-    put_unit(p, both, (int)u, NG + s.table_row, s, k / s.nmt, k % s.nmt, s.start / box * box,
-             s.tbase + k * s.nt);
-  }
-  if (sequences && !bad)
-    for (int b = tid; b < B; b += PLAN_T) {
-      const SharedSeq s = seq[b];
-      const int64_t q0 = seq[p.group_begin[s.group]].q_off;  // the group's first row
-      RowInfo r = {0, s.ubase, s.nmt, s.alone ? -1 : tile_base(q0, p.G, row_tile, s.group), 0, {}};
-      for (int i = 0; i < s.rows; ++i) {
-        r.i = i;
-        r.of_group = (int)(s.q_off - q0) + i;
-        p.rows[s.q_off + i] = r;
-      }
-    }
   __syncthreads();
   // CTA c starts at the first tile at or after position c * VT / C of the virtual line, C at
   // most VT, so that every CTA between the first and the last of a unit has tiles of it
-  const int64_t X = p.switch_tiles, VT = TT + U * X;
-  const int C = (int)min((int64_t)p.n_ctas, max(VT, (int64_t)1));
+  const int32_t* ubeg = U <= CACHED_UNITS ? sm.ubeg : p.ubeg;
+  const int X = p.switch_tiles;
+  const int64_t VT = TT + U * X;
+  const int C = (int)min((int64_t)min(p.n_ctas, CACHED_CTAS), max(VT, (int64_t)1));
+  const int64_t part = VT / C;
+  const int rest = (int)(VT - part * C);
   for (int c = tid; c <= p.n_ctas; c += PLAN_T) {
     int2 e = make_int2((int32_t)TT, (int32_t)U);
     if (c < C && TT > 0) {
-      const int64_t v0 = (int64_t)c * VT / C;
-      const int u = last_at_most((int)U, v0, [&](int i) { return p.ubeg[i] + (int64_t)i * X; });
-      const int64_t into = v0 - (p.ubeg[u] + (int64_t)u * X) - X;  // < 0: before its tiles
-      e = make_int2((int32_t)(p.ubeg[u] + (into > 0 ? into : 0)), u);
+      const int64_t v0 = c * part + (int)((uint32_t)(c * rest) / (uint32_t)C);
+      const int u = last_at_most((int)U, v0, [&](int i) { return ubeg[i] + (int64_t)i * X; });
+      const int64_t into = v0 - (ubeg[u] + (int64_t)u * X) - X;  // < 0: before its tiles
+      e = make_int2((int32_t)(ubeg[u] + (into > 0 ? into : 0)), u);
     }
     p.cta_tab[c] = e;
+    if (c <= C) sm.cta[c] = e.x;
   }
-  for (int u = tid; u < (int)U; u += PLAN_T)
-    p.unit_ctas[u] =
-        make_int2(cta_of_tile(vpos_of_tile(p.ubeg[u], u, (int)X), VT, C),
-                  cta_of_tile(vpos_of_tile((int64_t)p.ubeg[u + 1] - 1, u, (int)X), VT, C));
+  __syncthreads();
+  // A unit's CTAs: the one whose range holds a tile is the last that starts at or before it.
+  for (int u = tid; u < (int)U; u += PLAN_T) {
+    auto holder = [&](int t) { return last_at_most(C, t, [&](int i) { return sm.cta[i]; }); };
+    p.unit_ctas[u] = make_int2(holder(ubeg[u]), holder(ubeg[u + 1] - 1));
+  }
 }
 
 // One output row (window row, query head) per group of 8 lanes, HD / 8 columns a lane: joins
@@ -304,14 +368,14 @@ __global__ void __launch_bounds__(256) combine_shared_kernel(AttnParams pa, Attn
     int2 ca = make_int2(0, -1);
     if (r.mbase >= 0) {
       const int64_t pr = (int64_t)r.of_group * pb.G + hl;
-      ua = pa.tile_unit[r.mbase + (int)(pr / pa.row_tile)] + g;
-      ra = (int)(pr % pa.row_tile);
+      ua = pa.tile_unit[r.mbase + (int)(pr >> pa.row_log2)] + g;
+      ra = (int)(pr & ((1 << pa.row_log2) - 1));
       ca = pa.unit_ctas[ua];
     }
     // the partials' rows, first those of the sequence's unit
     const int ns = cs.y - cs.x + 1, n = ns + ca.y - ca.x + 1;
     const int64_t at_s = ((int64_t)cs.x + us) * MT + rs % MT;
-    const int64_t at_a = ((int64_t)ca.x + ua) * pa.row_tile + ra;
+    const int64_t at_a = (((int64_t)ca.x + ua) << pa.row_log2) + ra;
     float m = -INFINITY, l = 0.f, acc[PER];
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] = 0.f;
@@ -322,7 +386,7 @@ __global__ void __launch_bounds__(256) combine_shared_kernel(AttnParams pa, Attn
       for (int k = 0; k < MAXP; ++k) {  // an unused place repeats the last one, with l = 0
         const int i = min(k0 + k, n - 1);
         const bool own = i < ns;
-        const int64_t at = own ? at_s + (int64_t)i * MT : at_a + (int64_t)(i - ns) * pa.row_tile;
+        const int64_t at = own ? at_s + (int64_t)i * MT : at_a + ((int64_t)(i - ns) << pa.row_log2);
         ml[k] = (own ? pb.part_ml : pa.part_ml)[at];
         if (k0 + k >= n) ml[k] = make_float2(-INFINITY, 0.f);
         const float4* src = reinterpret_cast<const float4*>((own ? pb.part_o : pa.part_o) + at * HD) + sub;

@@ -323,3 +323,21 @@ def test_fork_extend_attend_trim_compact_together(kernel):
     sv.spec_pages_trim(ref, table, lens, None, (T + al).contiguous(), **kw)
     assert lens[:3].tolist() == (T + al).tolist()
     assert sv.workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("B,NG", [(1100, 3), (1100, 1100), (700, 350)])
+def test_batches_beyond_the_plans_tables(kernel, B, NG):
+    """More sequences and groups than the plan keeps on chip, more units than it does, and
+    groups of one."""
+    gb = [B * n // NG for n in range(NG + 1)]
+    groups = [(17 + n % 9, [(17 + n % 9 + (7 * b) % 30, b % 3) for b in range(gb[n], gb[n + 1])])
+              for n in range(NG)]
+    w, x, gbeg, P = inputs(groups, Hq=4, Hkv=2, d=64, seed=B + NG)
+    assert_within(run(x, pages(x, gbeg, P, 16, seed=5), gbeg, P), w, x)
+
+
+def test_groups_of_very_different_sizes(kernel):
+    """So many groups beside a large one that the plan lays its units out group by group."""
+    groups = [(20, [(21 + b % 5, 3) for b in range(260)])] + [(9, [(12, 0)])] * 9000
+    w, x, gbeg, P = inputs(groups, Hq=16, Hkv=1, d=64, seed=3)
+    assert_within(run(x, pages(x, gbeg, P, 8, seed=5), gbeg, P), w, x)
