@@ -344,15 +344,42 @@ def spec_verify_attn_paged(q, k_pages, v_pages, block_table, seq_lens, draft_len
     return out
 
 
-def _here(device, **tensors):
-    """Every tensor given lies on `device`, and it is the current one: a launch goes to the
+_I32 = (torch.int32,)
+_KV = (torch.bfloat16, torch.uint8, torch.float8_e4m3fn)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
+def _dev(t, name, dtypes) -> int:
+    """Checks a tensor as `_need` does; returns its device's index."""
+    try:
+        if t.dtype in dtypes and t.is_contiguous():
+            d = t.get_device()
+            if d >= 0:
+                return d
+    except AttributeError:
+        pass
+    _need(t, name, dtypes)
+    return t.get_device()
+
+
+def _one_device(devs):
+    """The call's tensors lie on one device, and it is the current one: a launch goes to the
     current device's stream."""
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError("%s lies on %s, the call's tensors on %s" % (name, t.device, device))
-    if device.index != torch.cuda.current_device():
-        raise ValueError("the tensors lie on %s, the current device is cuda:%d"
-                         % (device, torch.cuda.current_device()))
+    d = devs[0]
+    for o in devs:
+        if o != d:
+            raise ValueError("the call's tensors lie on several devices: %s" % sorted(set(devs)))
+    if d != _current_device():
+        raise ValueError("the tensors lie on cuda:%d, the current device is cuda:%d"
+                         % (d, _current_device()))
+    return d
+
+
+def _stream_on(stream, dev):
+    if stream is None:
+        return _raw_stream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def shared_workspace_bytes(desc: AttnDesc, num_groups: int) -> int:
@@ -370,43 +397,48 @@ def spec_verify_attn_shared(q, k_pages, v_pages, block_table, seq_lens, draft_le
     group_begin[n] .. group_begin[n + 1] - 1 (int32 [groups + 1]) hold the same K/V at
     positions 0 .. prefix_len[n] - 1 (int32 [groups]), read through the block-table row of
     the group's first sequence and attended once for all of them."""
-    _need(q, "q", (torch.bfloat16,))
-    _need(k_pages, "k_pages", (torch.bfloat16, torch.uint8, torch.float8_e4m3fn))
-    _need(v_pages, "v_pages", (k_pages.dtype,))
-    for t, n in ((block_table, "block_table"), (seq_lens, "seq_lens"), (draft_len, "draft_len"),
-                 (group_begin, "group_begin"), (prefix_len, "prefix_len")):
-        _need(t, n, _I32)
-    if kv_scale is not None:
-        _need(kv_scale, "kv_scale", (torch.float32,))
-    if q.dim() != 3 or k_pages.dim() != 4 or v_pages.shape != k_pages.shape or \
-            q.shape[2] != k_pages.shape[3]:
+    devs = [_dev(q, "q", (torch.bfloat16,)), _dev(k_pages, "k_pages", _KV),
+            _dev(v_pages, "v_pages", (k_pages.dtype,)), _dev(block_table, "block_table", _I32),
+            _dev(seq_lens, "seq_lens", _I32), _dev(draft_len, "draft_len", _I32),
+            _dev(group_begin, "group_begin", _I32), _dev(prefix_len, "prefix_len", _I32)]
+    if q.dim() != 3 or k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
         raise ValueError("q must be [rows, Hq, d], k/v pages [num_blocks, block_size, Hkv, d]")
-    B = seq_lens.shape[0]
-    if block_table.dim() != 2 or block_table.shape[0] != B or draft_len.shape != (B,):
-        raise ValueError("block_table must be [B, max_blocks], draft_len [B]")
-    groups = prefix_len.shape[0]
-    if group_begin.shape != (groups + 1,) or prefix_len.dim() != 1:
+    rows, hq, d = q.shape
+    nb, bs, hkv, dk = k_pages.shape
+    B, table = seq_lens.numel(), block_table.shape
+    groups = prefix_len.numel()
+    if dk != d:
+        raise ValueError("q and the pages must have one head dimension")
+    if seq_lens.dim() != 1 or len(table) != 2 or table[0] != B or draft_len.shape != (B,):
+        raise ValueError("seq_lens and draft_len must be [B], block_table [B, max_blocks]")
+    if prefix_len.dim() != 1 or group_begin.shape != (groups + 1,):
         raise ValueError("group_begin must be [groups + 1], prefix_len [groups]")
-    nb, bs, hkv, d = k_pages.shape
-    if kv_scale is not None and kv_scale.shape != (2, hkv):
-        raise ValueError("kv_scale must be [2, Hkv]")
-    desc = attn_desc(q, k_pages.view(nb * bs, hkv, d), B, max_draft_len, max_seq_len, softmax_scale)
+    fp8 = k_pages.dtype != torch.bfloat16
+    scale = None
+    if kv_scale is not None:
+        devs.append(_dev(kv_scale, "kv_scale", (torch.float32,)))
+        if kv_scale.shape != (2, hkv):
+            raise ValueError("kv_scale must be [2, Hkv]")
+        scale = kv_scale.data_ptr()
+    desc = AttnDesc(B, hq, hkv, d, max_draft_len, max_seq_len, rows, nb * bs,
+                    SV_FP8_E4M3 if fp8 else SV_BF16, softmax_scale, 0)
     if out is None:
         out = torch.empty_like(q)
-    _need(out, "out", (torch.bfloat16,))
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
+    else:
+        devs.append(_dev(out, "out", (torch.bfloat16,)))
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
     if workspace is None:
         workspace = new_workspace(shared_workspace_bytes(desc, groups), q.device)
-    _here(q.device, k_pages=k_pages, v_pages=v_pages, block_table=block_table, seq_lens=seq_lens,
-          draft_len=draft_len, group_begin=group_begin, prefix_len=prefix_len, kv_scale=kv_scale,
-          out=out, workspace=workspace)
-    st = load_library().spec_verify_attn_shared(
-        ctypes.byref(desc), _ptr(q), _ptr(k_pages), _ptr(v_pages), nb, bs, _ptr(block_table),
-        block_table.shape[1], _ptr(seq_lens), _ptr(draft_len), groups, _ptr(group_begin),
-        _ptr(prefix_len), _ptr(kv_scale), _ptr(out), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream))
-    _check(st, "spec_verify_attn_shared")
+    devs.append(_dev(workspace, "workspace", (torch.uint8,)))
+    dev = _one_device(devs)
+    st = (_lib or load_library()).spec_verify_attn_shared(
+        ctypes.byref(desc), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), nb, bs,
+        block_table.data_ptr(), table[1], seq_lens.data_ptr(), draft_len.data_ptr(), groups,
+        group_begin.data_ptr(), prefix_len.data_ptr(), scale, out.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _stream_on(stream, dev))
+    if st:
+        _check(st, "spec_verify_attn_shared")
     return out
 
 
@@ -431,6 +463,8 @@ class PagePools:
         spans.sort()
         if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
             raise ValueError("the pools must not overlap")
+        self.device = self.tensors[0].get_device() if self.tensors else -1
+        self.pages = tuple(self.tensors[0].shape[:2]) if self.tensors else (0, 0)
         self.array = (PageData * len(self.tensors))(*[
             PageData(t.data_ptr(), t.numel() // t.shape[0] * t.element_size())
             for t in self.tensors])
@@ -451,41 +485,32 @@ def pages_workspace_bytes(num_blocks: int, table_rows: int) -> int:
     return n
 
 
-_I32 = (torch.int32,)
-
-
 def _page_table(ref_count, block_table, cached_len, block_size, lists, pools, workspace):
-    """The C descriptor of the pages' state, after the checks; (table, workspace)."""
-    for t, n in ((ref_count, "ref_count"), (block_table, "block_table"),
-                 (cached_len, "cached_len")):
-        _need(t, n, _I32)
-    if ref_count.dim() != 1 or cached_len.dim() != 1 or block_table.dim() != 2 or \
-            block_table.shape[0] != cached_len.shape[0]:
+    """The checks that the page operators share: (the C descriptor, the workspace, the
+    device's index)."""
+    devs = [_dev(ref_count, "ref_count", _I32), _dev(block_table, "block_table", _I32),
+            _dev(cached_len, "cached_len", _I32)]
+    table, blocks, rows = block_table.shape, ref_count.numel(), cached_len.numel()
+    if ref_count.dim() != 1 or cached_len.dim() != 1 or len(table) != 2 or table[0] != rows:
         raise ValueError("ref_count must be [num_blocks], cached_len [rows], block_table "
                          "[rows, max_blocks]")
     n = None
-    for name, t in lists.items():
+    for name, t in lists:
         if t is None:
             continue
-        _need(t, name, _I32)
-        if t.dim() != 1 or (n is not None and t.shape[0] != n):
+        devs.append(_dev(t, name, _I32))
+        if t.dim() != 1 or (n is not None and t.numel() != n):
             raise ValueError("the call's lists must be one-dimensional and of one length")
-        n = t.shape[0]
-    dev = ref_count.device
-    _here(dev, block_table=block_table, cached_len=cached_len, **lists)
-    if pools is not None and len(pools):
-        if pools.tensors[0].device != dev:
-            raise ValueError("the pools lie on %s, the state on %s" % (pools.tensors[0].device, dev))
-        if tuple(pools.tensors[0].shape[:2]) != (ref_count.shape[0], block_size):
+        n = t.numel()
+    if pools is not None and pools.tensors:
+        devs.append(pools.device)
+        if pools.pages != (blocks, block_size):
             raise ValueError("a pool must be [num_blocks, block_size, ...] of the state's pages")
     if workspace is None:
-        workspace = new_workspace(pages_workspace_bytes(ref_count.shape[0], cached_len.shape[0]),
-                                  dev)
-    _need(workspace, "workspace", (torch.uint8,))
-    _here(dev, workspace=workspace)
-    return PageTable(ref_count.shape[0], block_size, cached_len.shape[0], block_table.shape[1],
-                     ref_count.data_ptr(), block_table.data_ptr(),
-                     cached_len.data_ptr()), workspace
+        workspace = new_workspace(pages_workspace_bytes(blocks, rows), ref_count.device)
+    devs.append(_dev(workspace, "workspace", (torch.uint8,)))
+    return (PageTable(blocks, block_size, rows, table[1], ref_count.data_ptr(),
+                      block_table.data_ptr(), cached_len.data_ptr()), workspace, _one_device(devs))
 
 
 def _as_pools(pools) -> PagePools:
@@ -498,13 +523,15 @@ def spec_pages_fork(ref_count, block_table, cached_len, parents, children, *, bl
     of their first ``fork_len`` (int32 [n]) positions or whole: the same pages, each counted
     once more; no page data moves. State, changed in place: ref_count int32 [num_blocks],
     block_table int32 [rows, max_blocks], cached_len int32 [rows]."""
-    t, ws = _page_table(ref_count, block_table, cached_len, block_size,
-                        dict(parents=parents, children=children, fork_len=fork_len), None,
-                        workspace)
-    st = load_library().spec_pages_fork(
-        ctypes.byref(t), parents.shape[0], _ptr(parents), _ptr(children), _ptr(fork_len),
-        _ptr(ws), ws.numel(), _stream(stream))
-    _check(st, "spec_pages_fork")
+    t, ws, dev = _page_table(ref_count, block_table, cached_len, block_size,
+                             (("parents", parents), ("children", children), ("fork_len", fork_len)),
+                             None, workspace)
+    st = (_lib or load_library()).spec_pages_fork(
+        ctypes.byref(t), parents.numel(), parents.data_ptr(), children.data_ptr(),
+        None if fork_len is None else fork_len.data_ptr(), ws.data_ptr(), ws.numel(),
+        _stream_on(stream, dev))
+    if st:
+        _check(st, "spec_pages_fork")
 
 
 def spec_pages_extend(ref_count, block_table, cached_len, rows, new_len, *, block_size: int,
@@ -515,24 +542,27 @@ def spec_pages_extend(ref_count, block_table, cached_len, rows, new_len, *, bloc
     PagePools (``page_pools``) or a list of pool tensors. Too few free pages: nothing
     changes and ``workspace_status`` returns 9 (SV_ERR_NO_PAGES)."""
     pools = _as_pools(pools)
-    t, ws = _page_table(ref_count, block_table, cached_len, block_size,
-                        dict(new_len=new_len, rows=rows), pools, workspace)
-    st = load_library().spec_pages_extend(
-        ctypes.byref(t), new_len.shape[0], _ptr(rows), _ptr(new_len), len(pools), pools.array,
-        _ptr(ws), ws.numel(), _stream(stream))
-    _check(st, "spec_pages_extend")
+    t, ws, dev = _page_table(ref_count, block_table, cached_len, block_size,
+                             (("new_len", new_len), ("rows", rows)), pools, workspace)
+    st = (_lib or load_library()).spec_pages_extend(
+        ctypes.byref(t), new_len.numel(), None if rows is None else rows.data_ptr(),
+        new_len.data_ptr(), len(pools.tensors), pools.array, ws.data_ptr(), ws.numel(),
+        _stream_on(stream, dev))
+    if st:
+        _check(st, "spec_pages_extend")
 
 
 def spec_pages_trim(ref_count, block_table, cached_len, rows, new_len, *, block_size: int,
                     workspace=None, stream=None) -> None:
     """Give back the positions of row r = rows[i] from new_len[i] on (``rows`` None: rows
     0 .. n - 1): the pages past them lose a count, and their entries become -1."""
-    t, ws = _page_table(ref_count, block_table, cached_len, block_size,
-                        dict(new_len=new_len, rows=rows), None, workspace)
-    st = load_library().spec_pages_trim(
-        ctypes.byref(t), new_len.shape[0], _ptr(rows), _ptr(new_len), _ptr(ws), ws.numel(),
-        _stream(stream))
-    _check(st, "spec_pages_trim")
+    t, ws, dev = _page_table(ref_count, block_table, cached_len, block_size,
+                             (("new_len", new_len), ("rows", rows)), None, workspace)
+    st = (_lib or load_library()).spec_pages_trim(
+        ctypes.byref(t), new_len.numel(), None if rows is None else rows.data_ptr(),
+        new_len.data_ptr(), ws.data_ptr(), ws.numel(), _stream_on(stream, dev))
+    if st:
+        _check(st, "spec_pages_trim")
 
 
 def spec_pages_compact(ref_count, block_table, cached_len, *, block_size: int, pools=(),
@@ -541,17 +571,20 @@ def spec_pages_compact(ref_count, block_table, cached_len, *, block_size: int, p
     every row's entries follow. Fills ``remap`` (int32 [num_blocks]: the new page of each
     page, -1 if it was free) and ``num_live`` (int32 [1]: L) when they are given."""
     pools = _as_pools(pools)
-    t, ws = _page_table(ref_count, block_table, cached_len, block_size, {}, pools, workspace)
-    for o, name, n in ((remap, "remap", ref_count.shape[0]), (num_live, "num_live", 1)):
+    t, ws, dev = _page_table(ref_count, block_table, cached_len, block_size, (), pools, workspace)
+    out = [None, None]
+    for i, (o, name, n) in enumerate(((remap, "remap", t.num_blocks), (num_live, "num_live", 1))):
         if o is not None:
-            _need(o, name, _I32)
+            if _dev(o, name, _I32) != dev:
+                raise ValueError("%s lies on another device" % name)
             if o.numel() != n:
                 raise ValueError("%s must hold %d values" % (name, n))
-    _here(ref_count.device, remap=remap, num_live=num_live)
-    st = load_library().spec_pages_compact(
-        ctypes.byref(t), len(pools), pools.array, _ptr(remap), _ptr(num_live), _ptr(ws),
-        ws.numel(), _stream(stream))
-    _check(st, "spec_pages_compact")
+            out[i] = o.data_ptr()
+    st = (_lib or load_library()).spec_pages_compact(
+        ctypes.byref(t), len(pools.tensors), pools.array, out[0], out[1], ws.data_ptr(),
+        ws.numel(), _stream_on(stream, dev))
+    if st:
+        _check(st, "spec_pages_compact")
 
 
 def spec_accept(logits, draft_tokens, draft_len, *, max_draft_len: int, accept_len=None,
