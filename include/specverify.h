@@ -237,13 +237,15 @@ SV_API sv_status spec_verify_attn_shared(const sv_attn_desc* desc, const void* q
  * check changes nothing and sets the workspace flag (sv_workspace_status:
  * SV_ERR_DEVICE_SHAPE). A row may stand in a call once only. An entry in use that names
  * no page of the pool, or a free one, means that the state was damaged before the call:
- * it is reported, and no memory outside the arrays is touched, but the call's effect on
- * the other entries is then unspecified (spec_pages_compact changes nothing).
+ * it is reported by the call that meets it, and no memory outside the arrays is touched,
+ * but the call's effect on that page's count is then unspecified (spec_pages_compact
+ * changes nothing).
  */
+#define SV_MAX_TABLE_ROWS (1 << 20)
 typedef struct {
   int32_t num_blocks;         /* pages of the pool, >= 1; times block_size <= 2^31 - 1025 */
   int32_t block_size;         /* positions per page: a power of two in [8, 65536] */
-  int32_t table_rows;         /* rows of block_table and cached_len, >= 0 */
+  int32_t table_rows;         /* rows of block_table and cached_len, 0 .. SV_MAX_TABLE_ROWS */
   int32_t max_blocks_per_seq; /* entries of a row, >= 1 */
   int32_t* ref_count;         /* [num_blocks], 16-byte aligned */
   int32_t* block_table;       /* [table_rows, max_blocks_per_seq], row-major */

@@ -567,7 +567,7 @@ bool pool_sizes_ok(int32_t num_blocks, int32_t block_size) {
 sv_status check_pages(const sv_page_table* t, int32_t n, const void* ws, size_t ws_bytes) {
   if (!t) return SV_ERR_NULL;
   if (!pool_sizes_ok(t->num_blocks, t->block_size) || t->table_rows < 0 ||
-      t->max_blocks_per_seq < 1 || n < 0 || n > t->table_rows)
+      t->table_rows > SV_MAX_TABLE_ROWS || t->max_blocks_per_seq < 1 || n < 0 || n > t->table_rows)
     return SV_ERR_SHAPE;
   if (!t->ref_count || (t->table_rows > 0 && (!t->block_table || !t->cached_len)) || !ws)
     return SV_ERR_NULL;
@@ -595,7 +595,7 @@ sv_status check_pools(const sv_page_table* t, int32_t num_pools, const sv_page_d
 extern "C" {
 
 SV_API size_t spec_pages_workspace_size(int32_t num_blocks, int32_t table_rows) {
-  if (!pool_sizes_ok(num_blocks, 8) || table_rows < 0) return 0;
+  if (!pool_sizes_ok(num_blocks, 8) || table_rows < 0 || table_rows > SV_MAX_TABLE_ROWS) return 0;
   return pages_ws_bytes(num_blocks, table_rows);
 }
 

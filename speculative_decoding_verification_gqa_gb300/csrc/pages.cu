@@ -3,16 +3,19 @@
 // State (the caller's): ref_count[p], the number of table entries in use that name page p
 // (p is free iff it is 0); block_table[r, j], the page of positions j * bs .. of row r;
 // cached_len[r], the positions row r holds, so that its entries in use are those with
-// j < ceil(cached_len[r] / bs). Every operator checks all rows of the call before it
-// changes anything, in a first kernel that ends with one verdict (PagesHdr::ok); the
-// kernels after it do nothing when that is 0.
+// j < ceil(cached_len[r] / bs). Every operator checks all rows of the call before it changes
+// anything. fork and trim are one kernel, whose CTAs each make the same checks and whose
+// last CTA writes the lengths, which the checks read; extend and compact begin with a kernel
+// that ends with one verdict (PagesHdr::ok), and the kernels after it do nothing when that
+// is 0.
 //
 // Results do not depend on the order in which threads run: counts change by integer
 // additions, free pages are taken lowest first by ranks from a prefix sum over the pool,
 // and ties between rows go by their order in the call.
 //
-// All of it is bound by latency (a few dependent kernels) until tables of a million entries
-// or megabytes of page data are touched; the page data then moves at the copy bandwidth.
+// All of it is bound by latency (launches, and a chain of dependent reads) until tables of a
+// million entries or megabytes of page data are touched; the page data then moves at the
+// copy bandwidth.
 #include "internal.cuh"
 
 namespace sv {
@@ -20,7 +23,7 @@ namespace {
 
 constexpr int PT = 1024;          // threads of the planning kernels
 constexpr int CHUNK = 4096;       // pages counted by one CTA (PT threads x 4)
-constexpr int AT = 256;           // threads of the applying kernels
+constexpr int AT = 256;           // threads of the other kernels
 constexpr int SEG = 512;          // table entries of one work item
 constexpr int FORK_ROWS = 8;      // consecutive children of one work item
 constexpr int COPY_BYTES = 16384; // page bytes of one copying work item
@@ -29,7 +32,7 @@ constexpr int TABLE_CTAS = 64;    // compact: CTAs that check the tables
 // Verdict and totals of a call; every field is written before it is read in each call.
 struct PagesHdr {
   int32_t ok;
-  int32_t rows_bad;   // a check on the rows failed
+  int32_t rows_bad;   // extend: a check on the rows failed
   int32_t need;       // extend: pages taken
   int32_t cows;       // extend: rows that part from a shared page
   int32_t live;       // compact: L
@@ -45,9 +48,9 @@ struct Pages {
   uint32_t* flags;
   uint32_t* ticket;  // zero between calls
   PagesHdr* hdr;
-  int32_t *mark, *row_a, *row_b, *row_c, *row_d;  // [table_rows] each
-  int32_t* chunk;                         // [chunks], then [TABLE_CTAS] of compact
-  int32_t *blk_a, *blk_b;                 // [num_blocks] each
+  int32_t *row_a, *row_b, *row_c, *row_d, *row_e;  // [table_rows] each
+  int32_t* chunk;                         // [chunks + 1], then [TABLE_CTAS] of compact
+  int32_t *blk_a, *blk_b, *blk_c;         // [num_blocks] each
   int32_t *remap, *num_live;              // compact: outputs or null
   int chunks;
   int bs_log2;
@@ -141,21 +144,15 @@ __device__ __forceinline__ bool row_ok(const Pages& a, int r) {
   return r >= 0 && r < a.t.table_rows;
 }
 
-// Marks the rows of `list` (null: row i); true where one stands twice or lies outside the
-// table.
-__device__ bool mark_rows(const Pages& a, const int32_t* list) {
-  bool bad = false;
-  for (int i = threadIdx.x; i < a.n; i += PT) {
-    const int r = list ? list[i] : i;
-    if (row_ok(a, r)) a.mark[r] = 0;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.n; i += PT) {
-    const int r = list ? list[i] : i;
-    if (!row_ok(a, r) || atomicAdd(a.mark + r, 1) != 0) bad = true;
-  }
-  return bad;
+// A set of table rows in shared memory, a bit each.
+extern __shared__ uint32_t s_rows[];
+__device__ __forceinline__ void clear_rows(const Pages& a) {
+  for (int i = threadIdx.x; i < (a.t.table_rows + 31) / 32; i += blockDim.x) s_rows[i] = 0;
 }
+__device__ __forceinline__ bool add_row(int r) {  // false if it was there
+  return (atomicOr(s_rows + (r >> 5), 1u << (r & 31)) >> (r & 31) & 1) == 0;
+}
+__device__ __forceinline__ bool has_row(int r) { return (s_rows[r >> 5] >> (r & 31) & 1) != 0; }
 
 __device__ __forceinline__ void verdict(const Pages& a, bool ok) {
   if (threadIdx.x == 0) {
@@ -166,150 +163,227 @@ __device__ __forceinline__ void verdict(const Pages& a, bool ok) {
 
 // ---------------------------------------------------------------------------- fork
 
-// One CTA: children distinct, empty and not parents; lengths within the parents'.
-// row_a[i]: the child's length.
-__global__ void __launch_bounds__(PT) fork_plan(const Pages a) {
+// Checks: children distinct, empty and not parents; lengths within the parents'. An item:
+// FORK_ROWS consecutive children, SEG entries. A run of children of one parent reads each
+// entry once and adds the run's length to its page's count at once.
+__global__ void __launch_bounds__(AT) fork_kernel(const Pages a, int segs) {
   pdl_trigger();
   pdl_wait();
+  clear_rows(a);
+  __syncthreads();
   bool bad = false;
-  for (int i = threadIdx.x; i < a.n; i += PT)
-    if (row_ok(a, a.rows[i])) a.mark[a.rows[i]] = 0;
+  for (int i = threadIdx.x; i < a.n; i += AT) {
+    const int c = a.to[i];
+    if (!row_ok(a, c) || !add_row(c)) bad = true;
+  }
   __syncthreads();
-  bad |= mark_rows(a, a.to);
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.n; i += PT) {
+  for (int i = threadIdx.x; i < a.n; i += AT) {
     const int p = a.rows[i], c = a.to[i];
-    if (!row_ok(a, p) || !row_ok(a, c) || __ldcg(a.mark + p) != 0 || a.t.cached_len[c] != 0) {
+    if (!row_ok(a, p) || !row_ok(a, c) || has_row(p) || a.t.cached_len[c] != 0) {
       bad = true;
       continue;
     }
     const int have = a.t.cached_len[p], len = a.fork_len ? a.fork_len[i] : have;
     if (!len_fits(a, have) || len < 0 || len > have) bad = true;
-    a.row_a[i] = len;
   }
-  verdict(a, !__syncthreads_or(bad));
-}
-
-// An item: FORK_ROWS consecutive children, SEG entries. A run of children of one parent
-// reads each entry once and adds the run's length to its page's count at once.
-__global__ void __launch_bounds__(AT) fork_apply(const Pages a, int segs) {
-  pdl_trigger();
-  pdl_wait();
-  if (!a.hdr->ok) return;
+  bad = __syncthreads_or(bad);
+  auto length = [&](int i) { return a.fork_len ? a.fork_len[i] : a.t.cached_len[a.rows[i]]; };
   const int64_t stride = a.t.max_blocks_per_seq;
   const int groups = (a.n + FORK_ROWS - 1) / FORK_ROWS;
-  const int64_t items = (int64_t)groups * segs;
+  const int64_t items = bad ? 0 : (int64_t)groups * segs;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int i0 = (int)(it / segs) * FORK_ROWS, s = (int)(it % segs);
-    const int i1 = min(i0 + FORK_ROWS, a.n);
-    if (s == 0 && threadIdx.x < i1 - i0)
-      a.t.cached_len[a.to[i0 + threadIdx.x]] = a.row_a[i0 + threadIdx.x];
-    int nmax = 0;
-    for (int i = i0; i < i1; ++i) nmax = max(nmax, pages_of(a.row_a[i], a.bs_log2));
+    const int cnt = min(FORK_ROWS, a.n - i0);
+    // the item's rows, read at once
+    int par[FORK_ROWS], child[FORK_ROWS], pages[FORK_ROWS], nmax = 0;
+#pragma unroll
+    for (int k = 0; k < FORK_ROWS; ++k) {
+      par[k] = k < cnt ? a.rows[i0 + k] : -1;
+      child[k] = k < cnt ? a.to[i0 + k] : -1;
+      pages[k] = k < cnt ? pages_of(length(i0 + k), a.bs_log2) : 0;
+      nmax = max(nmax, pages[k]);
+    }
     for (int j = s * SEG + threadIdx.x; j < min(nmax, (s + 1) * SEG); j += AT) {
       int prev = -1, e = -1, add = 0;
-      for (int i = i0; i < i1; ++i) {
-        if (j >= pages_of(a.row_a[i], a.bs_log2)) continue;
-        const int p = a.rows[i];
-        if (p != prev) {
+#pragma unroll
+      for (int k = 0; k < FORK_ROWS; ++k) {
+        if (j >= pages[k]) continue;
+        if (par[k] != prev) {
           if (add) atomicAdd(a.t.ref_count + e, add);
           add = 0;
-          prev = p;
-          e = a.t.block_table[p * stride + j];
+          prev = par[k];
+          e = a.t.block_table[prev * stride + j];
           if (e < 0 || e >= a.t.num_blocks) atomicOr(a.flags, FLAG_PAGES_SHAPE);
         }
         if (e >= 0 && e < a.t.num_blocks) ++add;
-        a.t.block_table[a.to[i] * stride + j] = e;
+        a.t.block_table[child[k] * stride + j] = e;
       }
       if (add) atomicAdd(a.t.ref_count + e, add);
     }
   }
+  if (!last_cta(a)) return;  // every CTA has read the lengths
+  if (bad) {
+    if (threadIdx.x == 0) atomicOr(a.flags, FLAG_PAGES_SHAPE);
+    return;
+  }
+  for (int i = threadIdx.x; i < a.n; i += AT) a.t.cached_len[a.to[i]] = length(i);
 }
 
 // ---------------------------------------------------------------------------- trim
 
-// One CTA: rows distinct, 0 <= new <= old. row_a[i]: the old length.
-__global__ void __launch_bounds__(PT) trim_plan(const Pages a) {
+// Checks: rows distinct, 0 <= new <= old. An item: a row, SEG entries. A page that several
+// rows of the call drop loses a count for each.
+__global__ void __launch_bounds__(AT) trim_kernel(const Pages a, int segs) {
   pdl_trigger();
   pdl_wait();
-  bool bad = mark_rows(a, a.rows);
-  for (int i = threadIdx.x; i < a.n; i += PT) {
-    const int r = row_at(a, i);
-    if (!row_ok(a, r)) continue;
-    const int old = a.t.cached_len[r], to = a.to[i];
-    if (!len_fits(a, old) || to < 0 || to > old) bad = true;
-    a.row_a[i] = old;
+  clear_rows(a);
+  __syncthreads();
+  bool bad = false;
+  constexpr int NR = 4;  // rows of a thread whose reads run together
+  for (int i0 = threadIdx.x; i0 < a.n; i0 += NR * AT) {
+    int r[NR], to[NR], old[NR];
+#pragma unroll
+    for (int k = 0; k < NR; ++k) {
+      const int i = i0 + k * AT;
+      r[k] = i < a.n ? row_at(a, i) : -1;
+      to[k] = i < a.n ? a.to[i] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < NR; ++k) old[k] = row_ok(a, r[k]) ? a.t.cached_len[r[k]] : 0;
+#pragma unroll
+    for (int k = 0; k < NR; ++k)
+      if (i0 + k * AT < a.n && (!row_ok(a, r[k]) || !add_row(r[k]) || !len_fits(a, old[k]) ||
+                                to[k] < 0 || to[k] > old[k]))
+        bad = true;
   }
-  verdict(a, !__syncthreads_or(bad));
-}
-
-__global__ void __launch_bounds__(AT) trim_apply(const Pages a, int segs) {
-  pdl_trigger();
-  pdl_wait();
-  if (!a.hdr->ok) return;
+  bad = __syncthreads_or(bad);
   const int64_t stride = a.t.max_blocks_per_seq;
-  const int64_t items = (int64_t)a.n * segs;
+  const int64_t items = bad ? 0 : (int64_t)a.n * segs;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int i = (int)(it / segs), s = (int)(it % segs);
+    const int s = (int)(it / a.n), i = (int)(it - (int64_t)s * a.n);
     const int r = row_at(a, i), to = a.to[i];
     const int j0 = pages_of(to, a.bs_log2) + s * SEG;
-    const int j1 = min(pages_of(a.row_a[i], a.bs_log2), j0 + SEG);
-    if (s == 0 && threadIdx.x == 0) a.t.cached_len[r] = to;
-    for (int j = j0 + threadIdx.x; j < j1; j += AT) {
-      int32_t* at = a.t.block_table + r * stride + j;
-      const int e = *at;
-      *at = -1;
-      if (e < 0 || e >= a.t.num_blocks) {
-        atomicOr(a.flags, FLAG_PAGES_SHAPE);
-      } else if (atomicSub(a.t.ref_count + e, 1) <= 0) {  // was free: a count stays >= 0
-        atomicAdd(a.t.ref_count + e, 1);
-        atomicOr(a.flags, FLAG_PAGES_SHAPE);
+    const int j1 = min(pages_of(a.t.cached_len[r], a.bs_log2), j0 + SEG);
+    int32_t* row = a.t.block_table + r * stride + j0 + threadIdx.x;
+    const int mine = j1 - j0 - (int)threadIdx.x;  // the thread's entries: 0, AT, .. below it
+    int e[SEG / AT], was[SEG / AT];
+#pragma unroll
+    for (int k = 0; k < SEG / AT; ++k)
+      if (k * AT < mine) {
+        e[k] = row[k * AT];
+        row[k * AT] = -1;
+      }
+#pragma unroll
+    for (int k = 0; k < SEG / AT; ++k) {
+      was[k] = 1;
+      if (k * AT < mine) {
+        if (e[k] < 0 || e[k] >= a.t.num_blocks)
+          atomicOr(a.flags, FLAG_PAGES_SHAPE);
+        else
+          was[k] = atomicSub(a.t.ref_count + e[k], 1);
       }
     }
+#pragma unroll
+    for (int k = 0; k < SEG / AT; ++k)
+      if (was[k] <= 0) {  // the page was free: a count stays >= 0
+        atomicAdd(a.t.ref_count + e[k], 1);
+        atomicOr(a.flags, FLAG_PAGES_SHAPE);
+      }
   }
+  if (!last_cta(a)) return;  // every CTA has read the lengths
+  if (bad) {
+    if (threadIdx.x == 0) atomicOr(a.flags, FLAG_PAGES_SHAPE);
+    return;
+  }
+  for (int i = threadIdx.x; i < a.n; i += AT) a.t.cached_len[row_at(a, i)] = a.to[i];
 }
 
 // -------------------------------------------------------------------------- extend
 
+// The last chunk c with chunk[c] <= k (the chunk that holds the page of rank k).
+__device__ __forceinline__ int chunk_of(const Pages& a, int k) {
+  int lo = 0, hi = a.chunks - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldcg(a.chunk + mid) <= k) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
 // CTA 0 plans the rows: row_a[i] the first fresh page's rank, row_b[i] the shared page that
 // row i parts from (-1: none), row_c the rows that do, in call order, row_d[i] the old
-// length. A row parts from its
-// partial last page when another holder of it remains: some holder is not in the call, or
-// a later row of the call is one. The other CTAs count the free pages of a chunk each; the
-// last to finish turns the counts into ranks and compares the free pages with the need.
+// length. A row parts from its partial last page when another holder of it remains: some
+// holder is not in the call, or a later row of the call is one. The other CTAs list the free
+// pages of a chunk each in blk_a; the last to finish turns their numbers into ranks, finds
+// the chunk of each row's first page (row_e) and compares the free pages with the need.
+// Up to PT rows what a row needs stays in its thread, and the holders of a page are counted
+// in a table in shared memory; beyond, by page in blk_b and blk_c.
+constexpr int SLOTS = 2 * PT;
 __global__ void __launch_bounds__(PT) extend_plan(const Pages a) {
+  __shared__ int s_page[SLOTS], s_cnt[SLOTS], s_last[SLOTS];
   pdl_trigger();
   pdl_wait();
   const int64_t stride = a.t.max_blocks_per_seq;
+  const bool small = a.n <= PT;
   if (blockIdx.x == 0) {
-    bool bad = mark_rows(a, a.rows);
-    auto partial_page = [&](int i) -> int {  // the page row i would write into, or -1
-      const int r = row_at(a, i);
-      if (!row_ok(a, r)) return -1;
-      const int old = a.t.cached_len[r];
-      if (!len_fits(a, old) || a.to[i] <= old || (old & ((1 << a.bs_log2) - 1)) == 0) return -1;
-      const int e = a.t.block_table[r * stride + (old >> a.bs_log2)];
-      return e >= 0 && e < a.t.num_blocks ? e : -2;
+    bool bad = false;
+    clear_rows(a);
+    for (int i = threadIdx.x; i < SLOTS; i += PT) {
+      s_page[i] = -1;
+      s_cnt[i] = 0;
+      s_last[i] = -1;
+    }
+    __syncthreads();
+    struct Row {
+      int old, to, page, ref;  // page: what the row would write into, -1 none, -2 damaged
     };
+    auto look = [&](int i) {
+      Row w = {0, 0, -1, 0};
+      const int r = row_at(a, i);
+      w.to = a.to[i];
+      if (!row_ok(a, r)) return w;
+      w.old = a.t.cached_len[r];
+      if (len_fits(a, w.old) && w.to > w.old && (w.old & ((1 << a.bs_log2) - 1)) != 0) {
+        const int e = a.t.block_table[r * stride + (w.old >> a.bs_log2)];
+        w.page = e >= 0 && e < a.t.num_blocks ? e : -2;
+        if (w.page >= 0) w.ref = a.t.ref_count[e];
+        if (w.page >= 0 && w.ref < 1) w.page = -2;
+      }
+      return w;
+    };
+    auto slot_of = [&](int page) {  // open addressing: at most PT pages in SLOTS places
+      int h = (int)((uint32_t)page * 2654435761u >> (32 - 11));
+      while (true) {
+        const int was = atomicCAS(s_page + h, -1, page);
+        if (was == -1 || was == page) return h;
+        h = (h + 1) & (SLOTS - 1);
+      }
+    };
+    static_assert(SLOTS == 1 << 11, "the hash keeps 11 bits");
+    int32_t *count = small ? s_cnt : a.blk_b, *last = small ? s_last : a.blk_c;
+    Row mine = {0, 0, -1, 0};
+    int slot = 0;
     for (int i = threadIdx.x; i < a.n; i += PT) {
       const int r = row_at(a, i);
-      if (!row_ok(a, r)) continue;
-      const int old = a.t.cached_len[r];
-      const int e = partial_page(i);
-      if (!len_fits(a, old) || !len_fits(a, a.to[i]) || a.to[i] < old || e == -2 ||
-          (e >= 0 && a.t.ref_count[e] < 1))
+      mine = look(i);
+      if (!row_ok(a, r) || !add_row(r) || !len_fits(a, mine.old) || !len_fits(a, mine.to) ||
+          mine.to < mine.old || mine.page == -2)
         bad = true;
-      if (e >= 0) {
-        a.blk_a[e] = 0;   // rows of the call that hold page e
-        a.blk_b[e] = -1;  // the last of them
+      if (mine.page >= 0) {
+        if (small) {
+          slot = slot_of(mine.page);
+        } else {
+          count[mine.page] = 0;
+          last[mine.page] = -1;
+        }
       }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < a.n; i += PT) {
-      const int e = partial_page(i);
-      if (e >= 0) {
-        atomicAdd(a.blk_a + e, 1);
-        atomicMax(a.blk_b + e, i);
+      const Row w = small ? mine : look(i);
+      if (w.page >= 0) {
+        atomicAdd(count + (small ? slot : w.page), 1);
+        atomicMax(last + (small ? slot : w.page), i);
       }
     }
     bad = __syncthreads_or(bad);
@@ -317,13 +391,18 @@ __global__ void __launch_bounds__(PT) extend_plan(const Pages a) {
     int cows = 0;
     for (int base = 0; base < a.n && !bad; base += PT) {
       const int i = base + threadIdx.x;
-      int cow = 0, e = -1;
+      int cow = 0;
       long long want = 0;
+      Row w = {0, 0, -1, 0};
       if (i < a.n) {
-        e = partial_page(i);
-        if (e >= 0 && a.t.ref_count[e] > 1)
-          cow = !(__ldcg(a.blk_a + e) == a.t.ref_count[e] && __ldcg(a.blk_b + e) == i);
-        want = cow + pages_of(a.to[i], a.bs_log2) - pages_of(a.t.cached_len[row_at(a, i)], a.bs_log2);
+        w = small ? mine : look(i);
+        if (w.page >= 0 && w.ref > 1) {
+          const int at = small ? slot : w.page;
+          const int cnt = small ? s_cnt[at] : __ldcg(count + at);
+          const int lst = small ? s_last[at] : __ldcg(last + at);
+          cow = !(cnt == w.ref && lst == i);
+        }
+        want = cow + pages_of(w.to, a.bs_log2) - pages_of(w.old, a.bs_log2);
       }
       long long total;
       int nc;
@@ -331,8 +410,8 @@ __global__ void __launch_bounds__(PT) extend_plan(const Pages a) {
       const int exc = scan_pt(cow, nc);
       if (i < a.n) {
         a.row_a[i] = (int32_t)(need + ex);
-        a.row_b[i] = cow ? e : -1;
-        a.row_d[i] = a.t.cached_len[row_at(a, i)];
+        a.row_b[i] = cow ? w.page : -1;
+        a.row_d[i] = w.old;
         if (cow) a.row_c[cows + exc] = i;
       }
       need += total;
@@ -349,36 +428,32 @@ __global__ void __launch_bounds__(PT) extend_plan(const Pages a) {
     const int4 v = chunk_counts(a, c);
     const int mine = (v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0);
     int total;
-    scan_pt(mine, total);
+    int32_t* dst = a.blk_a + (int64_t)c * CHUNK + scan_pt(mine, total);
+    const int p = c * CHUNK + threadIdx.x * 4;
+    if (v.x == 0) *dst++ = p;
+    if (v.y == 0) *dst++ = p + 1;
+    if (v.z == 0) *dst++ = p + 2;
+    if (v.w == 0) *dst++ = p + 3;
     if (threadIdx.x == 0) a.chunk[c] = total;
   }
   if (!last_cta(a)) return;
   const int free_pages = scan_chunks(a);
+  const bool bad = __ldcg(&a.hdr->rows_bad) != 0, few = __ldcg(&a.hdr->need) > free_pages;
   if (threadIdx.x == 0) {
-    const bool bad = __ldcg(&a.hdr->rows_bad) != 0, few = __ldcg(&a.hdr->need) > free_pages;
+    a.chunk[a.chunks] = free_pages;
     a.hdr->ok = !bad && !few;
     if (bad) atomicOr(a.flags, FLAG_PAGES_SHAPE);
     else if (few) atomicOr(a.flags, FLAG_NO_PAGES);
   }
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.n && !bad && !few; i += PT)
+    a.row_e[i] = chunk_of(a, __ldcg(a.row_a + i));
 }
 
-// blk_a[k]: the k-th free page, k < need.
-__global__ void __launch_bounds__(PT) extend_fresh(const Pages a) {
-  pdl_trigger();
-  pdl_wait();
-  const int need = a.hdr->need, base = a.chunk[blockIdx.x];
-  if (!a.hdr->ok || base >= need) return;
-  const int4 v = chunk_counts(a, blockIdx.x);
-  int total;
-  int k = base + scan_pt((v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0), total);
-  const int p = blockIdx.x * CHUNK + threadIdx.x * 4;
-  if (v.x == 0 && k < need) a.blk_a[k] = p;
-  k += v.x == 0;
-  if (v.y == 0 && k < need) a.blk_a[k] = p + 1;
-  k += v.y == 0;
-  if (v.z == 0 && k < need) a.blk_a[k] = p + 2;
-  k += v.z == 0;
-  if (v.w == 0 && k < need) a.blk_a[k] = p + 3;
+// The page of rank k, from chunk c on.
+__device__ __forceinline__ int page_of_rank(const Pages& a, int k, int c) {
+  while (k >= a.chunk[c + 1]) ++c;
+  return a.blk_a[(int64_t)c * CHUNK + k - a.chunk[c]];
 }
 
 // bytes (a multiple of 16) from src to dst by the CTA's threads, eight loads in flight each.
@@ -411,7 +486,7 @@ __global__ void __launch_bounds__(AT) extend_apply(const Pages a, const __grid_c
     const int cow = shared >= 0 ? 1 : 0;
     const int j0 = pages_of(old, a.bs_log2) - cow, j1 = pages_of(to, a.bs_log2);
     for (int j = j0 + lane; j < j1; j += 32) {
-      const int p = a.blk_a[a.row_a[i] + j - j0];
+      const int p = page_of_rank(a, a.row_a[i] + j - j0, a.row_e[i]);
       a.t.block_table[r * stride + j] = p;
       a.t.ref_count[p] = 1;
     }
@@ -430,7 +505,7 @@ __global__ void __launch_bounds__(AT) extend_apply(const Pages a, const __grid_c
     const int64_t b0 = (int64_t)s * COPY_BYTES;
     if (b0 >= filled) continue;
     uint8_t* base = (uint8_t*)pl.p[pool].base;
-    const int dst = a.blk_a[a.row_a[i]], src = a.row_b[i];
+    const int dst = page_of_rank(a, a.row_a[i], a.row_e[i]), src = a.row_b[i];
     copy_bytes(base + dst * pl.p[pool].page_bytes + b0, base + src * pl.p[pool].page_bytes + b0,
                (int)min(filled - b0, (int64_t)COPY_BYTES));
   }
@@ -462,7 +537,7 @@ __global__ void __launch_bounds__(PT) compact_plan(const Pages a, int table_ctas
       }
     }
     bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) a.chunk[a.chunks + blockIdx.x] = bad ? 1 : 0;
+    if (threadIdx.x == 0) a.chunk[a.chunks + 1 + blockIdx.x] = bad ? 1 : 0;
   } else {
     const int c = blockIdx.x - table_ctas;
     const int4 v = chunk_counts(a, c);
@@ -472,7 +547,7 @@ __global__ void __launch_bounds__(PT) compact_plan(const Pages a, int table_ctas
   }
   if (!last_cta(a)) return;
   bool bad = false;
-  for (int i = threadIdx.x; i < table_ctas; i += PT) bad |= __ldcg(a.chunk + a.chunks + i) != 0;
+  for (int i = threadIdx.x; i < table_ctas; i += PT) bad |= __ldcg(a.chunk + a.chunks + 1 + i) != 0;
   bad = __syncthreads_or(bad);
   const int live = scan_chunks(a);
   __syncthreads();
@@ -570,8 +645,8 @@ PagesWs pages_layout(int32_t num_blocks, int32_t table_rows) {
   size_t o = 256;  // the flag word and the ticket
   w.hdr = o;   o += 256;
   w.rows = o;  o = align_up(o + 5 * R, 256);
-  w.chunk = o; o = align_up(o + 4 * ((size_t)(num_blocks + CHUNK - 1) / CHUNK + TABLE_CTAS), 256);
-  w.blk = o;   o = align_up(o + 2 * N, 256);
+  w.chunk = o; o = align_up(o + 4 * ((size_t)(num_blocks + CHUNK - 1) / CHUNK + 1 + TABLE_CTAS), 256);
+  w.blk = o;   o = align_up(o + 3 * N, 256);
   w.total = o;
   return w;
 }
@@ -584,14 +659,15 @@ Pages make(const sv_page_table& t, void* ws) {
   a.flags = (uint32_t*)base;
   a.ticket = (uint32_t*)base + 1;
   a.hdr = (PagesHdr*)(base + w.hdr);
-  a.mark = (int32_t*)(base + w.rows);
-  a.row_a = a.mark + t.table_rows;
+  a.row_a = (int32_t*)(base + w.rows);
   a.row_b = a.row_a + t.table_rows;
   a.row_c = a.row_b + t.table_rows;
   a.row_d = a.row_c + t.table_rows;
+  a.row_e = a.row_d + t.table_rows;
   a.chunk = (int32_t*)(base + w.chunk);
   a.blk_a = (int32_t*)(base + w.blk);
   a.blk_b = a.blk_a + t.num_blocks;
+  a.blk_c = a.blk_b + t.num_blocks;
   a.chunks = (t.num_blocks + CHUNK - 1) / CHUNK;
   while ((1 << a.bs_log2) < t.block_size) ++a.bs_log2;
   return a;
@@ -609,8 +685,17 @@ PoolList pool_list(int n, const sv_page_data* p) {
   return l;
 }
 
-unsigned grid_for(int64_t items, int sms) {  // resident at once: 8 CTAs of AT threads an SM
-  const int64_t most = (int64_t)sms * (2048 / AT);
+size_t row_set_bytes(const sv_page_table& t) { return ((size_t)t.table_rows + 31) / 32 * 4; }
+template <class F>
+cudaError_t allow_set(F kernel, size_t bytes) {  // beyond what a launch may ask for unasked
+  return bytes <= 16 * 1024 ? cudaSuccess
+                            : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+// Resident at once, 8 CTAs of AT threads an SM; an odd number, so that what repeats along the
+// items (every other row dropped, say) falls to all CTAs.
+unsigned grid_for(int64_t items, int sms) {
+  const int64_t most = ((int64_t)sms * (2048 / AT) - 1) | 1;
   return (unsigned)(items < 1 ? 1 : items < most ? items : most);
 }
 
@@ -628,11 +713,12 @@ cudaError_t launch_pages_fork(const sv_page_table& t, int n, const int32_t* pare
   a.rows = parents;
   a.to = children;
   a.fork_len = fork_len;
-  cudaError_t e = launch_pdl(fork_plan, dim3(1), dim3(PT), 0, s, a);
+  const size_t set = row_set_bytes(t);
+  cudaError_t e = allow_set(fork_kernel, set);
   if (e != cudaSuccess) return e;
   const int segs = (t.max_blocks_per_seq + SEG - 1) / SEG;
   const int64_t items = (int64_t)((n + FORK_ROWS - 1) / FORK_ROWS) * segs;
-  return launch_pdl(fork_apply, dim3(grid_for(items, sms)), dim3(AT), 0, s, a, segs);
+  return launch_pdl(fork_kernel, dim3(grid_for(items, sms)), dim3(AT), set, s, a, segs);
 }
 
 cudaError_t launch_pages_trim(const sv_page_table& t, int n, const int32_t* rows,
@@ -641,10 +727,11 @@ cudaError_t launch_pages_trim(const sv_page_table& t, int n, const int32_t* rows
   a.n = n;
   a.rows = rows;
   a.to = new_len;
-  cudaError_t e = launch_pdl(trim_plan, dim3(1), dim3(PT), 0, s, a);
+  const size_t set = row_set_bytes(t);
+  cudaError_t e = allow_set(trim_kernel, set);
   if (e != cudaSuccess) return e;
   const int segs = (t.max_blocks_per_seq + SEG - 1) / SEG;
-  return launch_pdl(trim_apply, dim3(grid_for((int64_t)n * segs, sms)), dim3(AT), 0, s, a, segs);
+  return launch_pdl(trim_kernel, dim3(grid_for((int64_t)n * segs, sms)), dim3(AT), set, s, a, segs);
 }
 
 cudaError_t launch_pages_extend(const sv_page_table& t, int n, const int32_t* rows,
@@ -654,9 +741,10 @@ cudaError_t launch_pages_extend(const sv_page_table& t, int n, const int32_t* ro
   a.n = n;
   a.rows = rows;
   a.to = new_len;
-  cudaError_t e = launch_pdl(extend_plan, dim3(1 + a.chunks), dim3(PT), 0, s, a);
+  const size_t set = row_set_bytes(t);
+  cudaError_t e = allow_set(extend_plan, set);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(extend_fresh, dim3(a.chunks), dim3(PT), 0, s, a);
+  e = launch_pdl(extend_plan, dim3(1 + a.chunks), dim3(PT), set, s, a);
   if (e != cudaSuccess) return e;
   const PoolList l = pool_list(num_pools, pools);
   const int64_t copies = (int64_t)n * l.n * l.seg_max, rows_items = (n + AT / 32 - 1) / (AT / 32);

@@ -48,7 +48,7 @@ ALL = ["fork", "extend", "trim", "compact"]
 @pytest.mark.parametrize("which", ALL)
 @pytest.mark.parametrize("bad,status", [
     (dict(num_blocks=0), 2), (dict(num_blocks=1 << 28), 2), (dict(block_size=12), 2),
-    (dict(block_size=4), 2), (dict(block_size=1 << 17), 2), (dict(table_rows=-1), 2),
+    (dict(block_size=4), 2), (dict(block_size=1 << 17), 2), (dict(table_rows=-1), 2), (dict(table_rows=(1 << 20) + 1), 2),
     (dict(max_blocks_per_seq=0), 2), (dict(ref_count=None), 1), (dict(block_table=None), 1),
     (dict(cached_len=None), 1), (dict(ref_count=FAKE + 4), 4), (dict(block_table=ODD), 4),
     (dict(cached_len=ODD), 4)])
