@@ -339,7 +339,7 @@ def test_graph_replays_a_step_on_its_own_stream():
     assert d.status() == 0
 
 
-@pytest.mark.parametrize("op,launches", [("fork", 1), ("extend", 2), ("trim", 1), ("compact", 3)])
+@pytest.mark.parametrize("op,launches", [("fork", 1), ("extend", 2), ("trim", 1), ("compact", 2)])
 def test_failed_launch_is_reported_and_the_workspace_serves_on(op, launches):
     for k in range(launches):
         m = filled(4, 30, 8, [20, 9, 0, 16], max_blocks=6, seed=3)
@@ -393,6 +393,20 @@ def test_more_than_a_thousand_rows_part_from_shared_pages():
     to = [13 + r % 12 for r in rows]
     d.extend(rows, to)
     assert m.extend(rows, to)
+    assert d.status() == 0
+    d.same()
+
+
+@pytest.mark.parametrize("nb", [4096, 4097, 4096 * 11 - 3])
+def test_pools_of_many_chunks(nb):
+    """Around the pool size above which the ranks have a kernel of their own."""
+    bs, R = 8, 120
+    m = filled(R, nb, bs, [(37 * r) % 500 for r in range(R)], max_blocks=70, seed=nb)
+    d = Device(m, pools=1, width=4)
+    rows = list(range(0, R, 2))
+    d.trim(rows, [m.lens[r] // 3 for r in rows])
+    m.trim(rows, [m.lens[r] // 3 for r in rows])
+    assert d.compact() == m.compact()
     assert d.status() == 0
     d.same()
 
