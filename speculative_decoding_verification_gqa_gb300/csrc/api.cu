@@ -23,7 +23,10 @@ constexpr int SWITCH_TILES_TC_FP8 = SV_SWITCH_F8;
 constexpr int SWITCH_TILES_TC_BF16 = SV_SWITCH_BF16;
 constexpr int SWITCH_TILES_MMA = 2;
 constexpr int SWITCH_TILES_PREFIX = 3;    // 128-key tiles of 256 rows
-constexpr int SWITCH_TILES_SEQUENCE = 4;  // 64-key tiles, two CTAs per SM
+constexpr int SWITCH_TILES_SEQUENCE = 4;  // 64-key tiles of 128 rows
+// SM time of a 64-key tile of 128 rows (two at a time on an SM), in 128-key tiles of 256 rows.
+constexpr float SEQUENCE_COST_BF16 = 0.30f;
+constexpr float SEQUENCE_COST_FP8 = 0.42f;
 // Per-tile compute floor of each kernel, in CTAs streaming at once (a 128-key tile's
 // compute time x HBM bandwidth / the tile's bytes: bf16 about 0.9 us x 6.8 TB/s / 64 KB,
 // E4M3 about 0.89 us x 6.8 TB/s / 32 KB). The cost model is not applied to the mma.sync
@@ -474,6 +477,7 @@ SV_API sv_status spec_verify_attn_shared(const sv_attn_desc* desc, const void* q
     l.max_units = (int)lay.max_units[k];
     l.n_ctas = lay.n_ctas[k];
     l.kt = !lines ? attn_mma_kt() : k == 0 ? 128 : 64;
+    l.tile_cost = fp8 ? SEQUENCE_COST_FP8 : SEQUENCE_COST_BF16;
     if (lines) l.switch_tiles = k == 0 ? SWITCH_TILES_PREFIX : SWITCH_TILES_SEQUENCE;
     l.hdr = (PlanHdr*)(ws + lay.line[k].hdr);
     l.units = (int4*)(ws + lay.line[k].units);
@@ -489,8 +493,8 @@ SV_API sv_status spec_verify_attn_shared(const sv_attn_desc* desc, const void* q
   if (launch_plan_shared(line[0], line[1], lines, s) != cudaSuccess) return SV_ERR_CUDA;
   if (g_ev_start && cudaEventRecord(g_ev_start, s) != cudaSuccess) return SV_ERR_CUDA;
   if (lines) {
-    if (launch_attn_prefixes(line[0], fp8, s) != cudaSuccess) return SV_ERR_CUDA;
     if (launch_attn_sequences(line[1], fp8, s) != cudaSuccess) return SV_ERR_CUDA;
+    if (launch_attn_prefixes(line[0], fp8, s) != cudaSuccess) return SV_ERR_CUDA;
   } else if (launch_attn_mma_shared(line[1], fp8, s) != cudaSuccess) {
     return SV_ERR_CUDA;
   }

@@ -17,9 +17,14 @@
 //           K/V tile is read once for both row tiles, whose softmaxes alternate on the
 //           tensor cores. Bound by those: a step of both row tiles is 1152 clocks of MMAs.
 //   RT = 1  the sequences behind them. Units of 128 rows, 256 columns, 64-key tiles, two
-//           CTAs per SM: the units are short (a few hundred keys) and each starts with a
-//           read of Q and ends with one of O, which the other CTA's unit covers. Bound by
-//           the K/V stream.
+//           independent lanes of work in a CTA (its halves, each with its own warps, shared
+//           memory, TMEM and range of the line): the units are short (a few hundred keys) and
+//           each starts with a read of Q and ends with one of O, which the other half's unit
+//           covers. Bound by the K/V stream.
+// The two run at the same time, each on a share of the SMs that the plan chooses (the one is
+// bound by the tensor cores, the other by HBM): the sequences' kernel comes first, one CTA
+// per SM, those without a range leave at once, and the prefixes' CTAs take the SMs that are
+// free, the last of them those that the sequences leave.
 //
 //   warp 0   TMA producer of K tiles     warp 2   TMA producer of V tiles
 //   warp 1   S issuer: S_r = Q_r K^T     warp 3   P V issuer: O_r += P_r V
@@ -52,18 +57,18 @@ struct __align__(8) Bars {
   int abort;
 };
 
-// The 128 threads of row tile r's warpgroup meet; with `v`, whether it held for all of them.
-__device__ __forceinline__ void wg_sync(int r) {
-  asm volatile("barrier.sync %0, 128;" ::"r"(1 + r) : "memory");
+// The 128 threads of softmax warpgroup g meet; with `v`, whether it held for all of them.
+__device__ __forceinline__ void wg_sync(int g) {
+  asm volatile("barrier.sync %0, 128;" ::"r"(1 + g) : "memory");
 }
-__device__ __forceinline__ bool wg_and(int r, bool v) {
+__device__ __forceinline__ bool wg_and(int g, bool v) {
   __syncwarp();  // the reduction counts whole warps: arrive converged
   uint32_t o;
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.and.pred q, %2, 128, p;\n"
       " selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(o)
-      : "r"((uint32_t)v), "r"(1 + r)
+      : "r"((uint32_t)v), "r"(1 + g)
       : "memory");
   return o != 0;
 }
@@ -71,13 +76,13 @@ __device__ __forceinline__ bool wg_and(int r, bool v) {
 template <int HD, bool F8, int RT>
 struct Layout {
   static constexpr int KT = RT * HK;        // keys per tile
-  static constexpr uint32_t TMEM_COLS = RT * 256;
   static constexpr uint32_t COL_O = 0, COL_S = RT * 128, COL_P = RT * 192, COL_Q = RT * 224;
   static constexpr int CONV_WARP0 = SOFTMAX_WARP0 + 4 * RT;
   static constexpr int NCONV = 64 * RT;  // decoding threads
   static constexpr int BLK = KT * 128;      // one 128-byte-wide column block of a tile
   static constexpr int TILE = KT * HD * 2;  // one 16-bit tile
   static constexpr int RAW = F8 ? KT * HD : TILE;  // a tile as the cache has it
+  static constexpr int HALVES = RT == 2 ? 1 : 2;
   static constexpr int NS = HD == 64 && RT == 2 ? 4 : 3;  // stages of each ring
   static constexpr int K = 0;
   static constexpr int V = K + NS * RAW;
@@ -88,14 +93,16 @@ struct Layout {
   // a row tile's 128 bytes a row for reordering Q and O: its part of Q before that is
   // written and after it is used, or (E4M3, whose hi and lo terms come together) another
   static constexpr int STG = F8 ? Q + RT * QB : Q;
-  static constexpr int BARS = (F8 ? STG : Q) + RT * QB;
-  static constexpr int AMAX = BARS + (int)sizeof(Bars);  // E4M3: each query row's largest
-                                                         // magnitude (bf16 bits)
-  static constexpr size_t SMEM = (size_t)AMAX + (F8 ? RT * 512 : 0);
+  static constexpr int TILES = (F8 ? STG : Q) + RT * QB;  // bytes of all that, per half
+  static constexpr int BARS = HALVES * TILES;
+  static constexpr int AMAX = BARS + HALVES * (int)sizeof(Bars);  // E4M3: each query row's
+                                                                  // largest magnitude
+  static constexpr size_t SMEM = (size_t)AMAX + (F8 ? HALVES * RT * 512 : 0);
   static_assert(!F8 || HD == 128, "E4M3 rows of one head are one 128-byte swizzle row");
-  // 227 KB for a CTA, 228 KB with 1 KB per CTA of the SM's for two
-  static_assert(SMEM <= (RT == 2 ? 227 : 113) * 1024, "shared memory above the limit");
-  static constexpr int THREADS = 32 * CONV_WARP0 + (F8 ? NCONV : 0);
+  static_assert(TILES % 1024 == 0, "a half's tiles keep the swizzle's alignment");
+  static_assert(SMEM <= 227 * 1024, "dynamic shared memory above the per-CTA limit");
+  static constexpr int WARPS = CONV_WARP0 + (F8 ? NCONV / 32 : 0);  // of a half
+  static constexpr int THREADS = 32 * WARPS * HALVES;
 };
 
 // D[tmem] (+)= A[smem] * B[smem], 16-bit and E4M3 operands
@@ -141,20 +148,38 @@ struct Seg {
   int u, j0, j1;
 };
 
-__device__ __forceinline__ bool seg_next(const AttnParams& p, int num_units, int& t, int t_end,
-                                         int& u, Seg& s) {
-  if (t >= t_end || u >= num_units) return false;
-  const int4* src = reinterpret_cast<const int4*>(p.sunits + u);
-  const int4 a = src[0], b = src[1], c = src[2];
-  s.d = SharedUnit{(int64_t)(uint32_t)a.x | (int64_t)a.y << 32, a.z, a.w, b.x, b.y, b.z, b.w,
-                   c.x, c.y, c.z, c.w};
-  s.u = u;
-  s.j0 = t - s.d.tile;
-  s.j1 = min(t_end - s.d.tile, s.d.nt);
-  if (s.j1 <= s.j0) return false;
-  t = s.d.tile + s.j1;
-  ++u;
-  return true;
+// The units of a CTA's range [t0, t1) of the line, unit u0 holding its first tile. The first
+// unit comes last: every CTA then begins at the first key of some unit (its whole units, then
+// the head of the last, then the tail of the first, which begins about where the head ended),
+// so that at any time all row tiles of a prefix are near the same keys and share them through
+// L2. In the line's own order 128 prefix units of 134 MB read 1.0 GB from HBM.
+struct Walk {
+  int t0, t1, u0, u1;  // u1: the unit where the next range begins
+  int k;               // units visited; -1: none is left
+};
+
+__device__ __forceinline__ bool seg_next(const AttnParams& p, int num_units, Walk& w, Seg& s) {
+  if (w.k < 0) return false;
+  for (int pass = 0; pass < 2; ++pass) {
+    int u = w.u0 + 1 + w.k;
+    if (pass == 1 || u > w.u1 || u >= num_units) {
+      u = w.u0;
+      w.k = -1;
+    }
+    const int4* src = reinterpret_cast<const int4*>(p.sunits + u);
+    const int4 a = src[0], b = src[1], c = src[2];
+    s.d = SharedUnit{(int64_t)(uint32_t)a.x | (int64_t)a.y << 32, a.z, a.w, b.x, b.y, b.z, b.w,
+                     c.x, c.y, c.z, c.w};
+    s.u = u;
+    s.j0 = max(w.t0 - s.d.tile, 0);
+    s.j1 = min(w.t1 - s.d.tile, s.d.nt);
+    if (w.k < 0) break;
+    if (s.j1 > 0) {  // (a unit at the very end of the range has no tile of it)
+      ++w.k;
+      break;
+    }
+  }
+  return s.j1 > s.j0;
 }
 // Row tiles of a segment, and steps of its tile j.
 template <int RT>
@@ -167,34 +192,37 @@ __device__ __forceinline__ int steps_of(const Seg& s, int j) {
 }
 
 template <int HD, bool F8, int RT>
-__global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
+__global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, 1)
     attn_parts_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv) {
   using L = Layout<HD, F8, RT>;
   constexpr int KT = L::KT;
-  constexpr uint32_t TMEM_COLS = L::TMEM_COLS, COL_O = L::COL_O, COL_S = L::COL_S,
+  constexpr uint32_t COL_O = L::COL_O, COL_S = L::COL_S,
                      COL_P = L::COL_P, COL_Q = L::COL_Q;
-  extern __shared__ __align__(1024) uint8_t smem[];  // 128-byte swizzled tiles: 1 KiB aligned
-  Bars* bars = (Bars*)(smem + L::BARS);
+  extern __shared__ __align__(1024) uint8_t smem_cta[];  // 128-byte swizzled tiles: 1 KiB aligned
+  const int cta_warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // uniform, and so are
+  const int half = cta_warp / L::WARPS, warp = cta_warp % L::WARPS;    // the roles' branches
+  const int tid = threadIdx.x - half * L::WARPS * 32, lane = tid & 31;
+  const int worker = blockIdx.x * L::HALVES + half;  // whose range of the line this is
+  uint8_t* smem = smem_cta + half * L::TILES;
+  Bars* bars = (Bars*)(smem_cta + L::BARS) + half;
   volatile int* abort = &bars->abort;
   const Waiter wt{abort, p.flags, p.wait_limit > 0 ? p.wait_limit : TIMEOUT_CYCLES};
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform: the roles' branches too
-  // The prefixes' kernel waits for the plan and lets the sequences' kernel, which needs the
-  // plan only, fill the SMs as they empty. The sequences' kernel therefore knows that the
-  // plan is complete (every CTA before it had waited for it), and waits for the prefixes'
-  // kernel at its end, so that its completion stands for both.
-  if constexpr (RT == 2) pdl_wait();
+  // The sequences' kernel waits for the plan and lets the prefixes' kernel start. That one
+  // therefore knows that the plan is complete (every CTA before it had waited for it), and
+  // waits for the sequences' kernel at its end, so that its completion stands for both.
+  if constexpr (RT == 1) pdl_wait();
   pdl_trigger();
 
   const int num_units = p.hdr->num_units;
-  const int2 rb = p.cta_tab[blockIdx.x], re = p.cta_tab[blockIdx.x + 1];
-  const int t_begin = rb.x, t_end = re.x, u_first = rb.y;
-  const bool aligned = (saddr(smem) & 1023) == 0;  // the swizzle phases below assume it
-  if (t_begin >= t_end || !aligned) {              // uniform across the CTA
-    if (!aligned && tid == 0) atomicOr(p.flags, FLAG_ATTN_SHAPE);
-    if constexpr (RT == 1) pdl_wait();
-    return;
+  const int2 rb = p.cta_tab[worker], re = p.cta_tab[worker + 1];
+  // a half without a range finds no unit
+  const Walk walk0 = {rb.x, re.x, rb.y, re.y, rb.x < re.x && rb.y < num_units ? 0 : -1};
+  const bool aligned = (saddr(smem_cta) & 1023) == 0;  // the swizzle phases below assume it
+  if (p.cta_tab[blockIdx.x * L::HALVES].x >= p.cta_tab[(blockIdx.x + 1) * L::HALVES].x || !aligned) {
+    if (!aligned && threadIdx.x == 0) atomicOr(p.flags, FLAG_ATTN_SHAPE);
+    if constexpr (RT == 2) pdl_wait();
+    return;  // uniform across the CTA
   }
   if (tid == 0) {
     for (int s = 0; s < NST; ++s) {
@@ -219,17 +247,19 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
     bars->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 1) {
+  Bars* bars0 = (Bars*)(smem_cta + L::BARS);
+  if (cta_warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     saddr(&bars->tmem_base)),
-                 "r"(TMEM_COLS)
+                     saddr(&bars0->tmem_base)),
+                 "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, bars->tmem_base, 0);
+  const uint32_t tmem_cta = __shfl_sync(0xffffffffu, bars0->tmem_base, 0);
+  const uint32_t tmem = tmem_cta + half * 256;
   auto wwait = [&](uint64_t* bar, uint32_t par) -> bool {  // by a whole warp
     return __all_sync(0xffffffffu, mbar_wait(bar, par, wt));
   };
@@ -248,13 +278,16 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
     if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)tm) : "memory");
     const int box = min(p.block_size, KT), nbox = KT / box, tg = 32 / nbox;
     const bool mine = lane < nbox;
+    // A sequence's keys are read once, a prefix's by every row tile: the one stream must not
+    // push the other out of L2.
+    const uint64_t policy = RT == 1 ? policy_evict_first() : policy_evict_last();
     // test hook: the first tile of the range is never loaded, so every wait for it runs out
     const bool withhold = p.stall_first_tile != 0;
-    int t = t_begin, u = u_first;
+    Walk walk = walk0;
     Seg s;
     uint32_t it = 0;
     bool ok = true;
-    while (ok && seg_next(p, num_units, t, t_end, u, s)) {
+    while (ok && seg_next(p, num_units, walk, s)) {
       const int32_t* tab = p.block_table + (size_t)s.d.table_row * p.bt_stride;
       auto box_pos = [&](int j, int n) { return j * KT + n * box; };
       auto seen = [&](int pos) { return pos < s.d.nkeys && pos + box > s.d.start; };
@@ -292,11 +325,11 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
         if (mine) {
           const uint32_t dst = ring + st * L::RAW + lane * box * 128;
           if constexpr (F8) {
-            tma_load_3d(dst, tm, &full[st], 0, s.d.g, grow);
+            tma_load_3d(dst, tm, &full[st], 0, s.d.g, grow, policy);
           } else {
 #pragma unroll
             for (int c = 0; c < HD / 64; ++c)
-              tma_load_3d(dst + c * L::BLK, tm, &full[st], c * 64, s.d.g, grow);
+              tma_load_3d(dst + c * L::BLK, tm, &full[st], c * 64, s.d.g, grow, policy);
           }
         }
       }
@@ -320,11 +353,11 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
       // K and Q: K-major, 128-byte rows, 8-row groups 1024 B apart, 32 B per K step
       const uint64_t kdesc0 = smem_desc(saddr(smem + L::K), 16, 1024);
       const uint64_t qdesc0 = smem_desc(saddr(smem + L::Q), 16, 1024);
-      int t = t_begin, u = u_first;
+      Walk walk = walk0;
       Seg s;
       uint32_t it = 0, n[RT] = {}, units[RT] = {};
       bool ok = true;
-      while (ok && seg_next(p, num_units, t, t_end, u, s)) {
+      while (ok && seg_next(p, num_units, walk, s)) {
         const int nr = tiles_of<RT>(s);
         for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
           const uint32_t st = it % L::NS;
@@ -388,11 +421,11 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
       constexpr uint32_t ID_PV = F8 ? idesc_f16(HD, 1) : idesc_bf16(HD, 1);
       // V: MN-major, 64-column blocks L::BLK apart (LBO), 8-key groups 1024 B apart (SBO)
       const uint64_t vdesc0 = smem_desc(saddr(smem + (F8 ? L::CV : L::V)), L::BLK, 1024);
-      int t = t_begin, u = u_first;
+      Walk walk = walk0;
       Seg s;
       uint32_t it = 0, n[RT] = {};
       bool ok = true;
-      while (ok && seg_next(p, num_units, t, t_end, u, s)) {
+      while (ok && seg_next(p, num_units, walk, s)) {
         const int nr = tiles_of<RT>(s);
         for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
           constexpr uint32_t NV = F8 ? NCV : L::NS;
@@ -434,24 +467,27 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
   } else if (warp < L::CONV_WARP0) {
     // ------------------------------------------------------------ softmax of row tile r
     const int r = (warp - SOFTMAX_WARP0) >> 2;
-    const int rr = (warp & 3) * 32 + lane;  // the thread's row in its tile = TMEM lane
-    const uint32_t tq = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    int t = t_begin, u = u_first;
+    const int wg = r + half;                // its barrier
+    // the thread's row in its tile = its TMEM lane (a warp reaches the 32 lanes of its place
+    // in the CTA modulo 4)
+    const int rr = (cta_warp & 3) * 32 + lane;
+    const uint32_t tq = tmem + ((uint32_t)((cta_warp & 3) * 32) << 16);
+    Walk walk = walk0;
     Seg s;
     uint32_t it = 0, n = 0;  // tiles of the range; steps of this row tile
     bool ok = true;
     uint8_t* stg = smem + L::STG + r * L::QB;  // 128 bytes a row, 16-byte chunks swizzled
     uint8_t* qsm = smem + L::Q + r * L::QB;
-    uint32_t* row_amax = reinterpret_cast<uint32_t*>(smem + L::AMAX) + r * MT;
+    uint32_t* row_amax = reinterpret_cast<uint32_t*>(smem_cta + L::AMAX) + wg * MT;
     auto chunk_at = [](int row, int k) -> uint32_t { return row * 128 + ((k ^ (row & 7)) << 4); };
     // A warp whose wait failed stays until its warpgroup meets at the next unit, where all of
     // its warps leave together: none is left waiting at a barrier.
-    while (seg_next(p, num_units, t, t_end, u, s)) {
+    while (seg_next(p, num_units, walk, s)) {
       if (r >= tiles_of<RT>(s)) {
         it += s.j1 - s.j0;
         continue;
       }
-      if (!wg_and(r, ok)) break;  // (and the staging rows of the last unit have been read)
+      if (!wg_and(wg, ok)) break;  // (and the staging rows of the last unit have been read)
       const int row = r * MT + rr;
       const bool live = row < s.d.rows;
       float sc = p.scale_log2;  // score scale in log2 units
@@ -508,7 +544,7 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
             if (qc == 0) row_amax[qr] = amax;
           }
         }
-        wg_sync(r);
+        wg_sync(wg);
         sc = p.scale_log2 * p.kv_scale[s.d.g] *
              __int_as_float((127 - exponent(row_amax[rr])) << 23);
       } else {
@@ -520,14 +556,14 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
           for (int i = 0; i < QC; ++i)
             *reinterpret_cast<uint4*>(stg + chunk_at(q0 + i * QI, qc)) = v[i];
         }
-        wg_sync(r);
+        wg_sync(wg);
         if constexpr (L::QS) {  // the other half of the row waits for the first
           uint32_t rq[32];
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             *reinterpret_cast<uint4*>(rq + 4 * k) = *reinterpret_cast<uint4*>(stg + chunk_at(rr, k));
           tmem_st32(tq + COL_Q + r * 32, rq);
-          wg_sync(r);
+          wg_sync(wg);
           if (qc >= 8) {
 #pragma unroll
             for (int i = 0; i < QC; ++i)
@@ -665,10 +701,10 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
       }
       // 32 columns at a time through the staging rows (a warp's own 32), so that whole
       // 128-byte lines are written
-      const size_t at = ((size_t)blockIdx.x + s.u) * (RT * MT) + r * MT;
-      const int w0 = (warp & 3) * 32;
+      const size_t at = ((size_t)worker + s.u) * (RT * MT) + r * MT;
+      const int w0 = (cta_warp & 3) * 32;
 #pragma unroll 1
-      for (int c = 0; c < HD / 32; ++c) {
+      for (int c = 0; c < HD / 32 && r * MT + w0 < s.d.rows; ++c) {  // (warps with live rows)
         uint32_t ro[32];
         tmem_ld32(tq + COL_O + r * 128 + c * 32, ro);
         tmem_wait_ld();
@@ -707,11 +743,11 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
       const uint32_t dst_off = (c >> 2) * L::BLK + rw * 128;
       const uint32_t w0 = ((2 * (c & 3)) ^ ph) << 4, w1 = ((2 * (c & 3) + 1) ^ ph) << 4;
       constexpr int CR = L::NCONV / 8, RSTEP = CR * 128;  // rows of a pass
-      int t = t_begin, u = u_first;
+      Walk walk = walk0;
       Seg s;
       uint32_t it = 0;
       bool ok = true;
-      while (ok && seg_next(p, num_units, t, t_end, u, s)) {
+      while (ok && seg_next(p, num_units, walk, s)) {
         for (int j = s.j0; j < s.j1; ++j, ++it) {
           const uint32_t rs = it % L::NS, cs = it % NCV;
           if (!mbar_wait(&bars->v_full[rs], (it / L::NS) & 1, wt) ||
@@ -753,12 +789,12 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, RT == 2 ? 1 : 2)
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 1) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(TMEM_COLS)
+  if (cta_warp == 1) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_cta),
+                 "r"(512)
                  : "memory");
   }
-  if constexpr (RT == 1) pdl_wait();
+  if constexpr (RT == 2) pdl_wait();
 }
 
 template <int HD, bool F8, int RT>
@@ -773,7 +809,7 @@ cudaError_t launch_hd(const AttnParams& p, cudaStream_t s) {
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(p.n_ctas), dim3(L::THREADS), L::SMEM, s, p, mk, mv);
+  return launch_pdl(kernel, dim3(p.n_ctas / L::HALVES), dim3(L::THREADS), L::SMEM, s, p, mk, mv);
 }
 
 template <int RT>

@@ -178,6 +178,7 @@ struct AttnParams {
   int2* unit_ctas;            // [U] first and last CTA that a unit's tiles fall to
   int row_log2;               // log2 of the query rows of a prefix's unit
   int kt;                     // keys per tile of the line
+  float tile_cost;            // the sequences' line: SM time of its tiles in the prefixes' tiles
   int num_groups;
   const int32_t* group_begin;  // [num_groups + 1]
   const int32_t* prefix_len;   // [num_groups]

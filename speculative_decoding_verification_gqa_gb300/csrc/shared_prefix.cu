@@ -99,6 +99,7 @@ __device__ __forceinline__ void put_unit(const AttnParams& p, bool both, int u, 
 
 constexpr int CACHED = 1024;        // sequences, and groups, kept in shared memory
 constexpr int CACHED_UNITS = 1024;  // unit starts kept in shared memory
+constexpr int MIN_PART = 4;         // tiles that are worth a CTA of the prefixes
 constexpr int CACHED_CTAS = 1024;   // CTA starts (a launch has two per SM at most)
 
 struct PlanShared {
@@ -111,6 +112,7 @@ struct PlanShared {
     int4 entry[PLAN_T];
     int32_t cta[CACHED_CTAS + 1];
   };
+  unsigned long long prefix_units, prefix_tiles;
   int maxmt;
 };
 
@@ -122,8 +124,8 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
   const bool both = gridDim.x == 1;  // one line for all parts
   const bool prefixes = both || blockIdx.x == 0, sequences = both || blockIdx.x == 1;
   const AttnParams& p = prefixes && !both ? pa : pb;
-  const int tid = threadIdx.x, NG = p.num_groups, B = p.B, kt = p.kt, G = p.G;
-  const int box = min(p.block_size, kt), row_log2 = p.row_log2;
+  const int tid = threadIdx.x, NG = p.num_groups, B = p.B, G = p.G;
+  const int seq_box = min(p.block_size, pb.kt), row_log2 = p.row_log2;
   __shared__ PlanShared sm;
   pdl_trigger();
   pdl_wait();
@@ -133,7 +135,10 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
     T0 = p.seq_lens[tid];
     D0 = p.draft_len[tid];
   }
-  if (tid == 0) sm.maxmt = 0;
+  if (tid == 0) {
+    sm.maxmt = 0;
+    sm.prefix_units = sm.prefix_tiles = 0;
+  }
   bool bad = false;
   // the groups: consecutive ranges of the batch
   for (int n = tid; n < NG; n += PLAN_T) {
@@ -163,7 +168,7 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
     s.alone = P == 0;
     s.group = n;
     s.nmt = (G * s.rows + MT - 1) / MT;
-    s.nt = (s.nkeys - (P & ~(box - 1)) + kt - 1) / kt;
+    s.nt = (s.nkeys - (P & ~(seq_box - 1)) + pb.kt - 1) / pb.kt;
     return s;
   };
   int64_t q_total = 0, U = 0, TT = 0;
@@ -204,6 +209,8 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
     TT += tot[1];
     bad = __syncthreads_or(bad);
   }
+  // (both CTAs know the sequences' work, for the shares of the SMs)
+  const int64_t U_seq = U, TT_seq = TT;
   if (!sequences) U = TT = 0;
   bad = bad || q_total > p.q_rows || U > p.max_units || TT >= 0x7fffffffll;
   auto seq_at = [&](int b) {
@@ -228,7 +235,7 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
     s.table_row = g0;
     s.group = n;
     s.nmt = (G * s.rows + (1 << row_log2) - 1) >> row_log2;
-    s.nt = (P + kt - 1) / kt;
+    s.nt = (P + pa.kt - 1) / pa.kt;
     s.mbase = tile_base(q0, G, row_log2, n);
     return s;
   };
@@ -238,7 +245,7 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
                                 : last_at_most(B, u, [&](int i) { return seq[i].ubase; });
       const SharedSeq s = seq_at(b);
       const int k = u - s.ubase, g = k / s.nmt, tile = s.tbase + k * s.nt;
-      put_unit(p, both, u, NG + b, s, g, k - g * s.nmt, s.start & ~(box - 1), tile);
+      put_unit(p, both, u, NG + b, s, g, k - g * s.nmt, s.start & ~(seq_box - 1), tile);
       if (u < CACHED_UNITS) sm.ubeg[u] = tile;
     }
     // every window row, a warp per sequence
@@ -253,12 +260,12 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
       }
     }
   }
-  if (!bad && prefixes) {
-    for (int n = tid; n < NG; n += PLAN_T) {
-      const SharedSeq s = prefix_part(n);
-      atomicMax(&sm.maxmt, s.nmt);
-      if (both) p.parts[n] = s;
-    }
+  for (int n = tid; n < NG && !bad; n += PLAN_T) {
+    const SharedSeq s = prefix_part(n);
+    atomicMax(&sm.maxmt, s.nmt);
+    atomicAdd(&sm.prefix_units, (unsigned long long)p.Hkv * s.nmt);
+    atomicAdd(&sm.prefix_tiles, (unsigned long long)p.Hkv * s.nmt * s.nt);
+    if (both) p.parts[n] = s;
   }
   __syncthreads();
   // Units of the prefixes, entry (row tile mt, part v) by entry, the KV heads of an entry
@@ -312,24 +319,53 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
     if (bad) atomicOr(p.flags, FLAG_ATTN_SHAPE);
     p.hdr->num_units = (int32_t)U;
     p.hdr->total_tiles = (int32_t)TT;
-    p.hdr->kt = kt;
+    p.hdr->kt = p.kt;
     p.hdr->sum_w = bad ? 0 : q_total;
     p.ubeg[U] = (int32_t)TT;
     if (U <= CACHED_UNITS) sm.ubeg[U] = (int32_t)TT;
   }
   __syncthreads();
-  // CTA c starts at the first tile at or after position c * VT / C of the virtual line, C at
-  // most VT, so that every CTA between the first and the last of a unit has tiles of it
+  // CTA c starts at the first tile at or after its position on the virtual line. One line:
+  // the CTAs' parts of it are equal. Two lines run at the same time (attn_parts.cu): with W_p
+  // and W_s the work of the prefixes and the sequences, in prefix tiles, the sequences get the
+  // N SMs that finish theirs in T = (W_p + W_s) / SMs, the prefixes' CTAs on the other SMs
+  // get parts of T each, and the last N, which follow the sequences, what is left. No part
+  // is shorter than a tile, so every CTA between the first and the last of a unit has tiles
+  // of it.
   const int32_t* ubeg = U <= CACHED_UNITS ? sm.ubeg : p.ubeg;
   const int X = p.switch_tiles;
   const int64_t VT = TT + U * X;
-  const int C = (int)min((int64_t)min(p.n_ctas, CACHED_CTAS), max(VT, (int64_t)1));
-  const int64_t part = VT / C;
-  const int rest = (int)(VT - part * C);
+  int C1 = (int)min((int64_t)min(p.n_ctas, CACHED_CTAS), max(VT, (int64_t)1)), C2 = 0;
+  int64_t V1 = VT;  // C1 CTAs take equal parts of [0, V1), C2 after them of [V1, VT)
+  if (!both) {
+    const int sms = pa.n_ctas;  // one CTA of prefixes per SM
+    const int64_t VP = sm.prefix_tiles + sm.prefix_units * pa.switch_tiles;
+    const float ws = (float)(TT_seq + U_seq * pb.switch_tiles) * pb.tile_cost;
+    const float T = fmaxf(((float)VP + ws) / sms, (float)MIN_PART);
+    const int N = VP > 0 ? min(max((int)ceilf(ws / T), 1), max(sms - 1, 1)) : sms;
+    if (sequences) {
+      C1 = min(C1, 2 * N);
+    } else {
+      C1 = (int)min((int64_t)max(sms - N, 1), max(VT, (int64_t)1));
+      const int64_t early = (int64_t)(C1 * T);
+      if (VT - early >= N * MIN_PART) {
+        V1 = early;
+        C2 = N;
+      }
+    }
+  }
+  const int C = C1 + C2;
+  const int64_t part1 = V1 / C1, part2 = C2 > 0 ? (VT - V1) / C2 : 0;
+  const uint32_t rest1 = (uint32_t)(V1 - part1 * C1), rest2 = (uint32_t)(VT - V1 - part2 * C2);
+  auto begin_of = [&](int c) -> int64_t {
+    if (c <= C1) return c * part1 + c * rest1 / (uint32_t)C1;
+    const int k = c - C1;
+    return V1 + k * part2 + k * rest2 / (uint32_t)C2;
+  };
   for (int c = tid; c <= p.n_ctas; c += PLAN_T) {
     int2 e = make_int2((int32_t)TT, (int32_t)U);
     if (c < C && TT > 0) {
-      const int64_t v0 = c * part + (int)((uint32_t)(c * rest) / (uint32_t)C);
+      const int64_t v0 = begin_of(c);
       const int u = last_at_most((int)U, v0, [&](int i) { return ubeg[i] + (int64_t)i * X; });
       const int64_t into = v0 - (ubeg[u] + (int64_t)u * X) - X;  // < 0: before its tiles
       e = make_int2((int32_t)(ubeg[u] + (into > 0 ? into : 0)), u);
