@@ -342,7 +342,8 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
     const int64_t VP = sm.prefix_tiles + sm.prefix_units * pa.switch_tiles;
     const float ws = (float)(TT_seq + U_seq * pb.switch_tiles) * pb.tile_cost;
     const float T = fmaxf(((float)VP + ws) / sms, (float)MIN_PART);
-    const int N = VP > 0 ? min(max((int)ceilf(ws / T), 1), max(sms - 1, 1)) : sms;
+    const int half_n = ((int)ceilf(ws / T) + 1) / 2;  // pairs of SMs
+    const int N = VP > 0 ? min(max(2 * half_n, 2), max(sms - 2, 1)) : sms;
     if (sequences) {
       C1 = min(C1, 2 * N);
     } else {
@@ -483,7 +484,7 @@ SharedWs shared_ws_layout(const sv_attn_desc* d, int num_groups, int sms, bool l
   w.tile_unit = o; o = align_up(o + sizeof(int32_t) * prefix_tiles, 256);
   for (int k = lines ? 0 : 1; k < 2; ++k) {
     SharedWs::Line& l = w.line[k];
-    w.n_ctas[k] = lines && k == 1 ? 2 * sms : sms;
+    w.n_ctas[k] = lines && k == 1 ? 4 * ((sms + 1) / 2) : sms;  // (clusters of two CTAs)
     const size_t n_ctas = w.n_ctas[k], U = (size_t)w.max_units[k], slots = U + n_ctas;
     l.hdr = o;       o += 256;
     l.units = l.sunits = o;
