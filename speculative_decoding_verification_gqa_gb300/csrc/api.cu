@@ -25,8 +25,8 @@ constexpr int SWITCH_TILES_MMA = 2;
 constexpr int SWITCH_TILES_PREFIX = 3;    // 128-key tiles of 256 rows
 constexpr int SWITCH_TILES_SEQUENCE = 4;  // 64-key tiles of 128 rows
 // SM time of a 64-key tile of 128 rows (two at a time on an SM), in 128-key tiles of 256 rows.
-constexpr float SEQUENCE_COST_BF16 = 0.30f;
-constexpr float SEQUENCE_COST_FP8 = 0.48f;
+constexpr float SEQUENCE_COST_BF16 = 0.28f;
+constexpr float SEQUENCE_COST_FP8 = 0.45f;
 // Per-tile compute floor of each kernel, in CTAs streaming at once (a 128-key tile's
 // compute time x HBM bandwidth / the tile's bytes: bf16 about 0.9 us x 6.8 TB/s / 64 KB,
 // E4M3 about 0.89 us x 6.8 TB/s / 32 KB). The cost model is not applied to the mma.sync

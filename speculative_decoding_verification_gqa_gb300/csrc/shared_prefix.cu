@@ -356,12 +356,12 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
     }
   }
   const int C = C1 + C2;
-  const int64_t part1 = V1 / C1, part2 = C2 > 0 ? (VT - V1) / C2 : 0;
-  const uint32_t rest1 = (uint32_t)(V1 - part1 * C1), rest2 = (uint32_t)(VT - V1 - part2 * C2);
+  // (VT < 2^31 + 2^24: 32 bits without a sign)
   auto begin_of = [&](int c) -> int64_t {
-    if (c <= C1) return c * part1 + c * rest1 / (uint32_t)C1;
-    const int k = c - C1;
-    return V1 + k * part2 + k * rest2 / (uint32_t)C2;
+    const bool one = c <= C1;
+    const uint32_t k = one ? c : c - C1, n = one ? C1 : C2, v = (uint32_t)(one ? V1 : VT - V1);
+    const uint32_t part = v / n, rest = v - part * n;
+    return (one ? 0 : V1) + (int64_t)k * part + k * rest / n;
   };
   for (int c = tid; c <= p.n_ctas; c += PLAN_T) {
     int2 e = make_int2((int32_t)TT, (int32_t)U);
@@ -382,31 +382,31 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
   }
 }
 
-// One output row (window row, query head) per group of 8 lanes, HD / 8 columns a lane: joins
-// the partials that the row's prefix unit and its sequence's unit left, two at a time.
-// Memory-bound: reads each partial row (4 d + 8 bytes) once and writes 2 d bytes; what costs
-// is the chain of dependent reads before the partials (row, units, their CTAs), so rows are
-// many to a warp and their tables small.
+// One output row (window row, query head) per 16 lanes, HD / 16 columns a lane: joins the
+// partials that the row's prefix unit and its sequence's unit left, four at a time (a row has
+// two to four). Memory-bound: reads each partial row (4 d + 8 bytes) once and writes 2 d
+// bytes; what costs beside that is the chain of dependent reads before the partials (row,
+// units, their CTAs), so the tables are small and rows many.
 template <int HD>
-__global__ void __launch_bounds__(256) combine_shared_kernel(AttnParams pa, AttnParams pb) {
-  constexpr int PER = HD / 8, MAXP = 2;
+__global__ void __launch_bounds__(256, 4) combine_shared_kernel(AttnParams pa, AttnParams pb) {
+  constexpr int LANES = 16, PER = HD / LANES, MAXP = 3, ROWS = 256 / LANES;
   pdl_trigger();
   pdl_wait();
-  const int64_t rows = min(pa.hdr->sum_w, pb.hdr->sum_w) * pb.Hq;  // 0: the call was refused
-  const int sub = threadIdx.x & 7;
-  for (int64_t o = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3); o < rows;
-       o += (int64_t)gridDim.x * 32) {
-    const int64_t w = o / pb.Hq;
-    const int h = (int)(o - w * pb.Hq), g = h / pb.G, hl = h - g * pb.G;
-    const RowInfo r = pb.rows[w];
-    const int rs = r.i * pb.G + hl, us = r.ubase + g * r.nmt + rs / MT;
+  // 0: the call was refused. (32 bits: 2^22 units of 128 rows at most.)
+  const int rows = (int)(min(pa.hdr->sum_w, pb.hdr->sum_w) * pb.Hq);
+  const int sub = threadIdx.x % LANES;
+  for (int o = blockIdx.x * ROWS + threadIdx.x / LANES; o < rows; o += gridDim.x * ROWS) {
+    const int w = o / pb.Hq, h = o - w * pb.Hq, g = h / pb.G, hl = h - g * pb.G;
+    const int4 r0 = reinterpret_cast<const int4*>(pb.rows + w)[0];  // RowInfo: i, ubase, nmt,
+    const int of_group = pb.rows[w].of_group;                       // mbase
+    const int rs = r0.x * pb.G + hl, us = r0.y + g * r0.z + rs / MT;
     const int2 cs = pb.unit_ctas[us];
     int ua = 0, ra = 0;
     int2 ca = make_int2(0, -1);
-    if (r.mbase >= 0) {
-      const int64_t pr = (int64_t)r.of_group * pb.G + hl;
-      ua = pa.tile_unit[r.mbase + (int)(pr >> pa.row_log2)] + g;
-      ra = (int)(pr & ((1 << pa.row_log2) - 1));
+    if (r0.w >= 0) {
+      const int pr = of_group * pb.G + hl;
+      ua = pa.tile_unit[r0.w + (pr >> pa.row_log2)] + g;
+      ra = pr & ((1 << pa.row_log2) - 1);
       ca = pa.unit_ctas[ua];
     }
     // the partials' rows, first those of the sequence's unit
@@ -420,15 +420,15 @@ __global__ void __launch_bounds__(256) combine_shared_kernel(AttnParams pa, Attn
       float2 ml[MAXP];
       float4 ov[MAXP][PER / 4];
 #pragma unroll
-      for (int k = 0; k < MAXP; ++k) {  // an unused place repeats the last one, with l = 0
-        const int i = min(k0 + k, n - 1);
+      for (int k = 0; k < MAXP; ++k) {
+        const int i = k0 + k;
         const bool own = i < ns;
         const int64_t at = own ? at_s + (int64_t)i * MT : at_a + ((int64_t)(i - ns) << pa.row_log2);
-        ml[k] = (own ? pb.part_ml : pa.part_ml)[at];
-        if (k0 + k >= n) ml[k] = make_float2(-INFINITY, 0.f);
         const float4* src = reinterpret_cast<const float4*>((own ? pb.part_o : pa.part_o) + at * HD) + sub;
+        ml[k] = i < n ? (own ? pb.part_ml : pa.part_ml)[at] : make_float2(-INFINITY, 0.f);
 #pragma unroll
-        for (int e = 0; e < PER / 4; ++e) ov[k][e] = __ldcs(src + e * 8);
+        for (int e = 0; e < PER / 4; ++e)
+          ov[k][e] = i < n ? __ldcs(src + e * LANES) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
       float bm = m;
 #pragma unroll
@@ -440,8 +440,7 @@ __global__ void __launch_bounds__(256) combine_shared_kernel(AttnParams pa, Attn
       for (int e = 0; e < PER; ++e) acc[e] *= rescale;
 #pragma unroll
       for (int k = 0; k < MAXP; ++k) {
-        if (k0 + k >= n) continue;
-        const float wgt = exp2f(ml[k].x - mu);
+        const float wgt = exp2f(ml[k].x - mu);  // 0 for unused places (m = -inf)
         l += ml[k].y * wgt;
 #pragma unroll
         for (int e = 0; e < PER / 4; ++e) {
@@ -454,12 +453,12 @@ __global__ void __launch_bounds__(256) combine_shared_kernel(AttnParams pa, Attn
       m = bm;
     }
     const float inv = (pb.kv_scale ? pb.kv_scale[pb.Hkv + g] : 1.f) / l;
-    uint2* dst = reinterpret_cast<uint2*>((__nv_bfloat16*)pb.out + o * HD) + sub;
+    uint2* dst = reinterpret_cast<uint2*>((__nv_bfloat16*)pb.out + (int64_t)o * HD) + sub;
 #pragma unroll
     for (int e = 0; e < PER / 4; ++e) {
       const __nv_bfloat162 a = __floats2bfloat162_rn(acc[4 * e] * inv, acc[4 * e + 1] * inv);
       const __nv_bfloat162 c = __floats2bfloat162_rn(acc[4 * e + 2] * inv, acc[4 * e + 3] * inv);
-      dst[e * 8] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
+      dst[e * LANES] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&c));
     }
   }
 }
@@ -510,7 +509,7 @@ cudaError_t launch_plan_shared(const AttnParams& pa, const AttnParams& pb, bool 
 }
 
 cudaError_t launch_combine_shared(const AttnParams& pa, const AttnParams& pb, cudaStream_t s) {
-  const int64_t ctas = (pb.q_rows * pb.Hq + 31) / 32;
+  const int64_t ctas = (pb.q_rows * pb.Hq + 15) / 16;
   const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(ctas, 8 * (int64_t)pa.n_ctas));
   return pb.d == 128 ? launch_pdl(combine_shared_kernel<128>, dim3(grid), dim3(256), 0, s, pa, pb)
                      : launch_pdl(combine_shared_kernel<64>, dim3(grid), dim3(256), 0, s, pa, pb);
