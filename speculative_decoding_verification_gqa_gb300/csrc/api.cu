@@ -123,7 +123,7 @@ SV_API int sv_inject_wait_timeout(int64_t limit_cycles) {
   return g_stall_limit.exchange(limit_cycles > 0 ? (long long)limit_cycles : 0) > 0 ? 1 : 0;
 }
 
-SV_API int sv_version(void) { return 400; }  // 0.4.0: wait-timeout injection
+SV_API int sv_version(void) { return 500; }  // 0.5.0: shared prefixes, pages of a paged cache
 
 SV_API const char* sv_status_string(sv_status s) {
   switch (s) {
