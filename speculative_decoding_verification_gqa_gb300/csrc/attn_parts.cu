@@ -168,7 +168,7 @@ __device__ __forceinline__ bool seg_next(const AttnParams& p, int num_units, Wal
       w.k = -1;
     }
     const int4* src = reinterpret_cast<const int4*>(p.sunits + u);
-    const int4 a = __ldcg(src), b = __ldcg(src + 1), c = __ldcg(src + 2);
+    const int4 a = src[0], b = src[1], c = src[2];
     s.d = SharedUnit{(int64_t)(uint32_t)a.x | (int64_t)a.y << 32, a.z, a.w, b.x, b.y, b.z, b.w,
                      c.x, c.y, c.z, c.w};
     s.u = u;
@@ -215,11 +215,14 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, 1)
   if constexpr (RT == 1) pdl_wait();
   pdl_trigger();
 
-  // (the plan's tables are read past L1, which a grid that did not wait itself may find stale)
+  // (the prefixes' grid did not wait for the plan itself: it reads the start of the plan past
+  // L1 and fences, so that no line that L1 may have kept serves the unit table. Reading that
+  // past L1 every time instead costs a tenth of the call.)
   const int num_units = __ldcg(&p.hdr->num_units);
   const int2 rb = __ldcg(p.cta_tab + worker), re = __ldcg(p.cta_tab + worker + 1);
   // a half without a range finds no unit
   const Walk walk0 = {rb.x, re.x, rb.y, re.y, rb.x < re.x && rb.y < num_units ? 0 : -1};
+  if constexpr (RT == 2) __threadfence();
   const bool aligned = (saddr(smem_cta) & 1023) == 0;  // the swizzle phases below assume it
   const int cta_begin = __ldcg(&p.cta_tab[blockIdx.x * L::HALVES].x);
   const int cta_end = __ldcg(&p.cta_tab[(blockIdx.x + 1) * L::HALVES].x);
