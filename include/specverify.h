@@ -199,6 +199,9 @@ SV_API size_t spec_verify_attn_shared_workspace_size(const sv_attn_desc* desc,
  * are read through each sequence's own row, and what a block of another sequence than the
  * first holds before them is not used.
  *
+ * Same bits for the same arguments every time. Worth its joining of two results per row
+ * when a group has several sequences and its prefix is long beside what follows.
+ *
  *   group_begin  int32 [num_groups + 1], from 0 to batch, not decreasing (a group may be
  *                empty); 1 <= num_groups <= batch
  *   prefix_len   int32 [num_groups], 0 <= prefix_len[n] <= every seq_lens[b] of the group;
@@ -232,7 +235,9 @@ SV_API sv_status spec_verify_attn_shared(const sv_attn_desc* desc, const void* q
  * One verification step on rows with T_b cached positions: extend the rows to T_b + 1 +
  * D_b, write the window's K/V, attend, accept, trim the rows to T_b + accept_len[b].
  *
- * Every call is asynchronous, allocates nothing and may be captured into a graph. The rows
+ * A page's count may be larger than its entries (pages that the caller holds otherwise).
+ * Every call is asynchronous, allocates nothing and may be captured into a graph; the four
+ * may share a workspace, as calls of one entry point may. The rows
  * of a call are checked on the device before anything is changed; a call that fails a
  * check changes nothing and sets the workspace flag (sv_workspace_status:
  * SV_ERR_DEVICE_SHAPE). A row may stand in a call once only. An entry in use that names
@@ -511,7 +516,8 @@ SV_API sv_status sv_workspace_status(void* workspace, int clear, void* stream);
 /* Human-readable name of a status code (static string). */
 SV_API const char* sv_status_string(sv_status status);
 
-/* Attention kernel selection, for measurement and tests: 0 = automatic (default),
+/* Attention kernel selection, for measurement and tests (spec_verify_attn and its paged,
+ * host-lengths and shared-prefix forms): 0 = automatic (default),
  * 1 = warp-level mma.sync kernel, 2 = tcgen05 kernel. Returns the previous value, or -1
  * if the value is unknown or the kernel is not built. Process-wide. */
 SV_API int sv_set_attn_kernel(int which);
@@ -566,8 +572,10 @@ SV_API void sv_set_profile_events(void* start_event, void* stop_event);
 /* Fault injection for tests, on the host: after `after` more kernel launches of the
  * library, the next launch fails without reaching the GPU and the call that makes it
  * returns SV_ERR_CUDA (spec_verify_attn and the paged call launch three kernels in this
- * order: plan, attention, combine; the host-lengths call attention and combine;
- * spec_accept and spec_draft_signals one each). The call's earlier launches have run;
+ * order: plan, attention, combine; the host-lengths call attention and combine; the
+ * shared-prefix call plan, sequences, prefixes, combine, or with the mma.sync kernel plan,
+ * attention, combine; spec_accept, spec_draft_signals, spec_pages_fork and _trim one each;
+ * spec_pages_extend two; spec_pages_compact two, three beyond 4096 pages). The call's earlier launches have run;
  * its outputs are then unspecified, and its workspace serves the next call as it is. One
  * failure per arming; after < 0 disarms. Returns the launches that were still to go
  * before a pending failure, or -1 if none was pending. Process-wide. */

@@ -391,7 +391,8 @@ constexpr int64_t MAX_SHARED_UNITS = 1 << 22;
 sv_status check_shared(const sv_attn_desc* desc, int32_t num_groups) {
   const sv_status st = check_desc(desc);
   if (st != SV_OK) return st;
-  if (desc->sliding_window != 0 || num_groups < 1 || num_groups > std::max(desc->batch, 1))
+  if (desc->sliding_window != 0 || num_groups < 0 || num_groups > std::max(desc->batch, 1) ||
+      (num_groups == 0 && desc->batch > 0))
     return SV_ERR_SHAPE;
   const SharedWs lay = shared_ws_layout(desc, num_groups, 0, false);
   return lay.max_units[1] > MAX_SHARED_UNITS ? SV_ERR_SHAPE : SV_OK;

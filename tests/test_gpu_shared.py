@@ -236,7 +236,7 @@ def test_positions_past_32_bits_of_bytes(kernel):
     assert_within(out.view(torch.int16).cpu().numpy().view(np.uint16), w, x)
 
 
-@pytest.mark.parametrize("after", [0, 1, 2])
+@pytest.mark.parametrize("after", [0, 1, 2, 3])  # plan, sequences, prefixes, join
 def test_failed_launch_is_reported_and_the_workspace_serves_on(after):
     ensure_built()
     w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=20)
@@ -341,3 +341,94 @@ def test_groups_of_very_different_sizes(kernel):
     groups = [(20, [(21 + b % 5, 3) for b in range(260)])] + [(9, [(12, 0)])] * 9000
     w, x, gbeg, P = inputs(groups, Hq=16, Hkv=1, d=64, seed=3)
     assert_within(run(x, pages(x, gbeg, P, 8, seed=5), gbeg, P), w, x)
+
+
+def test_two_streams_at_once_and_a_given_stream(kernel):
+    """Calls on two streams with a workspace each, in flight together, and one on a stream
+    passed by argument: the bits of calls alone."""
+    cases = []
+    for seed, groups in ((30, TWO), (31, [(500, [(510 + 9 * b, b % 4) for b in range(12)])])):
+        w, x, gb, P = inputs(groups, Hq=8, Hkv=2, d=128, seed=seed)
+        pg = pages(x, gb, P, 16, seed=seed)
+        alone = run(x, pg, gb, P)
+        i32 = lambda a: torch.from_numpy(np.asarray(a, dtype=np.int32)).cuda()  # noqa: E731
+        t = to_device(x, pg)
+        cases.append((t, i32(gb), i32(P), x, alone, sv.new_workspace(1 << 27), torch.empty_like(t[0]),
+                      torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (q, k, v, bt, T, D, _), g_, p_, x, _, ws, out, s in cases:
+            sv.spec_verify_attn_shared(q, k, v, bt, T, D, g_, p_, out=out, workspace=ws, stream=s,
+                                       max_draft_len=int(x["draft_len"].max()),
+                                       max_seq_len=int(x["seq_lens"].max()))
+    torch.cuda.synchronize()
+    for _, _, _, _, alone, ws, out, _ in cases:
+        assert np.array_equal(out.view(torch.int16).cpu().numpy().view(np.uint16), alone)
+        assert sv.workspace_status(ws) == 0
+
+
+def test_calls_follow_each_other_without_a_wait(kernel):
+    """Calls of this and other kinds in one stream, each reading what the one before wrote:
+    the second's queries are the first's output, and the paged call's the second's."""
+    w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=32)
+    pg = pages(x, gb, P, 16, seed=4, junk=-1)
+    full = pages(x, gb, np.zeros_like(P), 16, seed=4)  # (the paged call reads every own entry)
+    q, k, v, bt, T, D, _ = to_device(x, pg)
+    _, k2, v2, bt2, _, _, _ = to_device(x, full)
+    i32 = lambda a: torch.from_numpy(np.asarray(a, dtype=np.int32)).cuda()  # noqa: E731
+    kw = dict(max_draft_len=7, max_seq_len=1000)
+    ws, ws2 = sv.new_workspace(1 << 27), sv.new_workspace(1 << 27)
+
+    def chain(wait):
+        a = sv.spec_verify_attn_shared(q, k, v, bt, T, D, i32(gb), i32(P), workspace=ws, **kw)
+        wait()
+        b = sv.spec_verify_attn_shared(a, k, v, bt, T, D, i32(gb), i32(P), workspace=ws, **kw)
+        wait()
+        c = sv.spec_verify_attn_paged(b, k2, v2, bt2, T, D, workspace=ws2, **kw)
+        wait()
+        d = sv.spec_verify_attn_shared(c, k, v, bt, T, D, i32(gb), i32(P), workspace=ws, **kw)
+        torch.cuda.synchronize()
+        return [t.clone() for t in (a, b, c, d)]
+
+    slow = chain(torch.cuda.synchronize)
+    for _ in range(10):
+        for s, f in zip(slow, chain(lambda: None)):
+            assert torch.equal(s, f)
+
+
+def test_nothing_in_the_batch():
+    ensure_built()
+    z = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = torch.zeros(0, 8, 128, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(4, 16, 2, 128, dtype=torch.bfloat16, device="cuda")
+    o = sv.spec_verify_attn_shared(q, k, k, torch.zeros(0, 3, dtype=torch.int32, device="cuda"), z[:0], z[:0],
+                                   torch.zeros(2, dtype=torch.int32, device="cuda"), z, max_draft_len=3,
+                                   max_seq_len=30)
+    assert o.shape == (0, 8, 128)
+
+
+def test_binding_refuses():
+    ensure_built()
+    w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=33)
+    q, k, v, bt, T, D, _ = to_device(x, pages(x, gb, P, 16, seed=4))
+    i32 = lambda a: torch.from_numpy(np.asarray(a, dtype=np.int32)).cuda()  # noqa: E731
+    kw = dict(max_draft_len=7, max_seq_len=1000)
+    ok = (q, k, v, bt, T, D, i32(gb), i32(P))
+
+    def bad(err, i, t, **more):
+        a = list(ok)
+        a[i] = t
+        with pytest.raises(err):
+            sv.spec_verify_attn_shared(*a, **{**kw, **more})
+
+    bad(TypeError, 0, q.float())
+    bad(TypeError, 4, T.long())
+    bad(TypeError, 6, i32(gb).cpu())
+    bad(TypeError, 7, None)
+    bad(ValueError, 0, q[:, :, :64].contiguous())
+    bad(ValueError, 1, k.transpose(0, 1))
+    bad(ValueError, 3, bt[:2])
+    bad(ValueError, 6, i32(gb)[:2])
+    bad(ValueError, 0, q, out=torch.empty_like(q)[:2])
+    bad(ValueError, 0, q, kv_scale=torch.ones(2, 3, device="cuda"))
+    bad(sv.SpecVerifyError, 0, q, workspace=sv.new_workspace(1024))
