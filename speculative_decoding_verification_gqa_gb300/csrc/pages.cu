@@ -25,6 +25,7 @@ constexpr int PT = 1024;          // threads of the planning kernels
 constexpr int CHUNK = 4096;       // pages counted by one CTA (PT threads x 4)
 constexpr int AT = 256;           // threads of the other kernels
 constexpr int SEG = 512;          // table entries of one work item
+constexpr int NR = 4;             // rows of a thread whose reads run together
 constexpr int FORK_ROWS = 8;      // consecutive children of one work item
 constexpr int COPY_BYTES = 16384; // page bytes of one copying work item
 constexpr int TABLE_CTAS = 64;    // compact: CTAs that check the tables
@@ -73,6 +74,8 @@ __device__ __forceinline__ int pages_of(int len, int bs_log2) {
 __device__ __forceinline__ bool len_fits(const Pages& a, int64_t len) {
   return len >= 0 && len <= ((int64_t)a.t.max_blocks_per_seq << a.bs_log2);
 }
+
+static_assert(PT == 1024, "the scan below has 32 warps' sums");
 
 // Exclusive scan of one whole number per thread over a block of PT threads.
 template <class T>
@@ -172,19 +175,35 @@ __global__ void __launch_bounds__(AT) fork_kernel(const Pages a, int segs) {
   clear_rows(a);
   __syncthreads();
   bool bad = false;
-  for (int i = threadIdx.x; i < a.n; i += AT) {
-    const int c = a.to[i];
-    if (!row_ok(a, c) || !add_row(c)) bad = true;
+  for (int i0 = threadIdx.x; i0 < a.n; i0 += NR * AT) {
+    int c[NR];
+#pragma unroll
+    for (int k = 0; k < NR; ++k) c[k] = i0 + k * AT < a.n ? a.to[i0 + k * AT] : 0;
+#pragma unroll
+    for (int k = 0; k < NR; ++k)
+      if (i0 + k * AT < a.n && (!row_ok(a, c[k]) || !add_row(c[k]))) bad = true;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < a.n; i += AT) {
-    const int p = a.rows[i], c = a.to[i];
-    if (!row_ok(a, p) || !row_ok(a, c) || has_row(p) || a.t.cached_len[c] != 0) {
-      bad = true;
-      continue;
+  for (int i0 = threadIdx.x; i0 < a.n; i0 += NR * AT) {
+    int p[NR], c[NR], have[NR], len[NR], used[NR];
+#pragma unroll
+    for (int k = 0; k < NR; ++k) {
+      const int i = i0 + k * AT;
+      p[k] = i < a.n ? a.rows[i] : -1;
+      c[k] = i < a.n ? a.to[i] : -1;
+      len[k] = i < a.n && a.fork_len ? a.fork_len[i] : 0;
     }
-    const int have = a.t.cached_len[p], len = a.fork_len ? a.fork_len[i] : have;
-    if (!len_fits(a, have) || len < 0 || len > have) bad = true;
+#pragma unroll
+    for (int k = 0; k < NR; ++k) {
+      const bool ok = row_ok(a, p[k]) && row_ok(a, c[k]);
+      have[k] = ok ? a.t.cached_len[p[k]] : 0;
+      used[k] = ok ? a.t.cached_len[c[k]] : 1;
+    }
+#pragma unroll
+    for (int k = 0; k < NR; ++k)
+      if (i0 + k * AT < a.n && (used[k] != 0 || has_row(p[k]) || !len_fits(a, have[k]) ||
+                                len[k] < 0 || len[k] > have[k]))
+        bad = true;
   }
   bad = __syncthreads_or(bad);
   auto length = [&](int i) { return a.fork_len ? a.fork_len[i] : a.t.cached_len[a.rows[i]]; };
@@ -239,7 +258,6 @@ __global__ void __launch_bounds__(AT) trim_kernel(const Pages a, int segs) {
   clear_rows(a);
   __syncthreads();
   bool bad = false;
-  constexpr int NR = 4;  // rows of a thread whose reads run together
   for (int i0 = threadIdx.x; i0 < a.n; i0 += NR * AT) {
     int r[NR], to[NR], old[NR];
 #pragma unroll

@@ -21,7 +21,11 @@ namespace sv {
 
 namespace {
 
-constexpr int PLAN_T = 1024;
+// Threads of the plan. It is a chain of barriers and short steps that each warp goes through:
+// a call of 2 sequences took 15.2, 13.6, 13.0 us with 1024, 512, 256 threads (captured), one
+// of 64 sequences 69.3, 68.7, 69.8.
+constexpr int PLAN_T = 512;
+static_assert(PLAN_T % 32 == 0 && PLAN_T <= 1024, "whole warps, whose sums one warp scans");
 
 // Exclusive scans of N values per thread over the block (PLAN_T threads).
 template <int N>
@@ -44,7 +48,7 @@ __device__ void scan_block(const int64_t (&v)[N], int64_t (&ex)[N], int64_t (&to
     for (int k = 0; k < N; ++k) s_warp[k][wid] = x[k];
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < N; ++k) w[k] = s_warp[k][lane];
+  for (int k = 0; k < N; ++k) w[k] = lane < PLAN_T / 32 ? s_warp[k][lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
 #pragma unroll
