@@ -711,6 +711,13 @@ PoolList pool_list(int n, const sv_page_data* p) {
   return l;
 }
 
+// Items of a row. A row has fewer than 2^31 positions, so at most 2^28 entries are in use,
+// however long it is.
+int segs_of(const sv_page_table& t) {
+  const int most = t.max_blocks_per_seq < (1 << 28) ? t.max_blocks_per_seq : 1 << 28;
+  return (most + SEG - 1) / SEG;
+}
+
 size_t row_set_bytes(const sv_page_table& t) { return ((size_t)t.table_rows + 31) / 32 * 4; }
 template <class F>
 cudaError_t allow_set(F kernel, size_t bytes) {  // beyond what a launch may ask for unasked
@@ -742,7 +749,7 @@ cudaError_t launch_pages_fork(const sv_page_table& t, int n, const int32_t* pare
   const size_t set = row_set_bytes(t);
   cudaError_t e = allow_set(fork_kernel, set);
   if (e != cudaSuccess) return e;
-  const int segs = (t.max_blocks_per_seq + SEG - 1) / SEG;
+  const int segs = segs_of(t);
   const int64_t items = (int64_t)((n + FORK_ROWS - 1) / FORK_ROWS) * segs;
   return launch_pdl(fork_kernel, dim3(grid_for(items, sms)), dim3(AT), set, s, a, segs);
 }
@@ -756,7 +763,7 @@ cudaError_t launch_pages_trim(const sv_page_table& t, int n, const int32_t* rows
   const size_t set = row_set_bytes(t);
   cudaError_t e = allow_set(trim_kernel, set);
   if (e != cudaSuccess) return e;
-  const int segs = (t.max_blocks_per_seq + SEG - 1) / SEG;
+  const int segs = segs_of(t);
   return launch_pdl(trim_kernel, dim3(grid_for((int64_t)n * segs, sms)), dim3(AT), set, s, a, segs);
 }
 
@@ -784,7 +791,7 @@ cudaError_t launch_pages_compact(const sv_page_table& t, int num_pools, const sv
   Pages a = make(t, ws);
   a.remap = remap;
   a.num_live = num_live;
-  const int segs = (t.max_blocks_per_seq + SEG - 1) / SEG;
+  const int segs = segs_of(t);
   const int64_t warps = (int64_t)t.table_rows * segs;
   const int table_ctas = (int)(warps > TABLE_CTAS * (PT / 32) ? TABLE_CTAS
                                                               : (warps + PT / 32 - 1) / (PT / 32));

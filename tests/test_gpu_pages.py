@@ -425,3 +425,33 @@ def test_a_table_of_very_many_rows():
     assert d.status() == 8
     assert d.compact() == m.compact()
     d.same()
+
+
+@pytest.mark.parametrize("op", ["fork", "extend", "trim", "compact"])
+def test_rows_of_very_many_entries(op):
+    """A table row may have any number of entries; a few of them are in use."""
+    bs = 8
+    m = Pages(64, 2, 9, bs)
+    for j in range(8):
+        m.table[0][j], m.ref[3 * j] = 3 * j, 1
+    m.lens[0] = 60
+    d = Device(m)
+    wide = (1 << 31) - 1
+    big = torch.empty(2 * wide, dtype=torch.int32, device=DEV).view(2, wide)
+    big[:, :9] = d.table
+    d.table = big
+    if op == "fork":
+        d.fork([0], [1], [50])
+        m.fork([0], [1], [50])
+    elif op == "extend":
+        d.extend([0, 1], [66, 20])
+        assert m.extend([0, 1], [66, 20])
+    elif op == "trim":
+        d.trim([0], [9])
+        m.trim([0], [9])
+    else:
+        d.compact()
+        m.compact()
+    assert d.status() == 0
+    d.table = big[:, :9].contiguous()
+    d.same(data=op == "compact")
