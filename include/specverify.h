@@ -240,7 +240,8 @@ SV_API sv_status spec_verify_attn_shared(const sv_attn_desc* desc, const void* q
  * may share a workspace, as calls of one entry point may. The rows
  * of a call are checked on the device before anything is changed; a call that fails a
  * check changes nothing and sets the workspace flag (sv_workspace_status:
- * SV_ERR_DEVICE_SHAPE). A row may stand in a call once only. An entry in use that names
+ * SV_ERR_DEVICE_SHAPE). A row may stand in a call once only. The arrays that a call changes
+ * must not overlap one another, its lists or its pools (SV_ERR_SHAPE). An entry in use that names
  * no page of the pool, or a free one, means that the state was damaged before the call:
  * it is reported by the call that meets it, and no memory outside the arrays is touched,
  * but the call's effect on that page's count is then unspecified (spec_pages_compact

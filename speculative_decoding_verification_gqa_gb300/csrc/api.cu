@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <initializer_list>
 
 #include "internal.cuh"
 
@@ -582,6 +583,37 @@ sv_status check_pages(const sv_page_table* t, int32_t n, const void* ws, size_t 
   return ws_bytes < pages_ws_bytes(t->num_blocks, t->table_rows) ? SV_ERR_WORKSPACE : SV_OK;
 }
 
+// Whether the arrays that a spec_pages_ call changes (the state, the workspace and `out`) and
+// the lists that it reads are apart. The kernels read a list more than once, so one that the
+// call itself changes would not be the one that was checked. Null arrays are none.
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+bool arrays_apart(const sv_page_table* t, const void* ws, std::initializer_list<Span> out,
+                  std::initializer_list<Span> lists, int num_pools = 0,
+                  const sv_page_data* pools = nullptr) {
+  Span a[12] = {{t->ref_count, 4 * (size_t)t->num_blocks},
+                {t->block_table, 4 * (size_t)t->table_rows * t->max_blocks_per_seq},
+                {t->cached_len, 4 * (size_t)t->table_rows},
+                {ws, pages_ws_bytes(t->num_blocks, t->table_rows)}};
+  int n = 4;
+  for (const Span& s : out) a[n++] = s;
+  const int changed = n;
+  for (const Span& s : lists) a[n++] = s;
+  auto meet = [](const Span& x, const Span& y) {
+    const uintptr_t b = (uintptr_t)x.at, c = (uintptr_t)y.at;
+    return x.at && y.at && b < c + y.bytes && c < b + x.bytes;
+  };
+  for (int i = 0; i < changed; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (meet(a[i], a[j])) return false;
+  for (int k = 0; k < num_pools; ++k)
+    for (int i = 0; i < n; ++i)
+      if (meet(a[i], {pools[k].base, (size_t)pools[k].page_bytes * t->num_blocks})) return false;
+  return true;
+}
+
 sv_status check_pools(const sv_page_table* t, int32_t num_pools, const sv_page_data* pools) {
   if (num_pools < 0 || num_pools > SV_MAX_PAGE_POOLS) return SV_ERR_SHAPE;
   if (num_pools > 0 && !pools) return SV_ERR_NULL;
@@ -611,6 +643,9 @@ SV_API sv_status spec_pages_fork(const sv_page_table* table, int32_t n, const in
   if (st != SV_OK || n == 0) return st;
   if (!parents || !children) return SV_ERR_NULL;
   if (!aligned(parents, 4) || !aligned(children, 4) || !aligned(fork_len, 4)) return SV_ERR_ALIGN;
+  const size_t list = 4 * (size_t)n;
+  if (!arrays_apart(table, workspace, {}, {{parents, list}, {children, list}, {fork_len, list}}))
+    return SV_ERR_SHAPE;
   const int sms = current_sms();
   if (sms <= 0) return SV_ERR_CUDA;
   return launch_pages_fork(*table, n, parents, children, fork_len, workspace, sms,
@@ -628,6 +663,9 @@ SV_API sv_status spec_pages_extend(const sv_page_table* table, int32_t n, const 
   if (st != SV_OK || n == 0) return st;
   if (!new_len) return SV_ERR_NULL;
   if (!aligned(rows, 4) || !aligned(new_len, 4)) return SV_ERR_ALIGN;
+  const size_t list = 4 * (size_t)n;
+  if (!arrays_apart(table, workspace, {}, {{rows, list}, {new_len, list}}, num_pools, pools))
+    return SV_ERR_SHAPE;
   const int sms = current_sms();
   if (sms <= 0) return SV_ERR_CUDA;
   return launch_pages_extend(*table, n, rows, new_len, num_pools, pools, workspace, sms,
@@ -643,6 +681,8 @@ SV_API sv_status spec_pages_trim(const sv_page_table* table, int32_t n, const in
   if (st != SV_OK || n == 0) return st;
   if (!new_len) return SV_ERR_NULL;
   if (!aligned(rows, 4) || !aligned(new_len, 4)) return SV_ERR_ALIGN;
+  const size_t list = 4 * (size_t)n;
+  if (!arrays_apart(table, workspace, {}, {{rows, list}, {new_len, list}})) return SV_ERR_SHAPE;
   const int sms = current_sms();
   if (sms <= 0) return SV_ERR_CUDA;
   return launch_pages_trim(*table, n, rows, new_len, workspace, sms, (cudaStream_t)stream) ==
@@ -658,6 +698,9 @@ SV_API sv_status spec_pages_compact(const sv_page_table* table, int32_t num_pool
   if (st == SV_OK) st = check_pools(table, num_pools, pools);
   if (st != SV_OK) return st;
   if (!aligned(remap, 4) || !aligned(num_live, 4)) return SV_ERR_ALIGN;
+  if (!arrays_apart(table, workspace, {{remap, 4 * (size_t)table->num_blocks}, {num_live, 4}}, {},
+                    num_pools, pools))
+    return SV_ERR_SHAPE;
   const int sms = current_sms();
   if (sms <= 0) return SV_ERR_CUDA;
   return launch_pages_compact(*table, num_pools, pools, remap, num_live, workspace, sms,

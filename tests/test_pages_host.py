@@ -85,6 +85,47 @@ def test_bad_pools_are_refused(lib, which, pools, status):
     assert call(lib, which, table(), pools=pools) == status
 
 
+SPREAD = dict(ref_count=1 << 30, block_table=2 << 30, cached_len=3 << 30)  # apart
+WS = 4 << 30
+
+
+@pytest.mark.parametrize("which", ALL)
+@pytest.mark.parametrize("a,b", [("ref_count", "block_table"), ("ref_count", "cached_len"),
+                                 ("block_table", "cached_len")])
+def test_state_arrays_that_overlap_are_refused(lib, which, a, b):
+    lists = (5 << 30, 6 << 30)
+    nbytes = dict(ref_count=64 * 4, block_table=4 * 8 * 4, cached_len=4 * 4)
+    for at in (SPREAD[b], SPREAD[b] + nbytes[b] // 16 * 16 - 16):
+        t = table(**{**SPREAD, a: at})
+        assert call(lib, which, t, lists=lists, pools=((7 << 30, 4096),), ws=WS) == 2
+    assert call(lib, which, table(**{**SPREAD, a: WS + 512}), lists=lists, ws=WS) == 2  # workspace
+
+
+@pytest.mark.parametrize("which", ["fork", "extend", "trim"])
+@pytest.mark.parametrize("name", [*SPREAD, "workspace"])
+@pytest.mark.parametrize("k", [0, 1])
+def test_lists_inside_what_the_call_changes_are_refused(lib, which, name, k):
+    """extend with new_len = cached_len itself, say."""
+    lists = [5 << 30, 6 << 30]
+    lists[k] = WS + 4 if name == "workspace" else SPREAD[name] + 4
+    assert call(lib, which, table(**SPREAD), lists=lists, pools=((7 << 30, 4096),), ws=WS) == 2
+
+
+@pytest.mark.parametrize("which", ["extend", "compact"])
+@pytest.mark.parametrize("name", [*SPREAD, "workspace"])
+def test_pools_over_the_state_are_refused(lib, which, name):
+    at = WS if name == "workspace" else SPREAD[name]
+    pools = ((7 << 30, 4096), (at - 63 * 4096, 4096))  # its last page
+    assert call(lib, which, table(**SPREAD), lists=(5 << 30, 6 << 30), pools=pools, ws=WS) == 2
+
+
+def test_outputs_of_compact_over_the_state_are_refused(lib):
+    t = table(**SPREAD)
+    for remap, live in ((SPREAD["ref_count"], None), (None, SPREAD["cached_len"] + 12),
+                        (5 << 30, (5 << 30) + 252), (WS - 4, None)):
+        assert lib.spec_pages_compact(ctypes.byref(t), 0, None, remap, live, WS, 1 << 20, None) == 2
+
+
 def test_null_pool_list_is_refused(lib):
     assert call(lib, "compact", table(), pools=(), num_pools=1) == 1
     assert call(lib, "compact", table(), num_pools=-1) == 2
