@@ -18,6 +18,7 @@ include/specverify.h:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -382,6 +383,18 @@ def _stream_on(stream, dev):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _allocating_on(stream, dev):
+    """Where a call allocates what it was not given: on the stream that it runs on, so that
+    the workspace's zeros come before the call there, and memory that is used again is used
+    in that stream's order."""
+    raw = _stream_on(stream, dev)
+    if raw == _raw_stream(dev):
+        return contextlib.nullcontext()
+    if raw == 0:
+        return torch.cuda.stream(torch.cuda.default_stream(dev))
+    return torch.cuda.stream(torch.cuda.ExternalStream(raw, device=dev))
+
+
 def shared_workspace_bytes(desc: AttnDesc, num_groups: int) -> int:
     n = load_library().spec_verify_attn_shared_workspace_size(ctypes.byref(desc), num_groups)
     if n == 0:
@@ -422,16 +435,19 @@ def spec_verify_attn_shared(q, k_pages, v_pages, block_table, seq_lens, draft_le
         scale = kv_scale.data_ptr()
     desc = AttnDesc(B, hq, hkv, d, max_draft_len, max_seq_len, rows, nb * bs,
                     SV_FP8_E4M3 if fp8 else SV_BF16, softmax_scale, 0)
-    if out is None:
-        out = torch.empty_like(q)
-    else:
+    if out is not None:
         devs.append(_dev(out, "out", (torch.bfloat16,)))
         if out.shape != q.shape:
             raise ValueError("out must have q's shape")
-    if workspace is None:
-        workspace = new_workspace(shared_workspace_bytes(desc, groups), q.device)
-    devs.append(_dev(workspace, "workspace", (torch.uint8,)))
+    if workspace is not None:
+        devs.append(_dev(workspace, "workspace", (torch.uint8,)))
     dev = _one_device(devs)
+    if out is None or workspace is None:
+        with _allocating_on(stream, dev):
+            if out is None:
+                out = torch.empty_like(q)
+            if workspace is None:
+                workspace = new_workspace(shared_workspace_bytes(desc, groups), q.device)
     st = (_lib or load_library()).spec_verify_attn_shared(
         ctypes.byref(desc), q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), nb, bs,
         block_table.data_ptr(), table[1], seq_lens.data_ptr(), draft_len.data_ptr(), groups,
@@ -485,7 +501,7 @@ def pages_workspace_bytes(num_blocks: int, table_rows: int) -> int:
     return n
 
 
-def _page_table(ref_count, block_table, cached_len, block_size, lists, pools, workspace):
+def _page_table(ref_count, block_table, cached_len, block_size, lists, pools, workspace, stream):
     """The checks that the page operators share: (the C descriptor, the workspace, the
     device's index)."""
     devs = [_dev(ref_count, "ref_count", _I32), _dev(block_table, "block_table", _I32),
@@ -506,11 +522,14 @@ def _page_table(ref_count, block_table, cached_len, block_size, lists, pools, wo
         devs.append(pools.device)
         if pools.pages != (blocks, block_size):
             raise ValueError("a pool must be [num_blocks, block_size, ...] of the state's pages")
+    if workspace is not None:
+        devs.append(_dev(workspace, "workspace", (torch.uint8,)))
+    dev = _one_device(devs)
     if workspace is None:
-        workspace = new_workspace(pages_workspace_bytes(blocks, rows), ref_count.device)
-    devs.append(_dev(workspace, "workspace", (torch.uint8,)))
+        with _allocating_on(stream, dev):
+            workspace = new_workspace(pages_workspace_bytes(blocks, rows), ref_count.device)
     return (PageTable(blocks, block_size, rows, table[1], ref_count.data_ptr(),
-                      block_table.data_ptr(), cached_len.data_ptr()), workspace, _one_device(devs))
+                      block_table.data_ptr(), cached_len.data_ptr()), workspace, dev)
 
 
 def _as_pools(pools) -> PagePools:
@@ -525,7 +544,7 @@ def spec_pages_fork(ref_count, block_table, cached_len, parents, children, *, bl
     block_table int32 [rows, max_blocks], cached_len int32 [rows]."""
     t, ws, dev = _page_table(ref_count, block_table, cached_len, block_size,
                              (("parents", parents), ("children", children), ("fork_len", fork_len)),
-                             None, workspace)
+                             None, workspace, stream)
     st = (_lib or load_library()).spec_pages_fork(
         ctypes.byref(t), parents.numel(), parents.data_ptr(), children.data_ptr(),
         None if fork_len is None else fork_len.data_ptr(), ws.data_ptr(), ws.numel(),
@@ -543,7 +562,7 @@ def spec_pages_extend(ref_count, block_table, cached_len, rows, new_len, *, bloc
     changes and ``workspace_status`` returns 9 (SV_ERR_NO_PAGES)."""
     pools = _as_pools(pools)
     t, ws, dev = _page_table(ref_count, block_table, cached_len, block_size,
-                             (("new_len", new_len), ("rows", rows)), pools, workspace)
+                             (("new_len", new_len), ("rows", rows)), pools, workspace, stream)
     st = (_lib or load_library()).spec_pages_extend(
         ctypes.byref(t), new_len.numel(), None if rows is None else rows.data_ptr(),
         new_len.data_ptr(), len(pools.tensors), pools.array, ws.data_ptr(), ws.numel(),
@@ -557,7 +576,7 @@ def spec_pages_trim(ref_count, block_table, cached_len, rows, new_len, *, block_
     """Give back the positions of row r = rows[i] from new_len[i] on (``rows`` None: rows
     0 .. n - 1): the pages past them lose a count, and their entries become -1."""
     t, ws, dev = _page_table(ref_count, block_table, cached_len, block_size,
-                             (("new_len", new_len), ("rows", rows)), None, workspace)
+                             (("new_len", new_len), ("rows", rows)), None, workspace, stream)
     st = (_lib or load_library()).spec_pages_trim(
         ctypes.byref(t), new_len.numel(), None if rows is None else rows.data_ptr(),
         new_len.data_ptr(), ws.data_ptr(), ws.numel(), _stream_on(stream, dev))
@@ -571,7 +590,8 @@ def spec_pages_compact(ref_count, block_table, cached_len, *, block_size: int, p
     every row's entries follow. Fills ``remap`` (int32 [num_blocks]: the new page of each
     page, -1 if it was free) and ``num_live`` (int32 [1]: L) when they are given."""
     pools = _as_pools(pools)
-    t, ws, dev = _page_table(ref_count, block_table, cached_len, block_size, (), pools, workspace)
+    t, ws, dev = _page_table(ref_count, block_table, cached_len, block_size, (), pools, workspace,
+                             stream)
     out = [None, None]
     for i, (o, name, n) in enumerate(((remap, "remap", t.num_blocks), (num_live, "num_live", 1))):
         if o is not None:

@@ -455,3 +455,25 @@ def test_rows_of_very_many_entries(op):
     assert d.status() == 0
     d.table = big[:, :9].contiguous()
     d.same(data=op == "compact")
+
+
+@pytest.mark.parametrize("as_number", [False, True])
+def test_workspace_is_made_on_the_stream_of_the_call(as_number):
+    """A call on a stream passed by argument, without a workspace, while the current stream is
+    busy: its zeros come before it, although the memory held other bits before."""
+    m = filled(2, 64, 16, [100, 0], max_blocks=9)
+    d = Device(m)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):  # what the allocator will hand out again
+        junk = torch.full((sv.pages_workspace_bytes(64, 2),), 255, dtype=torch.uint8, device=DEV)
+    ps, ch = d.i32([0]), d.i32([1])
+    del junk
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    sv.spec_pages_fork(d.ref, d.table, d.lens, ps, ch, block_size=16,
+                       stream=s.cuda_stream if as_number else s)
+    s.synchronize()
+    assert not torch.cuda.current_stream().query()  # that is still asleep
+    torch.cuda.synchronize()
+    m.fork([0], [1])
+    d.same()

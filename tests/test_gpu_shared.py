@@ -432,3 +432,23 @@ def test_binding_refuses():
     bad(ValueError, 0, q, out=torch.empty_like(q)[:2])
     bad(ValueError, 0, q, kv_scale=torch.ones(2, 3, device="cuda"))
     bad(sv.SpecVerifyError, 0, q, workspace=sv.new_workspace(1024))
+
+
+def test_memory_of_a_call_is_made_on_its_stream(kernel):
+    """A call on a stream passed by argument, without out and workspace, while the current
+    stream is busy."""
+    w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=41)
+    pg = pages(x, gb, P, 16, seed=41)
+    alone = run(x, pg, gb, P)
+    i32 = lambda a: torch.from_numpy(np.asarray(a, dtype=np.int32)).cuda()  # noqa: E731
+    q, k, v, bt, T, D, _ = to_device(x, pg)
+    g_, p_, s = i32(gb), i32(P), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    out = sv.spec_verify_attn_shared(q, k, v, bt, T, D, g_, p_, stream=s,
+                                     max_draft_len=int(x["draft_len"].max()),
+                                     max_seq_len=int(x["seq_lens"].max()))
+    s.synchronize()
+    assert not torch.cuda.current_stream().query()  # that is still asleep
+    torch.cuda.synchronize()
+    assert np.array_equal(out.view(torch.int16).cpu().numpy().view(np.uint16), alone)
