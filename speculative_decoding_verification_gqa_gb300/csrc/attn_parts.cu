@@ -593,9 +593,44 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, 1)
       const int last = RT == 2 ? s.d.nkeys - 1
                                : s.d.last0 + (s.d.mt * MT + (live ? row : 0)) / p.G;
 
+      // V rows of step h of tile j that are no keys of the part
+      auto clear_v = [&](int j, int h) -> bool {
+        const int key0 = j * KT + h * HK;
+        const int first = RT == 1 ? max(s.d.start - key0, 0) : 0, end = min(s.d.nkeys - key0, HK);
+        if (!F8 && r == 0 && (first > 0 || end < HK)) {
+          // V rows before and past the part's keys may hold any bits: zeros, so that P = 0
+          // never meets non-finite data
+          const uint32_t st = it % L::NS;
+          if (!wwait(&bars->v_full[st], (it / L::NS) & 1)) return false;
+          uint8_t* vt = smem + L::V + st * L::RAW + h * HK * 128;
+          for (int q = rr; q < HK * 8 * (HD / 64); q += 128) {  // 16-byte chunks
+            const int key = (q / 8) % HK;
+            if (key < first || key >= end)
+              *reinterpret_cast<uint4*>(vt + q / (8 * HK) * L::BLK + key * 128 + (q % 8) * 16) =
+                  make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+        }
+        return true;
+      };
+
       float m_ref = -INFINITY, lh = 0.f;
       bool good = true;
-      for (int j = s.j0; good && j < s.j1; ++j, ++it) {
+      // A warp without a live row keeps the steps' order only: its rows of P are whatever they
+      // were, and so its rows of O, which nobody reads. (A call of 128 sequences of 64 rows a
+      // KV head 263 us instead of 266, one of 2 sequences 14.1 instead of 14.4. The same as a
+      // condition inside the step's code cost 5%: it spilled.)
+      int j = s.j0;
+      if (RT == 1 && (cta_warp & 3) * 32 >= s.d.rows) {
+        for (; good && j < s.j1; ++j, ++it, ++n) {
+          good = wwait(&bars->s_full[r], n & 1);
+          mbar_arrive(&bars->s_free[r]);
+          if (good && n >= 1) good = wwait(&bars->o_done[r], (n - 1) & 1);
+          if (good) good = clear_v(j, 0);
+          if (good) mbar_arrive(&bars->p_full[r]);
+        }
+      }
+      for (; good && j < s.j1; ++j, ++it) {
         const int steps = steps_of<RT>(s, j);
         for (int h = 0; h < steps; ++h, ++n) {
           if (!(good = wwait(&bars->s_full[r], n & 1))) break;
@@ -678,21 +713,7 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, 1)
           }
           tmem_st32(tq + COL_P + r * 32, pk);
           tmem_wait_st();
-          const int first = RT == 1 ? max(s.d.start - key0, 0) : 0, end = min(s.d.nkeys - key0, HK);
-          if (!F8 && r == 0 && (first > 0 || end < HK)) {
-            // V rows before and past the part's keys may hold any bits: zeros, so that P = 0
-            // never meets non-finite data
-            const uint32_t st = it % L::NS;
-            if (!(good = wwait(&bars->v_full[st], (it / L::NS) & 1))) break;
-            uint8_t* vt = smem + L::V + st * L::RAW + h * HK * 128;
-            for (int q = rr; q < HK * 8 * (HD / 64); q += 128) {  // 16-byte chunks
-              const int key = (q / 8) % HK;
-              if (key < first || key >= end)
-                *reinterpret_cast<uint4*>(vt + q / (8 * HK) * L::BLK + key * 128 + (q % 8) * 16) =
-                    make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async();
-          }
+          if (!(good = clear_v(j, h))) break;
           fence_before();
           mbar_arrive(&bars->p_full[r]);
         }
