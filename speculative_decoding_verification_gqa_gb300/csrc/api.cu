@@ -23,9 +23,13 @@ namespace {
 constexpr int SWITCH_TILES_TC_FP8 = SV_SWITCH_F8;
 constexpr int SWITCH_TILES_TC_BF16 = SV_SWITCH_BF16;
 constexpr int SWITCH_TILES_MMA = 2;
-constexpr int SWITCH_TILES_PREFIX = 3;    // 128-key tiles of 256 rows
-constexpr int SWITCH_TILES_SEQUENCE = 4;  // 64-key tiles of 128 rows
-// SM time of a 64-key tile of 128 rows (two at a time on an SM), in 128-key tiles of 256 rows.
+// Shared prefixes. A unit's start in 128-key tiles of 256 rows and in 64-key tiles of 128 rows,
+// and the SM time of the latter (two at a time on an SM) in the former. Measured around them
+// (calls back to back; 64 sequences over a prefix of 8192, 128 over four of 16385, bf16; 32
+// over two of 32768, E4M3): 68.8, 254, 369 us; a sequence's start of 4: 69.6, 261, 372; costs
+// of 0.31 and 0.50: 68.9, 257, 371; a prefix's start of 2: 69.3, 254, 368.
+constexpr int SWITCH_TILES_PREFIX = 3;
+constexpr int SWITCH_TILES_SEQUENCE = 3;
 constexpr float SEQUENCE_COST_BF16 = 0.28f;
 constexpr float SEQUENCE_COST_FP8 = 0.45f;
 // Per-tile compute floor of each kernel, in CTAs streaming at once (a 128-key tile's

@@ -168,7 +168,9 @@ __device__ __forceinline__ void verdict(const Pages& a, bool ok) {
 
 // Checks: children distinct, empty and not parents; lengths within the parents'. An item:
 // FORK_ROWS consecutive children, SEG entries. A run of children of one parent reads each
-// entry once and adds the run's length to its page's count at once.
+// entry once and adds the run's length to its page's count at once. (992 children of up to
+// 2048 entries: 16.5 us captured; 17.2 with a row at a time in the checks. 6 children of 63
+// entries: 6.3.)
 __global__ void __launch_bounds__(AT) fork_kernel(const Pages a, int segs) {
   pdl_trigger();
   pdl_wait();
@@ -251,7 +253,9 @@ __global__ void __launch_bounds__(AT) fork_kernel(const Pages a, int segs) {
 // ---------------------------------------------------------------------------- trim
 
 // Checks: rows distinct, 0 <= new <= old. An item: a row, SEG entries. A page that several
-// rows of the call drop loses a count for each.
+// rows of the call drop loses a count for each. Bound by those atomics, 20 to 26 a ns at L2,
+// and the reads before them: 1024 rows that drop 0.5 million entries 19.3 us captured, 64 rows
+// that drop one or none 5.4.
 __global__ void __launch_bounds__(AT) trim_kernel(const Pages a, int segs) {
   pdl_trigger();
   pdl_wait();
@@ -336,6 +340,8 @@ __device__ __forceinline__ int chunk_of(const Pages& a, int k) {
 // the chunk of each row's first page (row_e) and compares the free pages with the need.
 // Up to PT rows what a row needs stays in its thread, and the holders of a page are counted
 // in a table in shared memory; beyond, by page in blk_b and blk_c.
+// (256 rows, of which 224 part from shared pages, 8 pools: 14.5 us captured with extend_apply,
+// of which this is the longer half; 8 rows 10.6.)
 constexpr int SLOTS = 2 * PT;
 __global__ void __launch_bounds__(PT) extend_plan(const Pages a) {
   __shared__ int s_page[SLOTS], s_cnt[SLOTS], s_last[SLOTS];
@@ -628,7 +634,8 @@ __global__ void __launch_bounds__(PT) compact_plan(const Pages a, int table_ctas
 }
 
 // Grid-stride over: the page data (move x pool x COPY_BYTES), the table entries, and the
-// counts of the pages that move.
+// counts of the pages that move. Memory-bound: 343 MB in 60 us (5.7 TB/s) when 2.9 thousand
+// pages of 2 pools, 32 KB each, move.
 __global__ void __launch_bounds__(AT) compact_apply(const Pages a, int segs,
                                                     const __grid_constant__ PoolList pl) {
   pdl_trigger();
