@@ -199,7 +199,8 @@ SV_API size_t spec_verify_attn_shared_workspace_size(const sv_attn_desc* desc,
  * are read through each sequence's own row, and what a block of another sequence than the
  * first holds before them is not used.
  *
- * Same bits for the same arguments every time. Worth its joining of two results per row
+ * Same bits for the same arguments every time (small calls run the
+ * mma.sync kernel, by a rule on the descriptor alone). Worth its joining of two results per row
  * when a group has several sequences and its prefix is long beside what follows.
  *
  *   group_begin  int32 [num_groups + 1], from 0 to batch, not decreasing (a group may be

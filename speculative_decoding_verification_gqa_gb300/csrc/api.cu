@@ -393,6 +393,22 @@ namespace {
 // the partials' slots are indexed with 32 bits.
 constexpr int64_t MAX_SHARED_UNITS = 1 << 22;
 
+// Small calls take the mma.sync kernel: three launches instead of four, no TMEM, no tensor
+// maps. The rule goes by what the host knows, the sequences' units and the longest sequence.
+// Calls back to back from Python, mma.sync against tcgen05, d 128, bf16 (E4M3):
+//     8 units of 512, 960 positions       18.9, 20.7 us against 20.3, 19.7 (18.1, 21.1: 22.8, 23.0)
+//    16 units of 80, 320, 1088            15.4, 16.2, 21.2 against 19.9, 20.2, 22.4
+//    64 units of 80, 320, 960             18.9, 22.5, 27.6 against 21.2, 22.9, 23.6
+//   128 units of 80, 320                  18.8, 26.4 against 20.9, 21.8 (19.1, 27.4: 26.1, 26.3)
+constexpr int64_t SMALL_WORK = 20480;  // units x positions
+constexpr int SMALL_SEQ = 1024;
+int pick_shared(const sv_attn_desc* d) {
+  const int64_t rows = (int64_t)(d->num_q_heads / d->num_kv_heads) * (1 + d->max_draft_len);
+  const int64_t units = d->num_kv_heads * (int64_t)d->batch * ((rows + MT - 1) / MT);
+  const bool small = d->max_seq_len <= SMALL_SEQ && units * d->max_seq_len <= SMALL_WORK;
+  return g_attn_kernel == 0 && small ? 1 : pick_kernel(d);
+}
+
 sv_status check_shared(const sv_attn_desc* desc, int32_t num_groups) {
   const sv_status st = check_desc(desc);
   if (st != SV_OK) return st;
@@ -447,7 +463,7 @@ SV_API sv_status spec_verify_attn_shared(const sv_attn_desc* desc, const void* q
                                  shared_ws_layout(desc, num_groups, sms, false).total))
     return SV_ERR_WORKSPACE;
 
-  const int which = pick_kernel(desc);
+  const int which = pick_shared(desc);
   const bool lines = which == 2;
   const SharedWs lay = shared_ws_layout(desc, num_groups, sms, lines);
   const PagedArgs pg = {block_table, max_blocks_per_seq, block_size, num_blocks};

@@ -236,17 +236,18 @@ def test_positions_past_32_bits_of_bytes(kernel):
     assert_within(out.view(torch.int16).cpu().numpy().view(np.uint16), w, x)
 
 
-@pytest.mark.parametrize("after", [0, 1, 2, 3])  # plan, sequences, prefixes, join
-def test_failed_launch_is_reported_and_the_workspace_serves_on(after):
+# plan, sequences, prefixes, join; or, for a small call, plan, attention, join
+@pytest.mark.parametrize("after,max_seq", [(0, 2000), (1, 2000), (2, 2000), (3, 2000), (0, 1000), (1, 1000), (2, 1000)])
+def test_failed_launch_is_reported_and_the_workspace_serves_on(after, max_seq):
     ensure_built()
     w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, seed=20)
     pg = pages(x, gb, P, 16, seed=4)
     ws = sv.new_workspace(1 << 27)
     sv.api.inject_launch_failure(after)
     with pytest.raises(sv.SpecVerifyError) as e:
-        run(x, pg, gb, P, workspace=ws)
+        run(x, pg, gb, P, workspace=ws, max_seq=max_seq)
     assert e.value.status == 6
-    assert_within(run(x, pg, gb, P, workspace=ws), w, x)
+    assert_within(run(x, pg, gb, P, workspace=ws, max_seq=max_seq), w, x)
     assert sv.workspace_status(ws) == 0
 
 
@@ -257,10 +258,10 @@ def test_bounded_wait_runs_out_and_the_call_returns(kv):
     pg = pages(x, gb, P, 16, seed=4)
     ws = sv.new_workspace(1 << 27)
     sv.api.inject_wait_timeout(100000)
-    run(x, pg, gb, P, workspace=ws)
+    run(x, pg, gb, P, workspace=ws, max_seq=2000)
     assert sv.workspace_status(ws, clear=True) == 7
     assert sv.api.inject_wait_timeout(0) == 0  # taken by that call
-    assert_within(run(x, pg, gb, P, workspace=ws), w, x)
+    assert_within(run(x, pg, gb, P, workspace=ws, max_seq=2000), w, x)
     assert sv.workspace_status(ws) == 0
 
 
@@ -452,3 +453,22 @@ def test_memory_of_a_call_is_made_on_its_stream(kernel):
     assert not torch.cuda.current_stream().query()  # that is still asleep
     torch.cuda.synchronize()
     assert np.array_equal(out.view(torch.int16).cpu().numpy().view(np.uint16), alone)
+
+
+@pytest.mark.parametrize("B,Hkv,max_seq,small", [
+    (2, 2, 1024, True), (2, 2, 1025, False), (20, 2, 512, True), (20, 2, 513, False)])
+def test_small_calls_take_the_mma_kernel(B, Hkv, max_seq, small):
+    """The automatic choice is by the descriptor: 1024 positions, and 20480 times units."""
+    ensure_built()
+    w, x, gb, P = inputs([(200, [(201 + 15 * b, b % 4) for b in range(B)])], Hq=4 * Hkv, Hkv=Hkv, d=128,
+                         seed=B)
+    pg = pages(x, gb, P, 16, seed=B)
+    got = run(x, pg, gb, P, max_seq=max_seq)
+    assert_within(got, w, x)
+    lib = sv.api.load_library()
+    same = []
+    for k in (1, 2):
+        prev = lib.sv_set_attn_kernel(k)
+        same.append(np.array_equal(run(x, pg, gb, P, max_seq=max_seq), got))
+        lib.sv_set_attn_kernel(prev)
+    assert same == [small, not small]
