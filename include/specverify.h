@@ -199,6 +199,10 @@ SV_API size_t spec_verify_attn_shared_workspace_size(const sv_attn_desc* desc,
  * are read through each sequence's own row, and what a block of another sequence than the
  * first holds before them is not used.
  *
+ * What the pages hold past a sequence's window, or before its prefix in a block of its own,
+ * may be anything, NaN too. A non-finite V at a position of the window reaches all rows of
+ * that sequence, also those that come before it, as in spec_verify_attn.
+ *
  * Same bits for the same arguments every time (small calls run the
  * mma.sync kernel, by a rule on the descriptor alone). Worth its joining of two results per row
  * when a group has several sequences and its prefix is long beside what follows.
