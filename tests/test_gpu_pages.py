@@ -301,6 +301,41 @@ def test_free_page_named_by_a_row():
     assert d.status() == 8 and min(d.ref.tolist()) == 0
 
 
+@pytest.mark.parametrize("count", [0, 1, 2])
+def test_rows_that_drop_a_page_more_often_than_it_is_counted(count):
+    """Three rows of a call name one page: the count ends at 0, and the call says so."""
+    m = filled(4, 20, 8, [20, 9, 5, 8], seed=6)
+    d = Device(m)
+    p = m.table[0][0]
+    for r in (1, 2):
+        d.ref[m.table[r][0]] = 0
+        d.table[r, 0] = p
+    d.ref[p] = count
+    d.trim([0, 1, 2, 3], [0, 0, 0, 0])
+    assert d.status() == 8
+    assert d.ref.tolist() == [0] * 20
+    assert d.lens.tolist() == [0] * 4 and bool((d.table == -1).all())
+
+
+@pytest.mark.parametrize("n", [7, 8, 9, 40])
+def test_rows_that_share_parts_of_their_pages_are_trimmed(n):
+    """Runs of rows that share some pages and not others, in call orders that keep and break
+    the runs, trimmed to different lengths."""
+    rng = random.Random(n)
+    m = Pages(400, 64, 40, 8)
+    assert m.extend([0, 1], [300, 130])
+    m.fork([rng.choice([0, 0, 1]) for _ in range(n)], list(range(2, 2 + n)),
+           [rng.randint(60, 130) for _ in range(n)])
+    assert m.extend(list(range(2, 2 + n)), [m.lens[r] + rng.randint(0, 12) for r in range(2, 2 + n)])
+    d = Device(m)
+    for rows in (list(range(2 + n)), rng.sample(range(2 + n), n)):
+        to = [rng.randint(0, m.lens[r]) for r in rows]
+        d.trim(rows, to)
+        m.trim(rows, to)
+        assert d.status() == 0
+        d.same(data=False)
+
+
 def test_graph_replays_a_step_on_its_own_stream():
     """fork, extend, trim and compact in one captured graph, replayed: the state at the start
     of every replay is put back, and the results are those of eager calls."""
