@@ -472,3 +472,44 @@ def test_small_calls_take_the_mma_kernel(B, Hkv, max_seq, small):
         same.append(np.array_equal(run(x, pg, gb, P, max_seq=max_seq), got))
         lib.sv_set_attn_kernel(prev)
     assert same == [small, not small]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+def test_longest_windows(kernel, kv):
+    """255 drafts, many row tiles a sequence, beside windows of one row."""
+    w, x, gb, P = inputs([(70, [(100, 255), (70, 0), (333, 254)]), (0, [(0, 255)])], Hq=8, Hkv=2, d=128,
+                         kv=kv, seed=50)
+    assert_within(run(x, pages(x, gb, P, 32, seed=1), gb, P), w, x)
+
+
+def test_largest_pages(kernel):
+    w, x, gb, P = inputs([(300, [(300, 3), (640, 1)]), (90, [(95, 2)])], Hq=8, Hkv=2, d=128, seed=51)
+    assert_within(run(x, pages(x, gb, P, 65536, seed=1), gb, P), w, x)
+
+
+def test_graphs_that_share_a_workspace(kernel):
+    """Two captured calls of different shapes on one workspace, replayed in turn."""
+    cases = []
+    ws = sv.new_workspace(1 << 27)
+    for seed, groups, Hkv in ((60, TWO, 2), (61, [(500, [(510 + 9 * b, b % 4) for b in range(12)])], 1)):
+        w, x, gb, P = inputs(groups, Hq=8, Hkv=Hkv, d=128, seed=seed)
+        pg = pages(x, gb, P, 16, seed=seed)
+        alone = run(x, pg, gb, P)
+        q, k, v, bt, T, D, _ = to_device(x, pg)
+        i32 = lambda a: torch.from_numpy(np.asarray(a, dtype=np.int32)).cuda()  # noqa: E731
+        args = (q, k, v, bt, T, D, i32(gb), i32(P))
+        kw = dict(max_draft_len=int(x["draft_len"].max()), max_seq_len=int(x["seq_lens"].max()),
+                  out=torch.empty_like(q), workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            sv.spec_verify_attn_shared(*args, **kw)
+        cases.append((graph, kw["out"], alone, args))
+    for _ in range(5):
+        for graph, out, _, _ in cases:
+            out.zero_()
+            graph.replay()
+    torch.cuda.synchronize()
+    for _, out, alone, _ in cases:
+        assert np.array_equal(out.view(torch.int16).cpu().numpy().view(np.uint16), alone)
+    assert sv.workspace_status(ws) == 0
