@@ -156,6 +156,10 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_mma_kernel(const AttnParams 
     const int l1 = (int)(min(t_end, ub + nt) - ub);
     if (l1 <= l0) break;  // cannot happen for a valid plan
     t = ub + l1;
+    if (SHARED && tid == 0) {  // for the join: who holds the unit's first tile, who its last
+      if (l0 == 0) p.unit_ctas[u].x = blockIdx.x;
+      if (l1 == nt) p.unit_ctas[u].y = blockIdx.x;
+    }
     const SharedSeq part = SHARED ? p.parts[b] : SharedSeq{};
     const int T = SHARED ? part.last0 : p.seq_lens[b];
     const int D = SHARED ? part.rows - 1 : p.draft_len[b];

@@ -372,6 +372,11 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, 1)
       uint32_t it = 0, n[RT] = {}, units[RT] = {};
       bool ok = true;
       while (ok && seg_next(p, num_units, walk, s)) {
+        if (lane == 0) {  // for the join: who holds the unit's first tile, who its last
+          if (s.j0 == 0) p.unit_ctas[s.u].x = worker;
+          if (s.j1 == s.d.nt) p.unit_ctas[s.u].y = worker;
+        }
+        __syncwarp();
         const int nr = tiles_of<RT>(s);
         for (int j = s.j0; ok && j < s.j1; ++j, ++it) {
           const uint32_t st = it % L::NS;

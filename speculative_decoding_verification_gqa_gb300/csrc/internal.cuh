@@ -175,7 +175,7 @@ struct AttnParams {
   RowInfo* rows;              // [window rows]
   SharedUnit* sunits;         // [U] (tcgen05 kernels)
   int32_t* tile_unit;         // [row tiles of the prefixes] first of the Hkv units of each
-  int2* unit_ctas;            // [U] first and last CTA that a unit's tiles fall to
+  int2* unit_ctas;            // [U] first and last CTA of a unit, as they note it
   int row_log2;               // log2 of the query rows of a prefix's unit
   int kt;                     // keys per tile of the line
   float tile_cost;            // the sequences' line: SM time of its tiles in the prefixes' tiles

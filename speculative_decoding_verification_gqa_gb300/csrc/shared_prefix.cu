@@ -104,7 +104,6 @@ __device__ __forceinline__ void put_unit(const AttnParams& p, bool both, int u, 
 constexpr int CACHED = 1024;        // sequences, and groups, kept in shared memory
 constexpr int CACHED_UNITS = 1024;  // unit starts kept in shared memory
 constexpr int MIN_PART = 4;         // tiles that are worth a CTA of the prefixes
-constexpr int CACHED_CTAS = 1024;   // CTA starts (a launch has two per SM at most)
 
 struct PlanShared {
   int32_t gb[CACHED + 1], len[CACHED];                      // groups
@@ -112,24 +111,23 @@ struct PlanShared {
   uint16_t n[CACHED];
   uint8_t D[CACHED];
   int32_t ubeg[CACHED_UNITS + 1];
-  union {  // first the one, then the other
-    int4 entry[PLAN_T];
-    int32_t cta[CACHED_CTAS + 1];
-  };
-  unsigned long long prefix_units, prefix_tiles;
+  int4 entry[PLAN_T];
+  uint32_t prefix_units, prefix_tiles;  // (of a valid call)
   int maxmt;
 };
 
-// CTA `line` of 2 (or the one CTA of a single line) checks the call, describes its parts and
-// writes its line: line 0 the prefixes (pa), line 1 the sequences (pb). Both CTAs make the
-// same checks, so a call is skipped as a whole. All of it is latency, a chain of dependent
+// Three CTAs check the call and describe its parts; the first writes the prefixes' line (pa),
+// the second the sequences' (pb), the third the window rows. (A single line: one CTA for all.)
+// All make the same checks, so a call is skipped as a whole. All of it is latency, a chain of dependent
 // steps, hence the tables in shared memory and arithmetic in 32 bits where it suffices.
 __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, AttnParams pb) {
   const bool both = gridDim.x == 1;  // one line for all parts
   const bool prefixes = both || blockIdx.x == 0, sequences = both || blockIdx.x == 1;
+  const bool window_rows = both || blockIdx.x == 2;
   const AttnParams& p = prefixes && !both ? pa : pb;
   const int tid = threadIdx.x, NG = p.num_groups, B = p.B, G = p.G;
   const int seq_box = min(p.block_size, pb.kt), row_log2 = p.row_log2;
+  const int prefix_log2 = __ffs(pa.kt) - 1, seq_log2 = __ffs(pb.kt) - 1;
   __shared__ PlanShared sm;
   pdl_trigger();
   pdl_wait();
@@ -172,7 +170,7 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
     s.alone = P == 0;
     s.group = n;
     s.nmt = (G * s.rows + MT - 1) / MT;
-    s.nt = (s.nkeys - (P & ~(seq_box - 1)) + pb.kt - 1) / pb.kt;
+    s.nt = (s.nkeys - (P & ~(seq_box - 1)) + pb.kt - 1) >> seq_log2;
     return s;
   };
   int64_t q_total = 0, U = 0, TT = 0;
@@ -206,7 +204,8 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
       } else {
         p.row_begin[b] = (int32_t)s.q_off;
       }
-      if (sequences && (both || B > CACHED)) seq[b] = s;
+      // (of two CTAs that write and read a long batch here, both write the same)
+      if (both || (B > CACHED && !prefixes)) seq[b] = s;
     }
     q_total += tot[0] >> 32;
     U += (uint32_t)tot[0];
@@ -239,7 +238,7 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
     s.table_row = g0;
     s.group = n;
     s.nmt = (G * s.rows + (1 << row_log2) - 1) >> row_log2;
-    s.nt = (P + pa.kt - 1) / pa.kt;
+    s.nt = (P + pa.kt - 1) >> prefix_log2;
     s.mbase = tile_base(q0, G, row_log2, n);
     return s;
   };
@@ -248,27 +247,28 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
       const int b = B <= CACHED ? last_at_most(B, u, [&](int i) { return sm.ub[i]; })
                                 : last_at_most(B, u, [&](int i) { return seq[i].ubase; });
       const SharedSeq s = seq_at(b);
-      const int k = u - s.ubase, g = k / s.nmt, tile = s.tbase + k * s.nt;
+      const int k = u - s.ubase, g = s.nmt == 1 ? k : k / s.nmt, tile = s.tbase + k * s.nt;
       put_unit(p, both, u, NG + b, s, g, k - g * s.nmt, s.start & ~(seq_box - 1), tile);
       if (u < CACHED_UNITS) sm.ubeg[u] = tile;
     }
-    // every window row, a warp per sequence
-    for (int b = tid >> 5; b < B; b += PLAN_T / 32) {
+  }
+  if (!bad && window_rows) {
+    for (int w = tid; w < (int)q_total; w += PLAN_T) {
+      const int b = last_at_most(B, w, first_row);
       const SharedSeq s = seq_at(b);
       const int q0 = first_row(group_at(s.group));  // the group's first row
-      const int mbase = s.alone ? -1 : tile_base(q0, G, row_log2, s.group);
-      for (int i = tid & 31; i < s.rows; i += 32) {
-        int4* dst = reinterpret_cast<int4*>(p.rows + s.q_off + i);
-        dst[0] = make_int4(i, s.ubase, s.nmt, mbase);
-        dst[1] = make_int4((int)s.q_off - q0 + i, 0, 0, 0);
-      }
+      int4* dst = reinterpret_cast<int4*>(p.rows + w);
+      dst[0] = make_int4(w - (int)s.q_off, s.ubase, s.nmt,
+                         s.alone ? -1 : tile_base(q0, G, row_log2, s.group));
+      dst[1] = make_int4(w - q0, 0, 0, 0);
     }
   }
+  if (!both && window_rows) return;
   for (int n = tid; n < NG && !bad; n += PLAN_T) {
     const SharedSeq s = prefix_part(n);
     atomicMax(&sm.maxmt, s.nmt);
-    atomicAdd(&sm.prefix_units, (unsigned long long)p.Hkv * s.nmt);
-    atomicAdd(&sm.prefix_tiles, (unsigned long long)p.Hkv * s.nmt * s.nt);
+    atomicAdd(&sm.prefix_units, (uint32_t)(p.Hkv * s.nmt));
+    atomicAdd(&sm.prefix_tiles, (uint32_t)(p.Hkv * s.nmt) * s.nt);
     if (both) p.parts[n] = s;
   }
   __syncthreads();
@@ -339,12 +339,12 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
   const int32_t* ubeg = U <= CACHED_UNITS ? sm.ubeg : p.ubeg;
   const int X = p.switch_tiles;
   const int64_t VT = TT + U * X;
-  int C1 = (int)min((int64_t)min(p.n_ctas, CACHED_CTAS), max(VT, (int64_t)1)), C2 = 0;
+  int C1 = (int)min((int64_t)p.n_ctas, max(VT, (int64_t)1)), C2 = 0;
   int64_t V1 = VT;  // C1 CTAs take equal parts of [0, V1), C2 after them of [V1, VT)
   if (!both) {
     const int sms = pa.n_ctas;  // one CTA of prefixes per SM
-    const int64_t VP = sm.prefix_tiles + sm.prefix_units * pa.switch_tiles;
-    const float ws = (float)(TT_seq + U_seq * pb.switch_tiles) * pb.tile_cost;
+    const uint32_t VP = sm.prefix_tiles + sm.prefix_units * pa.switch_tiles;
+    const float ws = (float)(uint32_t)(TT_seq + U_seq * pb.switch_tiles) * pb.tile_cost;
     const float T = fmaxf(((float)VP + ws) / sms, (float)MIN_PART);
     const int half_n = ((int)ceilf(ws / T) + 1) / 2;  // pairs of SMs
     const int N = VP > 0 ? min(max(2 * half_n, 2), max(sms - 2, 1)) : sms;
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
       C1 = min(C1, 2 * N);
     } else {
       C1 = (int)min((int64_t)max(sms - N, 1), max(VT, (int64_t)1));
-      const int64_t early = (int64_t)(C1 * T);
+      const int64_t early = (uint32_t)(C1 * T);
       if (VT - early >= N * MIN_PART) {
         V1 = early;
         C2 = N;
@@ -376,13 +376,6 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
       e = make_int2((int32_t)(ubeg[u] + (into > 0 ? into : 0)), u);
     }
     p.cta_tab[c] = e;
-    if (c <= C) sm.cta[c] = e.x;
-  }
-  __syncthreads();
-  // A unit's CTAs: the one whose range holds a tile is the last that starts at or before it.
-  for (int u = tid; u < (int)U; u += PLAN_T) {
-    auto holder = [&](int t) { return last_at_most(C, t, [&](int i) { return sm.cta[i]; }); };
-    p.unit_ctas[u] = make_int2(holder(ubeg[u]), holder(ubeg[u + 1] - 1));
   }
 }
 
@@ -405,14 +398,20 @@ __global__ void __launch_bounds__(256, 4) combine_shared_kernel(AttnParams pa, A
     const int4 r0 = reinterpret_cast<const int4*>(pb.rows + w)[0];  // RowInfo: i, ubase, nmt,
     const int of_group = pb.rows[w].of_group;                       // mbase
     const int rs = r0.x * pb.G + hl, us = r0.y + g * r0.z + rs / MT;
-    const int2 cs = pb.unit_ctas[us];
+    // (a unit whose CTAs gave up waiting may have left no note of them: any, but in range)
+    auto ctas_of = [](const AttnParams& l, int u) {
+      const int2 c = l.unit_ctas[u];
+      return make_int2((int)min((uint32_t)c.x, (uint32_t)(l.n_ctas - 1)),
+                       (int)min((uint32_t)c.y, (uint32_t)(l.n_ctas - 1)));
+    };
+    const int2 cs = ctas_of(pb, us);
     int ua = 0, ra = 0;
     int2 ca = make_int2(0, -1);
     if (r0.w >= 0) {
       const int pr = of_group * pb.G + hl;
       ua = pa.tile_unit[r0.w + (pr >> pa.row_log2)] + g;
       ra = pr & ((1 << pa.row_log2) - 1);
-      ca = pa.unit_ctas[ua];
+      ca = ctas_of(pa, ua);
     }
     // the partials' rows, first those of the sequence's unit
     const int ns = cs.y - cs.x + 1, n = ns + ca.y - ca.x + 1;
@@ -510,7 +509,7 @@ SharedWs shared_ws_layout(const sv_attn_desc* d, int num_groups, int sms, bool l
 
 cudaError_t launch_plan_shared(const AttnParams& pa, const AttnParams& pb, bool lines,
                                cudaStream_t s) {
-  return launch_pdl(plan_shared_kernel, dim3(lines ? 2 : 1), dim3(PLAN_T), 0, s, pa, pb);
+  return launch_pdl(plan_shared_kernel, dim3(lines ? 3 : 1), dim3(PLAN_T), 0, s, pa, pb);
 }
 
 cudaError_t launch_combine_shared(const AttnParams& pa, const AttnParams& pb, cudaStream_t s) {
