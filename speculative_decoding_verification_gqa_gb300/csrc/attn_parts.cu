@@ -37,10 +37,10 @@
 // for combine_shared. Every wait is bounded as in attn_tc.cu.
 //
 // Measured (one after another, cold caches): 64 sequences of up to 1024 own positions over a
-// prefix of 8192, Hq 32, Hkv 8, d 128, bf16: sequences 54 us (142 MB from HBM), prefixes 58 us
-// (36 MB, tensor pipe 62% busy); the whole call 68 us captured. 32 sequences of 16 rows over
-// two prefixes of 32768, Hq 64, E4M3: prefixes 343 us (156 MB, tensor pipe 76% busy), the
-// call 374 us, 1.5 PFLOP/s.
+// prefix of 8192, Hq 32, Hkv 8, d 128, bf16: sequences 56 us (142 MB from HBM), prefixes 58 us
+// (36 MB, tensor pipe 60% busy); the whole call 66 us captured. 32 sequences of 16 rows over
+// two prefixes of 32768, Hq 64, E4M3: prefixes 343 us (148 MB, tensor pipe 76% busy), the
+// call 372 us, 1.5 PFLOP/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -21,9 +21,10 @@ namespace sv {
 
 namespace {
 
-// Threads of the plan. It is a chain of barriers and short steps that each warp goes through:
-// a call of 2 sequences took 15.2, 13.6, 13.0 us with 1024, 512, 256 threads (captured), one
-// of 64 sequences 69.3, 68.7, 69.8.
+// Threads of the plan. It is a chain of barriers and short steps that each warp goes through,
+// 4 to 5 us (7 to 9 with the window rows and the units' CTAs in the same chain). Captured calls
+// with 256, 512, 768 threads: 2 sequences 10.1, 10.5, 11.5 us; 32 sequences 22.4, 22.9, 23.6;
+// 64 over a prefix of 8192 65.4, 65.4, 66.1; 100 in 8 groups 46.3, 44.7, 45.1.
 constexpr int PLAN_T = 512;
 static_assert(PLAN_T % 32 == 0 && PLAN_T <= 1024, "whole warps, whose sums one warp scans");
 
@@ -383,8 +384,8 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
 // partials that the row's prefix unit and its sequence's unit left, three at a time (a row has
 // two to four). Memory-bound: reads each partial row (4 d + 8 bytes) once and writes 2 d
 // bytes; what costs beside that is the chain of dependent reads before the partials (row,
-// units, their CTAs), so the tables are small and rows many. 10 us for 10 thousand rows of
-// d = 128 (17 MB from HBM), 18 us for 32 thousand (55 MB), each from cold caches.
+// units, their CTAs), so the tables are small and rows many. 12 us for 10 thousand rows of
+// d = 128 (22 MB from HBM), 17 us for 32 thousand (53 MB), each from cold caches.
 template <int HD>
 __global__ void __launch_bounds__(256, 4) combine_shared_kernel(AttnParams pa, AttnParams pb) {
   constexpr int LANES = 16, PER = HD / LANES, MAXP = 3, ROWS = 256 / LANES;
