@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
     TT += tot[1];
     bad = __syncthreads_or(bad);
   }
-  // (both CTAs know the sequences' work, for the shares of the SMs)
+  // (every CTA knows the sequences' work, for the shares of the SMs)
   const int64_t U_seq = U, TT_seq = TT;
   if (!sequences) U = TT = 0;
   bad = bad || q_total > p.q_rows || U > p.max_units || TT >= 0x7fffffffll;
