@@ -488,6 +488,8 @@ SV_API sv_status spec_verify_attn_shared(const sv_attn_desc* desc, const void* q
   p.group_begin = group_begin;
   p.prefix_len = prefix_len;
   p.flags = (uint32_t*)ws;
+  p.handover = (HandOver*)(ws + lay.handover);
+  p.prefix_ctas = lay.n_ctas[0];
   p.parts = (SharedSeq*)(ws + lay.parts);
   p.row_begin = (int32_t*)(ws + lay.row_begin);
   p.rows = (RowInfo*)(ws + lay.rows);

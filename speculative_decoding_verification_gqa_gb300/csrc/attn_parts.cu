@@ -216,23 +216,34 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, 1)
   Bars* bars = (Bars*)(smem_cta + L::BARS) + half;
   volatile int* abort = &bars->abort;
   const Waiter wt{abort, p.flags, p.wait_limit > 0 ? p.wait_limit : TIMEOUT_CYCLES};
-  // The sequences' kernel waits for the plan and lets the prefixes' kernel start. That one
-  // therefore knows that the plan is complete (every CTA before it had waited for it), and
-  // waits for the sequences' kernel at its end, so that its completion stands for both.
-  if constexpr (RT == 1) pdl_wait();
-  pdl_trigger();
+  // The sequences' kernel waits for the plan, hands what that wait made visible to it (the
+  // plan, and the inputs, which are older) over to the prefixes' CTAs, and lets them start.
+  // Those take it over before their first read, and wait for the sequences' kernel at their
+  // end, so that the completion of theirs stands for both.
+  if constexpr (RT == 1) {
+    pdl_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) hand_over(p.handover, p.prefix_ctas);
+    pdl_trigger();
+  } else {
+    pdl_trigger();
+    bool late = false;
+    if (threadIdx.x == 0 && !take_over(p.handover, wt.limit)) {
+      atomicOr(p.flags, FLAG_TIMEOUT);
+      late = true;
+    }
+    if (__syncthreads_or(late)) {
+      pdl_wait();
+      return;
+    }
+  }
 
-  // (the prefixes' grid did not wait for the plan itself: it reads the start of the plan past
-  // L1 and fences, so that no line that L1 may have kept serves the unit table. Reading that
-  // past L1 every time instead costs a tenth of the call.)
-  const int num_units = __ldcg(&p.hdr->num_units);
-  const int2 rb = __ldcg(p.cta_tab + worker), re = __ldcg(p.cta_tab + worker + 1);
+  const int num_units = p.hdr->num_units;
+  const int2 rb = p.cta_tab[worker], re = p.cta_tab[worker + 1];
   // a half without a range finds no unit
   const Walk walk0 = {rb.x, re.x, rb.y, re.y, rb.x < re.x && rb.y < num_units ? 0 : -1};
-  if constexpr (RT == 2) __threadfence();
   const bool aligned = (saddr(smem_cta) & 1023) == 0;  // the swizzle phases below assume it
-  const int cta_begin = __ldcg(&p.cta_tab[blockIdx.x * L::HALVES].x);
-  const int cta_end = __ldcg(&p.cta_tab[(blockIdx.x + 1) * L::HALVES].x);
+  const int cta_begin = p.cta_tab[blockIdx.x * L::HALVES].x;
+  const int cta_end = p.cta_tab[(blockIdx.x + 1) * L::HALVES].x;
   if (cta_begin >= cta_end || !aligned) {
     if (!aligned && threadIdx.x == 0) atomicOr(p.flags, FLAG_ATTN_SHAPE);
     if constexpr (RT == 2) pdl_wait();
@@ -297,6 +308,7 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, 1)
     const uint64_t policy = RT == 1 ? policy_evict_first() : policy_evict_last();
     // test hook: the first tile of the range is never loaded, so every wait for it runs out
     const bool withhold = p.stall_first_tile != 0;
+    if constexpr (RT == 2) fence_proxy_async_global();  // after take_over: K/V come by TMA
     Walk walk = walk0;
     Seg s;
     uint32_t it = 0;
@@ -307,7 +319,8 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, 1)
       auto seen = [&](int pos) { return pos < s.d.nkeys && pos + box > s.d.start; };
       auto fetch = [&](int jg) -> int {  // this lane's entry of the group starting at tile jg
         const int j = jg + lane / nbox, pos = box_pos(j, lane % nbox);
-        return j < s.j1 && seen(pos) ? __ldg(tab + ((s.d.kbase + pos) >> p.bs_log2)) : 0;
+        // (a plain load, as that of Q below: not the read-only path, which take_over does not order)
+        return j < s.j1 && seen(pos) ? tab[(s.d.kbase + pos) >> p.bs_log2] : 0;
       };
       int ent_cur = fetch(s.j0), ent_nxt = fetch(s.j0 + tg);
       for (int j = s.j0; j < s.j1; ++j, ++it) {
@@ -522,7 +535,7 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, 1)
                            qc;
       auto load_q = [&](int i) -> uint4 {  // called for i = 0, 1, ..
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (r * MT + q0 + i * QI < s.d.rows) v = __ldg(qbase + (int64_t)(qw * p.Hq + qh) * QC);
+        if (r * MT + q0 + i * QI < s.d.rows) v = qbase[(int64_t)(qw * p.Hq + qh) * QC];
         qw += dw;
         qh += dh;
         if (qh >= p.G) {

@@ -133,6 +133,7 @@ struct alignas(16) RowInfo {
   int32_t pad[3];
 };
 
+struct HandOver;  // below
 struct AttnParams {
   const void* q;
   const void* k;               // packed cache [kv_rows, Hkv, d], or the block pool
@@ -170,6 +171,8 @@ struct AttnParams {
   int bs_log2;
   int64_t num_blocks;
   // shared prefixes only
+  HandOver* handover;         // from the sequences' grid to the prefixes' (permits of
+  int prefix_ctas;            // prefix_ctas CTAs a call)
   SharedSeq* parts;           // [num_groups + B]
   int32_t* row_begin;         // [B] first window row of each sequence
   RowInfo* rows;              // [window rows]
@@ -228,11 +231,42 @@ __host__ __device__ inline bool cta_has_tiles(int c, int64_t TT, int C) {
 // start while the previous kernel on the stream drains; it lets its own dependents launch
 // (pdl_trigger: at once, except the tcgen05 attention kernel, whose CTAs release them when
 // their work is done) and waits for the previous grid's results (pdl_wait) before it reads
-// any input, so results are those of ordinary stream order.
+// any input, so results are those of ordinary stream order. The one exception is the prefixes'
+// grid of a shared-prefix call, which runs beside the grid before it and takes its inputs over
+// from that grid (HandOver, below).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
+
+// The order between two grids of which the second does not wait for the first's completion:
+// a CTA of the first, whose pdl_wait has made everything before it visible, releases one
+// permit for each CTA of the second (hand_over), and each of those takes a ticket and acquires
+// the permits up to it (take_over) before its first read. The counters only grow (modulo 2^32),
+// by the same number in every call, and every grid that took tickets has ended before the next
+// call's permits are released, so a ticket's permits are those of its own call.
+struct HandOver {
+  uint32_t permits, tickets;
+};
+__device__ __forceinline__ void hand_over(HandOver* h, uint32_t n) {  // by one thread
+  asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(&h->permits), "r"(n) : "memory");
+}
+// By one thread of the CTA, whose others meet it at a barrier before they read. False if the
+// permits did not come within `limit` clocks.
+__device__ __forceinline__ bool take_over(HandOver* h, long long limit) {
+  uint32_t ticket, permits;
+  asm volatile("atom.relaxed.gpu.global.add.u32 %0, [%1], 1;"
+               : "=r"(ticket)
+               : "l"(&h->tickets)
+               : "memory");
+  const long long t0 = clock64();
+  while (true) {
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(permits) : "l"(&h->permits) : "memory");
+    if ((int32_t)(permits - ticket) > 0) return true;
+    if (clock64() - t0 > limit) return false;
+  }
+}
+
 // Host-side fault injection (sv_inject_launch_failure): counts a launch, and returns true
 // for the one that was armed to fail.
 bool take_injected_launch_failure();
@@ -301,7 +335,7 @@ struct SharedWs {
   struct Line {
     size_t hdr, units, sunits, ubeg, unit_ctas, cta_tab, part_o, part_ml;
   };
-  size_t parts, row_begin, rows, tile_unit, total;
+  size_t handover, parts, row_begin, rows, tile_unit, total;
   Line line[2];
   int64_t max_units[2];
   int n_ctas[2];

@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
   pdl_trigger();
   pdl_wait();
   // the first lengths are asked for before the groups are looked at
+  const HandOver was = *p.handover;
   int T0 = 0, D0 = 0;
   if (tid < B) {
     T0 = p.seq_lens[tid];
@@ -322,6 +323,8 @@ __global__ void __launch_bounds__(PLAN_T) plan_shared_kernel(AttnParams pa, Attn
   if (bad) U = TT = 0;  // (every thread: nothing below is then written or run)
   if (tid == 0) {
     if (bad) atomicOr(p.flags, FLAG_ATTN_SHAPE);
+    // (a call whose prefixes' kernel was not launched has left permits without tickets)
+    if (prefixes && was.tickets != was.permits) p.handover->tickets = was.permits;
     p.hdr->num_units = (int32_t)U;
     p.hdr->total_tiles = (int32_t)TT;
     p.hdr->kt = p.kt;
@@ -481,7 +484,8 @@ SharedWs shared_ws_layout(const sv_attn_desc* d, int num_groups, int sms, bool l
       d->num_kv_heads * (int64_t)d->batch * ((G * (1 + d->max_draft_len) + MT - 1) / MT);
   w.max_units[0] = d->num_kv_heads * prefix_tiles;
   w.max_units[1] = seq_units + (lines ? 0 : w.max_units[0]);
-  size_t o = 256;  // the flag word
+  size_t o = 256;  // the flag word, and the sequences' and prefixes' hand-over
+  w.handover = 128;
   w.parts = o;     o = align_up(o + sizeof(SharedSeq) * ((size_t)num_groups + d->batch), 256);
   w.row_begin = o; o = align_up(o + sizeof(int32_t) * d->batch, 256);
   w.rows = o;      o = align_up(o + sizeof(RowInfo) * rows, 256);

@@ -513,3 +513,31 @@ def test_graphs_that_share_a_workspace(kernel):
     for _, out, alone, _ in cases:
         assert np.array_equal(out.view(torch.int16).cpu().numpy().view(np.uint16), alone)
     assert sv.workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+def test_prefixes_take_their_inputs_over_from_the_sequences_grid(kv):
+    """The prefixes' grid runs beside the sequences' and waits for neither the plan nor what
+    came before it. Each of its CTAs takes a ticket (a counter at byte 132 of the workspace)
+    and acquires a permit (byte 128) that the sequences' grid, which does wait, releases in the
+    same call: one per SM a call, also after a call whose prefixes' kernel was not launched."""
+    ensure_built()
+    w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=128, kv=kv, seed=70)
+    pg = pages(x, gb, P, 16, seed=4)
+    ws = sv.new_workspace(1 << 27)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    counters = lambda: ws[128:136].view(torch.int32).tolist()  # noqa: E731
+    for call in range(1, 4):
+        assert_within(run(x, pg, gb, P, workspace=ws, max_seq=2000), w, x)
+        assert counters() == [call * sms] * 2
+    sv.api.inject_launch_failure(2)  # plan, sequences, prefixes
+    with pytest.raises(sv.SpecVerifyError):
+        run(x, pg, gb, P, workspace=ws, max_seq=2000)
+    torch.cuda.synchronize()
+    assert counters() == [4 * sms, 3 * sms]
+    assert_within(run(x, pg, gb, P, workspace=ws, max_seq=2000), w, x)
+    assert counters() == [5 * sms] * 2
+    ws[128:136].view(torch.int32).fill_(-(sms // 2))  # they wrap in the next call
+    assert_within(run(x, pg, gb, P, workspace=ws, max_seq=2000), w, x)
+    assert counters() == [sms - sms // 2] * 2
+    assert sv.workspace_status(ws) == 0
