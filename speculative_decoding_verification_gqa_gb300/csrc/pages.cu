@@ -747,11 +747,16 @@ int segs_of(const sv_page_table& t, int seg = SEG) {
   return (most + seg - 1) / seg;
 }
 
-size_t row_set_bytes(const sv_page_table& t) { return ((size_t)t.table_rows + 31) / 32 * 4; }
+constexpr size_t set_bytes(int32_t rows) { return ((size_t)rows + 31) / 32 * 4; }
+size_t row_set_bytes(const sv_page_table& t) { return set_bytes(t.table_rows); }
+// Sets beyond what a launch may ask for unasked. The limit belongs to the kernel, not to the
+// call: it is the same for every size, so that no call lowers it between another one's setting
+// and launch.
 template <class F>
-cudaError_t allow_set(F kernel, size_t bytes) {  // beyond what a launch may ask for unasked
+cudaError_t allow_set(F kernel, size_t bytes) {
   return bytes <= 16 * 1024 ? cudaSuccess
-                            : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+                            : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   (int)set_bytes(SV_MAX_TABLE_ROWS));
 }
 
 // Resident at once, 8 CTAs of AT threads an SM; an odd number, so that what repeats along the

@@ -1,6 +1,7 @@
 """GPU tests of the page operators (fork, extend with copy on write, trim, compact) against
 the plain model: whole numbers and moved bits, so everything is compared for equality."""
 import random
+import threading
 
 import pytest
 import torch
@@ -512,3 +513,44 @@ def test_workspace_is_made_on_the_stream_of_the_call(as_number):
     torch.cuda.synchronize()
     m.fork([0], [1])
     d.same()
+
+
+@pytest.mark.parametrize("op", ["fork", "extend", "trim"])
+def test_host_threads_with_tables_of_different_sizes(op):
+    """Two host threads, each with a state, a stream and a workspace of its own; both tables have
+    more rows than a launch has room for unasked, one three times as many as the other."""
+    ensure_built()
+    bs, calls, bad = 8, 3000, []
+    start = threading.Barrier(2)
+
+    def work(R):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            ref = torch.zeros(64, dtype=torch.int32, device=DEV)
+            lens = torch.zeros(R, dtype=torch.int32, device=DEV)
+            table = torch.full((R, 2), -1, dtype=torch.int32, device=DEV)
+            a, b = (torch.tensor([r], dtype=torch.int32, device=DEV) for r in (R - 2, R - 1))
+            zero = torch.zeros(1, dtype=torch.int32, device=DEV)
+            ws = sv.new_workspace(sv.pages_workspace_bytes(64, R))
+            s.synchronize()
+            start.wait()
+            try:
+                for _ in range(calls):  # calls that leave an empty state as it is
+                    if op == "fork":
+                        sv.spec_pages_fork(ref, table, lens, a, b, block_size=bs, workspace=ws)
+                    elif op == "extend":
+                        sv.spec_pages_extend(ref, table, lens, a, zero, block_size=bs, workspace=ws)
+                    else:
+                        sv.spec_pages_trim(ref, table, lens, a, zero, block_size=bs, workspace=ws)
+            except sv.SpecVerifyError as e:
+                bad.append((R, e.status))
+            s.synchronize()
+            if sv.workspace_status(ws, stream=s) != 0 or int(lens.sum()) or int(ref.sum()):
+                bad.append((R, "state"))
+
+    threads = [threading.Thread(target=work, args=(R,)) for R in (300_000, 1 << 20)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert bad == []
