@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(AT) fork_kernel(const Pages a, int segs) {
   const int64_t stride = a.t.max_blocks_per_seq;
   const int groups = (a.n + FORK_ROWS - 1) / FORK_ROWS;
   const int64_t items = bad ? 0 : (int64_t)groups * segs;
+  int least = 1;  // the least count met: whoever adds to a free page first finds 0
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int i0 = (int)(it / segs) * FORK_ROWS, s = (int)(it % segs);
     const int cnt = min(FORK_ROWS, a.n - i0);
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(AT) fork_kernel(const Pages a, int segs) {
       for (int k = 0; k < FORK_ROWS; ++k) {
         if (j >= pages[k]) continue;
         if (par[k] != prev) {
-          if (add) atomicAdd(a.t.ref_count + e, add);
+          if (add) least = min(least, atomicAdd(a.t.ref_count + e, add));
           add = 0;
           prev = par[k];
           e = a.t.block_table[prev * stride + j];
@@ -241,9 +242,10 @@ __global__ void __launch_bounds__(AT) fork_kernel(const Pages a, int segs) {
         if (e >= 0 && e < a.t.num_blocks) ++add;
         a.t.block_table[child[k] * stride + j] = e;
       }
-      if (add) atomicAdd(a.t.ref_count + e, add);
+      if (add) least = min(least, atomicAdd(a.t.ref_count + e, add));
     }
   }
+  if (least < 1) atomicOr(a.flags, FLAG_PAGES_SHAPE);
   if (!last_cta(a)) return;  // every CTA has read the lengths
   if (bad) {
     if (threadIdx.x == 0) atomicOr(a.flags, FLAG_PAGES_SHAPE);

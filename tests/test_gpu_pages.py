@@ -554,3 +554,34 @@ def test_host_threads_with_tables_of_different_sizes(op):
     for t in threads:
         t.join()
     assert bad == []
+
+
+@pytest.mark.parametrize("kids", [1, 7, 8, 9, 31])
+@pytest.mark.parametrize("col", [0, 1, 600])
+def test_fork_of_a_row_that_names_a_free_page(kids, col):
+    """Damaged before the call, so the call says so, whichever item of the work meets the page,
+    and for children of one parent or of two that both name the page."""
+    bs, n = 8, 8 * 601 + 3
+    for parents in ([0], [0, 1]):
+        m = filled(3 + kids, 1400, bs, [n, n] + [0] * (1 + kids), seed=kids)
+        d = Device(m, pools=1, width=4)
+        p = m.table[0][col]
+        d.ref[p] = 0
+        if len(parents) == 2:
+            d.ref[m.table[1][col]] = 0
+            d.table[1, col] = p
+        d.fork([parents[k % len(parents)] for k in range(kids)], list(range(3, 3 + kids)))
+        assert d.status() == 8
+        d.trim([2], [0])  # a row that is sound
+        assert d.status() == 0
+
+
+def test_fork_beside_a_free_page_is_not_reported():
+    """An entry past the forked length, or of a row that is no parent, is not met."""
+    bs = 8
+    m = filled(4, 30, bs, [20, 9, 0, 0], seed=3)
+    d = Device(m)
+    d.ref[m.table[0][2]] = 0
+    d.ref[m.table[1][0]] = 0
+    d.fork([0, 0], [2, 3], [16, 9])
+    assert d.status() == 0
