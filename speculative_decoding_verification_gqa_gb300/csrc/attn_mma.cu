@@ -10,9 +10,11 @@
 // Nothing but the final O (or a split-KV partial) is written to global memory.
 //
 // FP8 E4M3 K/V: the raw 8-bit tile is staged by cp.async, then converted in shared memory
-// to f16 (every E4M3 value is exact in f16); Q is converted bf16 -> f16 on load and the
-// MMAs run in f16 with fp32 accumulation. The per-head K scale is folded into the score
-// scale and the V scale into the final normalisation.
+// to f16 (every E4M3 value is exact in f16); Q is converted bf16 -> f16 on load, each row
+// times the power of two that puts its largest magnitude in [128, 256) (f16 ends at 65504 and
+// has its last normal number at 2^-14, bf16 neither), and the MMAs run in f16 with fp32
+// accumulation. The row's factor and the per-head K scale are taken back by the score scale,
+// the V scale is folded into the final normalisation.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -88,13 +90,14 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   }
 }
 
-// bf16 x8 -> f16 x8 (exact for |x| in f16's normal range; tiny values round to f16).
-__device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v) {
+// bf16 x8 times f -> f16 x8 (exact for results in f16's normal range; of a row whose largest
+// magnitude is 128 or more, what rounds is below 2^-21 of that, by less than 2^-31 of it).
+__device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v, float f) {
   uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    float2 f = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w[e]));
-    __half2 h = __float22half2_rn(f);
+    const float2 x = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w[e]));
+    __half2 h = __float22half2_rn(make_float2(x.x * f, x.y * f));
     w[e] = *reinterpret_cast<uint32_t*>(&h);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
@@ -132,6 +135,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_mma_kernel(const AttnParams 
   constexpr int NS = KT / 8;    // n8 tiles of S
   constexpr int NO = HD / 8;    // n8 tiles of O
   extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ float s_scale[FP8 ? MT : 1];  // each query row's score scale in log2 units
   uint8_t* sQ = smem;
   uint8_t* sKV = smem + L::Q_BYTES;  // ring: [stage][K|V]
   const int STAGE_BYTES = FP8 ? 2 * L::T8_BYTES : 2 * L::T16_BYTES;
@@ -175,8 +179,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_mma_kernel(const AttnParams 
     const int kvis = SHARED ? part.start : first_visible_key(T, p.window);  // earlier rows
                                                                             // left the window
     const int64_t qo = SHARED ? part.q_off : p.q_off[b], ko = SHARED ? 0 : p.kv_off[b];
-    const float ks = FP8 ? p.kv_scale[g] : 1.f;
-    const float sc = p.scale_log2 * ks;
+    const float sc = FP8 ? p.scale_log2 * p.kv_scale[g] : p.scale_log2;
 
     __syncthreads();  // the previous segment is done with shared memory
     // ---- query-row tile: row r = (window position i, head in group hl)
@@ -189,7 +192,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_mma_kernel(const AttnParams 
         const uint4* src = reinterpret_cast<const uint4*>(
                                (const uint16_t*)p.q + ((qo + i) * p.Hq + (int64_t)g * p.G + hl) * HD) + c;
         val = __ldg(src);
-        if (FP8) val = bf16x8_to_f16x8(val);
+      }
+      if constexpr (FP8) {  // (a row's CH chunks lie in neighbouring lanes)
+        const uint32_t w[4] = {val.x, val.y, val.z, val.w};
+        uint32_t amax = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) amax = max(amax, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+#pragma unroll
+        for (int o = 1; o < L::CH; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        val = bf16x8_to_f16x8(val, exp2_of(q_exponent(amax)));
+        if (c == 0) s_scale[r] = sc * exp2_of(-q_exponent(amax));
       }
       *reinterpret_cast<uint4*>(sQ + L::swz(r, c)) = val;
     }
@@ -329,13 +341,17 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_mma_kernel(const AttnParams 
       }
       // ---- scale (log2 units) and window-causal mask: key j visible to row i iff j <= T+i
       // (and, under a sliding window, j >= T+i-window+1)
+      // (E4M3: the rows' scales are read again for every tile. Held in registers they make 194
+      // of a thread of d = 64; with more than 192 the join's CTAs do not fit beside this one,
+      // and a call of 31.9 us takes 35.6: 3 sequences of up to 4129 positions, Hq 8, Hkv 2.)
+      const float scA = FP8 ? s_scale[rA] : sc, scB = FP8 ? s_scale[rB] : sc;
       const int key0 = kofs + j * KT;
       const bool edge = key0 + KT > T || key0 < lo_max;
 #pragma unroll
       for (int n = 0; n < NS; ++n) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float x = s[n][e] * sc;
+          float x = s[n][e] * (e < 2 ? scA : scB);
           if (edge) {
             const int key = key0 + n * 8 + 2 * (lane & 3) + (e & 1);
             const int row_lim = T + (e < 2 ? iA : iB);

@@ -547,10 +547,6 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, 1)
       if constexpr (F8) {
         // row x 2^e, its largest magnitude in [128, 256), as hi + lo (attn_tc.cu); 2^-e joins
         // the K scale in the score scale
-        auto exponent = [](uint32_t amax) -> int {
-          const int eb = max((int)(amax >> 7), 1);
-          return amax == 0 ? 0 : min(max(134 - eb, -120), 120);
-        };
 #pragma unroll 1
         for (int i0 = 0; i0 < QC; i0 += 8) {
           uint4 v[8];
@@ -564,7 +560,7 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, 1)
             for (int k = 0; k < 4; ++k) amax = max(amax, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
             // the row's 16 lanes
             amax = lane < 16 ? __reduce_max_sync(0x0000ffffu, amax) : __reduce_max_sync(0xffff0000u, amax);
-            const float f = __int_as_float((exponent(amax) + 127) << 23);
+            const float f = exp2_of(q_exponent(amax));
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -577,8 +573,7 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, 1)
           }
         }
         wg_sync(wg);
-        sc = p.scale_log2 * p.kv_scale[s.d.g] *
-             __int_as_float((127 - exponent(row_amax[rr])) << 23);
+        sc = p.scale_log2 * p.kv_scale[s.d.g] * exp2_of(-q_exponent(row_amax[rr]));
       } else {
         uint4 v[QC];
 #pragma unroll

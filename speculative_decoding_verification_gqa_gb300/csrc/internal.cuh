@@ -227,6 +227,15 @@ __host__ __device__ inline bool cta_has_tiles(int c, int64_t TT, int C) {
   return (int64_t)(c + 1) * TT / C > (int64_t)c * TT / C;
 }
 
+// E4M3 K/V: the exponent e by which a query row is scaled before its conversion to a type of
+// smaller range, for the row's largest bf16 magnitude `amax` (its bits): 2^e puts that in
+// [128, 256); clamped so that 2^e and 2^-e are normal numbers; 0 for a row of zeros.
+__device__ __forceinline__ int q_exponent(uint32_t amax) {
+  const int eb = max((int)(amax >> 7), 1);  // amax in [2^(eb - 127), 2^(eb - 126))
+  return amax == 0 ? 0 : min(max(134 - eb, -120), 120);
+}
+__device__ __forceinline__ float exp2_of(int e) { return __int_as_float((e + 127) << 23); }
+
 // Programmatic dependent launch: every kernel of the library is launched so that it may
 // start while the previous kernel on the stream drains; it lets its own dependents launch
 // (pdl_trigger: at once, except the tcgen05 attention kernel, whose CTAs release them when

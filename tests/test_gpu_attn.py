@@ -426,3 +426,23 @@ def test_many_sequences_with_a_sliding_window(kernel):
     got = gpu_attn(x, window=200)
     units = [(0, 0), (300, 1), (519, 1), (257, 0)]
     assert_close(got, oracle_attn(w, x, units=units, window=200))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("e", [-80, -30, 20, 100])
+def test_queries_of_any_finite_magnitude(kernel, e, d, kv):
+    """q times 2^e under a softmax scale times 2^-e gives the same bits: every product and sum
+    is the same number times a power of two, far outside f16's range too."""
+    w, x = _small(B=3, Hq=8, Hkv=2, d=d, T=(513, 5, 129), D=(8, 2, 1), kv=kv, seed=73)
+    q, k, v, sc, T, D = dev_attn(x)
+
+    def call(q, scale):
+        o = sv.spec_verify_attn(q, k, v, T, D, max_draft_len=8, max_seq_len=513, kv_scale=sc,
+                                softmax_scale=scale)
+        assert bool(torch.isfinite(o.float()).all())
+        return o
+
+    big = (q.double() * 2.0 ** e).bfloat16()
+    assert bool((big.double() == q.double() * 2.0 ** e).all())  # powers of two: exact
+    assert torch.equal(call(big, 2.0 ** (-4 - e)), call(q, 2.0 ** -4))

@@ -541,3 +541,45 @@ def test_prefixes_take_their_inputs_over_from_the_sequences_grid(kv):
     assert_within(run(x, pg, gb, P, workspace=ws, max_seq=2000), w, x)
     assert counters() == [sms - sms // 2] * 2
     assert sv.workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("e", [-80, -30, 20, 100])
+def test_queries_of_any_finite_magnitude(kernel, e, d, kv):
+    """q times 2^e under a softmax scale times 2^-e: every product and sum is the same number
+    times a power of two, so the bits are the same, far outside f16's range too."""
+    w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=d, kv=kv, seed=71)
+    pg = pages(x, gb, P, 16, seed=4)
+    scale = 2.0 ** -4
+    want = run(x, pg, gb, P, softmax_scale=scale)
+    q = bf16_to_f64(x["q"])
+    assert np.abs(q).max() * 2.0 ** 20 > 65504 and np.abs(q).max() < 2 ** 20
+    big = q * 2.0 ** e
+    y = dict(x, q=(big.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16))
+    assert np.array_equal(bf16_to_f64(y["q"]), big)  # powers of two: exact
+    got = run(y, pg, gb, P, softmax_scale=scale * 2.0 ** -e)
+    assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_of_very_different_magnitudes(kernel, d, kv):
+    """Rows 2^24 times as large and as small as their neighbours, in one tile, each within the
+    bound: the softmax scale is that of the largest, so the others' weights are nearly even."""
+    import oracle
+    w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=d, kv=kv, seed=72)
+    q = bf16_to_f64(x["q"])
+    q[0::3] *= 2.0 ** 24
+    q[1::3] *= 2.0 ** -24
+    x["q"] = (q.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    assert np.array_equal(bf16_to_f64(x["q"]), q)
+    scale = 2.0 ** -28
+    got = bf16_to_f64(run(x, pages(x, gb, P, 16, seed=4), gb, P, softmax_scale=scale))
+    kw = dict(Hq=w.Hq, Hkv=w.Hkv, d=w.d, scale=scale, kv_scale=x["kv_scale"])
+    mag = x["v"] & (0x7F if x["v"].dtype == np.uint8 else 0x7FFF)
+    ref = oracle.verify_attn(x["q"], x["k"], x["v"], x["seq_lens"], x["draft_len"], **kw)
+    mag = oracle.verify_attn(x["q"], x["k"], mag.astype(x["v"].dtype), x["seq_lens"], x["draft_len"], **kw)
+    assert np.isfinite(got).all()
+    # the bound of assert_within: a scale of 2^-4 for the large rows is that of d = 256
+    assert (np.abs(got - ref) <= np.abs(ref) * 2.0 ** -8 + mag * (2.0 ** -8 + 2.0 ** -10)).all()
