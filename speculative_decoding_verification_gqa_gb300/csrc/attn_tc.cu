@@ -526,10 +526,7 @@ __device__ __forceinline__ void attn_tc_body(const AttnParams& p, const CUtensor
           for (int k = 0; k < 8; ++k)
             amax = max(amax, max(both[k] & 0x7fffu, (both[k] >> 16) & 0x7fffu));
         }
-        // amax in [2^(eb-127), 2^(eb-126)): e = 8 - (eb - 126), clamped to keep 2^+-e normal
-        const int eb = max((int)(amax >> 7), 1);
-        const int e2 = amax == 0 ? 0 : min(max(134 - eb, -120), 120);
-        const float f = __int_as_float((e2 + 127) << 23);
+        const float f = exp2_of(q_exponent(amax));
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {  // 8 columns (32 elements) at a time
           uint32_t hi[8], lo[8];
@@ -544,7 +541,7 @@ __device__ __forceinline__ void attn_tc_body(const AttnParams& p, const CUtensor
           tmem_st8(tq + COL_Q + 32 + wg * 16 + 8 * hh, lo);
         }
         tmem_wait_st();
-        sc = p.scale_log2 * p.kv_scale[s.g] * __int_as_float((127 - e2) << 23);
+        sc = p.scale_log2 * p.kv_scale[s.g] * q_unscale(amax);
       } else if (wg < HD / 64) {
         // Q row -> TMEM columns [COL_Q, COL_Q + HD/2) as packed bf16 pairs, 32 columns per
         // store (both warpgroups for d = 128, the first one for d = 64)

@@ -235,6 +235,12 @@ __device__ __forceinline__ int q_exponent(uint32_t amax) {
   return amax == 0 ? 0 : min(max(134 - eb, -120), 120);
 }
 __device__ __forceinline__ float exp2_of(int e) { return __int_as_float((e + 127) << 23); }
+// What the score scale of such a row takes it back by: 2^-e, or NaN for a row with an infinity
+// or a NaN in it. E4M3 has no infinity and its conversions saturate, so the row's scores would
+// be finite; all of them become NaN, and with them the row's output, as with bf16 K/V.
+__device__ __forceinline__ float q_unscale(uint32_t amax) {
+  return amax >= 0x7f80u ? __int_as_float(0x7fffffff) : exp2_of(-q_exponent(amax));
+}
 
 // Programmatic dependent launch: every kernel of the library is launched so that it may
 // start while the previous kernel on the stream drains; it lets its own dependents launch

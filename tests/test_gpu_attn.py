@@ -446,3 +446,21 @@ def test_queries_of_any_finite_magnitude(kernel, e, d, kv):
     big = (q.double() * 2.0 ** e).bfloat16()
     assert bool((big.double() == q.double() * 2.0 ** e).all())  # powers of two: exact
     assert torch.equal(call(big, 2.0 ** (-4 - e)), call(q, 2.0 ** -4))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "bf16 K of 0", "fp8_e4m3", "fp8_e4m3 K of 0"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_of_infinite_and_nan_queries_become_nan(kernel, d, kv):
+    """Scores of an infinity are infinite or NaN, whichever the key; other rows keep their
+    bits. One sequence on several CTAs, one of a single tile."""
+    w, x = _small(B=2, Hq=8, Hkv=2, d=d, T=(20000, 3), D=(2, 1), kv=kv.split()[0], seed=75)
+    if kv.endswith("0"):  # where q is infinite
+        x["k"][:, :, 9] = 0
+    clean = gpu_attn(x)
+    spoilt = np.zeros(x["q"].shape[:2], dtype=bool)
+    for r, h, bits in ((0, 2, 0x7F80), (1, 7, 0xFF80), (2, 0, 0x7FC0), (4, 5, 0x7F80)):
+        x["q"][r, h, 9] = bits
+        spoilt[r, h] = True
+    got = gpu_attn(x)
+    assert np.isnan(bf16_to_f64(got[spoilt])).all()
+    assert np.array_equal(got[~spoilt], clean[~spoilt])

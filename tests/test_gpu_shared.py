@@ -583,3 +583,31 @@ def test_rows_of_very_different_magnitudes(kernel, d, kv):
     assert np.isfinite(got).all()
     # the bound of assert_within: a scale of 2^-4 for the large rows is that of d = 256
     assert (np.abs(got - ref) <= np.abs(ref) * 2.0 ** -8 + mag * (2.0 ** -8 + 2.0 ** -10)).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "bf16 K of 0", "fp8_e4m3", "fp8_e4m3 K of 0"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_of_infinite_and_nan_queries_become_nan(kernel, d, kv):
+    """Scores of an infinity are infinite or NaN, whichever the key: no finite output may come
+    of them, with 8-bit keys too (E4M3 has no infinity). All other rows keep their bits."""
+    w, x, gb, P = inputs([(150, [(160, 1), (150, 2), (400, 3)])], Hq=4, Hkv=2, d=d, kv=kv.split()[0],
+                         seed=74)
+    if kv.endswith("0"):  # where q is infinite
+        x["k"][:, :, 5:] = 0
+    pg = pages(x, gb, P, 16, seed=4)
+    full = pages(x, gb, np.zeros_like(P), 16, seed=4)  # (the paged call reads every own entry)
+
+    def both():
+        q, k, v, bt, T, D, sc = to_device(x, full)
+        o = sv.spec_verify_attn_paged(q, k, v, bt, T, D, max_draft_len=3, max_seq_len=400, kv_scale=sc)
+        return run(x, pg, gb, P), o.view(torch.int16).cpu().numpy().view(np.uint16)
+
+    clean = both()
+    spoilt = np.zeros(x["q"].shape[:2], dtype=bool)
+    for r, h, bits in ((1, 2, [0x7F80]), (3, 0, [0xFF80]), (4, 3, [0x7FC0]), (5, 1, [0x7F80, 0xFF80]),
+                       (8, 0, [0x7F80] * (d - 5))):
+        x["q"][r, h, 5:5 + len(bits)] = bits
+        spoilt[r, h] = True
+    for got, want in zip(both(), clean):
+        assert np.isnan(bf16_to_f64(got[spoilt])).all()
+        assert np.array_equal(got[~spoilt], want[~spoilt])
