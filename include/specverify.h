@@ -114,7 +114,8 @@ SV_API size_t spec_verify_attn_workspace_size(const sv_attn_desc* desc);
  *   seq_lens int32 [B] = T_b (prefix length, excluding the window)
  *   draft_len int32 [B] = D_b
  *   kv_scale fp32 [2, Hkv] for SV_FP8_E4M3 (row 0 scales K, row 1 scales V: the real
- *            value of a code c is e4m3(c) * scale); must be NULL for SV_BF16
+ *            value of a code c is e4m3(c) * scale; K's are not negative); must be NULL for
+ *            SV_BF16
  *   out      bf16 [q_rows, Hq, d]; only the sum_b W_b packed rows are written
  *   workspace >= spec_verify_attn_workspace_size(desc) bytes, 256-byte aligned
  * q, k_cache, v_cache and out must be 16-byte aligned.

@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_mma_kernel(const AttnParams 
 #pragma unroll
         for (int o = 1; o < L::CH; o <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         val = bf16x8_to_f16x8(val, exp2_of(q_exponent(amax)));
-        if (c == 0) s_scale[r] = sc * q_unscale(amax);
+        if (c == 0) s_scale[r] = q_row_scale(sc, amax);
       }
       *reinterpret_cast<uint4*>(sQ + L::swz(r, c)) = val;
     }

@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, 1)
           }
         }
         wg_sync(wg);
-        sc = p.scale_log2 * p.kv_scale[s.d.g] * q_unscale(row_amax[rr]);
+        sc = q_row_scale(p.scale_log2 * p.kv_scale[s.d.g], row_amax[rr]);
       } else {
         uint4 v[QC];
 #pragma unroll

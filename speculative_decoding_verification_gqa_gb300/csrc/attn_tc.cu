@@ -541,7 +541,7 @@ __device__ __forceinline__ void attn_tc_body(const AttnParams& p, const CUtensor
           tmem_st8(tq + COL_Q + 32 + wg * 16 + 8 * hh, lo);
         }
         tmem_wait_st();
-        sc = p.scale_log2 * p.kv_scale[s.g] * q_unscale(amax);
+        sc = q_row_scale(p.scale_log2 * p.kv_scale[s.g], amax);
       } else if (wg < HD / 64) {
         // Q row -> TMEM columns [COL_Q, COL_Q + HD/2) as packed bf16 pairs, 32 columns per
         // store (both warpgroups for d = 128, the first one for d = 64)

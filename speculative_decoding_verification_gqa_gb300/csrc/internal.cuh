@@ -235,11 +235,16 @@ __device__ __forceinline__ int q_exponent(uint32_t amax) {
   return amax == 0 ? 0 : min(max(134 - eb, -120), 120);
 }
 __device__ __forceinline__ float exp2_of(int e) { return __int_as_float((e + 127) << 23); }
-// What the score scale of such a row takes it back by: 2^-e, or NaN for a row with an infinity
-// or a NaN in it. E4M3 has no infinity and its conversions saturate, so the row's scores would
-// be finite; all of them become NaN, and with them the row's output, as with bf16 K/V.
-__device__ __forceinline__ float q_unscale(uint32_t amax) {
-  return amax >= 0x7f80u ? __int_as_float(0x7fffffff) : exp2_of(-q_exponent(amax));
+// The score scale of such a row, which takes 2^e back: scale * 2^-e. NaN for a row with an
+// infinity or a NaN in it: E4M3 has no infinity and its conversions saturate, so the row's
+// scores would be finite; all of them become NaN, and with them the row's output, as with bf16
+// K/V. The least normal number instead of zero (a head whose K scale is 0) or of what
+// underflows: the scores of all keys are then 0 but for less than 2^-90, and a masked key's
+// stays -infinity, where -infinity * 0 is NaN.
+__device__ __forceinline__ float q_row_scale(float scale, uint32_t amax) {
+  constexpr float LEAST = 1.17549435e-38f;
+  const float s = scale * exp2_of(-q_exponent(amax));
+  return amax >= 0x7f80u ? __int_as_float(0x7fffffff) : fabsf(s) < LEAST ? LEAST : s;
 }
 
 // Programmatic dependent launch: every kernel of the library is launched so that it may

@@ -464,3 +464,13 @@ def test_rows_of_infinite_and_nan_queries_become_nan(kernel, d, kv):
     got = gpu_attn(x)
     assert np.isnan(bf16_to_f64(got[spoilt])).all()
     assert np.array_equal(got[~spoilt], clean[~spoilt])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [0.0, 1e-44, 1e-30])
+def test_heads_of_zeros_and_of_tiny_keys(kernel, scale, d):
+    """A K scale of 0, one below the normal numbers and one next to nothing: even weights over
+    the visible keys."""
+    w, x = _small(B=3, Hq=8, Hkv=2, d=d, T=(20000, 3, 129), D=(2, 1, 0), kv="fp8_e4m3", seed=77)
+    x["kv_scale"][0, 1] = scale
+    assert_close(gpu_attn(x), oracle_attn(w, x))

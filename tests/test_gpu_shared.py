@@ -611,3 +611,25 @@ def test_rows_of_infinite_and_nan_queries_become_nan(kernel, d, kv):
     for got, want in zip(both(), clean):
         assert np.isnan(bf16_to_f64(got[spoilt])).all()
         assert np.array_equal(got[~spoilt], want[~spoilt])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [0.0, 1e-44, 1e-30])
+def test_heads_of_zeros_and_of_tiny_keys(kernel, scale, d):
+    """A K scale of 0 (a head whose keys are all zero), one below the normal numbers and one
+    next to nothing: even weights over the visible keys, masked tiles and split parts among
+    them; the paged call's too. The other heads keep their bits."""
+    w, x, gb, P = inputs(TWO, Hq=8, Hkv=2, d=d, kv="fp8_e4m3", seed=76)
+    pg = pages(x, gb, P, 16, seed=4)
+    full = pages(x, gb, np.zeros_like(P), 16, seed=4)  # (the paged call reads every own entry)
+
+    def both():
+        q, k, v, bt, T, D, sc = to_device(x, full)
+        o = sv.spec_verify_attn_paged(q, k, v, bt, T, D, max_draft_len=7, max_seq_len=1000, kv_scale=sc)
+        return run(x, pg, gb, P), o.view(torch.int16).cpu().numpy().view(np.uint16)
+
+    clean = both()
+    x["kv_scale"][0, 1] = scale
+    for got, want in zip(both(), clean):
+        assert_within(got, w, x)
+        assert np.array_equal(got[:, :4], want[:, :4])
