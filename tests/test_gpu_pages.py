@@ -585,3 +585,45 @@ def test_fork_beside_a_free_page_is_not_reported():
     d.ref[m.table[1][0]] = 0
     d.fork([0, 0], [2, 3], [16, 9])
     assert d.status() == 0
+
+
+def test_calls_of_very_many_rows():
+    """A call of 2^18 rows of a table of 2^18 + 2^17: every row of it extends, half of them
+    from shared partial pages; the others are forked, and all are trimmed. Against the same on
+    tensors, as the model takes rows one by one."""
+    ensure_built()
+    bs, n, kids = 8, 1 << 18, 1 << 17
+    R, nb, mb = n + kids, 3 * (1 << 18), 3
+    i32 = lambda t: t.to(torch.int32)  # noqa: E731
+    rows = torch.randperm(R, device=DEV, generator=torch.Generator(DEV).manual_seed(5))
+    par, child = rows[:kids], rows[n:]  # every child has a parent of its own
+    ref = torch.zeros(nb, dtype=torch.int32, device=DEV)
+    lens = torch.zeros(R, dtype=torch.int32, device=DEV)
+    table = torch.full((R, mb), -1, dtype=torch.int32, device=DEV)
+    pool = torch.arange(nb * bs, dtype=torch.int32, device=DEV).view(nb, bs, 1).expand(nb, bs, 4).contiguous()
+    first = pool.clone()
+    kw = dict(block_size=bs, workspace=sv.new_workspace(sv.pages_workspace_bytes(nb, R)))
+    status = lambda: sv.workspace_status(kw["workspace"], clear=True)  # noqa: E731
+    # 2^18 rows take a page of 5 positions each, in call order
+    sv.spec_pages_extend(ref, table, lens, i32(rows[:n]), torch.full((n,), 5, dtype=torch.int32, device=DEV),
+                         pools=[pool], **kw)
+    assert status() == 0
+    assert torch.equal(table[rows[:n], 0], torch.arange(n, dtype=torch.int32, device=DEV))
+    sv.spec_pages_fork(ref, table, lens, i32(par), i32(child), **kw)
+    assert status() == 0
+    assert torch.equal(table[child, 0], table[par, 0]) and bool((lens[child] == 5).all())
+    assert bool((ref[:kids] == 2).all()) and bool((ref[kids:n] == 1).all())
+    # the children, then half of the other rows: each child takes a copy, the others a second page
+    call = torch.cat([child, rows[kids:n]])
+    to = torch.where(torch.arange(n, device=DEV) < kids, 6, 9)
+    sv.spec_pages_extend(ref, table, lens, i32(call), i32(to), pools=[pool], **kw)
+    assert status() == 0
+    fresh = torch.arange(n, n + n, dtype=torch.int32, device=DEV)
+    assert torch.equal(table[child, 0], fresh[:kids]) and torch.equal(table[rows[kids:n], 1], fresh[kids:])
+    assert bool((ref[:2 * n] == 1).all()) and bool((ref[2 * n:] == 0).all())
+    assert torch.equal(pool[n:n + kids, :5], first[:kids, :5]) and torch.equal(pool[n:n + kids, 5:], first[n:n + kids, 5:])
+    assert torch.equal(pool[:n], first[:n]) and torch.equal(pool[n + kids:], first[n + kids:])
+    sv.spec_pages_trim(ref, table, lens, i32(rows[torch.randperm(R, device=DEV)]),
+                       torch.zeros(R, dtype=torch.int32, device=DEV), **kw)
+    assert status() == 0
+    assert bool((ref == 0).all()) and bool((lens == 0).all()) and bool((table == -1).all())
