@@ -24,10 +24,11 @@ constexpr int SWITCH_TILES_TC_FP8 = SV_SWITCH_F8;
 constexpr int SWITCH_TILES_TC_BF16 = SV_SWITCH_BF16;
 constexpr int SWITCH_TILES_MMA = 2;
 // Shared prefixes. A unit's start in 128-key tiles of 256 rows and in 64-key tiles of 128 rows,
-// and the SM time of the latter (two at a time on an SM) in the former. Measured around them
-// (calls back to back; 64 sequences over a prefix of 8192, 128 over four of 16385, bf16; 32
-// over two of 32768, E4M3): 68.8, 254, 369 us; a sequence's start of 4: 69.6, 261, 372; costs
-// of 0.31 and 0.50: 68.9, 257, 371; a prefix's start of 2: 69.3, 254, 368.
+// and the SM time of the latter (two at a time on an SM) in the former. Measured around them at
+// d = 128 (short runs of calls back to back, below the power limit; 64 sequences over a prefix
+// of 8192, 128 over four of 16385, bf16; 32 over two of 32768, E4M3): 68.8, 254, 369 us; a
+// sequence's start of 4: 69.6, 261, 372; costs of 0.31 and 0.50: 68.9, 257, 371; a prefix's
+// start of 2: 69.3, 254, 368. They also divide the SMs at d = 64, where nothing was swept.
 constexpr int SWITCH_TILES_PREFIX = 3;
 constexpr int SWITCH_TILES_SEQUENCE = 3;
 constexpr float SEQUENCE_COST_BF16 = 0.28f;
@@ -395,7 +396,7 @@ constexpr int64_t MAX_SHARED_UNITS = 1 << 22;
 
 // Small calls take the mma.sync kernel: three launches instead of four, no TMEM, no tensor
 // maps. The rule goes by what the host knows, the sequences' units and the longest sequence.
-// Calls back to back from Python, mma.sync against tcgen05, d 128, bf16 (E4M3):
+// Calls back to back from Python, mma.sync against tcgen05, d 128, bf16 (E4M3; d 64 not swept):
 //     8 units of 512, 960 positions       18.9, 20.7 us against 20.3, 19.7 (18.1, 21.1: 22.8, 23.0)
 //    16 units of 80, 320, 1088            15.4, 16.2, 21.2 against 19.9, 20.2, 22.4
 //    64 units of 80, 320, 960             18.9, 22.5, 27.6 against 21.2, 22.9, 23.6

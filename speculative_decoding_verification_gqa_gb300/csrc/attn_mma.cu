@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) attn_mma_kernel(const AttnParams 
     const int D = SHARED ? part.rows - 1 : p.draft_len[b];
     // key tiles [j0, j1) of the sequence (tile j holds positions j*KT ..), out of the
     // unit's tiles [kb, kb + nt)
-    // (SHARED: the unit's first key is info.w itself, a multiple of the block size)
+    // (SHARED: the unit's first key is info.w itself, a multiple of min(block_size, KT))
     const int kb = SHARED ? 0 : info.w / KT;
     const int kofs = SHARED ? info.w : 0;
     const int j0 = kb + l0, j1 = kb + l1;

@@ -15,13 +15,18 @@
 //
 //   RT = 2  the prefixes. Units of 256 rows, all 512 columns, one CTA per SM: each 128-key
 //           K/V tile is read once for both row tiles, whose softmaxes alternate on the
-//           tensor cores. Bound by those: a step of both row tiles is 1152 clocks of MMAs,
-//           and takes 1150 to 1260; a unit's start and end take 9 to 12 thousand more.
+//           tensor cores. Bound by those in this layout: a step of both row tiles is 1152
+//           clocks of MMAs (bf16: 8 of the 16 score MMAs at 48 clocks, which with their half
+//           of Q in TMEM would take 32: 128 clocks of the 1152), and takes 1150 to 1260; a
+//           unit's start and end take 9 to 12 thousand more.
 //   RT = 1  the sequences behind them. Units of 128 rows, 256 columns, 64-key tiles, two
 //           independent lanes of work in a CTA (its halves, each with its own warps, shared
 //           memory, TMEM and range of the line): the units are short (a few hundred keys) and
-//           each starts with a read of Q and ends with one of O, which the other half's unit
-//           covers. Bound by the K/V stream.
+//           each starts with a read of Q and ends with a write of O, which the other half's
+//           unit covers. Bound by neither HBM (2.5 TB/s alone in the first case below) nor
+//           live tensor work: an MMA is issued for 128 rows however few of them live (36 at
+//           most there), 576 clocks for a step of 64 keys, so 10.4 of the 18.8 thousand clocks
+//           of a pair of units of nine tiles are MMAs, and 5.8 are starts and ends.
 // The two run at the same time, each on a share of the SMs that the plan chooses (the one is
 // bound by the tensor cores, the other by HBM): the sequences' kernel comes first, one CTA
 // per SM, those without a range leave at once, and the prefixes' CTAs take the SMs that are
@@ -37,10 +42,10 @@
 // for combine_shared. Every wait is bounded as in attn_tc.cu.
 //
 // Measured (one after another, cold caches): 64 sequences of up to 1024 own positions over a
-// prefix of 8192, Hq 32, Hkv 8, d 128, bf16: sequences 56 us (142 MB from HBM), prefixes 58 us
-// (36 MB, tensor pipe 60% busy); the whole call 66 us captured. 32 sequences of 16 rows over
-// two prefixes of 32768, Hq 64, E4M3: prefixes 343 us (148 MB, tensor pipe 76% busy), the
-// call 372 us, 1.5 PFLOP/s.
+// prefix of 8192, Hq 32, Hkv 8, d 128, bf16: sequences 55-57 us (142 MB from HBM), prefixes 57
+// us (36 MB, tensor pipe 61% busy); the whole call 65 us captured. 32 sequences of 16 rows over
+// two prefixes of 32768, Hq 64, E4M3: prefixes 339 us (148 MB, tensor pipe 78% busy), the
+// call 355-377 us (the power limit), 1.5 PFLOP/s.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

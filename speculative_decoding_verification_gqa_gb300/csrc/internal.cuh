@@ -95,7 +95,8 @@ inline AttnWs attn_ws_layout(int B, int Hkv, int G, int d, int max_draft, int n_
 // Shared prefixes (spec_verify_attn_shared): the keys of a call fall into parts, a group's
 // prefix and each sequence's own positions behind it. A part's units are (part, KV head,
 // row tile), its query rows the G * rows of consecutive window rows, so that a prefix is
-// read once per 128 rows of its whole group. A sequence's rows are then the join of two
+// read once per row tile (128 rows, or 256 on the tcgen05 kernels) of its whole group. A
+// sequence's rows are then the join of two
 // parts by the rule of the online softmax, except where its group's prefix is empty.
 // Parts 0 .. num_groups - 1 are the prefixes, part num_groups + b is sequence b.
 struct SharedSeq {

@@ -761,8 +761,10 @@ cudaError_t allow_set(F kernel, size_t bytes) {
                                                    (int)set_bytes(SV_MAX_TABLE_ROWS));
 }
 
-// Resident at once, 8 CTAs of AT threads an SM; an odd number, so that what repeats along the
-// items (every other row dropped, say) falls to all CTAs.
+// Up to 8 CTAs of AT threads for each SM; an odd number, so that what repeats along the items
+// (every other row dropped, say) falls to all CTAs. Not all of them are resident at once: the
+// registers of the copying kernels let 6 onto an SM and those of fork and trim 5, a table of
+// 2^20 rows one.
 unsigned grid_for(int64_t items, int sms) {
   const int64_t most = ((int64_t)sms * (2048 / AT) - 1) | 1;
   return (unsigned)(items < 1 ? 1 : items < most ? items : most);
