@@ -71,7 +71,7 @@ typedef enum {
   SV_ERR_NO_PAGES = 9      /* too few free pages (sv_workspace_status, spec_pages_extend) */
 } sv_status;
 
-typedef enum { SV_BF16 = 0, SV_FP8_E4M3 = 1, SV_FP32 = 2 } sv_dtype;
+typedef enum { SV_BF16 = 0, SV_FP8_E4M3 = 1, SV_FP32 = 2, SV_KV4 = 3 /* 4 bits: sv_kv4_pages */ } sv_dtype;
 
 /* Shape of one spec_verify_attn call. */
 typedef struct {
@@ -84,7 +84,8 @@ typedef struct {
   int64_t q_rows;         /* rows allocated in q and out, >= sum_b (1 + D_b) */
   int64_t kv_rows;        /* rows allocated in k_cache and v_cache, >= sum_b (T_b+1+D_b),
                              <= 2^31 - 1025 */
-  int32_t kv_dtype;       /* SV_BF16, or SV_FP8_E4M3 (OCP E4M3 codes) */
+  int32_t kv_dtype;       /* SV_BF16, or SV_FP8_E4M3 (OCP E4M3 codes); SV_KV4 for
+                             spec_verify_attn_kv4 and spec_attn_mass only */
   float softmax_scale;    /* scale on q.k; 0 selects 1/sqrt(head_dim) */
   int32_t sliding_window; /* 0: every earlier key; W >= 1: sliding-window attention over
                              the W most recent positions (see spec_verify_attn) */
@@ -344,6 +345,159 @@ SV_API sv_status spec_pages_compact(const sv_page_table* table, int32_t num_pool
                                     const sv_page_data* pools, int32_t* remap, int32_t* num_live,
                                     void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * A paged K/V cache held in 4 bits ("GPU and LLM, chapter 5", "PagedAttention (2)", for the
+ * pages). Every row (position, KV head) of head_dim elements is kept as E2M1 codes with an
+ * E4M3 scale for each 16 consecutive elements: an element stands for
+ *   kv_scale[K or V, head] * e4m3(its block's scale) * e2m1(its code),
+ * E2M1 being +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}. 4.5 bits an element.
+ *   k_codes, v_codes  [num_blocks, block_size, num_kv_heads, head_dim / 2] bytes, 16-byte
+ *                     aligned; byte i of a row holds element 2 i in its low four bits and
+ *                     2 i + 1 in its high ones
+ *   scales            E4M3 [num_blocks, block_size, num_kv_heads, 2, head_dim / 16], 16-byte
+ *                     aligned: K's block scales, then V's
+ *   kv_scale          fp32 [2, num_kv_heads], in [2^-100, 2^100] (row 0 K, row 1 V), such as
+ *                     the head's largest magnitude / (6 * 448)
+ * All three arrays move and are shared as pools of the spec_pages_ calls and spec_kv_evict
+ * (whose pages need whole 16 bytes a position: with head_dim 64 an even number of heads).
+ */
+typedef struct {
+  int64_t num_blocks;   /* >= 1; times block_size <= 2^31 - 1025 */
+  int32_t block_size;   /* positions per page: a power of two in [8, 65536] */
+  int32_t num_kv_heads; /* 1 .. 4096 */
+  int32_t head_dim;     /* 64 or 128 */
+  void* k_codes;
+  void* v_codes;
+  void* scales;
+  const float* kv_scale;
+} sv_kv4_pages;
+
+/* Bytes of workspace spec_kv4_write and spec_kv4_read need. 0 if batch < 0. */
+SV_API size_t spec_kv4_workspace_size(int32_t batch);
+
+/*
+ * spec_kv4_write -- rounds bf16 K and V rows into the pages: the window of a verification step
+ * (start = T_b, count = 1 + D_b) or a prompt (start = 0), before attention reads them.
+ * The packed rows of sequence b (count[b] of them, sequences back to back) go to positions
+ * start[b] .. start[b] + count[b] - 1 of its block-table row. For a block x of 16 elements and
+ * its head's scale s,
+ *   c = the E4M3 value nearest to max |x| / (6 s), at most 448,
+ *   each code the E2M1 value nearest to x_k / (s c), at most 6 in magnitude (0 if c = 0),
+ * nearest to the real quotients, ties to the even code. A block that holds an infinity or a
+ * NaN gets the scale NaN, and all of it reads as NaN.
+ *   block_table  int32 [batch, max_blocks_per_seq]
+ *   start, count int32 [batch], >= 0
+ *   rows         rows allocated in k and v, >= the sum of count; rows past the sum are not read
+ *   k, v         bf16, row r's [Hkv, head_dim] at element r * k_row_stride (v_row_stride), a
+ *                multiple of 8 and at least Hkv * head_dim (a slice of a fused projection);
+ *                16-byte aligned
+ * A start or count out of range is reported by sv_workspace_status (SV_ERR_DEVICE_SHAPE) and
+ * nothing is written; a row whose table entry names no page of the pool is reported and
+ * skipped. No two rows of a call may go to the same position of a page.
+ */
+SV_API sv_status spec_kv4_write(const sv_kv4_pages* pages, int32_t batch,
+                                const int32_t* block_table, int32_t max_blocks_per_seq,
+                                const int32_t* start, const int32_t* count, int64_t rows,
+                                const void* k, int64_t k_row_stride, const void* v,
+                                int64_t v_row_stride, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
+ * spec_kv4_read -- the rows at positions start[b] .. start[b] + count[b] - 1 of every sequence
+ * as bf16 (for a prefill that attends over the rounded rows, or to move a sequence to another
+ * cache). Arguments as for spec_kv4_write, with
+ *   k_out, v_out  bf16 [rows, Hkv, head_dim], 16-byte aligned; rows past the sum of count are
+ *                 left as they were, and a row whose table entry names no page reads as zeros
+ */
+SV_API sv_status spec_kv4_read(const sv_kv4_pages* pages, int32_t batch,
+                               const int32_t* block_table, int32_t max_blocks_per_seq,
+                               const int32_t* start, const int32_t* count, int64_t rows,
+                               void* k_out, void* v_out, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* Bytes of workspace spec_verify_attn_kv4 needs on the current CUDA device, for a descriptor
+ * with kv_dtype SV_KV4. 0 if invalid. */
+SV_API size_t spec_verify_attn_kv4_workspace_size(const sv_attn_desc* desc);
+
+/*
+ * spec_verify_attn_kv4 -- spec_verify_attn_paged over a 4-bit cache: the result is that of the
+ * values which the codes stand for (sliding window, table entries and device-side checks as
+ * there), computed on the codes: nothing of K or V is expanded in memory.
+ *   desc  kv_dtype SV_KV4; num_kv_heads and head_dim those of the pages; kv_rows is ignored
+ *   lse   fp32 [q_rows, Hq] or NULL: out, ln of the row's sum of exp(scale * q.k), for
+ *         spec_attn_mass; only the sum_b W_b packed rows are written
+ */
+SV_API sv_status spec_verify_attn_kv4(const sv_attn_desc* desc, const void* q,
+                                      const sv_kv4_pages* pages, const int32_t* block_table,
+                                      int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                      const int32_t* draft_len, void* out, float* lse,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace spec_attn_mass needs on the current CUDA device. 0 if invalid. */
+SV_API size_t spec_attn_mass_workspace_size(const sv_attn_desc* desc);
+
+/*
+ * spec_attn_mass -- adds up the attention weight that each cached position gets, per sequence
+ * and KV head: the measure by which spec_kv_evict chooses. For the first n_b window rows of
+ * sequence b (row_count[b]: after acceptance, accept_len[b]) and every position j,
+ *   mass[b, g, j] += sum over query heads h of group g and rows i < n_b with j <= T_b + i of
+ *                    exp(scale * q[i, h].K[j, g] - lse[i, h])
+ * Positions from T_b + n_b on are left as they were. The same bits every time. The whole prefix
+ * is counted (no sliding window: desc->sliding_window must be 0).
+ *   desc       as for spec_verify_attn_paged; kv_dtype SV_BF16, SV_FP8_E4M3 or SV_KV4
+ *   k_pages    the K pool (for SV_KV4 its codes)
+ *   scales     SV_KV4: the block scales of sv_kv4_pages; NULL otherwise
+ *   kv_scale   fp32 [2, Hkv] (row 0, K's, is read); NULL for SV_BF16
+ *   row_count  int32 [B], 0 <= row_count[b] <= 1 + D_b, or NULL: all rows
+ *   lse        fp32 [q_rows, Hq], such as spec_verify_attn_kv4 leaves, or NULL: the call works
+ *              it out, in a first pass over the keys (of the counted rows only)
+ *   mass       fp32 [B, Hkv, mass_stride], in and out; T_b + 1 + D_b <= mass_stride
+ * Lengths out of range are reported by sv_workspace_status (SV_ERR_DEVICE_SHAPE) and leave
+ * mass as it was; a table entry that names no page reads as zeros and is reported.
+ */
+SV_API sv_status spec_attn_mass(const sv_attn_desc* desc, const void* q, const void* k_pages,
+                                const void* scales, const float* kv_scale, int64_t num_blocks,
+                                int32_t block_size, const int32_t* block_table,
+                                int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                const int32_t* draft_len, const int32_t* row_count,
+                                const float* lse, float* mass, int64_t mass_stride,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+#define SV_MAX_EVICT_ROWS (1 << 16)
+/* Bytes of workspace spec_kv_evict needs for n rows. 0 if invalid. */
+SV_API size_t spec_kv_evict_workspace_size(int32_t n, int32_t num_kv_heads, int64_t mass_stride);
+
+/*
+ * spec_kv_evict -- cuts rows of a paged cache to a budget, each KV head by itself: row r =
+ * rows[i] with N = cached_len[r] positions keeps, of head g, its first keep_first[i] and its
+ * last keep_last positions and, of those between, the new_len[i] - keep_first[i] - keep_last of
+ * largest mass[r, g, :] (ties: the lowest position; NaN counts as least). In ascending order
+ * they become positions 0 .. new_len[i] - 1 of the row in every pool, and their mass goes with
+ * them; mass[r, g, new_len[i] .. N - 1] becomes 0. Rows with new_len[i] = N stay as they are.
+ * One call for each layer (its pools and its mass); after the last, spec_pages_trim to new_len
+ * sets cached_len and frees the pages. What a page holds past new_len[i] is left over.
+ *   rows        int32 [n], each row once, or NULL: rows 0 .. n - 1; n <= table_rows and
+ *               SV_MAX_EVICT_ROWS
+ *   new_len     int32 [n], 0 <= new_len[i] <= N; keep_first[i] + keep_last <= new_len[i] < N, or
+ *               new_len[i] = N
+ *   keep_first  int32 [n] (a shared prefix, say) or NULL: 0
+ *   mass        fp32 [table_rows, num_kv_heads, mass_stride], in and out; N <= mass_stride
+ *   kept        int32 [n, num_kv_heads, kept_stride] or NULL: out, the position that each new
+ *               position was; new_len[i] <= kept_stride; entries past new_len[i] are left
+ *   pools       HOST array, as for spec_pages_extend: [num_blocks, block_size, num_kv_heads,
+ *               any number of bytes that is a multiple of 8]
+ * The pages that hold positions keep_first[i] .. new_len[i] - 1 must be the row's alone (count
+ * 1). All rows are checked on the device before anything but kept is changed; a call that fails
+ * a check changes nothing else and sets the workspace flag (SV_ERR_DEVICE_SHAPE). The workspace
+ * serves later calls of any sizes that it is large enough for.
+ */
+SV_API sv_status spec_kv_evict(const sv_page_table* table, int32_t n, const int32_t* rows,
+                               const int32_t* new_len, const int32_t* keep_first,
+                               int32_t keep_last, int32_t num_kv_heads, float* mass,
+                               int64_t mass_stride, int32_t* kept, int64_t kept_stride,
+                               int32_t num_pools, const sv_page_data* pools, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 /* Bytes of workspace spec_accept needs on the current CUDA device. 0 if invalid. */
 SV_API size_t spec_accept_workspace_size(int32_t batch, int32_t max_draft_len, int32_t vocab);
 
@@ -586,8 +740,10 @@ SV_API void sv_set_profile_events(void* start_event, void* stop_event);
  * returns SV_ERR_CUDA (spec_verify_attn and the paged call launch three kernels in this
  * order: plan, attention, combine; the host-lengths call attention and combine; the
  * shared-prefix call plan, sequences, prefixes, combine, or with the mma.sync kernel plan,
- * attention, combine; spec_accept, spec_draft_signals, spec_pages_fork and _trim one each;
- * spec_pages_extend two; spec_pages_compact two, three beyond 4096 pages). The call's earlier launches have run;
+ * attention, combine; the 4-bit call plan, attention, combine; spec_accept, spec_draft_signals,
+ * spec_pages_fork and _trim, spec_kv4_write and _read one each; spec_pages_extend and
+ * spec_kv_evict two; spec_attn_mass one, three without lse; spec_pages_compact two, three beyond
+ * 4096 pages). The call's earlier launches have run;
  * its outputs are then unspecified, and its workspace serves the next call as it is. One
  * failure per arming; after < 0 disarms. Returns the launches that were still to go
  * before a pending failure, or -1 if none was pending. Process-wide. */

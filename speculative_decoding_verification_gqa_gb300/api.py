@@ -13,6 +13,10 @@ include/specverify.h:
   attended once per group.
 * ``spec_pages_fork``, ``spec_pages_extend``, ``spec_pages_trim``, ``spec_pages_compact`` --
   the block tables and pages of a paged cache (shared pages, copy on write).
+* ``spec_kv4_write``, ``spec_kv4_read``, ``spec_verify_attn_kv4`` -- a paged cache held in 4
+  bits: rows rounded into its pages, read back, and verify attention over them.
+* ``spec_attn_mass``, ``spec_kv_evict`` -- the attention weight that each cached position got,
+  added up, and eviction of the positions with the least.
 * ``spec_accept`` -- greedy acceptance (argmax per window row, first mismatch).
 * ``spec_accept_stochastic`` -- distribution-preserving acceptance for sampled decoding.
 """
@@ -30,7 +34,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libspecverify.so")
 
-SV_BF16, SV_FP8_E4M3, SV_FP32 = 0, 1, 2
+SV_BF16, SV_FP8_E4M3, SV_FP32, SV_KV4 = 0, 1, 2, 3
 STATUS = {0: "SV_OK", 1: "SV_ERR_NULL", 2: "SV_ERR_SHAPE", 3: "SV_ERR_DTYPE",
           4: "SV_ERR_ALIGN", 5: "SV_ERR_WORKSPACE", 6: "SV_ERR_CUDA", 7: "SV_ERR_TIMEOUT",
           8: "SV_ERR_DEVICE_SHAPE", 9: "SV_ERR_NO_PAGES"}
@@ -46,7 +50,11 @@ EXPORTS = ("spec_verify_attn_workspace_size", "spec_verify_attn", "spec_verify_a
            "spec_accept_stochastic",
            "spec_verify_attn_shared_workspace_size", "spec_verify_attn_shared",
            "spec_pages_workspace_size", "spec_pages_fork", "spec_pages_extend",
-           "spec_pages_trim", "spec_pages_compact")
+           "spec_pages_trim", "spec_pages_compact",
+           "spec_kv4_workspace_size", "spec_kv4_write", "spec_kv4_read",
+           "spec_verify_attn_kv4_workspace_size", "spec_verify_attn_kv4",
+           "spec_attn_mass_workspace_size", "spec_attn_mass",
+           "spec_kv_evict_workspace_size", "spec_kv_evict")
 
 
 class SpecVerifyError(RuntimeError):
@@ -79,6 +87,13 @@ class PageTable(ctypes.Structure):
 
 class PageData(ctypes.Structure):
     _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64)]
+
+
+class Kv4Pages(ctypes.Structure):
+    _fields_ = [("num_blocks", ctypes.c_int64), ("block_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("kv_scale", ctypes.c_void_p)]
 
 
 MAX_PAGE_POOLS = 256
@@ -153,6 +168,27 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.spec_pages_trim.restype = ctypes.c_int
         lib.spec_pages_compact.argtypes = [pt, i32, vp, vp, vp, vp, sz, vp]
         lib.spec_pages_compact.restype = ctypes.c_int
+        k4, ad = ctypes.POINTER(Kv4Pages), ctypes.POINTER(AttnDesc)
+        lib.spec_kv4_workspace_size.argtypes = [i32]
+        lib.spec_kv4_workspace_size.restype = sz
+        lib.spec_kv4_write.argtypes = [k4, i32, vp, i32, vp, vp, i64, vp, i64, vp, i64, vp, sz, vp]
+        lib.spec_kv4_write.restype = ctypes.c_int
+        lib.spec_kv4_read.argtypes = [k4, i32, vp, i32, vp, vp, i64, vp, vp, vp, sz, vp]
+        lib.spec_kv4_read.restype = ctypes.c_int
+        lib.spec_verify_attn_kv4_workspace_size.argtypes = [ad]
+        lib.spec_verify_attn_kv4_workspace_size.restype = sz
+        lib.spec_verify_attn_kv4.argtypes = [ad, vp, k4, vp, i32, vp, vp, vp, vp, vp, sz, vp]
+        lib.spec_verify_attn_kv4.restype = ctypes.c_int
+        lib.spec_attn_mass_workspace_size.argtypes = [ad]
+        lib.spec_attn_mass_workspace_size.restype = sz
+        lib.spec_attn_mass.argtypes = [ad, vp, vp, vp, vp, i64, i32, vp, i32, vp, vp, vp, vp, vp,
+                                       i64, vp, sz, vp]
+        lib.spec_attn_mass.restype = ctypes.c_int
+        lib.spec_kv_evict_workspace_size.argtypes = [i32, i32, i64]
+        lib.spec_kv_evict_workspace_size.restype = sz
+        lib.spec_kv_evict.argtypes = [pt, i32, vp, vp, vp, i32, i32, vp, i64, vp, i64, i32, vp, vp,
+                                      sz, vp]
+        lib.spec_kv_evict.restype = ctypes.c_int
         lib.sv_inject_launch_failure.argtypes = [ctypes.c_int]
         lib.sv_inject_launch_failure.restype = ctypes.c_int
         lib.sv_inject_wait_timeout.argtypes = [ctypes.c_int64]
@@ -605,6 +641,281 @@ def spec_pages_compact(ref_count, block_table, cached_len, *, block_size: int, p
         ws.numel(), _stream_on(stream, dev))
     if st:
         _check(st, "spec_pages_compact")
+
+
+_U8 = (torch.uint8,)
+_SCALES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def paged_attn_desc(q: torch.Tensor, k_pages: torch.Tensor, batch: int, max_draft_len: int,
+                    max_seq_len: int, softmax_scale: float = 0.0, sliding_window: int = 0, *,
+                    kv4: bool = False) -> AttnDesc:
+    """The descriptor of a call over K pages [num_blocks, block_size, Hkv, d] (``kv4``: 4-bit
+    codes, [num_blocks, block_size, Hkv, d / 2])."""
+    nb, bs, hkv, _ = k_pages.shape
+    dt = SV_KV4 if kv4 else SV_BF16 if k_pages.dtype == torch.bfloat16 else SV_FP8_E4M3
+    return AttnDesc(batch, q.shape[1], hkv, q.shape[2], max_draft_len, max_seq_len, q.shape[0],
+                    nb * bs, dt, float(softmax_scale), int(sliding_window))
+
+
+def _workspace_bytes(name: str, *args) -> int:
+    n = getattr(_lib or load_library(), name)(*args)
+    if n == 0:
+        raise SpecVerifyError(2, name)
+    return n
+
+
+def kv4_workspace_bytes(batch: int) -> int:
+    return _workspace_bytes("spec_kv4_workspace_size", batch)
+
+
+def verify_kv4_workspace_bytes(desc: AttnDesc) -> int:
+    return _workspace_bytes("spec_verify_attn_kv4_workspace_size", ctypes.byref(desc))
+
+
+def mass_workspace_bytes(desc: AttnDesc) -> int:
+    return _workspace_bytes("spec_attn_mass_workspace_size", ctypes.byref(desc))
+
+
+def evict_workspace_bytes(n: int, num_kv_heads: int, max_positions: int) -> int:
+    """``max_positions``: positions of mass, its last dimension."""
+    return _workspace_bytes("spec_kv_evict_workspace_size", n, num_kv_heads, max_positions)
+
+
+def _kv4_pages(k_codes, v_codes, scales, kv_scale, devs) -> Kv4Pages:
+    """The C descriptor of a 4-bit cache, its tensors' devices added to ``devs``."""
+    devs += [_dev(k_codes, "k_codes", _U8), _dev(v_codes, "v_codes", _U8),
+             _dev(scales, "scales", _SCALES), _dev(kv_scale, "kv_scale", (torch.float32,))]
+    if k_codes.dim() != 4 or v_codes.shape != k_codes.shape:
+        raise ValueError("k_codes and v_codes must be [num_blocks, block_size, Hkv, d / 2]")
+    nb, bs, hkv, half = k_codes.shape
+    if scales.shape != (nb, bs, hkv, 2, half // 8):
+        raise ValueError("scales must be [num_blocks, block_size, Hkv, 2, d / 16]")
+    if kv_scale.shape != (2, hkv):
+        raise ValueError("kv_scale must be [2, Hkv]")
+    return Kv4Pages(nb, bs, hkv, 2 * half, k_codes.data_ptr(), v_codes.data_ptr(),
+                    scales.data_ptr(), kv_scale.data_ptr())
+
+
+def _kv4_rows(block_table, start, count, devs, workspace, stream):
+    """The checks that spec_kv4_write and spec_kv4_read share: (batch, workspace, device)."""
+    devs += [_dev(block_table, "block_table", _I32), _dev(start, "start", _I32),
+             _dev(count, "count", _I32)]
+    B = start.numel()
+    if start.dim() != 1 or count.shape != (B,) or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("start and count must be [B], block_table [B, max_blocks]")
+    if workspace is not None:
+        devs.append(_dev(workspace, "workspace", _U8))
+    dev = _one_device(devs)
+    if workspace is None:
+        with _allocating_on(stream, dev):
+            workspace = new_workspace(kv4_workspace_bytes(B), start.device)
+    return B, workspace, dev
+
+
+def _row_stride(t, name, hkv, d, rows):
+    """Elements between the rows of t [rows, Hkv, d], whose heads lie side by side."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s has dtype %s, expected torch.bfloat16" % (name, t.dtype))
+    if t.dim() != 3 or t.shape[1:] != (hkv, d) or (rows is not None and t.shape[0] != rows):
+        raise ValueError("k and v must be [rows, Hkv, d] of the pages' heads")
+    if (d > 1 and t.stride(2) != 1) or (hkv > 1 and t.stride(1) != d):
+        raise ValueError("%s: a row's heads must be contiguous (rows may be apart)" % name)
+    if t.shape[0] <= 1:
+        return hkv * d
+    if t.stride(0) < hkv * d:
+        raise ValueError("%s: rows must not overlap" % name)
+    return t.stride(0)
+
+
+def spec_kv4_write(k, v, k_codes, v_codes, scales, kv_scale, block_table, start, count, *,
+                   workspace=None, stream=None) -> None:
+    """Round bf16 rows k, v [rows, Hkv, d] (rows may lie apart, as in a fused projection) into
+    the pages of a 4-bit cache: the count[b] rows of sequence b, packed in batch order, go to
+    positions start[b] .. of row b of block_table (int32 [B, max_blocks]; start, count int32
+    [B]). Changed in place: k_codes, v_codes uint8 [num_blocks, block_size, Hkv, d / 2] and
+    scales (uint8 or float8_e4m3fn) [num_blocks, block_size, Hkv, 2, d / 16]; kv_scale fp32
+    [2, Hkv] is the caller's."""
+    devs = []
+    pages = _kv4_pages(k_codes, v_codes, scales, kv_scale, devs)
+    ks = _row_stride(k, "k", pages.num_kv_heads, pages.head_dim, None)
+    vs = _row_stride(v, "v", pages.num_kv_heads, pages.head_dim, k.shape[0])
+    devs += [k.get_device(), v.get_device()]
+    B, workspace, dev = _kv4_rows(block_table, start, count, devs, workspace, stream)
+    st = (_lib or load_library()).spec_kv4_write(
+        ctypes.byref(pages), B, block_table.data_ptr(), block_table.shape[1], start.data_ptr(),
+        count.data_ptr(), k.shape[0], k.data_ptr(), ks, v.data_ptr(), vs, workspace.data_ptr(),
+        workspace.numel(), _stream_on(stream, dev))
+    if st:
+        _check(st, "spec_kv4_write")
+
+
+def spec_kv4_read(k_codes, v_codes, scales, kv_scale, block_table, start, count, *, rows=None,
+                  k_out=None, v_out=None, workspace=None, stream=None):
+    """The rows at positions start[b] .. start[b] + count[b] - 1 of every sequence of a 4-bit
+    cache, packed in batch order: (k, v) bf16 [rows, Hkv, d]. ``rows`` (at least the sum of
+    count) is needed where k_out and v_out are not given; rows past the sum are left as they
+    were (zeros in outputs made here)."""
+    devs = []
+    pages = _kv4_pages(k_codes, v_codes, scales, kv_scale, devs)
+    shape = (pages.num_kv_heads, pages.head_dim)
+    outs = [k_out, v_out]
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None:
+            devs.append(_dev(t, name, (torch.bfloat16,)))
+            rows = t.shape[0] if rows is None and t.dim() == 3 else rows
+            if t.shape != (rows, *shape):
+                raise ValueError("%s must be [rows, Hkv, d] of the pages' heads" % name)
+    if rows is None:
+        raise ValueError("rows, or k_out and v_out, must be given")
+    B, workspace, dev = _kv4_rows(block_table, start, count, devs, workspace, stream)
+    if k_out is None or v_out is None:
+        with _allocating_on(stream, dev):
+            for i in range(2):
+                if outs[i] is None:
+                    outs[i] = torch.zeros(rows, *shape, dtype=torch.bfloat16, device=k_codes.device)
+    st = (_lib or load_library()).spec_kv4_read(
+        ctypes.byref(pages), B, block_table.data_ptr(), block_table.shape[1], start.data_ptr(),
+        count.data_ptr(), rows, outs[0].data_ptr(), outs[1].data_ptr(), workspace.data_ptr(),
+        workspace.numel(), _stream_on(stream, dev))
+    if st:
+        _check(st, "spec_kv4_read")
+    return tuple(outs)
+
+
+def spec_verify_attn_kv4(q, k_codes, v_codes, scales, kv_scale, block_table, seq_lens, draft_len, *,
+                         max_draft_len: int, max_seq_len: int, out=None, lse=None, workspace=None,
+                         softmax_scale: float = 0.0, sliding_window: int = 0,
+                         stream=None) -> torch.Tensor:
+    """spec_verify_attn_paged over a 4-bit cache (see spec_kv4_write). Fills ``lse`` (fp32
+    [rows, Hq]: the natural log of each row's sum of exponentials) when it is given."""
+    devs = [_dev(q, "q", (torch.bfloat16,)), _dev(block_table, "block_table", _I32),
+            _dev(seq_lens, "seq_lens", _I32), _dev(draft_len, "draft_len", _I32)]
+    pages = _kv4_pages(k_codes, v_codes, scales, kv_scale, devs)
+    B = seq_lens.numel()
+    if q.dim() != 3 or q.shape[2] != pages.head_dim:
+        raise ValueError("q must be [rows, Hq, d] with the pages' d")
+    if seq_lens.dim() != 1 or draft_len.shape != (B,) or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("seq_lens and draft_len must be [B], block_table [B, max_blocks]")
+    desc = paged_attn_desc(q, k_codes, B, max_draft_len, max_seq_len, softmax_scale, sliding_window,
+                           kv4=True)
+    if out is not None:
+        devs.append(_dev(out, "out", (torch.bfloat16,)))
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    if lse is not None:
+        devs.append(_dev(lse, "lse", (torch.float32,)))
+        if lse.shape != q.shape[:2]:
+            raise ValueError("lse must be [rows, Hq]")
+    if workspace is not None:
+        devs.append(_dev(workspace, "workspace", _U8))
+    dev = _one_device(devs)
+    if out is None or workspace is None:
+        with _allocating_on(stream, dev):
+            if out is None:
+                out = torch.empty_like(q)
+            if workspace is None:
+                workspace = new_workspace(verify_kv4_workspace_bytes(desc), q.device)
+    st = (_lib or load_library()).spec_verify_attn_kv4(
+        ctypes.byref(desc), q.data_ptr(), ctypes.byref(pages), block_table.data_ptr(),
+        block_table.shape[1], seq_lens.data_ptr(), draft_len.data_ptr(), out.data_ptr(),
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
+        _stream_on(stream, dev))
+    if st:
+        _check(st, "spec_verify_attn_kv4")
+    return out
+
+
+def spec_attn_mass(q, k_pages, block_table, seq_lens, draft_len, mass, *, max_draft_len: int,
+                   max_seq_len: int, kv_scale=None, scales=None, lse=None, row_count=None,
+                   softmax_scale: float = 0.0, workspace=None, stream=None) -> torch.Tensor:
+    """Add to mass (fp32 [B, Hkv, positions], in place) the attention weight that the first
+    row_count[b] window rows of each sequence (int32 [B]: after acceptance, its accept_len;
+    None: all) give to every position, summed over rows and a KV head's query heads. k_pages as
+    for spec_verify_attn_paged, or 4-bit codes with their block ``scales``. ``lse`` (fp32
+    [rows, Hq], as spec_verify_attn_kv4 leaves it) spares the call a pass over the keys.
+    Returns mass."""
+    kv4 = scales is not None
+    devs = [_dev(q, "q", (torch.bfloat16,)), _dev(k_pages, "k_pages", _U8 if kv4 else _KV),
+            _dev(block_table, "block_table", _I32), _dev(seq_lens, "seq_lens", _I32),
+            _dev(draft_len, "draft_len", _I32), _dev(mass, "mass", (torch.float32,))]
+    if q.dim() != 3 or k_pages.dim() != 4:
+        raise ValueError("q must be [rows, Hq, d], k_pages [num_blocks, block_size, Hkv, d]")
+    nb, bs, hkv, dk = k_pages.shape
+    B, d = seq_lens.numel(), q.shape[2]
+    if dk * (2 if kv4 else 1) != d:
+        raise ValueError("q and the pages must have one head dimension")
+    if seq_lens.dim() != 1 or draft_len.shape != (B,) or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("seq_lens and draft_len must be [B], block_table [B, max_blocks]")
+    if mass.dim() != 3 or mass.shape[:2] != (B, hkv):
+        raise ValueError("mass must be [B, Hkv, positions]")
+    ptr = {}
+    for name, t, dt, shape in (("kv_scale", kv_scale, (torch.float32,), (2, hkv)),
+                               ("scales", scales, _SCALES, (nb, bs, hkv, 2, d // 16)),
+                               ("lse", lse, (torch.float32,), tuple(q.shape[:2])),
+                               ("row_count", row_count, _I32, (B,))):
+        ptr[name] = None
+        if t is not None:
+            devs.append(_dev(t, name, dt))
+            if tuple(t.shape) != shape:
+                raise ValueError("%s must be %s" % (name, list(shape)))
+            ptr[name] = t.data_ptr()
+    desc = paged_attn_desc(q, k_pages, B, max_draft_len, max_seq_len, softmax_scale, kv4=kv4)
+    if workspace is not None:
+        devs.append(_dev(workspace, "workspace", _U8))
+    dev = _one_device(devs)
+    if workspace is None:
+        with _allocating_on(stream, dev):
+            workspace = new_workspace(mass_workspace_bytes(desc), q.device)
+    st = (_lib or load_library()).spec_attn_mass(
+        ctypes.byref(desc), q.data_ptr(), k_pages.data_ptr(), ptr["scales"], ptr["kv_scale"], nb, bs,
+        block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), draft_len.data_ptr(),
+        ptr["row_count"], ptr["lse"], mass.data_ptr(), mass.shape[2], workspace.data_ptr(),
+        workspace.numel(), _stream_on(stream, dev))
+    if st:
+        _check(st, "spec_attn_mass")
+    return mass
+
+
+def spec_kv_evict(ref_count, block_table, cached_len, rows, new_len, mass, *, block_size: int,
+                  pools, keep_first=None, keep_last: int = 0, kept=None, workspace=None,
+                  stream=None) -> None:
+    """Cut row r = rows[i] (None: rows 0 .. n - 1) to new_len[i] positions, each KV head by
+    itself: its first keep_first[i] (int32 [n] or None) and last keep_last stay, and of the rest
+    those of largest mass (fp32 [rows, Hkv, positions]). They move to the front of the row's
+    pages in every pool ([num_blocks, block_size, Hkv, ...]), and mass with them, in place.
+    Fills ``kept`` (int32 [n, Hkv, k]: which position each was). Call it once a layer, then
+    spec_pages_trim with the same rows and new_len."""
+    pools = _as_pools(pools)
+    if mass.dim() != 3 or mass.shape[0] != cached_len.numel():
+        raise ValueError("mass must be [rows, Hkv, positions]")
+    hkv, n = mass.shape[1], new_len.numel()
+    for t in pools.tensors:
+        if t.dim() < 3 or t.shape[2] != hkv:
+            raise ValueError("a pool must be [num_blocks, block_size, Hkv, ...] with mass's Hkv")
+    devs = [_dev(mass, "mass", (torch.float32,))]
+    stride = 0
+    if kept is not None:
+        devs.append(_dev(kept, "kept", _I32))
+        if kept.dim() != 3 or kept.shape[:2] != (n, hkv):
+            raise ValueError("kept must be [n, Hkv, k]")
+        stride = kept.shape[2]
+    if workspace is None:
+        with _allocating_on(stream, _one_device(devs)):
+            workspace = new_workspace(evict_workspace_bytes(n, hkv, mass.shape[2]), mass.device)
+    t, ws, dev = _page_table(ref_count, block_table, cached_len, block_size,
+                             (("new_len", new_len), ("rows", rows), ("keep_first", keep_first)),
+                             pools, workspace, stream)
+    _one_device(devs + [dev])
+    st = (_lib or load_library()).spec_kv_evict(
+        ctypes.byref(t), n, None if rows is None else rows.data_ptr(), new_len.data_ptr(),
+        None if keep_first is None else keep_first.data_ptr(), keep_last, hkv, mass.data_ptr(),
+        mass.shape[2], None if kept is None else kept.data_ptr(), stride, len(pools.tensors),
+        pools.array, ws.data_ptr(), ws.numel(), _stream_on(stream, dev))
+    if st:
+        _check(st, "spec_kv_evict")
 
 
 def spec_accept(logits, draft_tokens, draft_len, *, max_draft_len: int, accept_len=None,

@@ -129,7 +129,7 @@ SV_API int sv_inject_wait_timeout(int64_t limit_cycles) {
   return g_stall_limit.exchange(limit_cycles > 0 ? (long long)limit_cycles : 0) > 0 ? 1 : 0;
 }
 
-SV_API int sv_version(void) { return 500; }  // 0.5.0: shared prefixes, pages of a paged cache
+SV_API int sv_version(void) { return 600; }  // 0.6.0: 4-bit caches, attention mass, eviction
 
 SV_API const char* sv_status_string(sv_status s) {
   switch (s) {
@@ -731,6 +731,295 @@ SV_API sv_status spec_pages_compact(const sv_page_table* table, int32_t num_pool
              ? SV_OK
              : SV_ERR_CUDA;
 }
+
+}  // extern "C"
+
+namespace {
+
+// Whether [a, a + na) and [b, b + nb) share a byte (null arrays share none).
+bool meet(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && x < y + nb && y < x + na;
+}
+
+sv_status check_kv4(const sv_kv4_pages* p) {
+  if (!p) return SV_ERR_NULL;
+  if (p->num_blocks < 1 || p->num_blocks > 0x7fffffff ||
+      !pool_sizes_ok((int32_t)p->num_blocks, p->block_size) || p->num_kv_heads < 1 ||
+      p->num_kv_heads > 4096 || (p->head_dim != 64 && p->head_dim != 128))
+    return SV_ERR_SHAPE;
+  if (!p->k_codes || !p->v_codes || !p->scales || !p->kv_scale) return SV_ERR_NULL;
+  if (!aligned(p->k_codes, 16) || !aligned(p->v_codes, 16) || !aligned(p->scales, 16) ||
+      !aligned(p->kv_scale, 4))
+    return SV_ERR_ALIGN;
+  return SV_OK;
+}
+
+sv_status check_kv4_rows(const sv_kv4_pages* p, int32_t batch, const int32_t* table,
+                         int32_t max_blocks, const int32_t* start, const int32_t* count,
+                         int64_t rows, const void* k, const void* v, void* ws, size_t ws_bytes) {
+  const sv_status st = check_kv4(p);
+  if (st != SV_OK) return st;
+  // (a CTA takes a row or more: the grid's limit, with room to spare)
+  if (batch < 0 || max_blocks < 1 || rows < 0 || rows > 0x7fffffff) return SV_ERR_SHAPE;
+  if (batch == 0) return SV_OK;
+  if (!table || !start || !count || !ws || (rows > 0 && (!k || !v))) return SV_ERR_NULL;
+  if (!aligned(table, 4) || !aligned(start, 4) || !aligned(count, 4) || !aligned(k, 16) ||
+      !aligned(v, 16) || !aligned(ws, 256))
+    return SV_ERR_ALIGN;
+  return ws_bytes < spec_kv4_workspace_size(batch) ? SV_ERR_WORKSPACE : SV_OK;
+}
+
+// The pages' arrays and one that a call reads or writes: apart?
+bool kv4_apart(const sv_kv4_pages* p, const void* at, size_t bytes) {
+  const size_t rows = (size_t)p->num_blocks * p->block_size * p->num_kv_heads;
+  return !meet(p->k_codes, rows * (p->head_dim / 2), at, bytes) &&
+         !meet(p->v_codes, rows * (p->head_dim / 2), at, bytes) &&
+         !meet(p->scales, rows * (p->head_dim / 8), at, bytes);
+}
+
+// The descriptor's checks, for a call that takes SV_KV4.
+sv_status check_desc_kv4(const sv_attn_desc* d) {
+  if (!d) return SV_ERR_NULL;
+  sv_attn_desc c = *d;
+  if (c.kv_dtype == SV_KV4) c.kv_dtype = SV_BF16;
+  return check_desc(&c);
+}
+
+float scale_log2_of(const sv_attn_desc* d) {
+  const float scale = d->softmax_scale > 0.f ? d->softmax_scale : 1.f / sqrtf((float)d->head_dim);
+  return scale * 1.4426950408889634f;
+}
+
+int kv4_rows_per_head(const sv_attn_desc* d) {
+  return d->num_q_heads / d->num_kv_heads * (1 + d->max_draft_len);
+}
+
+AttnWs kv4_layout(const sv_attn_desc* d, int sms) {
+  return attn_ws_layout(d->batch, d->num_kv_heads, d->num_q_heads / d->num_kv_heads, d->head_dim,
+                        d->max_draft_len, attn_kv4_ctas(kv4_rows_per_head(d), sms));
+}
+
+}  // namespace
+
+extern "C" {
+
+SV_API size_t spec_kv4_workspace_size(int32_t batch) { return batch < 0 ? 0 : 256; }
+
+SV_API sv_status spec_kv4_write(const sv_kv4_pages* pages, int32_t batch,
+                                const int32_t* block_table, int32_t max_blocks_per_seq,
+                                const int32_t* start, const int32_t* count, int64_t rows,
+                                const void* k, int64_t k_row_stride, const void* v,
+                                int64_t v_row_stride, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  const sv_status st = check_kv4_rows(pages, batch, block_table, max_blocks_per_seq, start, count,
+                                      rows, k, v, workspace, workspace_bytes);
+  if (st != SV_OK || batch == 0 || rows == 0) return st;
+  const int64_t width = (int64_t)pages->num_kv_heads * pages->head_dim;
+  for (const int64_t s : {k_row_stride, v_row_stride})
+    if (s < width || s % 8 != 0 || s > ((int64_t)1 << 40)) return SV_ERR_SHAPE;
+  if (!kv4_apart(pages, k, 2 * (size_t)((rows - 1) * k_row_stride + width)) ||
+      !kv4_apart(pages, v, 2 * (size_t)((rows - 1) * v_row_stride + width)))
+    return SV_ERR_SHAPE;
+  const int sms = current_sms();
+  if (sms <= 0) return SV_ERR_CUDA;
+  return launch_kv4_write(*pages, batch, block_table, max_blocks_per_seq, start, count, rows, k,
+                          k_row_stride, v, v_row_stride, workspace, sms,
+                          (cudaStream_t)stream) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
+SV_API sv_status spec_kv4_read(const sv_kv4_pages* pages, int32_t batch,
+                               const int32_t* block_table, int32_t max_blocks_per_seq,
+                               const int32_t* start, const int32_t* count, int64_t rows,
+                               void* k_out, void* v_out, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  const sv_status st = check_kv4_rows(pages, batch, block_table, max_blocks_per_seq, start, count,
+                                      rows, k_out, v_out, workspace, workspace_bytes);
+  if (st != SV_OK || batch == 0 || rows == 0) return st;
+  const size_t bytes = 2 * (size_t)rows * pages->num_kv_heads * pages->head_dim;
+  if (!kv4_apart(pages, k_out, bytes) || !kv4_apart(pages, v_out, bytes) ||
+      meet(k_out, bytes, v_out, bytes))
+    return SV_ERR_SHAPE;
+  const int sms = current_sms();
+  if (sms <= 0) return SV_ERR_CUDA;
+  return launch_kv4_read(*pages, batch, block_table, max_blocks_per_seq, start, count, rows, k_out,
+                         v_out, workspace, sms, (cudaStream_t)stream) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
+SV_API size_t spec_verify_attn_kv4_workspace_size(const sv_attn_desc* desc) {
+  if (check_desc_kv4(desc) != SV_OK || desc->kv_dtype != SV_KV4) return 0;
+  const int sms = current_sms();
+  return sms <= 0 ? 0 : kv4_layout(desc, sms).total;
+}
+
+SV_API sv_status spec_verify_attn_kv4(const sv_attn_desc* desc, const void* q,
+                                      const sv_kv4_pages* pages, const int32_t* block_table,
+                                      int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                      const int32_t* draft_len, void* out, float* lse,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  sv_status st = check_desc_kv4(desc);
+  if (st != SV_OK) return st;
+  if (desc->kv_dtype != SV_KV4) return SV_ERR_DTYPE;
+  st = check_kv4(pages);
+  if (st != SV_OK) return st;
+  if (pages->num_kv_heads != desc->num_kv_heads || pages->head_dim != desc->head_dim ||
+      max_blocks_per_seq < 1)
+    return SV_ERR_SHAPE;
+  if (desc->batch == 0) return SV_OK;
+  if (!q || !block_table || !seq_lens || !draft_len || !out || !workspace) return SV_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(block_table, 4) ||
+      !aligned(seq_lens, 4) || !aligned(draft_len, 4) || !aligned(workspace, 256))
+    return SV_ERR_ALIGN;
+  const int sms = current_sms();
+  if (sms <= 0) return SV_ERR_CUDA;
+  const AttnWs lay = kv4_layout(desc, sms);
+  if (workspace_bytes < lay.total) return SV_ERR_WORKSPACE;
+
+  const PagedArgs pg = {block_table, max_blocks_per_seq, pages->block_size, pages->num_blocks};
+  AttnParams p = shape_params(desc, pg, 1, sms);
+  // no more CTAs than tiles (the combine kernel reads every CTA's range that a unit spans)
+  const int64_t rows = kv4_rows_per_head(desc);
+  const int64_t tiles = (int64_t)desc->batch * desc->num_kv_heads * ((rows + MT - 1) / MT) *
+                        (((int64_t)desc->max_seq_len + desc->max_draft_len) / attn_kv4_kt() + 1);
+  p.n_ctas = (int)std::min<int64_t>(tiles, attn_kv4_ctas((int)rows, sms));
+  uint8_t* ws = (uint8_t*)workspace;
+  p.q = q;
+  p.k = pages->k_codes;
+  p.v = pages->v_codes;
+  p.kv4_scales = pages->scales;
+  p.out = out;
+  p.lse = lse;
+  p.kv_scale = pages->kv_scale;
+  p.seq_lens = seq_lens;
+  p.draft_len = draft_len;
+  p.flags = (uint32_t*)(ws + lay.ctrl);
+  p.hdr = (PlanHdr*)(ws + lay.hdr);
+  p.q_off = (int64_t*)(ws + lay.q_off);
+  p.kv_off = (int64_t*)(ws + lay.kv_off);
+  p.units = (int4*)(ws + lay.units);
+  p.ubeg = (int32_t*)(ws + lay.ubeg);
+  p.cta_tab = (int2*)(ws + lay.cta_tab);
+  p.part_o = (float*)(ws + lay.part_o);
+  p.part_ml = (float2*)(ws + lay.part_ml);
+  p.block_table = block_table;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (launch_plan(p, attn_kv4_kt(), s) != cudaSuccess) return SV_ERR_CUDA;
+  if (g_ev_start && cudaEventRecord(g_ev_start, s) != cudaSuccess) return SV_ERR_CUDA;
+  if (launch_attn_kv4(p, s) != cudaSuccess) return SV_ERR_CUDA;
+  if (g_ev_stop && cudaEventRecord(g_ev_stop, s) != cudaSuccess) return SV_ERR_CUDA;
+  return launch_combine(p, s) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+}
+
+SV_API size_t spec_attn_mass_workspace_size(const sv_attn_desc* desc) {
+  if (check_desc_kv4(desc) != SV_OK) return 0;
+  const int sms = current_sms();
+  return sms <= 0 ? 0 : mass_ws_bytes(desc, sms);
+}
+
+SV_API sv_status spec_attn_mass(const sv_attn_desc* desc, const void* q, const void* k_pages,
+                                const void* scales, const float* kv_scale, int64_t num_blocks,
+                                int32_t block_size, const int32_t* block_table,
+                                int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                const int32_t* draft_len, const int32_t* row_count,
+                                const float* lse, float* mass, int64_t mass_stride,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  const sv_status st = check_desc_kv4(desc);
+  if (st != SV_OK) return st;
+  if (num_blocks < 1 || num_blocks > 0x7fffffff || !pool_sizes_ok((int32_t)num_blocks, block_size) ||
+      max_blocks_per_seq < 1 || desc->sliding_window != 0 || mass_stride < 1 ||
+      mass_stride > ((int64_t)1 << 40))
+    return SV_ERR_SHAPE;
+  if (desc->batch == 0) return SV_OK;
+  if (!q || !k_pages || !block_table || !seq_lens || !draft_len || !mass || !workspace)
+    return SV_ERR_NULL;
+  if ((desc->kv_dtype == SV_KV4 && !scales) || (desc->kv_dtype != SV_BF16 && !kv_scale))
+    return SV_ERR_NULL;
+  if ((desc->kv_dtype != SV_KV4 && scales) || (desc->kv_dtype == SV_BF16 && kv_scale))
+    return SV_ERR_SHAPE;
+  if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(scales, 16) || !aligned(kv_scale, 4) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(draft_len, 4) ||
+      !aligned(row_count, 4) || !aligned(lse, 4) || !aligned(mass, 4) || !aligned(workspace, 256))
+    return SV_ERR_ALIGN;
+  const int sms = current_sms();
+  if (sms <= 0) return SV_ERR_CUDA;
+  if (workspace_bytes < mass_ws_bytes(desc, sms)) return SV_ERR_WORKSPACE;
+  return launch_mass(desc, scale_log2_of(desc), q, k_pages, scales, kv_scale, num_blocks, block_size,
+                     block_table, max_blocks_per_seq, seq_lens, draft_len, row_count, lse, mass,
+                     mass_stride, workspace, sms, (cudaStream_t)stream) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
+SV_API size_t spec_kv_evict_workspace_size(int32_t n, int32_t num_kv_heads, int64_t mass_stride) {
+  if (n < 0 || n > SV_MAX_EVICT_ROWS || num_kv_heads < 1 || num_kv_heads > 4096 || mass_stride < 1 ||
+      mass_stride > MAX_KV_ROWS)
+    return 0;
+  return evict_ws_bytes(n, num_kv_heads, mass_stride);
+}
+
+SV_API sv_status spec_kv_evict(const sv_page_table* table, int32_t n, const int32_t* rows,
+                               const int32_t* new_len, const int32_t* keep_first,
+                               int32_t keep_last, int32_t num_kv_heads, float* mass,
+                               int64_t mass_stride, int32_t* kept, int64_t kept_stride,
+                               int32_t num_pools, const sv_page_data* pools, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  // (the page operators' checks, whose own workspace size does not apply)
+  sv_status st = check_pages(table, n, workspace, ~(size_t)0);
+  if (st == SV_OK) st = check_pools(table, num_pools, pools);
+  if (st != SV_OK) return st;
+  const size_t need = spec_kv_evict_workspace_size(n, num_kv_heads, mass_stride);
+  if (need == 0 || keep_last < 0 || (kept && kept_stride < 0)) return SV_ERR_SHAPE;
+  int64_t slices = 1;
+  for (int k = 0; k < num_pools; ++k) {
+    const int64_t pos = pools[k].page_bytes / table->block_size;
+    if (pos % (8 * (int64_t)num_kv_heads) != 0) return SV_ERR_SHAPE;
+    slices += (pos / num_kv_heads + 255) / 256;
+  }
+  if (n * (int64_t)num_kv_heads * slices > 0x7fffffff) return SV_ERR_SHAPE;
+  if (n == 0) return SV_OK;
+  if (!new_len || !mass) return SV_ERR_NULL;
+  if (!aligned(rows, 4) || !aligned(new_len, 4) || !aligned(keep_first, 4) || !aligned(mass, 4) ||
+      !aligned(kept, 4))
+    return SV_ERR_ALIGN;
+  if (workspace_bytes < need) return SV_ERR_WORKSPACE;
+  // what the call changes and what it reads must be apart
+  const size_t list = 4 * (size_t)n;
+  const Span spans[] = {
+      {workspace, need},
+      {mass, 4 * (size_t)table->table_rows * num_kv_heads * mass_stride},
+      {kept, 4 * (size_t)n * num_kv_heads * kept_stride},
+      {rows, list},
+      {new_len, list},
+      {keep_first, list},
+      {table->ref_count, 4 * (size_t)table->num_blocks},
+      {table->block_table, 4 * (size_t)table->table_rows * table->max_blocks_per_seq},
+      {table->cached_len, 4 * (size_t)table->table_rows}};
+  const int ns = (int)(sizeof spans / sizeof spans[0]);
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < ns; ++j)
+      if (meet(spans[i].at, spans[i].bytes, spans[j].at, spans[j].bytes)) return SV_ERR_SHAPE;
+  for (int k = 0; k < num_pools; ++k) {
+    const size_t bytes = (size_t)pools[k].page_bytes * table->num_blocks;
+    for (int j = 0; j < ns; ++j)
+      if (meet(pools[k].base, bytes, spans[j].at, spans[j].bytes)) return SV_ERR_SHAPE;
+    for (int l = 0; l < k; ++l)
+      if (meet(pools[k].base, bytes, pools[l].base, (size_t)pools[l].page_bytes * table->num_blocks))
+        return SV_ERR_SHAPE;
+  }
+  return launch_evict(*table, n, rows, new_len, keep_first, keep_last, num_kv_heads, mass,
+                      mass_stride, kept, kept_stride, num_pools, pools, workspace,
+                      (cudaStream_t)stream) == cudaSuccess
+             ? SV_OK
+             : SV_ERR_CUDA;
+}
+
+}  // extern "C"
+
+extern "C" {
 
 SV_API size_t spec_accept_workspace_size(int32_t batch, int32_t max_draft_len, int32_t vocab) {
   if (batch < 0 || max_draft_len < 0 || max_draft_len > 255 || vocab <= 0) return 0;

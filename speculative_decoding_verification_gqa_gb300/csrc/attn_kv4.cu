@@ -1,0 +1,486 @@
+// attn_kv4.cu -- verify attention over a 4-bit paged cache (format: kv4.cuh) for few query rows
+// a KV head, on warp-level MMAs with the keys as the M dimension.
+//
+// The transposed products S^T = K Q^T and O^T = V^T P^T put the 16 keys (or 16 elements of d)
+// of an m16n8k16 step in M and up to 8 query rows in N, so that a single token's G rows fill
+// N = 8 instead of an eighth of M = 128, and K and V are the A operands, whose fragments each
+// lane decodes from the codes in its own registers: nothing of the 16-bit K or V is ever
+// written to shared memory. What makes the fragments fall in place:
+//   * the order of d within S^T is free as long as Q has the same: lane t of a key's four takes
+//     a quarter of the key's codes, contiguous (d 128: 16 bytes), four elements a k-step;
+//   * the order of d in O^T is free (a permutation of output rows): the lanes of row r of a
+//     fragment take the elements 16 r .. 16 r + 15 (d 128), which share one block scale;
+//   * an A fragment of V^T pairs two keys at one element, the codes pair two elements of one
+//     key: masks exchange the nibbles of two keys' words before the conversion, 4 operations
+//     for 16 codes;
+//   * P^T's fragments are the 8x8 transposes (movmatrix) of S^T's packed accumulators.
+// Row statistics: rows are columns of S^T, so a row's scores are spread over the lanes; the
+// reference maximum is the same in all lanes of a column and moves only when some lane of the
+// warp sees a score far above it, so the usual tile needs one vote and no exchange.
+//
+// A warp takes chunks of 32 keys, its own ring of cp.async stages, its own (O, m, l); the CTA's
+// four warps meet only at the end of a unit, where the parts are joined by the rule of the
+// online softmax. Units, tile line and the join across CTAs: internal.cuh.
+#include <cuda_bf16.h>
+
+#include "kv4.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int KT = 128;            // keys per tile of the line
+constexpr int CK = 32;             // keys of a chunk
+constexpr int NW = 4;              // warps
+constexpr int NTHREADS = NW * 32;
+constexpr int ST = 3;              // ring stages of a warp
+// Reference of a row: its largest score less SHIFT (log2 units), raised when a score is more
+// than RESCALE above that score. P = 2^(s - reference) then lies below 2^15 and the largest at
+// 2^7 or more, so that f16 (largest 65504, least step 2^-24) drops only weights below 2^-32 of
+// it: at the reference itself it would drop those below 2^-25, 3% of a row of a million keys.
+constexpr float SHIFT = 7.f, RESCALE = 8.f;
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+template <int N>  // bytes; not valid: zeros, nothing is read
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? N : 0;
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+template <int HD>
+struct L4 {
+  static constexpr int KS = HD / 16;        // k-steps of S^T, m-tiles of O^T
+  static constexpr int RB = HD / 2;         // bytes of a row's codes
+  static constexpr int SB = HD / 8;         // bytes of a row's scales (K, then V)
+  static constexpr int NB = HD / 16;        // blocks of a row
+  static constexpr int CODES = CK * RB;     // one tensor's codes of a stage
+  static constexpr int STAGE = 2 * CODES + CK * SB;
+  static constexpr int OSTRIDE = HD + 4;    // floats of an output row in shared memory
+  static constexpr int RING = ST * STAGE;
+};
+// The bytes a warp owns: its ring, which holds its output part at the end of a unit.
+template <int HD, int NT>
+constexpr int warp_bytes() {
+  return L4<HD>::RING > 8 * NT * L4<HD>::OSTRIDE * 4 ? L4<HD>::RING : 8 * NT * L4<HD>::OSTRIDE * 4;
+}
+
+// Where key kk of a chunk has its V codes: keys 2t, 2t + 1 of eight lie 4 rows apart, and d 128
+// exchanges the halves of the rows of t = 2, 3, so that a warp's loads, four keys (one of each
+// t) by eight elements' bytes, meet every bank once.
+__device__ __forceinline__ int v_place(int kk) { return (kk & ~7) | ((kk & 1) << 2) | ((kk >> 1) & 3); }
+
+// NT: n-tiles of 8 query rows. The unit's rows are taken 8 NT at a time, each pass over the
+// unit's keys of this CTA.
+template <int HD, int NT>
+__global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3) attn_kv4_kernel(const AttnParams p) {
+  using L = L4<HD>;
+  constexpr int KS = L::KS, ROWS = 8 * NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float s_m[NW][ROWS], s_l[NW][ROWS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r8 = lane >> 2, t4 = lane & 3;
+  uint8_t* ring = smem + warp * warp_bytes<HD, NT>();
+  pdl_trigger();
+  pdl_wait();
+  const int2 rb = p.cta_tab[blockIdx.x], re = p.cta_tab[blockIdx.x + 1];
+  const int64_t t_begin = rb.x, t_end = re.x;
+  if (t_begin >= t_end) return;
+  int u = rb.y;
+
+  for (int64_t t = t_begin; t < t_end; ++u) {
+    if (u >= p.hdr->num_units) break;  // cannot happen for a valid plan
+    const int4 info = p.units[u];
+    const int b = info.x, g = info.y, mt = info.z;
+    const int64_t ub = p.ubeg[u];
+    const int nt = p.ubeg[u + 1] - (int)ub;
+    const int l0 = (int)(t - ub);
+    const int l1 = (int)(min(t_end, ub + nt) - ub);
+    if (l1 <= l0) break;  // cannot happen for a valid plan
+    t = ub + l1;
+    const int T = p.seq_lens[b], D = p.draft_len[b];
+    const int rows_total = p.G * (D + 1);
+    const int rows = min(MT, rows_total - mt * MT);
+    const int nkeys = T + D + 1;
+    const int kvis = first_visible_key(T, p.window);
+    const int64_t qo = p.q_off[b];
+    const float sck = p.scale_log2 * p.kv_scale[g];
+    const int key_first = info.w + l0 * KT;
+    // chunks with a key of the sequence; this warp takes warp, warp + NW, ...
+    const int chunks = min((l1 - l0) * (KT / CK), (nkeys - key_first + CK - 1) / CK);
+    const int mine = chunks > warp ? (chunks - warp + NW - 1) / NW : 0;
+    const int32_t* tab = p.block_table + (size_t)b * p.bt_stride;
+    const bool whole = l0 == 0 && l1 == nt;
+
+    for (int sub = 0; sub < rows; sub += ROWS) {
+      // ---- the ring. Eight consecutive keys lie in one block: a chunk has four table entries,
+      // read a chunk ahead by the lanes
+      auto entry = [&](int i) -> int {  // this lane's entry of the warp's i-th chunk
+        const int pos = key_first + (warp + i * NW) * CK + 8 * t4;
+        if (i >= mine || pos >= nkeys || pos + 8 <= kvis) return 0;
+        return __ldg(tab + (pos >> p.bs_log2));
+      };
+      int ent = entry(0);
+      auto issue = [&](int i) {
+        if (i < mine) {
+          uint8_t* st = ring + (i % ST) * L::STAGE;
+          const int key0 = key_first + (warp + i * NW) * CK;
+          constexpr int CH = L::RB / 16;  // 16-byte pieces of a row's codes
+#pragma unroll
+          for (int j = 0; j < CH; ++j) {
+            const int kk = (j * 32 + lane) / CH, c = lane & (CH - 1);
+            const int blk = __shfl_sync(0xffffffffu, ent, kk >> 3);
+            const int key = key0 + kk;
+            bool ok = key < nkeys && key >= kvis;
+            if (ok && (blk < 0 || blk >= p.num_blocks)) {
+              atomicOr(p.flags, FLAG_ATTN_SHAPE);
+              ok = false;
+            }
+            const int64_t row = ok ? ((int64_t)blk << p.bs_log2) + (key & (p.block_size - 1)) : 0;
+            const size_t off = (size_t)(row * p.Hkv + g) * L::RB + c * 16;
+            cp_async<16>(smem_u32(st + kk * L::RB + c * 16), (const uint8_t*)p.k + off, ok);
+            const int vc = CH == 4 ? c ^ (((kk >> 2) & 1) << 1) : c;
+            cp_async<16>(smem_u32(st + L::CODES + v_place(kk) * L::RB + vc * 16),
+                         (const uint8_t*)p.v + off, ok);
+          }
+          const int blk = __shfl_sync(0xffffffffu, ent, lane >> 3);
+          const int key = key0 + lane;
+          const bool ok = key < nkeys && key >= kvis && blk >= 0 && blk < p.num_blocks;
+          const int64_t row = ok ? ((int64_t)blk << p.bs_log2) + (key & (p.block_size - 1)) : 0;
+          cp_async<L::SB>(smem_u32(st + 2 * L::CODES + lane * L::SB),
+                          (const uint8_t*)p.kv4_scales + (size_t)(row * p.Hkv + g) * L::SB, ok);
+          ent = entry(i + 1);
+        }
+        cp_async_commit();
+      };
+#pragma unroll
+      for (int i = 0; i < ST - 1; ++i) issue(i);
+
+      // ---- Q: column n = lane / 4 of each n-tile, the elements (HD / 4) t .. of its row
+      uint32_t qf[NT][KS][2];
+      float sc[NT][2];  // score scale (log2 units) of columns 2 t, 2 t + 1
+      int i_col[NT][2];  // window row of those columns
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int r = sub + n * 8 + r8;  // row of the unit
+        const bool live = r < rows;
+        const int rg = mt * MT + (live ? r : 0);
+        const uint4* src = reinterpret_cast<const uint4*>(
+            (const uint16_t*)p.q + ((qo + rg / p.G) * p.Hq + (int64_t)g * p.G + rg % p.G) * HD +
+            t4 * (HD / 4));
+        uint32_t w[HD / 8], amax = 0;
+#pragma unroll
+        for (int e = 0; e < HD / 32; ++e) {
+          const uint4 v = live ? __ldg(src + e) : make_uint4(0, 0, 0, 0);
+          w[4 * e] = v.x;
+          w[4 * e + 1] = v.y;
+          w[4 * e + 2] = v.z;
+          w[4 * e + 3] = v.w;
+        }
+#pragma unroll
+        for (int e = 0; e < HD / 8; ++e) amax = max(amax, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const float f = exp2_of(q_exponent(amax));  // f16's range: see q_exponent
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t x = w[2 * s + e];
+            qf[n][s][e] = pack_f16(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f);
+          }
+        const float mysc = q_row_scale(sck, amax);
+        const int myi = live ? rg / p.G : D;  // rows past the unit's see every key
+        const int from = (2 * t4) * 4;        // a lane that holds column 2 t
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sc[n][e] = __shfl_sync(0xffffffffu, mysc, from + 4 * e);
+          i_col[n][e] = __shfl_sync(0xffffffffu, myi, from + 4 * e);
+        }
+      }
+      float o[KS][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) o[s][n][0] = o[s][n][1] = o[s][n][2] = o[s][n][3] = 0.f;
+      }
+      const int lo_max = p.window > 0 ? max(T + D + 1 - p.window, 0) : 0;
+
+      for (int i = 0; i < mine; ++i) {
+        cp_async_wait<ST - 2>();
+        __syncwarp();  // the chunk's bytes of every lane are here; the last chunk's are read
+        issue(i + ST - 1);
+        const uint8_t* st = ring + (i % ST) * L::STAGE;
+        const uint8_t* sS = st + 2 * L::CODES;
+        const int key0 = key_first + (warp + i * NW) * CK;
+
+        // ---- S^T = K Q^T
+        float s[2][NT][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) s[h][n][0] = s[h][n][1] = s[h][n][2] = s[h][n][3] = 0.f;
+          uint32_t w[2][HD / 32], u[2][HD / 64];  // codes and scale pairs of keys r8, r8 + 8
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int kk = h * 16 + e * 8 + r8;
+            const uint8_t* row = st + kk * L::RB + t4 * (L::RB / 4);
+            if constexpr (HD == 128) {
+              const uint4 v = *reinterpret_cast<const uint4*>(row);
+              w[e][0] = v.x;
+              w[e][1] = v.y;
+              w[e][2] = v.z;
+              w[e][3] = v.w;
+              const uint32_t c = *reinterpret_cast<const uint16_t*>(sS + kk * L::SB + 2 * t4);
+              const uint32_t f = e4m3x2_to_f16x2(c);
+              u[e][0] = lo_twice(f);
+              u[e][1] = hi_twice(f);
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(row);
+              w[e][0] = v.x;
+              w[e][1] = v.y;
+              u[e][0] = lo_twice(e4m3x2_to_f16x2(sS[kk * L::SB + t4]));
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < HD / 32; ++q) {  // a word of codes: two k-steps
+            uint32_t x[4], y[4];
+            e2m1x8_to_f16(w[0][q], x);
+            e2m1x8_to_f16(w[1][q], y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[e] = hmul2(x[e], u[0][q >> 1]);
+              y[e] = hmul2(y[e], u[1][q >> 1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t a[4] = {x[2 * e], y[2 * e], x[2 * e + 1], y[2 * e + 1]};
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma_f16(s[h][n], a, qf[n][2 * q + e][0], qf[n][2 * q + e][1]);
+            }
+          }
+        }
+        // ---- scale, mask, reference maximum
+        const bool edge = key0 + CK > T || key0 < lo_max;
+        bool above = false;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float x = s[h][n][e] * sc[n][e & 1];
+              if (edge) {
+                const int key = key0 + h * 16 + r8 + (e >> 1) * 8;
+                const int hi = T + i_col[n][e & 1];
+                if (key > hi || (p.window > 0 && key <= hi - p.window)) x = -INFINITY;
+              }
+              s[h][n][e] = x;
+              above |= x > m[n][e & 1] + (SHIFT + RESCALE);
+            }
+        if (__any_sync(0xffffffffu, above)) {  // (m -inf: any finite score)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = fmaxf(fmaxf(s[0][n][e], s[0][n][e + 2]), fmaxf(s[1][n][e], s[1][n][e + 2]));
+#pragma unroll
+              for (int o2 = 4; o2 < 32; o2 <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o2));
+              const float mn = fmaxf(m[n][e], x - SHIFT);
+              const float al = mn == -INFINITY ? 1.f : ex2(m[n][e] - mn);
+              m[n][e] = mn;
+              l[n][e] *= al;
+#pragma unroll
+              for (int k = 0; k < KS; ++k) {
+                o[k][n][e] *= al;
+                o[k][n][e + 2] *= al;
+              }
+            }
+        }
+        // ---- P = 2^(s - m), its fragments
+        uint32_t pf[2][NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0];
+          const float m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float a0 = ex2(s[h][n][0] - m0), a1 = ex2(s[h][n][1] - m1);
+            const float a2 = ex2(s[h][n][2] - m0), a3 = ex2(s[h][n][3] - m1);
+            l[n][0] += a0 + a2;
+            l[n][1] += a1 + a3;
+            pf[h][n][0] = transpose8x8(pack_f16(a0, a1));
+            pf[h][n][1] = transpose8x8(pack_f16(a2, a3));
+          }
+        }
+        // ---- O^T += V^T P^T
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          constexpr int VW = HD / 64;  // words of codes a lane takes of each key
+          uint32_t w[4][VW], u[2];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {  // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+            const int kk = h * 16 + (e >> 1) * 8 + 2 * t4 + (e & 1);
+            const uint8_t* row = st + L::CODES + v_place(kk) * L::RB;
+            if constexpr (HD == 128) {
+              const int c = (r8 >> 1) ^ (((kk >> 2) & 1) << 1);
+              const uint2 v = *reinterpret_cast<const uint2*>(row + c * 16 + (r8 & 1) * 8);
+              w[e][0] = v.x;
+              w[e][1] = v.y;
+            } else {
+              w[e][0] = *reinterpret_cast<const uint32_t*>(row + r8 * 4);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint8_t* sv = sS + (h * 16 + e * 8 + 2 * t4) * L::SB + L::NB + (HD == 128 ? r8 : r8 >> 1);
+            u[e] = e4m3x2_to_f16x2((uint32_t)sv[0] | ((uint32_t)sv[L::SB] << 8));
+          }
+#pragma unroll
+          for (int q = 0; q < VW; ++q) {  // a word of each key: 4 m-tiles
+            uint32_t f[2][2][4];          // [keys 2 t, + 8][element 2 i, 2 i + 1][i]
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t k0 = w[2 * e][q], k1 = w[2 * e + 1][q];
+              e2m1x8_to_f16((k0 & 0x0f0f0f0fu) | ((k1 << 4) & 0xf0f0f0f0u), f[e][0]);
+              e2m1x8_to_f16(((k0 >> 4) & 0x0f0f0f0fu) | (k1 & 0xf0f0f0f0u), f[e][1]);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                f[e][0][x] = hmul2(f[e][0][x], u[e]);
+                f[e][1][x] = hmul2(f[e][1][x], u[e]);
+              }
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t a[4] = {f[0][0][x], f[0][1][x], f[1][0][x], f[1][1][x]};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma_f16(o[4 * q + x][n], a, pf[h][n][0], pf[h][n][1]);
+            }
+          }
+        }
+      }
+      cp_async_wait<0>();
+
+      // ---- join of the CTA's warps
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], x);
+          if (r8 == 0) {
+            s_m[warp][n * 8 + 2 * t4 + e] = m[n][e];
+            s_l[warp][n * 8 + 2 * t4 + e] = l[n][e];
+          }
+        }
+      __syncthreads();  // every warp is done with its ring, its (m, l) are written
+      float* part = reinterpret_cast<float*>(ring);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = n * 8 + 2 * t4 + e;
+          float M = s_m[0][r];
+#pragma unroll
+          for (int w = 1; w < NW; ++w) M = fmaxf(M, s_m[w][r]);
+          const float f = m[n][e] == -INFINITY ? 0.f : ex2(m[n][e] - M);
+          // elements: m-tile i, fragment rows r8 and r8 + 8 are (HD / 8) r8 + 2 i and + 1
+          float* dst = part + r * L::OSTRIDE + r8 * (HD / 8);
+#pragma unroll
+          for (int k = 0; k < KS; k += 2)
+            *reinterpret_cast<float4*>(dst + 2 * k) =
+                make_float4(o[k][n][e] * f, o[k][n][e + 2] * f, o[k + 1][n][e] * f, o[k + 1][n][e + 2] * f);
+        }
+      __syncthreads();
+      // (a warp without chunks: m = -inf, O = 0; a NaN in l or O stays)
+      for (int idx = tid; idx < ROWS * (HD / 4); idx += NTHREADS) {
+        const int r = idx / (HD / 4), c = idx % (HD / 4);
+        if (sub + r >= rows) break;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float M = s_m[0][r], lsum = 0.f;
+#pragma unroll
+        for (int w = 1; w < NW; ++w) M = fmaxf(M, s_m[w][r]);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const float4 v = *reinterpret_cast<const float4*>(
+              reinterpret_cast<const float*>(smem + w * warp_bytes<HD, NT>()) + r * L::OSTRIDE + c * 4);
+          acc.x += v.x;
+          acc.y += v.y;
+          acc.z += v.z;
+          acc.w += v.w;
+          lsum += s_m[w][r] == -INFINITY ? s_l[w][r] : s_l[w][r] * ex2(s_m[w][r] - M);
+        }
+        const int rg = mt * MT + sub + r;
+        const int64_t orow = (qo + rg / p.G) * p.Hq + (int64_t)g * p.G + rg % p.G;
+        if (whole) {
+          const float inv = p.kv_scale[p.Hkv + g] / lsum;
+          const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+          const __nv_bfloat162 y = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+          *reinterpret_cast<uint2*>((uint16_t*)p.out + orow * HD + c * 4) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+          if (p.lse && c == 0) p.lse[orow] = (M + log2f(lsum)) * 0.6931471805599453f;
+        } else {
+          const size_t slot = (size_t)blockIdx.x + u;
+          *reinterpret_cast<float4*>(p.part_o + (slot * MT + sub + r) * HD + c * 4) = acc;
+          if (c == 0) p.part_ml[slot * MT + sub + r] = make_float2(M, lsum);
+        }
+      }
+      __syncthreads();  // the parts are read before the rings are filled again
+    }
+  }
+}
+
+template <int HD, int NT>
+cudaError_t launch_nt(const AttnParams& p, cudaStream_t s) {
+  const size_t smem = (size_t)NW * warp_bytes<HD, NT>();
+  auto kernel = attn_kv4_kernel<HD, NT>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, dim3(p.n_ctas), dim3(NTHREADS), smem, s, p);
+}
+
+}  // namespace
+
+int attn_kv4_kt() { return KT; }
+// CTAs of a call on `sms` SMs: what an SM holds at once.
+int attn_kv4_ctas(int rows_per_kv, int sms) { return sms * (rows_per_kv <= 8 ? 4 : 3); }
+
+cudaError_t launch_attn_kv4(const AttnParams& p, cudaStream_t s) {
+  const bool one = p.G * (1 + p.max_draft) <= 8;
+  if (p.d == 128) return one ? launch_nt<128, 1>(p, s) : launch_nt<128, 2>(p, s);
+  return one ? launch_nt<64, 1>(p, s) : launch_nt<64, 2>(p, s);
+}
+
+}  // namespace sv

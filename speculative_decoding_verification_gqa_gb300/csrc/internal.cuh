@@ -193,6 +193,8 @@ struct AttnParams {
                               // run further ahead), 0 paired K + V stages
   long long wait_limit;       // tcgen05 kernel: clock cycles a barrier wait may take before
                               // it gives up (0: the default, about 2 s)
+  const void* kv4_scales;     // 4-bit cache: E4M3 [.., Hkv, 2, d / 16]
+  float* lse;                 // [q_rows, Hq] or nullptr: each row's log-sum-exp (natural)
   int stall_first_tile;       // test hook: every CTA's producer withholds the K and V loads
                               // of the first tile of its range, so the waits for it run out
 };
@@ -384,6 +386,30 @@ cudaError_t launch_attn_tc_hp(const AttnParams& p, bool fp8, const HostPlan& hp,
 // at most one CTA per SM. The CTAs check the lengths and work out the offsets themselves.
 bool attn_pair_applies(const AttnParams& p, bool fp8, int sms);
 cudaError_t launch_attn_pair(const AttnParams& p, cudaStream_t s);
+
+// 4-bit cache (attn_kv4.cu, kv4.cu).
+int attn_kv4_kt();
+int attn_kv4_ctas(int rows_per_kv, int sms);
+cudaError_t launch_attn_kv4(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_kv4_write(const sv_kv4_pages& p, int B, const int32_t* table, int max_blocks,
+                             const int32_t* start, const int32_t* count, int64_t rows,
+                             const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                             void* ws, int sms, cudaStream_t s);
+cudaError_t launch_kv4_read(const sv_kv4_pages& p, int B, const int32_t* table, int max_blocks,
+                            const int32_t* start, const int32_t* count, int64_t rows, void* k_out,
+                            void* v_out, void* ws, int sms, cudaStream_t s);
+// Accumulated attention weight (attn_mass.cu) and eviction by it (evict.cu).
+size_t mass_ws_bytes(const sv_attn_desc* d, int sms);
+cudaError_t launch_mass(const sv_attn_desc* d, float scale_log2, const void* q, const void* k_pages,
+                        const void* scales, const float* kv_scale, int64_t num_blocks, int block_size,
+                        const int32_t* table, int max_blocks, const int32_t* seq_lens,
+                        const int32_t* draft_len, const int32_t* row_count, const float* lse,
+                        float* mass, int64_t mass_stride, void* ws, int sms, cudaStream_t s);
+size_t evict_ws_bytes(int n, int Hkv, int64_t max_positions);
+cudaError_t launch_evict(const sv_page_table& t, int n, const int32_t* rows, const int32_t* new_len,
+                         const int32_t* keep_first, int keep_last, int Hkv, float* mass,
+                         int64_t mass_stride, int32_t* kept, int64_t kept_stride, int num_pools,
+                         const sv_page_data* pools, void* ws, cudaStream_t s);
 
 // Acceptance.
 struct AcceptWs {
