@@ -23,6 +23,8 @@ namespace {
 constexpr int SWITCH_TILES_TC_FP8 = SV_SWITCH_F8;
 constexpr int SWITCH_TILES_TC_BF16 = SV_SWITCH_BF16;
 constexpr int SWITCH_TILES_MMA = 2;
+constexpr int SWITCH_TILES_KV4 = 9;
+constexpr int TILE_FLOOR_KV4 = 259;
 // Shared prefixes. A unit's start in 128-key tiles of 256 rows and in 64-key tiles of 128 rows,
 // and the SM time of the latter (two at a time on an SM) in the former. Measured around them at
 // d = 128 (short runs of calls back to back, below the power limit; 64 sequences over a prefix
@@ -795,9 +797,23 @@ int kv4_rows_per_head(const sv_attn_desc* d) {
   return d->num_q_heads / d->num_kv_heads * (1 + d->max_draft_len);
 }
 
+// 1 = warp-level MMAs (attn_kv4.cu), 2 = tcgen05 (attn_kv4_tc.cu)
+constexpr int KV4_SMALL_ROWS = 16;
+int pick_kv4(const sv_attn_desc* d) {
+  if (!attn_tc_available() || g_attn_kernel == 1) return 1;
+  return g_attn_kernel == 2 || kv4_rows_per_head(d) > KV4_SMALL_ROWS ? 2 : 1;
+}
+
+// CTAs of a call at most: what the kernel holds on an SM at once.
+int kv4_ctas(const sv_attn_desc* d, int which, int sms) {
+  return which == 2 ? sms : attn_kv4_ctas(kv4_rows_per_head(d), sms);
+}
+
 AttnWs kv4_layout(const sv_attn_desc* d, int sms) {
+  // room for the most CTAs of either kernel, so that the workspace of a larger shape serves a
+  // smaller one, under any sv_set_attn_kernel
   return attn_ws_layout(d->batch, d->num_kv_heads, d->num_q_heads / d->num_kv_heads, d->head_dim,
-                        d->max_draft_len, attn_kv4_ctas(kv4_rows_per_head(d), sms));
+                        d->max_draft_len, attn_kv4_ctas(1, sms));
 }
 
 }  // namespace
@@ -880,12 +896,18 @@ SV_API sv_status spec_verify_attn_kv4(const sv_attn_desc* desc, const void* q,
   if (workspace_bytes < lay.total) return SV_ERR_WORKSPACE;
 
   const PagedArgs pg = {block_table, max_blocks_per_seq, pages->block_size, pages->num_blocks};
-  AttnParams p = shape_params(desc, pg, 1, sms);
-  // no more CTAs than tiles (the combine kernel reads every CTA's range that a unit spans)
-  const int64_t rows = kv4_rows_per_head(desc);
-  const int64_t tiles = (int64_t)desc->batch * desc->num_kv_heads * ((rows + MT - 1) / MT) *
+  const int which = pick_kv4(desc);
+  AttnParams p = shape_params(desc, pg, which, sms);
+  if (which == 2) {
+    p.switch_tiles = SWITCH_TILES_KV4;
+    p.tile_floor = TILE_FLOOR_KV4;
+  }
+  // no more CTAs than tiles (the combine kernel reads every CTA's range that a unit spans);
+  // both kernels' tiles are 128 keys
+  const int64_t tiles = (int64_t)desc->batch * desc->num_kv_heads *
+                        ((kv4_rows_per_head(desc) + MT - 1) / MT) *
                         (((int64_t)desc->max_seq_len + desc->max_draft_len) / attn_kv4_kt() + 1);
-  p.n_ctas = (int)std::min<int64_t>(tiles, attn_kv4_ctas((int)rows, sms));
+  p.n_ctas = (int)std::min<int64_t>(tiles, kv4_ctas(desc, which, sms));
   uint8_t* ws = (uint8_t*)workspace;
   p.q = q;
   p.k = pages->k_codes;
@@ -909,7 +931,8 @@ SV_API sv_status spec_verify_attn_kv4(const sv_attn_desc* desc, const void* q,
   cudaStream_t s = (cudaStream_t)stream;
   if (launch_plan(p, attn_kv4_kt(), s) != cudaSuccess) return SV_ERR_CUDA;
   if (g_ev_start && cudaEventRecord(g_ev_start, s) != cudaSuccess) return SV_ERR_CUDA;
-  if (launch_attn_kv4(p, s) != cudaSuccess) return SV_ERR_CUDA;
+  if ((which == 2 ? launch_attn_kv4_tc(p, s) : launch_attn_kv4(p, s)) != cudaSuccess)
+    return SV_ERR_CUDA;
   if (g_ev_stop && cudaEventRecord(g_ev_stop, s) != cudaSuccess) return SV_ERR_CUDA;
   return launch_combine(p, s) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }

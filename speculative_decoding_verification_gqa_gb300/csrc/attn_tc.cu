@@ -927,6 +927,23 @@ bool make_kv_map(CUtensorMap* map, const void* base, int64_t kv_rows, int hkv, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [kv_rows, Hkv, HD / 2] bytes of 4-bit codes -> boxes of a head's whole row x 1 head x box_rows
+// rows, swizzled over the row's 64 bytes (HD 64: 32 bytes).
+bool make_kv4_map(CUtensorMap* map, const void* base, int64_t kv_rows, int hkv, int hd,
+                  int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t rb = hd / 2;
+  const cuuint64_t dims[3] = {rb, (cuuint64_t)hkv, (cuuint64_t)kv_rows};
+  const cuuint64_t strides[2] = {rb, (cuuint64_t)hkv * rb};
+  const cuuint32_t box[3] = {(cuuint32_t)rb, 1, (cuuint32_t)box_rows};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            hd == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int HD, bool F8, bool WIN, bool SPLIT>
 cudaError_t launch_hd(const AttnParams& p, cudaStream_t s) {
   using L = TcLayout<HD, F8, SPLIT>;
@@ -989,6 +1006,11 @@ cudaError_t launch_hd_hp(const AttnParams& p, const HostPlan& hp, cudaStream_t s
 bool kv_tensor_map(CUtensorMap* map, const void* base, int64_t kv_rows, int hkv, int hd,
                    bool fp8, int box_rows) {
   return make_kv_map(map, base, kv_rows, hkv, hd, fp8, box_rows);
+}
+
+bool kv4_tensor_map(CUtensorMap* map, const void* base, int64_t kv_rows, int hkv, int hd,
+                    int box_rows) {
+  return make_kv4_map(map, base, kv_rows, hkv, hd, box_rows);
 }
 
 bool attn_tc_available() { return encode_fn() != nullptr; }

@@ -391,6 +391,7 @@ cudaError_t launch_attn_pair(const AttnParams& p, cudaStream_t s);
 int attn_kv4_kt();
 int attn_kv4_ctas(int rows_per_kv, int sms);
 cudaError_t launch_attn_kv4(const AttnParams& p, cudaStream_t s);
+cudaError_t launch_attn_kv4_tc(const AttnParams& p, cudaStream_t s);
 cudaError_t launch_kv4_write(const sv_kv4_pages& p, int B, const int32_t* table, int max_blocks,
                              const int32_t* start, const int32_t* count, int64_t rows,
                              const void* k, int64_t k_stride, const void* v, int64_t v_stride,

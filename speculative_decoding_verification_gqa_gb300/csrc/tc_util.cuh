@@ -17,6 +17,9 @@ namespace sv {
 // the encoding fails.
 bool kv_tensor_map(CUtensorMap* map, const void* base, int64_t kv_rows, int hkv, int hd,
                    bool fp8, int box_rows);
+// The same of 4-bit codes: boxes of a head's whole row (attn_tc.cu).
+bool kv4_tensor_map(CUtensorMap* map, const void* base, int64_t kv_rows, int hkv, int hd,
+                    int box_rows);
 
 namespace {
 

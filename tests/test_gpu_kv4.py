@@ -9,7 +9,7 @@ import speculative_decoding_verification_gqa_gb300 as sv
 from speculative_decoding_verification_gqa_gb300 import api
 
 from gpu_util import ensure_built
-from kv4_util import (Cache, DEV, E2M1, attention, block_table, e4m3_values, i32, quantise,
+from kv4_util import (Cache, DEV, attention, block_table, e4m3_values, i32, quantise,
                       values)
 
 pytestmark = pytest.mark.gpu
@@ -251,6 +251,14 @@ def check_out(out, lse, want, L, size, spread):
         assert ((lse.double() - L).abs() <= tol_l).all()
 
 
+@pytest.fixture(params=[1, 2], ids=["mma", "tcgen05"])
+def kernel(request):
+    """Both attention kernels, whatever the call's rows."""
+    prev = sv.set_attn_kernel(request.param)
+    yield request.param
+    sv.set_attn_kernel(prev)
+
+
 def run_attn(c, q, T, D, window=0, scale=0.0, max_seq=None, **kw):
     out = torch.full_like(q, 5.0)
     lse = torch.full(q.shape[:2], 5.0, device=DEV)
@@ -292,7 +300,7 @@ def check_attn(T, D, Hq, Hkv, d, bs, window=0, scale=0.0, seed=0, tail=2):
     ([127, 128, 129], [1, 0, 3]),        # tile edges
     ([500, 3, 0, 257], [3, 7, 2, 0]),    # windows across edges
 ])
-def test_small_batches(d, Hq, Hkv, T, D):
+def test_small_batches(kernel, d, Hq, Hkv, T, D):
     check_attn(T, D, Hq, Hkv, d, 16)
 
 
@@ -306,23 +314,23 @@ def test_small_batches(d, Hq, Hkv, T, D):
     ([100] * 70, [b % 4 for b in range(70)], 28, 4, 128, 16),
     ([513, 2, 1025], [7, 8, 3], 32, 4, 128, 1024),
 ])
-def test_larger_batches(T, D, Hq, Hkv, d, bs):
+def test_larger_batches(kernel, T, D, Hq, Hkv, d, bs):
     check_attn(T, D, Hq, Hkv, d, bs, seed=T[0])
 
 
 @pytest.mark.parametrize("window", [1, 5, 32, 100, 129, 1000, 100000])
 @pytest.mark.parametrize("D", [0, 3, 17])
-def test_sliding_windows(window, D):
+def test_sliding_windows(kernel, window, D):
     check_attn([0, 70, 700], [D, D, D // 2], 8, 2, 128, 16, window=window)
 
 
 @pytest.mark.parametrize("scale", [0.01, 1.0, 3.0])
-def test_scales(scale):
+def test_scales(kernel, scale):
     """3.0: scores of some hundreds, weights that are zero but for a few keys."""
     check_attn([333, 50], [2, 0], 8, 2, 128, 16, scale=scale)
 
 
-def test_rising_scores_move_the_reference():
+def test_rising_scores_move_the_reference(kernel):
     """Keys in ascending order of score: the reference maximum moves all the way."""
     c = Cache("kv4", [3001], 1, 128, 16, 5)
     q = make_q(1, 4, 128, 9)
@@ -339,7 +347,7 @@ def test_rising_scores_move_the_reference():
 
 
 @pytest.mark.parametrize("big", [1e30, 1e-30, 3e38])
-def test_queries_of_any_magnitude(big):
+def test_queries_of_any_magnitude(kernel, big):
     """Rows of large and of tiny elements: the softmax scale takes the magnitude back."""
     c = Cache("kv4", [200], 2, 128, 16, 3)
     q = make_q(1, 8, 128, 4)
@@ -354,7 +362,7 @@ def test_queries_of_any_magnitude(big):
 
 
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
-def test_a_query_row_with_an_infinity_is_nan_and_alone(bad):
+def test_a_query_row_with_an_infinity_is_nan_and_alone(kernel, bad):
     c = Cache("kv4", [300], 2, 128, 16, 3)
     q = make_q(1, 8, 128, 4)
     good, lse0, _ = run_attn(c, q, [299], [0])
@@ -367,7 +375,7 @@ def test_a_query_row_with_an_infinity_is_nan_and_alone(bad):
 
 
 @pytest.mark.parametrize("D", [0, 7, 31])
-def test_nan_rows_reach_their_head_only(D):
+def test_nan_rows_reach_their_head_only(kernel, D):
     """A NaN block of K at a position: the rows that see it; of V: all rows of the sequence and
     head may; other heads and sequences not."""
     T, Hkv, G = [400, 90], 2, 4
@@ -388,7 +396,7 @@ def test_nan_rows_reach_their_head_only(D):
     assert torch.equal(out[:D], good[:D]) and torch.equal(out[D, G:], good[D, G:])
 
 
-def test_zero_head_scales():
+def test_zero_head_scales(kernel):
     """A K scale of 0: even weights; a V scale of 0: zeros."""
     c = Cache("kv4", [100], 2, 128, 16, 3)
     c.hs[0, 0] = 0
@@ -405,7 +413,7 @@ def test_zero_head_scales():
 
 @pytest.mark.parametrize("T,D", [([-1, 5], [0, 0]), ([5, 101], [0, 0]), ([5, 5], [0, 4]), ([5, 5], [0, -1]),
                                  ([5, 95], [0, 1])])
-def test_lengths_out_of_range_leave_the_outputs(T, D):
+def test_lengths_out_of_range_leave_the_outputs(kernel, T, D):
     """At most 100 positions and 3 drafts; rows of the table that hold 96 positions."""
     c = Cache("kv4", [96, 96], 2, 64, 16, 1)
     table = c.table[:, :6].contiguous()
@@ -423,7 +431,7 @@ def test_lengths_out_of_range_leave_the_outputs(T, D):
     assert sv.workspace_status(ws) == 0 and torch.isfinite(out).all() and not (out == 5).all()
 
 
-def test_attention_with_a_table_entry_outside_the_pool():
+def test_attention_with_a_table_entry_outside_the_pool(kernel):
     c = Cache("kv4", [100, 40], 2, 128, 16, 1)
     c.table[0, 2] = c.blocks
     c.table[0, 4] = -7
@@ -448,7 +456,7 @@ def test_empty_batch():
 
 
 @pytest.mark.parametrize("T,D,Hq", [([3000, 17], [0, 0], 8), ([2000, 900], [7, 3], 32)])
-def test_same_bits_again_captured_and_on_another_stream(T, D, Hq):
+def test_same_bits_again_captured_and_on_another_stream(kernel, T, D, Hq):
     Hkv = 2
     c = Cache("kv4", [t + 1 + n for t, n in zip(T, D)], Hkv, 128, 16, 2)
     q = make_q(sum(D) + 2, Hq, 128, 3)
@@ -476,7 +484,7 @@ def test_same_bits_again_captured_and_on_another_stream(T, D, Hq):
         assert torch.equal(o3, out) and torch.equal(l3, lse)
 
 
-def test_two_calls_in_flight():
+def test_two_calls_in_flight(kernel):
     """Two streams, a workspace each."""
     jobs = []
     for k in range(2):
@@ -496,7 +504,7 @@ def test_two_calls_in_flight():
         assert all(torch.equal(o, jobs[k][5]) for o in outs[k])
 
 
-def test_launch_failures_leave_the_workspace_usable():
+def test_launch_failures_leave_the_workspace_usable(kernel):
     T, D = [500], [0]
     c = Cache("kv4", [501], 2, 128, 16, 2)
     q = make_q(1, 8, 128, 3)
@@ -510,5 +518,23 @@ def test_launch_failures_leave_the_workspace_usable():
     assert api.inject_launch_failure(-1) == -1
 
 
-def test_e2m1_table_is_the_formats():
-    assert E2M1 == (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+def test_one_workspace_serves_both_kernels():
+    """Calls of few rows and of many, and either kernel, one after another on one workspace."""
+    jobs = [([700, 30], [0, 0]), ([600, 500], [15, 7]), ([40, 2], [1, 0])]
+    c = Cache("kv4", [800, 600], 2, 128, 16, 2)
+    ws = None
+    desc = sv.paged_attn_desc(make_q(32, 16, 128, 0), c.k, 2, 31, 1000, kv4=True)
+    ws = sv.new_workspace(sv.verify_kv4_workspace_bytes(desc))
+    for which in (0, 2, 1, 0):
+        prev = sv.set_attn_kernel(which)
+        for T, D in jobs:
+            q = make_q(sum(D) + 2, 16, 128, T[0])
+            out, lse, _ = run_attn(c, q, T, D, workspace=ws)
+            r = 0
+            for b, (t, n) in enumerate(zip(T, D)):
+                _, L, want, size, spread = attention(q[r:r + 1 + n], c.dense(b, t + 1 + n, 0), c.dense(b, t + 1 + n, 1),
+                                                     t, n, 8, 128 ** -0.5)
+                check_out(out[r:r + 1 + n], lse[r:r + 1 + n], want, L, size, spread)
+                r += 1 + n
+        sv.set_attn_kernel(prev)
+    assert sv.workspace_status(ws) == 0
