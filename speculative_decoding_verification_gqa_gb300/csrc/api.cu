@@ -23,8 +23,14 @@ namespace {
 constexpr int SWITCH_TILES_TC_FP8 = SV_SWITCH_F8;
 constexpr int SWITCH_TILES_TC_BF16 = SV_SWITCH_BF16;
 constexpr int SWITCH_TILES_MMA = 2;
+// 4-bit cache: a unit's start and the join in tiles' time; units from which on two neighbouring heads make
+// one; tiles of the longest sequence up to which a CTA takes a whole unit.
 constexpr int SWITCH_TILES_KV4 = 9;
-constexpr int TILE_FLOOR_KV4 = 259;
+constexpr int SWITCH_TILES_KV4_MMA = 2;
+constexpr int JOIN_TILES_KV4 = 12;
+constexpr int JOIN_TILES_KV4_MMA = 6;
+constexpr int KV4_PAIR_UNITS = 16;
+constexpr int KV4_WHOLE_TILES = 4;
 // Shared prefixes. A unit's start in 128-key tiles of 256 rows and in 64-key tiles of 128 rows,
 // and the SM time of the latter (two at a time on an SM) in the former. Measured around them at
 // d = 128 (short runs of calls back to back, below the power limit; 64 sequences over a prefix
@@ -793,8 +799,8 @@ float scale_log2_of(const sv_attn_desc* d) {
   return scale * 1.4426950408889634f;
 }
 
-int kv4_rows_per_head(const sv_attn_desc* d) {
-  return d->num_q_heads / d->num_kv_heads * (1 + d->max_draft_len);
+int64_t kv4_rows_per_head(const sv_attn_desc* d) {
+  return (int64_t)(d->num_q_heads / d->num_kv_heads) * (1 + d->max_draft_len);
 }
 
 // 1 = warp-level MMAs (attn_kv4.cu), 2 = tcgen05 (attn_kv4_tc.cu)
@@ -804,16 +810,41 @@ int pick_kv4(const sv_attn_desc* d) {
   return g_attn_kernel == 2 || kv4_rows_per_head(d) > KV4_SMALL_ROWS ? 2 : 1;
 }
 
-// CTAs of a call at most: what the kernel holds on an SM at once.
-int kv4_ctas(const sv_attn_desc* d, int which, int sms) {
-  return which == 2 ? sms : attn_kv4_ctas(kv4_rows_per_head(d), sms);
+// A call's units and ranges (line.cuh) on `sms` SMs with kernel `which`.
+void kv4_line(const sv_attn_desc* d, int which, int sms, Kv4Attn* p) {
+  const int64_t rows = kv4_rows_per_head(d);
+  const int ctas = which == 2 ? sms : attn_kv4_ctas((int)rows, sms);
+  const int64_t max_tiles = ((int64_t)d->max_seq_len + d->max_draft_len) / KV4_KT + 1;
+  p->mr = which == 2 ? MT : attn_kv4_rows((int)rows);
+  p->switch_tiles = which == 2 ? SWITCH_TILES_KV4 : SWITCH_TILES_KV4_MMA;
+  const int64_t per_head = (rows + p->mr - 1) / p->mr;  // row tiles
+  p->heads = d->num_kv_heads % 2 == 0 && (int64_t)d->batch * d->num_kv_heads >= KV4_PAIR_UNITS ? 2 : 1;
+  const int64_t units = (int64_t)d->batch * (d->num_kv_heads / p->heads) * per_head;
+  p->n_ctas = which == 2 ? ctas / p->heads : ctas;
+  p->join_tiles = which == 2 ? JOIN_TILES_KV4 : JOIN_TILES_KV4_MMA;
+  // Short sequences: a CTA for every unit, and no second launch.
+  p->no_join = which == 1 && max_tiles <= KV4_WHOLE_TILES && units <= 8 * (int64_t)ctas;
+  if (p->no_join) {
+    p->n_ctas = (int)units;
+    p->join_tiles = KV4_WHOLE_TILES;  // (no unit is longer)
+  } else {
+    p->n_ctas = (int)std::min<int64_t>(units * max_tiles, p->n_ctas);
+  }
 }
 
-AttnWs kv4_layout(const sv_attn_desc* d, int sms) {
-  // room for the most CTAs of either kernel, so that the workspace of a larger shape serves a
-  // smaller one, under any sv_set_attn_kernel
-  return attn_ws_layout(d->batch, d->num_kv_heads, d->num_q_heads / d->num_kv_heads, d->head_dim,
-                        d->max_draft_len, attn_kv4_ctas(1, sms));
+struct Kv4Ws {
+  size_t part_o, part_ml, total;
+};
+Kv4Ws kv4_layout(const sv_attn_desc* d, int sms) {
+  // The parts of either kernel and any rule on its units, so that the workspace of a larger
+  // shape serves a smaller one, under any sv_set_attn_kernel: at most two a range, its heads
+  // (two) times rows of each.
+  const size_t rows = std::max<size_t>(2 * (size_t)sms * MT, 2 * (size_t)attn_kv4_ctas(1, sms) * 2 * 16);
+  Kv4Ws w;
+  w.part_o = 256;
+  w.part_ml = w.part_o + rows * d->head_dim * sizeof(float);
+  w.total = w.part_ml + rows * sizeof(float2);
+  return w;
 }
 
 }  // namespace
@@ -882,8 +913,9 @@ SV_API sv_status spec_verify_attn_kv4(const sv_attn_desc* desc, const void* q,
   if (desc->kv_dtype != SV_KV4) return SV_ERR_DTYPE;
   st = check_kv4(pages);
   if (st != SV_OK) return st;
+  // (rows of q and heads together are indexed with 32 bits)
   if (pages->num_kv_heads != desc->num_kv_heads || pages->head_dim != desc->head_dim ||
-      max_blocks_per_seq < 1)
+      max_blocks_per_seq < 1 || desc->q_rows > 0x7fffffff / desc->num_q_heads)
     return SV_ERR_SHAPE;
   if (desc->batch == 0) return SV_OK;
   if (!q || !block_table || !seq_lens || !draft_len || !out || !workspace) return SV_ERR_NULL;
@@ -892,49 +924,50 @@ SV_API sv_status spec_verify_attn_kv4(const sv_attn_desc* desc, const void* q,
     return SV_ERR_ALIGN;
   const int sms = current_sms();
   if (sms <= 0) return SV_ERR_CUDA;
-  const AttnWs lay = kv4_layout(desc, sms);
+  const Kv4Ws lay = kv4_layout(desc, sms);
   if (workspace_bytes < lay.total) return SV_ERR_WORKSPACE;
 
-  const PagedArgs pg = {block_table, max_blocks_per_seq, pages->block_size, pages->num_blocks};
   const int which = pick_kv4(desc);
-  AttnParams p = shape_params(desc, pg, which, sms);
-  if (which == 2) {
-    p.switch_tiles = SWITCH_TILES_KV4;
-    p.tile_floor = TILE_FLOOR_KV4;
-  }
-  // no more CTAs than tiles (the combine kernel reads every CTA's range that a unit spans);
-  // both kernels' tiles are 128 keys
-  const int64_t tiles = (int64_t)desc->batch * desc->num_kv_heads *
-                        ((kv4_rows_per_head(desc) + MT - 1) / MT) *
-                        (((int64_t)desc->max_seq_len + desc->max_draft_len) / attn_kv4_kt() + 1);
-  p.n_ctas = (int)std::min<int64_t>(tiles, kv4_ctas(desc, which, sms));
   uint8_t* ws = (uint8_t*)workspace;
+  Kv4Attn p = {};
   p.q = q;
   p.k = pages->k_codes;
   p.v = pages->v_codes;
-  p.kv4_scales = pages->scales;
-  p.out = out;
-  p.lse = lse;
+  p.scales = pages->scales;
   p.kv_scale = pages->kv_scale;
   p.seq_lens = seq_lens;
   p.draft_len = draft_len;
-  p.flags = (uint32_t*)(ws + lay.ctrl);
-  p.hdr = (PlanHdr*)(ws + lay.hdr);
-  p.q_off = (int64_t*)(ws + lay.q_off);
-  p.kv_off = (int64_t*)(ws + lay.kv_off);
-  p.units = (int4*)(ws + lay.units);
-  p.ubeg = (int32_t*)(ws + lay.ubeg);
-  p.cta_tab = (int2*)(ws + lay.cta_tab);
+  p.block_table = block_table;
+  p.out = out;
+  p.lse = lse;
+  p.flags = (uint32_t*)ws;
   p.part_o = (float*)(ws + lay.part_o);
   p.part_ml = (float2*)(ws + lay.part_ml);
-  p.block_table = block_table;
+  p.B = desc->batch;
+  p.Hq = desc->num_q_heads;
+  p.Hkv = desc->num_kv_heads;
+  p.G = p.Hq / p.Hkv;
+  p.d = desc->head_dim;
+  p.max_draft = desc->max_draft_len;
+  p.max_seq = desc->max_seq_len;
+  // a window covering every position of the longest sequence is no window
+  p.window = (int64_t)desc->sliding_window > (int64_t)desc->max_seq_len + desc->max_draft_len
+                 ? 0
+                 : desc->sliding_window;
+  p.bt_stride = max_blocks_per_seq;
+  p.block_size = pages->block_size;
+  while ((1 << p.bs_log2) < p.block_size) ++p.bs_log2;
+  p.num_blocks = pages->num_blocks;
+  p.q_rows = desc->q_rows;
+  p.scale_log2 = scale_log2_of(desc);
+  kv4_line(desc, which, sms, &p);
   cudaStream_t s = (cudaStream_t)stream;
-  if (launch_plan(p, attn_kv4_kt(), s) != cudaSuccess) return SV_ERR_CUDA;
   if (g_ev_start && cudaEventRecord(g_ev_start, s) != cudaSuccess) return SV_ERR_CUDA;
   if ((which == 2 ? launch_attn_kv4_tc(p, s) : launch_attn_kv4(p, s)) != cudaSuccess)
     return SV_ERR_CUDA;
   if (g_ev_stop && cudaEventRecord(g_ev_stop, s) != cudaSuccess) return SV_ERR_CUDA;
-  return launch_combine(p, s) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
+  if (p.no_join) return SV_OK;
+  return launch_kv4_join(p, sms, s) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 SV_API size_t spec_attn_mass_workspace_size(const sv_attn_desc* desc) {
@@ -1000,7 +1033,7 @@ SV_API sv_status spec_kv_evict(const sv_page_table* table, int32_t n, const int3
   for (int k = 0; k < num_pools; ++k) {
     const int64_t pos = pools[k].page_bytes / table->block_size;
     if (pos % (8 * (int64_t)num_kv_heads) != 0) return SV_ERR_SHAPE;
-    slices += (pos / num_kv_heads + 255) / 256;
+    slices += (pos / num_kv_heads + 31) / 32;  // (evict.cu, SLICE)
   }
   if (n * (int64_t)num_kv_heads * slices > 0x7fffffff) return SV_ERR_SHAPE;
   if (n == 0) return SV_OK;

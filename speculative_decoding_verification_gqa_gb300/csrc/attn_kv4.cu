@@ -18,17 +18,21 @@
 // reference maximum is the same in all lanes of a column and moves only when some lane of the
 // warp sees a score far above it, so the usual tile needs one vote and no exchange.
 //
-// A warp takes chunks of 32 keys, its own ring of cp.async stages, its own (O, m, l); the CTA's
-// four warps meet only at the end of a unit, where the parts are joined by the rule of the
-// online softmax. Units, tile line and the join across CTAs: internal.cuh.
+// A warp takes chunks of 32 keys of one KV head, its own ring of cp.async stages, its own (O, m,
+// l). The CTA's four warps are spread over the unit's neighbouring heads, then over its keys;
+// they meet only at the end of a unit, where a head's parts are joined by the rule of the
+// online softmax. Units, their line and the join across CTAs (kv4_join, below): line.cuh.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 #include "kv4.cuh"
+#include "line.cuh"
 
 namespace sv {
 namespace {
 
-constexpr int KT = 128;            // keys per tile of the line
+constexpr int KT = KV4_KT;         // keys per tile of the line
 constexpr int CK = 32;             // keys of a chunk
 constexpr int NW = 4;              // warps
 constexpr int NTHREADS = NW * 32;
@@ -99,85 +103,97 @@ constexpr int warp_bytes() {
 // t) by eight elements' bytes, meet every bank once.
 __device__ __forceinline__ int v_place(int kk) { return (kk & ~7) | ((kk & 1) << 2) | ((kk >> 1) & 3); }
 
-// NT: n-tiles of 8 query rows. The unit's rows are taken 8 NT at a time, each pass over the
-// unit's keys of this CTA.
-template <int HD, int NT>
-__global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3) attn_kv4_kernel(const AttnParams p) {
+// Four columns of an output row from O (unnormalised) and the row's (reference, sum).
+template <int HD>
+__device__ __forceinline__ void store_row(const Kv4Attn& p, int64_t row, int g, int c, const float4& o,
+                                          float m, float l) {
+  const float inv = p.kv_scale[p.Hkv + g] / l;
+  const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+  const __nv_bfloat162 y = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  *reinterpret_cast<uint2*>((uint16_t*)p.out + row * HD + c * 4) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+  if (p.lse && c == 0) p.lse[row] = (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// NT: n-tiles of 8 query rows, of which a unit has as many for each of its heads. HG: heads of a
+// unit; warp w takes head w % HG and every (NW / HG)-th chunk of its keys.
+template <int HD, int NT, int HG>
+__global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3) attn_kv4_kernel(const Kv4Attn p) {
   using L = L4<HD>;
-  constexpr int KS = L::KS, ROWS = 8 * NT;
+  constexpr int KS = L::KS, ROWS = 8 * NT, NK = NW / HG;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_m[NW][ROWS], s_l[NW][ROWS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r8 = lane >> 2, t4 = lane & 3;
+  const int hg = warp % HG, kw = warp / HG;
   uint8_t* ring = smem + warp * warp_bytes<HD, NT>();
   pdl_trigger();
   pdl_wait();
-  const int2 rb = p.cta_tab[blockIdx.x], re = p.cta_tab[blockIdx.x + 1];
-  const int64_t t_begin = rb.x, t_end = re.x;
-  if (t_begin >= t_end) return;
-  int u = rb.y;
+  LineWalk walk;
+  if (!line_begin<NTHREADS>(p, blockIdx.x, walk)) return;
 
-  for (int64_t t = t_begin; t < t_end; ++u) {
-    if (u >= p.hdr->num_units) break;  // cannot happen for a valid plan
-    const int4 info = p.units[u];
-    const int b = info.x, g = info.y, mt = info.z;
-    const int64_t ub = p.ubeg[u];
-    const int nt = p.ubeg[u + 1] - (int)ub;
-    const int l0 = (int)(t - ub);
-    const int l1 = (int)(min(t_end, ub + nt) - ub);
-    if (l1 <= l0) break;  // cannot happen for a valid plan
-    t = ub + l1;
-    const int T = p.seq_lens[b], D = p.draft_len[b];
-    const int rows_total = p.G * (D + 1);
-    const int rows = min(MT, rows_total - mt * MT);
-    const int nkeys = T + D + 1;
-    const int kvis = first_visible_key(T, p.window);
-    const int64_t qo = p.q_off[b];
-    const float sck = p.scale_log2 * p.kv_scale[g];
-    const int key_first = info.w + l0 * KT;
-    // chunks with a key of the sequence; this warp takes warp, warp + NW, ...
-    const int chunks = min((l1 - l0) * (KT / CK), (nkeys - key_first + CK - 1) / CK);
-    const int mine = chunks > warp ? (chunks - warp + NW - 1) / NW : 0;
-    const int32_t* tab = p.block_table + (size_t)b * p.bt_stride;
-    const bool whole = l0 == 0 && l1 == nt;
+  LineSeg seg;
+  while (walk.next(p, seg)) {
+    {
+      const int b = seg.b, g = seg.g * HG + hg;
+      const int T = seg.T, D = seg.D;
+      const int row0 = seg.mt * ROWS;                 // of the (sequence, head)'s rows
+      const int rows = min(ROWS, p.G * (D + 1) - row0);
+      const int nkeys = T + D + 1;
+      const int kvis = first_visible_key(T, p.window);
+      const int64_t qo = seg.q_off;
+      const float sck = p.scale_log2 * p.kv_scale[g];
+      const int key_first = seg.kbase + seg.j0 * KT;
+      // chunks with a key of the sequence; this warp takes kw, kw + NK, ...
+      const int chunks = min((seg.j1 - seg.j0) * (KT / CK), (nkeys - key_first + CK - 1) / CK);
+      const int mine = chunks > kw ? (chunks - kw + NK - 1) / NK : 0;
+      const int32_t* tab = p.block_table + (size_t)b * p.bt_stride;
 
-    for (int sub = 0; sub < rows; sub += ROWS) {
       // ---- the ring. Eight consecutive keys lie in one block: a chunk has four table entries,
-      // read a chunk ahead by the lanes
+      // read a chunk ahead by the lanes, and from each lane's first address on everything is
+      // the entry's row times the bytes of a cache position
+      constexpr int CH = L::RB / 16;  // 16-byte pieces of a row's codes
+      const int code_bytes = p.Hkv * L::RB, scale_bytes = p.Hkv * L::SB;  // of a position
+      const int64_t lane_at = (int64_t)(lane / CH % 8) * code_bytes + g * L::RB + lane % CH * 16;
+      const uint8_t *kp = (const uint8_t*)p.k + lane_at, *vp = (const uint8_t*)p.v + lane_at;
+      const uint8_t* sp = (const uint8_t*)p.scales + (int64_t)(lane & 7) * scale_bytes + g * L::SB;
+      const uint32_t ring_at = smem_u32(ring);
+      // this lane's V place within the 32 / CH keys that a step covers
+      const uint32_t v_at = L::CODES + v_place(lane / CH) * L::RB +
+                            (CH == 4 ? (lane % CH) ^ (((lane / CH >> 2) & 1) << 1) : lane % CH) * 16;
+      constexpr int UNSEEN = -2;
       auto entry = [&](int i) -> int {  // this lane's entry of the warp's i-th chunk
-        const int pos = key_first + (warp + i * NW) * CK + 8 * t4;
-        if (i >= mine || pos >= nkeys || pos + 8 <= kvis) return 0;
+        const int pos = key_first + (kw + i * NK) * CK + 8 * t4;
+        if (i >= mine || pos >= nkeys || pos + 8 <= kvis) return UNSEEN;
         return __ldg(tab + (pos >> p.bs_log2));
       };
       int ent = entry(0);
       auto issue = [&](int i) {
         if (i < mine) {
-          uint8_t* st = ring + (i % ST) * L::STAGE;
-          const int key0 = key_first + (warp + i * NW) * CK;
-          constexpr int CH = L::RB / 16;  // 16-byte pieces of a row's codes
+          const uint32_t st = ring_at + (i % ST) * L::STAGE;
+          const int key0 = key_first + (kw + i * NK) * CK;
+          const bool full = key0 >= kvis && key0 + CK <= nkeys;
+          int base = -1;  // cache row of the first of this lane's eight keys
+          if (ent >= 0 && ent < p.num_blocks)
+            base = (ent << p.bs_log2) + ((key0 + 8 * t4) & (p.block_size - 1));
+          else if (ent != UNSEEN)
+            atomicOr(p.flags, FLAG_ATTN_SHAPE);  // an entry outside the pool
+          auto step = [&](bool all) {
 #pragma unroll
-          for (int j = 0; j < CH; ++j) {
-            const int kk = (j * 32 + lane) / CH, c = lane & (CH - 1);
-            const int blk = __shfl_sync(0xffffffffu, ent, kk >> 3);
-            const int key = key0 + kk;
-            bool ok = key < nkeys && key >= kvis;
-            if (ok && (blk < 0 || blk >= p.num_blocks)) {
-              atomicOr(p.flags, FLAG_ATTN_SHAPE);
-              ok = false;
+            for (int j = 0; j < CH; ++j) {
+              const int kk = (j * 32 + lane) / CH;
+              const int row = __shfl_sync(0xffffffffu, base, kk >> 3);
+              const bool ok = row >= 0 && (all || (key0 + kk < nkeys && key0 + kk >= kvis));
+              const int64_t off = ok ? (int64_t)row * code_bytes : 0;
+              cp_async<16>(st + (j * 32 + lane) * 16, kp + off, ok);
+              cp_async<16>(st + v_at + j * (32 / CH) * L::RB, vp + off, ok);
             }
-            const int64_t row = ok ? ((int64_t)blk << p.bs_log2) + (key & (p.block_size - 1)) : 0;
-            const size_t off = (size_t)(row * p.Hkv + g) * L::RB + c * 16;
-            cp_async<16>(smem_u32(st + kk * L::RB + c * 16), (const uint8_t*)p.k + off, ok);
-            const int vc = CH == 4 ? c ^ (((kk >> 2) & 1) << 1) : c;
-            cp_async<16>(smem_u32(st + L::CODES + v_place(kk) * L::RB + vc * 16),
-                         (const uint8_t*)p.v + off, ok);
-          }
-          const int blk = __shfl_sync(0xffffffffu, ent, lane >> 3);
-          const int key = key0 + lane;
-          const bool ok = key < nkeys && key >= kvis && blk >= 0 && blk < p.num_blocks;
-          const int64_t row = ok ? ((int64_t)blk << p.bs_log2) + (key & (p.block_size - 1)) : 0;
-          cp_async<L::SB>(smem_u32(st + 2 * L::CODES + lane * L::SB),
-                          (const uint8_t*)p.kv4_scales + (size_t)(row * p.Hkv + g) * L::SB, ok);
+            const int row = __shfl_sync(0xffffffffu, base, lane >> 3);
+            const bool ok = row >= 0 && (all || (key0 + lane < nkeys && key0 + lane >= kvis));
+            cp_async<L::SB>(st + 2 * L::CODES + lane * L::SB, sp + (ok ? (int64_t)row * scale_bytes : 0), ok);
+          };
+          if (full) step(true);
+          else step(false);
           ent = entry(i + 1);
         }
         cp_async_commit();
@@ -191,9 +207,9 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3) attn_kv4_kernel(con
       int i_col[NT][2];  // window row of those columns
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int r = sub + n * 8 + r8;  // row of the unit
+        const int r = n * 8 + r8;
         const bool live = r < rows;
-        const int rg = mt * MT + (live ? r : 0);
+        const int rg = row0 + (live ? r : 0);
         const uint4* src = reinterpret_cast<const uint4*>(
             (const uint16_t*)p.q + ((qo + rg / p.G) * p.Hq + (int64_t)g * p.G + rg % p.G) * HD +
             t4 * (HD / 4));
@@ -243,7 +259,7 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3) attn_kv4_kernel(con
         issue(i + ST - 1);
         const uint8_t* st = ring + (i % ST) * L::STAGE;
         const uint8_t* sS = st + 2 * L::CODES;
-        const int key0 = key_first + (warp + i * NW) * CK;
+        const int key0 = key_first + (kw + i * NK) * CK;
 
         // ---- S^T = K Q^T
         float s[2][NT][4];
@@ -292,33 +308,44 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3) attn_kv4_kernel(con
             }
           }
         }
-        // ---- scale, mask, reference maximum
-        const bool edge = key0 + CK > T || key0 < lo_max;
-        bool above = false;
+        // ---- mask, exponents above the reference, raised where one is far above
+        if (key0 + CK > T || key0 < lo_max) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float x = s[h][n][e] * sc[n][e & 1];
-              if (edge) {
+              for (int e = 0; e < 4; ++e) {
                 const int key = key0 + h * 16 + r8 + (e >> 1) * 8;
                 const int hi = T + i_col[n][e & 1];
-                if (key > hi || (p.window > 0 && key <= hi - p.window)) x = -INFINITY;
+                if (key > hi || (p.window > 0 && key <= hi - p.window)) s[h][n][e] = -INFINITY;
               }
-              s[h][n][e] = x;
-              above |= x > m[n][e & 1] + (SHIFT + RESCALE);
-            }
-        if (__any_sync(0xffffffffu, above)) {  // (m -inf: any finite score)
+        }
+        float x[2][NT][4];
+        bool above = false;
+        auto exponents = [&](int n, int e) {  // of column e of n-tile n
+          const float nm = m[n][e] == -INFINITY ? 0.f : -m[n][e];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            x[h][n][e] = fmaf(s[h][n][e], sc[n][e], nm);
+            x[h][n][e + 2] = fmaf(s[h][n][e + 2], sc[n][e], nm);
+          }
+          return fmaxf(fmaxf(x[0][n][e], x[0][n][e + 2]), fmaxf(x[1][n][e], x[1][n][e + 2]));
+        };
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            above |= exponents(n, e) > (m[n][e] == -INFINITY ? -INFINITY : SHIFT + RESCALE);
+        if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float x = fmaxf(fmaxf(s[0][n][e], s[0][n][e + 2]), fmaxf(s[1][n][e], s[1][n][e + 2]));
+              float y = fmaxf(fmaxf(s[0][n][e], s[0][n][e + 2]), fmaxf(s[1][n][e], s[1][n][e + 2])) * sc[n][e];
 #pragma unroll
-              for (int o2 = 4; o2 < 32; o2 <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o2));
-              const float mn = fmaxf(m[n][e], x - SHIFT);
+              for (int o2 = 4; o2 < 32; o2 <<= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o2));
+              const float mn = fmaxf(m[n][e], y - SHIFT);
               const float al = mn == -INFINITY ? 1.f : ex2(m[n][e] - mn);
               m[n][e] = mn;
               l[n][e] *= al;
@@ -327,24 +354,23 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3) attn_kv4_kernel(con
                 o[k][n][e] *= al;
                 o[k][n][e + 2] *= al;
               }
+              exponents(n, e);
             }
         }
-        // ---- P = 2^(s - m), its fragments
+        // ---- P = 2^x, its fragments
         uint32_t pf[2][NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0];
-          const float m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float a0 = ex2(s[h][n][0] - m0), a1 = ex2(s[h][n][1] - m1);
-            const float a2 = ex2(s[h][n][2] - m0), a3 = ex2(s[h][n][3] - m1);
-            l[n][0] += a0 + a2;
-            l[n][1] += a1 + a3;
-            pf[h][n][0] = transpose8x8(pack_f16(a0, a1));
-            pf[h][n][1] = transpose8x8(pack_f16(a2, a3));
+            float a[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[e] = ex2(x[h][n][e]);
+            l[n][0] += a[0] + a[2];
+            l[n][1] += a[1] + a[3];
+            pf[h][n][0] = transpose8x8(pack_f16(a[0], a[1]));
+            pf[h][n][1] = transpose8x8(pack_f16(a[2], a[3]));
           }
-        }
         // ---- O^T += V^T P^T
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -412,9 +438,9 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3) attn_kv4_kernel(con
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = n * 8 + 2 * t4 + e;
-          float M = s_m[0][r];
+          float M = s_m[hg][r];
 #pragma unroll
-          for (int w = 1; w < NW; ++w) M = fmaxf(M, s_m[w][r]);
+          for (int w = 1; w < NK; ++w) M = fmaxf(M, s_m[hg + w * HG][r]);
           const float f = m[n][e] == -INFINITY ? 0.f : ex2(m[n][e] - M);
           // elements: m-tile i, fragment rows r8 and r8 + 8 are (HD / 8) r8 + 2 i and + 1
           float* dst = part + r * L::OSTRIDE + r8 * (HD / 8);
@@ -425,36 +451,31 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3) attn_kv4_kernel(con
         }
       __syncthreads();
       // (a warp without chunks: m = -inf, O = 0; a NaN in l or O stays)
-      for (int idx = tid; idx < ROWS * (HD / 4); idx += NTHREADS) {
-        const int r = idx / (HD / 4), c = idx % (HD / 4);
-        if (sub + r >= rows) break;
+      for (int idx = tid; idx < HG * ROWS * (HD / 4); idx += NTHREADS) {
+        const int c = idx % (HD / 4), r = idx / (HD / 4) % ROWS, h = idx / (HD / 4) / ROWS;
+        if (r >= rows) continue;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float M = s_m[0][r], lsum = 0.f;
+        float M = s_m[h][r], lsum = 0.f;
 #pragma unroll
-        for (int w = 1; w < NW; ++w) M = fmaxf(M, s_m[w][r]);
+        for (int w = 1; w < NK; ++w) M = fmaxf(M, s_m[h + w * HG][r]);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
+        for (int w = 0; w < NK; ++w) {
+          const int ww = h + w * HG;
           const float4 v = *reinterpret_cast<const float4*>(
-              reinterpret_cast<const float*>(smem + w * warp_bytes<HD, NT>()) + r * L::OSTRIDE + c * 4);
+              reinterpret_cast<const float*>(smem + ww * warp_bytes<HD, NT>()) + r * L::OSTRIDE + c * 4);
           acc.x += v.x;
           acc.y += v.y;
           acc.z += v.z;
           acc.w += v.w;
-          lsum += s_m[w][r] == -INFINITY ? s_l[w][r] : s_l[w][r] * ex2(s_m[w][r] - M);
+          lsum += s_m[ww][r] == -INFINITY ? s_l[ww][r] : s_l[ww][r] * ex2(s_m[ww][r] - M);
         }
-        const int rg = mt * MT + sub + r;
-        const int64_t orow = (qo + rg / p.G) * p.Hq + (int64_t)g * p.G + rg % p.G;
-        if (whole) {
-          const float inv = p.kv_scale[p.Hkv + g] / lsum;
-          const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-          const __nv_bfloat162 y = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-          *reinterpret_cast<uint2*>((uint16_t*)p.out + orow * HD + c * 4) =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-          if (p.lse && c == 0) p.lse[orow] = (M + log2f(lsum)) * 0.6931471805599453f;
+        if (seg.whole) {
+          const int rg = row0 + r, gh = seg.g * HG + h;
+          store_row<HD>(p, (qo + rg / p.G) * p.Hq + (int64_t)gh * p.G + rg % p.G, gh, c, acc, M, lsum);
         } else {
-          const size_t slot = (size_t)blockIdx.x + u;
-          *reinterpret_cast<float4*>(p.part_o + (slot * MT + sub + r) * HD + c * 4) = acc;
-          if (c == 0) p.part_ml[slot * MT + sub + r] = make_float2(M, lsum);
+          const size_t at = ((size_t)(2 * blockIdx.x + seg.begins) * HG + h) * ROWS + r;
+          *reinterpret_cast<float4*>(p.part_o + at * HD + c * 4) = acc;
+          if (c == 0) p.part_ml[at] = make_float2(M, lsum);
         }
       }
       __syncthreads();  // the parts are read before the rings are filled again
@@ -462,25 +483,158 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3) attn_kv4_kernel(con
   }
 }
 
-template <int HD, int NT>
-cudaError_t launch_nt(const AttnParams& p, cudaStream_t s) {
+// ------------------------------------------------------------------------------ join
+
+constexpr int JT = 256;   // threads
+constexpr int JROWS = 8;  // rows of an item
+
+// The units that several CTAs share: their parts, in the CTAs' order, by the rule of the online
+// softmax. An item is JROWS rows of one head of a unit. With few parts a warp takes a row; with
+// many all warps take every eighth part of the same row and add up through shared memory, so
+// that one long sequence's hundreds of parts are not read one after another. Items in
+// contiguous ranges of the grid's CTAs, as the lines are walked.
+template <int HD>
+__global__ void __launch_bounds__(JT) kv4_join_kernel(const Kv4Attn p) {
+  __shared__ float4 s_o[JT / 32][HD / 4];
+  __shared__ float2 s_ml[JT / 32];
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  Line total;
+  if (!line_scan<JT>(p, total, 0, false, nullptr) || total.whole) return;
+  const int per = p.heads * ((p.mr + JROWS - 1) / JROWS);  // items of a unit
+  const int64_t items = total.units * per;
+  int64_t it = (int64_t)blockIdx.x * items / gridDim.x;
+  const int64_t end = (int64_t)(blockIdx.x + 1) * items / gridDim.x;
+  if (it >= end) return;
+  LineAt at;
+  line_scan<JT>(p, total, it / per, true, &at);
+  LineWalk walk = line_enter(p, at, it / per - at.units, true);
+  walk.v0 = 0;
+  walk.v1 = total.virt;
+  constexpr int LN = HD / 4;  // lanes of a row
+  while (it < end) {
+    const int64_t us = walk.us;
+    LineSeg s;
+    walk.next(p, s);  // the whole unit
+    const int64_t first = us + p.switch_tiles;
+    const int c0 = cta_of_tile(first, total.virt, total.ctas);
+    const int c1 = cta_of_tile(first + s.nt - 1, total.virt, total.ctas);
+    const int64_t next = min(end, (it / per + 1) * per);
+    if (c0 == c1) {  // one CTA's: written already
+      it = next;
+      continue;
+    }
+    const int rows = min(p.mr, p.G * (s.D + 1) - s.mt * p.mr);
+    const bool spread = c1 - c0 >= JT / 32;
+    for (; it < next; ++it) {
+      const int i = (int)(it % per), h = i % p.heads, r0 = i / p.heads * JROWS;
+      const int gh = s.g * p.heads + h;
+      // parts c0 + w, c0 + w + step, ... of row r
+      auto gather = [&](int r, int w, int step, float4& acc, float& m, float& l) {
+        constexpr int U = 8;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        m = -INFINITY;
+        l = 0.f;
+        for (int c = c0 + w; c <= c1; c += U * step) {
+          float2 ml[U];
+          float4 v[U];
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            const int cc = c + k * step;
+            const size_t at2 = ((size_t)(2 * cc + (cc == c0)) * p.heads + h) * p.mr + r;
+            ml[k] = cc <= c1 ? __ldcg(p.part_ml + at2) : make_float2(-INFINITY, 0.f);
+            v[k] = cc <= c1 && lane < LN ? __ldcg(reinterpret_cast<const float4*>(p.part_o + at2 * HD) + lane)
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          float mn = m;
+#pragma unroll
+          for (int k = 0; k < U; ++k) mn = fmaxf(mn, ml[k].x);
+          const float mu = mn == -INFINITY ? 0.f : mn;
+          const float f0 = ex2(m - mu);
+          m = mn;
+          l *= f0;
+          acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+#pragma unroll
+          for (int k = 0; k < U; ++k) {
+            // (a part without a reference: O = 0 and l = 0, or NaN, which stays)
+            const float f = ml[k].x == -INFINITY ? 1.f : ex2(ml[k].x - mu);
+            l += ml[k].y * f;
+            acc = make_float4(acc.x + v[k].x * f, acc.y + v[k].y * f, acc.z + v[k].z * f, acc.w + v[k].w * f);
+          }
+        }
+      };
+      auto out_row = [&](int r) {
+        const int rg = s.mt * p.mr + r;
+        return (s.q_off + rg / p.G) * p.Hq + (int64_t)gh * p.G + rg % p.G;
+      };
+      float4 acc;
+      float m, l;
+      if (!spread) {
+        const int r = r0 + warp;
+        if (r < rows) {
+          gather(r, 0, 1, acc, m, l);
+          if (lane < LN) store_row<HD>(p, out_row(r), gh, lane, acc, m, l);
+        }
+      } else {
+        for (int r = r0; r < min(rows, r0 + JROWS); ++r) {
+          gather(r, warp, JT / 32, acc, m, l);
+          if (lane < LN) s_o[warp][lane] = acc;
+          if (lane == 0) s_ml[warp] = make_float2(m, l);
+          __syncthreads();
+          if (warp == 0 && lane < LN) {
+            float M = -INFINITY, ls = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < JT / 32; ++w) M = fmaxf(M, s_ml[w].x);
+#pragma unroll
+            for (int w = 0; w < JT / 32; ++w) {
+              const float f = s_ml[w].x == -INFINITY ? 1.f : ex2(s_ml[w].x - M);
+              const float4 v = s_o[w][lane];
+              ls += s_ml[w].y * f;
+              o = make_float4(o.x + v.x * f, o.y + v.y * f, o.z + v.z * f, o.w + v.w * f);
+            }
+            store_row<HD>(p, out_row(r), gh, lane, o, M, ls);
+          }
+          __syncthreads();
+        }
+      }
+    }
+  }
+}
+
+template <int HD, int NT, int HG>
+cudaError_t launch_nt(const Kv4Attn& p, cudaStream_t s) {
   const size_t smem = (size_t)NW * warp_bytes<HD, NT>();
-  auto kernel = attn_kv4_kernel<HD, NT>;
+  auto kernel = attn_kv4_kernel<HD, NT, HG>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(p.n_ctas), dim3(NTHREADS), smem, s, p);
 }
+template <int HD, int NT>
+cudaError_t launch_nt(const Kv4Attn& p, cudaStream_t s) {
+  return p.heads == 4 ? launch_nt<HD, NT, 4>(p, s)
+         : p.heads == 2 ? launch_nt<HD, NT, 2>(p, s)
+                        : launch_nt<HD, NT, 1>(p, s);
+}
 
 }  // namespace
 
-int attn_kv4_kt() { return KT; }
-// CTAs of a call on `sms` SMs: what an SM holds at once.
+// CTAs of a call on `sms` SMs: what an SM holds at once; query rows of a unit and head.
 int attn_kv4_ctas(int rows_per_kv, int sms) { return sms * (rows_per_kv <= 8 ? 4 : 3); }
+int attn_kv4_rows(int rows_per_kv) { return rows_per_kv <= 8 ? 8 : 16; }
 
-cudaError_t launch_attn_kv4(const AttnParams& p, cudaStream_t s) {
-  const bool one = p.G * (1 + p.max_draft) <= 8;
-  if (p.d == 128) return one ? launch_nt<128, 1>(p, s) : launch_nt<128, 2>(p, s);
-  return one ? launch_nt<64, 1>(p, s) : launch_nt<64, 2>(p, s);
+cudaError_t launch_attn_kv4(const Kv4Attn& p, cudaStream_t s) {
+  if (p.d == 128) return p.mr == 8 ? launch_nt<128, 1>(p, s) : launch_nt<128, 2>(p, s);
+  return p.mr == 8 ? launch_nt<64, 1>(p, s) : launch_nt<64, 2>(p, s);
+}
+
+cudaError_t launch_kv4_join(const Kv4Attn& p, int sms, cudaStream_t s) {
+  const int64_t rows = (int64_t)p.G * (1 + p.max_draft);
+  const int64_t items = (int64_t)p.B * p.Hkv * ((rows + p.mr - 1) / p.mr) * ((p.mr + JROWS - 1) / JROWS);
+  const dim3 grid((unsigned)std::min<int64_t>(items, 4 * (int64_t)sms));
+  return p.d == 128 ? launch_pdl(kv4_join_kernel<128>, grid, dim3(JT), 0, s, p)
+                    : launch_pdl(kv4_join_kernel<64>, grid, dim3(JT), 0, s, p);
 }
 
 }  // namespace sv

@@ -4,10 +4,15 @@
 // The 4-bit rows reach the tensor cores as f16, which holds every value exactly: the codes
 // come to shared memory by TMA, a warpgroup decodes each 128-key tile of K and of V into
 // swizzled f16 operand tiles, and S = Q K^T and O += P V are tcgen05.mma kind::f16 with Q and P
-// in TMEM. Work (units of 128 query rows, tile line, join) as in attn_tc.cu.
+// in TMEM. Units of 128 query rows, their line and the join: line.cuh, kv4_join. Two neighbouring
+// CTAs take the two heads of a unit over the same keys, so that the second head's half of every
+// 128-byte line comes from L2 (with heads read at other times, 8 sequences of 32768 positions
+// and 8 heads took 700 MB from HBM where the codes and scales are 302).
 //
 //   warp 0       TMA producer: a stage is the K and V codes of a tile (boxes of one block each)
 //   warp 1       S issuer           warp 3   P V issuer
+//   warp 2       walks the line: the units of the CTA's range and where their rows lie in q and
+//                out, a unit ahead, through a ring in shared memory that the others read
 //   warps 4-11   softmax: warpgroup w owns keys [64 w, 64 w + 64) of every tile, with a score
 //                buffer S_w, a probability buffer P_w, an accumulator O_w and a running
 //                (reference, sum) of its own, so the two never wait for each other; they join
@@ -16,6 +21,14 @@
 //   warps 12-15  decode: a thread takes a key's row of K and of V. It fetches the row's block
 //                scales itself (cp.async, three tiles ahead; nobody else reads them), zero for
 //                keys outside the sequence, whose values are then zero whatever their codes.
+// 16 warps, because 17 would leave a thread 96 registers (five warps on a scheduler) and a
+// softmax thread holds 64 scores: with some 30 words spilled a tile took 3700 clocks, as next to
+// 220 KB of shared memory L1 has nothing to hold them.
+//
+// At the end of a unit O goes out, and at its start Q comes in, through 2 KB of shared memory a
+// warp, so that global memory sees 64-byte pieces of a row and not 16; the next unit's Q is
+// requested before this unit's O is written. (Row by row in 16-byte pieces, a change of units
+// took 20 thousand clocks, ten tiles' time.)
 //
 // TMEM columns: O_0, O_1 (128 each), S_0, S_1 (64 each), Q (64: f16 pairs), P_0, P_1 (32 each).
 // Every wait is bounded as in attn_tc.cu.
@@ -25,16 +38,18 @@
 
 #include "internal.cuh"
 #include "kv4.cuh"
+#include "line.cuh"
 #include "tc_util.cuh"
 
 namespace sv {
 namespace {
 
-constexpr int KT = 128;           // keys per tile
+constexpr int KT = KV4_KT;        // keys per tile
 constexpr int HK = KT / 2;        // keys per warpgroup per tile
 constexpr int NR = 4;             // raw stages
 constexpr int NSC = 4;            // tiles of block scales
 constexpr int NCV = 2;            // decoded stages, K and V each
+constexpr int NU = 4;             // units known ahead
 constexpr int NTHREADS = 512;
 constexpr int SOFT0 = 4, DEC0 = 12;  // first softmax and decoding warps
 constexpr int NSOFT = 256, NDEC = 128;
@@ -51,6 +66,13 @@ struct __align__(8) Bars {
   uint64_t q_full, s_final, pv_final;
   uint32_t tmem_base;
   int abort;
+  uint32_t qmax[2][128];  // start of a unit: each half row's largest magnitude
+  uint64_t unit_full[NU], unit_empty[NU];
+  struct Unit {
+    int32_t live;         // 0: no more units
+    int32_t b, g, T, D, j0, j1, kbase, rows, row0, begins, whole;
+    int32_t row[MT];      // row of q and out, times Hq, plus its head
+  } unit[NU];
   float xm[2][128], xl[2][128];  // end of a unit: each warpgroup's (reference, sum) per row
 };
 
@@ -65,7 +87,8 @@ struct Lay {
   static constexpr int VC = KC + NCV * TILE;
   static constexpr int RK = VC + NCV * TILE;    // stage s: K codes at RK + 2 s RAW, V behind
   static constexpr int SC = RK + NR * 2 * RAW;
-  static constexpr int BARS = SC + NSC * KT * SB;
+  static constexpr int STG = SC + NSC * KT * SB;  // 2 KB a softmax warp: 32 rows of 64 bytes
+  static constexpr int BARS = STG + NSOFT / 32 * 2048;
   static constexpr size_t SMEM = (size_t)BARS + sizeof(Bars);
   static_assert(SMEM <= 227 * 1024, "dynamic shared memory above the per-CTA limit");
 };
@@ -79,64 +102,38 @@ __device__ __forceinline__ bool elect_one() {
   return e != 0;
 }
 
-// One unit's share of a CTA's range (attn_tc.cu): tiles [j0, j1), tile j at position
-// kbase + j * KT.
-struct Seg {
-  int u, b, g, mt, j0, j1, kbase;
-  bool whole;
-};
-__device__ __forceinline__ bool seg_next(const AttnParams& p, int num_units, int64_t& t,
-                                         int64_t t_end, int& u, Seg& s) {
-  if (t >= t_end || u >= num_units) return false;
-  const int4 info = p.units[u];
-  const int64_t ub = p.ubeg[u];
-  const int nt = p.ubeg[u + 1] - (int)ub;
-  s.u = u;
-  s.b = info.x;
-  s.g = info.y;
-  s.mt = info.z;
-  s.kbase = info.w;
-  s.j0 = (int)(t - ub);
-  s.j1 = (int)(min(t_end, ub + nt) - ub);
-  if (s.j1 <= s.j0) return false;
-  s.whole = s.j0 == 0 && s.j1 == nt;
-  t = ub + s.j1;
-  ++u;
-  return true;
+// One arrival for a whole warp, after everything that its lanes did before.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if (elect_one()) mbar_arrive(bar);
+}
+template <int N>  // bytes: 16 or 8; not ok: zeros, nothing is read
+__device__ __forceinline__ void cp_async_scales(uint32_t dst, const void* src, bool ok) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
 }
 
-__device__ __forceinline__ void cp_async_scales16(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async_scales8(uint32_t dst, const void* src, bool ok) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
-}
-
-// Row r of a decoded tile from its codes (16-byte pieces) and scales: 32 elements a piece, in
+// Row r of a decoded tile from its codes (16-byte pieces, 32 elements each) and block scales, in
 // the 128-byte swizzled layout of 64-column blocks.
 template <int HD>
 __device__ __forceinline__ void decode_row(uint8_t* tile, int r, const uint4 (&w)[HD / 32],
                                            const uint32_t (&scale)[HD / 64]) {
   using L = Lay<HD>;
-  uint32_t u[HD / 16];  // each block's scale, twice
-#pragma unroll
-  for (int k = 0; k < HD / 32; ++k) {
-    const uint32_t f = e4m3x2_to_f16x2(k & 1 ? scale[k >> 1] >> 16 : scale[k >> 1] & 0xffffu);
-    u[2 * k] = lo_twice(f);
-    u[2 * k + 1] = hi_twice(f);
-  }
-  uint8_t* row = tile + r * 128;
+  const uint32_t at = r * 128 + ((r & 7) << 4);  // 16-byte place c of the row: at ^ (c << 4)
 #pragma unroll
   for (int c = 0; c < HD / 32; ++c) {
+    const uint32_t f = e4m3x2_to_f16x2(c & 1 ? scale[c >> 1] >> 16 : scale[c >> 1] & 0xffffu);
+    const uint32_t u[2] = {lo_twice(f), hi_twice(f)};  // the piece's two block scales, each twice
     const uint32_t q[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       uint32_t h[4];
       e2m1x8_to_f16(q[e], h);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) h[k] = hmul2(h[k], u[2 * c + (e >> 1)]);
-      const int chunk = (c & 1) * 4 + e;  // of the block's eight
-      *reinterpret_cast<uint4*>(row + (c >> 1) * L::BLK + ((chunk ^ (r & 7)) << 4)) =
+      for (int k = 0; k < 4; ++k) h[k] = hmul2(h[k], u[e >> 1]);
+      *reinterpret_cast<uint4*>(tile + (at ^ (((c & 1) * 4 + e) << 4)) + (c >> 1) * L::BLK) =
           make_uint4(h[0], h[1], h[2], h[3]);
     }
   }
@@ -144,7 +141,7 @@ __device__ __forceinline__ void decode_row(uint8_t* tile, int r, const uint4 (&w
 
 template <int HD>
 __global__ void __launch_bounds__(NTHREADS, 1)
-    attn_kv4_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tmk,
+    attn_kv4_tc_kernel(const Kv4Attn p, const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv) {
   using L = Lay<HD>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -153,12 +150,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const Waiter wt{abort, p.flags, p.wait_limit > 0 ? p.wait_limit : TIMEOUT_CYCLES};
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, and so are the roles
-  pdl_wait();  // the plan of this call is complete
-
-  const int num_units = p.hdr->num_units;
-  const int2 rb = p.cta_tab[blockIdx.x], re = p.cta_tab[blockIdx.x + 1];
-  const int64_t t_begin = rb.x, t_end = re.x;
-  if (t_begin >= t_end) return;  // uniform across the CTA
+  pdl_wait();
+  LineWalk walk;
+  const int range = blockIdx.x / p.heads, hsel = blockIdx.x % p.heads;
+  if (!line_begin<NTHREADS>(p, range, walk)) return;  // uniform across the CTA
   if (saddr(smem) & 1023) {      // the swizzle phases assume a 1 KiB-aligned base
     if (tid == 0) atomicOr(p.flags, FLAG_ATTN_SHAPE);
     return;
@@ -166,23 +161,27 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   if (tid == 0) {
     for (int s = 0; s < NR; ++s) {
       mbar_init(&bars->raw_full[s], 1);
-      mbar_init(&bars->raw_empty[s], NDEC);
+      mbar_init(&bars->raw_empty[s], NDEC / 32);
     }
     for (int s = 0; s < NCV; ++s) {
-      mbar_init(&bars->kc_full[s], NDEC);
+      mbar_init(&bars->kc_full[s], NDEC / 32);
       mbar_init(&bars->kc_empty[s], 1);
-      mbar_init(&bars->vc_full[s], NDEC);
+      mbar_init(&bars->vc_full[s], NDEC / 32);
       mbar_init(&bars->vc_empty[s], 1);
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&bars->s_full[w], 1);
-      mbar_init(&bars->s_free[w], NSOFT / 2);
-      mbar_init(&bars->p_full[w], NSOFT / 2);
+      mbar_init(&bars->s_free[w], NSOFT / 64);
+      mbar_init(&bars->p_full[w], NSOFT / 64);
       mbar_init(&bars->o_done[w], 1);
     }
-    mbar_init(&bars->q_full, NSOFT);
+    mbar_init(&bars->q_full, NSOFT / 32);
     mbar_init(&bars->s_final, 1);
     mbar_init(&bars->pv_final, 1);
+    for (int s = 0; s < NU; ++s) {
+      mbar_init(&bars->unit_full[s], 1);
+      mbar_init(&bars->unit_empty[s], NTHREADS / 32 - 1);
+    }
     bars->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -201,11 +200,18 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     return __all_sync(0xffffffffu, mbar_wait(bar, par, wt));
   };
   const int window = p.window;
-  int64_t t = t_begin;
-  int u = rb.y;
-  Seg s;
-  uint32_t it = 0;
+  uint32_t it = 0, unit_i = 0;  // tiles and units that this warp has begun
   bool ok = true;
+  Bars::Unit* s = nullptr;
+  // The next unit, by a whole warp of any role but the walker's; false at the end. The unit
+  // before is given back first.
+  auto next_unit = [&]() -> bool {
+    if (unit_i > 0) warp_arrive(&bars->unit_empty[(unit_i - 1) % NU]);
+    s = &bars->unit[unit_i % NU];
+    if (!wwait(&bars->unit_full[unit_i % NU], (unit_i / NU) & 1)) return false;
+    ++unit_i;
+    return s->live != 0;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -218,21 +224,22 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tmv) : "memory");
     }
     const int box = min(p.block_size, KT), nbox = KT / box, tg = 32 / nbox;
-    while (ok && seg_next(p, num_units, t, t_end, u, s)) {
-      const int T = p.seq_lens[s.b], nkeys = T + p.draft_len[s.b] + 1;
+    while (ok && next_unit()) {
+      const int T = s->T, nkeys = T + s->D + 1;
       const int kvis = first_visible_key(T, window);
-      const int32_t* tab = p.block_table + (size_t)s.b * p.bt_stride;
-      auto box_pos = [&](int j, int n) { return s.kbase + j * KT + n * box; };
+      const int32_t* tab = p.block_table + (size_t)s->b * p.bt_stride;
+      const int j0 = s->j0, j1 = s->j1, kbase = s->kbase, g = s->g;
+      auto box_pos = [&](int j, int n) { return kbase + j * KT + n * box; };
       auto visible = [&](int pos) { return pos < nkeys && pos + box > kvis; };
       auto fetch = [&](int jg) -> int {  // this lane's entry of the group starting at tile jg
         const int j = jg + lane / nbox, pos = box_pos(j, lane % nbox);
-        return j < s.j1 && visible(pos) ? __ldg(tab + (pos >> p.bs_log2)) : 0;
+        return j < j1 && visible(pos) ? __ldg(tab + (pos >> p.bs_log2)) : 0;
       };
-      int ent_cur = fetch(s.j0), ent_nxt = fetch(s.j0 + tg);
-      for (int j = s.j0; j < s.j1; ++j, ++it) {
+      int ent_cur = fetch(j0), ent_nxt = fetch(j0 + tg);
+      for (int j = j0; j < j1; ++j, ++it) {
         const uint32_t st = it % NR;
-        const int q = (j - s.j0) % tg;
-        if (q == 0 && j > s.j0) {
+        const int q = (j - j0) % tg;
+        if (q == 0 && j > j0) {
           ent_cur = ent_nxt;
           ent_nxt = fetch(j + tg);
         }
@@ -252,8 +259,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         __syncwarp();
         if (lane < nbox) {
           const uint32_t dst = saddr(smem + L::RK + st * 2 * L::RAW) + lane * box * L::RB;
-          tma_load_3d(dst, &tmk, &bars->raw_full[st], 0, s.g, row);
-          tma_load_3d(dst + L::RAW, &tmv, &bars->raw_full[st], 0, s.g, row);
+          tma_load_3d(dst, &tmk, &bars->raw_full[st], 0, g, row);
+          tma_load_3d(dst + L::RAW, &tmv, &bars->raw_full[st], 0, g, row);
         }
       }
     }
@@ -265,26 +272,51 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         }
       }
     }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ walker
+    bool more = true;
+    for (uint32_t n = 0; more; ++n) {
+      LineSeg g;
+      more = walk.next(p, g);
+      if (n >= NU && !wwait(&bars->unit_empty[n % NU], ((n / NU) - 1) & 1)) break;
+      Bars::Unit* d = &bars->unit[n % NU];
+      if (more) {
+        const int rows = min(MT, p.G * (g.D + 1) - g.mt * MT), head = g.g * p.heads + hsel;
+        for (int i = lane; i < rows; i += 32) {
+          const int rg = g.mt * MT + i;
+          d->row[i] = (int)((g.q_off + rg / p.G) * p.Hq + head * p.G + rg % p.G);
+        }
+        if (lane == 0) {
+          d->b = g.b;
+          d->g = head;
+          d->T = g.T;
+          d->D = g.D;
+          d->j0 = g.j0;
+          d->j1 = g.j1;
+          d->kbase = g.kbase;
+          d->rows = rows;
+          d->row0 = g.mt * MT;
+          d->begins = g.begins;
+          d->whole = g.whole;
+        }
+      }
+      if (lane == 0) d->live = more;
+      warp_arrive(&bars->unit_full[n % NU]);
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------ S_w = Q K_w^T issuer
     constexpr uint32_t ID_S = idesc_f16(HK, 0);
     // K: K-major, 128-byte rows, 8-row groups 1024 B apart; 32 B per K step
     const uint64_t kdesc0 = smem_desc(saddr(smem + L::KC), 16, 1024);
     uint32_t seg_i = 0;
-    while (ok && seg_next(p, num_units, t, t_end, u, s)) {
+    while (ok && next_unit()) {
       if (!wwait(&bars->q_full, seg_i & 1)) break;
       fence_after();
-      for (int j = s.j0; j < s.j1 && ok; ++j, ++it) {
+      for (int n = s->j1 - s->j0; n > 0 && ok; --n, ++it) {
         const uint32_t st = it % NCV;
-        if (!wwait(&bars->kc_full[st], (it / NCV) & 1)) {
-          ok = false;
-          break;
-        }
-        for (int w = 0; w < 2; ++w) {
-          if (it >= 1 && !wwait(&bars->s_free[w], (it - 1) & 1)) {
-            ok = false;
-            break;
-          }
+        ok = wwait(&bars->kc_full[st], (it / NCV) & 1);
+        for (int w = 0; w < 2 && ok; ++w) {
+          if (it >= 1 && !(ok = wwait(&bars->s_free[w], (it - 1) & 1))) break;
           fence_after();
           const uint64_t kd = kdesc0 + ((st * L::TILE + w * HK * 128) >> 4);
           if (elect_one()) {
@@ -310,25 +342,20 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     constexpr uint32_t ID_PV = idesc_f16(HD, 1);
     // V: MN-major, 64-column blocks L::BLK apart (LBO), 8-key groups 1024 B apart (SBO)
     const uint64_t vdesc0 = smem_desc(saddr(smem + L::VC), L::BLK, 1024);
-    while (ok && seg_next(p, num_units, t, t_end, u, s)) {
-      for (int j = s.j0; j < s.j1 && ok; ++j, ++it) {
+    while (ok && next_unit()) {
+      const int tiles = s->j1 - s->j0;
+      for (int j = 0; j < tiles && ok; ++j, ++it) {
         const uint32_t st = it % NCV;
-        if (!wwait(&bars->vc_full[st], (it / NCV) & 1)) {
-          ok = false;
-          break;
-        }
+        ok = wwait(&bars->vc_full[st], (it / NCV) & 1);
         const uint64_t vd = vdesc0 + ((st * L::TILE) >> 4);
-        for (int w = 0; w < 2; ++w) {
-          if (!wwait(&bars->p_full[w], it & 1)) {
-            ok = false;
-            break;
-          }
+        for (int w = 0; w < 2 && ok; ++w) {
+          if (!(ok = wwait(&bars->p_full[w], it & 1))) break;
           fence_after();
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < HK / 16; ++kk)
               mma_ts(tmem + COL_O + w * 128, tmem + COL_P + w * (HK / 2) + kk * 8,
-                     vd + (((w * HK + kk * 16) * 128) >> 4), ID_PV, (j == s.j0 && kk == 0) ? 0u : 1u);
+                     vd + (((w * HK + kk * 16) * 128) >> 4), ID_PV, (j == 0 && kk == 0) ? 0u : 1u);
             mma_commit(&bars->o_done[w]);
             if (w == 1) mma_commit(&bars->vc_empty[st]);
           }
@@ -344,36 +371,60 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   } else if (warp >= SOFT0 && warp < DEC0) {
     // ------------------------------------------------------------ softmax / epilogue
     const int wg = (warp - SOFT0) >> 2;
-    const int r = (warp & 3) * 32 + lane;  // query row = TMEM lane
-    const uint32_t tq = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const int r0w = (warp & 3) * 32;       // the warp's first query row = its quarter of the lanes
+    const int r = r0w + lane;
+    const uint32_t tq = tmem + ((uint32_t)r0w << 16);
     constexpr int OC = HD / 2;             // output columns of a warpgroup in the epilogue
-    while (ok && seg_next(p, num_units, t, t_end, u, s)) {
-      const int T = p.seq_lens[s.b] - s.kbase;  // positions below: relative to kbase
-      const int D = p.draft_len[s.b];
-      const int rows = min(MT, p.G * (D + 1) - s.mt * MT);
-      const bool live = r < rows;
-      const int rg = s.mt * MT + r;
-      const int i_row = live ? rg / p.G : D;
+    constexpr int QC = HD / 64;            // 64-byte pieces of its half of a Q row
+    uint8_t* stg = smem + L::STG + (warp - SOFT0) * 2048;
+    // 16-byte place c of row i in the staging area: rows are 64 bytes, pairs of rows exchange
+    // places so that eight lanes, of one row each or four of two, meet every bank once
+    auto place = [&](int i, int c) { return stg + i * 64 + ((c ^ ((i >> 1) & 3)) << 4); };
+    const int si = lane >> 2, sc4 = lane & 3;  // row (of eight) and place of a coalesced access
+    uint4 qv[QC][4];
+    auto request_q = [&]() {  // of unit s
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = r0w + k * 8 + si;
+        const bool have = i < s->rows;
+        const uint4* src = reinterpret_cast<const uint4*>((const uint16_t*)p.q +
+                                                          (int64_t)(have ? s->row[i] : 0) * HD + wg * (HD / 2)) + sc4;
+#pragma unroll
+        for (int c = 0; c < QC; ++c) qv[c][k] = have ? __ldg(src + c * 4) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    bool more = next_unit();
+    if (more) request_q();
+    while (ok && more) {
+      const int T = s->T - s->kbase;  // positions below: relative to kbase
+      const int rows = s->rows, j0 = s->j0, j1 = s->j1;
+      const int i_row = r < rows ? (s->row0 + r) / p.G : s->D;
       const int hi_row = T + i_row;            // the row's last visible key
       const int lo_row = hi_row + 1 - window;  // its first, under a sliding window
-      const int64_t orow = (p.q_off[s.b] + i_row) * p.Hq + (int64_t)s.g * p.G + (live ? rg % p.G : 0);
       // Q row x 2^e -> f16 pairs in TMEM; each warpgroup writes its half
       float sc;
       {
-        const uint4* src = reinterpret_cast<const uint4*>((const uint16_t*)p.q + orow * HD);
         uint32_t rq[HD / 4], amax = 0;
 #pragma unroll
-        for (int e = 0; e < HD / 16; ++e) {
-          const uint4 v = live ? __ldg(src + wg * (HD / 16) + e) : make_uint4(0, 0, 0, 0);
-          const uint4 o = live ? __ldg(src + (wg ^ 1) * (HD / 16) + e) : make_uint4(0, 0, 0, 0);
-          rq[4 * e] = v.x;
-          rq[4 * e + 1] = v.y;
-          rq[4 * e + 2] = v.z;
-          rq[4 * e + 3] = v.w;
-          const uint32_t both[8] = {v.x, v.y, v.z, v.w, o.x, o.y, o.z, o.w};
+        for (int c = 0; c < QC; ++c) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) amax = max(amax, max(both[k] & 0x7fffu, (both[k] >> 16) & 0x7fffu));
+          for (int k = 0; k < 4; ++k) *reinterpret_cast<uint4*>(place(k * 8 + si, sc4)) = qv[c][k];
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4 v = *reinterpret_cast<const uint4*>(place(lane, k));
+            rq[16 * c + 4 * k] = v.x;
+            rq[16 * c + 4 * k + 1] = v.y;
+            rq[16 * c + 4 * k + 2] = v.z;
+            rq[16 * c + 4 * k + 3] = v.w;
+          }
+          __syncwarp();
         }
+#pragma unroll
+        for (int e = 0; e < HD / 4; ++e) amax = max(amax, max(rq[e] & 0x7fffu, (rq[e] >> 16) & 0x7fffu));
+        bars->qmax[wg][r] = amax;
+        softmax_pair_and(true);
+        amax = max(amax, bars->qmax[wg ^ 1][r]);
         const float f = exp2_of(q_exponent(amax));
 #pragma unroll
         for (int e = 0; e < HD / 4; ++e)
@@ -383,15 +434,15 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         else
           tmem_st16(tq + COL_Q + wg * 16, rq);
         tmem_wait_st();
-        sc = q_row_scale(p.scale_log2 * p.kv_scale[s.g], amax);
+        sc = q_row_scale(p.scale_log2 * p.kv_scale[s->g], amax);
       }
       fence_before();
-      mbar_arrive(&bars->q_full);
+      warp_arrive(&bars->q_full);
 
       float m_ref = -INFINITY, lh = 0.f;
       uint32_t it_last = 0;
       bool good = true;
-      for (int j = s.j0; j < s.j1; ++j, ++it) {
+      for (int j = j0; j < j1; ++j, ++it) {
         if (!good) continue;
         it_last = it;
         if (!(good = wwait(&bars->s_full[wg], it & 1))) continue;
@@ -406,7 +457,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           for (int c = 0; c < HK / 32; ++c) reg_fence32(raw + c * 32);
         }
         fence_before();
-        mbar_arrive(&bars->s_free[wg]);  // the scores are in registers: the next S_w may start
+        warp_arrive(&bars->s_free[wg]);  // the scores are in registers: the next S_w may start
         const int key0 = j * KT + wg * HK;
         if (key0 + HK - 1 > hi_row) {
           const int lim = hi_row - key0;
@@ -475,7 +526,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         tmem_st32(tq + COL_P + wg * (HK / 2), pk);
         tmem_wait_st();
         fence_before();
-        mbar_arrive(&bars->p_full[wg]);
+        warp_arrive(&bars->p_full[wg]);
       }
       if (good) {
         good = wwait(&bars->o_done[wg], it_last & 1);
@@ -490,6 +541,17 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       fence_after();  // the other warpgroup's accumulator is complete too
 
       // ---- epilogue: join the two accumulators; this warpgroup's half of the columns
+      const Bars::Unit* o = s;
+      const bool whole = o->whole;
+      const size_t part0 = ((size_t)(2 * range + o->begins) * p.heads + hsel) * MT;
+      // (the unit is given back by next_unit: what is needed of it below is read first)
+      int orow[4];  // the rows of this thread's coalesced accesses
+#pragma unroll
+      for (int k = 0; k < 4; ++k) orow[k] = o->row[min(r0w + k * 8 + si, rows - 1)];
+      const int my_row = o->row[min(r, rows - 1)];
+      const float vs = p.kv_scale[p.Hkv + o->g];
+      more = next_unit();
+      if (more) request_q();
       const float m0 = bars->xm[0][r], m1 = bars->xm[1][r];
       const float m = fmaxf(m0, m1);
       const float a0 = m0 == -INFINITY ? 0.f : ex2(m0 - m);
@@ -497,43 +559,60 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       // (a sum without a reference is 0, or NaN, which stays)
       const float l = (m0 == -INFINITY ? bars->xl[0][r] : a0 * bars->xl[0][r]) +
                       (m1 == -INFINITY ? bars->xl[1][r] : a1 * bars->xl[1][r]);
-      const float inv = s.whole ? p.kv_scale[p.Hkv + s.g] / l : 1.f;
-      auto merged = [&](uint32_t o0, uint32_t o1) {  // an accumulator without keys is skipped
-        return (a0 != 0.f ? a0 * __uint_as_float(o0) : 0.f) +
-               (a1 != 0.f ? a1 * __uint_as_float(o1) : 0.f);
-      };
-#pragma unroll 1
-      for (int c = 0; c < OC / 16; ++c) {
-        uint32_t r0[16], r1[16];
-        tmem_ld16(tq + COL_O + wg * OC + c * 16, r0);
-        tmem_ld16(tq + COL_O + 128 + wg * OC + c * 16, r1);
+      const float inv = whole ? vs / l : 1.f;
+      auto joined = [&](int col, float (&v)[16]) {  // 16 columns of this thread's row
+        uint32_t x0[16], x1[16];
+        tmem_ld16(tq + COL_O + col, x0);
+        tmem_ld16(tq + COL_O + 128 + col, x1);
         tmem_wait_ld();
-        reg_fence16(r0);
-        reg_fence16(r1);
-        if (live) {
-          if (s.whole) {
-            uint32_t pk[8];
+        reg_fence16(x0);
+        reg_fence16(x1);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              pk[e] = pack_bf16(merged(r0[2 * e], r1[2 * e]) * inv,
-                                merged(r0[2 * e + 1], r1[2 * e + 1]) * inv);
-            uint4* d4 = reinterpret_cast<uint4*>((uint16_t*)p.out + orow * HD + wg * OC + c * 16);
-            d4[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            d4[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-          } else {
-            const size_t slot = (size_t)blockIdx.x + s.u;
-            float4* d4 = reinterpret_cast<float4*>(p.part_o + (slot * MT + r) * HD + wg * OC + c * 16);
+        for (int e = 0; e < 16; ++e)  // an accumulator without keys is skipped
+          v[e] = ((a0 != 0.f ? a0 * __uint_as_float(x0[e]) : 0.f) +
+                  (a1 != 0.f ? a1 * __uint_as_float(x1[e]) : 0.f)) * inv;
+      };
+      // 64 bytes of each of the warp's rows: from the rows' threads to whole pieces
+      auto flush = [&](uint8_t* base, int row_bytes, bool by_row) {
+        __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              d4[e] = make_float4(merged(r0[4 * e], r1[4 * e]), merged(r0[4 * e + 1], r1[4 * e + 1]),
-                                  merged(r0[4 * e + 2], r1[4 * e + 2]),
-                                  merged(r0[4 * e + 3], r1[4 * e + 3]));
+        for (int k = 0; k < 4; ++k) {
+          const int i = k * 8 + si;
+          const uint4 v = *reinterpret_cast<const uint4*>(place(i, sc4));
+          if (r0w + i < rows)
+            *reinterpret_cast<uint4*>(base + (int64_t)(by_row ? r0w + i : orow[k]) * row_bytes + sc4 * 16) = v;
+        }
+        __syncwarp();
+      };
+      if (whole) {
+#pragma unroll 1
+        for (int c = 0; c < OC / 32; ++c) {  // 32 columns of bf16
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float v[16];
+            joined(wg * OC + c * 32 + h * 16, v);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              *reinterpret_cast<uint4*>(place(lane, 2 * h + e)) =
+                  make_uint4(pack_bf16(v[8 * e], v[8 * e + 1]), pack_bf16(v[8 * e + 2], v[8 * e + 3]),
+                             pack_bf16(v[8 * e + 4], v[8 * e + 5]), pack_bf16(v[8 * e + 6], v[8 * e + 7]));
           }
+          flush((uint8_t*)p.out + (wg * OC + c * 32) * 2, HD * 2, false);
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < OC / 16; ++c) {
+          float v[16];
+          joined(wg * OC + c * 16, v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<float4*>(place(lane, e)) = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          flush((uint8_t*)(p.part_o + part0 * HD + wg * OC + c * 16), HD * 4, true);
         }
       }
-      if (live && wg == 0) {
-        if (!s.whole) p.part_ml[((size_t)blockIdx.x + s.u) * MT + r] = make_float2(m, l);
-        else if (p.lse) p.lse[orow] = (m + log2f(l)) * 0.6931471805599453f;
+      if (r < rows && wg == 0) {
+        if (!whole) p.part_ml[part0 + r] = make_float2(m, l);
+        else if (p.lse) p.lse[my_row] = (m + log2f(l)) * 0.6931471805599453f;
       }
       fence_before();  // TMEM reads above complete before the next unit's MMAs
     }
@@ -545,36 +624,40 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     // codes' 16-byte pieces as TMA swizzled them: the piece's index XOR address bits 7.. (64-
     // byte rows: two bits, 32-byte rows: one)
     const int sw = HD == 128 ? (r >> 1) & 3 : (r >> 2) & 1;
-    while (ok && seg_next(p, num_units, t, t_end, u, s)) {
-      const int T = p.seq_lens[s.b], nkeys = T + p.draft_len[s.b] + 1;
-      const int kvis = first_visible_key(T, window);
-      const int32_t* tab = p.block_table + (size_t)s.b * p.bt_stride;
+    while (ok && next_unit()) {
+      const int nkeys = s->T + s->D + 1;
+      const int kvis = first_visible_key(s->T, window);
+      const int32_t* tab = p.block_table + (size_t)s->b * p.bt_stride;
+      const uint8_t* scales = (const uint8_t*)p.scales + s->g * L::SB;
+      const int64_t row_bytes = (int64_t)p.Hkv * L::SB;
+      const int j0 = s->j0, j1 = s->j1, pos0 = s->kbase + r;
       auto entry = [&](int j) -> int {  // the page of this thread's key of tile j
-        const int pos = s.kbase + j * KT + r;
-        return j < s.j1 && pos < nkeys && pos >= kvis ? __ldg(tab + (pos >> p.bs_log2)) : -1;
+        const int pos = pos0 + j * KT;
+        return j < j1 && pos < nkeys && pos >= kvis ? __ldg(tab + (pos >> p.bs_log2)) : -1;
       };
       auto fetch = [&](int j, int blk) {  // its block scales, into the ring
-        const int pos = s.kbase + j * KT + r;
+        const int pos = pos0 + j * KT;
         const bool have = blk >= 0 && blk < p.num_blocks;
-        const int64_t row = have ? ((int64_t)blk << p.bs_log2) + (pos & (p.block_size - 1)) : 0;
-        const uint8_t* src = (const uint8_t*)p.kv4_scales + (size_t)(row * p.Hkv + s.g) * L::SB;
-        const uint32_t dst = saddr(ssc + (j % NSC) * KT * L::SB);
-        if constexpr (HD == 128) cp_async_scales16(dst, src, have);
-        else cp_async_scales8(dst, src, have);
+        const int row = have ? (blk << p.bs_log2) + (pos & (p.block_size - 1)) : 0;
+        cp_async_scales<L::SB>(saddr(ssc + (j % NSC) * KT * L::SB), scales + row * row_bytes, have);
         asm volatile("cp.async.commit_group;" ::: "memory");
       };
       {
         int e0[NSC - 1];
 #pragma unroll
-        for (int k = 0; k < NSC - 1; ++k) e0[k] = entry(s.j0 + k);
+        for (int k = 0; k < NSC - 1; ++k) e0[k] = entry(j0 + k);
 #pragma unroll
-        for (int k = 0; k < NSC - 1; ++k) fetch(s.j0 + k, e0[k]);
+        for (int k = 0; k < NSC - 1; ++k) fetch(j0 + k, e0[k]);
       }
-      int ent = entry(s.j0 + NSC - 1);
-      for (int j = s.j0; j < s.j1; ++j, ++it) {
+      int ent = entry(j0 + NSC - 1);
+      for (int j = j0; j < j1; ++j, ++it) {
         const uint32_t rs = it % NR, cs = it % NCV;
         fetch(j + NSC - 1, ent);  // (its ring place was read a tile ago)
         ent = entry(j + NSC);
+        const uint32_t free_par = ((it / NCV) - 1) & 1;
+        if (!(ok = wwait(&bars->raw_full[rs], (it / NR) & 1) &&
+                   (it < NCV || wwait(&bars->kc_empty[cs], free_par))))
+          break;
         asm volatile("cp.async.wait_group %0;" ::"n"(NSC - 1) : "memory");
         uint32_t sk[HD / 64], sv[HD / 64];  // E4M3 scales of K and of V
         const uint8_t* sp = ssc + (j % NSC) * KT * L::SB;
@@ -589,10 +672,6 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           sk[0] = v.x;
           sv[0] = v.y;
         }
-        if (!mbar_wait(&bars->raw_full[rs], (it / NR) & 1, wt)) {
-          ok = false;
-          break;
-        }
         uint4 wk[HD / 32], wv[HD / 32];
         const uint8_t* src = rsrc + rs * 2 * L::RAW;
 #pragma unroll
@@ -600,21 +679,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           wk[c] = *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4));
           wv[c] = *reinterpret_cast<const uint4*>(src + L::RAW + ((c ^ sw) << 4));
         }
-        mbar_arrive(&bars->raw_empty[rs]);
-        if (it >= NCV && !mbar_wait(&bars->kc_empty[cs], ((it / NCV) - 1) & 1, wt)) {
-          ok = false;
-          break;
-        }
+        warp_arrive(&bars->raw_empty[rs]);
         decode_row<HD>(smem + L::KC + cs * L::TILE, r, wk, sk);
         fence_proxy_async();
-        mbar_arrive(&bars->kc_full[cs]);
-        if (it >= NCV && !mbar_wait(&bars->vc_empty[cs], ((it / NCV) - 1) & 1, wt)) {
-          ok = false;
-          break;
-        }
+        warp_arrive(&bars->kc_full[cs]);
+        if (!(ok = it < NCV || wwait(&bars->vc_empty[cs], free_par))) break;
         decode_row<HD>(smem + L::VC + cs * L::TILE, r, wv, sv);
         fence_proxy_async();
-        mbar_arrive(&bars->vc_full[cs]);
+        warp_arrive(&bars->vc_full[cs]);
       }
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
@@ -634,24 +706,24 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 // ---------------------------------------------------------------- host side
 
 template <int HD>
-cudaError_t launch_hd(const AttnParams& p, cudaStream_t s) {
+cudaError_t launch_hd(const Kv4Attn& p, cudaStream_t s) {
   using L = Lay<HD>;
   CUtensorMap mk, mv;
   const int box = min(p.block_size, KT);
-  if (!kv4_tensor_map(&mk, p.k, p.kv_rows, p.Hkv, HD, box) ||
-      !kv4_tensor_map(&mv, p.v, p.kv_rows, p.Hkv, HD, box))
+  const int64_t rows = p.num_blocks * p.block_size;
+  if (!kv4_tensor_map(&mk, p.k, rows, p.Hkv, HD, box) ||
+      !kv4_tensor_map(&mv, p.v, rows, p.Hkv, HD, box))
     return cudaErrorInvalidValue;
   auto kernel = attn_kv4_tc_kernel<HD>;
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(p.n_ctas), dim3(NTHREADS), L::SMEM, s, p, mk, mv);
+  return launch_pdl(kernel, dim3(p.n_ctas * p.heads), dim3(NTHREADS), L::SMEM, s, p, mk, mv);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_kv4_tc(const AttnParams& p, cudaStream_t s) {
-  if (p.kv_rows <= 0 || p.kv_rows > 0x7fffffffLL) return cudaErrorNotSupported;
+cudaError_t launch_attn_kv4_tc(const Kv4Attn& p, cudaStream_t s) {
   return p.d == 128 ? launch_hd<128>(p, s) : launch_hd<64>(p, s);
 }
 

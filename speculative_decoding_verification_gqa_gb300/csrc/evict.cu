@@ -8,11 +8,12 @@
 //           a radix select over order-preserving 32-bit keys (11, 11 and 10 bits, histograms
 //           in shared memory), then writes src in one ordered pass. CTA 0 of a row also makes
 //           the row's checks and leaves a verdict in the workspace.
-//   move    after every verdict is in: each CTA takes a column slice (up to 256 bytes) of one
+//   move    after every verdict is in: each CTA takes a column slice (SLICE bytes) of one
 //           pool's rows of one (row, KV head), or its weights, and gathers forwards in place:
 //           src[k] >= k, so what a batch of destinations overwrites has been read by the
 //           batches before it or by itself, whose loads end before its stores begin. Slices
-//           never touch each other's bytes, so nothing else orders them.
+//           never touch each other's bytes, so nothing else orders them. A batch is a chain of
+//           dependent reads (src, table, data), so many narrow slices in flight pay.
 // Select reads the weights (4 bytes a position) four times, from L2 after the first; move is
 // bound by memory.
 #include "internal.cuh"
@@ -23,6 +24,7 @@ namespace {
 constexpr int ST = 1024;        // threads of select
 constexpr int MTH = 256;        // threads of move
 constexpr int BINS = 2048;
+constexpr int SLICE = 32;       // bytes of a column slice (a sector)
 
 struct EvictArgs {
   sv_page_table t;
@@ -292,10 +294,10 @@ __global__ void __launch_bounds__(MTH) move_kernel(const EvictArgs a, const __gr
   --s;
   for (int k = 0; k < pools.n; ++k) {
     const int64_t pos_bytes = pools.p[k].page_bytes >> a.bs_log2, row_bytes = pos_bytes / a.Hkv;
-    const int n = (int)((row_bytes + 255) / 256);
+    const int n = (int)((row_bytes + SLICE - 1) / SLICE);
     if (s < n) {
-      uint8_t* base = (uint8_t*)pools.p[k].base + g * row_bytes + s * 256;
-      const int bytes = (int)min((int64_t)256, row_bytes - s * 256);
+      uint8_t* base = (uint8_t*)pools.p[k].base + g * row_bytes + s * SLICE;
+      const int bytes = (int)min((int64_t)SLICE, row_bytes - s * SLICE);
       if (bytes % 16 == 0 && row_bytes % 16 == 0)
         move_slice<16>(a, p, src, base, row_bytes, pos_bytes, bytes / 16);
       else
@@ -336,7 +338,7 @@ cudaError_t launch_evict(const sv_page_table& t, int n, const int32_t* rows, con
   a.slices = 1;
   for (int k = 0; k < num_pools; ++k) {
     pl.p[k] = pools[k];
-    a.slices += (int)((pools[k].page_bytes / t.block_size / Hkv + 255) / 256);
+    a.slices += (int)((pools[k].page_bytes / t.block_size / Hkv + SLICE - 1) / SLICE);
   }
   const cudaError_t e = launch_pdl(select_kernel, dim3((unsigned)(n * Hkv)), dim3(ST), 0, s, a);
   if (e != cudaSuccess) return e;

@@ -193,8 +193,6 @@ struct AttnParams {
                               // run further ahead), 0 paired K + V stages
   long long wait_limit;       // tcgen05 kernel: clock cycles a barrier wait may take before
                               // it gives up (0: the default, about 2 s)
-  const void* kv4_scales;     // 4-bit cache: E4M3 [.., Hkv, 2, d / 16]
-  float* lse;                 // [q_rows, Hq] or nullptr: each row's log-sum-exp (natural)
   int stall_first_tile;       // test hook: every CTA's producer withholds the K and V loads
                               // of the first tile of its range, so the waits for it run out
 };
@@ -387,11 +385,35 @@ cudaError_t launch_attn_tc_hp(const AttnParams& p, bool fp8, const HostPlan& hp,
 bool attn_pair_applies(const AttnParams& p, bool fp8, int sms);
 cudaError_t launch_attn_pair(const AttnParams& p, cudaStream_t s);
 
-// 4-bit cache (attn_kv4.cu, kv4.cu).
-int attn_kv4_kt();
+// 4-bit cache (attn_kv4.cu, attn_kv4_tc.cu, kv4.cu; work line: line.cuh).
+struct Kv4Attn {
+  const void* q;
+  const void *k, *v, *scales;  // the pages' codes and block scales
+  const float* kv_scale;
+  const int32_t *seq_lens, *draft_len, *block_table;
+  void* out;
+  float* lse;                  // [q_rows, Hq] or nullptr
+  uint32_t* flags;
+  float* part_o;               // [2 * n_ctas][heads][mr][d]: parts of units that CTAs share
+  float2* part_ml;             // [2 * n_ctas][heads][mr] (reference in log2 units, sum)
+  int B, Hq, Hkv, G, d, max_draft, max_seq, window;
+  int bt_stride, block_size, bs_log2;
+  int64_t num_blocks, q_rows;
+  float scale_log2;
+  int heads;                   // neighbouring KV heads of a unit
+  int mr;                      // query rows of a unit and head
+  int n_ctas;                  // ranges of the line
+  int switch_tiles;            // a unit's start in tiles' time
+  int join_tiles;              // the join's time in tiles' time
+  bool no_join;                // whatever the lengths, a CTA takes a whole unit
+  long long wait_limit;
+};
+constexpr int KV4_KT = 128;    // keys per tile of the line
 int attn_kv4_ctas(int rows_per_kv, int sms);
-cudaError_t launch_attn_kv4(const AttnParams& p, cudaStream_t s);
-cudaError_t launch_attn_kv4_tc(const AttnParams& p, cudaStream_t s);
+int attn_kv4_rows(int rows_per_kv);
+cudaError_t launch_attn_kv4(const Kv4Attn& p, cudaStream_t s);
+cudaError_t launch_attn_kv4_tc(const Kv4Attn& p, cudaStream_t s);
+cudaError_t launch_kv4_join(const Kv4Attn& p, int sms, cudaStream_t s);
 cudaError_t launch_kv4_write(const sv_kv4_pages& p, int B, const int32_t* table, int max_blocks,
                              const int32_t* start, const int32_t* count, int64_t rows,
                              const void* k, int64_t k_stride, const void* v, int64_t v_stride,

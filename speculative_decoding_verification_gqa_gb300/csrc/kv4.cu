@@ -3,10 +3,10 @@
 // For a block x of 16 elements of a row and the head's scale s (format: kv4.cuh)
 //   c = E4M3(max |x| / (6 s)),  code_k = E2M1(x_k / (s c))  (0 where c = 0),
 // each the nearest value of its type to the REAL quotient, ties to the even code, saturating.
-// The quotients are formed in fp32 as products with a reciprocal, whose error is below 2^-22
-// of them (three roundings of 2^-24, and less than one more for the division): the product is
-// converted twice, a little smaller and a little larger (2^-21), and where the two codes
-// differ, about one block in 2^13, the choice is made in 64 bits, where x and the middle of
+// The quotients are formed in fp32 as products with a reciprocal, whose error is below 2^-21
+// of them (the reciprocal's 2^-23 and three roundings of 2^-24): the product is formed twice,
+// a little smaller and a little larger (2^-20), and where the two codes differ, about one
+// block in 2^12, the choice is made in 64 bits, where x and the middle of
 // two codes times s c are exact (8 and 31 significant bits). So the codes do not depend on
 // how the quotient is computed, and a reference in 64 bits gives the same.
 // A block with an infinity or a NaN gets the scale NaN: it reads as NaN, all 16 elements.
@@ -37,9 +37,10 @@ struct Kv4Args {
   uint32_t* flags;
   int row_items;            // blocks of a row: 2 (K, V) x Hkv x d / 16
   int cta_rows;
+  int lanes, rows_at_once;  // threads of a row, and rows that the CTA's threads take at once
 };
 
-constexpr int MAX_CTA_ROWS = 32;
+constexpr int MAX_CTA_ROWS = 64;
 
 // The cache row of each packed row [r0, r0 + a.cta_rows) in s_row: -1 for rows past the
 // sequences' total, -2 where the table names no page of the pool. False, with the flag set,
@@ -95,19 +96,18 @@ __device__ bool locate(const Kv4Args& a, int64_t r0, int64_t* s_row) {
   return true;
 }
 
-// A CTA's item i: block `blk` of head h of K (which 0) or V (1) of its row r.
+// Block `blk` of head h of K (which 0) or V (1): a thread's place in a row, for every row that
+// it takes.
 struct Item {
-  int r, which, h, blk;
+  int which, h, blk;
 };
-__device__ __forceinline__ Item item_of(const Kv4Args& a, int i) {
+__device__ __forceinline__ Item item_of(const Kv4Args& a, int i) {  // item i of a row
   const int nb = a.d >> 4;  // 4 or 8
   Item t;
   t.blk = i & (nb - 1);
-  const int e = i / nb;  // (row, which, head)
-  const int w = e / a.Hkv;
-  t.h = e - w * a.Hkv;
-  t.which = w & 1;
-  t.r = w >> 1;
+  const int e = i / nb;  // which, head
+  t.which = e >= a.Hkv;
+  t.h = e - (t.which ? a.Hkv : 0);
   return t;
 }
 
@@ -119,14 +119,6 @@ __device__ __forceinline__ uint32_t to_e4m3(float x) {  // one value, in the low
 __device__ __forceinline__ float e4m3_value(uint32_t c) {
   const uint32_t h = e4m3x2_to_f16x2(c);
   return __half2float(__ushort_as_half((unsigned short)(h & 0xffffu)));
-}
-// Two values -> a byte of two E2M1 codes, the first in the low nibble; nearest even, saturating.
-__device__ __forceinline__ uint32_t to_e2m1x2(float lo, float hi) {
-  uint32_t r;
-  asm("{\n .reg .b8 b;\n cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n mov.b32 %0, {b, b, b, b};\n}\n"
-      : "=r"(r)
-      : "f"(hi), "f"(lo));
-  return r & 0xffu;
 }
 __device__ __forceinline__ double e2m1_magnitude(uint32_t c) {  // of its low 3 bits
   c &= 7;
@@ -141,7 +133,32 @@ __device__ __forceinline__ bool takes_upper(double a, double unit, double lower,
   return a > mid || (a == mid && (upper_code & 1) == 0);
 }
 
-constexpr float LESS = 1.f - 0x1p-21f, MORE = 1.f + 0x1p-21f;
+constexpr float LESS = 1.f - 0x1p-20f, MORE = 1.f + 0x1p-20f;
+
+__device__ __forceinline__ float reciprocal(float x) {  // to 2^-23
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// (a, b) * (s, s)
+__device__ __forceinline__ float2 mul2(float a, float b, float s) {
+  float2 r;
+  asm("{\n .reg .b64 v, w;\n mov.b64 v, {%2, %3};\n mov.b64 w, {%4, %4};\n mul.rn.f32x2 v, v, w;\n"
+      " mov.b64 {%0, %1}, v;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a), "f"(b), "f"(s));
+  return r;
+}
+// Eight values -> eight E2M1 codes, the first in the lowest nibble; nearest even, saturating.
+__device__ __forceinline__ uint32_t to_e2m1x8(const float2 (&y)[4]) {
+  uint32_t r;
+  asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(r)
+      : "f"(y[0].x), "f"(y[0].y), "f"(y[1].x), "f"(y[1].y), "f"(y[2].x), "f"(y[2].y), "f"(y[3].x), "f"(y[3].y));
+  return r;
+}
 
 __device__ __noinline__ uint32_t scale_code_exact(float amax, float head, uint32_t lo, uint32_t hi) {
   return takes_upper(amax, 6.0 * (double)head, e4m3_value(lo), e4m3_value(hi), hi) ? hi : lo;
@@ -161,18 +178,18 @@ __device__ __noinline__ uint32_t codes_exact(const uint4 v, double unit, uint32_
   return out;
 }
 
-// 8 elements -> 8 codes.
-__device__ __forceinline__ uint32_t encode8(const uint4 v, float inv, double unit) {
+// 8 elements -> 8 codes; less and more: the reciprocal of the unit a little smaller and larger.
+__device__ __forceinline__ uint32_t encode8(const uint4 v, float less, float more, float head, float c) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t lo = 0, hi = 0;
+  float2 lo[4], hi[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float y0 = __uint_as_float(w[e] << 16) * inv;
-    const float y1 = __uint_as_float(w[e] & 0xffff0000u) * inv;
-    lo |= to_e2m1x2(y0 * LESS, y1 * LESS) << (8 * e);
-    hi |= to_e2m1x2(y0 * MORE, y1 * MORE) << (8 * e);
+    const float x0 = __uint_as_float(w[e] << 16), x1 = __uint_as_float(w[e] & 0xffff0000u);
+    lo[e] = mul2(x0, x1, less);
+    hi[e] = mul2(x0, x1, more);
   }
-  return lo == hi ? lo : codes_exact(v, unit, lo, hi);
+  const uint32_t a = to_e2m1x8(lo), b = to_e2m1x8(hi);
+  return a == b ? a : codes_exact(v, (double)head * (double)c, a, b);
 }
 
 __device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {  // of bf16 pairs, NaN kept
@@ -182,65 +199,67 @@ __device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {  // of bf
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
-// N: items of a thread whose loads run together.
+// N: rows of a thread whose loads run together.
 template <int N>
 __global__ void __launch_bounds__(NTH) kv4_write_kernel(const Kv4Args a) {
   __shared__ int64_t s_row[MAX_CTA_ROWS];
   const int64_t r0 = (int64_t)blockIdx.x * a.cta_rows;
-  const int items = (int)min((int64_t)a.cta_rows, a.rows - r0) * a.row_items;
+  const int rows = (int)min((int64_t)a.cta_rows, a.rows - r0);
+  const int lr = threadIdx.x / a.lanes, li = threadIdx.x - lr * a.lanes;
   pdl_trigger();
   pdl_wait();
   bool located = false;
-  for (int i0 = threadIdx.x; i0 < items + (int)threadIdx.x; i0 += N * NTH) {
-    uint4 x[N][2];
-    float head[N];
+  for (int i = li; i < a.row_items + li; i += a.lanes) {  // (one pass but for very many heads)
+    const bool in = i < a.row_items && lr < a.rows_at_once;
+    const Item t = item_of(a, in ? i : 0);
+    const uint16_t* src = (t.which ? a.v : a.k) + t.h * a.d + t.blk * 16;
+    const int64_t stride = t.which ? a.v_stride : a.k_stride;
+    const float head = __ldg(a.head_scale + t.which * a.Hkv + t.h);
+    const float inv6 = reciprocal(6.f * head);
+    for (int rr = 0; rr < rows; rr += N * a.rows_at_once) {
+      uint4 x[N][2];
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      x[n][0] = x[n][1] = make_uint4(0, 0, 0, 0);
-      head[n] = 1.f;
-      if (i0 + n * NTH < items) {
-        const Item t = item_of(a, i0 + n * NTH);
-        const uint16_t* src = t.which ? a.v + (r0 + t.r) * a.v_stride : a.k + (r0 + t.r) * a.k_stride;
-        const uint4* s4 = reinterpret_cast<const uint4*>(src + t.h * a.d + t.blk * 16);
-        x[n][0] = __ldg(s4);
-        x[n][1] = __ldg(s4 + 1);
-        head[n] = __ldg(a.head_scale + t.which * a.Hkv + t.h);
-      }
-    }
-    if (!located) {
-      if (!locate(a, r0, s_row)) return;
-      located = true;
-    }
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      if (i0 + n * NTH >= items) continue;
-      const Item t = item_of(a, i0 + n * NTH);
-      const int64_t row = s_row[t.r];
-      if (row < 0) continue;
-      uint32_t m = abs_max2(abs_max2(abs_max2(x[n][0].x, x[n][0].y), abs_max2(x[n][0].z, x[n][0].w)),
-                            abs_max2(abs_max2(x[n][1].x, x[n][1].y), abs_max2(x[n][1].z, x[n][1].w)));
-      m = abs_max2(m, m >> 16) & 0xffffu;
-      uint32_t c;
-      uint2 code = make_uint2(0, 0);
-      if (m >= 0x7f80u) {  // an infinity or a NaN
-        c = 0x7fu;
-      } else {
-        const float amax = __uint_as_float(m << 16);
-        const float q = amax * (1.f / (6.f * head[n]));
-        const uint32_t lo = to_e4m3(q * LESS), hi = to_e4m3(q * MORE);
-        c = lo == hi ? lo : scale_code_exact(amax, head[n], lo, hi);
-        if (c != 0) {
-          const float cv = e4m3_value(c);
-          const float inv = 1.f / (head[n] * cv);
-          const double unit = (double)head[n] * (double)cv;
-          code.x = encode8(x[n][0], inv, unit);
-          code.y = encode8(x[n][1], inv, unit);
+      for (int n = 0; n < N; ++n) {
+        const int r = rr + n * a.rows_at_once + lr;
+        x[n][0] = x[n][1] = make_uint4(0, 0, 0, 0);
+        if (in && r < rows) {
+          const uint4* s4 = reinterpret_cast<const uint4*>(src + (r0 + r) * stride);
+          x[n][0] = __ldg(s4);
+          x[n][1] = __ldg(s4 + 1);
         }
       }
-      const int64_t at = row * a.Hkv + t.h;
-      uint8_t* dst = (t.which ? a.vc : a.kc) + at * (a.d >> 1) + t.blk * 8;
-      *reinterpret_cast<uint2*>(dst) = code;
-      a.sc[at * (a.d >> 3) + t.which * (a.d >> 4) + t.blk] = (uint8_t)c;
+      if (!located) {
+        if (!locate(a, r0, s_row)) return;
+        located = true;
+      }
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const int r = rr + n * a.rows_at_once + lr;
+        const int64_t row = in && r < rows ? s_row[r] : -1;
+        if (row < 0) continue;
+        uint32_t m = abs_max2(abs_max2(abs_max2(x[n][0].x, x[n][0].y), abs_max2(x[n][0].z, x[n][0].w)),
+                              abs_max2(abs_max2(x[n][1].x, x[n][1].y), abs_max2(x[n][1].z, x[n][1].w)));
+        m = abs_max2(m, m >> 16) & 0xffffu;
+        uint32_t c;
+        uint2 code = make_uint2(0, 0);
+        if (m >= 0x7f80u) {  // an infinity or a NaN
+          c = 0x7fu;
+        } else {
+          const float amax = __uint_as_float(m << 16);
+          const float q = amax * inv6;
+          const uint32_t lo = to_e4m3(q * LESS), hi = to_e4m3(q * MORE);
+          c = lo == hi ? lo : scale_code_exact(amax, head, lo, hi);
+          if (c != 0) {
+            const float cv = e4m3_value(c);
+            const float inv = reciprocal(head * cv);
+            code.x = encode8(x[n][0], inv * LESS, inv * MORE, head, cv);
+            code.y = encode8(x[n][1], inv * LESS, inv * MORE, head, cv);
+          }
+        }
+        const int64_t at = row * a.Hkv + t.h;
+        *reinterpret_cast<uint2*>((t.which ? a.vc : a.kc) + at * (a.d >> 1) + t.blk * 8) = code;
+        a.sc[at * (a.d >> 3) + t.which * (a.d >> 4) + t.blk] = (uint8_t)c;
+      }
     }
   }
 }
@@ -249,53 +268,56 @@ template <int N>
 __global__ void __launch_bounds__(NTH) kv4_read_kernel(const Kv4Args a) {
   __shared__ int64_t s_row[MAX_CTA_ROWS];
   const int64_t r0 = (int64_t)blockIdx.x * a.cta_rows;
-  const int items = (int)min((int64_t)a.cta_rows, a.rows - r0) * a.row_items;
+  const int rows = (int)min((int64_t)a.cta_rows, a.rows - r0);
+  const int lr = threadIdx.x / a.lanes, li = threadIdx.x - lr * a.lanes;
   pdl_trigger();
   pdl_wait();
   if (!locate(a, r0, s_row)) return;
-  for (int i0 = threadIdx.x; i0 < items; i0 += N * NTH) {
-    uint2 code[N];
-    uint32_t c[N];
-    float head[N];
+  if (lr >= a.rows_at_once) return;
+  for (int i = li; i < a.row_items; i += a.lanes) {
+    const Item t = item_of(a, i);
+    const uint8_t* src = (t.which ? a.vc : a.kc) + (int64_t)t.h * (a.d >> 1) + t.blk * 8;
+    const uint8_t* ssc = a.sc + (int64_t)t.h * (a.d >> 3) + t.which * (a.d >> 4) + t.blk;
+    uint16_t* dst = (t.which ? a.v_out : a.k_out) + (r0 * a.Hkv + t.h) * a.d + t.blk * 16;
+    const int code_bytes = a.Hkv * (a.d >> 1), scale_bytes = a.Hkv * (a.d >> 3), out_elems = a.Hkv * a.d;
+    const float head = __ldg(a.head_scale + t.which * a.Hkv + t.h);
+    for (int rr = lr; rr < rows; rr += N * a.rows_at_once) {
+      uint2 code[N];
+      uint32_t c[N];
+      int64_t row[N];
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      code[n] = make_uint2(0, 0);
-      c[n] = 0;
-      head[n] = 0.f;
-      if (i0 + n * NTH < items) {
-        const Item t = item_of(a, i0 + n * NTH);
-        const int64_t row = s_row[t.r];
-        if (row >= 0) {
-          const int64_t at = row * a.Hkv + t.h;
-          code[n] = __ldg(reinterpret_cast<const uint2*>((t.which ? a.vc : a.kc) + at * (a.d >> 1)) + t.blk);
-          c[n] = __ldg(a.sc + at * (a.d >> 3) + t.which * (a.d >> 4) + t.blk);
-          head[n] = __ldg(a.head_scale + t.which * a.Hkv + t.h);
+      for (int n = 0; n < N; ++n) {
+        const int r = rr + n * a.rows_at_once;
+        row[n] = r < rows ? s_row[r] : -1;
+        code[n] = make_uint2(0, 0);
+        c[n] = 0;
+        if (row[n] >= 0) {
+          code[n] = __ldg(reinterpret_cast<const uint2*>(src + row[n] * code_bytes));
+          c[n] = __ldg(ssc + row[n] * scale_bytes);
         }
       }
-    }
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      if (i0 + n * NTH >= items) continue;
-      const Item t = item_of(a, i0 + n * NTH);
-      if (s_row[t.r] == -1) continue;  // past the sequences' total: left as it was
-      const uint32_t u = lo_twice(e4m3x2_to_f16x2(c[n]));
-      uint32_t out[8];
+      for (int n = 0; n < N; ++n) {
+        if (row[n] == -1) continue;  // past the sequences' total: left as it was
+        const uint32_t u = lo_twice(e4m3x2_to_f16x2(c[n]));
+        uint32_t out[8];
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        uint32_t h[4];
-        e2m1x8_to_f16(w ? code[n].y : code[n].x, h);
+        for (int w = 0; w < 2; ++w) {
+          uint32_t h[4];
+          e2m1x8_to_f16(w ? code[n].y : code[n].x, h);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {  // exact in f16, then two roundings: to fp32, to bf16
-          const uint32_t p = hmul2(h[e], u);
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p));
-          const __nv_bfloat162 o = __floats2bfloat162_rn(f.x * head[n], f.y * head[n]);
-          out[4 * w + e] = *reinterpret_cast<const uint32_t*>(&o);
+          for (int e = 0; e < 4; ++e) {  // exact in f16, then two roundings: to fp32, to bf16
+            const uint32_t p = hmul2(h[e], u);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p));
+            const float2 y = mul2(f.x, f.y, head);
+            const __nv_bfloat162 o = __floats2bfloat162_rn(y.x, y.y);
+            out[4 * w + e] = *reinterpret_cast<const uint32_t*>(&o);
+          }
         }
+        uint4* d4 = reinterpret_cast<uint4*>(dst + (int64_t)(rr + n * a.rows_at_once) * out_elems);
+        d4[0] = make_uint4(out[0], out[1], out[2], out[3]);
+        d4[1] = make_uint4(out[4], out[5], out[6], out[7]);
       }
-      uint16_t* dst = (t.which ? a.v_out : a.k_out) + ((r0 + t.r) * a.Hkv + t.h) * a.d + t.blk * 16;
-      uint4* d4 = reinterpret_cast<uint4*>(dst);
-      d4[0] = make_uint4(out[0], out[1], out[2], out[3]);
-      d4[1] = make_uint4(out[4], out[5], out[6], out[7]);
     }
   }
 }
@@ -303,10 +325,13 @@ __global__ void __launch_bounds__(NTH) kv4_read_kernel(const Kv4Args a) {
 template <class K1, class K4>
 cudaError_t launch_rows(K1 one, K4 four, Kv4Args a, int sms, cudaStream_t s) {
   a.row_items = 2 * a.Hkv * (a.d / 16);
-  // rows of a CTA: an item a thread while that leaves no SM with more than a CTA, else four
-  const bool few = a.rows * a.row_items <= (int64_t)sms * NTH;
-  const int want = (few ? 1 : 4) * NTH / a.row_items;
-  a.cta_rows = want < 1 ? 1 : want > MAX_CTA_ROWS ? MAX_CTA_ROWS : want;
+  a.lanes = a.row_items < NTH ? a.row_items : NTH;
+  a.rows_at_once = NTH / a.lanes;
+  // An item a thread while that leaves no SM with more than two CTAs; else 16 rows a thread, four
+  // at a time, so that the scan for the rows' places costs little next to them.
+  const bool few = a.rows * a.row_items <= 2 * (int64_t)sms * NTH;
+  const int want = few ? a.rows_at_once : 16 * a.rows_at_once;
+  a.cta_rows = want > MAX_CTA_ROWS ? MAX_CTA_ROWS : want;
   const unsigned grid = (unsigned)((a.rows + a.cta_rows - 1) / a.cta_rows);
   return launch_pdl(few ? one : four, dim3(grid), dim3(NTH), 0, s, a);
 }

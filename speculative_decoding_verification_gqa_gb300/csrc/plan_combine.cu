@@ -414,9 +414,8 @@ __device__ __forceinline__ void combine_row(const AttnParams& p, int u, int r, i
   const float inv = vs / L;
   const int rg = mt * MT + r;
   const int i = rg / p.G, hl = rg % p.G;
-  const int64_t orow = (p.q_off[b] + i) * p.Hq + (int64_t)g * p.G + hl;
-  if (p.lse && lane == 0) p.lse[orow] = (mx + log2f(L)) * 0.6931471805599453f;
-  __nv_bfloat16* dst = (__nv_bfloat16*)p.out + orow * HD + lane * PER;
+  __nv_bfloat16* dst = (__nv_bfloat16*)p.out +
+                       ((p.q_off[b] + i) * p.Hq + (int64_t)g * p.G + hl) * HD + lane * PER;
   if constexpr (PER == 4) {
     __nv_bfloat162 a = __floats2bfloat162_rn(acc[0] * inv, acc[1] * inv);
     __nv_bfloat162 c = __floats2bfloat162_rn(acc[2] * inv, acc[3] * inv);
