@@ -813,7 +813,7 @@ int pick_kv4(const sv_attn_desc* d) {
 // A call's units and ranges (line.cuh) on `sms` SMs with kernel `which`.
 void kv4_line(const sv_attn_desc* d, int which, int sms, Kv4Attn* p) {
   const int64_t rows = kv4_rows_per_head(d);
-  const int ctas = which == 2 ? sms : attn_kv4_ctas((int)rows, sms);
+  const int ctas = which == 2 ? sms : attn_kv4_ctas(sms);
   const int64_t max_tiles = ((int64_t)d->max_seq_len + d->max_draft_len) / KV4_KT + 1;
   p->mr = which == 2 ? MT : attn_kv4_rows((int)rows);
   p->switch_tiles = which == 2 ? SWITCH_TILES_KV4 : SWITCH_TILES_KV4_MMA;
@@ -839,7 +839,7 @@ Kv4Ws kv4_layout(const sv_attn_desc* d, int sms) {
   // The parts of either kernel and any rule on its units, so that the workspace of a larger
   // shape serves a smaller one, under any sv_set_attn_kernel: at most two a range, its heads
   // (two) times rows of each.
-  const size_t rows = std::max<size_t>(2 * (size_t)sms * MT, 2 * (size_t)attn_kv4_ctas(1, sms) * 2 * 16);
+  const size_t rows = std::max<size_t>(2 * (size_t)sms * MT, 2 * (size_t)attn_kv4_ctas(sms) * 2 * 16);
   Kv4Ws w;
   w.part_o = 256;
   w.part_ml = w.part_o + rows * d->head_dim * sizeof(float);
@@ -1033,7 +1033,7 @@ SV_API sv_status spec_kv_evict(const sv_page_table* table, int32_t n, const int3
   for (int k = 0; k < num_pools; ++k) {
     const int64_t pos = pools[k].page_bytes / table->block_size;
     if (pos % (8 * (int64_t)num_kv_heads) != 0) return SV_ERR_SHAPE;
-    slices += (pos / num_kv_heads + 31) / 32;  // (evict.cu, SLICE)
+    slices += (pos / num_kv_heads + 31) / 32;  // (at most: evict.cu, SLICE)
   }
   if (n * (int64_t)num_kv_heads * slices > 0x7fffffff) return SV_ERR_SHAPE;
   if (n == 0) return SV_OK;

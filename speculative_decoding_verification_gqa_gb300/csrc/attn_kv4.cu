@@ -37,6 +37,8 @@ constexpr int CK = 32;             // keys of a chunk
 constexpr int NW = 4;              // warps
 constexpr int NTHREADS = NW * 32;
 constexpr int ST = 3;              // ring stages of a warp
+constexpr int SM_CTAS = 3;         // CTAs of an SM: 168 registers a thread. (64 sequences of up to
+                                   // 8192 positions, single tokens: 76.8 us; 4 CTAs 81.2, 5: 92)
 // Reference of a row: its largest score less SHIFT (log2 units), raised when a score is more
 // than RESCALE above that score. P = 2^(s - reference) then lies below 2^15 and the largest at
 // 2^7 or more, so that f16 (largest 65504, least step 2^-24) drops only weights below 2^-32 of
@@ -60,7 +62,7 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -68,7 +70,7 @@ __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -118,7 +120,7 @@ __device__ __forceinline__ void store_row(const Kv4Attn& p, int64_t row, int g, 
 // NT: n-tiles of 8 query rows, of which a unit has as many for each of its heads. HG: heads of a
 // unit; warp w takes head w % HG and every (NW / HG)-th chunk of its keys.
 template <int HD, int NT, int HG>
-__global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3) attn_kv4_kernel(const Kv4Attn p) {
+__global__ void __launch_bounds__(NTHREADS, SM_CTAS) attn_kv4_kernel(const Kv4Attn p) {
   using L = L4<HD>;
   constexpr int KS = L::KS, ROWS = 8 * NT, NK = NW / HG;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -127,8 +129,8 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3) attn_kv4_kernel(con
   const int r8 = lane >> 2, t4 = lane & 3;
   const int hg = warp % HG, kw = warp / HG;
   uint8_t* ring = smem + warp * warp_bytes<HD, NT>();
-  pdl_trigger();
   pdl_wait();
+  pdl_trigger();  // after the wait: the join kernel reads the lengths before its own
   LineWalk walk;
   if (!line_begin<NTHREADS>(p, blockIdx.x, walk)) return;
 
@@ -267,6 +269,7 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3) attn_kv4_kernel(con
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
           for (int n = 0; n < NT; ++n) s[h][n][0] = s[h][n][1] = s[h][n][2] = s[h][n][3] = 0.f;
+          float s2[NT][4] = {};  // the odd k-steps: two chains of MMAs
           uint32_t w[2][HD / 32], u[2][HD / 64];  // codes and scale pairs of keys r8, r8 + 8
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -304,9 +307,13 @@ __global__ void __launch_bounds__(NTHREADS, NT == 1 ? 4 : 3) attn_kv4_kernel(con
               const uint32_t a[4] = {x[2 * e], y[2 * e], x[2 * e + 1], y[2 * e + 1]};
 #pragma unroll
               for (int n = 0; n < NT; ++n)
-                mma_f16(s[h][n], a, qf[n][2 * q + e][0], qf[n][2 * q + e][1]);
+                mma_f16(e ? s2[n] : s[h][n], a, qf[n][2 * q + e][0], qf[n][2 * q + e][1]);
             }
           }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[h][n][e] += s2[n][e];
         }
         // ---- mask, exponents above the reference, raised where one is far above
         if (key0 + CK > T || key0 < lo_max) {
@@ -498,18 +505,24 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const Kv4Attn p) {
   __shared__ float4 s_o[JT / 32][HD / 4];
   __shared__ float2 s_ml[JT / 32];
   pdl_trigger();
-  pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  Line total;
-  if (!line_scan<JT>(p, total, 0, false, nullptr) || total.whole) return;
+  // The lengths are read before the wait: the attention kernel's CTAs let this one start when
+  // they have waited themselves, so whatever wrote the lengths is complete.
   const int per = p.heads * ((p.mr + JROWS - 1) / JROWS);  // items of a unit
-  const int64_t items = total.units * per;
-  int64_t it = (int64_t)blockIdx.x * items / gridDim.x;
-  const int64_t end = (int64_t)(blockIdx.x + 1) * items / gridDim.x;
-  if (it >= end) return;
+  Line total;
   LineAt at;
-  line_scan<JT>(p, total, it / per, true, &at);
-  LineWalk walk = line_enter(p, at, it / per - at.units, true);
+  int64_t it = 0, end = 0;
+  const bool any = line_scan<JT>(p, total, &at, [&](bool& by_unit) -> int64_t {
+    const int64_t items = total.whole ? 0 : total.units * per;
+    it = (int64_t)blockIdx.x * items / gridDim.x;
+    end = (int64_t)(blockIdx.x + 1) * items / gridDim.x;
+    by_unit = true;
+    return it < end ? it / per : -1;
+  });
+  LineWalk walk;
+  if (any) walk = line_enter(p, at, it / per - at.units, true);
+  pdl_wait();
+  if (!any) return;
   walk.v0 = 0;
   walk.v1 = total.virt;
   constexpr int LN = HD / 4;  // lanes of a row
@@ -621,7 +634,7 @@ cudaError_t launch_nt(const Kv4Attn& p, cudaStream_t s) {
 }  // namespace
 
 // CTAs of a call on `sms` SMs: what an SM holds at once; query rows of a unit and head.
-int attn_kv4_ctas(int rows_per_kv, int sms) { return sms * (rows_per_kv <= 8 ? 4 : 3); }
+int attn_kv4_ctas(int sms) { return sms * SM_CTAS; }
 int attn_kv4_rows(int rows_per_kv) { return rows_per_kv <= 8 ? 8 : 16; }
 
 cudaError_t launch_attn_kv4(const Kv4Attn& p, cudaStream_t s) {

@@ -6,16 +6,20 @@
 // sums have the same bits every time, without atomics.
 //
 // Keys are the M dimension (S^T = K Q^T, m16n8k16): the sum over rows then runs along a
-// thread's own accumulators, and only at the end over the four lanes of a key. K fragments are
-// built in registers straight from the cache's rows: the order of d is free as long as Q has
-// the same, so lane t of a key's four takes whole 16-byte pieces (every fourth) of its row.
-// Q lies in shared memory in fragment order.
+// thread's own accumulators, and only at the end over the four lanes of a key. A warp takes
+// chunks of 32 keys through a ring of cp.async stages of its own and builds the K fragments from
+// the raw rows: the order of d is free as long as Q has the same, so lane t of a key's four takes
+// whole 16-byte pieces (every fourth) of its row. Q lies in shared memory in fragment order.
 //
-// Without given log-sums a first pass over the keys reduces (max, sum) for every row, each
-// CTA for its own tiles, and a second kernel joins those into L.
+// Without given log-sums a first pass over the keys reduces (max, sum) for every row, 64 rows at
+// a time in registers, each lane for its own keys, and each CTA for its own tiles; the second
+// pass begins every unit by joining those.
 //
-// Work: tiles of 256 keys (8 warps x 32) of each (sequence, KV head), end to end on one line,
-// an equal range of it for each CTA, which finds its place by scanning the lengths itself.
+// Work: a unit is a sequence and one or two neighbouring KV heads, whose rows share 128-byte
+// lines of a 4-bit cache; its 12 warps take the heads in turn and 32 keys each, a tile. Units lie
+// end to end on one line, a unit's start and every tile as long as their work: a tile's fixed
+// part and one for every 8 rows. Each CTA (one an SM) takes the tiles that begin in its equal
+// share of the line, and finds its place by scanning the lengths itself.
 #include <cuda_bf16.h>
 
 #include "kv4.cuh"
@@ -23,11 +27,12 @@
 namespace sv {
 namespace {
 
-constexpr int NW = 8;
+constexpr int NW = 12;
 constexpr int NTHREADS = NW * 32;
-constexpr int KT = NW * 32;      // keys of a tile
+constexpr int CK = 32;           // keys of a chunk
 constexpr int RB = 128;          // query rows held at once
-constexpr float LN2 = 0.6931471805599453f, LOG2E = 1.4426950408889634f;
+constexpr int RS = 64;           // in the pass for the log-sums
+constexpr float LOG2E = 1.4426950408889634f;
 
 struct MassArgs {
   const uint16_t* q;
@@ -36,7 +41,6 @@ struct MassArgs {
   const float* kv_scale;
   const int32_t *table, *seq_lens, *draft_len, *row_count;
   const float* lse;          // [rows, Hq] natural, or null
-  float* lse_ws;             // [rows, Hq], written by the joining kernel
   float2* part;              // [n_ctas + B * Hkv][max_rows] (max, sum) in log2 units
   float* mass;
   uint32_t* flags;
@@ -44,6 +48,8 @@ struct MassArgs {
   int B, Hq, Hkv, G, max_draft, max_seq, bt_stride, block_size, bs_log2;
   int max_rows;              // G * (1 + max_draft)
   int n_ctas;
+  int heads;                 // of a unit
+  int fixed;                 // a tile's loads and decoding, in 8 rows' time
   float scale_log2;
 };
 
@@ -55,13 +61,13 @@ __device__ __forceinline__ float ex2(float x) {
 template <bool F16>
 __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   if constexpr (F16)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -76,6 +82,15 @@ struct LM {
   static constexpr int LANEB = ROWB / 4 < 16 ? ROWB / 4 : 16;  // bytes of a lane's piece
   static constexpr int PIECES = ROWB / 4 / LANEB;
   static constexpr int PE = TY == BF16 ? LANEB / 2 : TY == E4M3 ? LANEB : LANEB * 2;  // elements
+  static constexpr int SB = TY == KV4 ? HD / 8 : 0;   // bytes of a row's block scales
+  static constexpr int STAGE = CK * (ROWB + SB);
+  static constexpr int ST = TY == BF16 ? 2 : 4;       // ring stages of a warp
+  static constexpr int CH = ROWB / 16;                // 16-byte pieces of a row
+  // where piece c of row kk of a stage lies: rows of 128 bytes and more exchange places so that
+  // eight lanes, four pieces of two rows, meet every bank once
+  __device__ static __forceinline__ int place(int kk, int c) {
+    return kk * CH + (ROWB == 256 ? c ^ ((kk & 1) << 2) : ROWB == 128 ? c ^ ((kk & 1) << 2) : c);
+  }
   // first of the 8 elements of lane t in k-steps 2 j, 2 j + 1
   __device__ static __forceinline__ int elem(int j, int t) {
     return PE * (4 * (8 * j / PE) + t) + 8 * j % PE;
@@ -91,41 +106,60 @@ __device__ __forceinline__ bool lengths(const MassArgs& a, int b, int& T, int& D
          (((int64_t)T + D + a.block_size) >> a.bs_log2) <= a.bt_stride &&
          (int64_t)T + 1 + D <= a.mass_stride;
 }
-// Tiles of a KV head: keys that a counted row sees.
-__device__ __forceinline__ int tiles_of(int T, int n) {
-  return n == 0 ? 0 : (int)(((int64_t)T + n + KT - 1) / KT);
+// A sequence's units: their tiles (up to the keys that a counted row sees), the length of a tile
+// on the line (its rows' MMAs and exponentials by 8 rows, `fixed` of that for its loads and
+// decoding) and of a unit with its START (all 0 without a counted row).
+constexpr int START = 16;
+struct SeqLine {
+  int tiles, tile;
+};
+__device__ __forceinline__ SeqLine line_of(const MassArgs& a, int T, int n) {
+  if (n == 0) return SeqLine{0, 1};
+  const int keys = NW / a.heads * CK;  // of a tile
+  SeqLine s;
+  s.tiles = (int)(((int64_t)T + n + keys - 1) / keys);
+  s.tile = a.fixed + (a.G * n + 15) / 16 * 2;
+  return s;
+}
+__device__ __forceinline__ int64_t unit_length(const SeqLine& s) {
+  return s.tiles == 0 ? 0 : START + (int64_t)s.tiles * s.tile;
 }
 
-// A CTA's place on the line.
+// A CTA's place on the line, whose range is [v0, v1).
 struct Place {
-  int64_t total, t, end, q_off;
-  int b;        // sequence of tile t
-  int64_t in_b; // tiles of it before t
+  int64_t total, v0, v1;
+  int b;                // sequence that holds v0
+  int64_t base, q_off;  // where that begins on the line, and its first packed row
 };
-// Scan of the lengths: totals, and the sequence that holds tile c * total / n_ctas. One CTA's
-// threads together; false (flag set) if a length is out of range.
+__device__ __forceinline__ int64_t ceil_div(int64_t x, int y) { return x <= 0 ? 0 : (x + y - 1) / y; }
+__device__ __forceinline__ int64_t range_begin(const MassArgs& a, int64_t total, int c) {
+  return c * total / a.n_ctas;
+}
+// Scan of the lengths: totals, and the sequence that holds the range's beginning. One CTA's
+// threads together; false (flag set) if a length is out of range. One pass for up to NTHREADS
+// sequences, whose shares stay in registers, else two.
 __device__ bool find_place(const MassArgs& a, Place& pl) {
   __shared__ int64_t s_warp[NW][2];
   __shared__ int64_t s_place[3];
-  __shared__ int64_t s_total;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   bool bad = false;
-  int64_t begin = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t carry_t = 0, carry_q = 0;
-    for (int base = 0; base < a.B; base += NTHREADS) {
-      const int b = base + tid;
-      int64_t v[2] = {0, 0};
-      if (b < a.B) {
-        int T, D, n;
-        if (lengths(a, b, T, D, n)) {
-          v[0] = (int64_t)a.Hkv * tiles_of(T, n);
-          v[1] = 1 + D;
-        } else {
-          bad = true;
-        }
+  int64_t carry[2] = {0, 0}, v[2], x[2];  // line and rows; of this thread's sequence; before it
+  auto shares = [&](int base) {
+    const int b = base + tid;
+    v[0] = v[1] = 0;
+    if (b < a.B) {
+      int T, D, n;
+      if (lengths(a, b, T, D, n)) {
+        v[0] = a.Hkv / a.heads * unit_length(line_of(a, T, n));
+        v[1] = 1 + D;
+      } else {
+        bad = true;
       }
-      int64_t x[2] = {v[0], v[1]};
+    }
+    x[0] = v[0];
+    x[1] = v[1];
+    const int nw = min(NW, (a.B - base + 31) / 32);
+    if (wid < nw) {
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
@@ -137,86 +171,172 @@ __device__ bool find_place(const MassArgs& a, Place& pl) {
         s_warp[wid][0] = x[0];
         s_warp[wid][1] = x[1];
       }
-      __syncthreads();
-      int64_t before[2] = {0, 0}, all[2] = {0, 0};
-#pragma unroll
-      for (int w = 0; w < NW; ++w)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          before[k] += w < wid ? s_warp[w][k] : 0;
-          all[k] += s_warp[w][k];
-        }
-      const int64_t tb = carry_t + before[0] + x[0] - v[0];
-      if (pass == 1 && begin >= tb && begin < tb + v[0]) {
-        s_place[0] = b;
-        s_place[1] = begin - tb;
-        s_place[2] = carry_q + before[1] + x[1] - v[1];
-      }
-      carry_t += all[0];
-      carry_q += all[1];
-      __syncthreads();
     }
-    if (pass == 0) {
-      bad |= carry_q > a.q_rows;
-      if (__syncthreads_or(bad)) {
-        if (tid == 0) atomicOr(a.flags, FLAG_ATTN_SHAPE);
-        return false;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      int64_t before = carry[k];
+      for (int w = 0; w < nw; ++w) {
+        const int64_t y = s_warp[w][k];
+        if (w < wid) before += y;
+        carry[k] += y;
       }
-      pl.total = carry_t;
-      begin = blockIdx.x * carry_t / a.n_ctas;
-      pl.t = begin;
-      pl.end = (blockIdx.x + 1) * carry_t / a.n_ctas;
+      x[k] += before - v[k];  // exclusive
+    }
+  };
+  for (int base = 0; base < a.B; base += NTHREADS) {
+    if (base > 0) __syncthreads();
+    shares(base);
+  }
+  if (__syncthreads_or(bad || carry[1] > a.q_rows)) {
+    if (tid == 0) atomicOr(a.flags, FLAG_ATTN_SHAPE);
+    return false;
+  }
+  pl.total = carry[0];
+  pl.v0 = range_begin(a, pl.total, blockIdx.x);
+  pl.v1 = range_begin(a, pl.total, blockIdx.x + 1);
+  if (pl.v0 >= pl.v1) return false;
+  auto look = [&](int base) {
+    if (pl.v0 >= x[0] && pl.v0 < x[0] + v[0]) {
+      s_place[0] = base + tid;
+      s_place[1] = x[0];
+      s_place[2] = x[1];
+    }
+  };
+  if (a.B <= NTHREADS) {
+    look(0);
+  } else {
+    carry[0] = carry[1] = 0;
+    for (int base = 0; base < a.B; base += NTHREADS) {
+      __syncthreads();
+      shares(base);
+      look(base);
     }
   }
-  if (pl.t >= pl.end) return false;
   __syncthreads();
   pl.b = (int)s_place[0];
-  pl.in_b = s_place[1];
+  pl.base = s_place[1];
   pl.q_off = s_place[2];
   return true;
 }
 
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+template <int N>  // bytes; not valid: zeros, nothing is read
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? N : 0;
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
 // STATS: the first pass, (max, sum) of each row over the CTA's tiles; else the weights.
-template <int HD, int TY, bool STATS>
-__global__ void __launch_bounds__(NTHREADS, 2) mass_kernel(const MassArgs a) {
+template <int HD, int TY, bool STATS, int HG>
+__global__ void __launch_bounds__(NTHREADS, 1) mass_kernel(const MassArgs a) {
   using L = LM<HD, TY>;
-  constexpr int KS = L::KS;
+  constexpr int NK = NW / HG, KT = NK * CK;          // chunks and keys of a tile, each head
+  constexpr int KS = L::KS, ST = L::ST, ROWS = STATS ? RS : RB / HG;  // rows held of each head
   constexpr bool F16 = TY != BF16;
-  extern __shared__ __align__(16) uint8_t smem[];
-  uint4* sQ = reinterpret_cast<uint4*>(smem);                 // [RB / 8][KS / 2][32]
-  float2* s_row = reinterpret_cast<float2*>(smem + RB * HD * 2);  // [RB] (score scale, log-sum)
-  int* s_i = reinterpret_cast<int*>(s_row + RB);              // [RB] window row
-  float2* s_ml = reinterpret_cast<float2*>(s_i + RB);         // STATS: [NW][RB]
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint4* sQ0 = reinterpret_cast<uint4*>(smem);                           // [HG][ROWS / 8][KS / 2][32]
+  float2* s_row0 = reinterpret_cast<float2*>(smem + HG * ROWS * HD * 2); // [HG][ROWS] (score scale, log-sum)
+  int* s_i = reinterpret_cast<int*>(s_row0 + HG * ROWS);                 // [ROWS] window row
+  float2* s_ml = reinterpret_cast<float2*>(smem);  // STATS, in Q's place: [NW][ROWS]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r8 = lane >> 2, t4 = lane & 3;
+  const int hg = warp % HG, kw = warp / HG;
+  const uint4* sQ = sQ0 + hg * ROWS / 8 * (KS / 2) * 32;
+  const float2* s_row = s_row0 + hg * ROWS;
+  uint8_t* ring = smem + HG * ROWS * (HD * 2 + 8) + ROWS * 4 + warp * ST * L::STAGE;
   pdl_trigger();
   pdl_wait();
   Place pl;
   if (!find_place(a, pl)) return;
-  const float* lse = a.lse ? a.lse : a.lse_ws;
+  const int code_bytes = a.Hkv * L::ROWB, scale_bytes = a.Hkv * L::SB;  // of a cache position
 
-  int64_t t = pl.t;
-  for (int b = pl.b; t < pl.end; ++b) {
+  for (int b = pl.b; b < a.B && pl.base < pl.v1; ++b) {
     int T, D, n;
     lengths(a, b, T, D, n);
-    const int nt = tiles_of(T, n);
+    const SeqLine sl = line_of(a, T, n);
+    const int nt = sl.tiles, W = sl.tile;
+    const int64_t length = unit_length(sl);
     const int nkeys = T + n;             // keys that a counted row sees
     const int rows = a.G * n;
     const int32_t* tab = a.table + (size_t)b * a.bt_stride;
-    for (int64_t in_b = pl.in_b; in_b < (int64_t)a.Hkv * nt && t < pl.end;) {
-      const int g = (int)(in_b / nt), j0 = (int)(in_b - (int64_t)g * nt);
-      const int j1 = (int)min((int64_t)nt, j0 + (pl.end - t));
-      const float sck = a.scale_log2 * (TY == BF16 ? 1.f : a.kv_scale[g]);
-      for (int rb = 0; rb < rows; rb += RB) {
-        const int nr = min(RB, rows - rb), ntile = (nr + 7) / 8;
+    const int groups = a.Hkv / HG;
+    // units with tiles that begin in the range
+    for (int gg = length == 0 || pl.v0 <= pl.base ? 0 : (int)min((int64_t)groups, (pl.v0 - pl.base) / length);
+         length > 0 && gg < groups && pl.base + gg * length < pl.v1; ++gg) {
+      const int64_t first = pl.base + gg * length + START;  // where the unit's first tile begins
+      const int j0 = (int)min((int64_t)nt, ceil_div(pl.v0 - first, W));
+      const int j1 = (int)min((int64_t)nt, ceil_div(pl.v1 - first, W));
+      if (j0 >= j1) continue;
+      const int g = gg * HG + hg;
+      // this warp's chunks of the tiles: 32 keys of each
+      const int key_first = j0 * KT + kw * CK;
+      const int mine = key_first < nkeys ? min(j1 - j0, (nkeys - key_first + KT - 1) / KT) : 0;
+      const int64_t lane_at = (int64_t)(lane / L::CH % 8) * code_bytes + g * L::ROWB + lane % L::CH * 16;
+      const uint8_t* kp = a.k + lane_at;
+      const uint8_t* sp = TY == KV4 ? a.scales + (int64_t)(lane & 7) * scale_bytes + g * L::SB : nullptr;
+      float* dst = a.mass + ((int64_t)b * a.Hkv + g) * a.mass_stride;
+      for (int rb = 0; rb < rows; rb += ROWS) {
+        const int nr = min(ROWS, rows - rb), ntile = (nr + 15) / 16 * 2;  // (two at a time)
+        // ---- the ring. Eight consecutive keys lie in one block: a chunk has four table entries,
+        // read a chunk ahead by the lanes
+        constexpr int UNSEEN = -2;
+        auto entry = [&](int i) -> int {
+          const int pos = key_first + i * KT + 8 * t4;
+          return i < mine && pos < nkeys ? __ldg(tab + (pos >> a.bs_log2)) : UNSEEN;
+        };
+        int ent = entry(0);
+        auto issue = [&](int i) {
+          if (i < mine) {
+            const uint32_t st = smem_u32(ring + (i % ST) * L::STAGE);
+            const int key0 = key_first + i * KT;
+            int base = -1;  // cache row of the first of this lane's eight keys
+            if (ent >= 0 && ent < a.num_blocks)
+              base = (ent << a.bs_log2) + ((key0 + 8 * t4) & (a.block_size - 1));
+            else if (ent != UNSEEN)
+              atomicOr(a.flags, FLAG_ATTN_SHAPE);  // an entry outside the pool
+            constexpr int PER = 32 / L::CH;  // keys of a step (2: within eight, 4, 8, 16)
+#pragma unroll
+            for (int j = 0; j < L::CH; ++j) {
+              const int kk = j * PER + lane / L::CH;
+              const int row = __shfl_sync(0xffffffffu, base, kk >> 3);
+              const bool ok = row >= 0 && key0 + kk < nkeys;
+              // (the lane's address holds its key of a step; steps shorter than eight keys walk on)
+              const int64_t at = (int64_t)(row + (PER < 8 ? (j * PER & 7) : 0)) * code_bytes;
+              cp_async<16>(st + L::place(kk, lane % L::CH) * 16, kp + (ok ? at : 0), ok);
+            }
+            if constexpr (TY == KV4) {
+              const int row = __shfl_sync(0xffffffffu, base, lane >> 3);
+              const bool ok = row >= 0 && key0 + lane < nkeys;
+              cp_async<L::SB>(st + CK * L::ROWB + lane * L::SB, sp + (ok ? (int64_t)row * scale_bytes : 0), ok);
+            }
+            ent = entry(i + 1);
+          }
+          cp_async_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < ST - 1; ++i) issue(i);
+
         __syncthreads();  // the last block's readers are done
         // ---- Q rows rb .. of the unit, in fragment order; row = window row i, head of the group
-        for (int idx = tid; idx < ntile * 8 * (HD / 8); idx += NTHREADS) {
-          const int r = idx / (HD / 8), c = idx % (HD / 8);  // 8 elements; a row's lie in
-          const int j = c >> 2, tt = c & 3;                  // neighbouring lanes
+        for (int idx = tid; idx < HG * ntile * 8 * (HD / 8); idx += NTHREADS) {
+          const int rr = idx / (HD / 8), c = idx % (HD / 8);  // 8 elements; a row's lie in
+          const int j = c >> 2, tt = c & 3;                   // neighbouring lanes
+          const int h = rr / (ntile * 8), r = rr - h * ntile * 8;
           const int rg = rb + r;
           const bool live = r < nr;
-          const int64_t row = live ? (pl.q_off + rg / a.G) * a.Hq + (int64_t)g * a.G + rg % a.G : 0;
+          const int64_t row = live ? (pl.q_off + rg / a.G) * a.Hq + (int64_t)(gg * HG + h) * a.G + rg % a.G : 0;
+          const float sck = a.scale_log2 * (TY == BF16 ? 1.f : a.kv_scale[gg * HG + h]);
           uint4 v = make_uint4(0, 0, 0, 0);
           if (live) v = __ldg(reinterpret_cast<const uint4*>(a.q + row * HD + L::elem(j, tt)));
           float sc = sck;
@@ -236,47 +356,85 @@ __global__ void __launch_bounds__(NTHREADS, 2) mass_kernel(const MassArgs a) {
             v = make_uint4(w[0], w[1], w[2], w[3]);
             sc = q_row_scale(sck, amax);
           }
-          sQ[((r >> 3) * (KS / 2) + j) * 32 + (r & 7) * 4 + tt] = v;
+          sQ0[((h * ROWS / 8 + (r >> 3)) * (KS / 2) + j) * 32 + (r & 7) * 4 + tt] = v;
           if (c == 0) {
             // rows past the block's: weight 2^-inf
-            s_row[r] = make_float2(sc, !live ? INFINITY : STATS ? 0.f : lse[row] * LOG2E);
+            s_row0[h * ROWS + r] = make_float2(sc, !live ? INFINITY : STATS || !a.lse ? 0.f : a.lse[row] * LOG2E);
             s_i[r] = live ? rg / a.G : n - 1;
           }
         }
-        if constexpr (STATS)
-          for (int i = tid; i < NW * RB; i += NTHREADS) s_ml[i] = make_float2(-INFINITY, 0.f);
         __syncthreads();
-        for (int j = j0; j < j1; ++j) {
-          const int key0 = j * KT + warp * 32;
-          if (key0 >= nkeys) continue;
+        if (!STATS && !a.lse) {
+          // L from the parts of the first pass: of the CTAs in whose ranges tiles of the unit
+          // begin, four lanes a row
+          const int c0 = cta_of_tile(first, pl.total, a.n_ctas);
+          const int c1 = cta_of_tile(first + (int64_t)(nt - 1) * W, pl.total, a.n_ctas);
+          const int64_t unit = (int64_t)b * groups + gg;
+          for (int idx = tid; idx < (HG * nr * 4 + 31) / 32 * 32; idx += NTHREADS) {
+            const int e = min(idx >> 2, HG * nr - 1), h = e / nr, r = e - h * nr;
+            float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+            for (int c = c0 + t4; c <= c1; c += 4) {
+              if (c > c0 && c < c1 && ceil_div(range_begin(a, pl.total, c) - first, W) >=
+                                          ceil_div(range_begin(a, pl.total, c + 1) - first, W))
+                continue;  // no tile begins there
+              const float2 v = __ldcg(a.part + ((unit + c) * HG + h) * a.max_rows + rb + r);
+              const float mn = fmaxf(m, v.x), mm = mn == -INFINITY ? 0.f : mn;
+              l = l * ex2(m - mm) + (v.x == -INFINITY ? v.y : v.y * ex2(v.x - mm));
+              m = mn;
+            }
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+              const float m2 = __shfl_xor_sync(0xffffffffu, m, o), l2 = __shfl_xor_sync(0xffffffffu, l, o);
+              const float mn = fmaxf(m, m2), mm = mn == -INFINITY ? 0.f : mn;
+              l = (m == -INFINITY ? l : l * ex2(m - mm)) + (m2 == -INFINITY ? l2 : l2 * ex2(m2 - mm));
+              m = mn;
+            }
+            if (t4 == 0 && (idx >> 2) < HG * nr) s_row0[h * ROWS + r].y = m + log2f(l);
+          }
+          __syncthreads();
+        }
+        float ml[STATS ? ROWS / 8 : 1][4];  // rows 2 t, 2 t + 1 of each n-tile: this lane's (max,
+                                            // sum) over its own keys
+        if constexpr (STATS)
+#pragma unroll
+          for (int q = 0; q < ROWS / 8; ++q) {
+            ml[q][0] = ml[q][1] = -INFINITY;
+            ml[q][2] = ml[q][3] = 0.f;
+          }
+        for (int i = 0; i < mine; ++i) {
+          cp_async_wait<ST - 2>();
+          __syncwarp();  // the chunk's bytes of every lane are here; the last chunk's are read
+          issue(i + ST - 1);
+          const uint8_t* st = ring + (i % ST) * L::STAGE;
+          const int key0 = key_first + i * KT;
+          float old[2][2];  // what the chunk's keys have had so far
+          if constexpr (!STATS)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int key = key0 + h * 16 + e * 8 + r8;
+                old[h][e] = t4 == 0 && key < nkeys ? dst[key] : 0.f;
+              }
           // ---- K fragments of 32 keys (two m-tiles)
           uint32_t kf[2][KS][4];
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int key = key0 + h * 16 + e * 8 + r8;
-              bool ok = key < nkeys;
-              int64_t row = 0;
-              if (ok) {
-                const int blk = __ldg(tab + (key >> a.bs_log2));
-                ok = blk >= 0 && blk < a.num_blocks;
-                if (!ok) atomicOr(a.flags, FLAG_ATTN_SHAPE);
-                row = ok ? ((int64_t)blk << a.bs_log2) + (key & (a.block_size - 1)) : 0;
-              }
-              const int64_t at = row * a.Hkv + g;
-              const uint8_t* src = a.k + at * L::ROWB + t4 * L::LANEB;
+              const int kk = h * 16 + e * 8 + r8;
 #pragma unroll
-              for (int i = 0; i < L::PIECES; ++i) {
+              for (int x0 = 0; x0 < L::PIECES; ++x0) {
                 uint32_t w[L::LANEB / 4];
                 if constexpr (L::LANEB == 16) {
-                  const uint4 v = ok ? __ldg(reinterpret_cast<const uint4*>(src + i * 64)) : make_uint4(0, 0, 0, 0);
+                  const uint4 v = *reinterpret_cast<const uint4*>(st + L::place(kk, x0 * 4 + t4) * 16);
                   w[0] = v.x;
                   w[1] = v.y;
                   w[2] = v.z;
                   w[3] = v.w;
                 } else {
-                  const uint2 v = ok ? __ldg(reinterpret_cast<const uint2*>(src + i * 32)) : make_uint2(0, 0);
+                  const uint2 v = *reinterpret_cast<const uint2*>(st + kk * L::ROWB + t4 * 8);
                   w[0] = v.x;
                   w[1] = v.y;
                 }
@@ -284,19 +442,18 @@ __global__ void __launch_bounds__(NTHREADS, 2) mass_kernel(const MassArgs a) {
                 if constexpr (TY == BF16) {
 #pragma unroll
                   for (int x = 0; x < PS; ++x) {
-                    kf[h][i * PS + x][e] = w[2 * x];
-                    kf[h][i * PS + x][e + 2] = w[2 * x + 1];
+                    kf[h][x0 * PS + x][e] = w[2 * x];
+                    kf[h][x0 * PS + x][e + 2] = w[2 * x + 1];
                   }
                 } else if constexpr (TY == E4M3) {
 #pragma unroll
                   for (int x = 0; x < PS; ++x) {
-                    kf[h][i * PS + x][e] = e4m3x2_to_f16x2(w[x] & 0xffffu);
-                    kf[h][i * PS + x][e + 2] = e4m3x2_to_f16x2(w[x] >> 16);
+                    kf[h][x0 * PS + x][e] = e4m3x2_to_f16x2(w[x] & 0xffffu);
+                    kf[h][x0 * PS + x][e + 2] = e4m3x2_to_f16x2(w[x] >> 16);
                   }
                 } else {
-                  const uint8_t* sp = a.scales + at * (HD / 8) + t4 * (HD / 64);
-                  uint32_t f = 0;
-                  if (ok) f = HD == 128 ? *reinterpret_cast<const uint16_t*>(sp) : *sp;
+                  const uint8_t* ss = st + CK * L::ROWB + kk * L::SB + t4 * (HD / 64);
+                  uint32_t f = HD == 128 ? *reinterpret_cast<const uint16_t*>(ss) : *ss;
                   f = e4m3x2_to_f16x2(f);
                   const uint32_t u[2] = {lo_twice(f), hi_twice(f)};
 #pragma unroll
@@ -312,71 +469,76 @@ __global__ void __launch_bounds__(NTHREADS, 2) mass_kernel(const MassArgs a) {
                 }
               }
             }
-          const bool edge = key0 + 32 > T;  // a key that some counted row does not see
+          const bool edge = key0 + CK > T;  // a key that some counted row does not see
           float acc[2][2] = {};  // keys r8, r8 + 8 of each m-tile
-          for (int q = 0; q < ntile; ++q) {
-            float s[2][4] = {};
+          // of n-tiles q, q + 1: four chains of MMAs
+          auto scores = [&](int q, float (&s)[2][2][4]) {
 #pragma unroll
-            for (int jj = 0; jj < KS / 2; ++jj) {
-              const uint4 v = sQ[(q * (KS / 2) + jj) * 32 + lane];
+            for (int jj = 0; jj < KS / 2; ++jj)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                mma<F16>(s[h], kf[h][2 * jj], v.x, v.y);
-                mma<F16>(s[h], kf[h][2 * jj + 1], v.z, v.w);
-              }
-            }
-            const float4 rr = *reinterpret_cast<const float4*>(s_row + q * 8 + 2 * t4);
-            if constexpr (STATS) {
-              const int2 ii = *reinterpret_cast<const int2*>(s_i + q * 8 + 2 * t4);
+              for (int w = 0; w < 2; ++w) {
+                const uint4 v = sQ[((q + w) * (KS / 2) + jj) * 32 + lane];
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {  // rows 2 t, 2 t + 1
-                float x[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  x[k] = s[k >> 1][(k & 1) * 2 + e] * (e ? rr.z : rr.x);
-                  const int key = key0 + (k >> 1) * 16 + (k & 1) * 8 + r8;
-                  if (edge && (key > T + (e ? ii.y : ii.x) || key >= nkeys)) x[k] = -INFINITY;
-                }
-                float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                const float mu = mx == -INFINITY ? 0.f : mx;
-                float sum = (ex2(x[0] - mu) + ex2(x[1] - mu)) + (ex2(x[2] - mu) + ex2(x[3] - mu));
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (r8 == 0) {
-                  float2* ml = s_ml + warp * RB + q * 8 + 2 * t4 + e;
-                  const float2 o = *ml;
-                  const float m = fmaxf(o.x, mx), mm = m == -INFINITY ? 0.f : m;
-                  *ml = make_float2(m, o.y * ex2(o.x - mm) + sum * ex2(mx - mm));
+                for (int h = 0; h < 2; ++h) {
+                  mma<F16>(s[w][h], kf[h][2 * jj], v.x, v.y);
+                  mma<F16>(s[w][h], kf[h][2 * jj + 1], v.z, v.w);
                 }
               }
-            } else {
-              float w[2][4];
+            if (edge) {
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  w[h][e] = ex2(fmaf(s[h][e], e & 1 ? rr.z : rr.x, e & 1 ? -rr.w : -rr.y));
-              if (edge) {
-                const int2 ii = *reinterpret_cast<const int2*>(s_i + q * 8 + 2 * t4);
+              for (int w = 0; w < 2; ++w) {
+                const int2 ii = *reinterpret_cast<const int2*>(s_i + (q + w) * 8 + 2 * t4);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                   for (int e = 0; e < 4; ++e) {
                     const int key = key0 + h * 16 + (e >> 1) * 8 + r8;
-                    if (key > T + (e & 1 ? ii.y : ii.x)) w[h][e] = 0.f;
+                    if (key > T + (e & 1 ? ii.y : ii.x)) s[w][h][e] = -INFINITY;
                   }
               }
+            }
+          };
+          if constexpr (STATS) {
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                acc[h][0] += w[h][0] + w[h][1];
-                acc[h][1] += w[h][2] + w[h][3];
+            for (int q = 0; q < ROWS / 8; q += 2) {
+              if (q >= ntile) break;
+              float s[2][2][4] = {};
+              scores(q, s);
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                const float4 rr = *reinterpret_cast<const float4*>(s_row + (q + w) * 8 + 2 * t4);
+                float(&o)[4] = ml[q + w];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {  // rows 2 t, 2 t + 1
+                  const float sc = e ? rr.z : rr.x;
+                  const float a0 = s[w][0][e], a1 = s[w][0][e + 2], a2 = s[w][1][e], a3 = s[w][1][e + 2];
+                  const float mx = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * sc;
+                  const float m = fmaxf(o[e], mx), nm = m == -INFINITY ? 0.f : -m;
+                  const float sum = (ex2(fmaf(a0, sc, nm)) + ex2(fmaf(a1, sc, nm))) +
+                                    (ex2(fmaf(a2, sc, nm)) + ex2(fmaf(a3, sc, nm)));
+                  o[2 + e] = fmaf(o[2 + e], ex2(o[e] + nm), sum);
+                  o[e] = m;
+                }
               }
             }
-          }
-          if constexpr (!STATS) {
-            float* dst = a.mass + ((int64_t)b * a.Hkv + g) * a.mass_stride;
+          } else {
+            for (int q = 0; q < ntile; q += 2) {
+              float s[2][2][4] = {};
+              scores(q, s);
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                const float4 rr = *reinterpret_cast<const float4*>(s_row + (q + w) * 8 + 2 * t4);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  float x[4];
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    x[e] = ex2(fmaf(s[w][h][e], e & 1 ? rr.z : rr.x, e & 1 ? -rr.w : -rr.y));
+                  acc[h][0] += x[0] + x[1];
+                  acc[h][1] += x[2] + x[3];
+                }
+              }
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -385,100 +547,82 @@ __global__ void __launch_bounds__(NTHREADS, 2) mass_kernel(const MassArgs a) {
                 v += __shfl_xor_sync(0xffffffffu, v, 1);
                 v += __shfl_xor_sync(0xffffffffu, v, 2);
                 const int key = key0 + h * 16 + e * 8 + r8;
-                if (t4 == 0 && key < nkeys) dst[key] += v;
+                if (t4 == 0 && key < nkeys) dst[key] = old[h][e] + v;
               }
           }
         }
+        cp_async_wait<0>();
         if constexpr (STATS) {
+          // lanes of a column, then the head's warps
+          __syncthreads();  // Q is read
+#pragma unroll
+          for (int q = 0; q < ROWS / 8; ++q)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float m = ml[q][e];
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+              // (a lane without a maximum has the sum 0, or NaN, which stays)
+              float l = ml[q][e] == -INFINITY ? ml[q][2 + e] : ml[q][2 + e] * ex2(ml[q][e] - m);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+              if (r8 == 0) s_ml[warp * ROWS + q * 8 + 2 * t4 + e] = make_float2(m, l);
+            }
           __syncthreads();
-          const int64_t slot = blockIdx.x + (int64_t)b * a.Hkv + g;
-          for (int r = tid; r < nr; r += NTHREADS) {
+          const int64_t slot = blockIdx.x + (int64_t)b * groups + gg;
+          for (int e = tid; e < HG * nr; e += NTHREADS) {
+            const int h = e / nr, r = e - h * nr;
             float m = -INFINITY, l = 0.f;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) m = fmaxf(m, s_ml[w * RB + r].x);
+            for (int w = 0; w < NK; ++w) m = fmaxf(m, s_ml[(w * HG + h) * ROWS + r].x);
             const float mm = m == -INFINITY ? 0.f : m;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) l += s_ml[w * RB + r].y * ex2(s_ml[w * RB + r].x - mm);
-            a.part[slot * a.max_rows + rb + r] = make_float2(m, l);
+            for (int w = 0; w < NK; ++w) {
+              const float2 v = s_ml[(w * HG + h) * ROWS + r];
+              l += v.x == -INFINITY ? v.y : v.y * ex2(v.x - mm);
+            }
+            a.part[(slot * HG + h) * a.max_rows + rb + r] = make_float2(m, l);
           }
         }
       }
-      t += j1 - j0;
-      in_b += j1 - j0;
     }
-    pl.in_b = 0;
-    pl.q_off += 1 + D;
-  }
-}
-
-// L of every counted row: the parts of the CTAs whose ranges hold its (sequence, KV head)'s
-// tiles, joined in order. The CTAs walk the line as the pass before did; a CTA takes the units
-// whose first tile is in its range.
-__global__ void __launch_bounds__(NTHREADS) mass_join_kernel(const MassArgs a) {
-  pdl_trigger();
-  pdl_wait();
-  Place pl;
-  if (!find_place(a, pl)) return;
-  int64_t t = pl.t;
-  for (int b = pl.b; t < pl.end; ++b) {
-    int T, D, n;
-    lengths(a, b, T, D, n);
-    const int nt = tiles_of(T, n);
-    const int rows = a.G * n;
-    for (int64_t in_b = pl.in_b; in_b < (int64_t)a.Hkv * nt && t < pl.end;) {
-      const int g = (int)(in_b / nt), j0 = (int)(in_b - (int64_t)g * nt);
-      if (j0 == 0) {
-        // the line's ranges: tile x is CTA ((x + 1) n_ctas - 1) / total's
-        const int c0 = cta_of_tile(t, pl.total, a.n_ctas), c1 = cta_of_tile(t + nt - 1, pl.total, a.n_ctas);
-        const int64_t unit = (int64_t)b * a.Hkv + g;
-        for (int r = threadIdx.x; r < rows; r += NTHREADS) {
-          float m = -INFINITY, l = 0.f;
-          for (int c = c0; c <= c1; ++c) {
-            if (!cta_has_tiles(c, pl.total, a.n_ctas)) continue;
-            const float2 v = a.part[(unit + c) * a.max_rows + r];
-            const float mn = fmaxf(m, v.x), mm = mn == -INFINITY ? 0.f : mn;
-            l = l * ex2(m - mm) + v.y * ex2(v.x - mm);
-            m = mn;
-          }
-          a.lse_ws[(pl.q_off + r / a.G) * a.Hq + (int64_t)g * a.G + r % a.G] = (m + log2f(l)) * LN2;
-        }
-      }
-      const int64_t step = min((int64_t)nt - j0, pl.end - t);
-      t += step;
-      in_b += step;
-    }
-    pl.in_b = 0;
+    pl.base += groups * length;
     pl.q_off += 1 + D;
   }
 }
 
 struct MassWs {
-  size_t lse, part, total;
+  size_t part, total;
 };
-int mass_ctas(int sms) { return 2 * sms; }
+int mass_ctas(int sms) { return sms; }
 MassWs mass_ws(const sv_attn_desc* d, int sms) {
   MassWs w;
   const size_t max_rows = (size_t)(d->num_q_heads / d->num_kv_heads) * (1 + d->max_draft_len);
-  const size_t slots = (size_t)mass_ctas(sms) + (size_t)d->batch * d->num_kv_heads;
-  w.lse = 256;
-  w.part = align_up(w.lse + 4 * (size_t)d->q_rows * d->num_q_heads, 256);
+  const size_t slots = 2 * (size_t)mass_ctas(sms) + (size_t)d->batch * d->num_kv_heads;
+  w.part = 256;
   w.total = align_up(w.part + 8 * slots * max_rows, 256);
   return w;
 }
 
-template <int HD, int TY, bool STATS>
+template <int HD, int TY, bool STATS, int HG>
 cudaError_t launch_pass(const MassArgs& a, cudaStream_t s) {
-  const size_t smem = RB * HD * 2 + RB * (sizeof(float2) + sizeof(int)) + (STATS ? NW * RB * sizeof(float2) : 0);
-  auto kernel = mass_kernel<HD, TY, STATS>;
+  using L = LM<HD, TY>;
+  constexpr int ROWS = STATS ? RS : RB / HG;
+  constexpr size_t smem = HG * ROWS * (HD * 2 + 8) + ROWS * 4 + NW * L::ST * L::STAGE;
+  static_assert(smem <= 226 * 1024 && NW * ROWS * 8 <= HG * ROWS * HD * 2, "shared memory of an SM");
+  auto kernel = mass_kernel<HD, TY, STATS, HG>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(a.n_ctas), dim3(NTHREADS), smem, s, a);
 }
+template <int HD, int TY, bool STATS>
+cudaError_t launch_pass(const MassArgs& a, cudaStream_t s) {
+  return a.heads == 2 ? launch_pass<HD, TY, STATS, 2>(a, s) : launch_pass<HD, TY, STATS, 1>(a, s);
+}
 template <int HD, int TY>
 cudaError_t launch_all(const MassArgs& a, cudaStream_t s) {
   if (!a.lse) {
-    cudaError_t e = launch_pass<HD, TY, true>(a, s);
-    if (e == cudaSuccess) e = launch_pdl(mass_join_kernel, dim3(a.n_ctas), dim3(NTHREADS), 0, s, a);
+    const cudaError_t e = launch_pass<HD, TY, true>(a, s);
     if (e != cudaSuccess) return e;
   }
   return launch_pass<HD, TY, false>(a, s);
@@ -504,7 +648,6 @@ cudaError_t launch_mass(const sv_attn_desc* d, float scale_log2, const void* q, 
   a.draft_len = draft_len;
   a.row_count = row_count;
   a.lse = lse;
-  a.lse_ws = (float*)((uint8_t*)ws + w.lse);
   a.part = (float2*)((uint8_t*)ws + w.part);
   a.mass = mass;
   a.flags = (uint32_t*)ws;
@@ -522,6 +665,11 @@ cudaError_t launch_mass(const sv_attn_desc* d, float scale_log2, const void* q, 
   while ((1 << a.bs_log2) < block_size) ++a.bs_log2;
   a.max_rows = a.G * (1 + d->max_draft_len);
   a.n_ctas = mass_ctas(sms);
+  // (swept: bf16 1, 2, 3, 8 of the largest case 134, 128, 134, 146 us; 4 bits 1, 3, 4, 8: 26.0,
+  // 24.3, 24.5, 25.5)
+  a.fixed = d->kv_dtype == SV_BF16 ? 2 : 3;
+  // two heads while their rows fit where one's would: half as many units to start
+  a.heads = a.Hkv % 2 == 0 && a.max_rows <= RB / 2 ? 2 : 1;
   a.scale_log2 = scale_log2;
   if (d->head_dim == 128)
     return d->kv_dtype == SV_BF16 ? launch_all<128, BF16>(a, s)

@@ -22,9 +22,12 @@ namespace sv {
 namespace {
 
 constexpr int ST = 1024;        // threads of select
-constexpr int MTH = 256;        // threads of move
 constexpr int BINS = 2048;
-constexpr int SLICE = 32;       // bytes of a column slice (a sector)
+constexpr int MTH = 256;        // threads of move
+// Bytes of a column slice, and pieces of 16 of a thread in flight. (32 rows of 16384 positions cut
+// to 4096, 4 heads of 128 bytes, two pools: 82 us; slices of 32 and 128 bytes 95, 127; 2 and 8
+// pieces 96, 88.)
+constexpr int SLICE = 64, MOVES = 4;
 
 struct EvictArgs {
   sv_page_table t;
@@ -158,9 +161,15 @@ __global__ void __launch_bounds__(ST) select_kernel(const EvictArgs a) {
       const uint32_t mask = pass == 2 ? 1023u : 2047u;
       for (int x = tid; x < BINS; x += ST) s_hist[x] = 0;
       __syncthreads();
-      for (int j = p.first + tid; j < p.mid; j += ST) {
-        const uint32_t k = key_of(w[j]);
-        if ((k & known) == prefix) atomicAdd(&s_hist[(k >> shift) & mask], 1u);
+      for (int j0 = p.first + tid; j0 < p.mid; j0 += 8 * ST) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = j0 + e * ST < p.mid ? w[j0 + e * ST] : 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t k = key_of(x[e]);
+          if (j0 + e * ST < p.mid && (k & known) == prefix) atomicAdd(&s_hist[(k >> shift) & mask], 1u);
+        }
       }
       __syncthreads();
       // thread x has bins 2 x and 2 x + 1 counted from the top
@@ -223,36 +232,48 @@ struct VecOf<8> {
   using type = uint2;
 };
 
-// One slice: `cols` pieces of V bytes at `base`, rows of `row_bytes`, positions through the
-// table's row.
+// One slice: `cols` pieces of V bytes at `base`, positions `pos_bytes` apart in a page, through
+// the table's row. The next batch's places (src, then the table) are looked up while this one's
+// data is on its way.
 template <int V>
 __device__ __forceinline__ void move_slice(const EvictArgs& a, const RowPlan& p, const int32_t* src,
-                                           uint8_t* base, int64_t row_bytes, int64_t pos_bytes, int cols) {
+                                           uint8_t* base, int64_t pos_bytes, int cols) {
   using T = typename VecOf<V>::type;
-  constexpr int U = 8;
+  constexpr int U = MOVES;
   const int32_t* tab = a.t.block_table + (int64_t)p.r * a.t.max_blocks_per_seq;
-  const int per = MTH / cols;  // destinations of a batch and unroll step
+  const int per = MTH / cols;  // destinations of an unroll step
   const int lr = threadIdx.x / cols, lc = threadIdx.x % cols;
-  auto at = [&](int pos) {
-    const int64_t page = tab[pos >> a.bs_log2];
-    return base + ((page << a.bs_log2) + (pos & ((1 << a.bs_log2) - 1))) * pos_bytes + lc * V;
-  };
-  for (int k0 = p.first; k0 < p.m; k0 += per * U) {
-    T v[U];
-    int from[U];
+  base += lc * V;
+  auto row_of = [&](int pos) { return (tab[pos >> a.bs_log2] << a.bs_log2) + (pos & ((1 << a.bs_log2) - 1)); };
+  int from[U], to[U];  // cache rows; from -1: nothing to move
+  auto look = [&](int k0) {
 #pragma unroll
     for (int e = 0; e < U; ++e) {
       const int k = k0 + e * per + lr;
       from[e] = lr < per && k < p.m ? src[k] : -1;
-      if (from[e] == k) from[e] = -1;  // stays where it is
     }
 #pragma unroll
-    for (int e = 0; e < U; ++e)
-      if (from[e] >= 0) v[e] = *reinterpret_cast<const T*>(at(from[e]));
+    for (int e = 0; e < U; ++e) {
+      const int k = k0 + e * per + lr;
+      if (from[e] == k) from[e] = -1;  // stays where it is
+      to[e] = from[e] >= 0 ? row_of(k) : 0;
+      if (from[e] >= 0) from[e] = row_of(from[e]);
+    }
+  };
+  look(p.first);
+  for (int k0 = p.first; k0 < p.m; k0 += per * U) {
+    T v[U];
+    int dst[U];
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      dst[e] = from[e] >= 0 ? to[e] : -1;
+      if (from[e] >= 0) v[e] = *reinterpret_cast<const T*>(base + from[e] * pos_bytes);
+    }
+    look(k0 + per * U);
     __syncthreads();  // the batch is read
 #pragma unroll
     for (int e = 0; e < U; ++e)
-      if (from[e] >= 0) *reinterpret_cast<T*>(at(k0 + e * per + lr)) = v[e];
+      if (dst[e] >= 0) *reinterpret_cast<T*>(base + dst[e] * pos_bytes) = v[e];
   }
 }
 
@@ -299,9 +320,9 @@ __global__ void __launch_bounds__(MTH) move_kernel(const EvictArgs a, const __gr
       uint8_t* base = (uint8_t*)pools.p[k].base + g * row_bytes + s * SLICE;
       const int bytes = (int)min((int64_t)SLICE, row_bytes - s * SLICE);
       if (bytes % 16 == 0 && row_bytes % 16 == 0)
-        move_slice<16>(a, p, src, base, row_bytes, pos_bytes, bytes / 16);
+        move_slice<16>(a, p, src, base, pos_bytes, bytes / 16);
       else
-        move_slice<8>(a, p, src, base, row_bytes, pos_bytes, bytes / 8);
+        move_slice<8>(a, p, src, base, pos_bytes, bytes / 8);
       return;
     }
     s -= n;

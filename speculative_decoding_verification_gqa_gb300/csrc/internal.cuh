@@ -409,7 +409,7 @@ struct Kv4Attn {
   long long wait_limit;
 };
 constexpr int KV4_KT = 128;    // keys per tile of the line
-int attn_kv4_ctas(int rows_per_kv, int sms);
+int attn_kv4_ctas(int sms);
 int attn_kv4_rows(int rows_per_kv);
 cudaError_t launch_attn_kv4(const Kv4Attn& p, cudaStream_t s);
 cudaError_t launch_attn_kv4_tc(const Kv4Attn& p, cudaStream_t s);

@@ -322,18 +322,19 @@ __global__ void __launch_bounds__(NTH) kv4_read_kernel(const Kv4Args a) {
   }
 }
 
-template <class K1, class K4>
-cudaError_t launch_rows(K1 one, K4 four, Kv4Args a, int sms, cudaStream_t s) {
+template <class K1, class KN>
+cudaError_t launch_rows(K1 one, KN some, int thread_rows, Kv4Args a, int sms, cudaStream_t s) {
   a.row_items = 2 * a.Hkv * (a.d / 16);
   a.lanes = a.row_items < NTH ? a.row_items : NTH;
   a.rows_at_once = NTH / a.lanes;
-  // An item a thread while that leaves no SM with more than two CTAs; else 16 rows a thread, four
-  // at a time, so that the scan for the rows' places costs little next to them.
+  // An item a thread while that leaves no SM with more than two CTAs; else `thread_rows`, some of
+  // them at a time, so that the scan for the rows' places costs little next to them. (49 thousand
+  // rows of 8 heads written and read back: 8 and 16 rows 129 us, 4 and 4 134, 2 and 2 162.)
   const bool few = a.rows * a.row_items <= 2 * (int64_t)sms * NTH;
-  const int want = few ? a.rows_at_once : 16 * a.rows_at_once;
+  const int want = few ? a.rows_at_once : thread_rows * a.rows_at_once;
   a.cta_rows = want > MAX_CTA_ROWS ? MAX_CTA_ROWS : want;
   const unsigned grid = (unsigned)((a.rows + a.cta_rows - 1) / a.cta_rows);
-  return launch_pdl(few ? one : four, dim3(grid), dim3(NTH), 0, s, a);
+  return launch_pdl(few ? one : some, dim3(grid), dim3(NTH), 0, s, a);
 }
 
 Kv4Args args_of(const sv_kv4_pages& p, int B, const int32_t* table, int max_blocks,
@@ -368,7 +369,7 @@ cudaError_t launch_kv4_write(const sv_kv4_pages& p, int B, const int32_t* table,
   a.v = (const uint16_t*)v;
   a.k_stride = k_stride;
   a.v_stride = v_stride;
-  return launch_rows(kv4_write_kernel<1>, kv4_write_kernel<4>, a, sms, s);
+    return launch_rows(kv4_write_kernel<1>, kv4_write_kernel<2>, 8, a, sms, s);
 }
 
 cudaError_t launch_kv4_read(const sv_kv4_pages& p, int B, const int32_t* table, int max_blocks,
@@ -377,7 +378,7 @@ cudaError_t launch_kv4_read(const sv_kv4_pages& p, int B, const int32_t* table, 
   Kv4Args a = args_of(p, B, table, max_blocks, start, count, rows, ws);
   a.k_out = (uint16_t*)k_out;
   a.v_out = (uint16_t*)v_out;
-  return launch_rows(kv4_read_kernel<1>, kv4_read_kernel<4>, a, sms, s);
+  return launch_rows(kv4_read_kernel<1>, kv4_read_kernel<4>, 16, a, sms, s);
 }
 
 }  // namespace sv

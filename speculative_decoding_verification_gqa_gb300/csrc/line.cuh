@@ -60,26 +60,28 @@ struct LineAt {  // a sequence, and what lies before it
   int64_t virt, units, rows;
 };
 
-// One pass over the lengths by a CTA of NTH threads: the totals; with `at`, also the sequence
-// that holds virtual position (or, with by_unit, unit) `target`. False if a length is out of
-// range or the rows are more than q's.
-template <int NTH>
-__device__ bool line_scan(const Kv4Attn& p, Line& total, int64_t target, bool by_unit, LineAt* at) {
+// The totals, by a CTA of NTH threads; then the sequence that holds a virtual position (or, with
+// by_unit, a unit) which `target(by_unit)` works out from them (-1: none). False if there is
+// none or, with the flag set, if a length is out of range or the rows are more than q's. One
+// pass over the lengths for up to NTH sequences, whose shares stay in registers, else two.
+template <int NTH, class Target>
+__device__ bool line_scan(const Kv4Attn& p, Line& total, LineAt* at, Target target) {
   constexpr int NWARP = NTH / 32;
   __shared__ int64_t s_warp[NWARP][4];
   __shared__ int64_t s_at[4];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int groups = line_groups(p);
   int64_t carry[4] = {0, 0, 0, 0};
-  int longest = 0;  // tiles of the longest unit of this thread's sequences
+  int64_t v[4], x[4];  // of this thread's sequence: virtual tiles, tiles, units, rows; before it
+  int longest = 0;     // tiles of the longest unit of this thread's sequences
   bool bad = false;
-  for (int base = 0; base < p.B; base += NTH) {
+  auto shares = [&](int base) {
     const int b = base + tid;
-    int64_t v[4] = {0, 0, 0, 0};  // virtual tiles, tiles, units, rows
+    v[0] = v[1] = v[2] = v[3] = 0;
+    LineSeq s;
     if (b < p.B) {
-      LineSeq s;
-      int kb;
       if (line_seq(p, b, s)) {
+        int kb;
         longest = max(longest, line_tiles(p, s.T, s.D, 0, kb));
         v[0] = s.virt * groups;
         v[1] = s.tiles * groups;
@@ -89,38 +91,36 @@ __device__ bool line_scan(const Kv4Attn& p, Line& total, int64_t target, bool by
         bad = true;
       }
     }
-    int64_t x[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1)
+    for (int k = 0; k < 4; ++k) x[k] = v[k];
+    const int nw = min(NWARP, (p.B - base + 31) / 32);  // warps with a sequence
+    if (wid < nw) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x[k], o);
-        if (lane >= o) x[k] += y;
-      }
-    if (lane == 31)
+      for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s_warp[wid][k] = x[k];
+        for (int k = 0; k < 4; ++k) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, x[k], o);
+          if (lane >= o) x[k] += y;
+        }
+      if (lane == 31)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s_warp[wid][k] = x[k];
+    }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       int64_t before = carry[k];
-      for (int w = 0; w < NWARP; ++w) {
+      for (int w = 0; w < nw; ++w) {
         const int64_t y = s_warp[w][k];
         if (w < wid) before += y;
         carry[k] += y;
       }
       x[k] += before - v[k];  // exclusive
     }
-    if (at) {
-      const int k = by_unit ? 2 : 0;
-      if (target >= x[k] && target < x[k] + v[k]) {
-        s_at[0] = b;
-        s_at[1] = x[0];
-        s_at[2] = x[2];
-        s_at[3] = x[3];
-      }
-    }
-    __syncthreads();  // s_warp is reused
+  };
+  for (int base = 0; base < p.B; base += NTH) {
+    if (base > 0) __syncthreads();  // s_warp is reused
+    shares(base);
   }
   total.virt = carry[0];
   total.tiles = carry[1];
@@ -130,8 +130,35 @@ __device__ bool line_scan(const Kv4Attn& p, Line& total, int64_t target, bool by
   const int64_t share = total.ctas > 0 ? carry[0] / total.ctas : 0;
   total.whole = !__syncthreads_or(longest > share + p.join_tiles) && carry[2] <= p.n_ctas;
   if (total.whole) total.ctas = (int)carry[2];
-  if (__syncthreads_or(bad || carry[3] > p.q_rows)) return false;
-  if (at) *at = LineAt{(int)s_at[0], s_at[1], s_at[2], s_at[3]};
+  if (__syncthreads_or(bad || carry[3] > p.q_rows)) {
+    if (tid == 0) atomicOr(p.flags, FLAG_ATTN_SHAPE);
+    return false;
+  }
+  bool by_unit = false;
+  const int64_t t = target(by_unit);
+  if (t < 0) return false;
+  const int k = by_unit ? 2 : 0;
+  auto look = [&](int base) {
+    if (t >= x[k] && t < x[k] + v[k]) {
+      s_at[0] = base + tid;
+      s_at[1] = x[0];
+      s_at[2] = x[2];
+      s_at[3] = x[3];
+    }
+  };
+  if (p.B <= NTH) {
+    look(0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) carry[i] = 0;
+    for (int base = 0; base < p.B; base += NTH) {
+      __syncthreads();
+      shares(base);
+      look(base);
+    }
+  }
+  __syncthreads();
+  *at = LineAt{(int)s_at[0], s_at[1], s_at[2], s_at[3]};
   return true;
 }
 
@@ -211,24 +238,25 @@ __device__ __forceinline__ LineWalk line_enter(const Kv4Attn& p, const LineAt& a
 template <int NTH>
 __device__ bool line_begin(const Kv4Attn& p, int c, LineWalk& w) {
   Line total;
-  if (!line_scan<NTH>(p, total, 0, false, nullptr)) {
-    if (threadIdx.x == 0) atomicOr(p.flags, FLAG_ATTN_SHAPE);
-    return false;
-  }
   LineAt at;
-  if (c >= total.ctas) return false;
+  int64_t v0 = 0, v1 = 0;
+  if (!line_scan<NTH>(p, total, &at, [&](bool& by_unit) -> int64_t {
+        if (c >= total.ctas) return -1;
+        by_unit = total.whole;
+        if (total.whole) return c;
+        v0 = (int64_t)c * total.virt / total.ctas;
+        v1 = (int64_t)(c + 1) * total.virt / total.ctas;
+        return v0;
+      }))
+    return false;
   if (total.whole) {
-    line_scan<NTH>(p, total, c, true, &at);
     w = line_enter(p, at, c - at.units, true);
-    w.v0 = w.us;
     int kb;
-    w.v1 = w.us + p.switch_tiles + line_tiles(p, p.seq_lens[w.b], p.draft_len[w.b], w.mt, kb);
-    return true;
+    v0 = w.us;
+    v1 = w.us + p.switch_tiles + line_tiles(p, p.seq_lens[w.b], p.draft_len[w.b], w.mt, kb);
+  } else {
+    w = line_enter(p, at, v0 - at.virt, false);
   }
-  const int64_t v0 = (int64_t)c * total.virt / total.ctas;
-  const int64_t v1 = (int64_t)(c + 1) * total.virt / total.ctas;
-  line_scan<NTH>(p, total, v0, false, &at);
-  w = line_enter(p, at, v0 - at.virt, false);
   w.v0 = v0;
   w.v1 = v1;
   return true;
