@@ -284,7 +284,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         const int rows = min(MT, p.G * (g.D + 1) - g.mt * MT), head = g.g * p.heads + hsel;
         for (int i = lane; i < rows; i += 32) {
           const int rg = g.mt * MT + i;
-          d->row[i] = (int)((g.q_off + rg / p.G) * p.Hq + head * p.G + rg % p.G);
+          const int row = (int)((g.q_off + rg / p.G) * p.Hq + head * p.G + rg % p.G);
+          d->row[i] = row;
+#pragma unroll
+          for (int c = 0; c < HD / 64; ++c)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"((const uint16_t*)p.q + (int64_t)row * HD + c * 64));
         }
         if (lane == 0) {
           d->b = g.b;
@@ -395,16 +399,13 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     };
     bool more = next_unit();
     if (more) request_q();
-    while (ok && more) {
-      const int T = s->T - s->kbase;  // positions below: relative to kbase
-      const int rows = s->rows, j0 = s->j0, j1 = s->j1;
-      const int i_row = r < rows ? (s->row0 + r) / p.G : s->D;
-      const int hi_row = T + i_row;            // the row's last visible key
-      const int lo_row = hi_row + 1 - window;  // its first, under a sliding window
-      // Q row x 2^e -> f16 pairs in TMEM; each warpgroup writes its half
-      float sc;
+    while (true) {
+      // The warpgroups leave together if a warp of either is without a unit (a wait gave up).
+      if (!softmax_pair_and(more)) break;
+      // Q row x 2^e -> f16 pairs in TMEM; each warpgroup writes its half, and they exchange the
+      // halves' maxima
+      uint32_t rq[HD / 4], amax = 0;
       {
-        uint32_t rq[HD / 4], amax = 0;
 #pragma unroll
         for (int c = 0; c < QC; ++c) {
 #pragma unroll
@@ -423,21 +424,26 @@ __global__ void __launch_bounds__(NTHREADS, 1)
 #pragma unroll
         for (int e = 0; e < HD / 4; ++e) amax = max(amax, max(rq[e] & 0x7fffu, (rq[e] >> 16) & 0x7fffu));
         bars->qmax[wg][r] = amax;
-        softmax_pair_and(true);
-        amax = max(amax, bars->qmax[wg ^ 1][r]);
-        const float f = exp2_of(q_exponent(amax));
-#pragma unroll
-        for (int e = 0; e < HD / 4; ++e)
-          rq[e] = pack_f16(__uint_as_float(rq[e] << 16) * f, __uint_as_float(rq[e] & 0xffff0000u) * f);
-        if constexpr (HD == 128)
-          tmem_st32(tq + COL_Q + wg * 32, rq);
-        else
-          tmem_st16(tq + COL_Q + wg * 16, rq);
-        tmem_wait_st();
-        sc = q_row_scale(p.scale_log2 * p.kv_scale[s->g], amax);
       }
+      softmax_pair_and(true);
+      amax = max(amax, bars->qmax[wg ^ 1][r]);
+      const float f = exp2_of(q_exponent(amax));
+#pragma unroll
+      for (int e = 0; e < HD / 4; ++e)
+        rq[e] = pack_f16(__uint_as_float(rq[e] << 16) * f, __uint_as_float(rq[e] & 0xffff0000u) * f);
+      if constexpr (HD == 128)
+        tmem_st32(tq + COL_Q + wg * 32, rq);
+      else
+        tmem_st16(tq + COL_Q + wg * 16, rq);
+      tmem_wait_st();
+      const float sc = q_row_scale(p.scale_log2 * p.kv_scale[s->g], amax);
       fence_before();
       warp_arrive(&bars->q_full);
+      const int T = s->T - s->kbase;  // positions below: relative to kbase
+      const int rows = s->rows, j0 = s->j0, j1 = s->j1;
+      const int i_row = r < rows ? (s->row0 + r) / p.G : s->D;
+      const int hi_row = T + i_row;            // the row's last visible key
+      const int lo_row = hi_row + 1 - window;  // its first, under a sliding window
 
       float m_ref = -INFINITY, lh = 0.f;
       uint32_t it_last = 0;
@@ -534,10 +540,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
       bars->xm[wg][r] = m_ref;
       bars->xl[wg][r] = lh;
-      if (!softmax_pair_and(good)) {
-        ok = false;
-        break;
-      }
+      if (!softmax_pair_and(good)) break;
       fence_after();  // the other warpgroup's accumulator is complete too
 
       // ---- epilogue: join the two accumulators; this warpgroup's half of the columns
