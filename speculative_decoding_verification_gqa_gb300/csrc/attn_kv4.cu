@@ -493,22 +493,21 @@ __global__ void __launch_bounds__(NTHREADS, SM_CTAS) attn_kv4_kernel(const Kv4At
 // ------------------------------------------------------------------------------ join
 
 constexpr int JT = 256;   // threads
-constexpr int JROWS = 8;  // rows of an item
 
 // The units that several CTAs share: their parts, in the CTAs' order, by the rule of the online
-// softmax. An item is JROWS rows of one head of a unit. With few parts a warp takes a row; with
-// many all warps take every eighth part of the same row and add up through shared memory, so
-// that one long sequence's hundreds of parts are not read one after another. Items in
-// contiguous ranges of the grid's CTAs, as the lines are walked.
+// softmax. An item is `jrows` rows of one head of a unit. With few parts a warp takes a row; with
+// many all warps take every eighth part of the same row and add up through shared memory, and
+// an item is that row, so that one long sequence's hundreds of parts are not read one after
+// another. Items in contiguous ranges of the grid's CTAs, as the lines are walked.
 template <int HD>
-__global__ void __launch_bounds__(JT) kv4_join_kernel(const Kv4Attn p) {
+__global__ void __launch_bounds__(JT) kv4_join_kernel(const Kv4Attn p, int jrows) {
   __shared__ float4 s_o[JT / 32][HD / 4];
   __shared__ float2 s_ml[JT / 32];
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // The lengths are read before the wait: the attention kernel's CTAs let this one start when
   // they have waited themselves, so whatever wrote the lengths is complete.
-  const int per = p.heads * ((p.mr + JROWS - 1) / JROWS);  // items of a unit
+  const int per = p.heads * ((p.mr + jrows - 1) / jrows);  // items of a unit
   Line total;
   LineAt at;
   int64_t it = 0, end = 0;
@@ -541,7 +540,7 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const Kv4Attn p) {
     const int rows = min(p.mr, p.G * (s.D + 1) - s.mt * p.mr);
     const bool spread = c1 - c0 >= JT / 32;
     for (; it < next; ++it) {
-      const int i = (int)(it % per), h = i % p.heads, r0 = i / p.heads * JROWS;
+      const int i = (int)(it % per), h = i % p.heads, r0 = i / p.heads * jrows;
       const int gh = s.g * p.heads + h;
       // parts c0 + w, c0 + w + step, ... of row r
       auto gather = [&](int r, int w, int step, float4& acc, float& m, float& l) {
@@ -585,12 +584,12 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const Kv4Attn p) {
       float m, l;
       if (!spread) {
         const int r = r0 + warp;
-        if (r < rows) {
+        if (warp < jrows && r < rows) {
           gather(r, 0, 1, acc, m, l);
           if (lane < LN) store_row<HD>(p, out_row(r), gh, lane, acc, m, l);
         }
       } else {
-        for (int r = r0; r < min(rows, r0 + JROWS); ++r) {
+        for (int r = r0; r < min(rows, r0 + jrows); ++r) {
           gather(r, warp, JT / 32, acc, m, l);
           if (lane < LN) s_o[warp][lane] = acc;
           if (lane == 0) s_ml[warp] = make_float2(m, l);
@@ -644,10 +643,13 @@ cudaError_t launch_attn_kv4(const Kv4Attn& p, cudaStream_t s) {
 
 cudaError_t launch_kv4_join(const Kv4Attn& p, int sms, cudaStream_t s) {
   const int64_t rows = (int64_t)p.G * (1 + p.max_draft);
-  const int64_t items = (int64_t)p.B * p.Hkv * ((rows + p.mr - 1) / p.mr) * ((p.mr + JROWS - 1) / JROWS);
+  const int64_t units = (int64_t)p.B * (p.Hkv / p.heads) * ((rows + p.mr - 1) / p.mr);
+  // rows of an item: one where a unit has many parts
+  const int jrows = p.n_ctas >= JT / 32 * units ? 1 : JT / 32;
+  const int64_t items = units * p.heads * ((p.mr + jrows - 1) / jrows);
   const dim3 grid((unsigned)std::min<int64_t>(items, 4 * (int64_t)sms));
-  return p.d == 128 ? launch_pdl(kv4_join_kernel<128>, grid, dim3(JT), 0, s, p)
-                    : launch_pdl(kv4_join_kernel<64>, grid, dim3(JT), 0, s, p);
+  return p.d == 128 ? launch_pdl(kv4_join_kernel<128>, grid, dim3(JT), 0, s, p, jrows)
+                    : launch_pdl(kv4_join_kernel<64>, grid, dim3(JT), 0, s, p, jrows);
 }
 
 }  // namespace sv
