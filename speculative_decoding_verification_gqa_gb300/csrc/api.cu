@@ -23,14 +23,6 @@ namespace {
 constexpr int SWITCH_TILES_TC_FP8 = SV_SWITCH_F8;
 constexpr int SWITCH_TILES_TC_BF16 = SV_SWITCH_BF16;
 constexpr int SWITCH_TILES_MMA = 2;
-// 4-bit cache: a unit's start and the join in tiles' time; units from which on two neighbouring heads make
-// one; tiles of the longest sequence up to which a CTA takes a whole unit.
-constexpr int SWITCH_TILES_KV4 = 9;
-constexpr int SWITCH_TILES_KV4_MMA = 2;
-constexpr int JOIN_TILES_KV4 = 12;
-constexpr int JOIN_TILES_KV4_MMA = 6;
-constexpr int KV4_PAIR_UNITS = 16;
-constexpr int KV4_WHOLE_TILES = 4;
 // Shared prefixes. A unit's start in 128-key tiles of 256 rows and in 64-key tiles of 128 rows,
 // and the SM time of the latter (two at a time on an SM) in the former. Measured around them at
 // d = 128 (short runs of calls back to back, below the power limit; 64 sequences over a prefix
@@ -803,32 +795,83 @@ int64_t kv4_rows_per_head(const sv_attn_desc* d) {
   return (int64_t)(d->num_q_heads / d->num_kv_heads) * (1 + d->max_draft_len);
 }
 
-// 1 = warp-level MMAs (attn_kv4.cu), 2 = tcgen05 (attn_kv4_tc.cu)
+// The rules of a 4-bit attention call. The times are of calls replayed from a graph, d = 128, by
+// sequences x longest of their ragged lengths, 8 KV heads and 4 query heads each if not stated.
+//
+// Virtual tiles charged for starting a unit. The tcgen05 kernel at 0-8 tiles of 2, 4, 6, 9, 13:
+// 32 x 4000, 8 tokens 71.3, 69.5, 70.0, 71.9, 75.4 us; 57 x 457, 16 tokens, 7 query heads 57.4,
+// 55.5, 54.7, 54.7, 54.8. The mma kernel at 0, 1, 2, 4, 8, one token: 64 x 8000 84.9, 76.5, 77.6,
+// 80.0, 86.4; one of 30000, 4 KV heads 20.7, 20.6, 22.5, 21.3, 22.5.
+constexpr int SWITCH_TILES_KV4 = 6;
+constexpr int SWITCH_TILES_KV4_MMA = 1;
+// What the join costs in tiles: ranges are whole units where the longest is no longer than an
+// even share and this. At 0, 3, 6, 24, one token: 100 x 900 33.9, 31.4, 30.9, 30.9; 4 x 1000
+// 14.3, 14.4, 20.5, 20.5; 32 of 4096 each 44.4, 44.0, 43.9, 80.8.
+constexpr int JOIN_TILES_KV4 = 3;
+// Short sequences: up to KV4_SHORT_TILES tiles of the longest, a CTA takes a whole unit and no
+// join runs; up to twice that where the units fill half of the CTAs. At twice, whole and split:
+// 200 x 1000, one token 57.1 and 59.5; 16 x 1000, 8 tokens 22.6 and 26.6; but with 128 units,
+// 32 x 1000, one token 20.5 and 18.4, 8 x 1000, 8 tokens 20.5 and 18.5. At four times, with 800
+// units, 200 x 2000 87.9 and 82.4.
+constexpr int KV4_SHORT_TILES = 4;
+// Two neighbouring heads make one unit from this many heads of all sequences on (they share
+// lines of HBM, but are half as many units), with short sequences heads times row tiles. Two and
+// one: 32 x 8000, one token 44.6 and 46.9; 64 x 8000 76.8 and 105.2; 16 x 8000 30.8 and 28.7;
+// short, 8 tokens, 64 x 700 34.8 and 37.5; 32 x 1000 36.7 and 26.7.
+constexpr int KV4_PAIR_UNITS = 256;
+constexpr int KV4_PAIR_UNITS_SHORT = 1024;
+// The mma kernel (row tiles of 16, no start to speak of) up to 16 rows a KV head, and for more
+// rows in calls of so many of its tiles of 128 x 128 altogether; else the tcgen05 kernel (row
+// tiles of 128). The mma kernel's and the tcgen05 kernel's time with 4 KV heads, at 32, 48, 64,
+// 128 rows: 64 x 16000 168 155, 219 156, 274 158, 483 161; 64 x 4000 63.2 69.4, 75.8 69.6,
+// 90.9 71.7, 153 75.8; 8 x 4000 22.5 28.2, 24.6 28.6, 24.6 28.7, 35.1 28.7; one of 20000
+// 18.5 26.5, 20.5 26.6, 22.5 26.6, 28.8 28.3; short, 64 x 500 24.6 39.6, 24.6 41.0, 28.7 41.3,
+// 43.3 43.9; 64 x 1000 36.4 45.1, 38.0 47.0, 43.1 46.1, 64.8 49.4. d = 64: 64 x 4000 43.3 62.9,
+// 51.3 62.6, 61.0 64.2, 96.3 65.5. Many rows: 16 x 300 with 2 KV heads at 256, 512 rows
+// 18.0 20.5, 26.3 20.5.
 constexpr int KV4_SMALL_ROWS = 16;
+constexpr int KV4_MMA_ROWS = 256;
+constexpr int64_t KV4_MMA_TILES = 6144;
+constexpr int64_t KV4_MMA_TILES_SHORT = 12288;  // short sequences
+constexpr int64_t KV4_MMA_TILES_FEW = 32768;    // up to 32 rows
+
+int64_t kv4_max_tiles(const sv_attn_desc* d) {
+  return ((int64_t)d->max_seq_len + d->max_draft_len) / KV4_KT + 1;
+}
+
+// 1 = warp-level MMAs (attn_kv4.cu), 2 = tcgen05 (attn_kv4_tc.cu)
 int pick_kv4(const sv_attn_desc* d) {
   if (!attn_tc_available() || g_attn_kernel == 1) return 1;
-  return g_attn_kernel == 2 || kv4_rows_per_head(d) > KV4_SMALL_ROWS ? 2 : 1;
+  if (g_attn_kernel == 2) return 2;
+  const int64_t rows = kv4_rows_per_head(d), tiles = kv4_max_tiles(d);
+  const int64_t all = (int64_t)d->batch * d->num_kv_heads * ((rows + 15) / 16) * tiles * d->head_dim / 128;
+  const int64_t most = rows <= 2 * KV4_SMALL_ROWS        ? KV4_MMA_TILES_FEW
+                       : tiles <= 2 * KV4_SHORT_TILES ? KV4_MMA_TILES_SHORT
+                                                      : KV4_MMA_TILES;
+  return rows <= KV4_SMALL_ROWS || (rows <= KV4_MMA_ROWS && all <= most) ? 1 : 2;
 }
 
 // A call's units and ranges (line.cuh) on `sms` SMs with kernel `which`.
 void kv4_line(const sv_attn_desc* d, int which, int sms, Kv4Attn* p) {
-  const int64_t rows = kv4_rows_per_head(d);
+  const int64_t rows = kv4_rows_per_head(d), max_tiles = kv4_max_tiles(d);
   const int ctas = which == 2 ? sms : attn_kv4_ctas(sms);
-  const int64_t max_tiles = ((int64_t)d->max_seq_len + d->max_draft_len) / KV4_KT + 1;
   p->mr = which == 2 ? MT : attn_kv4_rows((int)rows);
   p->switch_tiles = which == 2 ? SWITCH_TILES_KV4 : SWITCH_TILES_KV4_MMA;
-  const int64_t per_head = (rows + p->mr - 1) / p->mr;  // row tiles
-  p->heads = d->num_kv_heads % 2 == 0 && (int64_t)d->batch * d->num_kv_heads >= KV4_PAIR_UNITS ? 2 : 1;
-  const int64_t units = (int64_t)d->batch * (d->num_kv_heads / p->heads) * per_head;
-  p->n_ctas = which == 2 ? ctas / p->heads : ctas;
-  p->join_tiles = which == 2 ? JOIN_TILES_KV4 : JOIN_TILES_KV4_MMA;
-  // Short sequences: a CTA for every unit, and no second launch.
-  p->no_join = which == 1 && max_tiles <= KV4_WHOLE_TILES && units <= 8 * (int64_t)ctas;
+  p->join_tiles = JOIN_TILES_KV4;
+  const int64_t row_tiles = (rows + p->mr - 1) / p->mr;
+  const int64_t heads = (int64_t)d->batch * d->num_kv_heads;
+  const bool shrt = which == 1 && max_tiles <= 2 * KV4_SHORT_TILES;
+  const bool pair = shrt ? heads * row_tiles >= KV4_PAIR_UNITS_SHORT : heads >= KV4_PAIR_UNITS;
+  p->heads = d->num_kv_heads % 2 == 0 && pair ? 2 : 1;
+  const int64_t units = heads / p->heads * row_tiles;
+  // (at most 8 units' time a CTA: with more the ranges of several units cost less)
+  p->no_join = shrt && units <= 8 * (int64_t)ctas &&
+               (max_tiles <= KV4_SHORT_TILES || 2 * units >= ctas);
   if (p->no_join) {
     p->n_ctas = (int)units;
-    p->join_tiles = KV4_WHOLE_TILES;  // (no unit is longer)
+    p->join_tiles = 2 * KV4_SHORT_TILES;  // (no unit is longer)
   } else {
-    p->n_ctas = (int)std::min<int64_t>(units * max_tiles, p->n_ctas);
+    p->n_ctas = (int)std::min<int64_t>(units * max_tiles, which == 2 ? ctas / p->heads : ctas);
   }
 }
 
@@ -864,7 +907,7 @@ SV_API sv_status spec_kv4_write(const sv_kv4_pages* pages, int32_t batch,
   if (st != SV_OK || batch == 0 || rows == 0) return st;
   const int64_t width = (int64_t)pages->num_kv_heads * pages->head_dim;
   for (const int64_t s : {k_row_stride, v_row_stride})
-    if (s < width || s % 8 != 0 || s > ((int64_t)1 << 40)) return SV_ERR_SHAPE;
+    if (s < width || s % 8 != 0 || s > ((int64_t)1 << 30)) return SV_ERR_SHAPE;
   if (!kv4_apart(pages, k, 2 * (size_t)((rows - 1) * k_row_stride + width)) ||
       !kv4_apart(pages, v, 2 * (size_t)((rows - 1) * v_row_stride + width)))
     return SV_ERR_SHAPE;

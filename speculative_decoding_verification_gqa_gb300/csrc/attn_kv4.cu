@@ -492,23 +492,25 @@ __global__ void __launch_bounds__(NTHREADS, SM_CTAS) attn_kv4_kernel(const Kv4At
 
 // ------------------------------------------------------------------------------ join
 
-constexpr int JT = 256;   // threads
+constexpr int JT = 256;  // threads
+constexpr int SPREAD_PARTS = 8;
 
 // The units that several CTAs share: their parts, in the CTAs' order, by the rule of the online
-// softmax. An item is `jrows` rows of one head of a unit. With few parts a warp takes a row; with
-// many all warps take every eighth part of the same row and add up through shared memory, and
-// an item is that row, so that one long sequence's hundreds of parts are not read one after
-// another. Items in contiguous ranges of the grid's CTAs, as the lines are walked.
-template <int HD>
-__global__ void __launch_bounds__(JT) kv4_join_kernel(const Kv4Attn p, int jrows) {
+// softmax. An item is JROWS rows of one head of a unit, a warp each; or (SPREAD), where units
+// have many parts, one row, of which each warp takes every eighth part, added up through shared
+// memory, so that a long sequence's hundred parts are not read one after another. Items in
+// contiguous ranges of the grid's CTAs, as the lines are walked.
+template <int HD, bool SPREAD>
+__global__ void __launch_bounds__(JT) kv4_join_kernel(const Kv4Attn p) {
+  constexpr int JROWS = SPREAD ? 1 : JT / 32;
   __shared__ float4 s_o[JT / 32][HD / 4];
   __shared__ float2 s_ml[JT / 32];
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // The lengths are read before the wait: the attention kernel's CTAs let this one start when
   // they have waited themselves, so whatever wrote the lengths is complete.
-  const int per = p.heads * ((p.mr + jrows - 1) / jrows);  // items of a unit
-  Line total;
+  const int per = p.heads * ((p.mr + JROWS - 1) / JROWS);  // items of a unit
+  Line total = {};
   LineAt at;
   int64_t it = 0, end = 0;
   const bool any = line_scan<JT>(p, total, &at, [&](bool& by_unit) -> int64_t {
@@ -538,9 +540,8 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const Kv4Attn p, int jrows
       continue;
     }
     const int rows = min(p.mr, p.G * (s.D + 1) - s.mt * p.mr);
-    const bool spread = c1 - c0 >= JT / 32;
     for (; it < next; ++it) {
-      const int i = (int)(it % per), h = i % p.heads, r0 = i / p.heads * jrows;
+      const int i = (int)(it % per), h = i % p.heads, r0 = i / p.heads * JROWS;
       const int gh = s.g * p.heads + h;
       // parts c0 + w, c0 + w + step, ... of row r
       auto gather = [&](int r, int w, int step, float4& acc, float& m, float& l) {
@@ -582,34 +583,32 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const Kv4Attn p, int jrows
       };
       float4 acc;
       float m, l;
-      if (!spread) {
+      if (!SPREAD) {
         const int r = r0 + warp;
-        if (warp < jrows && r < rows) {
+        if (r < rows) {
           gather(r, 0, 1, acc, m, l);
           if (lane < LN) store_row<HD>(p, out_row(r), gh, lane, acc, m, l);
         }
-      } else {
-        for (int r = r0; r < min(rows, r0 + jrows); ++r) {
-          gather(r, warp, JT / 32, acc, m, l);
-          if (lane < LN) s_o[warp][lane] = acc;
-          if (lane == 0) s_ml[warp] = make_float2(m, l);
-          __syncthreads();
-          if (warp == 0 && lane < LN) {
-            float M = -INFINITY, ls = 0.f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      } else if (r0 < rows) {
+        gather(r0, warp, JT / 32, acc, m, l);
+        if (lane < LN) s_o[warp][lane] = acc;
+        if (lane == 0) s_ml[warp] = make_float2(m, l);
+        __syncthreads();
+        if (warp == 0 && lane < LN) {
+          float M = -INFINITY, ls = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < JT / 32; ++w) M = fmaxf(M, s_ml[w].x);
+          for (int w = 0; w < JT / 32; ++w) M = fmaxf(M, s_ml[w].x);
 #pragma unroll
-            for (int w = 0; w < JT / 32; ++w) {
-              const float f = s_ml[w].x == -INFINITY ? 1.f : ex2(s_ml[w].x - M);
-              const float4 v = s_o[w][lane];
-              ls += s_ml[w].y * f;
-              o = make_float4(o.x + v.x * f, o.y + v.y * f, o.z + v.z * f, o.w + v.w * f);
-            }
-            store_row<HD>(p, out_row(r), gh, lane, o, M, ls);
+          for (int w = 0; w < JT / 32; ++w) {
+            const float f = s_ml[w].x == -INFINITY ? 1.f : ex2(s_ml[w].x - M);
+            const float4 v = s_o[w][lane];
+            ls += s_ml[w].y * f;
+            o = make_float4(o.x + v.x * f, o.y + v.y * f, o.z + v.z * f, o.w + v.w * f);
           }
-          __syncthreads();
+          store_row<HD>(p, out_row(r0), gh, lane, o, M, ls);
         }
+        __syncthreads();
       }
     }
   }
@@ -625,9 +624,7 @@ cudaError_t launch_nt(const Kv4Attn& p, cudaStream_t s) {
 }
 template <int HD, int NT>
 cudaError_t launch_nt(const Kv4Attn& p, cudaStream_t s) {
-  return p.heads == 4 ? launch_nt<HD, NT, 4>(p, s)
-         : p.heads == 2 ? launch_nt<HD, NT, 2>(p, s)
-                        : launch_nt<HD, NT, 1>(p, s);
+  return p.heads == 2 ? launch_nt<HD, NT, 2>(p, s) : launch_nt<HD, NT, 1>(p, s);
 }
 
 }  // namespace
@@ -644,12 +641,13 @@ cudaError_t launch_attn_kv4(const Kv4Attn& p, cudaStream_t s) {
 cudaError_t launch_kv4_join(const Kv4Attn& p, int sms, cudaStream_t s) {
   const int64_t rows = (int64_t)p.G * (1 + p.max_draft);
   const int64_t units = (int64_t)p.B * (p.Hkv / p.heads) * ((rows + p.mr - 1) / p.mr);
-  // rows of an item: one where a unit has many parts
-  const int jrows = p.n_ctas >= JT / 32 * units ? 1 : JT / 32;
+  const bool spread = p.n_ctas >= SPREAD_PARTS * units;
+  const int jrows = spread ? 1 : JT / 32;
   const int64_t items = units * p.heads * ((p.mr + jrows - 1) / jrows);
   const dim3 grid((unsigned)std::min<int64_t>(items, 4 * (int64_t)sms));
-  return p.d == 128 ? launch_pdl(kv4_join_kernel<128>, grid, dim3(JT), 0, s, p, jrows)
-                    : launch_pdl(kv4_join_kernel<64>, grid, dim3(JT), 0, s, p, jrows);
+  auto kernel = p.d == 128 ? (spread ? kv4_join_kernel<128, true> : kv4_join_kernel<128, false>)
+                           : (spread ? kv4_join_kernel<64, true> : kv4_join_kernel<64, false>);
+  return launch_pdl(kernel, grid, dim3(JT), 0, s, p);
 }
 
 }  // namespace sv

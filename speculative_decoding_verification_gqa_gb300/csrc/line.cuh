@@ -237,7 +237,7 @@ __device__ __forceinline__ LineWalk line_enter(const Kv4Attn& p, const LineAt& a
 // length is out of range. By all NTH threads of the CTA.
 template <int NTH>
 __device__ bool line_begin(const Kv4Attn& p, int c, LineWalk& w) {
-  Line total;
+  Line total = {};
   LineAt at;
   int64_t v0 = 0, v1 = 0;
   if (!line_scan<NTH>(p, total, &at, [&](bool& by_unit) -> int64_t {
