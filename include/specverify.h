@@ -389,8 +389,8 @@ SV_API size_t spec_kv4_workspace_size(int32_t batch);
  *   start, count int32 [batch], >= 0
  *   rows         rows allocated in k and v, >= the sum of count; rows past the sum are not read
  *   k, v         bf16, row r's [Hkv, head_dim] at element r * k_row_stride (v_row_stride), a
- *                multiple of 8 and at least Hkv * head_dim (a slice of a fused projection);
- *                16-byte aligned
+ *                multiple of 8, at least Hkv * head_dim (a slice of a fused projection) and at
+ *                most 2^30; 16-byte aligned
  * A start or count out of range is reported by sv_workspace_status (SV_ERR_DEVICE_SHAPE) and
  * nothing is written; a row whose table entry names no page of the pool is reported and
  * skipped. No two rows of a call may go to the same position of a page.

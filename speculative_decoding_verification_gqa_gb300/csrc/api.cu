@@ -817,7 +817,9 @@ constexpr int KV4_SHORT_TILES = 4;
 // Two neighbouring heads make one unit from this many heads of all sequences on (they share
 // lines of HBM, but are half as many units), with short sequences heads times row tiles. Two and
 // one: 32 x 8000, one token 44.6 and 46.9; 64 x 8000 76.8 and 105.2; 16 x 8000 30.8 and 28.7;
-// short, 8 tokens, 64 x 700 34.8 and 37.5; 32 x 1000 36.7 and 26.7.
+// short, 8 tokens, 64 x 700 34.8 and 37.5; 32 x 1000 36.7 and 26.7. The tcgen05 kernel's pairs
+// are two CTAs side by side, which costs it no units: always. 32 tokens, 8 x 32768 each 147.2 and
+// 153.8; 32 x 4000 each 110.4 and 114.0; 8 x 2000 each 37.8 and 37.4; one of 20000 30.8 and 30.8.
 constexpr int KV4_PAIR_UNITS = 256;
 constexpr int KV4_PAIR_UNITS_SHORT = 1024;
 // The mma kernel (row tiles of 16, no start to speak of) up to 16 rows a KV head, and for more
@@ -861,7 +863,9 @@ void kv4_line(const sv_attn_desc* d, int which, int sms, Kv4Attn* p) {
   const int64_t row_tiles = (rows + p->mr - 1) / p->mr;
   const int64_t heads = (int64_t)d->batch * d->num_kv_heads;
   const bool shrt = which == 1 && max_tiles <= 2 * KV4_SHORT_TILES;
-  const bool pair = shrt ? heads * row_tiles >= KV4_PAIR_UNITS_SHORT : heads >= KV4_PAIR_UNITS;
+  const bool pair = which == 2 ? true
+                    : shrt     ? heads * row_tiles >= KV4_PAIR_UNITS_SHORT
+                               : heads >= KV4_PAIR_UNITS;
   p->heads = d->num_kv_heads % 2 == 0 && pair ? 2 : 1;
   const int64_t units = heads / p->heads * row_tiles;
   // (at most 8 units' time a CTA: with more the ranges of several units cost less)
@@ -1071,7 +1075,10 @@ SV_API sv_status spec_kv_evict(const sv_page_table* table, int32_t n, const int3
   if (st == SV_OK) st = check_pools(table, num_pools, pools);
   if (st != SV_OK) return st;
   const size_t need = spec_kv_evict_workspace_size(n, num_kv_heads, mass_stride);
-  if (need == 0 || keep_last < 0 || (kept && kept_stride < 0)) return SV_ERR_SHAPE;
+  if (need == 0 || keep_last < 0 || (kept && (kept_stride < 0 || kept_stride > MAX_KV_ROWS / 2)))
+    return SV_ERR_SHAPE;
+  // (the sizes below stay within 63 bits)
+  if ((int64_t)table->table_rows * num_kv_heads > ((int64_t)1 << 60) / mass_stride) return SV_ERR_SHAPE;
   int64_t slices = 1;
   for (int k = 0; k < num_pools; ++k) {
     const int64_t pos = pools[k].page_bytes / table->block_size;

@@ -318,6 +318,23 @@ def test_larger_batches(kernel, T, D, Hq, Hkv, d, bs):
     check_attn(T, D, Hq, Hkv, d, bs, seed=T[0])
 
 
+@pytest.mark.parametrize("T,D,Hq,Hkv,d,bs", [
+    ([b % 37 for b in range(599)] + [1900], [0] * 600, 4, 2, 64, 8),  # more sequences than threads, one split
+    ([b % 37 for b in range(600)], [b % 3 for b in range(600)], 4, 2, 64, 8),    # short: pairs of heads
+    ([9 * b for b in range(130)] + [1500], [2] * 131, 16, 4, 128, 32),           # long: pairs of heads
+    ([2000 + 8 * b for b in range(8)], [0] * 8, 16, 8, 64, 16),   # seven parts a unit: a warp joins a row
+    ([30, 1000, 16, 2000], [3, 2, 3, 1], 9, 3, 128, 16),          # heads that do not pair
+    ([1023, 600, 1000], [0, 0, 0], 16, 2, 128, 16),               # at the longest of the short
+])
+def test_batches_of_every_layout(kernel, T, D, Hq, Hkv, d, bs):
+    check_attn(T, D, Hq, Hkv, d, bs, seed=len(T))
+
+
+@pytest.mark.parametrize("B,T,G,D", [(1, 300, 8, 15), (70, 2000, 8, 3), (70, 2000, 8, 4), (3, 900, 16, 15)])
+def test_the_kernel_the_rules_choose(B, T, G, D):
+    check_attn([T - 7 * b for b in range(B)], [D] * B, 2 * G, 2, 64, 16)
+
+
 @pytest.mark.parametrize("window", [1, 5, 32, 100, 129, 1000, 100000])
 @pytest.mark.parametrize("D", [0, 3, 17])
 def test_sliding_windows(kernel, window, D):
@@ -482,6 +499,31 @@ def test_same_bits_again_captured_and_on_another_stream(kernel, T, D, Hq):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(o3, out) and torch.equal(l3, lse)
+
+
+def test_two_graphs_on_one_workspace(kernel):
+    """Replayed one after another, in either order and often."""
+    jobs, ws = [], sv.new_workspace(sv.verify_kv4_workspace_bytes(
+        sv.paged_attn_desc(make_q(40, 8, 128, 0), torch.empty(999, 16, 2, 64, dtype=torch.uint8, device=DEV), 3, 15,
+                           4000, kv4=True)))
+    for k, (T, D) in enumerate((([3000, 40, 7], [2, 0, 3]), ([900, 1700], [15, 3]))):
+        c = Cache("kv4", [t + 1 + n for t, n in zip(T, D)], 2, 128, 16, 30 + k)
+        q = make_q(sum(D) + len(D), 8, 128, k)
+        want = run_attn(c, q, T, D)[0]
+        out, Ti, Di = torch.zeros_like(q), i32(T), i32(D)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            sv.spec_verify_attn_kv4(q, c.k, c.v, c.scales, c.hs, c.table, Ti, Di, max_draft_len=max(D),
+                                    max_seq_len=max(T), out=out, workspace=ws)
+        jobs.append((g, out, want, c, q, Ti, Di))
+    for order in ([0, 1, 0, 0, 1, 1], [1, 0]):
+        for _, out, *_ in jobs:
+            out.zero_()
+        for k in order:
+            jobs[k][0].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(j[1], j[2]) for j in jobs)
 
 
 def test_two_calls_in_flight(kernel):

@@ -83,6 +83,25 @@ def test_many_sequences(kind):
 
 
 @pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("kind", ["e4m3", "kv4"])
+def test_more_sequences_than_threads(kind, given):
+    T = [(7 * b) % 41 for b in range(800)] + [1500]
+    D = [b % 2 for b in range(801)]
+    check_mass(kind, T, D, 4, 2, 64, 16, [b % (2 + k) if b % 5 else 0 for b, k in enumerate(D)], given)
+
+
+def test_no_row_counted():
+    """Nothing is added, whatever the log-sums hold, by either form of the call."""
+    T, D = [100, 3], [3, 0]
+    c = Cache("kv4", [104, 4], 2, 64, 16, 3)
+    q, mass = make_q(5, 4, 64, 1), torch.rand(2, 2, 104, device=DEV)
+    was = mass.clone()
+    mass_call(c, q, T, D, mass, n=[0, 0])
+    mass_call(c, q, T, D, mass, n=[0, 0], lse=torch.full((5, 4), float("nan"), device=DEV))
+    assert torch.equal(mass, was)
+
+
+@pytest.mark.parametrize("given", [False, True])
 def test_sharp_weights(given):
     """A scale at which all weight goes to a few keys."""
     check_mass("bf16", [600], [3], 8, 2, 128, 16, None, given, scale=2.0)
