@@ -740,9 +740,9 @@ SV_API void sv_set_profile_events(void* start_event, void* stop_event);
  * returns SV_ERR_CUDA (spec_verify_attn and the paged call launch three kernels in this
  * order: plan, attention, combine; the host-lengths call attention and combine; the
  * shared-prefix call plan, sequences, prefixes, combine, or with the mma.sync kernel plan,
- * attention, combine; the 4-bit call attention, join, or for short sequences attention alone; spec_accept, spec_draft_signals,
- * spec_pages_fork and _trim, spec_kv4_write and _read one each; spec_pages_extend and
- * spec_kv_evict two; spec_attn_mass one, two without lse; spec_pages_compact two, three beyond
+ * attention, combine; the 4-bit call attention, join, or for short sequences attention
+ * alone; spec_accept, spec_draft_signals, spec_pages_fork and _trim, spec_kv4_write and _read
+ * one each; spec_pages_extend and spec_kv_evict two; spec_attn_mass one, two without lse; spec_pages_compact two, three beyond
  * 4096 pages). The call's earlier launches have run;
  * its outputs are then unspecified, and its workspace serves the next call as it is. One
  * failure per arming; after < 0 disarms. Returns the launches that were still to go

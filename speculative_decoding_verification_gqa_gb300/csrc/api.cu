@@ -1008,6 +1008,10 @@ SV_API sv_status spec_verify_attn_kv4(const sv_attn_desc* desc, const void* q,
   p.q_rows = desc->q_rows;
   p.scale_log2 = scale_log2_of(desc);
   kv4_line(desc, which, sms, &p);
+  if (which == 2) {  // a pending wait-timeout injection applies to this launch
+    p.wait_limit = g_stall_limit.exchange(0);
+    p.stall_first_tile = p.wait_limit > 0;
+  }
   cudaStream_t s = (cudaStream_t)stream;
   if (g_ev_start && cudaEventRecord(g_ev_start, s) != cudaSuccess) return SV_ERR_CUDA;
   if ((which == 2 ? launch_attn_kv4_tc(p, s) : launch_attn_kv4(p, s)) != cudaSuccess)

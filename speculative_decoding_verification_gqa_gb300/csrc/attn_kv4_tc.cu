@@ -255,9 +255,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           ok = false;
           break;
         }
-        if (lane == 0) mbar_expect_tx(&bars->raw_full[st], 2 * L::RAW);
+        const bool withheld = it == 0 && p.stall_first_tile;
+        if (lane == 0 && !withheld) mbar_expect_tx(&bars->raw_full[st], 2 * L::RAW);
         __syncwarp();
-        if (lane < nbox) {
+        if (lane < nbox && !withheld) {
           const uint32_t dst = saddr(smem + L::RK + st * 2 * L::RAW) + lane * box * L::RB;
           tma_load_3d(dst, &tmk, &bars->raw_full[st], 0, g, row);
           tma_load_3d(dst + L::RAW, &tmv, &bars->raw_full[st], 0, g, row);
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       }
     }
     if (lane == 0) {  // leave no copy in flight (bounded)
-      for (uint32_t st = 0; st < NR && st < it; ++st) {
+      for (uint32_t st = p.stall_first_tile && it <= NR ? 1 : 0; st < NR && st < it; ++st) {
         const uint32_t par = ((it - 1 - st) / NR) & 1;
         const long long t0 = clock64();
         while (!mbar_try(&bars->raw_full[st], par) && clock64() - t0 < TIMEOUT_CYCLES) {

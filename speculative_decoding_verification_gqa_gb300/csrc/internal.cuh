@@ -406,7 +406,8 @@ struct Kv4Attn {
   int switch_tiles;            // a unit's start in tiles' time
   int join_tiles;              // the join's time in tiles' time
   bool no_join;                // whatever the lengths, a CTA takes a whole unit
-  long long wait_limit;
+  long long wait_limit;        // tcgen05 kernel, as in AttnParams
+  int stall_first_tile;
 };
 constexpr int KV4_KT = 128;    // keys per tile of the line
 int attn_kv4_ctas(int sms);

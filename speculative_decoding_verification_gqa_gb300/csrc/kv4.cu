@@ -369,7 +369,7 @@ cudaError_t launch_kv4_write(const sv_kv4_pages& p, int B, const int32_t* table,
   a.v = (const uint16_t*)v;
   a.k_stride = k_stride;
   a.v_stride = v_stride;
-    return launch_rows(kv4_write_kernel<1>, kv4_write_kernel<2>, 8, a, sms, s);
+  return launch_rows(kv4_write_kernel<1>, kv4_write_kernel<2>, 8, a, sms, s);
 }
 
 cudaError_t launch_kv4_read(const sv_kv4_pages& p, int B, const int32_t* table, int max_blocks,

@@ -560,6 +560,33 @@ def test_launch_failures_leave_the_workspace_usable(kernel):
     assert api.inject_launch_failure(-1) == -1
 
 
+@pytest.mark.parametrize("T,D", [([900, 5, 300], [7, 0, 3]), ([40], [1])])
+def test_a_wait_that_runs_out_is_reported(T, D):
+    """With a short limit and every CTA's first tile withheld the waits for it run out: the
+    kernel returns well before the default limit of about 2 s, the workspace says so, and the
+    next call is right."""
+    import time
+    prev = sv.set_attn_kernel(2)
+    try:
+        c = Cache("kv4", [t + 1 + n for t, n in zip(T, D)], 2, 128, 16, 2)
+        q = make_q(sum(D) + len(D), 8, 128, 3)
+        out, lse, ws = run_attn(c, q, T, D)
+        torch.cuda.synchronize()
+        assert api.inject_wait_timeout(100000) == 0
+        t0 = time.perf_counter()
+        run_attn(c, q, T, D, workspace=ws)
+        torch.cuda.synchronize()
+        assert time.perf_counter() - t0 < 0.5
+        assert sv.workspace_status(ws, clear=True) == 7  # SV_ERR_TIMEOUT
+        assert api.inject_wait_timeout(0) == 0           # used once
+        again = run_attn(c, q, T, D, workspace=ws)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+        assert sv.workspace_status(ws) == 0
+    finally:
+        api.inject_wait_timeout(0)
+        sv.set_attn_kernel(prev)
+
+
 def test_one_workspace_serves_both_kernels():
     """Calls of few rows and of many, and either kernel, one after another on one workspace."""
     jobs = [([700, 30], [0, 0]), ([600, 500], [15, 7]), ([40, 2], [1, 0])]
