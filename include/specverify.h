@@ -742,15 +742,15 @@ SV_API void sv_set_profile_events(void* start_event, void* stop_event);
  * shared-prefix call plan, sequences, prefixes, combine, or with the mma.sync kernel plan,
  * attention, combine; the 4-bit call attention, join, or for short sequences attention
  * alone; spec_accept, spec_draft_signals, spec_pages_fork and _trim, spec_kv4_write and _read
- * one each; spec_pages_extend and spec_kv_evict two; spec_attn_mass one, two without lse; spec_pages_compact two, three beyond
- * 4096 pages). The call's earlier launches have run;
- * its outputs are then unspecified, and its workspace serves the next call as it is. One
+ * one each; spec_pages_extend and spec_kv_evict two; spec_attn_mass one, two without lse;
+ * spec_pages_compact two, three beyond 4096 pages). The call's earlier launches have run; its
+ * outputs are then unspecified, and its workspace serves the next call as it is. One
  * failure per arming; after < 0 disarms. Returns the launches that were still to go
  * before a pending failure, or -1 if none was pending. Process-wide. */
 SV_API int sv_inject_launch_failure(int after);
 
 /* Fault injection for tests, on the device side of the tcgen05 attention kernel's bounded
- * waits: the next verify-attention launch of that kernel gives every barrier wait
+ * waits: the next verify-attention launch of that kernel (or of the 4-bit call's) gives every barrier wait
  * `limit_cycles` clock cycles instead of about 2 s, and each of its CTAs withholds the K
  * and V loads of the first tile of its range, so the waits for that tile run out. The kernel
  * then sets SV_ERR_TIMEOUT in the workspace (read it with sv_workspace_status); every role
