@@ -805,9 +805,12 @@ int64_t kv4_rows_per_head(const sv_attn_desc* d) {
 constexpr int SWITCH_TILES_KV4 = 6;
 constexpr int SWITCH_TILES_KV4_MMA = 1;
 // What the join costs in tiles: ranges are whole units where the longest is no longer than an
-// even share and this. At 0, 3, 6, 24, one token: 100 x 900 33.9, 31.4, 30.9, 30.9; 4 x 1000
-// 14.3, 14.4, 20.5, 20.5; 32 of 4096 each 44.4, 44.0, 43.9, 80.8.
-constexpr int JOIN_TILES_KV4 = 3;
+// even share and this. The tcgen05 kernel, 32 tokens, at 0, 3, 8, 16: 16 x 8192 each 94.4, 94.5,
+// 90.4, 90.4; 12 x 2000 each 40.0, 33.9, 34.0, 33.9; 8 x 4000 each 39.0, 39.0, 39.0, 49.2. The mma
+// kernel, one token, at 0, 3, 6, 24: 100 x 900 33.9, 31.4, 30.9, 30.9; 4 x 1000 14.3, 14.4, 20.5,
+// 20.5; 32 of 4096 each 44.4, 44.0, 43.9, 80.8.
+constexpr int JOIN_TILES_KV4 = 8;
+constexpr int JOIN_TILES_KV4_MMA = 3;
 // Short sequences: up to KV4_SHORT_TILES tiles of the longest, a CTA takes a whole unit and no
 // join runs; up to twice that where the units fill half of the CTAs. At twice, whole and split:
 // 200 x 1000, one token 57.1 and 59.5; 16 x 1000, 8 tokens 22.6 and 26.6; but with 128 units,
@@ -859,7 +862,7 @@ void kv4_line(const sv_attn_desc* d, int which, int sms, Kv4Attn* p) {
   const int ctas = which == 2 ? sms : attn_kv4_ctas(sms);
   p->mr = which == 2 ? MT : attn_kv4_rows((int)rows);
   p->switch_tiles = which == 2 ? SWITCH_TILES_KV4 : SWITCH_TILES_KV4_MMA;
-  p->join_tiles = JOIN_TILES_KV4;
+  p->join_tiles = which == 2 ? JOIN_TILES_KV4 : JOIN_TILES_KV4_MMA;
   const int64_t row_tiles = (rows + p->mr - 1) / p->mr;
   const int64_t heads = (int64_t)d->batch * d->num_kv_heads;
   const bool shrt = which == 1 && max_tiles <= 2 * KV4_SHORT_TILES;

@@ -496,13 +496,14 @@ constexpr int JT = 256;  // threads
 constexpr int SPREAD_PARTS = 8;
 
 // The units that several CTAs share: their parts, in the CTAs' order, by the rule of the online
-// softmax. An item is JROWS rows of one head of a unit, a warp each; or (SPREAD), where units
-// have many parts, one row, of which each warp takes every eighth part, added up through shared
-// memory, so that a long sequence's hundred parts are not read one after another. Items in
-// contiguous ranges of the grid's CTAs, as the lines are walked.
-template <int HD, bool SPREAD>
+// softmax. An item is JROWS rows of one head of a unit, RW for each warp, whose parts are asked
+// for together; or (RW = 0), where units have many parts, one row, of which each warp takes every
+// eighth part, added up through shared memory, so that a long sequence's hundred parts are not
+// read one after another. Items in contiguous ranges of the grid's CTAs, as the lines are walked.
+template <int HD, int RWS>
 __global__ void __launch_bounds__(JT) kv4_join_kernel(const Kv4Attn p) {
-  constexpr int JROWS = SPREAD ? 1 : JT / 32;
+  constexpr bool SPREAD = RWS == 0;
+  constexpr int RW = SPREAD ? 1 : RWS, JROWS = SPREAD ? 1 : RW * (JT / 32);
   __shared__ float4 s_o[JT / 32][HD / 4];
   __shared__ float2 s_ml[JT / 32];
   pdl_trigger();
@@ -543,37 +544,50 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const Kv4Attn p) {
     for (; it < next; ++it) {
       const int i = (int)(it % per), h = i % p.heads, r0 = i / p.heads * JROWS;
       const int gh = s.g * p.heads + h;
-      // parts c0 + w, c0 + w + step, ... of row r
-      auto gather = [&](int r, int w, int step, float4& acc, float& m, float& l) {
-        constexpr int U = 8;
-        acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        m = -INFINITY;
-        l = 0.f;
+      // parts c0 + w, c0 + w + step, ... of rows r, r + JT / 32, ...
+      float4 acc[RW];
+      float m[RW], l[RW];
+      auto gather = [&](int r, int w, int step) {
+        constexpr int U = 8 / RW;
+#pragma unroll
+        for (int e = 0; e < RW; ++e) {
+          acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+          m[e] = -INFINITY;
+          l[e] = 0.f;
+        }
         for (int c = c0 + w; c <= c1; c += U * step) {
-          float2 ml[U];
-          float4 v[U];
+          float2 ml[RW][U];
+          float4 v[RW][U];
 #pragma unroll
-          for (int k = 0; k < U; ++k) {
-            const int cc = c + k * step;
-            const size_t at2 = ((size_t)(2 * cc + (cc == c0)) * p.heads + h) * p.mr + r;
-            ml[k] = cc <= c1 ? __ldcg(p.part_ml + at2) : make_float2(-INFINITY, 0.f);
-            v[k] = cc <= c1 && lane < LN ? __ldcg(reinterpret_cast<const float4*>(p.part_o + at2 * HD) + lane)
-                                         : make_float4(0.f, 0.f, 0.f, 0.f);
-          }
-          float mn = m;
+          for (int e = 0; e < RW; ++e)
 #pragma unroll
-          for (int k = 0; k < U; ++k) mn = fmaxf(mn, ml[k].x);
-          const float mu = mn == -INFINITY ? 0.f : mn;
-          const float f0 = ex2(m - mu);
-          m = mn;
-          l *= f0;
-          acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+            for (int k = 0; k < U; ++k) {
+              const int cc = c + k * step, rr = r + e * (JT / 32);
+              const bool have = cc <= c1 && rr < rows;
+              const size_t at2 = ((size_t)(2 * cc + (cc == c0)) * p.heads + h) * p.mr + rr;
+              ml[e][k] = have ? __ldcg(p.part_ml + at2) : make_float2(-INFINITY, 0.f);
+              v[e][k] = have && lane < LN ? __ldcg(reinterpret_cast<const float4*>(p.part_o + at2 * HD) + lane)
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
 #pragma unroll
-          for (int k = 0; k < U; ++k) {
-            // (a part without a reference: O = 0 and l = 0, or NaN, which stays)
-            const float f = ml[k].x == -INFINITY ? 1.f : ex2(ml[k].x - mu);
-            l += ml[k].y * f;
-            acc = make_float4(acc.x + v[k].x * f, acc.y + v[k].y * f, acc.z + v[k].z * f, acc.w + v[k].w * f);
+          for (int e = 0; e < RW; ++e) {
+            float mn = m[e];
+#pragma unroll
+            for (int k = 0; k < U; ++k) mn = fmaxf(mn, ml[e][k].x);
+            const float mu = mn == -INFINITY ? 0.f : mn;
+            const float f0 = ex2(m[e] - mu);
+            float4 o = acc[e];
+            m[e] = mn;
+            l[e] *= f0;
+            o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+              // (a part without a reference: O = 0 and l = 0, or NaN, which stays)
+              const float f = ml[e][k].x == -INFINITY ? 1.f : ex2(ml[e][k].x - mu);
+              l[e] += ml[e][k].y * f;
+              o = make_float4(o.x + v[e][k].x * f, o.y + v[e][k].y * f, o.z + v[e][k].z * f, o.w + v[e][k].w * f);
+            }
+            acc[e] = o;
           }
         }
       };
@@ -581,18 +595,17 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const Kv4Attn p) {
         const int rg = s.mt * p.mr + r;
         return (s.q_off + rg / p.G) * p.Hq + (int64_t)gh * p.G + rg % p.G;
       };
-      float4 acc;
-      float m, l;
       if (!SPREAD) {
-        const int r = r0 + warp;
-        if (r < rows) {
-          gather(r, 0, 1, acc, m, l);
-          if (lane < LN) store_row<HD>(p, out_row(r), gh, lane, acc, m, l);
+        gather(r0 + warp, 0, 1);
+#pragma unroll
+        for (int e = 0; e < RW; ++e) {
+          const int r = r0 + warp + e * (JT / 32);
+          if (r < rows && lane < LN) store_row<HD>(p, out_row(r), gh, lane, acc[e], m[e], l[e]);
         }
       } else if (r0 < rows) {
-        gather(r0, warp, JT / 32, acc, m, l);
-        if (lane < LN) s_o[warp][lane] = acc;
-        if (lane == 0) s_ml[warp] = make_float2(m, l);
+        gather(r0, warp, JT / 32);
+        if (lane < LN) s_o[warp][lane] = acc[0];
+        if (lane == 0) s_ml[warp] = make_float2(m[0], l[0]);
         __syncthreads();
         if (warp == 0 && lane < LN) {
           float M = -INFINITY, ls = 0.f;
@@ -641,12 +654,17 @@ cudaError_t launch_attn_kv4(const Kv4Attn& p, cudaStream_t s) {
 cudaError_t launch_kv4_join(const Kv4Attn& p, int sms, cudaStream_t s) {
   const int64_t rows = (int64_t)p.G * (1 + p.max_draft);
   const int64_t units = (int64_t)p.B * (p.Hkv / p.heads) * ((rows + p.mr - 1) / p.mr);
-  const bool spread = p.n_ctas >= SPREAD_PARTS * units;
-  const int jrows = spread ? 1 : JT / 32;
+  // (4 rows a warp where a unit has 128)
+  const int rw = p.n_ctas >= SPREAD_PARTS * units ? 0 : p.mr > 16 ? 4 : 1;
+  const int jrows = rw ? rw * (JT / 32) : 1;
   const int64_t items = units * p.heads * ((p.mr + jrows - 1) / jrows);
   const dim3 grid((unsigned)std::min<int64_t>(items, 4 * (int64_t)sms));
-  auto kernel = p.d == 128 ? (spread ? kv4_join_kernel<128, true> : kv4_join_kernel<128, false>)
-                           : (spread ? kv4_join_kernel<64, true> : kv4_join_kernel<64, false>);
+  auto kernel = p.d == 128 ? (rw == 0   ? kv4_join_kernel<128, 0>
+                              : rw == 1 ? kv4_join_kernel<128, 1>
+                                        : kv4_join_kernel<128, 4>)
+                           : (rw == 0   ? kv4_join_kernel<64, 0>
+                              : rw == 1 ? kv4_join_kernel<64, 1>
+                                        : kv4_join_kernel<64, 4>);
   return launch_pdl(kernel, grid, dim3(JT), 0, s, p);
 }
 
