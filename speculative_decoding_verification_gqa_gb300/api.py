@@ -719,11 +719,14 @@ def _row_stride(t, name, hkv, d, rows):
         raise TypeError("%s must be a CUDA tensor" % name)
     if t.dtype != torch.bfloat16:
         raise TypeError("%s has dtype %s, expected torch.bfloat16" % (name, t.dtype))
-    if t.dim() != 3 or t.shape[1:] != (hkv, d) or (rows is not None and t.shape[0] != rows):
+    shape = t.shape
+    if len(shape) != 3 or shape != (shape[0] if rows is None else rows, hkv, d):
         raise ValueError("k and v must be [rows, Hkv, d] of the pages' heads")
+    if t.is_contiguous():
+        return hkv * d
     if (d > 1 and t.stride(2) != 1) or (hkv > 1 and t.stride(1) != d):
         raise ValueError("%s: a row's heads must be contiguous (rows may be apart)" % name)
-    if t.shape[0] <= 1:
+    if shape[0] <= 1:
         return hkv * d
     if t.stride(0) < hkv * d:
         raise ValueError("%s: rows must not overlap" % name)
