@@ -534,6 +534,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) mass_kernel(const MassArgs a) {
 #pragma unroll
                   for (int e = 0; e < 4; ++e)
                     x[e] = ex2(fmaf(s[w][h][e], e & 1 ? rr.z : rr.x, e & 1 ? -rr.w : -rr.y));
+                  if (edge) {  // (a row without numbers has NaN for the keys that it does not see too)
+                    const int2 ii = *reinterpret_cast<const int2*>(s_i + (q + w) * 8 + 2 * t4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                      if (key0 + h * 16 + (e >> 1) * 8 + r8 > T + (e & 1 ? ii.y : ii.x)) x[e] = 0.f;
+                  }
                   acc[h][0] += x[0] + x[1];
                   acc[h][1] += x[2] + x[3];
                 }

@@ -90,6 +90,54 @@ def test_more_sequences_than_threads(kind, given):
     check_mass(kind, T, D, 4, 2, 64, 16, [b % (2 + k) if b % 5 else 0 for b, k in enumerate(D)], given)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "kv4"])
+def test_scores_that_rise(kind):
+    """Scores that grow along the keys by some hundred binary digits in steps: a row's first
+    maximum lies far below its last."""
+    T, D, Hq, Hkv, d = [2000, 300], [3, 0], 8, 2, 64
+    c = Cache(kind, [t + 1 + k for t, k in zip(T, D)], Hkv, d, 16, 9)
+    q = make_q(5, Hq, d, 4).abs()
+    for b, t in enumerate(T):
+        n = t + 1 + D[b]
+        at = c.rows(b, n).to(DEV)
+        if kind == "bf16":
+            k = c.k.view(-1, Hkv, d)
+            k[at] = ((torch.arange(n, device=DEV) // 100)[:, None, None] * 2.0).expand(n, Hkv, d).to(torch.bfloat16)
+        else:
+            c.k.view(-1, Hkv, d // 2)[at] = 0x22  # ones
+            s = c.scales.view(-1, Hkv, 2, d // 16)
+            s[at, :, 0] = (8 + 4 * (torch.arange(n, device=DEV) // 100))[:, None, None].to(torch.uint8)
+    if kind == "kv4":
+        c.hs[0] = 40.0
+    before = torch.zeros(2, Hkv, 2010, device=DEV)
+    got = mass_call(c, q, T, D, before.clone())
+    off = 0
+    for b, (t, k) in enumerate(zip(T, D)):
+        P, L, _, size, _ = attention(q[off:off + 1 + k], c.dense(b, t + 1 + k, 0), None, t, k, Hq // Hkv, d ** -0.5)
+        off += 1 + k
+        add = P.sum((1, 2))
+        tol = add * (2.5 * float(size.max()) * 2 ** -17 + 2 ** -15 + float(L.abs().max()) * 2 ** -22) + 1e-30
+        assert b == 1 or float(L.max()) > 139  # 2 x 100 binary digits above the first scores
+        assert ((got[b, :, :t + 1 + k].double() - add).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "kv4"])
+@pytest.mark.parametrize("given", [False, True])
+def test_a_row_without_numbers_reaches_its_own_keys_only(kind, given):
+    """An infinity in the second row of a window: NaN for the keys that it sees, the others'
+    weights after them."""
+    T, D = [140], [3]
+    c = Cache(kind, [144], 1, 64, 16, 3)
+    q = make_q(4, 2, 64, 1)
+    _, L, _, _, _ = attention(q, c.dense(0, 144, 0), None, 140, 3, 2, 64 ** -0.5)
+    lse = L.float()
+    q[1, 0, 5] = float("inf")
+    lse[1, 0] = float("nan")
+    got = mass_call(c, q, T, D, torch.zeros(1, 1, 144, device=DEV), lse=lse if given else None)[0, 0]
+    assert torch.isnan(got[:142]).all()
+    assert torch.isfinite(got[142:]).all() and (got[142:] > 0).all()
+
+
 def test_no_row_counted():
     """Nothing is added, whatever the log-sums hold, by either form of the call."""
     T, D = [100, 3], [3, 0]
