@@ -26,6 +26,7 @@ import contextlib
 import ctypes
 import math
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -168,20 +169,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.spec_pages_trim.restype = ctypes.c_int
         lib.spec_pages_compact.argtypes = [pt, i32, vp, vp, vp, vp, sz, vp]
         lib.spec_pages_compact.restype = ctypes.c_int
-        k4, ad = ctypes.POINTER(Kv4Pages), ctypes.POINTER(AttnDesc)
+        ad = ctypes.POINTER(AttnDesc)
         lib.spec_kv4_workspace_size.argtypes = [i32]
         lib.spec_kv4_workspace_size.restype = sz
-        lib.spec_kv4_write.argtypes = [k4, i32, vp, i32, vp, vp, i64, vp, i64, vp, i64, vp, sz, vp]
+        lib.spec_kv4_write.argtypes = [vp, i32, vp, i32, vp, vp, i64, vp, i64, vp, i64, vp, sz, vp]
         lib.spec_kv4_write.restype = ctypes.c_int
-        lib.spec_kv4_read.argtypes = [k4, i32, vp, i32, vp, vp, i64, vp, vp, vp, sz, vp]
+        lib.spec_kv4_read.argtypes = [vp, i32, vp, i32, vp, vp, i64, vp, vp, vp, sz, vp]
         lib.spec_kv4_read.restype = ctypes.c_int
         lib.spec_verify_attn_kv4_workspace_size.argtypes = [ad]
         lib.spec_verify_attn_kv4_workspace_size.restype = sz
-        lib.spec_verify_attn_kv4.argtypes = [ad, vp, k4, vp, i32, vp, vp, vp, vp, vp, sz, vp]
+        lib.spec_verify_attn_kv4.argtypes = [vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp]
         lib.spec_verify_attn_kv4.restype = ctypes.c_int
         lib.spec_attn_mass_workspace_size.argtypes = [ad]
         lib.spec_attn_mass_workspace_size.restype = sz
-        lib.spec_attn_mass.argtypes = [ad, vp, vp, vp, vp, i64, i32, vp, i32, vp, vp, vp, vp, vp,
+        lib.spec_attn_mass.argtypes = [vp, vp, vp, vp, vp, i64, i32, vp, i32, vp, vp, vp, vp, vp,
                                        i64, vp, sz, vp]
         lib.spec_attn_mass.restype = ctypes.c_int
         lib.spec_kv_evict_workspace_size.argtypes = [i32, i32, i64]
@@ -682,8 +683,22 @@ def evict_workspace_bytes(n: int, num_kv_heads: int, max_positions: int) -> int:
     return _workspace_bytes("spec_kv_evict_workspace_size", n, num_kv_heads, max_positions)
 
 
-def _kv4_pages(k_codes, v_codes, scales, kv_scale, devs) -> Kv4Pages:
-    """The C descriptor of a 4-bit cache, its tensors' devices added to ``devs``."""
+# sv_kv4_pages and sv_attn_desc as bytes: packing them takes a fraction of the time of filling
+# a ctypes structure, half a microsecond of a call that takes ten.
+_KV4_PAGES = struct.Struct("@qiiixxxxPPPP")
+_ATTN_DESC = struct.Struct("@iiiiiiqqifixxxx")
+
+
+def _packed_desc(B, Hq, hkv, d, max_draft_len, max_seq_len, q_rows, dtype, scale, window) -> bytes:
+    try:
+        return _ATTN_DESC.pack(B, Hq, hkv, d, max_draft_len, max_seq_len, q_rows, 0, dtype, scale, window)
+    except struct.error as e:
+        raise ValueError("max_draft_len, max_seq_len, softmax_scale or sliding_window: %s" % e)
+
+
+def _kv4_pages(k_codes, v_codes, scales, kv_scale, devs):
+    """(KV heads, head dimension, C descriptor) of a 4-bit cache, its tensors' devices added to
+    ``devs``."""
     devs += [_dev(k_codes, "k_codes", _U8), _dev(v_codes, "v_codes", _U8),
              _dev(scales, "scales", _SCALES), _dev(kv_scale, "kv_scale", (torch.float32,))]
     if k_codes.dim() != 4 or v_codes.shape != k_codes.shape:
@@ -693,8 +708,8 @@ def _kv4_pages(k_codes, v_codes, scales, kv_scale, devs) -> Kv4Pages:
         raise ValueError("scales must be [num_blocks, block_size, Hkv, 2, d / 16]")
     if kv_scale.shape != (2, hkv):
         raise ValueError("kv_scale must be [2, Hkv]")
-    return Kv4Pages(nb, bs, hkv, 2 * half, k_codes.data_ptr(), v_codes.data_ptr(),
-                    scales.data_ptr(), kv_scale.data_ptr())
+    return hkv, 2 * half, _KV4_PAGES.pack(nb, bs, hkv, 2 * half, k_codes.data_ptr(),
+                                          v_codes.data_ptr(), scales.data_ptr(), kv_scale.data_ptr())
 
 
 def _kv4_rows(block_table, start, count, devs, workspace, stream):
@@ -742,13 +757,13 @@ def spec_kv4_write(k, v, k_codes, v_codes, scales, kv_scale, block_table, start,
     scales (uint8 or float8_e4m3fn) [num_blocks, block_size, Hkv, 2, d / 16]; kv_scale fp32
     [2, Hkv] is the caller's."""
     devs = []
-    pages = _kv4_pages(k_codes, v_codes, scales, kv_scale, devs)
-    ks = _row_stride(k, "k", pages.num_kv_heads, pages.head_dim, None)
-    vs = _row_stride(v, "v", pages.num_kv_heads, pages.head_dim, k.shape[0])
+    hkv, d, pages = _kv4_pages(k_codes, v_codes, scales, kv_scale, devs)
+    ks = _row_stride(k, "k", hkv, d, None)
+    vs = _row_stride(v, "v", hkv, d, k.shape[0])
     devs += [k.get_device(), v.get_device()]
     B, workspace, dev = _kv4_rows(block_table, start, count, devs, workspace, stream)
     st = (_lib or load_library()).spec_kv4_write(
-        ctypes.byref(pages), B, block_table.data_ptr(), block_table.shape[1], start.data_ptr(),
+        pages, B, block_table.data_ptr(), block_table.shape[1], start.data_ptr(),
         count.data_ptr(), k.shape[0], k.data_ptr(), ks, v.data_ptr(), vs, workspace.data_ptr(),
         workspace.numel(), _stream_on(stream, dev))
     if st:
@@ -762,8 +777,7 @@ def spec_kv4_read(k_codes, v_codes, scales, kv_scale, block_table, start, count,
     count) is needed where k_out and v_out are not given; rows past the sum are left as they
     were (zeros in outputs made here)."""
     devs = []
-    pages = _kv4_pages(k_codes, v_codes, scales, kv_scale, devs)
-    shape = (pages.num_kv_heads, pages.head_dim)
+    *shape, pages = _kv4_pages(k_codes, v_codes, scales, kv_scale, devs)
     outs = [k_out, v_out]
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         if t is not None:
@@ -780,7 +794,7 @@ def spec_kv4_read(k_codes, v_codes, scales, kv_scale, block_table, start, count,
                 if outs[i] is None:
                     outs[i] = torch.zeros(rows, *shape, dtype=torch.bfloat16, device=k_codes.device)
     st = (_lib or load_library()).spec_kv4_read(
-        ctypes.byref(pages), B, block_table.data_ptr(), block_table.shape[1], start.data_ptr(),
+        pages, B, block_table.data_ptr(), block_table.shape[1], start.data_ptr(),
         count.data_ptr(), rows, outs[0].data_ptr(), outs[1].data_ptr(), workspace.data_ptr(),
         workspace.numel(), _stream_on(stream, dev))
     if st:
@@ -796,21 +810,19 @@ def spec_verify_attn_kv4(q, k_codes, v_codes, scales, kv_scale, block_table, seq
     [rows, Hq]: the natural log of each row's sum of exponentials) when it is given."""
     devs = [_dev(q, "q", (torch.bfloat16,)), _dev(block_table, "block_table", _I32),
             _dev(seq_lens, "seq_lens", _I32), _dev(draft_len, "draft_len", _I32)]
-    pages = _kv4_pages(k_codes, v_codes, scales, kv_scale, devs)
-    B = seq_lens.numel()
-    if q.dim() != 3 or q.shape[2] != pages.head_dim:
+    hkv, d, pages = _kv4_pages(k_codes, v_codes, scales, kv_scale, devs)
+    B, shape = seq_lens.numel(), q.shape
+    if len(shape) != 3 or shape[2] != d:
         raise ValueError("q must be [rows, Hq, d] with the pages' d")
     if seq_lens.dim() != 1 or draft_len.shape != (B,) or block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("seq_lens and draft_len must be [B], block_table [B, max_blocks]")
-    desc = paged_attn_desc(q, k_codes, B, max_draft_len, max_seq_len, softmax_scale, sliding_window,
-                           kv4=True)
     if out is not None:
         devs.append(_dev(out, "out", (torch.bfloat16,)))
-        if out.shape != q.shape:
+        if out.shape != shape:
             raise ValueError("out must have q's shape")
     if lse is not None:
         devs.append(_dev(lse, "lse", (torch.float32,)))
-        if lse.shape != q.shape[:2]:
+        if lse.shape != shape[:2]:
             raise ValueError("lse must be [rows, Hq]")
     if workspace is not None:
         devs.append(_dev(workspace, "workspace", _U8))
@@ -820,9 +832,13 @@ def spec_verify_attn_kv4(q, k_codes, v_codes, scales, kv_scale, block_table, seq
             if out is None:
                 out = torch.empty_like(q)
             if workspace is None:
+                desc = paged_attn_desc(q, k_codes, B, max_draft_len, max_seq_len, softmax_scale,
+                                       sliding_window, kv4=True)
                 workspace = new_workspace(verify_kv4_workspace_bytes(desc), q.device)
+    desc = _packed_desc(B, shape[1], hkv, d, max_draft_len, max_seq_len, shape[0], SV_KV4,
+                        softmax_scale, sliding_window)
     st = (_lib or load_library()).spec_verify_attn_kv4(
-        ctypes.byref(desc), q.data_ptr(), ctypes.byref(pages), block_table.data_ptr(),
+        desc, q.data_ptr(), pages, block_table.data_ptr(),
         block_table.shape[1], seq_lens.data_ptr(), draft_len.data_ptr(), out.data_ptr(),
         None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel(),
         _stream_on(stream, dev))
@@ -865,15 +881,18 @@ def spec_attn_mass(q, k_pages, block_table, seq_lens, draft_len, mass, *, max_dr
             if tuple(t.shape) != shape:
                 raise ValueError("%s must be %s" % (name, list(shape)))
             ptr[name] = t.data_ptr()
-    desc = paged_attn_desc(q, k_pages, B, max_draft_len, max_seq_len, softmax_scale, kv4=kv4)
     if workspace is not None:
         devs.append(_dev(workspace, "workspace", _U8))
     dev = _one_device(devs)
     if workspace is None:
         with _allocating_on(stream, dev):
+            desc = paged_attn_desc(q, k_pages, B, max_draft_len, max_seq_len, softmax_scale, kv4=kv4)
             workspace = new_workspace(mass_workspace_bytes(desc), q.device)
+    dt = SV_KV4 if kv4 else SV_BF16 if k_pages.dtype == torch.bfloat16 else SV_FP8_E4M3
+    desc = _packed_desc(B, q.shape[1], hkv, d, max_draft_len, max_seq_len, q.shape[0], dt,
+                        softmax_scale, 0)
     st = (_lib or load_library()).spec_attn_mass(
-        ctypes.byref(desc), q.data_ptr(), k_pages.data_ptr(), ptr["scales"], ptr["kv_scale"], nb, bs,
+        desc, q.data_ptr(), k_pages.data_ptr(), ptr["scales"], ptr["kv_scale"], nb, bs,
         block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), draft_len.data_ptr(),
         ptr["row_count"], ptr["lse"], mass.data_ptr(), mass.shape[2], workspace.data_ptr(),
         workspace.numel(), _stream_on(stream, dev))

@@ -83,6 +83,22 @@ def test_layout_of_the_structure():
     assert [getattr(api.Kv4Pages, n).offset for n, _ in api.Kv4Pages._fields_] == [0, 8, 12, 16, 24, 32, 40, 48]
 
 
+def test_packed_descriptors_are_the_structures():
+    d = desc(softmax_scale=0.25, sliding_window=7, q_rows=1 << 40, kv_rows=5)
+    fields = [getattr(d, n) for n, _ in api.AttnDesc._fields_]
+    assert api._ATTN_DESC.pack(*fields) == bytes(d)
+    p = pages(num_blocks=1 << 33)
+    assert api._KV4_PAGES.pack(*[getattr(p, n) for n, _ in api.Kv4Pages._fields_]) == bytes(p)
+
+
+@pytest.mark.parametrize("bad", [dict(max_seq_len=1 << 31), dict(max_draft_len=-1 << 40), dict(window=1 << 31),
+                                 dict(scale="1"), dict(max_seq_len=2.5)])
+def test_arguments_that_the_descriptor_cannot_hold(bad):
+    a = dict(B=1, Hq=4, hkv=1, d=64, max_draft_len=0, max_seq_len=9, q_rows=3, dtype=0, scale=0.0, window=0)
+    with pytest.raises(ValueError):
+        api._packed_desc(**{**a, **bad})
+
+
 BAD_PAGES = [
     (dict(num_blocks=0), 2), (dict(num_blocks=1 << 31), 2), (dict(num_blocks=1 << 28), 2), (dict(block_size=12), 2),
     (dict(block_size=4), 2), (dict(block_size=1 << 17), 2), (dict(num_kv_heads=0), 2), (dict(num_kv_heads=4097), 2),
