@@ -481,9 +481,9 @@ SV_API size_t spec_kv_evict_workspace_size(int32_t n, int32_t num_kv_heads, int6
  *   new_len     int32 [n], 0 <= new_len[i] <= N; keep_first[i] + keep_last <= new_len[i] < N, or
  *               new_len[i] = N
  *   keep_first  int32 [n] (a shared prefix, say) or NULL: 0
- *   mass        fp32 [table_rows, num_kv_heads, mass_stride], in and out; N <= mass_stride
+ *   mass        fp32 [table_rows, num_kv_heads, mass_stride], in and out; N <= mass_stride <= 2^30
  *   kept        int32 [n, num_kv_heads, kept_stride] or NULL: out, the position that each new
- *               position was; new_len[i] <= kept_stride; entries past new_len[i] are left
+ *               position was; new_len[i] <= kept_stride <= 2^30; entries past new_len[i] are left
  *   pools       HOST array, as for spec_pages_extend: [num_blocks, block_size, num_kv_heads,
  *               any number of bytes that is a multiple of 8]
  * The pages that hold positions keep_first[i] .. new_len[i] - 1 must be the row's alone (count

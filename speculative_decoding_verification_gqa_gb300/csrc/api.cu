@@ -1065,8 +1065,9 @@ SV_API sv_status spec_attn_mass(const sv_attn_desc* desc, const void* q, const v
 }
 
 SV_API size_t spec_kv_evict_workspace_size(int32_t n, int32_t num_kv_heads, int64_t mass_stride) {
+  // (positions and those that a CTA looks ahead to are 32 bits)
   if (n < 0 || n > SV_MAX_EVICT_ROWS || num_kv_heads < 1 || num_kv_heads > 4096 || mass_stride < 1 ||
-      mass_stride > MAX_KV_ROWS)
+      mass_stride > (int64_t)1 << 30)
     return 0;
   return evict_ws_bytes(n, num_kv_heads, mass_stride);
 }
@@ -1082,7 +1083,7 @@ SV_API sv_status spec_kv_evict(const sv_page_table* table, int32_t n, const int3
   if (st == SV_OK) st = check_pools(table, num_pools, pools);
   if (st != SV_OK) return st;
   const size_t need = spec_kv_evict_workspace_size(n, num_kv_heads, mass_stride);
-  if (need == 0 || keep_last < 0 || (kept && (kept_stride < 0 || kept_stride > MAX_KV_ROWS / 2)))
+  if (need == 0 || keep_last < 0 || (kept && (kept_stride < 0 || kept_stride > (int64_t)1 << 30)))
     return SV_ERR_SHAPE;
   // (the sizes below stay within 63 bits)
   if ((int64_t)table->table_rows * num_kv_heads > ((int64_t)1 << 60) / mass_stride) return SV_ERR_SHAPE;

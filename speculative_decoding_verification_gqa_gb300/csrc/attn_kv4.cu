@@ -22,6 +22,10 @@
 // l). The CTA's four warps are spread over the unit's neighbouring heads, then over its keys;
 // they meet only at the end of a unit, where a head's parts are joined by the rule of the
 // online softmax. Units, their line and the join across CTAs (kv4_join, below): line.cuh.
+//
+// Measured (d 128): 64 single tokens over up to 8192 positions, 32 query and 8 KV heads, 76.8 us
+// with the join, 308 MB at 4.0 TB/s: half of the issue slots go to decoding, MMAs and exponentials
+// for 8 rows a head of which 4 are live; the rest is the latency that 12 warps an SM leave.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -30,6 +30,11 @@
 // requested before this unit's O is written. (Row by row in 16-byte pieces, a change of units
 // took 20 thousand clocks, ten tiles' time.)
 //
+// Measured (d 128): a tile takes 2050 clocks, of which its MMAs take 1024 (issuing them alone
+// would give 1.9 PFLOP/s); decoding and softmax warps issue 1200 instructions a scheduler a
+// tile. 8 sequences of 32768 positions, 16 tokens, 64 query and 8 KV heads: 140 us with the join,
+// 0.98 PFLOP/s; 16 of 8192, 32 tokens, 32 and 8 heads: 84 us, 0.82.
+//
 // TMEM columns: O_0, O_1 (128 each), S_0, S_1 (64 each), Q (64: f16 pairs), P_0, P_1 (32 each).
 // Every wait is bounded as in attn_tc.cu.
 #include <cuda.h>

@@ -20,6 +20,13 @@
 // end to end on one line, a unit's start and every tile as long as their work: a tile's fixed
 // part and one for every 8 rows. Each CTA (one an SM) takes the tiles that begin in its equal
 // share of the line, and finds its place by scanning the lengths itself.
+//
+// Measured (d 128): 32 sequences of up to 16384 positions, 8 tokens, 32 query and 4 KV heads,
+// bf16: the first pass 61 us, the second 70, of 278 MB each (4.0 to 4.5 TB/s) with half of the
+// issue slots taken; 16 of up to 8192, 9 tokens, 8 KV heads, 4 bits, log-sums given: 24.6 us for
+// 43 MB, a chain of short phases (scan, Q, ten chunks a warp). On tcgen05 with K by TMA (a key
+// in a TMEM lane, a row's sum in a register) they took 122 to 131 and 28 us: a page of 16 rows
+// makes 2 KB boxes, about 100 clocks each.
 #include <cuda_bf16.h>
 
 #include "kv4.cuh"

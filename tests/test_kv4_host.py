@@ -189,8 +189,8 @@ def test_bad_mass_calls(lib, kw, bad, status):
 
 @pytest.mark.parametrize("bad,status", [
     (dict(num_blocks=0), 2), (dict(block_size=12), 2), (dict(ref_count=None), 1), (dict(n=5), 2), (dict(n=-1), 2),
-    (dict(last=-1), 2), (dict(heads=0), 2), (dict(heads=4097), 2), (dict(stride=0), 2), (dict(stride=1 << 32), 2),
-    (dict(kept=FAKE, ks=-1), 2), (dict(kept=FAKE, ks=1 << 31), 2), (dict(new=None), 1), (dict(mass=None), 1),
+    (dict(last=-1), 2), (dict(heads=0), 2), (dict(heads=4097), 2), (dict(stride=0), 2), (dict(stride=(1 << 30) + 1), 2),
+    (dict(kept=FAKE, ks=-1), 2), (dict(kept=FAKE, ks=(1 << 30) + 1), 2), (dict(new=None), 1), (dict(mass=None), 1),
     (dict(new=FAKE + 2), 4), (dict(rows=FAKE + 2), 4), (dict(first=FAKE + 1), 4), (dict(mass=(5 << 30) + 2), 4),
     (dict(kept=FAKE + 2, ks=9), 4), (dict(ws=None), 1), (dict(ws=(7 << 30) + 16), 4), (dict(bytes=1024), 5),
     (dict(pools=((6 << 30, 2048 + 16),)), 2), (dict(pools=((6 << 30, 256),), heads=4), 2),  # 4 bytes a head
@@ -212,7 +212,7 @@ def test_workspace_sizes(lib):
     assert lib.spec_kv4_workspace_size(-1) == 0 and lib.spec_kv4_workspace_size(1 << 20) > 0
     size = lib.spec_kv_evict_workspace_size
     assert size(-1, 2, 100) == 0 and size(2, 0, 100) == 0 and size(2, 4097, 100) == 0 and size(2, 2, 0) == 0
-    assert size((1 << 16) + 1, 2, 100) == 0 and size(2, 2, 1 << 32) == 0
+    assert size((1 << 16) + 1, 2, 100) == 0 and size(2, 2, (1 << 30) + 1) == 0 < size(2, 2, 1 << 30)
     assert 0 < size(0, 2, 100) <= size(1, 2, 100) < size(2, 2, 1000) < size(9, 3, 1000)
 
 
