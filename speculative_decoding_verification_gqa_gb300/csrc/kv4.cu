@@ -15,9 +15,10 @@
 // 8 bytes of codes, a scale). The scan that finds each row's sequence and position runs in
 // every CTA (counts of a batch are a few KB in L2) while a write's loads are in flight.
 //
-// Measured: 49 thousand rows of 8 heads, d 128, written in 70 us (0.26 GB, 3.7 TB/s; 57% of the
-// issue slots: two products, two conversions and a comparison for each element) and read back in
-// 62 us (4.2 TB/s); 197 thousand read back in 191 us (5.4 TB/s, three quarters of it writes).
+// Measured: 197 thousand rows of 8 heads, d 128, read back in 161 us (1.03 GB, 6.4 TB/s: 0.95 of a
+// copy; 191 us with two stores of 16 bytes); 49 thousand written and read back in 117 us (133),
+// where the write is bound by issue: two products, two conversions and a comparison for each
+// element.
 #include <cuda_bf16.h>
 
 #include "kv4.cuh"
@@ -203,8 +204,33 @@ __device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {  // of bf
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
+// 32 bytes of a thread, in one access where they are aligned (W32), so that no 32-byte sector is
+// touched twice.
+template <bool W32>
+__device__ __forceinline__ void load32(const void* p, uint4 (&x)[2]) {
+  if constexpr (W32) {
+    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(x[0].x), "=r"(x[0].y), "=r"(x[0].z), "=r"(x[0].w), "=r"(x[1].x), "=r"(x[1].y), "=r"(x[1].z), "=r"(x[1].w)
+        : "l"(p));
+  } else {
+    x[0] = __ldg(reinterpret_cast<const uint4*>(p));
+    x[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  }
+}
+template <bool W32>
+__device__ __forceinline__ void store32(void* p, const uint32_t (&x)[8]) {
+  if constexpr (W32) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+  }
+}
+
 // N: rows of a thread whose loads run together.
-template <int N>
+template <int N, bool W32>
 __global__ void __launch_bounds__(NTH) kv4_write_kernel(const Kv4Args a) {
   __shared__ int64_t s_row[MAX_CTA_ROWS];
   const int64_t r0 = (int64_t)blockIdx.x * a.cta_rows;
@@ -226,11 +252,7 @@ __global__ void __launch_bounds__(NTH) kv4_write_kernel(const Kv4Args a) {
       for (int n = 0; n < N; ++n) {
         const int r = rr + n * a.rows_at_once + lr;
         x[n][0] = x[n][1] = make_uint4(0, 0, 0, 0);
-        if (in && r < rows) {
-          const uint4* s4 = reinterpret_cast<const uint4*>(src + (r0 + r) * stride);
-          x[n][0] = __ldg(s4);
-          x[n][1] = __ldg(s4 + 1);
-        }
+        if (in && r < rows) load32<W32>(src + (r0 + r) * stride, x[n]);
       }
       if (!located) {
         if (!locate(a, r0, s_row)) return;
@@ -268,7 +290,7 @@ __global__ void __launch_bounds__(NTH) kv4_write_kernel(const Kv4Args a) {
   }
 }
 
-template <int N>
+template <int N, bool W32>
 __global__ void __launch_bounds__(NTH) kv4_read_kernel(const Kv4Args a) {
   __shared__ int64_t s_row[MAX_CTA_ROWS];
   const int64_t r0 = (int64_t)blockIdx.x * a.cta_rows;
@@ -318,9 +340,7 @@ __global__ void __launch_bounds__(NTH) kv4_read_kernel(const Kv4Args a) {
             out[4 * w + e] = *reinterpret_cast<const uint32_t*>(&o);
           }
         }
-        uint4* d4 = reinterpret_cast<uint4*>(dst + (int64_t)(rr + n * a.rows_at_once) * out_elems);
-        d4[0] = make_uint4(out[0], out[1], out[2], out[3]);
-        d4[1] = make_uint4(out[4], out[5], out[6], out[7]);
+        store32<W32>(dst + (int64_t)(rr + n * a.rows_at_once) * out_elems, out);
       }
     }
   }
@@ -333,13 +353,16 @@ cudaError_t launch_rows(K1 one, KN some, int thread_rows, Kv4Args a, int sms, cu
   a.rows_at_once = NTH / a.lanes;
   // An item a thread while that leaves no SM with more than two CTAs; else `thread_rows`, some of
   // them at a time, so that the scan for the rows' places costs little next to them. (49 thousand
-  // rows of 8 heads written and read back: 8 and 16 rows 129 us, 4 and 4 134, 2 and 2 162.)
+  // rows of 8 heads written and read back, by 16 bytes: 8 and 16 rows 129 us, 4 and 4 134, 2 and 2 162.)
   const bool few = a.rows * a.row_items <= 2 * (int64_t)sms * NTH;
   const int want = few ? a.rows_at_once : thread_rows * a.rows_at_once;
   a.cta_rows = want > MAX_CTA_ROWS ? MAX_CTA_ROWS : want;
   const unsigned grid = (unsigned)((a.rows + a.cta_rows - 1) / a.cta_rows);
   return launch_pdl(few ? one : some, dim3(grid), dim3(NTH), 0, s, a);
 }
+
+// Whether rows of bf16, `stride` elements apart, begin on 32 bytes.
+bool aligned32(const void* p, int64_t stride) { return ((uintptr_t)p & 31) == 0 && stride % 16 == 0; }
 
 Kv4Args args_of(const sv_kv4_pages& p, int B, const int32_t* table, int max_blocks,
                 const int32_t* start, const int32_t* count, int64_t rows, void* ws) {
@@ -373,7 +396,9 @@ cudaError_t launch_kv4_write(const sv_kv4_pages& p, int B, const int32_t* table,
   a.v = (const uint16_t*)v;
   a.k_stride = k_stride;
   a.v_stride = v_stride;
-  return launch_rows(kv4_write_kernel<1>, kv4_write_kernel<2>, 8, a, sms, s);
+  if (aligned32(k, k_stride) && aligned32(v, v_stride))
+    return launch_rows(kv4_write_kernel<1, true>, kv4_write_kernel<2, true>, 8, a, sms, s);
+  return launch_rows(kv4_write_kernel<1, false>, kv4_write_kernel<2, false>, 8, a, sms, s);
 }
 
 cudaError_t launch_kv4_read(const sv_kv4_pages& p, int B, const int32_t* table, int max_blocks,
@@ -382,7 +407,9 @@ cudaError_t launch_kv4_read(const sv_kv4_pages& p, int B, const int32_t* table, 
   Kv4Args a = args_of(p, B, table, max_blocks, start, count, rows, ws);
   a.k_out = (uint16_t*)k_out;
   a.v_out = (uint16_t*)v_out;
-  return launch_rows(kv4_read_kernel<1>, kv4_read_kernel<4>, 16, a, sms, s);
+  if (aligned32(k_out, 16) && aligned32(v_out, 16))
+    return launch_rows(kv4_read_kernel<1, true>, kv4_read_kernel<4, true>, 16, a, sms, s);
+  return launch_rows(kv4_read_kernel<1, false>, kv4_read_kernel<4, false>, 16, a, sms, s);
 }
 
 }  // namespace sv

@@ -98,6 +98,33 @@ def test_read_rows_are_the_values(d):
     assert sv.workspace_status(ws) == 0
 
 
+@pytest.mark.parametrize("which", ["k", "v", "both"])
+@pytest.mark.parametrize("count", [3, 2000])
+def test_rows_on_16_bytes_only(which, count):
+    """Arrays and row strides that are multiples of 16 bytes but not of 32: the same as others."""
+    Hkv, d, bs, pad = 3, 64, 16, 8  # rows of Hkv d + 8 elements
+    gen = torch.Generator().manual_seed(count)
+    table, blocks = block_table([count], bs, gen)
+    x = [torch.randn(count, Hkv, d, generator=gen).to(torch.bfloat16).to(DEV) for _ in "kv"]
+    hs = torch.full((2, Hkv), 0.002, device=DEV)
+    args = (hs, table.to(DEV), i32([0]), i32([count]))
+    want, got = (empty_pages(blocks, bs, Hkv, d, 0) for _ in range(2))
+    odd = []
+    for name, t in zip("kv", x):
+        flat = torch.zeros(count * (Hkv * d + pad) + pad, dtype=torch.bfloat16, device=DEV)
+        o = flat[pad:].view(count, Hkv * d + pad)[:, :Hkv * d].view(count, Hkv, d)
+        o.copy_(t)
+        odd.append(o if which in (name, "both") else t)
+    sv.spec_kv4_write(*x, *want, *args)
+    sv.spec_kv4_write(*odd, *got, *args)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    outs = [torch.full((count * Hkv * d + pad,), 9.0, dtype=torch.bfloat16, device=DEV)[pad:].view(count, Hkv, d)
+            if which in (name, "both") else torch.zeros(count, Hkv, d, dtype=torch.bfloat16, device=DEV) for name in "kv"]
+    assert which == "v" or outs[0].data_ptr() % 32 == 16
+    sv.spec_kv4_read(*want, *args, k_out=outs[0], v_out=outs[1])
+    assert all(torch.equal(a, b) for a, b in zip(outs, sv.spec_kv4_read(*want, *args, rows=count)))
+
+
 def _near_middles(hs, gen):
     """bf16 blocks whose elements lie next to the middles of two codes, and whose largest lies
     next to the middle of two block scales."""
