@@ -16,7 +16,7 @@
 //           dependent reads (src, table, data), so many narrow slices in flight pay.
 // Select reads the weights (4 bytes a position) four times, from L2 after the first; move is
 // bound by memory. Measured: 32 rows of 16384 positions to 4096, 4 heads of 128 bytes, two pools:
-// select 17 us, move 53 us for 277 MB (5.2 TB/s).
+// select 17 us, move 46 us for 277 MB (6.0 TB/s).
 #include "internal.cuh"
 
 namespace sv {
@@ -25,10 +25,11 @@ namespace {
 constexpr int ST = 1024;        // threads of select
 constexpr int BINS = 2048;
 constexpr int MTH = 256;        // threads of move
-// Bytes of a column slice, and pieces of 16 of a thread in flight. (32 rows of 16384 positions cut
-// to 4096, 4 heads of 128 bytes, two pools: 82 us; slices of 32 and 128 bytes 95, 127; 2 and 8
-// pieces 96, 88.)
-constexpr int SLICE = 64, MOVES = 4;
+// Bytes of a column slice, and pieces of 32 of a thread in flight. (32 rows of 16384 positions cut
+// to 4096, 4 heads of 128 bytes, two pools, with the copy of the weights: 73 us; slices of 32 and
+// 128 bytes 89 and 90; 1, 3, 4 and 8 pieces 88, 74, 76 and 95; 128 and 512 threads 100 and 85;
+// pieces of 16 bytes 82.)
+constexpr int SLICE = 64, MOVES = 2;
 
 struct EvictArgs {
   sv_page_table t;
@@ -232,6 +233,34 @@ template <>
 struct VecOf<8> {
   using type = uint2;
 };
+struct Vec32 {
+  uint4 x[2];
+};
+template <>
+struct VecOf<32> {
+  using type = Vec32;
+};
+template <class T>
+__device__ __forceinline__ void load_piece(const uint8_t* p, T& v) {
+  v = *reinterpret_cast<const T*>(p);
+}
+template <class T>
+__device__ __forceinline__ void store_piece(uint8_t* p, const T& v) {
+  *reinterpret_cast<T*>(p) = v;
+}
+__device__ __forceinline__ void load_piece(const uint8_t* p, Vec32& v) {  // (a whole sector at once)
+  uint4 &a = v.x[0], &b = v.x[1];
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void store_piece(uint8_t* p, const Vec32& v) {
+  const uint4 &a = v.x[0], &b = v.x[1];
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+               "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
 
 // One slice: `cols` pieces of V bytes at `base`, positions `pos_bytes` apart in a page, through
 // the table's row. The next batch's places (src, then the table) are looked up while this one's
@@ -268,13 +297,13 @@ __device__ __forceinline__ void move_slice(const EvictArgs& a, const RowPlan& p,
 #pragma unroll
     for (int e = 0; e < U; ++e) {
       dst[e] = from[e] >= 0 ? to[e] : -1;
-      if (from[e] >= 0) v[e] = *reinterpret_cast<const T*>(base + from[e] * pos_bytes);
+      if (from[e] >= 0) load_piece(base + from[e] * pos_bytes, v[e]);
     }
     look(k0 + per * U);
     __syncthreads();  // the batch is read
 #pragma unroll
     for (int e = 0; e < U; ++e)
-      if (dst[e] >= 0) *reinterpret_cast<T*>(base + dst[e] * pos_bytes) = v[e];
+      if (dst[e] >= 0) store_piece(base + dst[e] * pos_bytes, v[e]);
   }
 }
 
@@ -320,7 +349,9 @@ __global__ void __launch_bounds__(MTH) move_kernel(const EvictArgs a, const __gr
     if (s < n) {
       uint8_t* base = (uint8_t*)pools.p[k].base + g * row_bytes + s * SLICE;
       const int bytes = (int)min((int64_t)SLICE, row_bytes - s * SLICE);
-      if (bytes % 16 == 0 && row_bytes % 16 == 0)
+      if (((uintptr_t)pools.p[k].base | row_bytes | bytes) % 32 == 0)
+        move_slice<32>(a, p, src, base, pos_bytes, bytes / 32);
+      else if (bytes % 16 == 0 && row_bytes % 16 == 0)
         move_slice<16>(a, p, src, base, pos_bytes, bytes / 16);
       else
         move_slice<8>(a, p, src, base, pos_bytes, bytes / 8);

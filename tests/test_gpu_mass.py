@@ -302,6 +302,16 @@ def test_evict(lens, rows, new, first, last, Hkv, bs, widths, ties):
     check_evict(Rows(lens, Hkv, bs, widths, len(lens) + Hkv, ties=ties), rows, new, first, last)
 
 
+def test_pools_on_16_bytes_only():
+    """Page data that begins on 16 bytes but not on 32."""
+    s = Rows([700, 90], 2, 16, (128, 64), 5)
+    for i, p in enumerate(s.pools):
+        flat = torch.empty(p.numel() + 16, dtype=torch.uint8, device=DEV)
+        s.pools[i] = flat[16:].view(p.shape).copy_(p)
+        assert s.pools[i].data_ptr() % 32 == 16
+    check_evict(s, None, [300, 60], [4, 4], 16)
+
+
 def test_weights_of_every_kind():
     """Equal weights, zeros of either sign, infinities, subnormals and NaN (least of all)."""
     s = Rows([64, 64, 64], 2, 16, (64,), 3)
