@@ -15,10 +15,10 @@
 // 8 bytes of codes, a scale). The scan that finds each row's sequence and position runs in
 // every CTA (counts of a batch are a few KB in L2) while a write's loads are in flight.
 //
-// Measured: 197 thousand rows of 8 heads, d 128, read back in 161 us (1.03 GB, 6.4 TB/s: 0.95 of a
-// copy; 191 us with two stores of 16 bytes); 49 thousand written and read back in 117 us (133),
-// where the write is bound by issue: two products, two conversions and a comparison for each
-// element.
+// Measured: 197 thousand rows of 8 heads, d 128, read back in 157 us (1.03 GB, 6.6 TB/s: 0.97 of a
+// copy; 191 us with two stores of 16 bytes); 49 thousand written and read back in 108 us (133;
+// 117 with 3 CTAs of the write on an SM), where the write is bound by issue: two products, two
+// conversions and a comparison for each element.
 #include <cuda_bf16.h>
 
 #include "kv4.cuh"
@@ -231,7 +231,7 @@ __device__ __forceinline__ void store32(void* p, const uint32_t (&x)[8]) {
 
 // N: rows of a thread whose loads run together.
 template <int N, bool W32>
-__global__ void __launch_bounds__(NTH) kv4_write_kernel(const Kv4Args a) {
+__global__ void __launch_bounds__(NTH, 4) kv4_write_kernel(const Kv4Args a) {
   __shared__ int64_t s_row[MAX_CTA_ROWS];
   const int64_t r0 = (int64_t)blockIdx.x * a.cta_rows;
   const int rows = (int)min((int64_t)a.cta_rows, a.rows - r0);
@@ -353,7 +353,8 @@ cudaError_t launch_rows(K1 one, KN some, int thread_rows, Kv4Args a, int sms, cu
   a.rows_at_once = NTH / a.lanes;
   // An item a thread while that leaves no SM with more than two CTAs; else `thread_rows`, some of
   // them at a time, so that the scan for the rows' places costs little next to them. (49 thousand
-  // rows of 8 heads written and read back, by 16 bytes: 8 and 16 rows 129 us, 4 and 4 134, 2 and 2 162.)
+  // rows of 8 heads written and read back: 16 and 8 rows 108.5 us, 8 and 8 109.3, 8 and 16 110.9, 4
+  // and 16 114.6.)
   const bool few = a.rows * a.row_items <= 2 * (int64_t)sms * NTH;
   const int want = few ? a.rows_at_once : thread_rows * a.rows_at_once;
   a.cta_rows = want > MAX_CTA_ROWS ? MAX_CTA_ROWS : want;
@@ -397,8 +398,8 @@ cudaError_t launch_kv4_write(const sv_kv4_pages& p, int B, const int32_t* table,
   a.k_stride = k_stride;
   a.v_stride = v_stride;
   if (aligned32(k, k_stride) && aligned32(v, v_stride))
-    return launch_rows(kv4_write_kernel<1, true>, kv4_write_kernel<2, true>, 8, a, sms, s);
-  return launch_rows(kv4_write_kernel<1, false>, kv4_write_kernel<2, false>, 8, a, sms, s);
+    return launch_rows(kv4_write_kernel<1, true>, kv4_write_kernel<2, true>, 16, a, sms, s);
+  return launch_rows(kv4_write_kernel<1, false>, kv4_write_kernel<2, false>, 16, a, sms, s);
 }
 
 cudaError_t launch_kv4_read(const sv_kv4_pages& p, int B, const int32_t* table, int max_blocks,
@@ -408,8 +409,8 @@ cudaError_t launch_kv4_read(const sv_kv4_pages& p, int B, const int32_t* table, 
   a.k_out = (uint16_t*)k_out;
   a.v_out = (uint16_t*)v_out;
   if (aligned32(k_out, 16) && aligned32(v_out, 16))
-    return launch_rows(kv4_read_kernel<1, true>, kv4_read_kernel<4, true>, 16, a, sms, s);
-  return launch_rows(kv4_read_kernel<1, false>, kv4_read_kernel<4, false>, 16, a, sms, s);
+    return launch_rows(kv4_read_kernel<1, true>, kv4_read_kernel<4, true>, 8, a, sms, s);
+  return launch_rows(kv4_read_kernel<1, false>, kv4_read_kernel<4, false>, 8, a, sms, s);
 }
 
 }  // namespace sv
