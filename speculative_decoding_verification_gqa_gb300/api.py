@@ -158,16 +158,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.spec_accept_stochastic.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp,
                                                ctypes.c_float, vp, vp, vp, sz, vp]
         lib.spec_accept_stochastic.restype = ctypes.c_int
-        pt = ctypes.POINTER(PageTable)
         lib.spec_pages_workspace_size.argtypes = [i32, i32]
         lib.spec_pages_workspace_size.restype = sz
-        lib.spec_pages_fork.argtypes = [pt, i32, vp, vp, vp, vp, sz, vp]
+        lib.spec_pages_fork.argtypes = [vp, i32, vp, vp, vp, vp, sz, vp]
         lib.spec_pages_fork.restype = ctypes.c_int
-        lib.spec_pages_extend.argtypes = [pt, i32, vp, vp, i32, vp, vp, sz, vp]
+        lib.spec_pages_extend.argtypes = [vp, i32, vp, vp, i32, vp, vp, sz, vp]
         lib.spec_pages_extend.restype = ctypes.c_int
-        lib.spec_pages_trim.argtypes = [pt, i32, vp, vp, vp, sz, vp]
+        lib.spec_pages_trim.argtypes = [vp, i32, vp, vp, vp, sz, vp]
         lib.spec_pages_trim.restype = ctypes.c_int
-        lib.spec_pages_compact.argtypes = [pt, i32, vp, vp, vp, vp, sz, vp]
+        lib.spec_pages_compact.argtypes = [vp, i32, vp, vp, vp, vp, sz, vp]
         lib.spec_pages_compact.restype = ctypes.c_int
         ad = ctypes.POINTER(AttnDesc)
         lib.spec_kv4_workspace_size.argtypes = [i32]
@@ -187,7 +186,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         lib.spec_attn_mass.restype = ctypes.c_int
         lib.spec_kv_evict_workspace_size.argtypes = [i32, i32, i64]
         lib.spec_kv_evict_workspace_size.restype = sz
-        lib.spec_kv_evict.argtypes = [pt, i32, vp, vp, vp, i32, i32, vp, i64, vp, i64, i32, vp, vp,
+        lib.spec_kv_evict.argtypes = [vp, i32, vp, vp, vp, i32, i32, vp, i64, vp, i64, i32, vp, vp,
                                       sz, vp]
         lib.spec_kv_evict.restype = ctypes.c_int
         lib.sv_inject_launch_failure.argtypes = [ctypes.c_int]
@@ -518,6 +517,7 @@ class PagePools:
             raise ValueError("the pools must not overlap")
         self.device = self.tensors[0].get_device() if self.tensors else -1
         self.pages = tuple(self.tensors[0].shape[:2]) if self.tensors else (0, 0)
+        self.heads = {t.shape[2] if t.dim() > 2 else None for t in self.tensors}
         self.array = (PageData * len(self.tensors))(*[
             PageData(t.data_ptr(), t.numel() // t.shape[0] * t.element_size())
             for t in self.tensors])
@@ -536,6 +536,10 @@ def pages_workspace_bytes(num_blocks: int, table_rows: int) -> int:
     if n == 0:
         raise SpecVerifyError(2, "spec_pages_workspace_size")
     return n
+
+
+# sv_page_table as bytes: packing it takes a fraction of the time of filling a ctypes structure.
+_PAGE_TABLE = struct.Struct("@iiiiPPP")
 
 
 def _page_table(ref_count, block_table, cached_len, block_size, lists, pools, workspace, stream):
@@ -565,8 +569,12 @@ def _page_table(ref_count, block_table, cached_len, block_size, lists, pools, wo
     if workspace is None:
         with _allocating_on(stream, dev):
             workspace = new_workspace(pages_workspace_bytes(blocks, rows), ref_count.device)
-    return (PageTable(blocks, block_size, rows, table[1], ref_count.data_ptr(),
-                      block_table.data_ptr(), cached_len.data_ptr()), workspace, dev)
+    try:
+        packed = _PAGE_TABLE.pack(blocks, block_size, rows, table[1], ref_count.data_ptr(),
+                                  block_table.data_ptr(), cached_len.data_ptr())
+    except struct.error as e:
+        raise ValueError("block_size: %s" % e)
+    return packed, workspace, dev
 
 
 def _as_pools(pools) -> PagePools:
@@ -583,7 +591,7 @@ def spec_pages_fork(ref_count, block_table, cached_len, parents, children, *, bl
                              (("parents", parents), ("children", children), ("fork_len", fork_len)),
                              None, workspace, stream)
     st = (_lib or load_library()).spec_pages_fork(
-        ctypes.byref(t), parents.numel(), parents.data_ptr(), children.data_ptr(),
+        t, parents.numel(), parents.data_ptr(), children.data_ptr(),
         None if fork_len is None else fork_len.data_ptr(), ws.data_ptr(), ws.numel(),
         _stream_on(stream, dev))
     if st:
@@ -601,7 +609,7 @@ def spec_pages_extend(ref_count, block_table, cached_len, rows, new_len, *, bloc
     t, ws, dev = _page_table(ref_count, block_table, cached_len, block_size,
                              (("new_len", new_len), ("rows", rows)), pools, workspace, stream)
     st = (_lib or load_library()).spec_pages_extend(
-        ctypes.byref(t), new_len.numel(), None if rows is None else rows.data_ptr(),
+        t, new_len.numel(), None if rows is None else rows.data_ptr(),
         new_len.data_ptr(), len(pools.tensors), pools.array, ws.data_ptr(), ws.numel(),
         _stream_on(stream, dev))
     if st:
@@ -615,7 +623,7 @@ def spec_pages_trim(ref_count, block_table, cached_len, rows, new_len, *, block_
     t, ws, dev = _page_table(ref_count, block_table, cached_len, block_size,
                              (("new_len", new_len), ("rows", rows)), None, workspace, stream)
     st = (_lib or load_library()).spec_pages_trim(
-        ctypes.byref(t), new_len.numel(), None if rows is None else rows.data_ptr(),
+        t, new_len.numel(), None if rows is None else rows.data_ptr(),
         new_len.data_ptr(), ws.data_ptr(), ws.numel(), _stream_on(stream, dev))
     if st:
         _check(st, "spec_pages_trim")
@@ -630,7 +638,7 @@ def spec_pages_compact(ref_count, block_table, cached_len, *, block_size: int, p
     t, ws, dev = _page_table(ref_count, block_table, cached_len, block_size, (), pools, workspace,
                              stream)
     out = [None, None]
-    for i, (o, name, n) in enumerate(((remap, "remap", t.num_blocks), (num_live, "num_live", 1))):
+    for i, (o, name, n) in enumerate(((remap, "remap", ref_count.numel()), (num_live, "num_live", 1))):
         if o is not None:
             if _dev(o, name, _I32) != dev:
                 raise ValueError("%s lies on another device" % name)
@@ -638,7 +646,7 @@ def spec_pages_compact(ref_count, block_table, cached_len, *, block_size: int, p
                 raise ValueError("%s must hold %d values" % (name, n))
             out[i] = o.data_ptr()
     st = (_lib or load_library()).spec_pages_compact(
-        ctypes.byref(t), len(pools.tensors), pools.array, out[0], out[1], ws.data_ptr(),
+        t, len(pools.tensors), pools.array, out[0], out[1], ws.data_ptr(),
         ws.numel(), _stream_on(stream, dev))
     if st:
         _check(st, "spec_pages_compact")
@@ -913,10 +921,9 @@ def spec_kv_evict(ref_count, block_table, cached_len, rows, new_len, mass, *, bl
     pools = _as_pools(pools)
     if mass.dim() != 3 or mass.shape[0] != cached_len.numel():
         raise ValueError("mass must be [rows, Hkv, positions]")
-    hkv, n = mass.shape[1], new_len.numel()
-    for t in pools.tensors:
-        if t.dim() < 3 or t.shape[2] != hkv:
-            raise ValueError("a pool must be [num_blocks, block_size, Hkv, ...] with mass's Hkv")
+    (_, hkv, positions), n = mass.shape, new_len.numel()
+    if pools.tensors and pools.heads != {hkv}:
+        raise ValueError("a pool must be [num_blocks, block_size, Hkv, ...] with mass's Hkv")
     devs = [_dev(mass, "mass", (torch.float32,))]
     stride = 0
     if kept is not None:
@@ -926,15 +933,16 @@ def spec_kv_evict(ref_count, block_table, cached_len, rows, new_len, mass, *, bl
         stride = kept.shape[2]
     if workspace is None:
         with _allocating_on(stream, _one_device(devs)):
-            workspace = new_workspace(evict_workspace_bytes(n, hkv, mass.shape[2]), mass.device)
+            workspace = new_workspace(evict_workspace_bytes(n, hkv, positions), mass.device)
     t, ws, dev = _page_table(ref_count, block_table, cached_len, block_size,
                              (("new_len", new_len), ("rows", rows), ("keep_first", keep_first)),
                              pools, workspace, stream)
-    _one_device(devs + [dev])
+    if any(d != dev for d in devs):
+        _one_device(devs + [dev])
     st = (_lib or load_library()).spec_kv_evict(
-        ctypes.byref(t), n, None if rows is None else rows.data_ptr(), new_len.data_ptr(),
+        t, n, None if rows is None else rows.data_ptr(), new_len.data_ptr(),
         None if keep_first is None else keep_first.data_ptr(), keep_last, hkv, mass.data_ptr(),
-        mass.shape[2], None if kept is None else kept.data_ptr(), stride, len(pools.tensors),
+        positions, None if kept is None else kept.data_ptr(), stride, len(pools.tensors),
         pools.array, ws.data_ptr(), ws.numel(), _stream_on(stream, dev))
     if st:
         _check(st, "spec_kv_evict")
