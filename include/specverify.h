@@ -683,7 +683,7 @@ SV_API sv_status sv_workspace_status(void* workspace, int clear, void* stream);
 SV_API const char* sv_status_string(sv_status status);
 
 /* Attention kernel selection, for measurement and tests (spec_verify_attn and its paged,
- * host-lengths and shared-prefix forms): 0 = automatic (default),
+ * host-lengths, shared-prefix and 4-bit forms): 0 = automatic (default),
  * 1 = warp-level mma.sync kernel, 2 = tcgen05 kernel. Returns the previous value, or -1
  * if the value is unknown or the kernel is not built. Process-wide. */
 SV_API int sv_set_attn_kernel(int which);

@@ -1,5 +1,5 @@
 // attn_kv4.cu -- verify attention over a 4-bit paged cache (format: kv4.cuh) for few query rows
-// a KV head, on warp-level MMAs with the keys as the M dimension.
+// a KV head, or short sequences, on warp-level MMAs with the keys as the M dimension.
 //
 // The transposed products S^T = K Q^T and O^T = V^T P^T put the 16 keys (or 16 elements of d)
 // of an m16n8k16 step in M and up to 8 query rows in N, so that a single token's G rows fill
