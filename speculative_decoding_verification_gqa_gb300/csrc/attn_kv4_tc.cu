@@ -688,10 +688,12 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           wk[c] = *reinterpret_cast<const uint4*>(src + ((c ^ sw) << 4));
           wv[c] = *reinterpret_cast<const uint4*>(src + L::RAW + ((c ^ sw) << 4));
         }
-        warp_arrive(&bars->raw_empty[rs]);
         decode_row<HD>(smem + L::KC + cs * L::TILE, r, wk, sk);
+        // for the MMAs, and for the TMA that writes the stage next: it may not overtake the reads
+        // above (without a fence before this arrival it did, about once in a thousand units)
         fence_proxy_async();
         warp_arrive(&bars->kc_full[cs]);
+        warp_arrive(&bars->raw_empty[rs]);
         if (!(ok = it < NCV || wwait(&bars->vc_empty[cs], free_par))) break;
         decode_row<HD>(smem + L::VC + cs * L::TILE, r, wv, sv);
         fence_proxy_async();

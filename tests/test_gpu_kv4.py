@@ -357,6 +357,22 @@ def test_batches_of_every_layout(kernel, T, D, Hq, Hkv, d, bs):
     check_attn(T, D, Hq, Hkv, d, bs, seed=len(T))
 
 
+def test_many_units_a_cta_again_and_again():
+    """Six units a CTA of the tcgen05 kernel and full rows: the same bits every time, and right."""
+    T, D, Hkv, G = [(311 * b) % 1101 for b in range(150)], [7 - b % 3 for b in range(150)], 6, 16
+    prev = sv.set_attn_kernel(2)
+    try:
+        check_attn(T, D, G * Hkv, Hkv, 128, 64, seed=3)
+        c = Cache("kv4", [t + 1 + n for t, n in zip(T, D)], Hkv, 128, 64, 14)
+        q = make_q(sum(D) + len(D), G * Hkv, 128, 4)
+        first = run_attn(c, q, T, D)
+        for _ in range(40):
+            again = run_attn(c, q, T, D, workspace=first[2])
+            assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+    finally:
+        sv.set_attn_kernel(prev)
+
+
 @pytest.mark.parametrize("B,T,G,D", [(1, 300, 8, 15), (70, 2000, 8, 3), (70, 2000, 8, 4), (3, 900, 16, 15)])
 def test_the_kernel_the_rules_choose(B, T, G, D):
     check_attn([T - 7 * b for b in range(B)], [D] * B, 2 * G, 2, 64, 16)
