@@ -811,7 +811,10 @@ __device__ __forceinline__ void attn_tc_body(const AttnParams& p, const CUtensor
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k)
             w[k] = *reinterpret_cast<const uint4*>(rsrc + k * RSTEP);
-          mbar_arrive(&bars->kv_empty[rs]);  // the raw V tile is read
+          // The raw V tile is read; the TMA that writes the stage next is of another proxy, and
+          // may not overtake these reads.
+          fence_proxy_async();
+          mbar_arrive(&bars->kv_empty[rs]);
           const int lim = nkeys - j * KT;    // rows >= lim lie past the sequence's end
           const int low = kvis - j * KT;     // rows < low left the sliding window
 #pragma unroll
