@@ -815,6 +815,8 @@ __global__ void __launch_bounds__(Layout<HD, F8, RT>::THREADS, 1)
 #pragma unroll
           for (int k = 0; k < KT / CR; ++k)
             w[k] = *reinterpret_cast<const uint4*>(rsrc + k * RSTEP);
+          // As in attn_tc.cu: TMA, which writes the stage next, may not overtake these reads.
+          fence_proxy_async();
           mbar_arrive(&bars->v_empty[rs]);
           const int lim = s.d.nkeys - j * KT, low = s.d.start - j * KT;  // the part's keys
 #pragma unroll

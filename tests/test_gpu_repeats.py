@@ -9,6 +9,7 @@ import speculative_decoding_verification_gqa_gb300 as sv
 from speculative_decoding_verification_gqa_gb300 import synth
 
 from gpu_util import assert_close, dev_attn, ensure_built
+from shared_util import inputs, pages, to_device
 
 pytestmark = pytest.mark.gpu
 
@@ -55,4 +56,27 @@ def test_e4m3_the_same_bits_every_time(bs, window):
     ref = oracle.verify_attn(x["q"], x["k"], x["v"], x["seq_lens"], x["draft_len"], Hq=w.Hq, Hkv=w.Hkv, d=w.d,
                              kv_scale=x["kv_scale"], window=window,
                              units=[(b, (5 * b) % 4) for b in range(0, 120, 7)])
+    assert_close(first.view(torch.int16).cpu().numpy().view(np.uint16), ref)
+
+
+@pytest.mark.parametrize("bs", [16, 64])
+def test_e4m3_shared_prefixes_the_same_bits_every_time(bs):
+    """24 groups of 5 sequences of up to 128 rows a KV head: more than 3 units of the sequences
+    and nearly 2 of the prefixes for each SM."""
+    groups = [((311 * g) % 701, [((311 * g) % 701 + (211 * (5 * g + b)) % 500, 7 - b % 3) for b in range(5)])
+              for g in range(24)]
+    w, x, gb, P = inputs(groups, Hq=64, Hkv=4, d=128, kv="fp8_e4m3", seed=bs)
+    q, k, v, table, T, D, sc = to_device(x, pages(x, gb, P, bs, seed=bs))
+    gb, P = torch.from_numpy(gb).cuda(), torch.from_numpy(P).cuda()
+    ws = sv.new_workspace(1 << 28)
+
+    def call():
+        return sv.spec_verify_attn_shared(q, k, v, table, T, D, gb, P, max_draft_len=7, kv_scale=sc, workspace=ws,
+                                          max_seq_len=int(x["seq_lens"].max()))
+
+    first = call()
+    assert all(torch.equal(call(), first) for _ in range(AGAIN))
+    assert sv.workspace_status(ws) == 0
+    ref = oracle.verify_attn(x["q"], x["k"], x["v"], x["seq_lens"], x["draft_len"], Hq=w.Hq, Hkv=w.Hkv, d=w.d,
+                             kv_scale=x["kv_scale"], units=[(b, (5 * b) % 4) for b in range(0, 120, 7)])
     assert_close(first.view(torch.int16).cpu().numpy().view(np.uint16), ref)
