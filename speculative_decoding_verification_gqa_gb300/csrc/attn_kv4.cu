@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(NTHREADS, SM_CTAS) attn_kv4_kernel(const Kv4At
   const int hg = warp % HG, kw = warp / HG;
   uint8_t* ring = smem + warp * warp_bytes<HD, NT>();
   pdl_wait();
-  pdl_trigger();  // after the wait: the join kernel reads the lengths before its own
+  pdl_trigger();
   LineWalk walk;
   if (!line_begin<NTHREADS>(p, blockIdx.x, walk)) return;
 
@@ -511,9 +511,8 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const Kv4Attn p) {
   __shared__ float4 s_o[JT / 32][HD / 4];
   __shared__ float2 s_ml[JT / 32];
   pdl_trigger();
+  pdl_wait();  // before the lengths too: only this grid's own wait makes what wrote them visible
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // The lengths are read before the wait: the attention kernel's CTAs let this one start when
-  // they have waited themselves, so whatever wrote the lengths is complete.
   const int per = p.heads * ((p.mr + JROWS - 1) / JROWS);  // items of a unit
   Line total = {};
   LineAt at;
@@ -525,10 +524,8 @@ __global__ void __launch_bounds__(JT) kv4_join_kernel(const Kv4Attn p) {
     by_unit = true;
     return it < end ? it / per : -1;
   });
-  LineWalk walk;
-  if (any) walk = line_enter(p, at, it / per - at.units, true);
-  pdl_wait();
   if (!any) return;
+  LineWalk walk = line_enter(p, at, it / per - at.units, true);
   walk.v0 = 0;
   walk.v1 = total.virt;
   constexpr int LN = HD / 4;  // lanes of a row

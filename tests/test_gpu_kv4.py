@@ -650,3 +650,52 @@ def test_one_workspace_serves_both_kernels():
                 r += 1 + n
         sv.set_attn_kernel(prev)
     assert sv.workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("Hq,D", [(4, 0), (32, 7)])
+def test_lengths_that_the_kernel_before_has_changed(kernel, captured, Hq, D):
+    """spec_pages_trim sets the lengths directly before the call, whose few units are split over
+    CTAs: both of its grids go by the new ones, every time."""
+    Hkv, bs, full = 2, 16, [3000, 1500]
+    c = Cache("kv4", [n + 1 + D for n in full], Hkv, 128, bs, 2)
+    q = make_q(2 * (1 + D), Hq, 128, 3)
+    cuts = [[2003, 77], [311, 1499], [2999, 1], [45, 1003]]
+    want = [run_attn(c, q, n, [D, D], max_seq=3000)[:2] for n in cuts]
+    ref0 = torch.ones(c.blocks, dtype=torch.int32, device=DEV)
+    ref, table, length = ref0.clone(), c.table.clone(), i32([0, 0])
+    grown, new, Di = i32([n + 1 + D for n in full]), [i32(n) for n in cuts], i32([D, D])
+    pages_ws = sv.new_workspace(sv.pages_workspace_bytes(c.blocks, 2))
+    ws = sv.new_workspace(sv.verify_kv4_workspace_bytes(sv.paged_attn_desc(q, c.k, 2, D, 3000, kv4=True)))
+    outs = [(torch.full_like(q, 5.0), torch.full(q.shape[:2], 5.0, device=DEV)) for _ in cuts]
+
+    def step(n, out, lse):
+        ref.copy_(ref0)
+        table.copy_(c.table)
+        length.copy_(grown)
+        sv.spec_pages_trim(ref, table, length, None, n, block_size=bs, workspace=pages_ws)
+        # (the rows of the pages are all there still: the call goes by a table that was not cut)
+        sv.spec_verify_attn_kv4(q, c.k, c.v, c.scales, c.hs, c.table, length, Di, max_draft_len=D, max_seq_len=3000,
+                                out=out, lse=lse, workspace=ws)
+
+    def run():
+        for n, (out, lse) in zip(new, outs):
+            step(n, out, lse)
+
+    if captured:
+        run()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+    for _ in range(25):
+        for out, lse in outs:
+            out.fill_(5.0)
+            lse.fill_(5.0)
+        if captured:
+            g.replay()
+        else:
+            run()
+        for (out, lse), (o, l) in zip(outs, want):
+            assert torch.equal(out, o) and torch.equal(lse, l)
+    assert sv.workspace_status(ws) == 0 and sv.workspace_status(pages_ws) == 0
