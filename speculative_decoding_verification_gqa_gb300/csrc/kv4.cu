@@ -205,16 +205,19 @@ __device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {  // of bf
 }
 
 // 32 bytes of a thread, in one access where they are aligned (W32), so that no 32-byte sector is
-// touched twice.
+// touched twice. Volatile and with a clobber: what it reads the grid before may have written, so
+// the compiler must leave it behind pdl_wait.
 template <bool W32>
 __device__ __forceinline__ void load32(const void* p, uint4 (&x)[2]) {
   if constexpr (W32) {
-    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-        : "=r"(x[0].x), "=r"(x[0].y), "=r"(x[0].z), "=r"(x[0].w), "=r"(x[1].x), "=r"(x[1].y), "=r"(x[1].z), "=r"(x[1].w)
-        : "l"(p));
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(x[0].x), "=r"(x[0].y), "=r"(x[0].z), "=r"(x[0].w), "=r"(x[1].x), "=r"(x[1].y), "=r"(x[1].z),
+                   "=r"(x[1].w)
+                 : "l"(p)
+                 : "memory");
   } else {
-    x[0] = __ldg(reinterpret_cast<const uint4*>(p));
-    x[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    x[0] = *reinterpret_cast<const uint4*>(p);
+    x[1] = *(reinterpret_cast<const uint4*>(p) + 1);
   }
 }
 template <bool W32>

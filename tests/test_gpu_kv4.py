@@ -699,3 +699,39 @@ def test_lengths_that_the_kernel_before_has_changed(kernel, captured, Hq, D):
         for (out, lse), (o, l) in zip(outs, want):
             assert torch.equal(out, o) and torch.equal(lse, l)
     assert sv.workspace_status(ws) == 0 and sv.workspace_status(pages_ws) == 0
+
+
+@pytest.mark.parametrize("count", [3, 3000])
+def test_rows_that_the_kernel_before_has_made(count):
+    """Two sequences read into one buffer, one after the other, and each written from it to
+    another cache directly after: the rows of its own read, every time."""
+    Hkv, d, bs = 4, 128, 16
+    src = [Cache("kv4", [count], Hkv, d, bs, 40 + k) for k in range(2)]
+    start, n = i32([0]), i32([count])
+    ws = sv.new_workspace(sv.kv4_workspace_bytes(1))
+    hs = torch.full((2, Hkv), 0.004, device=DEV)
+
+    def move(k, buf, to):
+        c = src[k]
+        sv.spec_kv4_read(c.k, c.v, c.scales, c.hs, c.table, start, n, k_out=buf[0], v_out=buf[1], workspace=ws)
+        sv.spec_kv4_write(*buf, *to, hs, c.table, start, n, workspace=ws)
+
+    want, got = ([empty_pages(src[0].blocks, bs, Hkv, d) for _ in range(2)] for _ in range(2))
+    for k in range(2):
+        move(k, [torch.zeros(count, Hkv, d, dtype=torch.bfloat16, device=DEV) for _ in "kv"], want[k])
+        torch.cuda.synchronize()
+    buf = [torch.zeros(count, Hkv, d, dtype=torch.bfloat16, device=DEV) for _ in "kv"]
+    assert buf[0].data_ptr() % 32 == 0
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        for _ in range(3):
+            for k in range(2):
+                move(k, buf, got[k])
+    for _ in range(20):
+        for p in got[0] + got[1]:
+            p.fill_(CANARY)
+        g.replay()
+        for k in range(2):
+            assert all(torch.equal(a, b) for a, b in zip(got[k], want[k]))
+    assert sv.workspace_status(ws) == 0
