@@ -391,9 +391,10 @@ SV_API size_t spec_kv4_workspace_size(int32_t batch);
  *   k, v         bf16, row r's [Hkv, head_dim] at element r * k_row_stride (v_row_stride), a
  *                multiple of 8, at least Hkv * head_dim (a slice of a fused projection) and at
  *                most 2^30; 16-byte aligned
- * A start or count out of range is reported by sv_workspace_status (SV_ERR_DEVICE_SHAPE) and
- * nothing is written; a row whose table entry names no page of the pool is reported and
- * skipped. No two rows of a call may go to the same position of a page.
+ * A start or count out of range, or a sum of count above rows, is reported by
+ * sv_workspace_status (SV_ERR_DEVICE_SHAPE) and nothing is written; a row whose table entry
+ * names no page of the pool is reported and skipped. With rows = 0 nothing is launched, and start
+ * and count are not looked at. No two rows of a call may go to the same position of a page.
  */
 SV_API sv_status spec_kv4_write(const sv_kv4_pages* pages, int32_t batch,
                                 const int32_t* block_table, int32_t max_blocks_per_seq,

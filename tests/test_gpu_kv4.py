@@ -735,3 +735,18 @@ def test_rows_that_the_kernel_before_has_made(count):
         for k in range(2):
             assert all(torch.equal(a, b) for a, b in zip(got[k], want[k]))
     assert sv.workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("which", ["write", "read"])
+@pytest.mark.parametrize("start,count", [([0, 0], [0, 0]), ([0, 0], [1, 0]), ([-1, 0], [0, -1])])
+def test_a_call_without_rows_looks_at_nothing(which, start, count):
+    """rows = 0: the lengths, whatever they are, are not read and not reported."""
+    pages = empty_pages(4, 16, 2, 64)
+    x = torch.empty(0, 2, 64, dtype=torch.bfloat16, device=DEV)
+    ws = sv.new_workspace(sv.kv4_workspace_bytes(2))
+    args = (*pages, torch.ones(2, 2, device=DEV), i32([[0, 1], [2, 3]]), i32(start), i32(count))
+    if which == "write":
+        sv.spec_kv4_write(x, x, *args, workspace=ws)
+    else:
+        assert sv.spec_kv4_read(*args, rows=0, workspace=ws)[0].shape == (0, 2, 64)
+    assert sv.workspace_status(ws) == 0 and all((p == CANARY).all() for p in pages)
