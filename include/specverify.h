@@ -357,7 +357,8 @@ SV_API sv_status spec_pages_compact(const sv_page_table* table, int32_t num_pool
  *   scales            E4M3 [num_blocks, block_size, num_kv_heads, 2, head_dim / 16], 16-byte
  *                     aligned: K's block scales, then V's
  *   kv_scale          fp32 [2, num_kv_heads], in [2^-100, 2^100] (row 0 K, row 1 V), such as
- *                     the head's largest magnitude / (6 * 448)
+ *                     the head's largest magnitude / (6 * 448); or 0, for a head of zeros:
+ *                     everything finite of it is written, and reads, as 0
  * All three arrays move and are shared as pools of the spec_pages_ calls and spec_kv_evict
  * (whose pages need whole 16 bytes a position: with head_dim 64 an even number of heads).
  */
@@ -382,7 +383,8 @@ SV_API size_t spec_kv4_workspace_size(int32_t batch);
  * start[b] .. start[b] + count[b] - 1 of its block-table row. For a block x of 16 elements and
  * its head's scale s,
  *   c = the E4M3 value nearest to max |x| / (6 s), at most 448,
- *   each code the E2M1 value nearest to x_k / (s c), at most 6 in magnitude (0 if c = 0),
+ *   each code the E2M1 value nearest to x_k / (s c), at most 6 in magnitude (0 if c = 0;
+ *   c = 0 if s = 0),
  * nearest to the real quotients, ties to the even code. A block that holds an infinity or a
  * NaN gets the scale NaN, and all of it reads as NaN.
  *   block_table  int32 [batch, max_blocks_per_seq]

@@ -9,7 +9,8 @@
 // block in 2^12, the choice is made in 64 bits, where x and the middle of
 // two codes times s c are exact (8 and 31 significant bits). So the codes do not depend on
 // how the quotient is computed, and a reference in 64 bits gives the same.
-// A block with an infinity or a NaN gets the scale NaN: it reads as NaN, all 16 elements.
+// A block with an infinity or a NaN gets the scale NaN: it reads as NaN, all 16 elements. A head
+// scale of 0, which a head of zeros gets from its largest magnitude, makes other blocks zeros.
 //
 // Both calls move bytes and nothing else bounds them: a thread takes a block (32 bytes of bf16,
 // 8 bytes of codes, a scale). The scan that finds each row's sequence and position runs in
@@ -269,11 +270,11 @@ __global__ void __launch_bounds__(NTH, 4) kv4_write_kernel(const Kv4Args a) {
         uint32_t m = abs_max2(abs_max2(abs_max2(x[n][0].x, x[n][0].y), abs_max2(x[n][0].z, x[n][0].w)),
                               abs_max2(abs_max2(x[n][1].x, x[n][1].y), abs_max2(x[n][1].z, x[n][1].w)));
         m = abs_max2(m, m >> 16) & 0xffffu;
-        uint32_t c;
+        uint32_t c = 0;
         uint2 code = make_uint2(0, 0);
         if (m >= 0x7f80u) {  // an infinity or a NaN
           c = 0x7fu;
-        } else {
+        } else if (m != 0 && head != 0.f) {  // (a head scale of 0 has no quotients)
           const float amax = __uint_as_float(m << 16);
           const float q = amax * inv6;
           const uint32_t lo = to_e4m3(q * LESS), hi = to_e4m3(q * MORE);

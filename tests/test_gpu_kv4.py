@@ -750,3 +750,44 @@ def test_a_call_without_rows_looks_at_nothing(which, start, count):
     else:
         assert sv.spec_kv4_read(*args, rows=0, workspace=ws)[0].shape == (0, 2, 64)
     assert sv.workspace_status(ws) == 0 and all((p == CANARY).all() for p in pages)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("strided", [False, True])
+def test_a_head_scale_of_zero(kernel, d, strided):
+    """What the largest magnitude / (6 * 448) gives for a head of zeros: the head is written as
+    zeros, whatever finite it holds, and is read, attended and weighted as such."""
+    Hkv, G, bs, n = 3, 2, 16, 70
+    gen = torch.Generator().manual_seed(d)
+    fused = torch.randn(n, 3, Hkv, d, generator=gen).to(torch.bfloat16).to(DEV)
+    fused[:, 0, 1] = 0  # K of head 1 is zeros, V of head 2 has no scale
+    k, v = fused[:, 0], fused[:, 1]
+    if not strided:
+        k, v = k.contiguous(), v.contiguous()
+    hs = torch.stack([t.float().abs().amax((0, 2)) for t in (k, v)]) / (6 * 448)
+    hs[1, 2] = 0
+    assert hs[0, 1] == 0
+    table, blocks = block_table([n], bs, gen)
+    pages = empty_pages(blocks, bs, Hkv, d)
+    args = (*pages, hs, table.to(DEV), i32([0]), i32([n]))
+    sv.spec_kv4_write(k, v, *args)
+    kc, vc, sc = written(pages, places(table, bs, [0], [n]))
+    zeroed = [k.clone(), v.clone()]
+    zeroed[1][:, 2] = 0
+    for got, want in zip((kc, vc, sc), expect_rows(*zeroed, torch.where(hs == 0, torch.ones_like(hs), hs))):
+        assert torch.equal(got, want)
+    rk, rv = sv.spec_kv4_read(*args, rows=n)
+    assert (rk[:, 1] == 0).all() and (rv[:, 2] == 0).all() and rk.isfinite().all() and rv.isfinite().all()
+    q = make_q(1, Hkv * G, d, 7)
+    lse = torch.zeros(1, Hkv * G, device=DEV)
+    out = sv.spec_verify_attn_kv4(q, *pages, hs, table.to(DEV), i32([n - 1]), i32([0]), max_draft_len=0,
+                                  max_seq_len=n - 1, lse=lse)
+    mass = sv.spec_attn_mass(q, pages[0], table.to(DEV), i32([n - 1]), i32([0]), torch.zeros(1, Hkv, n, device=DEV),
+                             max_draft_len=0, max_seq_len=n - 1, kv_scale=hs, scales=pages[2], lse=lse)
+    assert out.isfinite().all() and (out[0, 2 * G:] == 0).all()
+    # ln n and even weights, to the arithmetic of the log-sum and the exponent (2^-19 and 2^-15)
+    assert ((lse[0, G:2 * G] - math.log(n)).abs() <= 2 ** -17).all()
+    assert ((mass[0, 1] * n - G).abs() <= G * 2 ** -14).all()
+    k[3, 1, 5] = math.inf  # and what is not finite is NaN still
+    sv.spec_kv4_write(k, v, *args)
+    assert sv.spec_kv4_read(*args, rows=n)[0][3, 1, :16].isnan().all()
