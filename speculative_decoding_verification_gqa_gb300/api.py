@@ -700,7 +700,7 @@ _ATTN_DESC = struct.Struct("@iiiiiiqqifixxxx")
 def _packed_desc(B, Hq, hkv, d, max_draft_len, max_seq_len, q_rows, dtype, scale, window) -> bytes:
     try:
         return _ATTN_DESC.pack(B, Hq, hkv, d, max_draft_len, max_seq_len, q_rows, 0, dtype, scale, window)
-    except (struct.error, OverflowError) as e:  # (a scale beyond 32 bits: the latter)
+    except struct.error as e:
         raise ValueError("max_draft_len, max_seq_len, softmax_scale or sliding_window: %s" % e)
 
 

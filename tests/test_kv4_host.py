@@ -255,9 +255,3 @@ def test_the_model_rounds_to_the_nearest():
 def test_the_model_keeps_the_heaviest():
     assert evict([0.0, 5.0, 1.0, 5.0, math.nan, 2.0], 6, 3, 1, 1) == [0, 1, 5]
     assert evict([1.0, 1.0, 1.0, 1.0], 4, 2, 0, 0) == [0, 1]
-
-
-@pytest.mark.parametrize("scale", [1e39, -1e300])
-def test_a_scale_that_32_bits_cannot_hold(scale):
-    with pytest.raises(ValueError):
-        api._packed_desc(1, 4, 1, 64, 0, 9, 3, 0, scale, 0)
