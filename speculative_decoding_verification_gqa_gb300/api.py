@@ -918,6 +918,8 @@ def spec_kv_evict(ref_count, block_table, cached_len, rows, new_len, mass, *, bl
     pages in every pool ([num_blocks, block_size, Hkv, ...]), and mass with them, in place.
     Fills ``kept`` (int32 [n, Hkv, k]: which position each was). Call it once a layer, then
     spec_pages_trim with the same rows and new_len."""
+    if not -1 << 31 <= keep_last < 1 << 31:  # (ctypes would pass its low 32 bits)
+        raise ValueError("keep_last must fit in 32 bits")
     pools = _as_pools(pools)
     if mass.dim() != 3 or mass.shape[0] != cached_len.numel():
         raise ValueError("mass must be [rows, Hkv, positions]")

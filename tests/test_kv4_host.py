@@ -255,3 +255,11 @@ def test_the_model_rounds_to_the_nearest():
 def test_the_model_keeps_the_heaviest():
     assert evict([0.0, 5.0, 1.0, 5.0, math.nan, 2.0], 6, 3, 1, 1) == [0, 1, 5]
     assert evict([1.0, 1.0, 1.0, 1.0], 4, 2, 0, 0) == [0, 1]
+
+
+@pytest.mark.parametrize("last", [(1 << 32) + 5, -(1 << 32), 1 << 31])
+def test_a_keep_last_that_32_bits_cannot_hold(last):
+    """Refused: its low 32 bits are another number of positions."""
+    one, bt = torch.zeros(1, dtype=torch.int32), torch.zeros(1, 4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="keep_last"):
+        api.spec_kv_evict(one, bt, one, None, one, torch.zeros(1, 2, 9), block_size=16, pools=[], keep_last=last)
