@@ -828,17 +828,19 @@ constexpr int KV4_PAIR_UNITS_SHORT = 1024;
 // The mma kernel (row tiles of 16, no start to speak of) up to 16 rows a KV head, and for more
 // rows in calls of so many of its tiles of 128 x 128 altogether; else the tcgen05 kernel (row
 // tiles of 128). The mma kernel's and the tcgen05 kernel's time with 4 KV heads, at 32, 48, 64,
-// 128 rows: 64 x 16000 168 155, 219 156, 274 158, 483 161; 64 x 4000 63.2 69.4, 75.8 69.6,
-// 90.9 71.7, 153 75.8; 8 x 4000 22.5 28.2, 24.6 28.6, 24.6 28.7, 35.1 28.7; one of 20000
-// 18.5 26.5, 20.5 26.6, 22.5 26.6, 28.8 28.3; short, 64 x 500 24.6 39.6, 24.6 41.0, 28.7 41.3,
-// 43.3 43.9; 64 x 1000 36.4 45.1, 38.0 47.0, 43.1 46.1, 64.8 49.4. d = 64: 64 x 4000 43.3 62.9,
-// 51.3 62.6, 61.0 64.2, 96.3 65.5. Many rows: 16 x 300 with 2 KV heads at 256, 512 rows
-// 18.0 20.5, 26.3 20.5.
+// 128 rows: 64 x 16000 170 154, 222 154, 276 155, 486 158; 64 x 4000 65.4 67.5, 79.4 67.0,
+// 94.2 68.1, 156 74.8; 8 x 4000 24.6 28.7, 26.7 28.7, 26.6 28.7, 37.4 28.7; one of 20000
+// 20.7 24.6, 22.4 26.6, 24.6 26.0, 32.5 28.7; short, 64 x 700 22.5 40.6, 30.0 40.8, 34.9 41.1,
+// 52.3 43.0. Many rows: 16 x 300 with 2 KV heads at 256, 512 rows 18.0 20.5, 26.3 20.5. With
+// d = 64 a tile of the tcgen05 kernel is not much shorter, and "few rows" are more: 64 x 16000
+// 103 135, 133 137, 163 137, 281 139; 64 x 4000 45.1 57.4, 53.0 57.5, 61.5 58.2, 96.8 59.4;
+// 8 x 4000 20.5 24.6, 20.8 24.6, 20.5 24.6, 28.7 24.7.
 constexpr int KV4_SMALL_ROWS = 16;
+constexpr int KV4_FEW_ROWS = 32, KV4_FEW_ROWS_64 = 48;
 constexpr int KV4_MMA_ROWS = 256;
 constexpr int64_t KV4_MMA_TILES = 6144;
 constexpr int64_t KV4_MMA_TILES_SHORT = 12288;  // short sequences
-constexpr int64_t KV4_MMA_TILES_FEW = 32768;    // up to 32 rows
+constexpr int64_t KV4_MMA_TILES_FEW = 32768, KV4_MMA_TILES_FEW_64 = 65536;  // up to "few" rows
 
 int64_t kv4_max_tiles(const sv_attn_desc* d) {
   return ((int64_t)d->max_seq_len + d->max_draft_len) / KV4_KT + 1;
@@ -850,7 +852,9 @@ int pick_kv4(const sv_attn_desc* d) {
   if (g_attn_kernel == 2) return 2;
   const int64_t rows = kv4_rows_per_head(d), tiles = kv4_max_tiles(d);
   const int64_t all = (int64_t)d->batch * d->num_kv_heads * ((rows + 15) / 16) * tiles * d->head_dim / 128;
-  const int64_t most = rows <= 2 * KV4_SMALL_ROWS        ? KV4_MMA_TILES_FEW
+  const bool d64 = d->head_dim == 64;
+  const int64_t most = rows <= (d64 ? KV4_FEW_ROWS_64 : KV4_FEW_ROWS)
+                           ? (d64 ? KV4_MMA_TILES_FEW_64 : KV4_MMA_TILES_FEW)
                        : tiles <= 2 * KV4_SHORT_TILES ? KV4_MMA_TILES_SHORT
                                                       : KV4_MMA_TILES;
   return rows <= KV4_SMALL_ROWS || (rows <= KV4_MMA_ROWS && all <= most) ? 1 : 2;

@@ -791,3 +791,22 @@ def test_a_head_scale_of_zero(kernel, d, strided):
     k[3, 1, 5] = math.inf  # and what is not finite is NaN still
     sv.spec_kv4_write(k, v, *args)
     assert sv.spec_kv4_read(*args, rows=n)[0][3, 1, :16].isnan().all()
+
+
+@pytest.mark.parametrize("d,D,which", [(64, 5, 1), (64, 7, 2), (128, 3, 1), (128, 5, 2)])
+def test_the_rule_takes_the_kernel_that_measures_faster(d, D, which):
+    """64 sequences of up to 4000 positions, 4 KV heads of 8 query heads: the bits are those of
+    the kernel whose time beside the rule is the smaller."""
+    B, Hkv, G = 64, 4, 8
+    T = [4000 - 37 * b for b in range(B)]
+    c = Cache("kv4", [t + 1 + D for t in T], Hkv, d, 16, d)
+    q = make_q(B * (1 + D), G * Hkv, d, D)
+    prev = sv.set_attn_kernel(0)
+    try:
+        got = run_attn(c, q, T, [D] * B)
+        for k in (1, 2):
+            sv.set_attn_kernel(k)
+            out = run_attn(c, q, T, [D] * B)
+            assert (torch.equal(out[0], got[0]) and torch.equal(out[1], got[1])) == (k == which)
+    finally:
+        sv.set_attn_kernel(prev)
