@@ -810,3 +810,22 @@ def test_the_rule_takes_the_kernel_that_measures_faster(d, D, which):
             assert (torch.equal(out[0], got[0]) and torch.equal(out[1], got[1])) == (k == which)
     finally:
         sv.set_attn_kernel(prev)
+
+
+@pytest.mark.parametrize("d,bs,window", [(64, 64, 0), (64, 8, 0), (128, 8, 0), (128, 16, 0), (128, 16, 150),
+                                         (64, 16, 150), (128, 64, 150)])
+def test_every_layout_with_many_units_a_cta_again_and_again(d, bs, window):
+    """Boxes of a whole tile and of 8 rows, both head dimensions, units that begin at a window:
+    the same bits every time, and right."""
+    T, D, Hkv, G = [(311 * b) % 1101 for b in range(150)], [7 - b % 3 for b in range(150)], 6, 16
+    prev = sv.set_attn_kernel(2)
+    try:
+        check_attn(T, D, G * Hkv, Hkv, d, bs, window=window, seed=3)
+        c = Cache("kv4", [t + 1 + n for t, n in zip(T, D)], Hkv, d, bs, 14)
+        q = make_q(sum(D) + len(D), G * Hkv, d, 4)
+        first = run_attn(c, q, T, D, window=window)
+        for _ in range(30):
+            again = run_attn(c, q, T, D, window=window, workspace=first[2])
+            assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+    finally:
+        sv.set_attn_kernel(prev)

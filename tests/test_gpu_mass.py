@@ -518,3 +518,122 @@ def test_a_decoding_loop_on_an_evicted_4_bit_cache():
         assert (mass[0, :, lens[0]:] == 0).all()
     assert max(lens) == budget and sv.workspace_status(kw["workspace"]) == 0 and sv.workspace_status(ews) == 0
     assert int(ref.sum()) == sum(-(-n // bs) for n in lens)
+
+
+# ------------------------------------------------- state between a call's two launches
+
+MASS_JOBS = [("bf16", [3000, 40, 700], [2, 0, 3], 32, 4), ("kv4", [900, 1700], [7, 3], 8, 2),
+             ("e4m3", [5000], [1], 16, 2)]
+
+
+def mass_jobs():
+    """(q, cache, T, D, keyword arguments, zeros for mass, what it becomes) without log-sums: the
+    second launch reads what the first left in the workspace."""
+    jobs = []
+    for k, (kind, T, D, Hq, Hkv) in enumerate(MASS_JOBS):
+        c = Cache(kind, [t + 1 + n for t, n in zip(T, D)], Hkv, 128, 16, 50 + k)
+        q = make_q(sum(D) + len(D), Hq, 128, k)
+        mass = torch.zeros(len(T), Hkv, max(T) + 10, device=DEV)
+        want = mass_call(c, q, T, D, mass.clone())
+        kw = dict(max_draft_len=max(D), max_seq_len=max(T), kv_scale=c.hs, scales=c.scales)
+        jobs.append((q, c, i32(T), i32(D), kw, mass, want))
+    torch.cuda.synchronize()
+    return jobs
+
+
+def mass_workspace(jobs):
+    n = max(sv.mass_workspace_bytes(sv.paged_attn_desc(q, c.k, len(T), kw["max_draft_len"], kw["max_seq_len"],
+                                                       kv4=c.scales is not None)) for q, c, T, D, kw, _, _ in jobs)
+    return sv.new_workspace(n)
+
+
+def capture(call):
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    return g
+
+
+def test_graphs_of_weights_on_one_workspace():
+    """Replayed one after another, in any order and often."""
+    jobs = mass_jobs()
+    ws = mass_workspace(jobs)
+    graphs = [capture(lambda: sv.spec_attn_mass(q, c.k, c.table, T, D, m, workspace=ws, **kw))
+              for q, c, T, D, kw, m, _ in jobs]
+    for order in ([0, 1, 2], [2, 0, 1, 1, 0, 2], [1, 0]):
+        for k in order:
+            jobs[k][5].zero_()
+            graphs[k].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(jobs[k][5], jobs[k][6]) for k in order)
+    assert sv.workspace_status(ws) == 0
+
+
+def test_weights_of_calls_in_flight():
+    """A stream and a workspace each."""
+    jobs = mass_jobs()
+    lanes = [(torch.cuda.Stream(), mass_workspace([j])) for j in jobs]
+    out = [[j[5].clone() for _ in range(15)] for j in jobs]
+    torch.cuda.synchronize()
+    for i in range(15):
+        for (q, c, T, D, kw, _, _), (s, ws), o in zip(jobs, lanes, out):
+            sv.spec_attn_mass(q, c.k, c.table, T, D, o[i], workspace=ws, stream=s, **kw)
+    torch.cuda.synchronize()
+    for j, o in zip(jobs, out):
+        assert all(torch.equal(m, j[6]) for m in o)
+    assert all(sv.workspace_status(ws) == 0 for _, ws in lanes)
+
+
+EVICT_JOBS = [dict(lens=[3000, 500], new=[1000, 500], last=32), dict(lens=[90, 2000, 700], new=[64, 9, 699], last=4)]
+
+
+def evict_jobs():
+    """(state, new_len, last, what to put back before a call, what it then becomes)."""
+    jobs = []
+    for k, j in enumerate(EVICT_JOBS):
+        done = Rows(j["lens"], 4, 16, (64, 64, 16), 60 + k)
+        check_evict(done, None, j["new"], None, j["last"])
+        s = Rows(j["lens"], 4, 16, (64, 64, 16), 60 + k)
+        jobs.append((s, i32(j["new"]), j["last"], [t.clone() for t in (*s.pools, s.mass)], (*done.pools, done.mass)))
+    torch.cuda.synchronize()
+    return jobs
+
+
+def evict_again(job, ws, stream=None):
+    """The state as it was, and the call, on one stream."""
+    s, new, last, old, _ = job
+    with torch.cuda.stream(stream or torch.cuda.current_stream()):
+        for t, o in zip((*s.pools, s.mass), old):
+            t.copy_(o)
+        sv.spec_kv_evict(s.ref, s.table, s.len, None, new, s.mass, block_size=16, pools=sv.page_pools(s.pools),
+                         keep_last=last, workspace=ws, stream=stream)
+
+
+def evicted(job):
+    return all(torch.equal(t, w) for t, w in zip((*job[0].pools, job[0].mass), job[4]))
+
+
+def test_graphs_of_evictions_on_one_workspace():
+    jobs = evict_jobs()
+    ws = sv.new_workspace(max(sv.evict_workspace_bytes(len(j[1]), 4, j[0].mass.shape[2]) for j in jobs))
+    graphs = [capture(lambda: evict_again(j, ws)) for j in jobs]
+    for order in ([0, 1], [1, 0, 0, 1], [1]):
+        for k in order:
+            graphs[k].replay()
+        torch.cuda.synchronize()
+        assert all(evicted(jobs[k]) for k in order)
+    assert sv.workspace_status(ws) == 0
+
+
+def test_evictions_in_flight():
+    """A stream and a workspace each."""
+    jobs = evict_jobs()
+    lanes = [(torch.cuda.Stream(), sv.new_workspace(sv.evict_workspace_bytes(len(j[1]), 4, j[0].mass.shape[2])))
+             for j in jobs]
+    torch.cuda.synchronize()
+    for _ in range(15):
+        for j, (s, ws) in zip(jobs, lanes):
+            evict_again(j, ws, s)
+    torch.cuda.synchronize()
+    assert all(evicted(j) for j in jobs) and all(sv.workspace_status(ws) == 0 for _, ws in lanes)
