@@ -108,7 +108,8 @@ SV_API size_t spec_verify_attn_workspace_size(const sv_attn_desc* desc);
  * chapter 5", "Sliding window: do not keep the distant past"). Key tiles wholly before
  * a unit's window are skipped, so a call reads about min(T_b + 1 + D_b, W + D_b) cache
  * rows per sequence and KV head. Cache rows of positions before T_b - W + 1 are never
- * used and may hold any bits (they may be reclaimed).
+ * used and may hold any bits (they may be reclaimed). An infinity or a NaN in V at a position
+ * that some row of a window sees may reach the output of all rows of that window and KV head.
  *
  *   q        bf16 [q_rows, Hq, d]
  *   k_cache  bf16 or E4M3 codes [kv_rows, Hkv, d]; v_cache likewise

@@ -23,9 +23,15 @@
 // they meet only at the end of a unit, where a head's parts are joined by the rule of the
 // online softmax. Units, their line and the join across CTAs (kv4_join, below): line.cuh.
 //
-// Measured (d 128): 64 single tokens over up to 8192 positions, 32 query and 8 KV heads, 76.8 us
-// with the join, 308 MB at 4.0 TB/s: half of the issue slots go to decoding, MMAs and exponentials
-// for 8 rows a head of which 4 are live; the rest is the latency that 12 warps an SM leave.
+// Rounding: Q is held in f16 after a power of two that puts its row's largest element in [128,
+// 256), P in f16 (2^-11 of a weight; SHIFT, below); O is accumulated from these, while the row's
+// sum, and with it the log-sum, is that of the unrounded fp32 weights. Scores, sums and O are fp32.
+//
+// Measured (d 128): 64 single tokens over up to 8192 positions, 32 query and 8 KV heads, 78 us
+// with the join, 308 MB at 3.9 TB/s. With half of the issue slots taken (decoding, MMAs and
+// exponentials for 8 rows a head of which 4 are live) and less than 60% of HBM it is bound by
+// latency, which 12 warps an SM do not cover. More than 8 rows a head (16 held) spill 46 words of
+// a thread at the 168 registers that three CTAs leave.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -42,7 +48,8 @@ constexpr int NW = 4;              // warps
 constexpr int NTHREADS = NW * 32;
 constexpr int ST = 3;              // ring stages of a warp
 constexpr int SM_CTAS = 3;         // CTAs of an SM: 168 registers a thread. (64 sequences of up to
-                                   // 8192 positions, single tokens: 76.8 us; 4 CTAs 81.2, 5: 92)
+                                   // 8192 positions, single tokens, with 3 CTAs 76.8 us, 4: 81.2,
+                                   // 5: 92)
 // Reference of a row: its largest score less SHIFT (log2 units), raised when a score is more
 // than RESCALE above that score. P = 2^(s - reference) then lies below 2^15 and the largest at
 // 2^7 or more, so that f16 (largest 65504, least step 2^-24) drops only weights below 2^-32 of

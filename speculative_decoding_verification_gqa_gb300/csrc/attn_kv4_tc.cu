@@ -23,7 +23,10 @@
 //                keys outside the sequence, whose values are then zero whatever their codes.
 // 16 warps, because 17 would leave a thread 96 registers (five warps on a scheduler) and a
 // softmax thread holds 64 scores: with some 30 words spilled a tile took 3700 clocks, as next to
-// 220 KB of shared memory L1 has nothing to hold them.
+// 220 KB of shared memory L1 has nothing to hold them. At 128 registers 24 words are spilled still
+// (d 128; none with d 64).
+//
+// Rounding: as in attn_kv4.cu (Q and P in f16, the sums those of the unrounded weights).
 //
 // At the end of a unit O goes out, and at its start Q comes in, through 2 KB of shared memory a
 // warp, so that global memory sees 64-byte pieces of a row and not 16; the next unit's Q is
@@ -32,8 +35,10 @@
 //
 // Measured (d 128): a tile takes 2050 clocks, of which its MMAs take 1024 (issuing them alone
 // would give 1.9 PFLOP/s); decoding and softmax warps issue 1200 instructions a scheduler a
-// tile. 8 sequences of 32768 positions, 16 tokens, 64 query and 8 KV heads: 140 us with the join,
-// 0.98 PFLOP/s; 16 of 8192, 32 tokens, 32 and 8 heads: 84 us, 0.82.
+// tile, half of their slots: the rest of its time is what its steps (S, scores to registers,
+// exponentials, P V) wait for one another, as each warpgroup has one score buffer. 8 sequences of
+// 32768 positions, 16 tokens, 64 query and 8 KV heads: 142 us with the join, 0.97 PFLOP/s; 16 of
+// 8192, 32 tokens, 32 and 8 heads: 84 us, 0.82.
 //
 // TMEM columns: O_0, O_1 (128 each), S_0, S_1 (64 each), Q (64: f16 pairs), P_0, P_1 (32 each).
 // Every wait is bounded as in attn_tc.cu.

@@ -22,9 +22,12 @@
 // share of the line, and finds its place by scanning the lengths itself.
 //
 // Measured (d 128): 32 sequences of up to 16384 positions, 8 tokens, 32 query and 4 KV heads,
-// bf16: the first pass 61 us, the second 70, of 278 MB each (4.0 to 4.5 TB/s) with half of the
-// issue slots taken; 16 of up to 8192, 9 tokens, 8 KV heads, 4 bits, log-sums given: 24.6 us for
-// 43 MB, a chain of short phases (scan, Q, ten chunks a warp). On tcgen05 with K by TMA (a key
+// bf16: the first pass 61 us, the second 70, of 278 MB each (4.0 to 4.5 TB/s; 62 us with log-sums
+// given); 16 of up to 8192, 9 tokens, 8 KV heads, 4 bits, log-sums given: 23.4-25 us for 43 MB, a
+// chain of short phases (scan, Q, ten chunks a warp). With 40 to 52% of the issue slots taken both
+// are bound by latency: 12 warps of up to 168 registers, 64 of which hold two tiles of decoded
+// keys, are all that an SM has. (The first pass spills up to 24 words a thread with bf16, 14 with
+// E4M3, 9 with 4 bits.) Q is held in f16 next to E4M3 and 4-bit keys. On tcgen05 with K by TMA (a key
 // in a TMEM lane, a row's sum in a register) they took 122 to 131 and 28 us: a page of 16 rows
 // makes 2 KB boxes, about 100 clocks each.
 #include <cuda_bf16.h>
